@@ -86,10 +86,11 @@ extern "C" {
 #define PA_ERR_CRC          -9  /* a compact page does not match its published CRC */
 
 /* Bits OR-ed into the int32 status word at byte 0 of the decode workspace
- * (and of the optional status word of kv_append_rows) by device code. */
+ * (and of the optional status word of the row appends and gathers) by device
+ * code. */
 #define PA_STATUS_BAD_PAGE   1  /* a page id outside [0, pool_pages): tile output is NaN */
 #define PA_STATUS_TIMEOUT    2  /* a bounded device wait gave up: outputs are invalid */
-#define PA_STATUS_BAD_ROW    4  /* kv_append_rows: position or page outside the table/pool */
+#define PA_STATUS_BAD_ROW    4  /* appends, gathers: position or page outside the table/pool */
 
 /* Thread-local message for the last failing call on this thread ("" if none). */
 const char* kv_last_error(void);
@@ -303,6 +304,96 @@ int lse_merge(const float* out_parts, const float* lse_parts,
 int kv_append_rows(void* pool, int64_t pool_pages, const int32_t* page_table,
                    int max_pages, const int32_t* positions, const void* rows,
                    int B, int row_bytes, int32_t* status, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Appends with the position rotation, and the 8-bit pool                   */
+/* (no counterpart in the source pages)                                     */
+/* ------------------------------------------------------------------------ */
+
+/* 8-bit pool: pages and rows as in the bf16 pool with one e4m3 code per value
+ * (row of 2*Hkv*head_dim bytes), beside it
+ *   scales  fp32 [pool_pages][2*Hkv][4]: one scale for every PA_SCALE_TOKENS
+ *           consecutive tokens (a block) of a page and every K head (first
+ *           Hkv) and V head; a value is code * scale.
+ * kv_append_rope_q8 writes powers of two in [2^-60, 2^120]. */
+#define PA_SCALE_TOKENS 16
+
+#define PA_ROPE_INTERLEAVED 1u  /* flags: pairs (2i, 2i+1); else (i, i + rot_dim/2) */
+
+/* Rotates the q and k of a step's new tokens by their positions, stores k and
+ * v in the pages and q in q_out: one launch.
+ *
+ * Token row r of the step belongs to the request b with cu_tokens[b] <= r <
+ * cu_tokens[b+1] and has position p = positions[b] + r - cu_tokens[b].  For
+ * i < rot_dim / 2 the pair (x1, x2) of every q and k head becomes
+ *     (x1 cos a - x2 sin a, x2 cos a + x1 sin a),   a = p * inv_freq[i],
+ * evaluated in FP32 with a reduced modulo 2 pi in 64-bit integers (any
+ * position keeps its angle to about 1e-7 for |inv_freq| <= 1); values behind
+ * rot_dim, and v, pass unchanged.  Results are rounded once, to bf16.
+ *
+ *   q, k, v    device bf16 [n_tokens][heads][head_dim] with the given strides
+ *              (elements) between tokens, so slices of one projection's output
+ *              serve; heads and values within a token are dense.
+ *   q_out      device bf16, its own token stride; q itself (same pointer and
+ *              stride) rotates in place.  q and q_out NULL: no q.  It may not
+ *              overlap q otherwise, nor k or v.
+ *   cu_tokens  device int32 [B+1], non-decreasing, cu_tokens[0] = 0; requests
+ *              may have no tokens; rows at and behind cu_tokens[B] (padding)
+ *              are neither read nor written.  NULL: one token per request,
+ *              n_tokens == B.
+ *   positions  device int32 [B], position of each request's first new token.
+ *   inv_freq   device fp32 [rot_dim / 2] (may be NULL when rot_dim is 0).
+ *   rot_dim    a multiple of 8 in [0, head_dim].
+ *   flags      0 or PA_ROPE_INTERLEAVED.
+ *   pool       device bf16 pages (layout above).  A token whose position or
+ *              page id lies outside the table or the pool is not stored and
+ *              ORs PA_STATUS_BAD_ROW into *status (if not NULL); its q is
+ *              rotated all the same.  Two tokens of a call may not share a
+ *              pool row, and no other call may use the rows meanwhile.
+ * Pointers to bf16 data 16-byte aligned, strides multiples of 8 elements.
+ * Supported head_dim: 64, 128, 256. */
+int kv_append_rope(const void* q, const void* k, const void* v, int64_t q_stride,
+                   int64_t k_stride, int64_t v_stride, void* q_out, int64_t q_out_stride,
+                   const int32_t* cu_tokens, const int32_t* positions, int n_tokens, int B,
+                   int n_q_heads, int n_kv_heads, int head_dim, const float* inv_freq,
+                   int rot_dim, unsigned flags, void* pool, int64_t pool_pages,
+                   const int32_t* page_table, int max_pages, int32_t* status,
+                   cudaStream_t stream);
+
+/* kv_append_rope into an 8-bit pool.  Arguments as above, except:
+ *   pool    device e4m3 pages, 16-byte aligned;  scales  device fp32, 16-byte
+ *           aligned (both as described at PA_SCALE_TOKENS).
+ * For every block and head that receives rows, with the rotated k (or v) in
+ * FP32: need = the smallest power of two s >= 2^-60 with |x| <= 448 s for all
+ * finite new values x.  If the request has older rows in the block (the first
+ * new position is not the block's first), the scale becomes max(old scale,
+ * need) and, when it grew, the older codes are multiplied by old / new and
+ * rounded to e4m3 again (exact unless a code becomes subnormal); a block with
+ * no older rows takes `need`, whatever its scale held.  New codes are x *
+ * (1 / scale) rounded to nearest even; a non-finite value is stored as NaN and
+ * sets no scale.  Rows of the block behind the new ones keep their codes.
+ * Requests of a call may not share a block that receives rows.
+ * Supported head_dim: 128, 256. */
+int kv_append_rope_q8(const void* q, const void* k, const void* v, int64_t q_stride,
+                      int64_t k_stride, int64_t v_stride, void* q_out, int64_t q_out_stride,
+                      const int32_t* cu_tokens, const int32_t* positions, int n_tokens, int B,
+                      int n_q_heads, int n_kv_heads, int head_dim, const float* inv_freq,
+                      int rot_dim, unsigned flags, void* pool, float* scales,
+                      int64_t pool_pages, const int32_t* page_table, int max_pages,
+                      int32_t* status, cudaStream_t stream);
+
+/* Rows of an 8-bit pool as bf16 values (code * scale, rounded to nearest
+ * even; exact for the scales kv_append_rope_q8 writes): out[r] = the row of
+ * token positions[b] + r - cu_tokens[b] of request b, rows and requests as in
+ * kv_append_rope.
+ *   out     device bf16 [n_tokens][2*n_kv_heads*head_dim] (a bf16 pool's row),
+ *           16-byte aligned; rows at and behind cu_tokens[B] are left alone.
+ * A position or page id outside the table or the pool gives a row of NaN and
+ * PA_STATUS_BAD_ROW.  Supported head_dim: 128, 256. */
+int kv_gather_q8(const void* pool, const float* scales, int64_t pool_pages,
+                 const int32_t* page_table, int max_pages, const int32_t* cu_tokens,
+                 const int32_t* positions, int n_tokens, int B, int n_kv_heads, int head_dim,
+                 void* out, int32_t* status, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Staging arena  ([KVE-bus], [KVE-lease], [SWS-queues], [SWS-lease])       */

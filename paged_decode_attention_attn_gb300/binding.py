@@ -32,7 +32,9 @@ PA_STATUS_BAD_ROW = 4
 PA_ARENA_RECORD_ONLY = 1
 PA_PAGE_EXACT, PA_PAGE_QUEUED, PA_PAGE_PUBLISHED, PA_PAGE_NOT_CONVERTIBLE = 0, 1, 2, 3
 PA_DECODE_KV_READY = 1
+PA_ROPE_INTERLEAVED = 1
 PAGE_TOKENS = 64
+SCALE_TOKENS = 16
 
 # Every symbol pagedattn.h declares.
 EXPORTED = [
@@ -41,7 +43,7 @@ EXPORTED = [
     "paged_decode_attn_lse_cuda_core", "paged_decode_attn_lse_noalloc",
     "paged_decode_attn_lse_append", "paged_decode_attn_test_stall",
     "paged_decode_attn_test_slice_wait", "lse_merge",
-    "kv_append_rows",
+    "kv_append_rows", "kv_append_rope", "kv_append_rope_q8", "kv_gather_q8",
     "kv_arena_create", "kv_arena_destroy", "kv_arena_drain", "kv_stage_layer",
     "kv_mark_attention_done", "kv_writeback_tail", "kv_load_resident", "kv_arena_get_stats",
     "kv_arena_fail_after", "kv_arena_call_log",
@@ -240,6 +242,14 @@ def _load():
     lib.lse_merge.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, vp]
     lib.kv_append_rows.restype = i32
     lib.kv_append_rows.argtypes = [vp, i64, vp, i32, vp, vp, i32, i32, vp, vp]
+    rope = [vp, vp, vp, i64, i64, i64, vp, i64, vp, vp, i32, i32, i32, i32, i32, vp, i32,
+            ctypes.c_uint, vp]
+    lib.kv_append_rope.restype = i32
+    lib.kv_append_rope.argtypes = rope + [i64, vp, i32, vp, vp]
+    lib.kv_append_rope_q8.restype = i32
+    lib.kv_append_rope_q8.argtypes = rope + [vp, i64, vp, i32, vp, vp]
+    lib.kv_gather_q8.restype = i32
+    lib.kv_gather_q8.argtypes = [vp, vp, i64, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp]
     lib.kv_arena_create.restype = i32
     lib.kv_arena_create.argtypes = [ctypes.POINTER(KvArenaDesc), ctypes.POINTER(vp)]
     for name in ("kv_arena_destroy", "kv_arena_drain"):
@@ -492,6 +502,146 @@ def kv_append_rows(pool, page_table, positions, rows, status=None, stream=None,
                               _dev(rows, torch.bfloat16, "rows"), B, row_elems * 2,
                               None if status is None else _dev(status, torch.int32, "status"),
                               _stream_handle(stream)))
+
+
+def _on(device, stream, call):
+    """Runs ``call(stream handle)`` with ``device`` current; ``stream`` None is
+    that device's current stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _on(device, stream, call)
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    elif stream.device != device:
+        raise ValueError(f"stream of {stream.device}, tensors on {device}")
+    _check(call(stream.cuda_stream))
+
+
+def _dev_on(device, t, dtype, name):
+    ptr = _dev(t, dtype, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the pool on {device}")
+    return ptr
+
+
+def _token_rows(device, t, name):
+    """Pointer and token stride of [tokens][heads][head_dim] activations whose
+    heads are dense within a token."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}, as the pool")
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be bfloat16 [tokens][heads][head_dim]")
+    st = t.stride()
+    if (st[2] != 1 and t.shape[2] > 1) or (st[1] != t.shape[2] and t.shape[1] > 1):
+        raise ValueError(f"{name} must be dense within a token")
+    # the stride of a single token is never used and torch keeps any value there
+    return t.data_ptr(), st[0] if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _pages(pool, scales, dtype):
+    """Device, kv row elements of a pool tensor [pages][64][row]."""
+    if not isinstance(pool, torch.Tensor) or pool.device.type != "cuda":
+        raise ValueError("pool must be a CUDA tensor")
+    if pool.dtype != dtype:
+        raise ValueError(f"pool must be {dtype}, got {pool.dtype}")
+    if pool.dim() != 3 or pool.shape[1] != PAGE_TOKENS or not pool.is_contiguous():
+        raise ValueError("pool must be contiguous [pages][64][2*Hkv*D]")
+    if scales is not None:
+        _dev_on(pool.device, scales, torch.float32, "scales")
+    return pool.device
+
+
+def _append_rope(fn, dtype, q, k, v, pool, scales, page_table, positions, inv_freq, q_out,
+                 cu_tokens, interleaved, status, stream):
+    dev = _pages(pool, scales, dtype)
+    k_ptr, k_st = _token_rows(dev, k, "k")
+    v_ptr, v_st = _token_rows(dev, v, "v")
+    n, n_kv, d = k.shape
+    if v.shape != k.shape or pool.shape[2] != 2 * n_kv * d:
+        raise ValueError("k and v must be [tokens][Hkv][D] and pool rows 2*Hkv*D")
+    if scales is not None and tuple(scales.shape) != (pool.shape[0], 2 * n_kv,
+                                                      PAGE_TOKENS // SCALE_TOKENS):
+        raise ValueError("scales must be [pages][2*Hkv][4]")
+    q_ptr = o_ptr = None
+    q_st = o_st = hq = 0
+    if q is not None:
+        if q_out is None:
+            raise ValueError("q_out is required with q (q itself rotates in place)")
+        q_ptr, q_st = _token_rows(dev, q, "q")
+        o_ptr, o_st = _token_rows(dev, q_out, "q_out")
+        hq = q.shape[1]
+        if q.shape[0] != n or q.shape[2] != d or q_out.shape != q.shape:
+            raise ValueError("q and q_out must be [tokens][Hq][D]")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    bn = page_table.shape[0]
+    if page_table.dim() != 2 or tuple(positions.shape) != (bn,):
+        raise ValueError("page_table must be [B][max_pages] and positions [B]")
+    if cu_tokens is not None and tuple(cu_tokens.shape) != (bn + 1,):
+        raise ValueError("cu_tokens must be [B + 1]")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    args = [q_ptr, k_ptr, v_ptr, q_st, k_st, v_st, o_ptr, o_st,
+            None if cu_tokens is None else _dev_on(dev, cu_tokens, torch.int32, "cu_tokens"),
+            _dev_on(dev, positions, torch.int32, "positions"), n, bn, hq, n_kv, d,
+            None if inv_freq is None else _dev_on(dev, inv_freq, torch.float32, "inv_freq"), rot,
+            PA_ROPE_INTERLEAVED if interleaved else 0, pool.data_ptr()]
+    if scales is not None:
+        args.append(scales.data_ptr())
+    args += [pool.shape[0], _dev_on(dev, page_table, torch.int32, "page_table"),
+             page_table.shape[1],
+             None if status is None else _dev_on(dev, status, torch.int32, "status")]
+    _on(dev, stream, lambda s: fn(*args, s))
+
+
+def kv_append_rope(q, k, v, pool, page_table, positions, inv_freq, q_out=None, cu_tokens=None,
+                   interleaved=False, status=None, stream=None):
+    """Rotate q [tokens][Hq][D] and k [tokens][Hkv][D] (bf16, any token stride)
+    by their positions, store k and v in the bf16 pool [pages][64][2*Hkv*D] and
+    q in q_out (q itself rotates in place; None, None: no q).  ``positions``
+    int32 [B]: position of each request's first new token; ``cu_tokens`` int32
+    [B+1]: each request's rows (None: one row per request); ``inv_freq`` fp32
+    [rot_dim/2], None: no rotation; ``interleaved``: pairs (2i, 2i+1) instead
+    of (i, i + rot_dim/2)."""
+    _append_rope(lib.kv_append_rope, torch.bfloat16, q, k, v, pool, None, page_table, positions,
+                 inv_freq, q_out, cu_tokens, interleaved, status, stream)
+
+
+def kv_append_rope_q8(q, k, v, pool, scales, page_table, positions, inv_freq, q_out=None,
+                      cu_tokens=None, interleaved=False, status=None, stream=None):
+    """kv_append_rope into an 8-bit pool: pool float8_e4m3fn
+    [pages][64][2*Hkv*D], scales fp32 [pages][2*Hkv][4] (one per 16 tokens and
+    head)."""
+    if scales is None:
+        raise ValueError("scales must be [pages][2*Hkv][4]")
+    _append_rope(lib.kv_append_rope_q8, torch.float8_e4m3fn, q, k, v, pool, scales, page_table,
+                 positions, inv_freq, q_out, cu_tokens, interleaved, status, stream)
+
+
+def kv_gather_q8(pool, scales, page_table, positions, cu_tokens, out, status=None, stream=None):
+    """Rows of an 8-bit pool as bf16 values: out [rows][2*Hkv*D]; row r is token
+    positions[b] + r - cu_tokens[b] of the request b that holds it (cu_tokens
+    None: one row per request)."""
+    if scales is None or scales.dim() != 3:
+        raise ValueError("scales must be [pages][2*Hkv][4]")
+    dev = _pages(pool, scales, torch.float8_e4m3fn)
+    heads = scales.shape[1]
+    if tuple(scales.shape) != (pool.shape[0], heads, PAGE_TOKENS // SCALE_TOKENS) or \
+            heads % 2 or heads == 0 or pool.shape[2] % heads:
+        raise ValueError("scales must be [pages][2*Hkv][4]")
+    if out.dim() != 2 or out.shape[1] != pool.shape[2]:
+        raise ValueError("out must be [rows][2*Hkv*D]")
+    bn = page_table.shape[0]
+    if page_table.dim() != 2 or tuple(positions.shape) != (bn,):
+        raise ValueError("page_table must be [B][max_pages] and positions [B]")
+    if cu_tokens is not None and tuple(cu_tokens.shape) != (bn + 1,):
+        raise ValueError("cu_tokens must be [B + 1]")
+    args = (pool.data_ptr(), scales.data_ptr(), pool.shape[0],
+            _dev_on(dev, page_table, torch.int32, "page_table"), page_table.shape[1],
+            None if cu_tokens is None else _dev_on(dev, cu_tokens, torch.int32, "cu_tokens"),
+            _dev_on(dev, positions, torch.int32, "positions"), out.shape[0], bn, heads // 2,
+            pool.shape[2] // heads, _dev_on(dev, out, torch.bfloat16, "out"),
+            None if status is None else _dev_on(dev, status, torch.int32, "status"))
+    _on(dev, stream, lambda s: lib.kv_gather_q8(*args, s))
 
 
 class Arena:
