@@ -17,11 +17,11 @@ FAKE = 1 << 20      # never dereferenced: every check below fails before a CUDA 
 
 def append(B, q8=False, **kw):
     a = dict(q=FAKE, k=FAKE, v=FAKE, q_stride=1024, k_stride=1024, v_stride=1024, q_out=FAKE,
-             q_out_stride=1024, cu=FAKE, positions=FAKE, n=4, B=2, hq=4, hkv=2, d=128, inv=FAKE,
+             q_out_stride=1024, cu=FAKE, positions=FAKE, n=4, batch=2, hq=4, hkv=2, d=128, inv=FAKE,
              rot=128, flags=0, pool=FAKE, scales=FAKE, pool_pages=4, table=FAKE, max_pages=4)
     a.update(kw)
     head = [a[x] for x in ("q", "k", "v", "q_stride", "k_stride", "v_stride", "q_out",
-                           "q_out_stride", "cu", "positions", "n", "B", "hq", "hkv", "d", "inv",
+                           "q_out_stride", "cu", "positions", "n", "batch", "hq", "hkv", "d", "inv",
                            "rot", "flags", "pool")]
     tail = [a["pool_pages"], a["table"], a["max_pages"], None, None]
     if q8:
@@ -31,7 +31,7 @@ def append(B, q8=False, **kw):
 
 @pytest.mark.parametrize("q8", [False, True])
 @pytest.mark.parametrize("kw,word", [
-    (dict(n=-1), "n_tokens"), (dict(B=-1), "n_tokens"), (dict(hkv=0), "n_kv_heads"),
+    (dict(n=-1), "n_tokens"), (dict(batch=-1), "n_tokens"), (dict(hkv=0), "n_kv_heads"),
     (dict(hq=0), "n_q_heads"), (dict(q=None), "q_out"), (dict(q_out=None), "q_out"),
     (dict(k=None), "null"), (dict(v=None), "null"), (dict(pool=None), "null"),
     (dict(positions=None), "null"), (dict(table=None), "null"), (dict(cu=None), "cu_tokens"),
@@ -61,7 +61,7 @@ def test_head_dims_that_are_not_built(B):
 
 def test_nothing_to_do_is_no_error(B):
     assert append(B, n=0) == B.PA_OK
-    assert append(B, True, B=0) == B.PA_OK
+    assert append(B, True, batch=0) == B.PA_OK
     assert B.lib.kv_gather_q8(0, 0, 0, 0, 0, 0, 0, 0, 3, 1, 128, 0, None, None) == B.PA_OK
 
 
