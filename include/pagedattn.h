@@ -395,6 +395,34 @@ int kv_gather_q8(const void* pool, const float* scales, int64_t pool_pages,
                  const int32_t* positions, int n_tokens, int B, int n_kv_heads, int head_dim,
                  void* out, int32_t* status, cudaStream_t stream);
 
+/* Workspace bytes paged_decode_attn_q8_lse needs (as
+ * paged_decode_attn_lse_workspace_bytes; 0 for an unsupported geometry). */
+size_t paged_decode_attn_q8_workspace_bytes(int B, int T, int n_q_heads, int n_kv_heads,
+                                            int head_dim);
+
+/* paged_decode_attn_lse over an 8-bit pool: the same definition with
+ * K_j, V_j = codes * scales (see PA_SCALE_TOKENS), the same tiles, status word,
+ * workspace rules and, with merged_out / merged_lse (both or neither), the same
+ * merge of every request's tiles in the same call as
+ * paged_decode_attn_lse_append.  Arguments as there, except:
+ *   pool    device e4m3 pages, 16-byte aligned.
+ *   scales  device fp32 [pool_pages][2*n_kv_heads][4], 16-byte aligned.  V
+ *           scales of the attended blocks must lie in [2^-100, 2^100] in
+ *           magnitude or be 0 (kv_append_rope_q8's do); a V scale above that,
+ *           or a NaN, makes the tile's output NaN.
+ * Codes of rows outside a tile may hold anything, NaN codes too; scales of
+ * blocks wholly outside the tiles are not used.
+ * Products run on the tensor cores in e4m3 with FP32 sums; q and the
+ * probabilities enter them as sums of several e4m3 parts, so results carry
+ * about an FP32 evaluation's error.
+ * Supported: head_dim 128 and 256, n_q_heads / n_kv_heads in 1..8. */
+int paged_decode_attn_q8_lse(const void* q, const void* pool, const float* scales,
+                             int64_t pool_pages, const int32_t* page_table, int max_pages,
+                             const int32_t* tiles, int B, int T, int n_q_heads, int n_kv_heads,
+                             int head_dim, float scale, float* out, float* lse,
+                             float* merged_out, float* merged_lse, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Staging arena  ([KVE-bus], [KVE-lease], [SWS-queues], [SWS-lease])       */
 /* ------------------------------------------------------------------------ */

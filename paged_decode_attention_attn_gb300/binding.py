@@ -44,6 +44,7 @@ EXPORTED = [
     "paged_decode_attn_lse_append", "paged_decode_attn_test_stall",
     "paged_decode_attn_test_slice_wait", "lse_merge",
     "kv_append_rows", "kv_append_rope", "kv_append_rope_q8", "kv_gather_q8",
+    "paged_decode_attn_q8_workspace_bytes", "paged_decode_attn_q8_lse",
     "kv_arena_create", "kv_arena_destroy", "kv_arena_drain", "kv_stage_layer",
     "kv_mark_attention_done", "kv_writeback_tail", "kv_load_resident", "kv_arena_get_stats",
     "kv_arena_fail_after", "kv_arena_call_log",
@@ -250,6 +251,11 @@ def _load():
     lib.kv_append_rope_q8.argtypes = rope + [vp, i64, vp, i32, vp, vp]
     lib.kv_gather_q8.restype = i32
     lib.kv_gather_q8.argtypes = [vp, vp, i64, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp]
+    lib.paged_decode_attn_q8_workspace_bytes.restype = sz
+    lib.paged_decode_attn_q8_workspace_bytes.argtypes = [i32] * 5
+    lib.paged_decode_attn_q8_lse.restype = i32
+    lib.paged_decode_attn_q8_lse.argtypes = [vp, vp, vp, i64, vp, i32, vp, i32, i32, i32, i32, i32,
+                                             ctypes.c_float, vp, vp, vp, vp, vp, sz, vp]
     lib.kv_arena_create.restype = i32
     lib.kv_arena_create.argtypes = [ctypes.POINTER(KvArenaDesc), ctypes.POINTER(vp)]
     for name in ("kv_arena_destroy", "kv_arena_drain"):
@@ -642,6 +648,48 @@ def kv_gather_q8(pool, scales, page_table, positions, cu_tokens, out, status=Non
             pool.shape[2] // heads, _dev_on(dev, out, torch.bfloat16, "out"),
             None if status is None else _dev_on(dev, status, torch.int32, "status"))
     _on(dev, stream, lambda s: lib.kv_gather_q8(*args, s))
+
+
+def alloc_workspace_q8(B, T, n_q_heads, n_kv_heads, head_dim, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace for paged_decode_attn_q8_lse."""
+    n = int(lib.paged_decode_attn_q8_workspace_bytes(B, T, n_q_heads, n_kv_heads, head_dim))
+    if n == 0:
+        raise PagedAttnError(PA_ERR_UNSUPPORTED, "geometry not supported")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def paged_decode_attn_q8_lse(q, pool, scales, page_table, tiles, scale, out, lse, workspace,
+                             merged_out=None, merged_lse=None, stream=None):
+    """paged_decode_attn_lse over an 8-bit pool: pool float8_e4m3fn
+    [pages][64][2*Hkv*D], scales fp32 [pages][2*Hkv][4]; q bf16 [B][Hq][D];
+    tiles host int32 [B][T][2]; out fp32 [B][T][Hq][D], lse fp32 [B][T][Hq];
+    ``merged_out`` [B][Hq][D] / ``merged_lse`` [B][Hq] receive the merge of
+    every request's tiles in the same call."""
+    dev = _pages(pool, scales, torch.float8_e4m3fn)
+    Bn, Hq, D = q.shape
+    n_kv = pool.shape[2] // (2 * D)
+    arr, tiles_ptr = _host_tiles(tiles)
+    if arr.ndim != 3 or arr.shape[0] != Bn or arr.shape[2] != 2:
+        raise ValueError("tiles must be [B][T][2]")
+    T = arr.shape[1]
+    if pool.shape[2] != 2 * n_kv * D or \
+            tuple(scales.shape) != (pool.shape[0], 2 * n_kv, PAGE_TOKENS // SCALE_TOKENS):
+        raise ValueError("pool must be [pages][64][2*Hkv*D] and scales [pages][2*Hkv][4]")
+    if page_table.dim() != 2 or page_table.shape[0] != Bn:
+        raise ValueError("page_table must be [B][max_pages]")
+    if tuple(out.shape) != (Bn, T, Hq, D) or tuple(lse.shape) != (Bn, T, Hq):
+        raise ValueError("out must be [B][T][Hq][D] and lse [B][T][Hq]")
+    if merged_out is not None and (merged_lse is None or tuple(merged_out.shape) != (Bn, Hq, D)
+                                   or tuple(merged_lse.shape) != (Bn, Hq)):
+        raise ValueError("merged_out must be [B][Hq][D] and merged_lse [B][Hq]")
+    args = (_dev_on(dev, q, torch.bfloat16, "q"), pool.data_ptr(), scales.data_ptr(),
+            pool.shape[0], _dev_on(dev, page_table, torch.int32, "page_table"),
+            page_table.shape[1], tiles_ptr, Bn, T, Hq, n_kv, D, float(scale),
+            _dev_on(dev, out, torch.float32, "out"), _dev_on(dev, lse, torch.float32, "lse"),
+            None if merged_out is None else _dev_on(dev, merged_out, torch.float32, "merged_out"),
+            None if merged_lse is None else _dev_on(dev, merged_lse, torch.float32, "merged_lse"),
+            _dev_on(dev, workspace, torch.uint8, "workspace"), workspace.numel())
+    _on(dev, stream, lambda s: lib.paged_decode_attn_q8_lse(*args, s))
 
 
 class Arena:

@@ -1,0 +1,304 @@
+"""Decode attention over the 8-bit pool against the float64 oracle, which
+attends the values that codes and scales stand for.
+
+Tolerances.  With A = scale max_j sum_d |q_d k_jd| over a row, an FP32 score
+(sums over head_dim, the scaling) is within 8 steps of 2^-24 of A, so a
+probability is within e = 2^-21 A + 2^-18 relative, the second term for the
+exponential (2^-22) and for the parts a probability is held in: 2^-16 at worst
+for one key, a quarter of that on the root mean square of several.  The output
+is then within (e + 2^-16) max |V| (a row may hang on one key), the log-sum-exp
+within e + 2^-22 |lse|.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from oracle import rope_q8 as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def B():
+    from paged_decode_attention_attn_gb300 import build
+    build.build()
+    from paged_decode_attention_attn_gb300 import binding
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return binding
+
+
+class Case:
+    def __init__(self, lengths, tiles=None, hq=24, hkv=4, d=256, seed=0, spare=3, scale=None,
+                 q_scale=1.0, v_exp=(-8, -5), k_exp=(-8, -5), max_pages=None):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        self.lengths, self.hq, self.hkv, self.d = list(lengths), hq, hkv, d
+        self.scale = d ** -0.5 if scale is None else scale
+        n_pages = [-(-n // 64) for n in lengths]
+        self.pages = sum(n_pages) + spare
+        perm = rng.permutation(self.pages)
+        self.table = np.zeros((len(lengths), max_pages or max(1, max(n_pages))), np.int32)
+        at = 0
+        for b, n in enumerate(n_pages):
+            self.table[b, :n] = perm[at:at + n]
+            at += n
+        tiles = [[(0, n)] for n in lengths] if tiles is None else tiles
+        T = max(len(t) for t in tiles)
+        self.tiles = np.zeros((len(lengths), T, 2), np.int32)
+        for b, tl in enumerate(tiles):
+            for i, r in enumerate(tl):
+                self.tiles[b, i] = r
+        self.q = (torch.randn(len(lengths), hq, d, generator=g, device=DEV) * q_scale).bfloat16()
+        x = torch.randn(self.pages, 64, 2 * hkv * d, generator=g, device=DEV) * 64
+        self.pool = x.to(E4M3)
+        ek = torch.randint(*k_exp, (self.pages, hkv, 4), generator=g, device=DEV)
+        ev = torch.randint(*v_exp, (self.pages, hkv, 4), generator=g, device=DEV)
+        self.scales = torch.exp2(torch.cat([ek, ev], 1).float())
+        # everything no request names, and the rows behind each last token: NaN
+        raw = self.pool.view(torch.uint8)
+        raw[torch.from_numpy(perm[at:].copy()).to(DEV)] = 0x7F
+        for b, n in enumerate(lengths):
+            if n % 64:
+                raw[int(self.table[b, n // 64]), n % 64:] = 0xFF
+        self.table_dev = torch.from_numpy(self.table).to(DEV)
+        shape = (len(lengths), T, hq)
+        self.out = torch.full(shape + (d,), 7.0, device=DEV)
+        self.lse = torch.full(shape, 7.0, device=DEV)
+        self.merged = torch.full((len(lengths), hq, d), 7.0, device=DEV)
+        self.merged_lse = torch.full((len(lengths), hq), 7.0, device=DEV)
+        self.ws = None
+
+    def run(self, B, merged=True, stream=None):
+        if self.ws is None:
+            self.ws = B.alloc_workspace_q8(len(self.lengths), self.tiles.shape[1], self.hq,
+                                           self.hkv, self.d)
+            torch.cuda.synchronize()
+        B.paged_decode_attn_q8_lse(
+            self.q, self.pool, self.scales, self.table_dev, self.tiles, self.scale, self.out,
+            self.lse, self.ws, merged_out=self.merged if merged else None,
+            merged_lse=self.merged_lse if merged else None, stream=stream)
+        torch.cuda.synchronize()
+        return int(self.ws[:4].view(torch.int32).item())
+
+    def history(self, b):
+        n = self.lengths[b]
+        pages = torch.from_numpy(self.table[b, :-(-n // 64)].astype(np.int64)).to(DEV)
+        codes = self.pool.view(torch.uint8)[pages].cpu().numpy().reshape(-1, 2 * self.hkv, self.d)
+        scales = self.scales[pages].double().cpu().numpy().transpose(0, 2, 1)
+        kv = R.pool_values(codes, scales.reshape(-1, 2 * self.hkv))[:n]
+        return kv[:, :self.hkv], kv[:, self.hkv:]
+
+    def check(self, requests=None):
+        for b in range(len(self.lengths)) if requests is None else requests:
+            K, V = self.history(b)
+            q = self.q[b].double().cpu().numpy()
+            outs, lses = oracle.tile_attention(q, K, V, self.tiles[b], self.scale)
+            want = list(zip(outs, lses)) + [oracle.lse_merge(outs, lses)]
+            got = [(self.out[b, t], self.lse[b, t]) for t in range(self.tiles.shape[1])]
+            got.append((self.merged[b], self.merged_lse[b]))
+            G = self.hq // self.hkv
+            for i, ((o, l), (wo, wl)) in enumerate(zip(got, want)):
+                o, l = o.double().cpu().numpy(), l.double().cpu().numpy()
+                what = f"request {b} tile {i}"
+                if np.all(wl == -np.inf):
+                    assert np.all(o == 0) and np.all(l == -np.inf), what
+                    continue
+                for h in range(self.hq):
+                    if not np.isfinite(wl[h]):
+                        assert np.isnan(o[h]).all() and np.isnan(l[h]), what
+                        continue
+                    A = self.scale * np.max(np.abs(K[:, h // G]) @ np.abs(q[h]))
+                    e = 2.0 ** -21 * A + 2.0 ** -18
+                    vmax = np.max(np.abs(V[:, h // G]))
+                    err = np.max(np.abs(o[h] - wo[h]))
+                    assert err <= (e + 2.0 ** -16) * vmax, (what, h, err, vmax, A)
+                    assert abs(l[h] - wl[h]) <= e + 2.0 ** -22 * abs(wl[h]), (what, h)
+
+
+LENGTHS = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 191, 192, 193, 1000]
+
+
+@pytest.mark.parametrize("geo", [(24, 4, 256), (32, 8, 128), (7, 1, 256), (8, 8, 128), (20, 5, 128),
+                                 (16, 2, 256)])
+def test_lengths_around_blocks_pages_and_steps(B, geo):
+    c = Case(LENGTHS, hq=geo[0], hkv=geo[1], d=geo[2], seed=geo[0])
+    assert c.run(B) == 0
+    c.check()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_tiles_that_start_and_end_anywhere(B, d):
+    tiles = [[(0, 1), (1, 700), (699, 700), (3, 3)], [(0, 0)], [(63, 65), (64, 128), (0, 64)],
+             [(5, 2001), (130, 131), (1990, 2100), (0, 2100)], [(0, 0), (17, 18)]]
+    c = Case([700, 0, 200, 2100, 40], tiles, hq=16, hkv=4, d=d, seed=3)
+    assert c.run(B) == 0
+    c.check()
+
+
+@pytest.mark.parametrize("lengths,tile,geo", [
+    ([40000], None, (24, 4, 256)), ([30011], 4096, (32, 8, 128)),
+    ([9000, 1, 20000, 12345, 64], 8192, (24, 4, 256)), ([5000] * 3, None, (8, 1, 128))])
+def test_long_histories_split_over_many_ctas(B, lengths, tile, geo):
+    tiles = None if tile is None else [[(s, min(n, s + tile)) for s in range(0, n, tile)]
+                                       for n in lengths]
+    c = Case(lengths, tiles, hq=geo[0], hkv=geo[1], d=geo[2], seed=len(lengths))
+    assert c.run(B) == 0
+    c.check()
+    first = [t.clone() for t in (c.out, c.lse, c.merged, c.merged_lse)]
+    for _ in range(3):                                # the workspace is ready for the next call
+        assert c.run(B) == 0
+        for a, b in zip(first, (c.out, c.lse, c.merged, c.merged_lse)):
+            assert torch.equal(a, b)
+
+
+def test_many_requests_and_units(B):
+    rng = np.random.default_rng(5)
+    lengths = [int(n) for n in rng.integers(1, 500, 301)]
+    c = Case(lengths, [[(0, n // 2), (n // 2, n)] for n in lengths], hq=16, hkv=4, d=128, seed=6)
+    assert c.run(B) == 0
+    c.check(requests=list(range(0, 301, 13)) + [300])
+
+
+def test_without_merge_and_with_one_tile(B):
+    c = Case([300, 70], hq=8, hkv=2, d=128, seed=8)
+    assert c.run(B, merged=False) == 0
+    assert torch.all(c.merged == 7.0) and torch.all(c.merged_lse == 7.0)
+    c.run(B)
+    assert torch.equal(c.merged, c.out[:, 0]) and torch.equal(c.merged_lse, c.lse[:, 0])
+
+
+@pytest.mark.parametrize("q_scale,v_exp,k_exp", [
+    (8.0, (-8, -5), (-5, -2)),          # scores in the hundreds: one key dominates
+    (1.0, (-50, 40), (-8, -5)),         # V scales far apart between blocks
+    (1e-3, (-60, -59), (-60, -59)),     # the smallest scales
+    (1.0, (95, 100), (-8, -5)), (2.0 ** -60, (-8, -5), (50, 56))])
+def test_wide_ranges_of_scales_and_scores(B, q_scale, v_exp, k_exp):
+    c = Case([3, 500, 1333], hq=12, hkv=2, d=256, seed=11, q_scale=q_scale, v_exp=v_exp,
+             k_exp=k_exp)
+    assert c.run(B) == 0
+    c.check()
+
+
+def test_growing_scores_move_the_running_maximum(B):
+    """Keys whose scores rise through the history, so the maximum moves in every
+    step, and fall again."""
+    c = Case([4000], hq=6, hkv=1, d=128, seed=12)
+    up = torch.linspace(-12, -1, 4 * c.pages, device=DEV).round()
+    order = torch.from_numpy(c.table[0].astype(np.int64)).to(DEV)
+    c.scales[order, 0] = torch.exp2(up[:4 * len(order)].view(-1, 4))
+    assert c.run(B) == 0
+    c.check()
+
+
+def test_q_with_a_wide_spread_of_magnitudes(B):
+    c = Case([777], hq=8, hkv=2, d=256, seed=13)
+    c.q *= torch.exp2(torch.randint(-20, 1, c.q.shape, device=DEV).float()).bfloat16()
+    c.q[0, 3] = 0                                        # a row of zeros: plain averages
+    c.q[0, 4] *= 2.0 ** 20
+    assert c.run(B) == 0
+    c.check()
+
+
+def test_scales_that_are_no_powers_of_two(B):
+    c = Case([500, 64], hq=8, hkv=2, d=128, seed=14)
+    c.scales *= 1 + torch.rand_like(c.scales)
+    c.scales[int(c.table[0, 2]), 2:, 1] = 0.0            # V blocks of zeros
+    c.scales[int(c.table[0, 3]), :2, 2] = 0.0
+    assert c.run(B) == 0
+    c.check()
+
+
+def test_nan_codes_and_scales_inside_a_tile_reach_that_tile_alone(B):
+    c = Case([300, 300, 300], [[(0, 150), (150, 300)]] * 3, hq=8, hkv=2, d=128, seed=15)
+    raw = c.pool.view(torch.uint8)
+    raw[int(c.table[0, 0]), 5, 0] = 0x7F                 # K of kv head 0, tile 0
+    raw[int(c.table[1, 4]), 1, 128 * 3 + 7] = 0xFF       # V of kv head 1, tile 1, dim 7
+    c.scales[int(c.table[2, 1]), 2, 0] = float("nan")    # V scale of kv head 0, tile 0
+    assert c.run(B) == 0
+    o, l = c.out, c.lse
+    assert o[0, 0, :4].isnan().all() and o[0, 0, 4:].isfinite().all() and o[0, 1].isfinite().all()
+    assert o[1, 1, 4:, 7].isnan().all() and o[1, 1, :4].isfinite().all() and o[1, 0].isfinite().all()
+    rest = torch.ones(128, dtype=torch.bool, device=DEV)
+    rest[7] = False
+    assert o[1, 1, 4:][:, rest].isfinite().all() and l[1].isfinite().all()
+    assert o[2, 0, :4].isnan().all() and o[2, 0, 4:].isfinite().all() and o[2, 1].isfinite().all()
+
+
+def test_bad_page_ids_are_reported_and_never_read(B):
+    c = Case([200, 200], hq=8, hkv=2, d=256, seed=16)
+    good = Case([200, 200], hq=8, hkv=2, d=256, seed=16)
+    assert good.run(B) == 0
+    c.table_dev[1, 1] = c.pages
+    c.table_dev[1, 2] = -7
+    assert c.run(B) == B.PA_STATUS_BAD_PAGE
+    assert c.out[1].isnan().all() and c.lse[1].isnan().all() and c.merged[1].isnan().all()
+    assert torch.equal(c.out[0], good.out[0]) and torch.equal(c.merged[0], good.merged[0])
+
+
+def test_another_stream_and_a_captured_graph(B):
+    c = Case([3000, 17, 500], [[(0, 2000), (2000, 3000)], [(0, 17)], [(0, 500)]], seed=17)
+    assert c.run(B) == 0
+    want = [t.clone() for t in (c.out, c.lse, c.merged, c.merged_lse)]
+    side = torch.cuda.Stream()
+    assert c.run(B, stream=side) == 0
+    assert all(torch.equal(a, b) for a, b in zip(want, (c.out, c.lse, c.merged, c.merged_lse)))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.paged_decode_attn_q8_lse(c.q, c.pool, c.scales, c.table_dev, c.tiles, c.scale, c.out,
+                                   c.lse, c.ws, merged_out=c.merged, merged_lse=c.merged_lse)
+    for _ in range(3):
+        c.out.zero_(), c.merged.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, (c.out, c.lse, c.merged, c.merged_lse)))
+    c.q.neg_()
+    graph.replay()
+    torch.cuda.synchronize()
+    c.check()
+
+
+def test_pages_may_sit_anywhere(B):
+    """Two pools that differ only in where the pages lie give the same bits."""
+    a = Case([1500, 700], hq=24, hkv=4, d=256, seed=18, spare=20)
+    assert a.run(B) == 0
+    want = a.out.clone()
+    perm = torch.randperm(a.pages, device=DEV)
+    raw = torch.empty_like(a.pool.view(torch.uint8))
+    raw[perm] = a.pool.view(torch.uint8)
+    scales = torch.empty_like(a.scales)
+    scales[perm] = a.scales
+    a.pool, a.scales = raw.view(E4M3), scales
+    a.table_dev = perm[a.table_dev.long()].int()
+    assert a.run(B) == 0
+    assert torch.equal(a.out, want)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_a_step_of_appends_and_attention(B, d):
+    """Prompt appended in chunks, then decode steps of one token each, every one
+    attended: the cache and the outputs match the oracle's at each step."""
+    hq, hkv, inv = 8, 2, 10000.0 ** (-np.arange(d // 2) / (d // 2))
+    inv = torch.from_numpy(inv.astype(np.float32)).to(DEV)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    c = Case([256, 256], hq=hq, hkv=hkv, d=d, seed=19)
+    at = [0, 0]
+    for new in ([100, 37], [20, 0], [1, 1], [1, 1], [1, 1]):
+        n = sum(new)
+        qkv = torch.randn(n, hq + 2 * hkv, d, generator=g, device=DEV).bfloat16()
+        q = torch.empty(n, hq, d, device=DEV, dtype=torch.bfloat16)
+        cu = torch.tensor([0, new[0], n], dtype=torch.int32, device=DEV)
+        pos = torch.tensor(at, dtype=torch.int32, device=DEV)
+        B.kv_append_rope_q8(qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], c.pool, c.scales,
+                            c.table_dev, pos, inv, q, cu_tokens=cu)
+        at = [a + m for a, m in zip(at, new)]
+        if min(new) == 0:
+            continue
+        c.q = torch.stack([q[new[0] - 1], q[n - 1]])     # each request's newest token
+        c.lengths = list(at)
+        c.tiles = np.array([[(0, a)] for a in at], np.int32)
+        assert c.run(B) == 0
+        c.check()
