@@ -58,7 +58,8 @@ L2_BYTES = 129e6
 FALLBACK_HBM_GBS = 6800.0
 # the decode kernel's translation unit: the .cu file and the headers it includes
 KERNEL_SOURCES = [os.path.join(ROOT, "paged_decode_attention_attn_gb300", "csrc", f)
-                  for f in ("decode_attn.cu", "merge_row.cuh", "ptx.cuh", "common.h")] + [
+                  for f in ("decode_attn.cu", "split_units.cuh", "merge_row.cuh", "ptx.cuh",
+                             "common.h")] + [
                       os.path.join(ROOT, "include", "pagedattn.h")]
 
 

@@ -49,13 +49,14 @@
 #include "common.h"
 #include "merge_row.cuh"
 #include "ptx.cuh"
+#include "split_units.cuh"
 
 namespace pa {
 namespace decode {
 
-constexpr int kPage = PA_PAGE_TOKENS;                    // tokens per page
+using namespace split;
+
 constexpr int kD = 256;                                  // head_dim
-constexpr int kMaxG = 8;                                 // query heads per kv head
 constexpr int kStages = 3;
 constexpr int kGroups = 4;                               // 16-token groups per page
 constexpr int kBoxCols = 64;                             // 128 B swizzle span
@@ -71,55 +72,12 @@ constexpr int kSmemBar = kSmemXML + kXMLBytes;
 constexpr int kSmemMisc = kSmemBar + 2 * kStages * 8;
 constexpr int kSmemUsed = kSmemMisc + 64;
 constexpr int kSmemAlloc = kSmemUsed + 1024;             // slack to align to 1 KiB
-constexpr int kMaxUnitsLarge = 1024;
-constexpr int kMaxUnitsSmall = 64;
 constexpr int kWidePages = 32;     // pages per SM from which a launch leaves SMs idle
 constexpr int kWideGridPct = 90;   // share of the SMs such a launch runs on
 constexpr int kSegmentCharge = 6;  // pages charged per segment when CTAs' shares are cut (measured: 3-8 best)
 constexpr uint64_t kWaitLimitNs = 2000000000ull;         // 2 s per wait
-// A split unit's merge reads up to kMaxPartsPerLane partials per lane of a
-// 32-lane team, which bounds the CTAs a unit may span and so the grid.
-constexpr int kMaxPartsPerLane = 5;
-constexpr int kMaxGrid = 32 * kMaxPartsPerLane;
-// How long a CTA that has stored its partial waits without seeing another
-// CTA of the unit arrive before it leaves its share of the merge to the
-// unit's last CTA.  The CTAs of a launch finish within ~25 us of each other
-// (per-SM streaming speeds differ by up to ~10% over a long launch), with
-// arrivals every few hundred ns; the limit matters only when some of them
-// cannot be resident at the same time (other work holds SMs), where waiting
-// longer would only delay them.
-constexpr uint64_t kSliceWaitNs = 50000ull;
-constexpr size_t kStatusBytes = 256;
-// A split unit's outputs are merged in at most this many slices, one per
-// waiting CTA: enough to spread the partials' loads, few enough that most of
-// a widely split unit's CTAs leave at once (their SMs then take the next
-// launch's first page loads).
-constexpr int kMaxSlices = 16;
-// Per unit: a 64-bit arrival word (count | leavers << 16 | generation << 32).
-constexpr size_t kCounterBytes = 8 * kMaxUnitsLarge;
-constexpr size_t kPartOBytes = size_t(kMaxG) * kD * 4;   // per partial slot
-constexpr size_t kPartMLBytes = size_t(kMaxG) * 2 * 4;
-constexpr float kLn2Hi = 0.693145751953125f;        // ln 2, high bits (exact products)
-constexpr float kLn2Lo = 1.428606765330187045e-06f; // ln 2 - kLn2Hi
 constexpr float kLog2e = 1.44269504088896341f;
-// The running softmax reference is kept on multiples of kRefStep (log2 units):
-// rescales and the weights between partials are then exact powers of two, and
-// every probability is the same number (up to an exact power of two) however
-// the tokens are split into tiles, chunks and warps.
-constexpr float kRefStep = 8.0f;
-
 static_assert(kSmemAlloc <= 232448, "shared memory budget");
-static_assert(kMaxSlices <= kMaxGrid - 1, "slices per split unit");
-
-struct Unit {
-  int32_t bt_g;        // (b * T + t) * Hkv + g
-  int32_t tok_start;
-  int32_t tok_end;
-  int32_t page_first;  // flattened index of the unit's first page in this launch
-  int32_t part_base;   // first partial slot (units covered by several CTAs)
-  int32_t n_parts;     // CTAs covering the unit
-  int32_t pair_total;  // completions the (request, kv head) tile counter reaches (fused merge)
-};
 
 template <int kMaxUnits>
 struct Params {
@@ -170,20 +128,6 @@ struct Params {
 // Kernel parameters travel in the 32 KiB parameter space.
 static_assert(sizeof(Params<kMaxUnitsLarge>) <= 32764, "kernel parameters too large");
 
-// Slices a unit split over n >= 2 CTAs is merged in: half its CTAs wait and
-// merge, the other half leave at once (their SMs take the next launch's first
-// page loads).  Measured per launch against n - 1 slices (both capped at 16),
-// one box: 4 x 31,744 tokens (n ~ 9) 77.76 -> 77.05 us, 2 x 32,768 (n ~ 19)
-// 44.18 -> 43.37 us, 1 x 32,768 (n ~ 38) and 1 x 262,144 unchanged; a third
-// of them cost 1 x 32,768 0.3 us, two thirds gained half as much.
-__host__ __device__ __forceinline__ int split_slices(int n) {
-  return n / 2 < kMaxSlices ? n / 2 : kMaxSlices;
-}
-
-__host__ __device__ __forceinline__ int unit_pages(int tok_start, int tok_end) {
-  return tok_end > tok_start ? (tok_end + kPage - 1) / kPage - tok_start / kPage : 0;
-}
-
 // CTAs of a launch of `total` flattened pages on a device of `sms` SMs.  A
 // launch of at least kWidePages pages per SM runs on kWideGridPct percent of
 // the SMs: with HBM saturated, fewer, longer streams finish sooner.  Measured
@@ -206,51 +150,6 @@ __host__ __forceinline__ int launch_grid(long long total, int sms, int n_kv_head
                                                   : (int)std::min<long long>(sms, total);
   if (grid >= n_kv_heads) grid -= grid % n_kv_heads;
   return grid;
-}
-
-// CTA whose page range [k P / grid, (k+1) P / grid) holds flattened page p.
-__host__ __device__ __forceinline__ int cta_of(long long p, long long total, int grid) {
-  return static_cast<int>(((p + 1) * grid - 1) / total);
-}
-
-template <int N>
-__device__ __forceinline__ int first_unit(const Params<N>& p, long long start) {
-  int lo = 0, hi = p.n_units - 1, ans = 0;
-  while (lo <= hi) {
-    const int mid = (lo + hi) >> 1;
-    if (p.units[mid].page_first <= start) {
-      ans = mid;
-      lo = mid + 1;
-    } else {
-      hi = mid - 1;
-    }
-  }
-  return ans;
-}
-
-// ln-domain LSE of a reference m (log2 units, a multiple of kRefStep) and a
-// sum l > 0: (m + e) ln 2 + ln f with l = f 2^e, f in [0.5, 1).  m + e is an
-// exact small integer, its product with the high part of ln 2 (a Cody-Waite
-// split) is exact, and the small terms go into the last addition, so the
-// result carries about one fp32 rounding, as a double evaluation rounded to
-// fp32 would -- without FP64 arithmetic, which is slow on this part (a double
-// log per row had cost microseconds of every launch's tail).
-__device__ __forceinline__ float lse_of(float m, float l) {
-  if (m == -INFINITY || !(l > 0.f)) return m * kLn2Hi + logf(l);   // -inf / degenerate
-  int e;
-  const float f = frexpf(l, &e);
-  const float t = m + static_cast<float>(e);
-  return t * kLn2Hi + fmaf(t, kLn2Lo, logf(f));
-}
-
-__device__ __forceinline__ float ref_ceil(float x) {
-  return ceilf(x * (1.0f / kRefStep)) * kRefStep;
-}
-
-// Weight of a partial whose reference is m relative to the common reference
-// big_m >= m (both multiples of kRefStep): exactly 2^(m - big_m), 0 for -inf.
-__device__ __forceinline__ float ref_weight(float m, float big_m) {
-  return (m == -INFINITY) ? 0.f : ptx::pow2i(static_cast<int>(m - big_m));
 }
 
 struct Shared {
@@ -323,151 +222,6 @@ struct FmaState {
   float m[kMaxG];
   float l[kMaxG];
 };
-
-// Called by every consumer thread once it has stored `done` parts of the
-// tile outputs of (request b, kv head g): a whole unsplit (or empty) unit
-// counts 1, a slice of a split unit 1.  With the fused merge, the CTA whose
-// parts complete the pair's count (`total`, over its T tiles) merges the T
-// tiles for the G query heads of g with the merge kernel's own row routine
-// (same bits as lse_merge over those partials), then resets the counter for
-// the next call.
-template <int kMaxUnits, int kConsumers, int kConsumerWarps>
-__device__ __forceinline__ void finish_unit(const Params<kMaxUnits>& p, const Shared& sh, int b,
-                                            int g, int ct, int warp, int lane, int done,
-                                            int total) {
-  if (p.m_out == nullptr) return;
-  ptx::named_barrier(1, kConsumers);       // this CTA's outputs are all stored
-  if (ct == 0) {
-    const int prev = ptx::atomic_add_acq_rel_gpu(p.req_counters + b * p.Hkv + g, done);
-    *sh.fin_flag = (prev + done == total) ? 1 : 0;
-  }
-  ptx::named_barrier(1, kConsumers);
-  if (*sh.fin_flag) {
-    for (int r = warp; r < p.G; r += kConsumerWarps) {
-      const int h = g * p.G + r;
-      mergerow::merge_row<true>(p.out, p.lse, b * p.T, p.T, p.Hq, h, kD,
-                                p.m_out + ((size_t)b * p.Hq + h) * kD,
-                                p.m_lse + (size_t)b * p.Hq + h, lane);
-    }
-    if (ct == 0) p.req_counters[b * p.Hkv + g] = 0;
-  }
-  ptx::named_barrier(1, kConsumers);
-}
-
-// Merges output float4s [o_lo, o_hi) of a split unit (o = row * kD/4 + float4
-// column) from its n partials (slots part_base ..): the unit's tile output and,
-// at column 0, its LSE.  The same merge rule as the tile merge: common
-// reference = max partial reference, weights exactly 2^(m_c - max), output =
-// weighted sum / summed weights.  Each output is taken by a team of t lanes
-// (t a power of two, as large as one pass over the outputs allows); lane j
-// adds partials j, j + t, ... in that order, and the team adds its lanes'
-// sums by a butterfly.  The arithmetic depends only on n and the range, never
-// on which CTA runs it, so slices merged by different CTAs, or twice, give
-// the same bits.  All of a lane's loads are issued before its arithmetic.
-template <int kMaxUnits, int kConsumers>
-__device__ __forceinline__ void merge_split_slice(const Params<kMaxUnits>& p, int part_base, int n,
-                                                  int o_lo, int o_hi, size_t orow0, int ct) {
-  constexpr int kVec = kD / 4;
-  const int len = o_hi - o_lo;
-  int t = 32;
-  while (t > 1 && kConsumers / t < len && (n + t / 2 - 1) / (t / 2) <= kMaxPartsPerLane) t >>= 1;
-  const int n_teams = kConsumers / t;
-  const int j = ct & (t - 1);
-  const int team = ct / t;
-  const float2* pml = reinterpret_cast<const float2*>(p.part_ml) + (size_t)part_base * kMaxG;
-  const float4* po = reinterpret_cast<const float4*>(p.part_o) + (size_t)part_base * kMaxG * kVec;
-  for (int base = o_lo; base < o_hi; base += n_teams) {
-    const int o = base + team;
-    const bool have = o < o_hi;
-    const int row = have ? o / kVec : 0;
-    const int dv = have ? o - row * kVec : 0;
-    float2 ml[kMaxPartsPerLane];
-    float4 v[kMaxPartsPerLane];
-#pragma unroll
-    for (int k = 0; k < kMaxPartsPerLane; ++k) {
-      const int c = j + k * t;
-      if (have && c < n) {
-        ml[k] = __ldcg(pml + (size_t)c * kMaxG + row);
-        v[k] = __ldcg(po + ((size_t)c * kMaxG + row) * kVec + dv);
-      } else {
-        ml[k] = make_float2(-INFINITY, 0.f);
-        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-    }
-    float big_m = -INFINITY;
-    int nan = 0;
-#pragma unroll
-    for (int k = 0; k < kMaxPartsPerLane; ++k) {
-      big_m = fmaxf(big_m, ml[k].x);
-      nan |= (ml[k].x != ml[k].x);
-    }
-    for (int off = t >> 1; off > 0; off >>= 1) {
-      big_m = fmaxf(big_m, __shfl_xor_sync(0xffffffffu, big_m, off));
-      nan |= __shfl_xor_sync(0xffffffffu, nan, off);
-    }
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < kMaxPartsPerLane; ++k) {
-      const float a = ref_weight(ml[k].x, big_m);
-      l = fmaf(a, ml[k].y, l);
-      acc.x = fmaf(a, v[k].x, acc.x);
-      acc.y = fmaf(a, v[k].y, acc.y);
-      acc.z = fmaf(a, v[k].z, acc.z);
-      acc.w = fmaf(a, v[k].w, acc.w);
-    }
-    for (int off = t >> 1; off > 0; off >>= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, off);
-      acc.x += __shfl_xor_sync(0xffffffffu, acc.x, off);
-      acc.y += __shfl_xor_sync(0xffffffffu, acc.y, off);
-      acc.z += __shfl_xor_sync(0xffffffffu, acc.z, off);
-      acc.w += __shfl_xor_sync(0xffffffffu, acc.w, off);
-    }
-    if (have && j == 0) {
-      const size_t orow = orow0 + row;
-      const float qnan = __int_as_float(0x7fc00000);
-      reinterpret_cast<float4*>(p.out + orow * kD)[dv] =
-          nan ? make_float4(qnan, qnan, qnan, qnan)
-              : make_float4(acc.x / l, acc.y / l, acc.z / l, acc.w / l);
-      if (dv == 0) p.lse[orow] = nan ? qnan : lse_of(big_m, l);
-    }
-  }
-}
-
-// Thread 0 of a CTA that has arrived at split unit `arrival` in generation
-// `gen`, with this unit's segment as its last: waits until every CTA of the
-// unit has arrived (the count reaches n, or the last CTA has already opened
-// the next generation), so every partial is stored and visible.  If no other
-// CTA of the unit arrives for slice_wait_ns while some have not, it records
-// itself as a leaver (the last CTA then merges every slice) and returns false.
-__device__ __forceinline__ bool wait_unit_complete(unsigned long long* arrival, unsigned gen,
-                                                   int n, uint64_t slice_wait_ns,
-                                                   uint64_t wait_limit_ns, int32_t* status) {
-  const uint64_t t0 = ptx::globaltimer_ns();
-  uint64_t t_seen = t0;
-  int seen = -1;
-  while (true) {
-    // Acquire polls: the one that sees every arrival synchronises with all
-    // of them (each arrival is an acquire-release add, and the opening add
-    // is in the release sequence of each).  Measured against relaxed polls
-    // followed by a fence: 25.33 -> 24.96 us per launch at 1 x 32,768 tokens,
-    // 78.17 -> 77.84 us with 4 x 31,744.
-    const unsigned long long v = ptx::load_acquire_gpu(arrival);
-    const int count = (int)(v & 0xffffu);
-    if ((unsigned)(v >> 32) != gen || count == n) return true;
-    const uint64_t now = ptx::globaltimer_ns();
-    if (count != seen) {
-      seen = count;
-      t_seen = now;
-    }
-    if (now - t_seen > slice_wait_ns && ptx::atomic_cas_gpu(arrival, v, v + (1ull << 16)) == v)
-      return false;
-    if (now - t0 > wait_limit_ns) {
-      atomicOr(status, PA_STATUS_TIMEOUT);
-      return false;
-    }
-  }
-}
 
 // ---------------------------------------------------------------------------
 // The kernel.
@@ -630,8 +384,7 @@ __global__ void __launch_bounds__(Shape<kTensorCores>::kThreads, 1)
       p.out[((size_t)bt * p.Hq + g * G + row) * kD + d] = 0.f;
       if (d == 0) p.lse[(size_t)bt * p.Hq + g * G + row] = -INFINITY;
     }
-    finish_unit<kMaxUnits, kConsumers, kConsumerWarps>(p, sh, bt / p.T, g, ct, warp, lane, 1,
-                                                       U.pair_total);
+    finish_unit<kD, kConsumers>(p, sh, bt / p.T, g, ct, warp, lane, 1, U.pair_total);
   }
 
   int it = 0;
@@ -1042,63 +795,10 @@ __global__ void __launch_bounds__(Shape<kTensorCores>::kThreads, 1)
       }
     }
     if (!single) {
-      // Split unit: CTAs k0 .. k1 each stored a partial.  The barrier orders
-      // every thread's partial before thread 0's acquire-release arrival,
-      // which publishes it at device scope.  CTAs k0 .. k0 + S - 1 (S <= n - 1:
-      // their page ranges end inside this unit, so it is their last segment)
-      // wait until all n have arrived and each merges one of S slices of the
-      // unit's outputs, so the merge is spread over S SMs instead of loading
-      // every partial into one; the last CTA to arrive resets the count and
-      // opens the word's next generation for the next call.  A CTA that gave
-      // up waiting leaves its slice to the last CTA, which then merges every
-      // slice (a slice merged twice gets the same bits).  The other CTAs
-      // leave at once.
-      const int n = U.n_parts;
-      const int S = split_slices(n);
-      const int rank = (int)blockIdx.x - cta_of(pf, p.total_pages, p.grid);
-      const bool participant = rank < S;
-      unsigned long long* arrival = p.arrivals + u;
-      ptx::named_barrier(1, kConsumers);
-      if (ct == 0) {
-        const unsigned long long prev = ptx::atomic_add_acq_rel_gpu(arrival, 1ull);
-        const int arrived = (int)(prev & 0xffffu) + 1;
-        int mode = 0;  // 0: no slice here, 1: this CTA's slice, 2: every slice
-        int leavers = 0;
-        if (arrived == n) {
-          leavers = (int)((prev >> 16) & 0xffffu);
-          // Count and leavers back to zero, generation + 1 (a plain add: a
-          // waiting CTA that reads it still acquires every arrival, which
-          // it follows in the word's order of modifications).
-          ptx::red_add_relaxed_gpu(arrival, (1ull << 32) -
-                                                ((unsigned long long)leavers << 16) -
-                                                (unsigned long long)n);
-          mode = leavers ? 2 : (participant ? 1 : 0);
-          if (leavers) atomicAdd(p.status + 1, leavers);   // diagnostic count, not an error
-        } else if (participant) {
-          mode = wait_unit_complete(arrival, (unsigned)(prev >> 32), n, p.slice_wait_ns,
-                                    p.wait_limit_ns, p.status) ? 1 : 0;
-        }
-        sh.merge_info[0] = mode;
-        sh.merge_info[1] = leavers;
-      }
-      ptx::named_barrier(1, kConsumers);
-      const int mode = sh.merge_info[0];
-      if (mode != 0) {
-        const int n_out = G * (kD / 4);
-        for (int sl = mode == 2 ? 0 : rank; sl < (mode == 2 ? S : rank + 1); ++sl) {
-          merge_split_slice<kMaxUnits, kConsumers>(
-              p, U.part_base, n, (int)((long long)sl * n_out / S),
-              (int)((long long)(sl + 1) * n_out / S), (size_t)bt * p.Hq + g * G, ct);
-        }
-        // Each slice counts once toward the pair's tile count (the slices
-        // of leavers are counted by the last CTA, which merged them).
-        const int done = mode == 2 ? sh.merge_info[1] + (participant ? 1 : 0) : 1;
-        finish_unit<kMaxUnits, kConsumers, kConsumerWarps>(p, sh, b, g, ct, warp, lane, done,
-                                                           U.pair_total);
-      }
+      finish_split_unit<kD, kConsumers>(p, sh, U, u, b, bt, g,
+                                        cta_of(pf, p.total_pages, p.grid), ct, warp, lane);
     } else {
-      finish_unit<kMaxUnits, kConsumers, kConsumerWarps>(p, sh, b, g, ct, warp, lane, 1,
-                                                         U.pair_total);
+      finish_unit<kD, kConsumers>(p, sh, b, g, ct, warp, lane, 1, U.pair_total);
     }
     ptx::named_barrier(1, kConsumers);
   }
@@ -1124,23 +824,6 @@ EncodeTiledFn encode_fn() {
       fn = reinterpret_cast<EncodeTiledFn>(ptr);
   });
   return fn;
-}
-
-// Partial slots reserved: one per unit of a launch plus one per CTA (a CTA
-// adds at most one split point), with room for grids up to 1,024 CTAs.
-size_t part_slots(int B, int T, int Hkv) {
-  const long long units = (long long)B * T * Hkv;
-  return (size_t)std::min<long long>(units, kMaxUnitsLarge) + 1024;
-}
-
-// Per (request, kv head) counters of finished tiles for the fused merge.
-size_t request_counter_bytes(int B, int Hkv) {
-  return ((size_t)B * Hkv * 4 + 255) / 256 * 256;
-}
-
-size_t workspace_bytes(int B, int T, int Hkv) {
-  return kStatusBytes + kCounterBytes + request_counter_bytes(B, Hkv) +
-         part_slots(B, T, Hkv) * (kPartOBytes + kPartMLBytes);
 }
 
 template <int N, bool TC>
@@ -1208,7 +891,7 @@ int check_args(const void* q, const void* pool, int64_t pool_pages, const int32_
              "workspace must be 256-byte aligned");
   PA_REQUIRE(pool_pages * kPage < (1ll << 31), "pool too large for 32-bit row coordinates");
   PA_REQUIRE((long long)B * T * n_q_heads < (1ll << 31), "output too large");
-  const size_t need = workspace_bytes(B, T, n_kv_heads);
+  const size_t need = workspace_bytes(B, T, n_kv_heads, kD);
   PA_REQUIRE(ws_bytes >= need, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes,
              need);
   const long long max_tok = (long long)max_pages * kPage;
@@ -1262,36 +945,22 @@ int run(bool tensor_cores, const void* q, const void* pool, int64_t pool_pages,
   if (sms <= 0) return fail(PA_ERR_CUDA, "cannot query the device's SM count");
   sms = std::min(sms, kMaxGrid);
 
-  std::vector<Unit> units;
-  units.reserve((size_t)B * T * n_kv_heads);
-  // Kv-head-major order: the units of one kv head form a block of the page
-  // sequence, and every block has the same unit sizes, so the CTAs at the
-  // same offset of the n_kv_heads blocks stream the same physical pages (each
-  // its head's slice of every row) at about the same time.
-  for (int g = 0; g < n_kv_heads; ++g) {
-    for (int bt = 0; bt < B * T; ++bt) {
-      Unit u{};
-      u.bt_g = bt * n_kv_heads + g;
-      u.tok_start = tiles[2 * bt];
-      u.tok_end = tiles[2 * bt + 1];
-      units.push_back(u);
-    }
-  }
+  Plan plan;
+  const int rc_plan = plan_units(tiles, B, T, n_kv_heads, sms, launch_grid, kSegmentCharge, &plan);
+  if (rc_plan != PA_OK) return rc_plan;
+  const std::vector<Unit>& units = plan.units;
 
   Params<kMaxUnitsSmall> common{};
   common.q = static_cast<const __nv_bfloat16*>(q);
   common.page_table = page_table;
   common.out = out;
   common.lse = lse;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  common.status = reinterpret_cast<int32_t*>(ws);
-  common.arrivals = reinterpret_cast<unsigned long long*>(ws + kStatusBytes);
-  const size_t slots = part_slots(B, T, n_kv_heads);
-  const size_t rc_bytes = request_counter_bytes(B, n_kv_heads);
-  common.req_counters = reinterpret_cast<int32_t*>(ws + kStatusBytes + kCounterBytes);
-  common.part_o = reinterpret_cast<float*>(ws + kStatusBytes + kCounterBytes + rc_bytes);
-  common.part_ml = reinterpret_cast<float*>(ws + kStatusBytes + kCounterBytes + rc_bytes +
-                                            slots * kPartOBytes);
+  const Workspace ws(workspace, B, T, n_kv_heads, kD);
+  common.status = ws.status;
+  common.arrivals = ws.arrivals;
+  common.req_counters = ws.req_counters;
+  common.part_o = ws.part_o;
+  common.part_ml = ws.part_ml;
   common.pool_pages = pool_pages;
   common.max_pages = max_pages;
   common.T = T;
@@ -1313,65 +982,7 @@ int run(bool tensor_cores, const void* q, const void* pool, int64_t pool_pages,
   t_wait_limit_ns = 0;
   t_slice_wait_ns = -1;
 
-  // Launches of at most kMaxUnitsLarge units each; every launch partitions its
-  // own pages and reuses the workspace after the previous one (same stream).
-  // All launches are laid out first: the fused merge's per-(request, kv
-  // head) count spans every launch that holds a tile of the pair.
-  struct Launch {
-    size_t u0, n;
-    long long total;
-    int grid;
-  };
-  std::vector<Launch> launches;
-  for (size_t u0 = 0; u0 < units.size(); u0 += kMaxUnitsLarge) {
-    const size_t n = std::min<size_t>(kMaxUnitsLarge, units.size() - u0);
-    // The CTAs' equal shares are cut from the units' pages laid end to end,
-    // each unit preceded by kSegmentCharge pages that hold no data: a segment
-    // (one unit's part on one CTA) costs a Q load, a combine and a partial
-    // whatever its length, so a CTA whose range holds a unit start (one more
-    // segment) gets that many fewer pages to stream.
-    long long total = 0;
-    for (size_t i = u0; i < u0 + n; ++i) {
-      const int np = unit_pages(units[i].tok_start, units[i].tok_end);
-      if (np > 0) total += kSegmentCharge;
-      units[i].page_first = static_cast<int32_t>(total);
-      total += np;
-      PA_REQUIRE(total < (1ll << 31), "too many pages in one launch");
-    }
-    const int grid = launch_grid(total, sms, n_kv_heads);
-    int part_cursor = 0;
-    for (size_t i = u0; i < u0 + n; ++i) {
-      const int np = unit_pages(units[i].tok_start, units[i].tok_end);
-      if (np == 0) {
-        units[i].n_parts = 0;
-        continue;
-      }
-      const int k0 = cta_of(units[i].page_first, total, grid);
-      const int k1 = cta_of(units[i].page_first + np - 1, total, grid);
-      units[i].n_parts = k1 - k0 + 1;
-      if (units[i].n_parts > 1) {
-        units[i].part_base = part_cursor;
-        part_cursor += units[i].n_parts;
-      }
-    }
-    if ((size_t)part_cursor > slots)
-      return fail(PA_ERR_INVALID, "internal: %d partial slots exceed the %zu reserved",
-                  part_cursor, slots);
-    launches.push_back({u0, n, total > 0 ? total : 1, grid});
-  }
-  // Completions each (request, kv head) pair's tile count reaches: one per
-  // unsplit or empty unit, one per merge slice of a split unit.
-  {
-    std::vector<int32_t> pair_total((size_t)B * n_kv_heads, 0);
-    auto pair_of = [&](const Unit& U) {
-      const int bt = U.bt_g / n_kv_heads;
-      return (size_t)(bt / T) * n_kv_heads + (U.bt_g - bt * n_kv_heads);
-    };
-    for (const Unit& U : units)
-      pair_total[pair_of(U)] += U.n_parts > 1 ? split_slices(U.n_parts) : 1;
-    for (Unit& U : units) U.pair_total = pair_total[pair_of(U)];
-  }
-  for (const Launch& L : launches) {
+  for (const Launch& L : plan.launches) {
     common.n_requests = L.u0 == 0 ? B : 0;   // new rows are stored by the first launch
     int rc;
     if (L.n <= (size_t)kMaxUnitsSmall) {
@@ -1396,9 +1007,9 @@ int run(bool tensor_cores, const void* q, const void* pool, int64_t pool_pages,
 extern "C" size_t paged_decode_attn_lse_workspace_bytes(int B, int T, int n_q_heads,
                                                         int n_kv_heads, int head_dim) {
   if (B < 0 || T < 0 || head_dim != pa::decode::kD || n_kv_heads < 1 ||
-      n_q_heads % n_kv_heads != 0 || n_q_heads / n_kv_heads > pa::decode::kMaxG)
+      n_q_heads % n_kv_heads != 0 || n_q_heads / n_kv_heads > pa::split::kMaxG)
     return 0;
-  return pa::decode::workspace_bytes(B, T, n_kv_heads);
+  return pa::split::workspace_bytes(B, T, n_kv_heads, pa::decode::kD);
 }
 
 extern "C" int paged_decode_attn_lse(const void* q, const void* pool, int64_t pool_pages,
@@ -1537,7 +1148,7 @@ extern "C" int paged_decode_attn_lse_noalloc(const void* q, const void* pool, in
   rc = noalloc_scratch(&scratch);
   if (rc != PA_OK) return rc;
   // Status word and arrival counters must start at zero.
-  const cudaError_t e = cudaMemsetAsync(scratch, 0, pa::decode::kStatusBytes + pa::decode::kCounterBytes,
+  const cudaError_t e = cudaMemsetAsync(scratch, 0, pa::split::kStatusBytes + pa::split::kCounterBytes,
                                         stream);
   if (e != cudaSuccess)
     return pa::fail(PA_ERR_CUDA, "clearing the scratch array failed: %s", cudaGetErrorString(e));
@@ -1556,9 +1167,9 @@ extern "C" int paged_decode_attn_lse_noalloc(const void* q, const void* pool, in
 
 extern "C" int paged_decode_attn_test_slice_wait(int64_t slice_wait_ns) {
   pa::clear_error();
-  if (slice_wait_ns < -1 || slice_wait_ns > (int64_t)pa::decode::kSliceWaitNs)
+  if (slice_wait_ns < -1 || slice_wait_ns > (int64_t)pa::split::kSliceWaitNs)
     return pa::fail(PA_ERR_INVALID, "slice_wait_ns must be -1 (clear) or in [0, %llu]",
-                    (unsigned long long)pa::decode::kSliceWaitNs);
+                    (unsigned long long)pa::split::kSliceWaitNs);
   pa::decode::t_slice_wait_ns = slice_wait_ns;
   return PA_OK;
 }
