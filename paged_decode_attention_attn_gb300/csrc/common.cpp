@@ -65,6 +65,20 @@ bool current_context_id(unsigned long long* id) {
   return get_id(ctx, id) == CUDA_SUCCESS;
 }
 
+EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
 }  // namespace pa
 
 extern "C" const char* kv_last_error(void) { return pa::g_message; }

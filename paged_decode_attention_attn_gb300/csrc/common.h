@@ -4,6 +4,7 @@
 #include <cstdarg>
 #include <cstdint>
 #include <mutex>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "pagedattn.h"
@@ -21,6 +22,13 @@ int sm_count();
 // lifetime, so a context destroyed and made again gets a new one); false if
 // no context is current or the driver cannot say.
 bool current_context_id(unsigned long long* id);
+
+// The driver's cuTensorMapEncodeTiled, nullptr if it has none.
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled();
 
 // A per-context setting (a kernel attribute, say): apply(set) runs `set`
 // (returning cudaError_t) unless it already succeeded in the context now

@@ -75,7 +75,6 @@ constexpr int kSmemAlloc = kSmemUsed + 1024;             // slack to align to 1 
 constexpr int kWidePages = 32;     // pages per SM from which a launch leaves SMs idle
 constexpr int kWideGridPct = 90;   // share of the SMs such a launch runs on
 constexpr int kSegmentCharge = 6;  // pages charged per segment when CTAs' shares are cut (measured: 3-8 best)
-constexpr uint64_t kWaitLimitNs = 2000000000ull;         // 2 s per wait
 constexpr float kLog2e = 1.44269504088896341f;
 static_assert(kSmemAlloc <= 232448, "shared memory budget");
 
@@ -807,25 +806,6 @@ __global__ void __launch_bounds__(Shape<kTensorCores>::kThreads, 1)
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
-}
-
 template <int N, bool TC>
 cudaError_t launch(const CUtensorMap& tmap, const Params<N>& prm, int grid, cudaStream_t stream) {
   static PerContext smem_limit;   // the attribute lives in the context
@@ -857,12 +837,6 @@ int launch_units(const CUtensorMap& tmap, const std::vector<Unit>& units, size_t
     return fail(PA_ERR_CUDA, "paged decode launch failed: %s", cudaGetErrorString(e));
   return PA_OK;
 }
-
-// Test hook state (paged_decode_attn_test_stall): consumed by the next run()
-// on the calling thread.
-thread_local int t_stall_iteration = -1;
-thread_local unsigned long long t_wait_limit_ns = 0;
-thread_local long long t_slice_wait_ns = -1;   // < 0: kSliceWaitNs
 
 // Every host-side check of a decode call; enqueues nothing and touches no
 // device state.  B * T == 0 passes (the call is then a no-op).
@@ -925,7 +899,7 @@ int run(bool tensor_cores, const void* q, const void* pool, int64_t pool_pages,
                        flags, merged_out, merged_lse);
   if (rc0 != PA_OK || (long long)B * T == 0) return rc0;
   const int G = n_q_heads / n_kv_heads;
-  EncodeTiledFn enc = encode_fn();
+  EncodeTiledFn enc = encode_tiled();
   if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
 
   const int row_elems = 2 * n_kv_heads * kD;
@@ -975,12 +949,10 @@ int run(bool tensor_cores, const void* q, const void* pool, int64_t pool_pages,
   common.kv_ready = (flags & PA_DECODE_KV_READY) ? 1 : 0;
   common.m_out = merged_out;
   common.m_lse = merged_lse;
-  common.wait_limit_ns = t_wait_limit_ns ? t_wait_limit_ns : kWaitLimitNs;
-  common.stall_iteration = t_stall_iteration;
-  common.slice_wait_ns = t_slice_wait_ns >= 0 ? (unsigned long long)t_slice_wait_ns : kSliceWaitNs;
-  t_stall_iteration = -1;
-  t_wait_limit_ns = 0;
-  t_slice_wait_ns = -1;
+  const TestHooks hooks = take_test_hooks();
+  common.wait_limit_ns = hooks.wait_limit_ns;
+  common.stall_iteration = hooks.stall_iteration;
+  common.slice_wait_ns = hooks.slice_wait_ns;
 
   for (const Launch& L : plan.launches) {
     common.n_requests = L.u0 == 0 ? B : 0;   // new rows are stored by the first launch
@@ -1165,27 +1137,29 @@ extern "C" int paged_decode_attn_lse_noalloc(const void* q, const void* pool, in
   return PA_OK;
 }
 
+thread_local pa::split::TestHooks pa::split::t_hooks;
+
 extern "C" int paged_decode_attn_test_slice_wait(int64_t slice_wait_ns) {
   pa::clear_error();
   if (slice_wait_ns < -1 || slice_wait_ns > (int64_t)pa::split::kSliceWaitNs)
     return pa::fail(PA_ERR_INVALID, "slice_wait_ns must be -1 (clear) or in [0, %llu]",
                     (unsigned long long)pa::split::kSliceWaitNs);
-  pa::decode::t_slice_wait_ns = slice_wait_ns;
+  pa::split::t_hooks.slice_wait_ns = slice_wait_ns < 0 ? pa::split::kSliceWaitNs : slice_wait_ns;
   return PA_OK;
 }
 
 extern "C" int paged_decode_attn_test_stall(int iteration, uint64_t wait_limit_ns) {
   pa::clear_error();
   if (iteration == -1 && wait_limit_ns == 0) {   // clear a pending setting
-    pa::decode::t_stall_iteration = -1;
-    pa::decode::t_wait_limit_ns = 0;
+    pa::split::t_hooks.stall_iteration = -1;
+    pa::split::t_hooks.wait_limit_ns = pa::split::kWaitLimitNs;
     return PA_OK;
   }
-  if (iteration < 0 || wait_limit_ns == 0 || wait_limit_ns > pa::decode::kWaitLimitNs)
+  if (iteration < 0 || wait_limit_ns == 0 || wait_limit_ns > pa::split::kWaitLimitNs)
     return pa::fail(PA_ERR_INVALID,
                     "iteration must be >= 0 and wait_limit_ns in (0, %llu]",
-                    (unsigned long long)pa::decode::kWaitLimitNs);
-  pa::decode::t_stall_iteration = iteration;
-  pa::decode::t_wait_limit_ns = wait_limit_ns;
+                    (unsigned long long)pa::split::kWaitLimitNs);
+  pa::split::t_hooks.stall_iteration = iteration;
+  pa::split::t_hooks.wait_limit_ns = wait_limit_ns;
   return PA_OK;
 }

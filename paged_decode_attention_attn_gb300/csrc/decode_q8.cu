@@ -1,141 +1,804 @@
-// Paged GQA decode attention over an 8-bit pool, per tile, with its
-// log-sum-exp: the definition written out in FP32, one CTA per (tile, kv head).
+// Split-KV paged GQA decode attention over an 8-bit (e4m3) pool with a per-tile
+// log-sum-exp, for sm_103a.
+//
+// The bytes of the codes bound it: 2 D bytes per token and kv head, half of the
+// bf16 pool's, so each SM has half the time per token that the bf16 kernel has.
+// Both products therefore run on the fifth-generation tensor cores straight
+// from the codes as TMA leaves them in shared memory; no thread touches a code.
+//
+//  * Work split, partials and merge: as the bf16 kernel (split_units.cuh).  A
+//    CTA streams its pages two at a time: a step is 128 tokens of one kv head.
+//  * S = K Q^T: M = 128 tokens, N = 16, K = D.  q (bf16, 8 significant bits) is
+//    scaled by a power of two per head and held as hi + lo / 16 in e4m3 (4 bits
+//    each, and a sign between them): 16 columns for 8 heads, exact for values
+//    down to 2^-14 of the head's largest.
+//  * Softmax: a thread per token.  Scores are kept relative to a running
+//    reference per head, a multiple of 8 (log2), that bounds x_j + log2 sv_j
+//    (sv the token's V scale), so w_j = 2^(x_j - ref) sv_j lies in [0, 1] and
+//    the largest in (2^-8, 1] whatever the scales; it moves rarely, and then by
+//    an exact power of two.  w is held as kParts e4m3 parts, each the rounding
+//    of what the parts before left, 32 times finer (that stays below 256 =
+//    2^8, as w 2^8 does): 4 bits and a sign per part, 2^-33 absolute at the end.
+//  * O^T = V^T P^T: M = 128 dims (a step's V codes as they lie, M-major), N =
+//    8 kParts, K = 128 tokens.  Every step's product starts from zero in tensor
+//    memory and is added to fp32 registers (a thread per dim), so the long sum
+//    is rounded to nearest and rescaled there.
+//  * Warps: 0-3 softmax, 4-7 output, 8 TMA, 9 MMA, 10 q.  All waits are on
+//    mbarriers with a time limit; S, P and the products have two buffers each.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <cstring>
 #include <vector>
 
 #include "common.h"
 #include "fp8.cuh"
-#include "merge_row.cuh"
 #include "ptx.cuh"
+#include "split_units.cuh"
+#include "tc.cuh"
 
 namespace pa {
 namespace decode_q8 {
 
-constexpr int kPage = PA_PAGE_TOKENS;
-constexpr int kMaxG = 8;
-constexpr int kWarps = 8;
-constexpr int kMaxTiles = 1024;            // tiles per launch
-constexpr size_t kStatusBytes = 256;
+using namespace split;
 
+constexpr int kBlock = PA_SCALE_TOKENS;
+constexpr int kStep = 2 * kPage;            // tokens per step
+constexpr int kStepBlocks = kStep / kBlock;
+constexpr int kParts = 4;                   // e4m3 parts of a probability
+constexpr float kFirstPart = 256.f;         // scale of the first part
+constexpr float kPartRatio = 32.f;          // of each further one
+constexpr int kPCols = kParts * kMaxG;      // N of the second product
+constexpr int kQCols = 2 * kMaxG;           // N of the first product
+constexpr int kChunk = 128;                 // dims per 128-byte row
+constexpr int kTmemCols = 256;
+constexpr int kRefs = 4;                    // reference slots, two steps more than P buffers
+constexpr int kSoftmaxWarps = 4, kOutWarps = 4;
+constexpr int kOut = kOutWarps * 32;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 32 * 11;           // the last warp: q
+constexpr int kSegmentCharge = 6;           // pages charged per unit start
+constexpr int kWidePages = 32, kWideGridPct = 90;
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr int kMaxScaleExp = 100;           // largest |log2| of a V scale
+
+static_assert(kStep == kSoftmaxWarps * 32 && kChunk == kOut, "a thread per token and per dim");
+
+// Shared memory of a CTA; offsets from a 1024-byte boundary.
+template <int D>
+struct Smem {
+  static constexpr int kChunks = D / kChunk;
+  static constexpr int kPageBytes = kPage * kChunk;              // one page, one chunk
+  static constexpr int kChunkBytes = 2 * kPageBytes;             // one step, one chunk
+  static constexpr int kHalfBytes = kChunks * kChunkBytes;       // K (or V) of a step
+  static constexpr int kStageBytes = 2 * kHalfBytes;
+  static constexpr int kStages = D == 256 ? 3 : 6;
+  static constexpr int kPBytes = kPCols * kChunk;
+  static constexpr int kQChunkBytes = kQCols * kChunk;
+  static constexpr int kQBytes = kChunks * kQChunkBytes;
+  static constexpr int kP = kStages * kStageBytes;
+  static constexpr int kQ = kP + 2 * kPBytes;
+  static constexpr int kScales = kQ + 2 * kQBytes;               // [stage][K | V][block]
+  static constexpr int kScaleBytes = 2 * kStepBlocks * 4;
+  static constexpr int kQScale = kScales + kStages * kScaleBytes;  // [2][kMaxG]
+  static constexpr int kRef = kQScale + 2 * kMaxG * 4;             // [kRefs][kMaxG]
+  static constexpr int kSegL = kRef + kRefs * kMaxG * 4;           // [2][warp][kMaxG]
+  static constexpr int kSegRef = kSegL + 2 * kSoftmaxWarps * kMaxG * 4;   // [2][kMaxG]
+  static constexpr int kWarpMax = kSegRef + 2 * kMaxG * 4;         // [warp][kMaxG]
+  static constexpr int kBars = kWarpMax + kSoftmaxWarps * kMaxG * 4;
+  // mbarriers: full, empty per stage; S, P, product, q, sums: full and empty;
+  // all products done; reference slots written
+  static constexpr int kFull = 0, kEmpty = kStages, kSFull = 2 * kStages, kSEmpty = kSFull + 2,
+                       kPFull = kSEmpty + 2, kOFull = kPFull + 2, kOEmpty = kOFull + 2,
+                       kQFull = kOEmpty + 2, kQEmpty = kQFull + 2, kLFull = kQEmpty + 2,
+                       kLEmpty = kLFull + 2, kDrain = kLEmpty + 2, kRefFull = kDrain + 1,
+                       kNumBars = kRefFull + kRefs;
+  static constexpr int kMisc = kBars + kNumBars * 8;               // ints, see View
+  static constexpr int kUsed = kMisc + (kStages + 2 + 8) * 4;
+  static constexpr int kAlloc = kUsed + 1024;
+  static_assert(kAlloc <= 232448, "shared memory budget");
+};
+
+template <int kMaxUnits>
 struct Params {
   const __nv_bfloat16* q;
-  const uint8_t* pool;
   const float* scales;
   const int32_t* page_table;
   float* out;
   float* lse;
   int32_t* status;
+  unsigned long long* arrivals;
+  int32_t* req_counters;
+  float* part_o;
+  float* part_ml;
   long long pool_pages;
-  int max_pages, T, Hq, Hkv, G, bt0;
-  float scale;
-  int2 tiles[kMaxTiles];
+  long long total_pages;
+  int max_pages;
+  int T;
+  int Hq;
+  int Hkv;
+  int G;
+  int n_units;
+  int grid;
+  float scale_log2;
+  unsigned long long wait_limit_ns;
+  int stall_iteration;
+  unsigned long long slice_wait_ns;
+  float* m_out;
+  float* m_lse;
+  Unit units[kMaxUnits];
+};
+static_assert(sizeof(Params<kMaxUnitsLarge>) <= 32764, "kernel parameters too large");
+
+struct View {
+  uint8_t* base;
+  uint32_t addr;          // shared-space address of base
+  uint32_t bars;
+  volatile int* poison;   // [stages] step holds a page that is not there
+  volatile int* seg_poison;  // [2]
+  volatile int* abort_flag;
+  volatile int* fin_flag;
+  volatile int* merge_info;
+  __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
 };
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) decode_kernel(const __grid_constant__ Params p) {
-  constexpr int kDims = D / 32;
-  ptx::launch_dependents();
-  ptx::grid_dependency_wait();
-  __shared__ float xo[kWarps][kMaxG][D];
-  __shared__ float xm[kWarps][kMaxG], xl[kWarps][kMaxG];
-  __shared__ int s_bad;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int i = blockIdx.x / p.Hkv, g = blockIdx.x - i * p.Hkv;
-  const int bt = p.bt0 + i, b = bt / p.T;
-  const int2 tile = p.tiles[i];
-  if (threadIdx.x == 0) s_bad = 0;
-  __syncthreads();
-  float q[kMaxG][kDims], o[kMaxG][kDims], m[kMaxG], l[kMaxG];
-#pragma unroll
-  for (int h = 0; h < kMaxG; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
-#pragma unroll
-    for (int d = 0; d < kDims; ++d) {
-      o[h][d] = 0.f;
-      q[h][d] = h < p.G ? __bfloat162float(
-                              p.q[((size_t)b * p.Hq + g * p.G + h) * D + lane * kDims + d])
-                        : 0.f;
+// Waits for phase `n` (0, 1, ...) of a barrier.  False once the time limit or
+// another warp's has run out.
+template <class P>
+__device__ __forceinline__ bool wait_phase(const P& p, const View& v, int bar, int n) {
+  const uint32_t b = v.bar(bar);
+  const uint32_t parity = n & 1;
+  if (ptx::mbar_try_wait(b, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (true) {
+    if (ptx::mbar_try_wait(b, parity)) return true;
+    if (*v.abort_flag) return false;
+    if (ptx::globaltimer_ns() - t0 > p.wait_limit_ns) {
+      atomicOr(p.status, PA_STATUS_TIMEOUT);
+      *v.abort_flag = 1;
+      return false;
     }
   }
-  for (int j = tile.x + warp; j < tile.y; j += kWarps) {
-    const long long page = p.page_table[(size_t)b * p.max_pages + j / kPage];
-    if (page < 0 || page >= p.pool_pages) {
-      if (lane == 0) {
-        atomicOr(p.status, PA_STATUS_BAD_PAGE);
-        s_bad = 1;
+}
+
+// A CTA's part of a unit: its pages [lo, hi).
+struct Segment {
+  Unit U;
+  int u, pf, lo, hi, bt, b, g, first_tok;
+  __device__ __forceinline__ int steps() const { return (hi - lo + 1) / 2; }
+};
+
+// Calls f(segment, index) for every segment of this CTA until f returns false.
+template <class P, class F>
+__device__ __forceinline__ void for_segments(const P& p, F f) {
+  const int start = static_cast<int>((long long)blockIdx.x * p.total_pages / p.grid);
+  const int end = static_cast<int>((long long)(blockIdx.x + 1) * p.total_pages / p.grid);
+  int index = 0;
+  for (int u = first_unit(p, start); u < p.n_units && p.units[u].page_first < end; ++u) {
+    Segment s;
+    s.U = p.units[u];
+    const int np = unit_pages(s.U.tok_start, s.U.tok_end);
+    if (np == 0) continue;
+    s.u = u;
+    s.pf = s.U.page_first;
+    s.lo = max(start, s.pf) - s.pf;
+    s.hi = min(end, s.pf + np) - s.pf;
+    if (s.hi <= s.lo) continue;   // only the unit's segment charge falls in this range
+    s.bt = s.U.bt_g / p.Hkv;
+    s.g = s.U.bt_g - s.bt * p.Hkv;
+    s.b = s.bt / p.T;
+    s.first_tok = s.U.tok_start / kPage * kPage;
+    if (!f(s, index)) return;
+    ++index;
+  }
+}
+
+__device__ __forceinline__ bool any_in_group(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst), "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// Largest of a warp's floats (NaN ignored): integer maximum of an order-preserving
+// mapping.
+__device__ __forceinline__ float warp_max(float x) {
+  const int b = __float_as_int(fmaxf(x, -INFINITY));
+  const int m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
+  return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
+}
+
+// ---------------------------------------------------------------------------
+// Warp 8: pages and scales into the stage ring.
+// ---------------------------------------------------------------------------
+template <int D, class P>
+__device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtensorMap* tmap,
+                                         int lane) {
+  using S = Smem<D>;
+  int it = 0;
+  bool ok = true;
+  const uint64_t pol = ptx::policy_evict_first();   // every page is read once
+  for_segments(p, [&](const Segment& s, int) {
+    const int32_t* prow = p.page_table + (size_t)s.b * p.max_pages + s.U.tok_start / kPage;
+    for (int base = s.lo; ok && base < s.hi; base += 32) {
+      const int cnt = min(32, s.hi - base);
+      const int my_pid = lane < cnt ? __ldg(prow + base + lane) : 0;
+      for (int j = 0; ok && j < cnt; j += 2, ++it) {
+        const int stage = it % S::kStages;
+        const int n = min(2, cnt - j);
+        const int pid0 = __shfl_sync(0xffffffffu, my_pid, j);
+        const int pid1 = __shfl_sync(0xffffffffu, my_pid, (j + 1) & 31);
+        if (lane == 0) {
+          ok = it < S::kStages || wait_phase(p, v, S::kEmpty + stage, it / S::kStages - 1);
+          if (ok) {
+            const uint32_t full = v.bar(S::kFull + stage);
+            const uint32_t dst = v.addr + stage * S::kStageBytes;
+            const uint32_t sc = v.addr + S::kScales + stage * S::kScaleBytes;
+            // set before the arrival that publishes it
+            const bool bad0 = pid0 < 0 || (long long)pid0 >= p.pool_pages;
+            const bool bad1 = n > 1 && (pid1 < 0 || (long long)pid1 >= p.pool_pages);
+            if (bad0 || bad1) atomicOr(p.status, PA_STATUS_BAD_PAGE);
+            v.poison[stage] = bad0 || bad1 ? 1 : 0;
+            if (it != p.stall_iteration || blockIdx.x != 0) {
+              ptx::mbar_arrive_expect_tx(full, n * (2 * S::kChunks * S::kPageBytes + 32));
+              for (int k = 0; k < n; ++k) {
+                const int pid = k ? (bad1 ? 0 : pid1) : (bad0 ? 0 : pid0);
+#pragma unroll
+                for (int c = 0; c < S::kChunks; ++c) {
+                  const uint32_t at = dst + c * S::kChunkBytes + k * S::kPageBytes;
+                  ptx::tma_load_2d_hint(at, tmap, s.g * D + c * kChunk, pid * kPage, full, pol);
+                  ptx::tma_load_2d_hint(at + S::kHalfBytes, tmap,
+                                        (p.Hkv + s.g) * D + c * kChunk, pid * kPage, full, pol);
+                }
+                const float* from = p.scales + ((size_t)pid * 2 * p.Hkv + s.g) * 4;
+                bulk_load(sc + k * 16, from, 16, full);
+                bulk_load(sc + kStepBlocks * 4 + k * 16, from + (size_t)p.Hkv * 4, 16, full);
+              }
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
       }
-      continue;
     }
-    const uint8_t* row = p.pool + ((size_t)page * kPage + j % kPage) * (2 * p.Hkv * D) + g * D +
-                         lane * kDims;
-    const float* sc = p.scales + ((size_t)page * 2 * p.Hkv + g) * 4 + j % kPage / PA_SCALE_TOKENS;
-    float k[kDims], v[kDims];
+    return ok;
+  });
+  // Every page of this CTA is requested: the next kernel in the stream may
+  // start its prologue.
+  if (lane == 0) ptx::launch_dependents();
+  if (lane == 0) {
+    // The copies issued land before the CTA can exit, whatever became of the
+    // other warps.
+    for (int k = max(0, it - S::kStages); k < it; ++k)
+      ptx::mbar_wait_bounded(v.bar(S::kFull + k % S::kStages), (k / S::kStages) & 1,
+                             p.wait_limit_ns);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Warp 9, one thread: the products.
+// ---------------------------------------------------------------------------
+template <int D, class P>
+__device__ __forceinline__ void mma_thread(const P& p, const View& v, uint32_t tmem) {
+  using S = Smem<D>;
+  constexpr uint32_t kIdescS = tc::idesc_e4m3(kStep, kQCols, false);
+  constexpr uint32_t kIdescO = tc::idesc_e4m3(kChunk, kPCols, true);
+  int it = 0;
+  int last_pages = 0;
+  bool ok = true;
+  // O^T of step j: its K = 32 token slices, of the pages that were loaded.
+  auto second = [&](int j, int pages) {
+    ok = wait_phase(p, v, S::kPFull + (j & 1), j >> 1) &&
+         (j < 2 || wait_phase(p, v, S::kOEmpty + (j & 1), (j >> 1) - 1));
+    if (!ok) return;
+    tc::fence_after();
+    const uint32_t val = v.addr + (j % S::kStages) * S::kStageBytes + S::kHalfBytes;
+    const uint64_t pd = tc::desc_sw128(v.addr + S::kP + (j & 1) * S::kPBytes);
+    const uint32_t d = tmem + 2 * kQCols + (j & 1) * S::kChunks * kPCols;
 #pragma unroll
-    for (int d = 0; d < kDims; d += 4) {
-      float y[4];
-      fp8::unpack4(*reinterpret_cast<const uint32_t*>(row + d), y);
+    for (int c = 0; c < S::kChunks; ++c) {
+      for (int k = 0; k < 2 * pages; ++k)
+        tc::mma_e4m3(d + c * kPCols, tc::desc_sw128(val + c * S::kChunkBytes + k * 32 * kChunk),
+                     pd + 2 * k, kIdescO, k > 0);
+    }
+    tc::commit(v.bar(S::kOFull + (j & 1)));
+    tc::commit(v.bar(S::kEmpty + j % S::kStages));
+  };
+  for_segments(p, [&](const Segment& s, int seg) {
+    ok = ok && wait_phase(p, v, S::kQFull + (seg & 1), seg >> 1);
+    const int steps = s.steps();
+    for (int i = 0; ok && i < steps; ++i, ++it) {
+      const int stage = it % S::kStages;
+      ok = wait_phase(p, v, S::kFull + stage, it / S::kStages) &&
+           (it < 2 || wait_phase(p, v, S::kSEmpty + (it & 1), (it >> 1) - 1));
+      if (!ok) break;
+      tc::fence_after();
+      const uint32_t key = v.addr + stage * S::kStageBytes;
+      const uint32_t qs = v.addr + S::kQ + (seg & 1) * S::kQBytes;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) k[d + e] = y[e];
-      fp8::unpack4(*reinterpret_cast<const uint32_t*>(row + p.Hkv * D + d), y);
+      for (int c = 0; c < S::kChunks; ++c) {
+        const uint64_t a = tc::desc_sw128(key + c * S::kChunkBytes);
+        const uint64_t b = tc::desc_sw128(qs + c * S::kQChunkBytes);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[d + e] = y[e] * sc[p.Hkv * 4];
+        for (int k = 0; k < 4; ++k)
+          tc::mma_e4m3(tmem + (it & 1) * kQCols, a + 2 * k, b + 2 * k, kIdescS, c + k > 0);
+      }
+      tc::commit(v.bar(S::kSFull + (it & 1)));
+      if (i == steps - 1) tc::commit(v.bar(S::kQEmpty + (seg & 1)));
+      if (it > 0) second(it - 1, last_pages);
+      last_pages = min(2, s.hi - (s.lo + 2 * i));
+    }
+    return ok;
+  });
+  if (ok && it > 0) second(it - 1, last_pages);
+  // Every product, and every arrival that follows from one, ends before the
+  // CTA can.
+  tc::commit(v.bar(S::kDrain));
+  ptx::mbar_wait_bounded(v.bar(S::kDrain), 0, p.wait_limit_ns);
+}
+
+// ---------------------------------------------------------------------------
+// Warp 10: q of each segment as hi and lo parts, and its scale.
+// ---------------------------------------------------------------------------
+template <int D, class P>
+__device__ __forceinline__ void q_warp(const P& p, const View& v, int lane) {
+  using S = Smem<D>;
+  constexpr int kDims = D / 32;             // dims per lane
+  using Vec = typename std::conditional<kDims == 8, uint4, uint2>::type;
+  for_segments(p, [&](const Segment& s, int seg) {
+    if (seg >= 2 && !wait_phase(p, v, S::kQEmpty + (seg & 1), (seg >> 1) - 1)) return false;
+    const uint32_t buf = v.addr + S::kQ + (seg & 1) * S::kQBytes;
+    float* qscale = reinterpret_cast<float*>(v.base + S::kQScale) + (seg & 1) * kMaxG;
+    const __nv_bfloat16* src = p.q + ((size_t)s.b * p.Hq + s.g * p.G) * D + lane * kDims;
+    Vec raw[kMaxG];
+#pragma unroll
+    for (int h = 0; h < kMaxG; ++h) {
+      raw[h] = Vec{};
+      if (h < p.G) raw[h] = __ldg(reinterpret_cast<const Vec*>(src + h * D));
     }
 #pragma unroll
     for (int h = 0; h < kMaxG; ++h) {
-      float x = 0.f;
+      float y[kDims];
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[h]);
+      unsigned amax = 0;
 #pragma unroll
-      for (int d = 0; d < kDims; ++d) x = fmaf(q[h][d], k[d], x);
+      for (int i = 0; i < kDims / 2; ++i) {
+        y[2 * i] = ptx::bf16_lo_to_f32(w[i]);
+        y[2 * i + 1] = ptx::bf16_hi_to_f32(w[i]);
+      }
 #pragma unroll
-      for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-      x *= p.scale * sc[0];
-      const float m_new = fmaxf(m[h], x);
-      const float a = expf(m[h] - m_new), w = expf(x - m_new);
-      l[h] = l[h] * a + w;
+      for (int i = 0; i < kDims; ++i) amax = max(amax, __float_as_uint(y[i]) & 0x7fffffffu);
+      amax = __reduce_max_sync(0xffffffffu, amax);
+      // largest value to [128, 256); NaN and infinities to NaN codes
+      const int e = amax ? min(7 - ((int)(amax >> 23) - 127), 120) : 0;
+      const float up = ptx::pow2i(e);
+      if (lane == 0) qscale[h] = p.scale_log2 * ptx::pow2i(-e);
+      uint32_t hi[kDims / 4], lo[kDims / 4];
 #pragma unroll
-      for (int d = 0; d < kDims; ++d) o[h][d] = o[h][d] * a + w * v[d];
-      m[h] = m_new;
+      for (int i = 0; i < kDims / 4; ++i) {
+        float z[4], f[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          z[k] = fabsf(y[4 * i + k]) <= 3.4e38f ? y[4 * i + k] * up : __int_as_float(0x7fc00000);
+        hi[i] = fp8::pack4(z[0], z[1], z[2], z[3]);
+        fp8::unpack4(hi[i], f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] = (z[k] - f[k]) * 16.f;
+        lo[i] = fp8::pack4(z[0], z[1], z[2], z[3]);
+      }
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const int row = part * kMaxG + h;
+        const int col = lane * kDims;
+        const uint32_t at = buf + col / kChunk * S::kQChunkBytes + row * kChunk +
+                            (((col % kChunk >> 4) ^ (row & 7)) << 4) + (col & 15);
+#pragma unroll
+        for (int i = 0; i < kDims / 4; ++i)
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * i), "r"(part ? lo[i] : hi[i])
+                       : "memory");
+      }
     }
-  }
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(v.bar(S::kQFull + (seg & 1)));
+    return true;
+  });
+}
+
+// ---------------------------------------------------------------------------
+// Warps 0-3: a thread per token of a step.
+// ---------------------------------------------------------------------------
+template <int D, class P>
+__device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_t tmem, int warp,
+                                              int lane) {
+  using S = Smem<D>;
+  const int tok = warp * 32 + lane;
+  int it = 0;
+  bool fail = false;
+  float* wmax = reinterpret_cast<float*>(v.base + S::kWarpMax);
+  for_segments(p, [&](const Segment& s, int seg) {
+    float qs[kMaxG], ref[kMaxG], l[kMaxG];
+    fail |= !wait_phase(p, v, S::kQFull + (seg & 1), seg >> 1);
+    const float* qscale = reinterpret_cast<float*>(v.base + S::kQScale) + (seg & 1) * kMaxG;
 #pragma unroll
-  for (int h = 0; h < kMaxG; ++h) {
+    for (int h = 0; h < kMaxG; ++h) {
+      qs[h] = qscale[h];
+      ref[h] = -INFINITY;
+      l[h] = 0.f;
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(v.bar(S::kQEmpty + (seg & 1)));
+    int poisoned = 0;
+    const int steps = s.steps();
+    for (int i = 0; i < steps; ++i, ++it) {
+      const int stage = it % S::kStages;
+      const int tok0 = s.first_tok + (s.lo + 2 * i) * kPage;
+      const int pages = min(2, s.hi - (s.lo + 2 * i));
+      const bool loaded = tok < pages * kPage;
+      const bool live = loaded && tok0 + tok >= s.U.tok_start && tok0 + tok < s.U.tok_end;
+      float x[kMaxG];
+      float sv = 0.f, up = 0.f;
+      bool need = false;
+      fail = fail || !wait_phase(p, v, S::kFull + stage, it / S::kStages) ||
+             !wait_phase(p, v, S::kSFull + (it & 1), it >> 1);
+      if (!fail) {
+        const float* sc = reinterpret_cast<const float*>(v.base + S::kScales +
+                                                         stage * S::kScaleBytes);
+        const float sk = sc[tok / kBlock];
+        sv = sc[kStepBlocks + tok / kBlock];
+        poisoned |= v.poison[stage];
+        tc::fence_after();
+        uint32_t r[16];
+        tc::ld16(tmem + (it & 1) * kQCols + ((uint32_t)(warp * 32) << 16), r);
+        tc::wait_ld(r);
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(v.bar(S::kSEmpty + (it & 1)));
+        // 2^up >= |sv|
+        const unsigned sb = __float_as_uint(sv) & 0x7fffffffu;
+        if (!(fabsf(sv) <= ptx::pow2i(kMaxScaleExp))) sv = __int_as_float(0x7fc00000);
+        up = (float)max(min((int)(sb >> 23) - 127 + ((sb & 0x7fffffu) ? 1 : 0), kMaxScaleExp),
+                        -kMaxScaleExp);
 #pragma unroll
-    for (int d = 0; d < kDims; ++d) xo[warp][h][lane * kDims + d] = o[h][d];
-    xm[warp][h] = m[h];
-    xl[warp][h] = l[h];
+        for (int h = 0; h < kMaxG; ++h) {
+          const float d = __uint_as_float(r[h]) + __uint_as_float(r[kMaxG + h]) * 0.0625f;
+          x[h] = live ? d * sk * qs[h] : -INFINITY;
+          need |= x[h] + up > ref[h];
+        }
+      }
+      if (any_in_group(2, kStep, need || fail)) {
+        if (any_in_group(3, kStep, fail)) return false;
+#pragma unroll
+        for (int h = 0; h < kMaxG; ++h) {
+          const float m = warp_max(x[h] + up);
+          if (lane == 0) wmax[warp * kMaxG + h] = m;
+        }
+        ptx::named_barrier(2, kStep);
+#pragma unroll
+        for (int h = 0; h < kMaxG; ++h) {
+          float m = wmax[h];
+#pragma unroll
+          for (int w = 1; w < kSoftmaxWarps; ++w) m = fmaxf(m, wmax[w * kMaxG + h]);
+          const float to = fmaxf(ref[h], ref_ceil(m));
+          l[h] *= ref_weight(ref[h], to);
+          ref[h] = to;
+        }
+      }
+      if (tok == 0) {
+        float* slot = reinterpret_cast<float*>(v.base + S::kRef) + (it % kRefs) * kMaxG;
+#pragma unroll
+        for (int h = 0; h < kMaxG; ++h) slot[h] = ref[h];
+        ptx::mbar_arrive(v.bar(S::kRefFull + it % kRefs));
+      }
+      // the product that read this P buffer is done
+      if (it >= 2) fail = !wait_phase(p, v, S::kOFull + (it & 1), (it >> 1) - 1);
+      const uint32_t prow = v.addr + S::kP + (it & 1) * S::kPBytes + (tok & 15);
+      const int chunk = tok >> 4;
+#pragma unroll
+      for (int h = 0; h < kMaxG; h += 2) {
+        float w[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float e = ptx::ex2(x[h + k] - (ref[h + k] == -INFINITY ? 0.f : ref[h + k]));
+          l[h + k] += e;
+          w[k] = live ? e * sv * kFirstPart : 0.f;
+        }
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          const uint32_t c = fp8::pack2(w[0], w[1]);
+          const int row = part * kMaxG + h;
+          asm volatile("st.shared.u8 [%0], %1;" ::"r"(prow + row * kChunk +
+                                                       ((chunk ^ (row & 7)) << 4)),
+                       "r"(c)
+                       : "memory");
+          asm volatile("st.shared.u8 [%0], %1;" ::"r"(prow + (row + 1) * kChunk +
+                                                       ((chunk ^ ((row + 1) & 7)) << 4)),
+                       "r"(c >> 8)
+                       : "memory");
+          if (part + 1 < kParts) {
+            const float2 f = fp8::unpack2(c);
+            w[0] = (w[0] - f.x) * kPartRatio;
+            w[1] = (w[1] - f.y) * kPartRatio;
+          }
+        }
+      }
+      if (loaded && !live) {
+        // A NaN code in a row outside the tile would reach the product (0 x NaN).
+        const uint32_t row = v.addr + stage * S::kStageBytes + S::kHalfBytes + tok * kChunk;
+#pragma unroll
+        for (int c = 0; c < S::kChunks; ++c)
+          for (int k = 0; k < kChunk; k += 16)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             row + c * S::kChunkBytes + k),
+                         "r"(0u)
+                         : "memory");
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(v.bar(S::kPFull + (it & 1)));
+    }
+    // ---- the segment's sums, references and poison to the output warps ----
+    if (seg >= 2) fail |= !wait_phase(p, v, S::kLEmpty + (seg & 1), (seg >> 1) - 1);
+    float* seg_l = reinterpret_cast<float*>(v.base + S::kSegL) +
+                   ((seg & 1) * kSoftmaxWarps + warp) * kMaxG;
+#pragma unroll
+    for (int h = 0; h < kMaxG; ++h) {
+#pragma unroll
+      for (int off = 16; off; off >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
+      if (lane == 0) seg_l[h] = l[h];
+    }
+    if (tok == 0) {
+      float* sr = reinterpret_cast<float*>(v.base + S::kSegRef) + (seg & 1) * kMaxG;
+#pragma unroll
+      for (int h = 0; h < kMaxG; ++h) sr[h] = ref[h];
+      v.seg_poison[seg & 1] = poisoned;
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(v.bar(S::kLFull + (seg & 1)));
+    return true;
+  });
+}
+
+// ---------------------------------------------------------------------------
+// Warps 4-7: a thread per dim of each chunk.
+// ---------------------------------------------------------------------------
+template <int D, class P>
+__device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t tmem, int warp,
+                                             int lane) {
+  using S = Smem<D>;
+  const int ct = warp * 32 + lane;
+  const float qnan = __int_as_float(0x7fc00000);
+  // Empty units: output 0, LSE -inf.
+  for (int u = blockIdx.x; u < p.n_units; u += p.grid) {
+    const Unit U = p.units[u];
+    if (unit_pages(U.tok_start, U.tok_end) != 0) continue;
+    const int bt = U.bt_g / p.Hkv;
+    const int g = U.bt_g - bt * p.Hkv;
+    const size_t orow = (size_t)bt * p.Hq + g * p.G;
+    for (int i = ct; i < p.G * D; i += kOut) p.out[orow * D + i] = 0.f;
+    if (ct < p.G) p.lse[orow + ct] = -INFINITY;
+    finish_unit<D, kOut>(p, v, bt / p.T, g, ct, warp, lane, 1, U.pair_total);
   }
+  int it = 0;
+  for_segments(p, [&](const Segment& s, int seg) {
+    float acc[S::kChunks][kMaxG], ref[kMaxG];
+#pragma unroll
+    for (int h = 0; h < kMaxG; ++h) {
+      ref[h] = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < S::kChunks; ++c) acc[c][h] = 0.f;
+    }
+    bool fail = false;
+    const int steps = s.steps();
+    for (int i = 0; i < steps; ++i, ++it) {
+      // A slot is written again four steps on, behind a product that waits
+      // for this step's buffer.
+      fail = !wait_phase(p, v, S::kRefFull + it % kRefs, it / kRefs) ||
+             !wait_phase(p, v, S::kOFull + (it & 1), it >> 1);
+      if (fail) break;
+      const float* slot = reinterpret_cast<const float*>(v.base + S::kRef) + (it % kRefs) * kMaxG;
+      bool moved = false;
+      float to[kMaxG];
+#pragma unroll
+      for (int h = 0; h < kMaxG; ++h) {
+        to[h] = slot[h];
+        moved |= to[h] != ref[h];
+      }
+      if (moved) {
+#pragma unroll
+        for (int h = 0; h < kMaxG; ++h) {
+          const float a = ref_weight(ref[h], to[h]);
+#pragma unroll
+          for (int c = 0; c < S::kChunks; ++c) acc[c][h] *= a;
+          ref[h] = to[h];
+        }
+      }
+      tc::fence_after();
+      const uint32_t d = tmem + 2 * kQCols + (it & 1) * S::kChunks * kPCols +
+                         ((uint32_t)(warp * 32) << 16);
+#pragma unroll
+      for (int c = 0; c < S::kChunks; ++c) {
+        uint32_t r[kPCols / 16][16];
+#pragma unroll
+        for (int k = 0; k < kPCols / 16; ++k) tc::ld16(d + c * kPCols + 16 * k, r[k]);
+#pragma unroll
+        for (int k = 0; k < kPCols / 16; ++k) tc::wait_ld(r[k]);
+#pragma unroll
+        for (int h = 0; h < kMaxG; ++h) {
+          float sum = 0.f;
+#pragma unroll
+          for (int part = kParts - 1; part >= 0; --part) {
+            const int col = part * kMaxG + h;
+            sum = fmaf(sum, 1.0f / kPartRatio, __uint_as_float(r[col / 16][col % 16]));
+          }
+          acc[c][h] = fmaf(sum, 1.0f / kFirstPart, acc[c][h]);
+        }
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(v.bar(S::kOEmpty + (it & 1)));
+    }
+    fail = fail || !wait_phase(p, v, S::kLFull + (seg & 1), seg >> 1);
+    if (any_in_group(1, kOut, fail)) return false;
+    // ---- the segment's output or partial ----
+    const float* seg_l = reinterpret_cast<const float*>(v.base + S::kSegL) +
+                         (seg & 1) * kSoftmaxWarps * kMaxG;
+    const float* sr = reinterpret_cast<const float*>(v.base + S::kSegRef) + (seg & 1) * kMaxG;
+    const bool nan = v.seg_poison[seg & 1] != 0;
+    float l[kMaxG];
+#pragma unroll
+    for (int h = 0; h < kMaxG; ++h) {
+      l[h] = (seg_l[h] + seg_l[kMaxG + h]) + (seg_l[2 * kMaxG + h] + seg_l[3 * kMaxG + h]);
+      ref[h] = sr[h];
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(v.bar(S::kLEmpty + (seg & 1)));
+    const int first_cta = cta_of(s.pf, p.total_pages, p.grid);
+    if (s.U.n_parts == 1) {
+      const size_t orow = (size_t)s.bt * p.Hq + s.g * p.G;
+#pragma unroll
+      for (int h = 0; h < kMaxG; ++h) {
+        if (h >= p.G) continue;
+#pragma unroll
+        for (int c = 0; c < S::kChunks; ++c)
+          p.out[(orow + h) * D + c * kChunk + ct] = nan ? qnan : acc[c][h] / l[h];
+        if (ct == h) p.lse[orow + h] = nan ? qnan : lse_of(ref[h], l[h]);
+      }
+      finish_unit<D, kOut>(p, v, s.b, s.g, ct, warp, lane, 1, s.U.pair_total);
+    } else {
+      const size_t slot = s.U.part_base + (int)blockIdx.x - first_cta;
+#pragma unroll
+      for (int h = 0; h < kMaxG; ++h) {
+        if (h >= p.G) continue;
+        // The reference bounds V's scales too; the partial's is moved to the
+        // sum's own magnitude, so that partials of blocks whose V scales lie
+        // far apart still meet near their weights.
+        int k = 0;
+        if (l[h] > 0.f && l[h] <= 3.4e38f) {
+          frexpf(l[h], &k);
+          k = max(-112, min(112, (k + 132) / 8 * 8 - 128));
+        }
+        const float down = ptx::pow2i(-k);
+#pragma unroll
+        for (int c = 0; c < S::kChunks; ++c)
+          p.part_o[(slot * kMaxG + h) * D + c * kChunk + ct] = acc[c][h] * down;
+        if (ct == h) {
+          p.part_ml[(slot * kMaxG + h) * 2 + 0] = nan ? qnan : ref[h] + (float)k;
+          p.part_ml[(slot * kMaxG + h) * 2 + 1] = l[h] * down;
+        }
+      }
+      finish_split_unit<D, kOut>(p, v, s.U, s.u, s.b, s.bt, s.g, first_cta, ct, warp, lane);
+    }
+    ptx::named_barrier(1, kOut);
+    return true;
+  });
+}
+
+template <int D, int kMaxUnits>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_q8_kernel(const __grid_constant__ CUtensorMap tmap,
+                     const __grid_constant__ Params<kMaxUnits> p) {
+  using S = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  View v;
+  v.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                      ~uintptr_t(1023));
+  v.addr = ptx::smem_addr(v.base);
+  v.bars = v.addr + S::kBars;
+  int* misc = reinterpret_cast<int*>(v.base + S::kMisc);
+  v.poison = misc;
+  v.seg_poison = misc + S::kStages;
+  v.abort_flag = misc + S::kStages + 2;
+  v.fin_flag = misc + S::kStages + 3;
+  v.merge_info = misc + S::kStages + 4;
+  int* tmem_slot = misc + S::kStages + 6;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kNumBars; ++i) {
+      int n = 1;
+      if (i >= S::kSEmpty && i < S::kOFull) n = kSoftmaxWarps;        // S empty, P full
+      if (i >= S::kOEmpty && i < S::kQFull) n = kOutWarps;
+      if (i >= S::kQEmpty && i < S::kLFull) n = kSoftmaxWarps + 1;    // and the last product
+      if (i >= S::kLFull && i < S::kLEmpty) n = kSoftmaxWarps;
+      if (i >= S::kLEmpty && i < S::kDrain) n = kOutWarps;
+      ptx::mbar_init(v.bar(i), n);
+    }
+    *v.abort_flag = 0;
+    ptx::mbar_init_fence();
+  }
+  if (warp == kTmaWarp && lane == 0) ptx::prefetch_tensormap(&tmap);
+  if (warp == kMmaWarp) tc::alloc(ptx::smem_addr(tmem_slot), kTmemCols);
+  tc::fence_before();
   __syncthreads();
-  for (int idx = threadIdx.x; idx < p.G * D; idx += kWarps * 32) {
-    const int h = idx / D, d = idx - h * D;
-    float big = -INFINITY, acc = 0.f, sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) big = fmaxf(big, xm[w][h]);
-    for (int w = 0; w < kWarps; ++w) {
-      if (xm[w][h] == -INFINITY && xl[w][h] == 0.f) continue;
-      const float a = expf(xm[w][h] - big);
-      acc += a * xo[w][h][d];
-      sum += a * xl[w][h];
-    }
-    const size_t r = (size_t)bt * p.Hq + g * p.G + h;
-    const bool empty = tile.y <= tile.x;
-    const float nan = __int_as_float(0x7fc00000);
-    p.out[r * D + d] = s_bad ? nan : empty ? 0.f : acc / sum;
-    if (d == 0) p.lse[r] = s_bad ? nan : empty ? -INFINITY : big + logf(sum);
-  }
-}
-
-__global__ void merge_kernel(const float* out, const float* lse, int T, int H, int D, float* m_out,
-                             float* m_lse) {
-  ptx::launch_dependents();
+  tc::fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile int*>(tmem_slot);
   ptx::grid_dependency_wait();
-  const int b = blockIdx.x / H, h = blockIdx.x - b * H;
-  mergerow::merge_row<false>(out, lse, b * T, T, H, h, D, m_out + (size_t)blockIdx.x * D,
-                             m_lse + blockIdx.x, threadIdx.x);
+  if (warp < kSoftmaxWarps) {
+    softmax_warps<D>(p, v, tmem, warp, lane);
+  } else if (warp < kSoftmaxWarps + kOutWarps) {
+    output_warps<D>(p, v, tmem, warp - kSoftmaxWarps, lane);
+  } else if (warp == kTmaWarp) {
+    tma_warp<D>(p, v, &tmap, lane);
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) mma_thread<D>(p, v, tmem);
+  } else {
+    q_warp<D>(p, v, lane);
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == kMmaWarp) tc::dealloc(tmem, kTmemCols);
 }
 
-size_t workspace_bytes() { return kStatusBytes; }
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+int launch_grid(long long total, int sms, int n_kv_heads) {
+  if (total <= 0) return 1;
+  int grid = total >= (long long)kWidePages * sms ? std::max(1, sms * kWideGridPct / 100)
+                                                  : (int)std::min<long long>(sms, total);
+  if (grid >= n_kv_heads) grid -= grid % n_kv_heads;
+  return grid;
+}
+
+template <int D, int N>
+int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L,
+                 const Params<kMaxUnitsSmall>& common, cudaStream_t stream) {
+  static_assert(N >= kMaxUnitsSmall, "");
+  Params<N> prm;
+  std::memcpy(static_cast<void*>(&prm), &common, offsetof(Params<kMaxUnitsSmall>, units));
+  prm.n_units = static_cast<int>(L.n);
+  prm.total_pages = L.total;
+  prm.grid = L.grid;
+  std::memcpy(prm.units, plan.units.data() + L.u0, L.n * sizeof(Unit));
+  static PerContext smem_limit;   // the attribute lives in the context
+  cudaError_t e = smem_limit.apply([] {
+    return cudaFuncSetAttribute(decode_q8_kernel<D, N>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kAlloc);
+  });
+  if (e == cudaSuccess)
+    e = launch_dependent(decode_q8_kernel<D, N>, dim3(L.grid), dim3(kThreads), Smem<D>::kAlloc,
+                         stream, tmap, prm);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess)
+    return fail(PA_ERR_CUDA, "8-bit paged decode launch failed: %s", cudaGetErrorString(e));
+  return PA_OK;
+}
 
 int run(const void* q, const void* pool, const float* scales, int64_t pool_pages,
         const int32_t* page_table, int max_pages, const int32_t* tiles, int B, int T, int Hq,
@@ -152,7 +815,7 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   PA_REQUIRE(q && pool && scales && page_table && tiles && out && lse && workspace,
              "null pointer argument");
   PA_REQUIRE(max_pages >= 1 && pool_pages >= 1, "max_pages and pool_pages must be >= 1");
-  auto aligned = [](const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+  auto aligned = [](const void* ptr, int n) { return reinterpret_cast<uintptr_t>(ptr) % n == 0; };
   PA_REQUIRE(aligned(q, 16), "q must be 16-byte aligned");
   PA_REQUIRE(aligned(pool, 16), "pool must be 16-byte aligned");
   PA_REQUIRE(aligned(scales, 16), "scales must be 16-byte aligned");
@@ -163,8 +826,9 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   PA_REQUIRE(aligned(merged_out, 16), "merged_out must be 16-byte aligned");
   PA_REQUIRE(pool_pages < (1ll << 31) / kPage, "pool too large for 32-bit row coordinates");
   PA_REQUIRE((long long)B * T * Hq < (1ll << 31), "output too large");
-  PA_REQUIRE(ws_bytes >= workspace_bytes(), "workspace of %zu bytes is smaller than the %zu needed",
-             ws_bytes, workspace_bytes());
+  const size_t need = workspace_bytes(B, T, Hkv, D);
+  PA_REQUIRE(ws_bytes >= need, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes,
+             need);
   const long long max_tok = (long long)max_pages * kPage;
   for (long long i = 0; i < (long long)B * T; ++i) {
     const int s = tiles[2 * i], e = tiles[2 * i + 1];
@@ -172,37 +836,63 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
                "tile %lld of request %lld is [%d, %d), outside [0, %lld]", i % T, i / T, s, e,
                max_tok);
   }
-  Params p{};
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.pool = static_cast<const uint8_t*>(pool);
-  p.scales = scales;
-  p.page_table = page_table;
-  p.out = out;
-  p.lse = lse;
-  p.status = static_cast<int32_t*>(workspace);
-  p.pool_pages = pool_pages;
-  p.max_pages = max_pages;
-  p.T = T;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.G = Hq / Hkv;
-  p.scale = scale;
-  for (int bt0 = 0; bt0 < B * T; bt0 += kMaxTiles) {
-    const int n = B * T - bt0 < kMaxTiles ? B * T - bt0 : kMaxTiles;
-    p.bt0 = bt0;
-    for (int i = 0; i < n; ++i)
-      p.tiles[i] = make_int2(tiles[2 * (bt0 + i)], tiles[2 * (bt0 + i) + 1]);
-    if (D == 128)
-      PA_CHECK_CUDA(launch_dependent(decode_kernel<128>, dim3(n * Hkv), dim3(kWarps * 32), 0,
-                                     stream, p));
-    else
-      PA_CHECK_CUDA(launch_dependent(decode_kernel<256>, dim3(n * Hkv), dim3(kWarps * 32), 0,
-                                     stream, p));
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
+  CUtensorMap tmap;
+  {
+    const int row = 2 * Hkv * D;
+    const cuuint64_t dims[2] = {(cuuint64_t)row, (cuuint64_t)pool_pages * kPage};
+    const cuuint64_t strides[1] = {(cuuint64_t)row};
+    const cuuint32_t box[2] = {kChunk, kPage};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(&tmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims,
+                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   }
-  if (merged_out)
-    PA_CHECK_CUDA(launch_dependent(merge_kernel, dim3(B * Hq), dim3(32), 0, stream, out, lse, T,
-                                   Hq, D, merged_out, merged_lse));
-  PA_CHECK_CUDA(cudaGetLastError());
+  int sms = sm_count();
+  if (sms <= 0) return fail(PA_ERR_CUDA, "cannot query the device's SM count");
+  sms = std::min(sms, kMaxGrid);
+  Plan plan;
+  int rc = plan_units(tiles, B, T, Hkv, sms, launch_grid, kSegmentCharge, &plan);
+  if (rc != PA_OK) return rc;
+
+  Params<kMaxUnitsSmall> common{};
+  common.q = static_cast<const __nv_bfloat16*>(q);
+  common.scales = scales;
+  common.page_table = page_table;
+  common.out = out;
+  common.lse = lse;
+  const Workspace ws(workspace, B, T, Hkv, D);
+  common.status = ws.status;
+  common.arrivals = ws.arrivals;
+  common.req_counters = ws.req_counters;
+  common.part_o = ws.part_o;
+  common.part_ml = ws.part_ml;
+  common.pool_pages = pool_pages;
+  common.max_pages = max_pages;
+  common.T = T;
+  common.Hq = Hq;
+  common.Hkv = Hkv;
+  common.G = Hq / Hkv;
+  common.scale_log2 = scale * kLog2e;
+  common.m_out = merged_out;
+  common.m_lse = merged_lse;
+  const TestHooks hooks = take_test_hooks();
+  common.wait_limit_ns = hooks.wait_limit_ns;
+  common.stall_iteration = hooks.stall_iteration;
+  common.slice_wait_ns = hooks.slice_wait_ns;
+  for (const Launch& L : plan.launches) {
+    const bool small = L.n <= (size_t)kMaxUnitsSmall;
+    if (D == 128)
+      rc = small ? launch_units<128, kMaxUnitsSmall>(tmap, plan, L, common, stream)
+                 : launch_units<128, kMaxUnitsLarge>(tmap, plan, L, common, stream);
+    else
+      rc = small ? launch_units<256, kMaxUnitsSmall>(tmap, plan, L, common, stream)
+                 : launch_units<256, kMaxUnitsLarge>(tmap, plan, L, common, stream);
+    if (rc != PA_OK) return rc;
+  }
   return PA_OK;
 }
 
@@ -213,9 +903,9 @@ extern "C" size_t paged_decode_attn_q8_workspace_bytes(int B, int T, int n_q_hea
                                                        int head_dim) {
   if (B < 0 || T < 0 || (head_dim != 128 && head_dim != 256) || n_kv_heads < 1 ||
       n_q_heads < n_kv_heads || n_q_heads % n_kv_heads != 0 ||
-      n_q_heads / n_kv_heads > pa::decode_q8::kMaxG)
+      n_q_heads / n_kv_heads > pa::split::kMaxG)
     return 0;
-  return pa::decode_q8::workspace_bytes();
+  return pa::split::workspace_bytes(B, T, n_kv_heads, head_dim);
 }
 
 extern "C" int paged_decode_attn_q8_lse(const void* q, const void* pool, const float* scales,
@@ -226,7 +916,11 @@ extern "C" int paged_decode_attn_q8_lse(const void* q, const void* pool, const f
                                         float* merged_lse, void* workspace,
                                         size_t workspace_bytes, cudaStream_t stream) {
   pa::clear_error();
-  return pa::decode_q8::run(q, pool, scales, pool_pages, page_table, max_pages, tiles, B, T,
-                            n_q_heads, n_kv_heads, head_dim, scale, out, lse, merged_out,
-                            merged_lse, workspace, workspace_bytes, stream);
+  try {
+    return pa::decode_q8::run(q, pool, scales, pool_pages, page_table, max_pages, tiles, B, T,
+                              n_q_heads, n_kv_heads, head_dim, scale, out, lse, merged_out,
+                              merged_lse, workspace, workspace_bytes, stream);
+  } catch (const std::exception& e) {
+    return pa::fail(PA_ERR_INVALID, "host memory for the plan: %s", e.what());
+  }
 }

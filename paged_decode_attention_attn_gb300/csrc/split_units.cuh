@@ -47,6 +47,7 @@ constexpr uint64_t kSliceWaitNs = 50000ull;
 // a widely split unit's CTAs leave at once (their SMs then take the next
 // launch's first page loads).
 constexpr int kMaxSlices = 16;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;         // 2 s per bounded device wait
 // Per unit: a 64-bit arrival word (count | leavers << 16 | generation << 32).
 constexpr size_t kCounterBytes = 8 * kMaxUnitsLarge;
 constexpr float kLn2Hi = 0.693145751953125f;        // ln 2, high bits (exact products)
@@ -335,6 +336,20 @@ __device__ __forceinline__ void finish_split_unit(const P& p, const Sh& sh, cons
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
+// Settings of the test hooks (paged_decode_attn_test_stall and
+// _test_slice_wait): consumed by the next decode call on the calling thread.
+struct TestHooks {
+  int stall_iteration = -1;
+  unsigned long long wait_limit_ns = kWaitLimitNs;
+  unsigned long long slice_wait_ns = kSliceWaitNs;
+};
+extern thread_local TestHooks t_hooks;
+inline TestHooks take_test_hooks() {
+  const TestHooks h = t_hooks;
+  t_hooks = TestHooks();
+  return h;
+}
+
 // Partial slots reserved: one per unit of a launch plus one per CTA (a CTA
 // adds at most one split point), with room for grids up to 1,024 CTAs.
 inline size_t part_slots(int B, int T, int Hkv) {

@@ -302,3 +302,28 @@ def test_a_step_of_appends_and_attention(B, d):
         c.tiles = np.array([[(0, a)] for a in at], np.int32)
         assert c.run(B) == 0
         c.check()
+
+
+def test_ctas_that_leave_the_merge_to_the_last_one(B):
+    """A split unit's CTAs that do not wait for each other give the same bits."""
+    c = Case([20000, 9000], hq=24, hkv=4, d=256, seed=20)
+    assert c.run(B) == 0
+    want = [t.clone() for t in (c.out, c.lse, c.merged, c.merged_lse)]
+    B.test_slice_wait(0)
+    assert c.run(B) == 0
+    assert all(torch.equal(a, b) for a, b in zip(want, (c.out, c.lse, c.merged, c.merged_lse)))
+
+
+@pytest.mark.parametrize("iteration", [0, 1, 4])
+def test_a_wait_that_runs_out_is_reported_and_the_context_survives(B, iteration):
+    """One step's loads of CTA 0 stay unarmed; with a 50 ms limit every warp
+    gives up, the call reports it, and the next one is right again."""
+    c = Case([64000], hq=24, hkv=4, d=256, seed=21)
+    assert c.run(B) == 0
+    want = c.out.clone()
+    B.test_stall(iteration, 50_000_000)
+    assert c.run(B) & B.PA_STATUS_TIMEOUT
+    c.ws = None
+    c.out.zero_()
+    assert c.run(B) == 0
+    assert torch.equal(c.out, want)
