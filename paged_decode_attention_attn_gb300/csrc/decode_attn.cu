@@ -80,6 +80,7 @@ static_assert(kSmemAlloc <= 232448, "shared memory budget");
 
 template <int kMaxUnits>
 struct Params {
+  static constexpr bool kSecondOut = false;
   const __nv_bfloat16* q;
   const int32_t* page_table;
   float* out;

@@ -23,8 +23,13 @@
 //    8 kParts, K = 128 tokens.  Every step's product starts from zero in tensor
 //    memory and is added to fp32 registers (a thread per dim), so the long sum
 //    is rounded to nearest and rescaled there.
-//  * Warps: 0-3 softmax, 4-7 output, 8 TMA, 9 MMA, 10 q.  All waits are on
-//    mbarriers with a time limit; S, P and the products have two buffers each.
+//  * Warps: 0-3 softmax, 4-7 output, 8 TMA, 9 first product, 10 second product,
+//    11-14 q.  All waits are on mbarriers with a time limit; S, P and the
+//    products have two buffers each.  Each product has a warp of its own: with
+//    one thread for both, a step of 256 dims took 1.4 us, 0.86 us of it the
+//    issue of its 16 instructions and the rest waits that did not overlap.
+//  * A launch starts under programmatic dependent launch; only what reads or
+//    writes global memory waits for the kernels before it.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -57,8 +62,10 @@ constexpr int kTmemCols = 256;
 constexpr int kRefs = 4;                    // reference slots, two steps more than P buffers
 constexpr int kSoftmaxWarps = 4, kOutWarps = 4;
 constexpr int kOut = kOutWarps * 32;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 32 * 11;           // the last warp: q
+constexpr int kTmaWarp = 8, kScoreWarp = 9, kProductWarp = 10, kFirstQWarp = 11;
+constexpr int kQWarps = 4;
+constexpr int kThreads = 32 * (kFirstQWarp + kQWarps);
+constexpr int kHeadsPerQWarp = kMaxG / kQWarps;
 constexpr int kSegmentCharge = 6;           // pages charged per unit start
 constexpr int kWidePages = 32, kWideGridPct = 90;
 constexpr float kLog2e = 1.44269504088896341f;
@@ -89,11 +96,11 @@ struct Smem {
   static constexpr int kWarpMax = kSegRef + 2 * kMaxG * 4;         // [warp][kMaxG]
   static constexpr int kBars = kWarpMax + kSoftmaxWarps * kMaxG * 4;
   // mbarriers: full, empty per stage; S, P, product, q, sums: full and empty;
-  // all products done; reference slots written
+  // all of a warp's products done; reference slots written
   static constexpr int kFull = 0, kEmpty = kStages, kSFull = 2 * kStages, kSEmpty = kSFull + 2,
                        kPFull = kSEmpty + 2, kOFull = kPFull + 2, kOEmpty = kOFull + 2,
                        kQFull = kOEmpty + 2, kQEmpty = kQFull + 2, kLFull = kQEmpty + 2,
-                       kLEmpty = kLFull + 2, kDrain = kLEmpty + 2, kRefFull = kDrain + 1,
+                       kLEmpty = kLFull + 2, kDrain = kLEmpty + 2, kRefFull = kDrain + 2,
                        kNumBars = kRefFull + kRefs;
   static constexpr int kMisc = kBars + kNumBars * 8;               // ints, see View
   static constexpr int kUsed = kMisc + (kStages + 2 + 8) * 4;
@@ -128,6 +135,10 @@ struct Params {
   unsigned long long slice_wait_ns;
   float* m_out;
   float* m_lse;
+  // One tile per request: its output is the merged one too, written with it.
+  static constexpr bool kSecondOut = true;
+  float* out2;
+  float* lse2;
   Unit units[kMaxUnits];
 };
 static_assert(sizeof(Params<kMaxUnitsLarge>) <= 32764, "kernel parameters too large");
@@ -232,11 +243,14 @@ __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtens
   int it = 0;
   bool ok = true;
   const uint64_t pol = ptx::policy_evict_first();   // every page is read once
-  for_segments(p, [&](const Segment& s, int) {
+  for_segments(p, [&](const Segment& s, int seg) {
+    if (seg == 0) ptx::grid_dependency_wait();
     const int32_t* prow = p.page_table + (size_t)s.b * p.max_pages + s.U.tok_start / kPage;
+    int next_pid = s.lo + lane < s.hi ? __ldg(prow + s.lo + lane) : 0;
     for (int base = s.lo; ok && base < s.hi; base += 32) {
       const int cnt = min(32, s.hi - base);
-      const int my_pid = lane < cnt ? __ldg(prow + base + lane) : 0;
+      const int my_pid = next_pid;
+      if (base + 32 + lane < s.hi) next_pid = __ldg(prow + base + 32 + lane);
       for (int j = 0; ok && j < cnt; j += 2, ++it) {
         const int stage = it % S::kStages;
         const int n = min(2, cnt - j);
@@ -290,126 +304,158 @@ __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtens
 }
 
 // ---------------------------------------------------------------------------
-// Warp 9, one thread: the products.
+// Warp 9: scores.  Warp 10: products with V.  The whole warp follows the steps,
+// so that descriptors stay in uniform registers; one elected lane issues.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// Every product this warp issued, and every arrival that follows from one,
+// ends before the CTA can.
+template <class P>
+__device__ __forceinline__ void drain(const P& p, const View& v, int bar) {
+  if (elect()) tc::commit(v.bar(bar));
+  __syncwarp();
+  ptx::mbar_wait_bounded(v.bar(bar), 0, p.wait_limit_ns);
+}
+
 template <int D, class P>
-__device__ __forceinline__ void mma_thread(const P& p, const View& v, uint32_t tmem) {
+__device__ __forceinline__ void score_warp(const P& p, const View& v, uint32_t tmem) {
   using S = Smem<D>;
-  constexpr uint32_t kIdescS = tc::idesc_e4m3(kStep, kQCols, false);
-  constexpr uint32_t kIdescO = tc::idesc_e4m3(kChunk, kPCols, true);
+  constexpr uint32_t kIdesc = tc::idesc_e4m3(kStep, kQCols, false);
   int it = 0;
-  int last_pages = 0;
-  bool ok = true;
-  // O^T of step j: its K = 32 token slices, of the pages that were loaded.
-  auto second = [&](int j, int pages) {
-    ok = wait_phase(p, v, S::kPFull + (j & 1), j >> 1) &&
-         (j < 2 || wait_phase(p, v, S::kOEmpty + (j & 1), (j >> 1) - 1));
-    if (!ok) return;
-    tc::fence_after();
-    const uint32_t val = v.addr + (j % S::kStages) * S::kStageBytes + S::kHalfBytes;
-    const uint64_t pd = tc::desc_sw128(v.addr + S::kP + (j & 1) * S::kPBytes);
-    const uint32_t d = tmem + 2 * kQCols + (j & 1) * S::kChunks * kPCols;
-#pragma unroll
-    for (int c = 0; c < S::kChunks; ++c) {
-      for (int k = 0; k < 2 * pages; ++k)
-        tc::mma_e4m3(d + c * kPCols, tc::desc_sw128(val + c * S::kChunkBytes + k * 32 * kChunk),
-                     pd + 2 * k, kIdescO, k > 0);
-    }
-    tc::commit(v.bar(S::kOFull + (j & 1)));
-    tc::commit(v.bar(S::kEmpty + j % S::kStages));
-  };
   for_segments(p, [&](const Segment& s, int seg) {
-    ok = ok && wait_phase(p, v, S::kQFull + (seg & 1), seg >> 1);
+    if (!__all_sync(0xffffffffu, wait_phase(p, v, S::kQFull + (seg & 1), seg >> 1))) return false;
     const int steps = s.steps();
-    for (int i = 0; ok && i < steps; ++i, ++it) {
+    for (int i = 0; i < steps; ++i, ++it) {
       const int stage = it % S::kStages;
-      ok = wait_phase(p, v, S::kFull + stage, it / S::kStages) &&
-           (it < 2 || wait_phase(p, v, S::kSEmpty + (it & 1), (it >> 1) - 1));
-      if (!ok) break;
+      const bool ok = wait_phase(p, v, S::kFull + stage, it / S::kStages) &&
+                      (it < 2 || wait_phase(p, v, S::kSEmpty + (it & 1), (it >> 1) - 1));
+      if (!__all_sync(0xffffffffu, ok)) return false;
       tc::fence_after();
-      const uint32_t key = v.addr + stage * S::kStageBytes;
-      const uint32_t qs = v.addr + S::kQ + (seg & 1) * S::kQBytes;
+      const uint64_t a = tc::desc_sw128(v.addr + stage * S::kStageBytes);
+      const uint64_t b = tc::desc_sw128(v.addr + S::kQ + (seg & 1) * S::kQBytes);
+      if (elect()) {
 #pragma unroll
-      for (int c = 0; c < S::kChunks; ++c) {
-        const uint64_t a = tc::desc_sw128(key + c * S::kChunkBytes);
-        const uint64_t b = tc::desc_sw128(qs + c * S::kQChunkBytes);
+        for (int c = 0; c < S::kChunks; ++c) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc::mma_e4m3(tmem + (it & 1) * kQCols, a + 2 * k, b + 2 * k, kIdescS, c + k > 0);
+          for (int k = 0; k < 4; ++k)
+            tc::mma_e4m3(tmem + (it & 1) * kQCols, a + (c * S::kChunkBytes >> 4) + 2 * k,
+                         b + (c * S::kQChunkBytes >> 4) + 2 * k, kIdesc, c + k > 0);
+        }
+        tc::commit(v.bar(S::kSFull + (it & 1)));
+        if (i == steps - 1) tc::commit(v.bar(S::kQEmpty + (seg & 1)));
       }
-      tc::commit(v.bar(S::kSFull + (it & 1)));
-      if (i == steps - 1) tc::commit(v.bar(S::kQEmpty + (seg & 1)));
-      if (it > 0) second(it - 1, last_pages);
-      last_pages = min(2, s.hi - (s.lo + 2 * i));
+      __syncwarp();
     }
-    return ok;
+    return true;
   });
-  if (ok && it > 0) second(it - 1, last_pages);
-  // Every product, and every arrival that follows from one, ends before the
-  // CTA can.
-  tc::commit(v.bar(S::kDrain));
-  ptx::mbar_wait_bounded(v.bar(S::kDrain), 0, p.wait_limit_ns);
+  drain(p, v, S::kDrain);
+}
+
+template <int D, class P>
+__device__ __forceinline__ void product_warp(const P& p, const View& v, uint32_t tmem) {
+  using S = Smem<D>;
+  constexpr uint32_t kIdesc = tc::idesc_e4m3(kChunk, kPCols, true);
+  constexpr uint32_t kSlice = 32 * kChunk >> 4;   // 32 tokens of a chunk, in descriptor units
+  int it = 0;
+  for_segments(p, [&](const Segment& s, int) {
+    const int steps = s.steps();
+    for (int i = 0; i < steps; ++i, ++it) {
+      const int stage = it % S::kStages;
+      const bool two = s.lo + 2 * i + 1 < s.hi;   // both pages of the step are there
+      const bool ok = wait_phase(p, v, S::kPFull + (it & 1), it >> 1) &&
+                      (it < 2 || wait_phase(p, v, S::kOEmpty + (it & 1), (it >> 1) - 1));
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      tc::fence_after();
+      const uint64_t a = tc::desc_sw128(v.addr + stage * S::kStageBytes + S::kHalfBytes);
+      const uint64_t b = tc::desc_sw128(v.addr + S::kP + (it & 1) * S::kPBytes);
+      const uint32_t d = tmem + 2 * kQCols + (it & 1) * S::kChunks * kPCols;
+      if (elect()) {
+#pragma unroll
+        for (int c = 0; c < S::kChunks; ++c) {
+          const uint64_t ac = a + (c * S::kChunkBytes >> 4);
+          tc::mma_e4m3(d + c * kPCols, ac, b, kIdesc, false);
+          tc::mma_e4m3(d + c * kPCols, ac + kSlice, b + 2, kIdesc, true);
+          if (two) {
+            tc::mma_e4m3(d + c * kPCols, ac + 2 * kSlice, b + 4, kIdesc, true);
+            tc::mma_e4m3(d + c * kPCols, ac + 3 * kSlice, b + 6, kIdesc, true);
+          }
+        }
+        tc::commit(v.bar(S::kOFull + (it & 1)));
+        tc::commit(v.bar(S::kEmpty + stage));
+      }
+      __syncwarp();
+    }
+    return true;
+  });
+  drain(p, v, S::kDrain + 1);
 }
 
 // ---------------------------------------------------------------------------
-// Warp 10: q of each segment as hi and lo parts, and its scale.
+// Warps 11-14, two heads each: q of a segment as hi and lo parts, and its
+// scale.  (One warp for all heads took 2.2 us at 128 dims and 4.8 at 256, the
+// longest part of a launch's start.)
 // ---------------------------------------------------------------------------
 template <int D, class P>
-__device__ __forceinline__ void q_warp(const P& p, const View& v, int lane) {
+__device__ __forceinline__ void q_warp(const P& p, const View& v, int warp, int lane) {
   using S = Smem<D>;
   constexpr int kDims = D / 32;             // dims per lane
   using Vec = typename std::conditional<kDims == 8, uint4, uint2>::type;
   for_segments(p, [&](const Segment& s, int seg) {
-    if (seg >= 2 && !wait_phase(p, v, S::kQEmpty + (seg & 1), (seg >> 1) - 1)) return false;
-    const uint32_t buf = v.addr + S::kQ + (seg & 1) * S::kQBytes;
-    float* qscale = reinterpret_cast<float*>(v.base + S::kQScale) + (seg & 1) * kMaxG;
+    if (seg == 0) ptx::grid_dependency_wait();
     const __nv_bfloat16* src = p.q + ((size_t)s.b * p.Hq + s.g * p.G) * D + lane * kDims;
-    Vec raw[kMaxG];
+    Vec raw[kHeadsPerQWarp];
 #pragma unroll
-    for (int h = 0; h < kMaxG; ++h) {
-      raw[h] = Vec{};
-      if (h < p.G) raw[h] = __ldg(reinterpret_cast<const Vec*>(src + h * D));
+    for (int i = 0; i < kHeadsPerQWarp; ++i) {
+      const int h = warp * kHeadsPerQWarp + i;
+      raw[i] = Vec{};
+      if (h < p.G) raw[i] = __ldg(reinterpret_cast<const Vec*>(src + h * D));
     }
+    if (seg >= 2 && !__all_sync(0xffffffffu, wait_phase(p, v, S::kQEmpty + (seg & 1),
+                                                        (seg >> 1) - 1)))
+      return false;
+    float* qscale = reinterpret_cast<float*>(v.base + S::kQScale) + (seg & 1) * kMaxG;
+    const int col = lane * kDims;
+    const uint32_t buf = v.addr + S::kQ + (seg & 1) * S::kQBytes +
+                         col / kChunk * S::kQChunkBytes + (col & 15);
 #pragma unroll
-    for (int h = 0; h < kMaxG; ++h) {
+    for (int i = 0; i < kHeadsPerQWarp; ++i) {
+      const int h = warp * kHeadsPerQWarp + i;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[i]);
       float y[kDims];
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[h]);
       unsigned amax = 0;
 #pragma unroll
-      for (int i = 0; i < kDims / 2; ++i) {
-        y[2 * i] = ptx::bf16_lo_to_f32(w[i]);
-        y[2 * i + 1] = ptx::bf16_hi_to_f32(w[i]);
+      for (int k = 0; k < kDims / 2; ++k) {
+        y[2 * k] = ptx::bf16_lo_to_f32(w[k]);
+        y[2 * k + 1] = ptx::bf16_hi_to_f32(w[k]);
+        amax = max(amax, max(__float_as_uint(y[2 * k]) & 0x7fffffffu,
+                             __float_as_uint(y[2 * k + 1]) & 0x7fffffffu));
       }
-#pragma unroll
-      for (int i = 0; i < kDims; ++i) amax = max(amax, __float_as_uint(y[i]) & 0x7fffffffu);
       amax = __reduce_max_sync(0xffffffffu, amax);
       // largest value to [128, 256); NaN and infinities to NaN codes
       const int e = amax ? min(7 - ((int)(amax >> 23) - 127), 120) : 0;
       const float up = ptx::pow2i(e);
       if (lane == 0) qscale[h] = p.scale_log2 * ptx::pow2i(-e);
-      uint32_t hi[kDims / 4], lo[kDims / 4];
+      const uint32_t at = buf + h * kChunk + (((col % kChunk >> 4) ^ h) << 4);
 #pragma unroll
-      for (int i = 0; i < kDims / 4; ++i) {
+      for (int k = 0; k < kDims / 4; ++k) {
         float z[4], f[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          z[k] = fabsf(y[4 * i + k]) <= 3.4e38f ? y[4 * i + k] * up : __int_as_float(0x7fc00000);
-        hi[i] = fp8::pack4(z[0], z[1], z[2], z[3]);
-        fp8::unpack4(hi[i], f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) z[k] = (z[k] - f[k]) * 16.f;
-        lo[i] = fp8::pack4(z[0], z[1], z[2], z[3]);
-      }
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        const int row = part * kMaxG + h;
-        const int col = lane * kDims;
-        const uint32_t at = buf + col / kChunk * S::kQChunkBytes + row * kChunk +
-                            (((col % kChunk >> 4) ^ (row & 7)) << 4) + (col & 15);
-#pragma unroll
-        for (int i = 0; i < kDims / 4; ++i)
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * i), "r"(part ? lo[i] : hi[i])
-                       : "memory");
+        for (int j = 0; j < 4; ++j)
+          z[j] = fabsf(y[4 * k + j]) <= 3.4e38f ? y[4 * k + j] * up : __int_as_float(0x7fc00000);
+        const uint32_t hi = fp8::pack4(z[0], z[1], z[2], z[3]);
+        fp8::unpack4(hi, f);
+        const uint32_t lo = fp8::pack4((z[0] - f[0]) * 16.f, (z[1] - f[1]) * 16.f,
+                                       (z[2] - f[2]) * 16.f, (z[3] - f[3]) * 16.f);
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * k), "r"(hi) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + kMaxG * kChunk + 4 * k), "r"(lo)
+                     : "memory");
       }
     }
     ptx::fence_proxy_async_smem();
@@ -498,14 +544,16 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
           ref[h] = to;
         }
       }
+      // Step it - 2's product is done: its P buffer is free, and so is the
+      // reference slot of step it - 4 (the product waited for the output warps
+      // to be through with that step).
+      if (it >= 2) fail = !wait_phase(p, v, S::kOFull + (it & 1), (it >> 1) - 1);
       if (tok == 0) {
         float* slot = reinterpret_cast<float*>(v.base + S::kRef) + (it % kRefs) * kMaxG;
 #pragma unroll
         for (int h = 0; h < kMaxG; ++h) slot[h] = ref[h];
         ptx::mbar_arrive(v.bar(S::kRefFull + it % kRefs));
       }
-      // the product that read this P buffer is done
-      if (it >= 2) fail = !wait_phase(p, v, S::kOFull + (it & 1), (it >> 1) - 1);
       const uint32_t prow = v.addr + S::kP + (it & 1) * S::kPBytes + (tok & 15);
       const int chunk = tok >> 4;
 #pragma unroll
@@ -582,6 +630,7 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
   using S = Smem<D>;
   const int ct = warp * 32 + lane;
   const float qnan = __int_as_float(0x7fc00000);
+  ptx::grid_dependency_wait();   // earlier kernels may still read the outputs
   // Empty units: output 0, LSE -inf.
   for (int u = blockIdx.x; u < p.n_units; u += p.grid) {
     const Unit U = p.units[u];
@@ -589,8 +638,14 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
     const int bt = U.bt_g / p.Hkv;
     const int g = U.bt_g - bt * p.Hkv;
     const size_t orow = (size_t)bt * p.Hq + g * p.G;
-    for (int i = ct; i < p.G * D; i += kOut) p.out[orow * D + i] = 0.f;
-    if (ct < p.G) p.lse[orow + ct] = -INFINITY;
+    for (int i = ct; i < p.G * D; i += kOut) {
+      p.out[orow * D + i] = 0.f;
+      if (p.out2) p.out2[orow * D + i] = 0.f;
+    }
+    if (ct < p.G) {
+      p.lse[orow + ct] = -INFINITY;
+      if (p.lse2) p.lse2[orow + ct] = -INFINITY;
+    }
     finish_unit<D, kOut>(p, v, bt / p.T, g, ct, warp, lane, 1, U.pair_total);
   }
   int it = 0;
@@ -674,9 +729,16 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
       for (int h = 0; h < kMaxG; ++h) {
         if (h >= p.G) continue;
 #pragma unroll
-        for (int c = 0; c < S::kChunks; ++c)
-          p.out[(orow + h) * D + c * kChunk + ct] = nan ? qnan : acc[c][h] / l[h];
-        if (ct == h) p.lse[orow + h] = nan ? qnan : lse_of(ref[h], l[h]);
+        for (int c = 0; c < S::kChunks; ++c) {
+          const float o = nan ? qnan : acc[c][h] / l[h];
+          p.out[(orow + h) * D + c * kChunk + ct] = o;
+          if (p.out2) p.out2[(orow + h) * D + c * kChunk + ct] = o;
+        }
+        if (ct == h) {
+          const float x = nan ? qnan : lse_of(ref[h], l[h]);
+          p.lse[orow + h] = x;
+          if (p.lse2) p.lse2[orow + h] = x;
+        }
       }
       finish_unit<D, kOut>(p, v, s.b, s.g, ct, warp, lane, 1, s.U.pair_total);
     } else {
@@ -735,34 +797,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i >= S::kQEmpty && i < S::kLFull) n = kSoftmaxWarps + 1;    // and the last product
       if (i >= S::kLFull && i < S::kLEmpty) n = kSoftmaxWarps;
       if (i >= S::kLEmpty && i < S::kDrain) n = kOutWarps;
+      if (i >= S::kQFull && i < S::kQEmpty) n = kQWarps;
       ptx::mbar_init(v.bar(i), n);
     }
     *v.abort_flag = 0;
     ptx::mbar_init_fence();
   }
   if (warp == kTmaWarp && lane == 0) ptx::prefetch_tensormap(&tmap);
-  if (warp == kMmaWarp) tc::alloc(ptx::smem_addr(tmem_slot), kTmemCols);
+  if (warp == kScoreWarp) tc::alloc(ptx::smem_addr(tmem_slot), kTmemCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile int*>(tmem_slot);
-  ptx::grid_dependency_wait();
   if (warp < kSoftmaxWarps) {
     softmax_warps<D>(p, v, tmem, warp, lane);
   } else if (warp < kSoftmaxWarps + kOutWarps) {
     output_warps<D>(p, v, tmem, warp - kSoftmaxWarps, lane);
   } else if (warp == kTmaWarp) {
     tma_warp<D>(p, v, &tmap, lane);
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) mma_thread<D>(p, v, tmem);
+  } else if (warp == kScoreWarp) {
+    score_warp<D>(p, v, tmem);
+  } else if (warp == kProductWarp) {
+    product_warp<D>(p, v, tmem);
   } else {
-    q_warp<D>(p, v, lane);
+    q_warp<D>(p, v, warp - kFirstQWarp, lane);
   }
   __syncwarp();
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == kMmaWarp) tc::dealloc(tmem, kTmemCols);
+  if (warp == kScoreWarp) tc::dealloc(tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------------------
@@ -877,8 +941,8 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   common.Hkv = Hkv;
   common.G = Hq / Hkv;
   common.scale_log2 = scale * kLog2e;
-  common.m_out = merged_out;
-  common.m_lse = merged_lse;
+  (T == 1 ? common.out2 : common.m_out) = merged_out;
+  (T == 1 ? common.lse2 : common.m_lse) = merged_lse;
   const TestHooks hooks = take_test_hooks();
   common.wait_limit_ns = hooks.wait_limit_ns;
   common.stall_iteration = hooks.stall_iteration;

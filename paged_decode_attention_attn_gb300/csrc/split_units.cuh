@@ -6,7 +6,8 @@
 // into one contiguous page range per CTA.  A kernel's parameter struct P has
 // the fields these functions name (out, lse, status, arrivals, req_counters,
 // part_o, part_ml, total_pages, grid, T, Hq, Hkv, G, n_units, units, m_out,
-// m_lse, wait_limit_ns, slice_wait_ns); its shared-memory view Sh has fin_flag
+// m_lse, wait_limit_ns, slice_wait_ns, and out2, lse2 where kSecondOut says that
+// outputs are written twice); its shared-memory view Sh has fin_flag
 // and merge_info.  The kConsumers threads that call a function meet at named
 // barrier 1.
 #pragma once
@@ -231,10 +232,17 @@ __device__ __forceinline__ void merge_split_slice(const P& p, int part_base, int
     if (have && j == 0) {
       const size_t orow = orow0 + row;
       const float qnan = __int_as_float(0x7fc00000);
-      reinterpret_cast<float4*>(p.out + orow * kD)[dv] =
-          nan ? make_float4(qnan, qnan, qnan, qnan)
-              : make_float4(acc.x / l, acc.y / l, acc.z / l, acc.w / l);
-      if (dv == 0) p.lse[orow] = nan ? qnan : lse_of(big_m, l);
+      const float4 v4 = nan ? make_float4(qnan, qnan, qnan, qnan)
+                            : make_float4(acc.x / l, acc.y / l, acc.z / l, acc.w / l);
+      reinterpret_cast<float4*>(p.out + orow * kD)[dv] = v4;
+      const float x = dv == 0 ? (nan ? qnan : lse_of(big_m, l)) : 0.f;
+      if (dv == 0) p.lse[orow] = x;
+      if constexpr (P::kSecondOut) {
+        if (p.out2) {
+          reinterpret_cast<float4*>(p.out2 + orow * kD)[dv] = v4;
+          if (dv == 0) p.lse2[orow] = x;
+        }
+      }
     }
   }
 }
