@@ -12,7 +12,8 @@
 //    scaled by a power of two per head and held as hi + lo / 16 in e4m3 (4 bits
 //    each, and a sign between them): 16 columns for 8 heads, exact for values
 //    down to 2^-14 of the head's largest.
-//  * Softmax: a thread per token.  Scores are kept relative to a running
+//  * Softmax: a thread per token, two groups of threads taking every other step,
+//    each with its own reference and sum.  Scores are kept relative to a running
 //    reference per head, a multiple of 8 (log2), that bounds x_j + log2 sv_j
 //    (sv the token's V scale), so w_j = 2^(x_j - ref) sv_j lies in [0, 1] and
 //    the largest in (2^-8, 1] whatever the scales; it moves rarely, and then by
@@ -23,11 +24,14 @@
 //    8 kParts, K = 128 tokens.  Every step's product starts from zero in tensor
 //    memory and is added to fp32 registers (a thread per dim), so the long sum
 //    is rounded to nearest and rescaled there.
-//  * Warps: 0-3 softmax, 4-7 output, 8 TMA, 9 first product, 10 second product,
-//    11-14 q.  All waits are on mbarriers with a time limit; S, P and the
-//    products have two buffers each.  Each product has a warp of its own: with
-//    one thread for both, a step of 256 dims took 1.4 us, 0.86 us of it the
-//    issue of its 16 instructions and the rest waits that did not overlap.
+//  * Warps: 0-7 softmax, 8-11 output, 12 TMA, 13 scores, 14 products, 15 q (16
+//    warps leave 128 registers a thread; 17 leave 96).  All waits are on
+//    mbarriers with a time limit; S, P and the products have two buffers each.
+//    Each product has a warp of its own: with one thread for both, a step of
+//    256 dims took 1.4 us, 0.86 us of it the issue of its 16 instructions and
+//    the rest waits that did not overlap.  K and V have a ring each, because a
+//    K stage is free as soon as its scores are, a V stage a softmax and a
+//    product later.
 //  * A launch starts under programmatic dependent launch; only what reads or
 //    writes global memory waits for the kernels before it.
 #include <cuda.h>
@@ -60,18 +64,19 @@ constexpr int kQCols = 2 * kMaxG;           // N of the first product
 constexpr int kChunk = 128;                 // dims per 128-byte row
 constexpr int kTmemCols = 256;
 constexpr int kRefs = 4;                    // reference slots, two steps more than P buffers
-constexpr int kSoftmaxWarps = 4, kOutWarps = 4;
+constexpr int kGroups = 2;                  // softmax groups
+constexpr int kGroupWarps = 4, kOutWarps = 4;
 constexpr int kOut = kOutWarps * 32;
-constexpr int kTmaWarp = 8, kScoreWarp = 9, kProductWarp = 10, kFirstQWarp = 11;
-constexpr int kQWarps = 4;
-constexpr int kThreads = 32 * (kFirstQWarp + kQWarps);
-constexpr int kHeadsPerQWarp = kMaxG / kQWarps;
+constexpr int kSoftmaxWarps = kGroups * kGroupWarps;
+constexpr int kTmaWarp = 12, kScoreWarp = 13, kProductWarp = 14;
+constexpr int kScaleCopies = 4;             // lanes that copy a step's scales
+constexpr int kThreads = 32 * 16;           // the last warp: q
 constexpr int kSegmentCharge = 6;           // pages charged per unit start
 constexpr int kWidePages = 32, kWideGridPct = 90;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kMaxScaleExp = 100;           // largest |log2| of a V scale
 
-static_assert(kStep == kSoftmaxWarps * 32 && kChunk == kOut, "a thread per token and per dim");
+static_assert(kStep == kGroupWarps * 32 && kChunk == kOut, "a thread per token and per dim");
 
 // Shared memory of a CTA; offsets from a 1024-byte boundary.
 template <int D>
@@ -80,30 +85,35 @@ struct Smem {
   static constexpr int kPageBytes = kPage * kChunk;              // one page, one chunk
   static constexpr int kChunkBytes = 2 * kPageBytes;             // one step, one chunk
   static constexpr int kHalfBytes = kChunks * kChunkBytes;       // K (or V) of a step
-  static constexpr int kStageBytes = 2 * kHalfBytes;
-  static constexpr int kStages = D == 256 ? 3 : 6;
+  static constexpr int kStages = D == 256 ? 3 : 6;               // of K, and of V
+  static constexpr int kV = kStages * kHalfBytes;
   static constexpr int kPBytes = kPCols * kChunk;
   static constexpr int kQChunkBytes = kQCols * kChunk;
   static constexpr int kQBytes = kChunks * kQChunkBytes;
-  static constexpr int kP = kStages * kStageBytes;
+  static constexpr int kP = 2 * kV;
   static constexpr int kQ = kP + 2 * kPBytes;
-  static constexpr int kScales = kQ + 2 * kQBytes;               // [stage][K | V][block]
+  // Scales and poison marks of a step come with its K.  The K of step i + kStages
+  // is loaded once the scores of step i are done, which the softmax of step i - 2
+  // (it has read its scales) precedes: kStages + 2 slots.
+  static constexpr int kSlots = kStages + 2;
+  static constexpr int kScales = kQ + 2 * kQBytes;               // [slot][K | V][block]
   static constexpr int kScaleBytes = 2 * kStepBlocks * 4;
-  static constexpr int kQScale = kScales + kStages * kScaleBytes;  // [2][kMaxG]
+  static constexpr int kQScale = kScales + kSlots * kScaleBytes;  // [2][kMaxG]
   static constexpr int kRef = kQScale + 2 * kMaxG * 4;             // [kRefs][kMaxG]
   static constexpr int kSegL = kRef + kRefs * kMaxG * 4;           // [2][warp][kMaxG]
-  static constexpr int kSegRef = kSegL + 2 * kSoftmaxWarps * kMaxG * 4;   // [2][kMaxG]
-  static constexpr int kWarpMax = kSegRef + 2 * kMaxG * 4;         // [warp][kMaxG]
+  static constexpr int kSegRef = kSegL + 2 * kSoftmaxWarps * kMaxG * 4;   // [2][group][kMaxG]
+  static constexpr int kWarpMax = kSegRef + 2 * kGroups * kMaxG * 4;      // [warp][kMaxG]
   static constexpr int kBars = kWarpMax + kSoftmaxWarps * kMaxG * 4;
-  // mbarriers: full, empty per stage; S, P, product, q, sums: full and empty;
-  // all of a warp's products done; reference slots written
-  static constexpr int kFull = 0, kEmpty = kStages, kSFull = 2 * kStages, kSEmpty = kSFull + 2,
-                       kPFull = kSEmpty + 2, kOFull = kPFull + 2, kOEmpty = kOFull + 2,
-                       kQFull = kOEmpty + 2, kQEmpty = kQFull + 2, kLFull = kQEmpty + 2,
-                       kLEmpty = kLFull + 2, kDrain = kLEmpty + 2, kRefFull = kDrain + 2,
-                       kNumBars = kRefFull + kRefs;
+  // mbarriers: full, empty per K and V stage; S, P, product, q, sums: full and
+  // empty; all of a warp's products done; reference slots written
+  static constexpr int kKFull = 0, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages,
+                       kVEmpty = kVFull + kStages, kSFull = kVEmpty + kStages,
+                       kSEmpty = kSFull + 2, kPFull = kSEmpty + 2, kOFull = kPFull + 2,
+                       kOEmpty = kOFull + 2, kQFull = kOEmpty + 2, kQEmpty = kQFull + 2,
+                       kLFull = kQEmpty + 2, kLEmpty = kLFull + 2, kDrain = kLEmpty + 2,
+                       kRefFull = kDrain + 2, kNumBars = kRefFull + kRefs;
   static constexpr int kMisc = kBars + kNumBars * 8;               // ints, see View
-  static constexpr int kUsed = kMisc + (kStages + 2 + 8) * 4;
+  static constexpr int kUsed = kMisc + (kSlots + 2 * kGroups + 6) * 4;
   static constexpr int kAlloc = kUsed + 1024;
   static_assert(kAlloc <= 232448, "shared memory budget");
 };
@@ -147,8 +157,8 @@ struct View {
   uint8_t* base;
   uint32_t addr;          // shared-space address of base
   uint32_t bars;
-  volatile int* poison;   // [stages] step holds a page that is not there
-  volatile int* seg_poison;  // [2]
+  volatile int* poison;      // [slots] step holds a page that is not there
+  volatile int* seg_poison;  // [2][group]
   volatile int* abort_flag;
   volatile int* fin_flag;
   volatile int* merge_info;
@@ -217,12 +227,24 @@ __device__ __forceinline__ bool any_in_group(int id, int threads, bool x) {
   return r != 0;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
+// One lane of a converged warp.  What a whole warp computes alike stays in
+// uniform registers, which TMA and tcgen05 instructions take their operands
+// from; a branch on the lane index would cost a move for each.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst), "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// 16 bytes from global to shared memory, and an arrival at `bar` once the
+// thread's copies have landed.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Largest of a warp's floats (NaN ignored): integer maximum of an order-preserving
@@ -234,87 +256,135 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// Warp 8: pages and scales into the stage ring.
+// Warp 12: the pages' K (with the step's scales) and V into their rings.  V
+// follows a step behind K, in the order in which the stages become free.
 // ---------------------------------------------------------------------------
+struct StepPages {
+  int pid[2];
+  int n;       // pages of the step
+  int head;
+};
+
+template <int D, class P>
+__device__ __forceinline__ bool load_keys(const P& p, const View& v, const CUtensorMap* tmap,
+                                          uint64_t pol, int it, int lane, StepPages& s) {
+  using S = Smem<D>;
+  const int stage = it % S::kStages, slot = it % S::kSlots;
+  const bool free = it < S::kStages || wait_phase(p, v, S::kKEmpty + stage, it / S::kStages - 1);
+  if (!__all_sync(0xffffffffu, free)) return false;
+  const uint32_t full = v.bar(S::kKFull + stage);
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    // a page that is not there: page 0 in its place, the step marked
+    if (k < s.n && (s.pid[k] < 0 || (long long)s.pid[k] >= p.pool_pages)) {
+      bad = true;
+      s.pid[k] = 0;
+    }
+  }
+  const bool armed = it != p.stall_iteration || blockIdx.x != 0;
+  if (elect()) {
+    if (bad) atomicOr(p.status, PA_STATUS_BAD_PAGE);
+    v.poison[slot] = bad ? 1 : 0;   // set before the arrival that publishes it
+    if (armed) {
+      ptx::mbar_arrive_expect_tx(full, s.n * S::kChunks * S::kPageBytes);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (k >= s.n) break;
+        const uint32_t dst = v.addr + stage * S::kHalfBytes + k * S::kPageBytes;
+#pragma unroll
+        for (int c = 0; c < S::kChunks; ++c)
+          ptx::tma_load_2d_hint(dst + c * S::kChunkBytes, tmap, s.head * D + c * kChunk,
+                                s.pid[k] * kPage, full, pol);
+      }
+    }
+  }
+  // The scales (K's and V's of each page, 16 bytes) by four lanes' copies: TMA
+  // operations of one thread go out ~80 ns apart, too slow for such pieces.
+  if (armed && lane < kScaleCopies) {
+    const int k = lane >> 1, kind = lane & 1;
+    if (k < s.n)
+      copy16(v.addr + S::kScales + slot * S::kScaleBytes + kind * kStepBlocks * 4 + k * 16,
+             p.scales + (((size_t)s.pid[k] * 2 + kind) * p.Hkv + s.head) * 4);
+    arrive_after_copies(full);
+  }
+  __syncwarp();
+  return true;
+}
+
+template <int D, class P>
+__device__ __forceinline__ bool load_values(const P& p, const View& v, const CUtensorMap* tmap,
+                                            uint64_t pol, int it, const StepPages& s) {
+  using S = Smem<D>;
+  const int stage = it % S::kStages;
+  const bool free = it < S::kStages || wait_phase(p, v, S::kVEmpty + stage, it / S::kStages - 1);
+  if (!__all_sync(0xffffffffu, free)) return false;
+  const uint32_t full = v.bar(S::kVFull + stage);
+  if (elect()) {
+    ptx::mbar_arrive_expect_tx(full, s.n * S::kChunks * S::kPageBytes);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k >= s.n) break;
+      const uint32_t dst = v.addr + S::kV + stage * S::kHalfBytes + k * S::kPageBytes;
+#pragma unroll
+      for (int c = 0; c < S::kChunks; ++c)
+        ptx::tma_load_2d_hint(dst + c * S::kChunkBytes, tmap, (p.Hkv + s.head) * D + c * kChunk,
+                              s.pid[k] * kPage, full, pol);
+    }
+  }
+  __syncwarp();
+  return true;
+}
+
 template <int D, class P>
 __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtensorMap* tmap,
                                          int lane) {
   using S = Smem<D>;
-  int it = 0;
-  bool ok = true;
+  int keys = 0, values = 0;   // steps loaded
+  StepPages last;
   const uint64_t pol = ptx::policy_evict_first();   // every page is read once
   for_segments(p, [&](const Segment& s, int seg) {
     if (seg == 0) ptx::grid_dependency_wait();
     const int32_t* prow = p.page_table + (size_t)s.b * p.max_pages + s.U.tok_start / kPage;
     int next_pid = s.lo + lane < s.hi ? __ldg(prow + s.lo + lane) : 0;
-    for (int base = s.lo; ok && base < s.hi; base += 32) {
+    for (int base = s.lo; base < s.hi; base += 32) {
       const int cnt = min(32, s.hi - base);
       const int my_pid = next_pid;
       if (base + 32 + lane < s.hi) next_pid = __ldg(prow + base + 32 + lane);
-      for (int j = 0; ok && j < cnt; j += 2, ++it) {
-        const int stage = it % S::kStages;
-        const int n = min(2, cnt - j);
-        const int pid0 = __shfl_sync(0xffffffffu, my_pid, j);
-        const int pid1 = __shfl_sync(0xffffffffu, my_pid, (j + 1) & 31);
-        if (lane == 0) {
-          ok = it < S::kStages || wait_phase(p, v, S::kEmpty + stage, it / S::kStages - 1);
-          if (ok) {
-            const uint32_t full = v.bar(S::kFull + stage);
-            const uint32_t dst = v.addr + stage * S::kStageBytes;
-            const uint32_t sc = v.addr + S::kScales + stage * S::kScaleBytes;
-            // set before the arrival that publishes it
-            const bool bad0 = pid0 < 0 || (long long)pid0 >= p.pool_pages;
-            const bool bad1 = n > 1 && (pid1 < 0 || (long long)pid1 >= p.pool_pages);
-            if (bad0 || bad1) atomicOr(p.status, PA_STATUS_BAD_PAGE);
-            v.poison[stage] = bad0 || bad1 ? 1 : 0;
-            if (it != p.stall_iteration || blockIdx.x != 0) {
-              ptx::mbar_arrive_expect_tx(full, n * (2 * S::kChunks * S::kPageBytes + 32));
-              for (int k = 0; k < n; ++k) {
-                const int pid = k ? (bad1 ? 0 : pid1) : (bad0 ? 0 : pid0);
-#pragma unroll
-                for (int c = 0; c < S::kChunks; ++c) {
-                  const uint32_t at = dst + c * S::kChunkBytes + k * S::kPageBytes;
-                  ptx::tma_load_2d_hint(at, tmap, s.g * D + c * kChunk, pid * kPage, full, pol);
-                  ptx::tma_load_2d_hint(at + S::kHalfBytes, tmap,
-                                        (p.Hkv + s.g) * D + c * kChunk, pid * kPage, full, pol);
-                }
-                const float* from = p.scales + ((size_t)pid * 2 * p.Hkv + s.g) * 4;
-                bulk_load(sc + k * 16, from, 16, full);
-                bulk_load(sc + kStepBlocks * 4 + k * 16, from + (size_t)p.Hkv * 4, 16, full);
-              }
-            }
-          }
+      for (int j = 0; j < cnt; j += 2) {
+        StepPages now;
+        now.pid[0] = __shfl_sync(0xffffffffu, my_pid, j);
+        now.pid[1] = __shfl_sync(0xffffffffu, my_pid, (j + 1) & 31);
+        now.n = min(2, cnt - j);
+        now.head = s.g;
+        if (!load_keys<D>(p, v, tmap, pol, keys, lane, now)) return false;
+        ++keys;
+        if (keys > 1) {
+          if (!load_values<D>(p, v, tmap, pol, values, last)) return false;
+          ++values;
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
+        last = now;
       }
     }
-    return ok;
+    return true;
   });
+  if (values < keys && load_values<D>(p, v, tmap, pol, values, last)) ++values;
   // Every page of this CTA is requested: the next kernel in the stream may
   // start its prologue.
   if (lane == 0) ptx::launch_dependents();
-  if (lane == 0) {
-    // The copies issued land before the CTA can exit, whatever became of the
-    // other warps.
-    for (int k = max(0, it - S::kStages); k < it; ++k)
-      ptx::mbar_wait_bounded(v.bar(S::kFull + k % S::kStages), (k / S::kStages) & 1,
-                             p.wait_limit_ns);
-  }
+  // The copies issued land before the CTA can exit, whatever became of the
+  // other warps.
+  for (int k = max(0, keys - S::kStages); k < keys; ++k)
+    ptx::mbar_wait_bounded(v.bar(S::kKFull + k % S::kStages), (k / S::kStages) & 1,
+                           p.wait_limit_ns);
+  for (int k = max(0, values - S::kStages); k < values; ++k)
+    ptx::mbar_wait_bounded(v.bar(S::kVFull + k % S::kStages), (k / S::kStages) & 1,
+                           p.wait_limit_ns);
 }
 
 // ---------------------------------------------------------------------------
-// Warp 9: scores.  Warp 10: products with V.  The whole warp follows the steps,
-// so that descriptors stay in uniform registers; one elected lane issues.
+// Warp 13: scores.  Warp 14: products with V.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ bool elect() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-
 // Every product this warp issued, and every arrival that follows from one,
 // ends before the CTA can.
 template <class P>
@@ -334,11 +404,11 @@ __device__ __forceinline__ void score_warp(const P& p, const View& v, uint32_t t
     const int steps = s.steps();
     for (int i = 0; i < steps; ++i, ++it) {
       const int stage = it % S::kStages;
-      const bool ok = wait_phase(p, v, S::kFull + stage, it / S::kStages) &&
+      const bool ok = wait_phase(p, v, S::kKFull + stage, it / S::kStages) &&
                       (it < 2 || wait_phase(p, v, S::kSEmpty + (it & 1), (it >> 1) - 1));
       if (!__all_sync(0xffffffffu, ok)) return false;
       tc::fence_after();
-      const uint64_t a = tc::desc_sw128(v.addr + stage * S::kStageBytes);
+      const uint64_t a = tc::desc_sw128(v.addr + stage * S::kHalfBytes);
       const uint64_t b = tc::desc_sw128(v.addr + S::kQ + (seg & 1) * S::kQBytes);
       if (elect()) {
 #pragma unroll
@@ -349,6 +419,10 @@ __device__ __forceinline__ void score_warp(const P& p, const View& v, uint32_t t
                          b + (c * S::kQChunkBytes >> 4) + 2 * k, kIdesc, c + k > 0);
         }
         tc::commit(v.bar(S::kSFull + (it & 1)));
+        // and an arrival of its own: the scales and the mark that came with K,
+        // whose barrier may be phases ahead by the time softmax looks
+        ptx::mbar_arrive(v.bar(S::kSFull + (it & 1)));
+        tc::commit(v.bar(S::kKEmpty + stage));
         if (i == steps - 1) tc::commit(v.bar(S::kQEmpty + (seg & 1)));
       }
       __syncwarp();
@@ -369,11 +443,12 @@ __device__ __forceinline__ void product_warp(const P& p, const View& v, uint32_t
     for (int i = 0; i < steps; ++i, ++it) {
       const int stage = it % S::kStages;
       const bool two = s.lo + 2 * i + 1 < s.hi;   // both pages of the step are there
-      const bool ok = wait_phase(p, v, S::kPFull + (it & 1), it >> 1) &&
+      const bool ok = wait_phase(p, v, S::kVFull + stage, it / S::kStages) &&
+                      wait_phase(p, v, S::kPFull + (it & 1), it >> 1) &&
                       (it < 2 || wait_phase(p, v, S::kOEmpty + (it & 1), (it >> 1) - 1));
       if (!__all_sync(0xffffffffu, ok)) return false;
       tc::fence_after();
-      const uint64_t a = tc::desc_sw128(v.addr + stage * S::kStageBytes + S::kHalfBytes);
+      const uint64_t a = tc::desc_sw128(v.addr + S::kV + stage * S::kHalfBytes);
       const uint64_t b = tc::desc_sw128(v.addr + S::kP + (it & 1) * S::kPBytes);
       const uint32_t d = tmem + 2 * kQCols + (it & 1) * S::kChunks * kPCols;
       if (elect()) {
@@ -388,7 +463,7 @@ __device__ __forceinline__ void product_warp(const P& p, const View& v, uint32_t
           }
         }
         tc::commit(v.bar(S::kOFull + (it & 1)));
-        tc::commit(v.bar(S::kEmpty + stage));
+        tc::commit(v.bar(S::kVEmpty + stage));
       }
       __syncwarp();
     }
@@ -398,24 +473,21 @@ __device__ __forceinline__ void product_warp(const P& p, const View& v, uint32_t
 }
 
 // ---------------------------------------------------------------------------
-// Warps 11-14, two heads each: q of a segment as hi and lo parts, and its
-// scale.  (One warp for all heads took 2.2 us at 128 dims and 4.8 at 256, the
-// longest part of a launch's start.)
+// Warp 15: q of a segment as hi and lo parts, and its scale.
 // ---------------------------------------------------------------------------
 template <int D, class P>
-__device__ __forceinline__ void q_warp(const P& p, const View& v, int warp, int lane) {
+__device__ __forceinline__ void q_warp(const P& p, const View& v, int lane) {
   using S = Smem<D>;
   constexpr int kDims = D / 32;             // dims per lane
   using Vec = typename std::conditional<kDims == 8, uint4, uint2>::type;
   for_segments(p, [&](const Segment& s, int seg) {
     if (seg == 0) ptx::grid_dependency_wait();
     const __nv_bfloat16* src = p.q + ((size_t)s.b * p.Hq + s.g * p.G) * D + lane * kDims;
-    Vec raw[kHeadsPerQWarp];
+    Vec raw[kMaxG];
 #pragma unroll
-    for (int i = 0; i < kHeadsPerQWarp; ++i) {
-      const int h = warp * kHeadsPerQWarp + i;
-      raw[i] = Vec{};
-      if (h < p.G) raw[i] = __ldg(reinterpret_cast<const Vec*>(src + h * D));
+    for (int h = 0; h < kMaxG; ++h) {
+      raw[h] = Vec{};
+      if (h < p.G) raw[h] = __ldg(reinterpret_cast<const Vec*>(src + h * D));
     }
     if (seg >= 2 && !__all_sync(0xffffffffu, wait_phase(p, v, S::kQEmpty + (seg & 1),
                                                         (seg >> 1) - 1)))
@@ -425,34 +497,30 @@ __device__ __forceinline__ void q_warp(const P& p, const View& v, int warp, int 
     const uint32_t buf = v.addr + S::kQ + (seg & 1) * S::kQBytes +
                          col / kChunk * S::kQChunkBytes + (col & 15);
 #pragma unroll
-    for (int i = 0; i < kHeadsPerQWarp; ++i) {
-      const int h = warp * kHeadsPerQWarp + i;
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[i]);
-      float y[kDims];
+    for (int h = 0; h < kMaxG; ++h) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[h]);
       unsigned amax = 0;
 #pragma unroll
-      for (int k = 0; k < kDims / 2; ++k) {
-        y[2 * k] = ptx::bf16_lo_to_f32(w[k]);
-        y[2 * k + 1] = ptx::bf16_hi_to_f32(w[k]);
-        amax = max(amax, max(__float_as_uint(y[2 * k]) & 0x7fffffffu,
-                             __float_as_uint(y[2 * k + 1]) & 0x7fffffffu));
-      }
+      for (int k = 0; k < kDims / 2; ++k)
+        amax = max(amax, max(w[k] << 16 & 0x7fffffffu, w[k] & 0x7fff0000u));
       amax = __reduce_max_sync(0xffffffffu, amax);
-      // largest value to [128, 256); NaN and infinities to NaN codes
+      // Largest value to [128, 256).  A head with a NaN or an infinity becomes
+      // NaN (its scores would be).
       const int e = amax ? min(7 - ((int)(amax >> 23) - 127), 120) : 0;
-      const float up = ptx::pow2i(e);
+      const float up = amax < 0x7f800000u ? ptx::pow2i(e) : __int_as_float(0x7fc00000);
       if (lane == 0) qscale[h] = p.scale_log2 * ptx::pow2i(-e);
       const uint32_t at = buf + h * kChunk + (((col % kChunk >> 4) ^ h) << 4);
 #pragma unroll
       for (int k = 0; k < kDims / 4; ++k) {
-        float z[4], f[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          z[j] = fabsf(y[4 * k + j]) <= 3.4e38f ? y[4 * k + j] * up : __int_as_float(0x7fc00000);
-        const uint32_t hi = fp8::pack4(z[0], z[1], z[2], z[3]);
+        const float z0 = ptx::bf16_lo_to_f32(w[2 * k]) * up;
+        const float z1 = ptx::bf16_hi_to_f32(w[2 * k]) * up;
+        const float z2 = ptx::bf16_lo_to_f32(w[2 * k + 1]) * up;
+        const float z3 = ptx::bf16_hi_to_f32(w[2 * k + 1]) * up;
+        const uint32_t hi = fp8::pack4(z0, z1, z2, z3);
+        float f[4];
         fp8::unpack4(hi, f);
-        const uint32_t lo = fp8::pack4((z[0] - f[0]) * 16.f, (z[1] - f[1]) * 16.f,
-                                       (z[2] - f[2]) * 16.f, (z[3] - f[3]) * 16.f);
+        const uint32_t lo = fp8::pack4((z0 - f[0]) * 16.f, (z1 - f[1]) * 16.f,
+                                       (z2 - f[2]) * 16.f, (z3 - f[3]) * 16.f);
         asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * k), "r"(hi) : "memory");
         asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + kMaxG * kChunk + 4 * k), "r"(lo)
                      : "memory");
@@ -466,16 +534,17 @@ __device__ __forceinline__ void q_warp(const P& p, const View& v, int warp, int 
 }
 
 // ---------------------------------------------------------------------------
-// Warps 0-3: a thread per token of a step.
+// Warps 0-3 and 4-7: a thread per token of every other step.
 // ---------------------------------------------------------------------------
 template <int D, class P>
-__device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_t tmem, int warp,
-                                              int lane) {
+__device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_t tmem, int group,
+                                              int warp, int lane) {
   using S = Smem<D>;
+  const int barrier = 2 + 2 * group;
   const int tok = warp * 32 + lane;
   int it = 0;
   bool fail = false;
-  float* wmax = reinterpret_cast<float*>(v.base + S::kWarpMax);
+  float* wmax = reinterpret_cast<float*>(v.base + S::kWarpMax) + group * kGroupWarps * kMaxG;
   for_segments(p, [&](const Segment& s, int seg) {
     float qs[kMaxG], ref[kMaxG], l[kMaxG];
     fail |= !wait_phase(p, v, S::kQFull + (seg & 1), seg >> 1);
@@ -491,7 +560,9 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
     int poisoned = 0;
     const int steps = s.steps();
     for (int i = 0; i < steps; ++i, ++it) {
+      if ((it & 1) != group) continue;
       const int stage = it % S::kStages;
+      const int slot = it % S::kSlots;
       const int tok0 = s.first_tok + (s.lo + 2 * i) * kPage;
       const int pages = min(2, s.hi - (s.lo + 2 * i));
       const bool loaded = tok < pages * kPage;
@@ -499,21 +570,20 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       float x[kMaxG];
       float sv = 0.f, up = 0.f;
       bool need = false;
-      fail = fail || !wait_phase(p, v, S::kFull + stage, it / S::kStages) ||
-             !wait_phase(p, v, S::kSFull + (it & 1), it >> 1);
+      fail = fail || !wait_phase(p, v, S::kSFull + group, it >> 1);
       if (!fail) {
         const float* sc = reinterpret_cast<const float*>(v.base + S::kScales +
-                                                         stage * S::kScaleBytes);
+                                                         slot * S::kScaleBytes);
         const float sk = sc[tok / kBlock];
         sv = sc[kStepBlocks + tok / kBlock];
-        poisoned |= v.poison[stage];
+        poisoned |= v.poison[slot];
         tc::fence_after();
         uint32_t r[16];
-        tc::ld16(tmem + (it & 1) * kQCols + ((uint32_t)(warp * 32) << 16), r);
+        tc::ld16(tmem + group * kQCols + ((uint32_t)(warp * 32) << 16), r);
         tc::wait_ld(r);
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(v.bar(S::kSEmpty + (it & 1)));
+        if (lane == 0) ptx::mbar_arrive(v.bar(S::kSEmpty + group));
         // 2^up >= |sv|
         const unsigned sb = __float_as_uint(sv) & 0x7fffffffu;
         if (!(fabsf(sv) <= ptx::pow2i(kMaxScaleExp))) sv = __int_as_float(0x7fc00000);
@@ -526,19 +596,19 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
           need |= x[h] + up > ref[h];
         }
       }
-      if (any_in_group(2, kStep, need || fail)) {
-        if (any_in_group(3, kStep, fail)) return false;
+      if (any_in_group(barrier, kStep, need || fail)) {
+        if (any_in_group(barrier + 1, kStep, fail)) return false;
 #pragma unroll
         for (int h = 0; h < kMaxG; ++h) {
           const float m = warp_max(x[h] + up);
           if (lane == 0) wmax[warp * kMaxG + h] = m;
         }
-        ptx::named_barrier(2, kStep);
+        ptx::named_barrier(barrier, kStep);
 #pragma unroll
         for (int h = 0; h < kMaxG; ++h) {
           float m = wmax[h];
 #pragma unroll
-          for (int w = 1; w < kSoftmaxWarps; ++w) m = fmaxf(m, wmax[w * kMaxG + h]);
+          for (int w = 1; w < kGroupWarps; ++w) m = fmaxf(m, wmax[w * kMaxG + h]);
           const float to = fmaxf(ref[h], ref_ceil(m));
           l[h] *= ref_weight(ref[h], to);
           ref[h] = to;
@@ -547,14 +617,14 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       // Step it - 2's product is done: its P buffer is free, and so is the
       // reference slot of step it - 4 (the product waited for the output warps
       // to be through with that step).
-      if (it >= 2) fail = !wait_phase(p, v, S::kOFull + (it & 1), (it >> 1) - 1);
+      if (it >= 2) fail = !wait_phase(p, v, S::kOFull + group, (it >> 1) - 1);
       if (tok == 0) {
-        float* slot = reinterpret_cast<float*>(v.base + S::kRef) + (it % kRefs) * kMaxG;
+        float* to = reinterpret_cast<float*>(v.base + S::kRef) + (it % kRefs) * kMaxG;
 #pragma unroll
-        for (int h = 0; h < kMaxG; ++h) slot[h] = ref[h];
+        for (int h = 0; h < kMaxG; ++h) to[h] = ref[h];
         ptx::mbar_arrive(v.bar(S::kRefFull + it % kRefs));
       }
-      const uint32_t prow = v.addr + S::kP + (it & 1) * S::kPBytes + (tok & 15);
+      const uint32_t prow = v.addr + S::kP + group * S::kPBytes + (tok & 15);
       const int chunk = tok >> 4;
 #pragma unroll
       for (int h = 0; h < kMaxG; h += 2) {
@@ -586,7 +656,8 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       }
       if (loaded && !live) {
         // A NaN code in a row outside the tile would reach the product (0 x NaN).
-        const uint32_t row = v.addr + stage * S::kStageBytes + S::kHalfBytes + tok * kChunk;
+        fail |= !wait_phase(p, v, S::kVFull + stage, it / S::kStages);
+        const uint32_t row = v.addr + S::kV + stage * S::kHalfBytes + tok * kChunk;
 #pragma unroll
         for (int c = 0; c < S::kChunks; ++c)
           for (int k = 0; k < kChunk; k += 16)
@@ -597,12 +668,12 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(v.bar(S::kPFull + (it & 1)));
+      if (lane == 0) ptx::mbar_arrive(v.bar(S::kPFull + group));
     }
     // ---- the segment's sums, references and poison to the output warps ----
     if (seg >= 2) fail |= !wait_phase(p, v, S::kLEmpty + (seg & 1), (seg >> 1) - 1);
     float* seg_l = reinterpret_cast<float*>(v.base + S::kSegL) +
-                   ((seg & 1) * kSoftmaxWarps + warp) * kMaxG;
+                   ((seg & 1) * kSoftmaxWarps + group * kGroupWarps + warp) * kMaxG;
 #pragma unroll
     for (int h = 0; h < kMaxG; ++h) {
 #pragma unroll
@@ -610,10 +681,11 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       if (lane == 0) seg_l[h] = l[h];
     }
     if (tok == 0) {
-      float* sr = reinterpret_cast<float*>(v.base + S::kSegRef) + (seg & 1) * kMaxG;
+      float* sr = reinterpret_cast<float*>(v.base + S::kSegRef) +
+                  ((seg & 1) * kGroups + group) * kMaxG;
 #pragma unroll
       for (int h = 0; h < kMaxG; ++h) sr[h] = ref[h];
-      v.seg_poison[seg & 1] = poisoned;
+      v.seg_poison[(seg & 1) * kGroups + group] = poisoned;
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(v.bar(S::kLFull + (seg & 1)));
@@ -622,7 +694,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
 }
 
 // ---------------------------------------------------------------------------
-// Warps 4-7: a thread per dim of each chunk.
+// Warps 8-11: a thread per dim of each chunk.
 // ---------------------------------------------------------------------------
 template <int D, class P>
 __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t tmem, int warp,
@@ -666,22 +738,27 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
              !wait_phase(p, v, S::kOFull + (it & 1), it >> 1);
       if (fail) break;
       const float* slot = reinterpret_cast<const float*>(v.base + S::kRef) + (it % kRefs) * kMaxG;
+      // The two groups' references move apart: the sum keeps the largest seen
+      // (a rescale where a slot is above it) and weighs each step's product.
+      float by[kMaxG];
       bool moved = false;
-      float to[kMaxG];
 #pragma unroll
       for (int h = 0; h < kMaxG; ++h) {
-        to[h] = slot[h];
-        moved |= to[h] != ref[h];
+        by[h] = slot[h];
+        moved |= by[h] > ref[h];
       }
       if (moved) {
 #pragma unroll
         for (int h = 0; h < kMaxG; ++h) {
-          const float a = ref_weight(ref[h], to[h]);
+          const float to = fmaxf(ref[h], by[h]);
+          const float a = ref_weight(ref[h], to);
 #pragma unroll
           for (int c = 0; c < S::kChunks; ++c) acc[c][h] *= a;
-          ref[h] = to[h];
+          ref[h] = to;
         }
       }
+#pragma unroll
+      for (int h = 0; h < kMaxG; ++h) by[h] = ref_weight(by[h], ref[h]) * (1.0f / kFirstPart);
       tc::fence_after();
       const uint32_t d = tmem + 2 * kQCols + (it & 1) * S::kChunks * kPCols +
                          ((uint32_t)(warp * 32) << 16);
@@ -700,7 +777,7 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
             const int col = part * kMaxG + h;
             sum = fmaf(sum, 1.0f / kPartRatio, __uint_as_float(r[col / 16][col % 16]));
           }
-          acc[c][h] = fmaf(sum, 1.0f / kFirstPart, acc[c][h]);
+          acc[c][h] = fmaf(sum, by[h], acc[c][h]);
         }
       }
       tc::fence_before();
@@ -712,13 +789,19 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
     // ---- the segment's output or partial ----
     const float* seg_l = reinterpret_cast<const float*>(v.base + S::kSegL) +
                          (seg & 1) * kSoftmaxWarps * kMaxG;
-    const float* sr = reinterpret_cast<const float*>(v.base + S::kSegRef) + (seg & 1) * kMaxG;
-    const bool nan = v.seg_poison[seg & 1] != 0;
+    const float* sr = reinterpret_cast<const float*>(v.base + S::kSegRef) +
+                      (seg & 1) * kGroups * kMaxG;
+    const bool nan = (v.seg_poison[(seg & 1) * kGroups] | v.seg_poison[(seg & 1) * kGroups + 1]) != 0;
     float l[kMaxG];
 #pragma unroll
     for (int h = 0; h < kMaxG; ++h) {
-      l[h] = (seg_l[h] + seg_l[kMaxG + h]) + (seg_l[2 * kMaxG + h] + seg_l[3 * kMaxG + h]);
-      ref[h] = sr[h];
+      l[h] = 0.f;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const float* w = seg_l + g * kGroupWarps * kMaxG + h;
+        l[h] = fmaf(ref_weight(sr[g * kMaxG + h], ref[h]),
+                    (w[0] + w[kMaxG]) + (w[2 * kMaxG] + w[3 * kMaxG]), l[h]);
+      }
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(v.bar(S::kLEmpty + (seg & 1)));
@@ -783,21 +866,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   v.bars = v.addr + S::kBars;
   int* misc = reinterpret_cast<int*>(v.base + S::kMisc);
   v.poison = misc;
-  v.seg_poison = misc + S::kStages;
-  v.abort_flag = misc + S::kStages + 2;
-  v.fin_flag = misc + S::kStages + 3;
-  v.merge_info = misc + S::kStages + 4;
-  int* tmem_slot = misc + S::kStages + 6;
+  misc += S::kSlots;
+  v.seg_poison = misc;
+  misc += 2 * kGroups;
+  v.abort_flag = misc;
+  v.fin_flag = misc + 1;
+  v.merge_info = misc + 2;
+  int* tmem_slot = misc + 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kNumBars; ++i) {
       int n = 1;
-      if (i >= S::kSEmpty && i < S::kOFull) n = kSoftmaxWarps;        // S empty, P full
+      if (i < S::kKEmpty) n = 1 + kScaleCopies;                       // K full
+      if (i >= S::kSFull && i < S::kSEmpty) n = 2;                    // products and scales
+      if (i >= S::kSEmpty && i < S::kOFull) n = kGroupWarps;          // S empty, P full
       if (i >= S::kOEmpty && i < S::kQFull) n = kOutWarps;
       if (i >= S::kQEmpty && i < S::kLFull) n = kSoftmaxWarps + 1;    // and the last product
       if (i >= S::kLFull && i < S::kLEmpty) n = kSoftmaxWarps;
       if (i >= S::kLEmpty && i < S::kDrain) n = kOutWarps;
-      if (i >= S::kQFull && i < S::kQEmpty) n = kQWarps;
       ptx::mbar_init(v.bar(i), n);
     }
     *v.abort_flag = 0;
@@ -810,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile int*>(tmem_slot);
   if (warp < kSoftmaxWarps) {
-    softmax_warps<D>(p, v, tmem, warp, lane);
+    softmax_warps<D>(p, v, tmem, warp / kGroupWarps, warp % kGroupWarps, lane);
   } else if (warp < kSoftmaxWarps + kOutWarps) {
     output_warps<D>(p, v, tmem, warp - kSoftmaxWarps, lane);
   } else if (warp == kTmaWarp) {
@@ -820,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kProductWarp) {
     product_warp<D>(p, v, tmem);
   } else {
-    q_warp<D>(p, v, warp - kFirstQWarp, lane);
+    q_warp<D>(p, v, lane);
   }
   __syncwarp();
   tc::fence_before();
