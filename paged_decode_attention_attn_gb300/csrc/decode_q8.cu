@@ -56,6 +56,7 @@ using namespace split;
 constexpr int kBlock = PA_SCALE_TOKENS;
 constexpr int kStep = 2 * kPage;            // tokens per step
 constexpr int kStepBlocks = kStep / kBlock;
+constexpr int kBlocksPerPage = kPage / kBlock;
 constexpr int kParts = 4;                   // e4m3 parts of a probability
 constexpr float kFirstPart = 256.f;         // scale of the first part
 constexpr float kPartRatio = 32.f;          // of each further one
@@ -103,7 +104,8 @@ struct Smem {
   static constexpr int kSegL = kRef + kRefs * kMaxG * 4;           // [2][warp][kMaxG]
   static constexpr int kSegRef = kSegL + 2 * kSoftmaxWarps * kMaxG * 4;   // [2][group][kMaxG]
   static constexpr int kWarpMax = kSegRef + 2 * kGroups * kMaxG * 4;      // [warp][kMaxG]
-  static constexpr int kBars = kWarpMax + kSoftmaxWarps * kMaxG * 4;
+  static constexpr int kFactor = kWarpMax + kSoftmaxWarps * kMaxG * 4;    // [kMaxG]
+  static constexpr int kBars = kFactor + kMaxG * 4;
   // mbarriers: full, empty per K and V stage; S, P, product, q, sums: full and
   // empty; all of a warp's products done; reference slots written
   static constexpr int kKFull = 0, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages,
@@ -165,23 +167,49 @@ struct View {
   __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
 };
 
-// Waits for phase `n` (0, 1, ...) of a barrier.  False once the time limit or
-// another warp's has run out.
-template <class P>
-__device__ __forceinline__ bool wait_phase(const P& p, const View& v, int bar, int n) {
-  const uint32_t b = v.bar(bar);
-  const uint32_t parity = n & 1;
-  if (ptx::mbar_try_wait(b, parity)) return true;
+// A position in a ring of kN buffers and the parity of its barriers' phase: a
+// reader waits for `full` with it, a writer for `empty` with the other parity
+// (which a fresh barrier passes).
+template <int kN>
+struct Ring {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == kN) {
+      i = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// The slow side of a wait, out of line: the roles' loops stay short (a warp on
+// its own runs ~6 cycles per instruction, and every line of code is fetched
+// cold in a launch).
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                       int32_t* status, volatile int* abort_flag) {
   const uint64_t t0 = ptx::globaltimer_ns();
   while (true) {
-    if (ptx::mbar_try_wait(b, parity)) return true;
-    if (*v.abort_flag) return false;
-    if (ptx::globaltimer_ns() - t0 > p.wait_limit_ns) {
-      atomicOr(p.status, PA_STATUS_TIMEOUT);
-      *v.abort_flag = 1;
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (ptx::globaltimer_ns() - t0 > limit_ns) {
+      atomicOr(status, PA_STATUS_TIMEOUT);
+      *abort_flag = 1;
       return false;
     }
   }
+}
+
+// Waits for the phase of the given parity to be complete.  False once the time
+// limit, or another warp's, has run out.
+template <class P>
+__device__ __forceinline__ bool wait(const P& p, const View& v, int bar, uint32_t parity) {
+  const uint32_t b = v.bar(bar);
+  return ptx::mbar_try_wait(b, parity) ||
+         wait_long(b, parity, p.wait_limit_ns, p.status, v.abort_flag);
+}
+template <class P>
+__device__ __forceinline__ bool warp_wait(const P& p, const View& v, int bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait(p, v, bar, parity));
 }
 
 // A CTA's part of a unit: its pages [lo, hi).
@@ -259,116 +287,87 @@ __device__ __forceinline__ float warp_max(float x) {
 // Warp 12: the pages' K (with the step's scales) and V into their rings.  V
 // follows a step behind K, in the order in which the stages become free.
 // ---------------------------------------------------------------------------
-struct StepPages {
-  int pid[2];
-  int n;       // pages of the step
-  int head;
-};
-
-template <int D, class P>
-__device__ __forceinline__ bool load_keys(const P& p, const View& v, const CUtensorMap* tmap,
-                                          uint64_t pol, int it, int lane, StepPages& s) {
-  using S = Smem<D>;
-  const int stage = it % S::kStages, slot = it % S::kSlots;
-  const bool free = it < S::kStages || wait_phase(p, v, S::kKEmpty + stage, it / S::kStages - 1);
-  if (!__all_sync(0xffffffffu, free)) return false;
-  const uint32_t full = v.bar(S::kKFull + stage);
-  bool bad = false;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    // a page that is not there: page 0 in its place, the step marked
-    if (k < s.n && (s.pid[k] < 0 || (long long)s.pid[k] >= p.pool_pages)) {
-      bad = true;
-      s.pid[k] = 0;
-    }
-  }
-  const bool armed = it != p.stall_iteration || blockIdx.x != 0;
-  if (elect()) {
-    if (bad) atomicOr(p.status, PA_STATUS_BAD_PAGE);
-    v.poison[slot] = bad ? 1 : 0;   // set before the arrival that publishes it
-    if (armed) {
-      ptx::mbar_arrive_expect_tx(full, s.n * S::kChunks * S::kPageBytes);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (k >= s.n) break;
-        const uint32_t dst = v.addr + stage * S::kHalfBytes + k * S::kPageBytes;
-#pragma unroll
-        for (int c = 0; c < S::kChunks; ++c)
-          ptx::tma_load_2d_hint(dst + c * S::kChunkBytes, tmap, s.head * D + c * kChunk,
-                                s.pid[k] * kPage, full, pol);
-      }
-    }
-  }
-  // The scales (K's and V's of each page, 16 bytes) by four lanes' copies: TMA
-  // operations of one thread go out ~80 ns apart, too slow for such pieces.
-  if (armed && lane < kScaleCopies) {
-    const int k = lane >> 1, kind = lane & 1;
-    if (k < s.n)
-      copy16(v.addr + S::kScales + slot * S::kScaleBytes + kind * kStepBlocks * 4 + k * 16,
-             p.scales + (((size_t)s.pid[k] * 2 + kind) * p.Hkv + s.head) * 4);
-    arrive_after_copies(full);
-  }
-  __syncwarp();
-  return true;
-}
-
-template <int D, class P>
-__device__ __forceinline__ bool load_values(const P& p, const View& v, const CUtensorMap* tmap,
-                                            uint64_t pol, int it, const StepPages& s) {
-  using S = Smem<D>;
-  const int stage = it % S::kStages;
-  const bool free = it < S::kStages || wait_phase(p, v, S::kVEmpty + stage, it / S::kStages - 1);
-  if (!__all_sync(0xffffffffu, free)) return false;
-  const uint32_t full = v.bar(S::kVFull + stage);
-  if (elect()) {
-    ptx::mbar_arrive_expect_tx(full, s.n * S::kChunks * S::kPageBytes);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (k >= s.n) break;
-      const uint32_t dst = v.addr + S::kV + stage * S::kHalfBytes + k * S::kPageBytes;
-#pragma unroll
-      for (int c = 0; c < S::kChunks; ++c)
-        ptx::tma_load_2d_hint(dst + c * S::kChunkBytes, tmap, (p.Hkv + s.head) * D + c * kChunk,
-                              s.pid[k] * kPage, full, pol);
-    }
-  }
-  __syncwarp();
-  return true;
-}
-
 template <int D, class P>
 __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtensorMap* tmap,
                                          int lane) {
   using S = Smem<D>;
-  int keys = 0, values = 0;   // steps loaded
-  StepPages last;
+  Ring<S::kStages> kr, vr;
+  Ring<S::kSlots> slot;
+  int keys = 0, values = 0;            // steps loaded
+  int row0 = 0, row1 = 0, n_last = 0, col_last = 0;   // the step whose V is next
   const uint64_t pol = ptx::policy_evict_first();   // every page is read once
+  auto boxes = [&](uint32_t dst, uint32_t full, int col, int r0, int r1, int n) {
+#pragma unroll
+    for (int c = 0; c < S::kChunks; ++c)
+      ptx::tma_load_2d_hint(dst + c * S::kChunkBytes, tmap, col + c * kChunk, r0, full, pol);
+    if (n > 1) {
+#pragma unroll
+      for (int c = 0; c < S::kChunks; ++c)
+        ptx::tma_load_2d_hint(dst + c * S::kChunkBytes + S::kPageBytes, tmap, col + c * kChunk, r1,
+                              full, pol);
+    }
+  };
+  auto load_values = [&]() {
+    if (!warp_wait(p, v, S::kVEmpty + vr.i, vr.phase ^ 1)) return false;
+    if (elect()) {
+      const uint32_t full = v.bar(S::kVFull + vr.i);
+      ptx::mbar_arrive_expect_tx(full, n_last * S::kChunks * S::kPageBytes);
+      boxes(v.addr + S::kV + vr.i * S::kHalfBytes, full, col_last, row0, row1, n_last);
+    }
+    __syncwarp();
+    vr.next();
+    ++values;
+    return true;
+  };
+  const int lane_page = (lane >> 1) & 1, lane_kind = lane & 1;   // scale copies of lanes 0-3
   for_segments(p, [&](const Segment& s, int seg) {
     if (seg == 0) ptx::grid_dependency_wait();
     const int32_t* prow = p.page_table + (size_t)s.b * p.max_pages + s.U.tok_start / kPage;
+    const float* scales = p.scales + ((size_t)lane_kind * p.Hkv + s.g) * kBlocksPerPage;
+    const int scale_stride = 2 * p.Hkv * kBlocksPerPage;
     int next_pid = s.lo + lane < s.hi ? __ldg(prow + s.lo + lane) : 0;
     for (int base = s.lo; base < s.hi; base += 32) {
       const int cnt = min(32, s.hi - base);
-      const int my_pid = next_pid;
+      // a page that is not there: page 0 in its place, its step marked
+      const bool bad = lane < cnt && (uint32_t)next_pid >= (uint32_t)p.pool_pages;
+      const uint32_t bad_pages = __ballot_sync(0xffffffffu, bad);
+      const int my_pid = bad ? 0 : next_pid;
+      if (bad) atomicOr(p.status, PA_STATUS_BAD_PAGE);
       if (base + 32 + lane < s.hi) next_pid = __ldg(prow + base + 32 + lane);
       for (int j = 0; j < cnt; j += 2) {
-        StepPages now;
-        now.pid[0] = __shfl_sync(0xffffffffu, my_pid, j);
-        now.pid[1] = __shfl_sync(0xffffffffu, my_pid, (j + 1) & 31);
-        now.n = min(2, cnt - j);
-        now.head = s.g;
-        if (!load_keys<D>(p, v, tmap, pol, keys, lane, now)) return false;
-        ++keys;
-        if (keys > 1) {
-          if (!load_values<D>(p, v, tmap, pol, values, last)) return false;
-          ++values;
+        const int pid0 = __shfl_sync(0xffffffffu, my_pid, j);
+        const int pid1 = __shfl_sync(0xffffffffu, my_pid, (j + 1) & 31);
+        const int n = min(2, cnt - j);
+        if (!warp_wait(p, v, S::kKEmpty + kr.i, kr.phase ^ 1)) return false;
+        const uint32_t full = v.bar(S::kKFull + kr.i);
+        if (keys != p.stall_iteration || blockIdx.x != 0) {
+          if (elect()) {
+            v.poison[slot.i] = (bad_pages >> j) & 3;   // set before the arrival that publishes it
+            ptx::mbar_arrive_expect_tx(full, n * S::kChunks * S::kPageBytes);
+            boxes(v.addr + kr.i * S::kHalfBytes, full, s.g * D, pid0 * kPage, pid1 * kPage, n);
+          }
+          // The scales (K's and V's of each page, 16 bytes) by four lanes.
+          if (lane < kScaleCopies) {
+            if (lane_page < n)
+              copy16(v.addr + S::kScales + slot.i * S::kScaleBytes + lane_kind * kStepBlocks * 4 +
+                         lane_page * 16,
+                     scales + (size_t)(lane_page ? pid1 : pid0) * scale_stride);
+            arrive_after_copies(full);
+          }
+          __syncwarp();
         }
-        last = now;
+        kr.next();
+        slot.next();
+        if (keys++ > 0 && !load_values()) return false;
+        row0 = pid0 * kPage;
+        row1 = pid1 * kPage;
+        n_last = n;
+        col_last = (p.Hkv + s.g) * D;
       }
     }
     return true;
   });
-  if (values < keys && load_values<D>(p, v, tmap, pol, values, last)) ++values;
+  if (values < keys) load_values();
   // Every page of this CTA is requested: the next kernel in the stream may
   // start its prologue.
   if (lane == 0) ptx::launch_dependents();
@@ -398,35 +397,37 @@ template <int D, class P>
 __device__ __forceinline__ void score_warp(const P& p, const View& v, uint32_t tmem) {
   using S = Smem<D>;
   constexpr uint32_t kIdesc = tc::idesc_e4m3(kStep, kQCols, false);
-  int it = 0;
-  for_segments(p, [&](const Segment& s, int seg) {
-    if (!__all_sync(0xffffffffu, wait_phase(p, v, S::kQFull + (seg & 1), seg >> 1))) return false;
-    const int steps = s.steps();
-    for (int i = 0; i < steps; ++i, ++it) {
-      const int stage = it % S::kStages;
-      const bool ok = wait_phase(p, v, S::kKFull + stage, it / S::kStages) &&
-                      (it < 2 || wait_phase(p, v, S::kSEmpty + (it & 1), (it >> 1) - 1));
-      if (!__all_sync(0xffffffffu, ok)) return false;
+  Ring<S::kStages> kr;
+  Ring<2> sr, qr;
+  for_segments(p, [&](const Segment& s, int) {
+    if (!warp_wait(p, v, S::kQFull + qr.i, qr.phase)) return false;
+    const uint64_t b = tc::desc_sw128(v.addr + S::kQ + qr.i * S::kQBytes);
+    for (int left = s.steps(); left > 0; --left) {
+      if (!warp_wait(p, v, S::kSEmpty + sr.i, sr.phase ^ 1) ||
+          !warp_wait(p, v, S::kKFull + kr.i, kr.phase))
+        return false;
       tc::fence_after();
-      const uint64_t a = tc::desc_sw128(v.addr + stage * S::kHalfBytes);
-      const uint64_t b = tc::desc_sw128(v.addr + S::kQ + (seg & 1) * S::kQBytes);
+      const uint64_t a = tc::desc_sw128(v.addr + kr.i * S::kHalfBytes);
       if (elect()) {
 #pragma unroll
         for (int c = 0; c < S::kChunks; ++c) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc::mma_e4m3(tmem + (it & 1) * kQCols, a + (c * S::kChunkBytes >> 4) + 2 * k,
+            tc::mma_e4m3(tmem + sr.i * kQCols, a + (c * S::kChunkBytes >> 4) + 2 * k,
                          b + (c * S::kQChunkBytes >> 4) + 2 * k, kIdesc, c + k > 0);
         }
-        tc::commit(v.bar(S::kSFull + (it & 1)));
+        tc::commit(v.bar(S::kSFull + sr.i));
+        tc::commit(v.bar(S::kKEmpty + kr.i));
         // and an arrival of its own: the scales and the mark that came with K,
         // whose barrier may be phases ahead by the time softmax looks
-        ptx::mbar_arrive(v.bar(S::kSFull + (it & 1)));
-        tc::commit(v.bar(S::kKEmpty + stage));
-        if (i == steps - 1) tc::commit(v.bar(S::kQEmpty + (seg & 1)));
+        ptx::mbar_arrive(v.bar(S::kSFull + sr.i));
+        if (left == 1) tc::commit(v.bar(S::kQEmpty + qr.i));
       }
       __syncwarp();
+      kr.next();
+      sr.next();
     }
+    qr.next();
     return true;
   });
   drain(p, v, S::kDrain);
@@ -437,20 +438,19 @@ __device__ __forceinline__ void product_warp(const P& p, const View& v, uint32_t
   using S = Smem<D>;
   constexpr uint32_t kIdesc = tc::idesc_e4m3(kChunk, kPCols, true);
   constexpr uint32_t kSlice = 32 * kChunk >> 4;   // 32 tokens of a chunk, in descriptor units
-  int it = 0;
+  Ring<S::kStages> vr;
+  Ring<2> pr;
   for_segments(p, [&](const Segment& s, int) {
-    const int steps = s.steps();
-    for (int i = 0; i < steps; ++i, ++it) {
-      const int stage = it % S::kStages;
-      const bool two = s.lo + 2 * i + 1 < s.hi;   // both pages of the step are there
-      const bool ok = wait_phase(p, v, S::kVFull + stage, it / S::kStages) &&
-                      wait_phase(p, v, S::kPFull + (it & 1), it >> 1) &&
-                      (it < 2 || wait_phase(p, v, S::kOEmpty + (it & 1), (it >> 1) - 1));
-      if (!__all_sync(0xffffffffu, ok)) return false;
+    for (int page = s.lo; page < s.hi; page += 2) {
+      const bool two = page + 1 < s.hi;   // both pages of the step are there
+      if (!warp_wait(p, v, S::kOEmpty + pr.i, pr.phase ^ 1) ||
+          !warp_wait(p, v, S::kVFull + vr.i, vr.phase) ||
+          !warp_wait(p, v, S::kPFull + pr.i, pr.phase))
+        return false;
       tc::fence_after();
-      const uint64_t a = tc::desc_sw128(v.addr + S::kV + stage * S::kHalfBytes);
-      const uint64_t b = tc::desc_sw128(v.addr + S::kP + (it & 1) * S::kPBytes);
-      const uint32_t d = tmem + 2 * kQCols + (it & 1) * S::kChunks * kPCols;
+      const uint64_t a = tc::desc_sw128(v.addr + S::kV + vr.i * S::kHalfBytes);
+      const uint64_t b = tc::desc_sw128(v.addr + S::kP + pr.i * S::kPBytes);
+      const uint32_t d = tmem + 2 * kQCols + pr.i * S::kChunks * kPCols;
       if (elect()) {
 #pragma unroll
         for (int c = 0; c < S::kChunks; ++c) {
@@ -462,10 +462,12 @@ __device__ __forceinline__ void product_warp(const P& p, const View& v, uint32_t
             tc::mma_e4m3(d + c * kPCols, ac + 3 * kSlice, b + 6, kIdesc, true);
           }
         }
-        tc::commit(v.bar(S::kOFull + (it & 1)));
-        tc::commit(v.bar(S::kVEmpty + stage));
+        tc::commit(v.bar(S::kOFull + pr.i));
+        tc::commit(v.bar(S::kVEmpty + vr.i));
       }
       __syncwarp();
+      vr.next();
+      pr.next();
     }
     return true;
   });
@@ -473,62 +475,73 @@ __device__ __forceinline__ void product_warp(const P& p, const View& v, uint32_t
 }
 
 // ---------------------------------------------------------------------------
-// Warp 15: q of a segment as hi and lo parts, and its scale.
+// q of a segment as hi and lo parts, and its scales: the output warps, two
+// heads each, for a CTA's first segment (on one warp it takes 3.7 us, the
+// longest part of a launch's start), warp 15 ahead of time for the others.
 // ---------------------------------------------------------------------------
-template <int D, class P>
-__device__ __forceinline__ void q_warp(const P& p, const View& v, int lane) {
+template <int D, int kHeads, class P>
+__device__ __forceinline__ void convert_q(const P& p, const View& v, const Segment& s, int buffer,
+                                          int h0, int lane) {
   using S = Smem<D>;
   constexpr int kDims = D / 32;             // dims per lane
   using Vec = typename std::conditional<kDims == 8, uint4, uint2>::type;
+  const __nv_bfloat16* src = p.q + ((size_t)s.b * p.Hq + s.g * p.G + h0) * D + lane * kDims;
+  Vec raw[kHeads];
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    raw[h] = Vec{};
+    if (h0 + h < p.G) raw[h] = __ldg(reinterpret_cast<const Vec*>(src + h * D));
+  }
+  float* qscale = reinterpret_cast<float*>(v.base + S::kQScale) + buffer * kMaxG + h0;
+  const int col = lane * kDims;
+  const uint32_t buf = v.addr + S::kQ + buffer * S::kQBytes + col / kChunk * S::kQChunkBytes +
+                       (col & 15);
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[h]);
+    unsigned amax = 0;
+#pragma unroll
+    for (int k = 0; k < kDims / 2; ++k)
+      amax = max(amax, max(w[k] << 16 & 0x7fffffffu, w[k] & 0x7fff0000u));
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    // Largest value to [128, 256).  A head with a NaN or an infinity becomes
+    // NaN (its scores would be).
+    const int e = amax ? min(7 - ((int)(amax >> 23) - 127), 120) : 0;
+    const float up = amax < 0x7f800000u ? ptx::pow2i(e) : __int_as_float(0x7fc00000);
+    if (lane == 0) qscale[h] = p.scale_log2 * ptx::pow2i(-e);
+    const uint32_t at = buf + (h0 + h) * kChunk + (((col % kChunk >> 4) ^ (h0 + h)) << 4);
+#pragma unroll
+    for (int k = 0; k < kDims / 4; ++k) {
+      const float z0 = ptx::bf16_lo_to_f32(w[2 * k]) * up;
+      const float z1 = ptx::bf16_hi_to_f32(w[2 * k]) * up;
+      const float z2 = ptx::bf16_lo_to_f32(w[2 * k + 1]) * up;
+      const float z3 = ptx::bf16_hi_to_f32(w[2 * k + 1]) * up;
+      const uint32_t hi = fp8::pack4(z0, z1, z2, z3);
+      float f[4];
+      fp8::unpack4(hi, f);
+      const uint32_t lo = fp8::pack4((z0 - f[0]) * 16.f, (z1 - f[1]) * 16.f, (z2 - f[2]) * 16.f,
+                                     (z3 - f[3]) * 16.f);
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * k), "r"(hi) : "memory");
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + kMaxG * kChunk + 4 * k), "r"(lo)
+                   : "memory");
+    }
+  }
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+}
+
+template <int D, class P>
+__device__ __forceinline__ void q_warp(const P& p, const View& v, int lane) {
+  using S = Smem<D>;
+  Ring<2> qr;
   for_segments(p, [&](const Segment& s, int seg) {
-    if (seg == 0) ptx::grid_dependency_wait();
-    const __nv_bfloat16* src = p.q + ((size_t)s.b * p.Hq + s.g * p.G) * D + lane * kDims;
-    Vec raw[kMaxG];
-#pragma unroll
-    for (int h = 0; h < kMaxG; ++h) {
-      raw[h] = Vec{};
-      if (h < p.G) raw[h] = __ldg(reinterpret_cast<const Vec*>(src + h * D));
+    if (seg > 0) {
+      if (seg == 1) ptx::grid_dependency_wait();
+      if (!warp_wait(p, v, S::kQEmpty + qr.i, qr.phase ^ 1)) return false;
+      convert_q<D, kMaxG>(p, v, s, qr.i, 0, lane);
+      if (lane < kOutWarps) ptx::mbar_arrive(v.bar(S::kQFull + qr.i));
     }
-    if (seg >= 2 && !__all_sync(0xffffffffu, wait_phase(p, v, S::kQEmpty + (seg & 1),
-                                                        (seg >> 1) - 1)))
-      return false;
-    float* qscale = reinterpret_cast<float*>(v.base + S::kQScale) + (seg & 1) * kMaxG;
-    const int col = lane * kDims;
-    const uint32_t buf = v.addr + S::kQ + (seg & 1) * S::kQBytes +
-                         col / kChunk * S::kQChunkBytes + (col & 15);
-#pragma unroll
-    for (int h = 0; h < kMaxG; ++h) {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[h]);
-      unsigned amax = 0;
-#pragma unroll
-      for (int k = 0; k < kDims / 2; ++k)
-        amax = max(amax, max(w[k] << 16 & 0x7fffffffu, w[k] & 0x7fff0000u));
-      amax = __reduce_max_sync(0xffffffffu, amax);
-      // Largest value to [128, 256).  A head with a NaN or an infinity becomes
-      // NaN (its scores would be).
-      const int e = amax ? min(7 - ((int)(amax >> 23) - 127), 120) : 0;
-      const float up = amax < 0x7f800000u ? ptx::pow2i(e) : __int_as_float(0x7fc00000);
-      if (lane == 0) qscale[h] = p.scale_log2 * ptx::pow2i(-e);
-      const uint32_t at = buf + h * kChunk + (((col % kChunk >> 4) ^ h) << 4);
-#pragma unroll
-      for (int k = 0; k < kDims / 4; ++k) {
-        const float z0 = ptx::bf16_lo_to_f32(w[2 * k]) * up;
-        const float z1 = ptx::bf16_hi_to_f32(w[2 * k]) * up;
-        const float z2 = ptx::bf16_lo_to_f32(w[2 * k + 1]) * up;
-        const float z3 = ptx::bf16_hi_to_f32(w[2 * k + 1]) * up;
-        const uint32_t hi = fp8::pack4(z0, z1, z2, z3);
-        float f[4];
-        fp8::unpack4(hi, f);
-        const uint32_t lo = fp8::pack4((z0 - f[0]) * 16.f, (z1 - f[1]) * 16.f,
-                                       (z2 - f[2]) * 16.f, (z3 - f[3]) * 16.f);
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * k), "r"(hi) : "memory");
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + kMaxG * kChunk + 4 * k), "r"(lo)
-                     : "memory");
-      }
-    }
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(v.bar(S::kQFull + (seg & 1)));
+    qr.next();
     return true;
   });
 }
@@ -547,7 +560,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
   float* wmax = reinterpret_cast<float*>(v.base + S::kWarpMax) + group * kGroupWarps * kMaxG;
   for_segments(p, [&](const Segment& s, int seg) {
     float qs[kMaxG], ref[kMaxG], l[kMaxG];
-    fail |= !wait_phase(p, v, S::kQFull + (seg & 1), seg >> 1);
+    fail |= !wait(p, v, S::kQFull + (seg & 1), (seg >> 1) & 1);
     const float* qscale = reinterpret_cast<float*>(v.base + S::kQScale) + (seg & 1) * kMaxG;
 #pragma unroll
     for (int h = 0; h < kMaxG; ++h) {
@@ -561,7 +574,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
     const int steps = s.steps();
     for (int i = 0; i < steps; ++i, ++it) {
       if ((it & 1) != group) continue;
-      const int stage = it % S::kStages;
+      const uint32_t phase = (it >> 1) & 1;
       const int slot = it % S::kSlots;
       const int tok0 = s.first_tok + (s.lo + 2 * i) * kPage;
       const int pages = min(2, s.hi - (s.lo + 2 * i));
@@ -570,7 +583,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       float x[kMaxG];
       float sv = 0.f, up = 0.f;
       bool need = false;
-      fail = fail || !wait_phase(p, v, S::kSFull + group, it >> 1);
+      fail = fail || !wait(p, v, S::kSFull + group, phase);
       if (!fail) {
         const float* sc = reinterpret_cast<const float*>(v.base + S::kScales +
                                                          slot * S::kScaleBytes);
@@ -617,7 +630,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       // Step it - 2's product is done: its P buffer is free, and so is the
       // reference slot of step it - 4 (the product waited for the output warps
       // to be through with that step).
-      if (it >= 2) fail = !wait_phase(p, v, S::kOFull + group, (it >> 1) - 1);
+      fail = !wait(p, v, S::kOFull + group, phase ^ 1);
       if (tok == 0) {
         float* to = reinterpret_cast<float*>(v.base + S::kRef) + (it % kRefs) * kMaxG;
 #pragma unroll
@@ -656,7 +669,8 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       }
       if (loaded && !live) {
         // A NaN code in a row outside the tile would reach the product (0 x NaN).
-        fail |= !wait_phase(p, v, S::kVFull + stage, it / S::kStages);
+        const int stage = it % S::kStages;
+        fail |= !wait(p, v, S::kVFull + stage, (it / S::kStages) & 1);
         const uint32_t row = v.addr + S::kV + stage * S::kHalfBytes + tok * kChunk;
 #pragma unroll
         for (int c = 0; c < S::kChunks; ++c)
@@ -671,15 +685,23 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       if (lane == 0) ptx::mbar_arrive(v.bar(S::kPFull + group));
     }
     // ---- the segment's sums, references and poison to the output warps ----
-    if (seg >= 2) fail |= !wait_phase(p, v, S::kLEmpty + (seg & 1), (seg >> 1) - 1);
+    fail |= !wait(p, v, S::kLEmpty + (seg & 1), ((seg >> 1) & 1) ^ 1);
     float* seg_l = reinterpret_cast<float*>(v.base + S::kSegL) +
                    ((seg & 1) * kSoftmaxWarps + group * kGroupWarps + warp) * kMaxG;
+    // Eight sums over 32 lanes: each exchange halves the heads a lane holds, the
+    // last two add lanes of one head.
 #pragma unroll
-    for (int h = 0; h < kMaxG; ++h) {
+    for (int n = kMaxG / 2; n; n >>= 1) {
+      const bool upper = lane & (4 * n);
 #pragma unroll
-      for (int off = 16; off; off >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], off);
-      if (lane == 0) seg_l[h] = l[h];
+      for (int h = 0; h < n; ++h) {
+        const float give = upper ? l[h] : l[h + n];
+        l[h] = (upper ? l[h + n] : l[h]) + __shfl_xor_sync(0xffffffffu, give, 4 * n);
+      }
     }
+    l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
+    l[0] += __shfl_xor_sync(0xffffffffu, l[0], 2);
+    if ((lane & 3) == 0) seg_l[lane >> 2] = l[0];
     if (tok == 0) {
       float* sr = reinterpret_cast<float*>(v.base + S::kSegRef) +
                   ((seg & 1) * kGroups + group) * kMaxG;
@@ -702,7 +724,12 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
   using S = Smem<D>;
   const int ct = warp * 32 + lane;
   const float qnan = __int_as_float(0x7fc00000);
-  ptx::grid_dependency_wait();   // earlier kernels may still read the outputs
+  ptx::grid_dependency_wait();   // earlier kernels write q and may still read the outputs
+  for_segments(p, [&](const Segment& s, int) {
+    convert_q<D, kMaxG / kOutWarps>(p, v, s, 0, warp * (kMaxG / kOutWarps), lane);
+    if (lane == 0) ptx::mbar_arrive(v.bar(S::kQFull));
+    return false;   // the first segment's
+  });
   // Empty units: output 0, LSE -inf.
   for (int u = blockIdx.x; u < p.n_units; u += p.grid) {
     const Unit U = p.units[u];
@@ -734,8 +761,8 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
     for (int i = 0; i < steps; ++i, ++it) {
       // A slot is written again four steps on, behind a product that waits
       // for this step's buffer.
-      fail = !wait_phase(p, v, S::kRefFull + it % kRefs, it / kRefs) ||
-             !wait_phase(p, v, S::kOFull + (it & 1), it >> 1);
+      fail = !wait(p, v, S::kRefFull + it % kRefs, (it / kRefs) & 1) ||
+             !wait(p, v, S::kOFull + (it & 1), (it >> 1) & 1);
       if (fail) break;
       const float* slot = reinterpret_cast<const float*>(v.base + S::kRef) + (it % kRefs) * kMaxG;
       // The two groups' references move apart: the sum keeps the largest seen
@@ -784,7 +811,7 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(v.bar(S::kOEmpty + (it & 1)));
     }
-    fail = fail || !wait_phase(p, v, S::kLFull + (seg & 1), seg >> 1);
+    fail = fail || !wait(p, v, S::kLFull + (seg & 1), (seg >> 1) & 1);
     if (any_in_group(1, kOut, fail)) return false;
     // ---- the segment's output or partial ----
     const float* seg_l = reinterpret_cast<const float*>(v.base + S::kSegL) +
@@ -792,62 +819,60 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
     const float* sr = reinterpret_cast<const float*>(v.base + S::kSegRef) +
                       (seg & 1) * kGroups * kMaxG;
     const bool nan = (v.seg_poison[(seg & 1) * kGroups] | v.seg_poison[(seg & 1) * kGroups + 1]) != 0;
-    float l[kMaxG];
+    const int first_cta = cta_of(s.pf, p.total_pages, p.grid);
+    const bool whole = s.U.n_parts == 1;
+    const size_t orow = (size_t)s.bt * p.Hq + s.g * p.G;
+    const size_t slot = s.U.part_base + (int)blockIdx.x - first_cta;
+    // A thread per head: its sum, and the factor of its outputs.
+    float* factor = reinterpret_cast<float*>(v.base + S::kFactor);
+    if (ct < kMaxG) {
+      float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int h = 0; h < kMaxG; ++h) {
-      l[h] = 0.f;
+      for (int g = 0; g < kGroups; ++g) m = fmaxf(m, sr[g * kMaxG + ct]);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const float* w = seg_l + g * kGroupWarps * kMaxG + h;
-        l[h] = fmaf(ref_weight(sr[g * kMaxG + h], ref[h]),
-                    (w[0] + w[kMaxG]) + (w[2 * kMaxG] + w[3 * kMaxG]), l[h]);
+        const float* w = seg_l + g * kGroupWarps * kMaxG + ct;
+        l = fmaf(ref_weight(sr[g * kMaxG + ct], m),
+                 (w[0] + w[kMaxG]) + (w[2 * kMaxG] + w[3 * kMaxG]), l);
       }
-    }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(v.bar(S::kLEmpty + (seg & 1)));
-    const int first_cta = cta_of(s.pf, p.total_pages, p.grid);
-    if (s.U.n_parts == 1) {
-      const size_t orow = (size_t)s.bt * p.Hq + s.g * p.G;
-#pragma unroll
-      for (int h = 0; h < kMaxG; ++h) {
-        if (h >= p.G) continue;
-#pragma unroll
-        for (int c = 0; c < S::kChunks; ++c) {
-          const float o = nan ? qnan : acc[c][h] / l[h];
-          p.out[(orow + h) * D + c * kChunk + ct] = o;
-          if (p.out2) p.out2[(orow + h) * D + c * kChunk + ct] = o;
+      float f, x;
+      if (whole) {
+        f = 1.0f / l;
+        x = lse_of(m, l);
+        if (ct < p.G) {
+          p.lse[orow + ct] = nan ? qnan : x;
+          if (p.lse2) p.lse2[orow + ct] = nan ? qnan : x;
         }
-        if (ct == h) {
-          const float x = nan ? qnan : lse_of(ref[h], l[h]);
-          p.lse[orow + h] = x;
-          if (p.lse2) p.lse2[orow + h] = x;
-        }
-      }
-      finish_unit<D, kOut>(p, v, s.b, s.g, ct, warp, lane, 1, s.U.pair_total);
-    } else {
-      const size_t slot = s.U.part_base + (int)blockIdx.x - first_cta;
-#pragma unroll
-      for (int h = 0; h < kMaxG; ++h) {
-        if (h >= p.G) continue;
+      } else {
         // The reference bounds V's scales too; the partial's is moved to the
         // sum's own magnitude, so that partials of blocks whose V scales lie
         // far apart still meet near their weights.
-        int k = 0;
-        if (l[h] > 0.f && l[h] <= 3.4e38f) {
-          frexpf(l[h], &k);
-          k = max(-112, min(112, (k + 132) / 8 * 8 - 128));
-        }
-        const float down = ptx::pow2i(-k);
-#pragma unroll
-        for (int c = 0; c < S::kChunks; ++c)
-          p.part_o[(slot * kMaxG + h) * D + c * kChunk + ct] = acc[c][h] * down;
-        if (ct == h) {
-          p.part_ml[(slot * kMaxG + h) * 2 + 0] = nan ? qnan : ref[h] + (float)k;
-          p.part_ml[(slot * kMaxG + h) * 2 + 1] = l[h] * down;
-        }
+        const int e = l > 0.f ? ((__float_as_int(l) >> 23) - 127 + 4) >> 3 << 3 : 0;
+        const int k = max(-112, min(112, e));
+        f = ptx::pow2i(-k);
+        p.part_ml[(slot * kMaxG + ct) * 2 + 0] = nan ? qnan : m + (float)k;
+        p.part_ml[(slot * kMaxG + ct) * 2 + 1] = l * f;
       }
-      finish_split_unit<D, kOut>(p, v, s.U, s.u, s.b, s.bt, s.g, first_cta, ct, warp, lane);
+      factor[ct] = nan ? qnan : f;
     }
+    ptx::named_barrier(1, kOut);
+    if (lane == 0) ptx::mbar_arrive(v.bar(S::kLEmpty + (seg & 1)));
+    float* dst = (whole ? p.out + orow * D : p.part_o + slot * kMaxG * D) + ct;
+    float* dst2 = whole && p.out2 ? p.out2 + orow * D + ct : nullptr;
+#pragma unroll
+    for (int h = 0; h < kMaxG; ++h) {
+      if (h >= p.G) break;
+      const float f = factor[h];
+#pragma unroll
+      for (int c = 0; c < S::kChunks; ++c) {
+        dst[h * D + c * kChunk] = acc[c][h] * f;
+        if (dst2) dst2[h * D + c * kChunk] = acc[c][h] * f;
+      }
+    }
+    if (whole)
+      finish_unit<D, kOut>(p, v, s.b, s.g, ct, warp, lane, 1, s.U.pair_total);
+    else
+      finish_split_unit<D, kOut>(p, v, s.U, s.u, s.b, s.bt, s.g, first_cta, ct, warp, lane);
     ptx::named_barrier(1, kOut);
     return true;
   });
@@ -881,6 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i >= S::kSFull && i < S::kSEmpty) n = 2;                    // products and scales
       if (i >= S::kSEmpty && i < S::kOFull) n = kGroupWarps;          // S empty, P full
       if (i >= S::kOEmpty && i < S::kQFull) n = kOutWarps;
+      if (i >= S::kQFull && i < S::kQEmpty) n = kOutWarps;
       if (i >= S::kQEmpty && i < S::kLFull) n = kSoftmaxWarps + 1;    // and the last product
       if (i >= S::kLFull && i < S::kLEmpty) n = kSoftmaxWarps;
       if (i >= S::kLEmpty && i < S::kDrain) n = kOutWarps;
