@@ -24,8 +24,8 @@
 //    8 kParts, K = 128 tokens.  Every step's product starts from zero in tensor
 //    memory and is added to fp32 registers (a thread per dim), so the long sum
 //    is rounded to nearest and rescaled there.
-//  * Warps: 0-7 softmax, 8-11 output, 12 TMA, 13 scores, 14 products, 15 q (16
-//    warps leave 128 registers a thread; 17 leave 96).  All waits are on
+//  * Warps: 0-7 softmax, 8-11 output, 12 TMA, 13 scores, 14 products, 15 what is
+//    done per segment (q, factors of the outputs, empty units; 16 warps leave 128 registers a thread; 17 leave 96).  All waits are on
 //    mbarriers with a time limit; S, P and the products have two buffers each.
 //    Each product has a warp of its own: with one thread for both, a step of
 //    256 dims took 1.4 us, 0.86 us of it the issue of its 16 instructions and
@@ -71,7 +71,7 @@ constexpr int kOut = kOutWarps * 32;
 constexpr int kSoftmaxWarps = kGroups * kGroupWarps;
 constexpr int kTmaWarp = 12, kScoreWarp = 13, kProductWarp = 14;
 constexpr int kScaleCopies = 4;             // lanes that copy a step's scales
-constexpr int kThreads = 32 * 16;           // the last warp: q
+constexpr int kThreads = 32 * 16;           // the last warp: per segment
 constexpr int kSegmentCharge = 6;           // pages charged per unit start
 constexpr int kWidePages = 32, kWideGridPct = 90;
 constexpr float kLog2e = 1.44269504088896341f;
@@ -104,16 +104,18 @@ struct Smem {
   static constexpr int kSegL = kRef + kRefs * kMaxG * 4;           // [2][warp][kMaxG]
   static constexpr int kSegRef = kSegL + 2 * kSoftmaxWarps * kMaxG * 4;   // [2][group][kMaxG]
   static constexpr int kWarpMax = kSegRef + 2 * kGroups * kMaxG * 4;      // [warp][kMaxG]
-  static constexpr int kFactor = kWarpMax + kSoftmaxWarps * kMaxG * 4;    // [kMaxG]
-  static constexpr int kBars = kFactor + kMaxG * 4;
+  static constexpr int kFactor = kWarpMax + kSoftmaxWarps * kMaxG * 4;    // [2][kMaxG]
+  static constexpr int kBars = kFactor + 2 * kMaxG * 4;
   // mbarriers: full, empty per K and V stage; S, P, product, q, sums: full and
-  // empty; all of a warp's products done; reference slots written
+  // empty; all of a warp's products done; reference slots written; a segment's
+  // factors: full and empty
   static constexpr int kKFull = 0, kKEmpty = kKFull + kStages, kVFull = kKEmpty + kStages,
                        kVEmpty = kVFull + kStages, kSFull = kVEmpty + kStages,
                        kSEmpty = kSFull + 2, kPFull = kSEmpty + 2, kOFull = kPFull + 2,
                        kOEmpty = kOFull + 2, kQFull = kOEmpty + 2, kQEmpty = kQFull + 2,
                        kLFull = kQEmpty + 2, kLEmpty = kLFull + 2, kDrain = kLEmpty + 2,
-                       kRefFull = kDrain + 2, kNumBars = kRefFull + kRefs;
+                       kRefFull = kDrain + 2, kFFull = kRefFull + kRefs, kFEmpty = kFFull + 2,
+                       kNumBars = kFEmpty + 2;
   static constexpr int kMisc = kBars + kNumBars * 8;               // ints, see View
   static constexpr int kUsed = kMisc + (kSlots + 2 * kGroups + 6) * 4;
   static constexpr int kAlloc = kUsed + 1024;
@@ -217,6 +219,11 @@ struct Segment {
   Unit U;
   int u, pf, lo, hi, bt, b, g, first_tok;
   __device__ __forceinline__ int steps() const { return (hi - lo + 1) / 2; }
+  __device__ __forceinline__ bool whole() const { return U.n_parts == 1; }
+  // the segment's partial slot, where the unit has several
+  __device__ __forceinline__ size_t slot() const {
+    return U.part_base + (int)blockIdx.x - U.first_cta;
+  }
 };
 
 // Calls f(segment, index) for every segment of this CTA until f returns false.
@@ -475,9 +482,9 @@ __device__ __forceinline__ void product_warp(const P& p, const View& v, uint32_t
 }
 
 // ---------------------------------------------------------------------------
-// q of a segment as hi and lo parts, and its scales: the output warps, two
+// q of a segment as hi and lo parts, and its scales: by the output warps, two
 // heads each, for a CTA's first segment (on one warp it takes 3.7 us, the
-// longest part of a launch's start), warp 15 ahead of time for the others.
+// longest part of a launch's start), by warp 15 ahead of time for the others.
 // ---------------------------------------------------------------------------
 template <int D, int kHeads, class P>
 __device__ __forceinline__ void convert_q(const P& p, const View& v, const Segment& s, int buffer,
@@ -530,20 +537,117 @@ __device__ __forceinline__ void convert_q(const P& p, const View& v, const Segme
   __syncwarp();
 }
 
+// ---------------------------------------------------------------------------
+// Warp 15: what is not done per step: q ahead of its segment, the factors of a
+// segment's outputs (and its log-sum-exp) from its sums, and empty units.
+// ---------------------------------------------------------------------------
 template <int D, class P>
-__device__ __forceinline__ void q_warp(const P& p, const View& v, int lane) {
+__device__ __forceinline__ bool segment_factors(const P& p, const View& v, const Segment& s,
+                                                Ring<2>& r, int lane) {
   using S = Smem<D>;
-  Ring<2> qr;
-  for_segments(p, [&](const Segment& s, int seg) {
-    if (seg > 0) {
-      if (seg == 1) ptx::grid_dependency_wait();
-      if (!warp_wait(p, v, S::kQEmpty + qr.i, qr.phase ^ 1)) return false;
+  if (!warp_wait(p, v, S::kFEmpty + r.i, r.phase ^ 1) ||
+      !warp_wait(p, v, S::kLFull + r.i, r.phase))
+    return false;
+  const float* seg_l = reinterpret_cast<const float*>(v.base + S::kSegL) +
+                       r.i * kSoftmaxWarps * kMaxG;
+  const float* sr = reinterpret_cast<const float*>(v.base + S::kSegRef) + r.i * kGroups * kMaxG;
+  float* factor = reinterpret_cast<float*>(v.base + S::kFactor) + r.i * kMaxG;
+  const bool nan = (v.seg_poison[r.i * kGroups] | v.seg_poison[r.i * kGroups + 1]) != 0;
+  if (lane < kMaxG) {
+    const float qnan = __int_as_float(0x7fc00000);
+    float m = -INFINITY, l = 0.f, f;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) m = fmaxf(m, sr[g * kMaxG + lane]);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const float* w = seg_l + g * kGroupWarps * kMaxG + lane;
+      l = fmaf(ref_weight(sr[g * kMaxG + lane], m),
+               (w[0] + w[kMaxG]) + (w[2 * kMaxG] + w[3 * kMaxG]), l);
+    }
+    if (s.whole()) {
+      f = 1.0f / l;
+      if (lane < p.G) {
+        const size_t row = (size_t)s.bt * p.Hq + s.g * p.G + lane;
+        const float x = nan ? qnan : lse_of(m, l);
+        p.lse[row] = x;
+        if (p.lse2) p.lse2[row] = x;
+      }
+    } else {
+      // The reference bounds V's scales too; the partial's is moved to the
+      // sum's own magnitude, so that partials of blocks whose V scales lie far
+      // apart still meet near their weights.
+      const int e = l > 0.f ? ((__float_as_int(l) >> 23) - 127 + 4) >> 3 << 3 : 0;
+      const int k = max(-112, min(112, e));
+      f = ptx::pow2i(-k);
+      reinterpret_cast<float2*>(p.part_ml)[s.slot() * kMaxG + lane] =
+          make_float2(nan ? qnan : m + (float)k, l * f);
+    }
+    factor[lane] = nan ? qnan : f;
+  }
+  __syncwarp();
+  if (lane == 0) {
+    ptx::mbar_arrive(v.bar(S::kLEmpty + r.i));
+    ptx::mbar_arrive(v.bar(S::kFFull + r.i));
+  }
+  r.next();
+  return true;
+}
+
+template <int D, class P>
+__device__ __forceinline__ void helper_warp(const P& p, const View& v, int lane) {
+  using S = Smem<D>;
+  Ring<2> qr, fr;
+  ptx::grid_dependency_wait();
+  // Empty units: output 0, LSE -inf.
+  for (int u = blockIdx.x; u < p.n_units; u += p.grid) {
+    const Unit& U = p.units[u];
+    if (unit_pages(U.tok_start, U.tok_end) != 0) continue;
+    const int bt = U.bt_g / p.Hkv;
+    const int g = U.bt_g - bt * p.Hkv;
+    const int b = bt / p.T;
+    const size_t row = (size_t)bt * p.Hq + g * p.G;
+    for (int i = lane; i < p.G * D; i += 32) {
+      p.out[row * D + i] = 0.f;
+      if (p.out2) p.out2[row * D + i] = 0.f;
+    }
+    if (lane < p.G) {
+      p.lse[row + lane] = -INFINITY;
+      if (p.lse2) p.lse2[row + lane] = -INFINITY;
+    }
+    if (p.m_out) {
+      // its part in the pair's merge, as finish_unit does it
+      int* counter = p.req_counters + b * p.Hkv + g;
+      __syncwarp();
+      int prev = lane == 0 ? ptx::atomic_add_acq_rel_gpu(counter, 1) : 0;
+      prev = __shfl_sync(0xffffffffu, prev, 0);
+      if (prev + 1 == U.pair_total) {
+        for (int r = 0; r < p.G; ++r) {
+          const int h = g * p.G + r;
+          mergerow::merge_row<true>(p.out, p.lse, b * p.T, p.T, p.Hq, h, D,
+                                    p.m_out + ((size_t)b * p.Hq + h) * D,
+                                    p.m_lse + (size_t)b * p.Hq + h, lane);
+        }
+        if (lane == 0) *counter = 0;
+      }
+    }
+  }
+  Segment last;
+  bool any = false, ok = true;
+  for_segments(p, [&](const Segment& s, int) {
+    if (any) {
+      ok = warp_wait(p, v, S::kQEmpty + qr.i, qr.phase ^ 1);
+      if (!ok) return false;
       convert_q<D, kMaxG>(p, v, s, qr.i, 0, lane);
       if (lane < kOutWarps) ptx::mbar_arrive(v.bar(S::kQFull + qr.i));
+      ok = segment_factors<D>(p, v, last, fr, lane);
+      if (!ok) return false;
     }
-    qr.next();
+    qr.next();   // (the output warps convert the first segment's)
+    last = s;
+    any = true;
     return true;
   });
+  if (any && ok) segment_factors<D>(p, v, last, fr, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -723,30 +827,12 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
                                              int lane) {
   using S = Smem<D>;
   const int ct = warp * 32 + lane;
-  const float qnan = __int_as_float(0x7fc00000);
   ptx::grid_dependency_wait();   // earlier kernels write q and may still read the outputs
   for_segments(p, [&](const Segment& s, int) {
     convert_q<D, kMaxG / kOutWarps>(p, v, s, 0, warp * (kMaxG / kOutWarps), lane);
     if (lane == 0) ptx::mbar_arrive(v.bar(S::kQFull));
     return false;   // the first segment's
   });
-  // Empty units: output 0, LSE -inf.
-  for (int u = blockIdx.x; u < p.n_units; u += p.grid) {
-    const Unit U = p.units[u];
-    if (unit_pages(U.tok_start, U.tok_end) != 0) continue;
-    const int bt = U.bt_g / p.Hkv;
-    const int g = U.bt_g - bt * p.Hkv;
-    const size_t orow = (size_t)bt * p.Hq + g * p.G;
-    for (int i = ct; i < p.G * D; i += kOut) {
-      p.out[orow * D + i] = 0.f;
-      if (p.out2) p.out2[orow * D + i] = 0.f;
-    }
-    if (ct < p.G) {
-      p.lse[orow + ct] = -INFINITY;
-      if (p.lse2) p.lse2[orow + ct] = -INFINITY;
-    }
-    finish_unit<D, kOut>(p, v, bt / p.T, g, ct, warp, lane, 1, U.pair_total);
-  }
   int it = 0;
   for_segments(p, [&](const Segment& s, int seg) {
     float acc[S::kChunks][kMaxG], ref[kMaxG];
@@ -764,28 +850,29 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
       fail = !wait(p, v, S::kRefFull + it % kRefs, (it / kRefs) & 1) ||
              !wait(p, v, S::kOFull + (it & 1), (it >> 1) & 1);
       if (fail) break;
-      const float* slot = reinterpret_cast<const float*>(v.base + S::kRef) + (it % kRefs) * kMaxG;
-      // The two groups' references move apart: the sum keeps the largest seen
-      // (a rescale where a slot is above it) and weighs each step's product.
-      float by[kMaxG];
-      bool moved = false;
+      const float4* slot = reinterpret_cast<const float4*>(v.base + S::kRef) +
+                           (it % kRefs) * (kMaxG / 4);
+      const float4 lo = slot[0], hi = slot[1];
+      float by[kMaxG] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      bool same = true;
 #pragma unroll
-      for (int h = 0; h < kMaxG; ++h) {
-        by[h] = slot[h];
-        moved |= by[h] > ref[h];
-      }
-      if (moved) {
+      for (int h = 0; h < kMaxG; ++h) same = same && by[h] == ref[h];
+      if (same) {
+#pragma unroll
+        for (int h = 0; h < kMaxG; ++h) by[h] = 1.0f / kFirstPart;
+      } else {
+        // The two groups' references move apart: the sum keeps the largest seen
+        // (a rescale where a slot is above it) and weighs each step's product.
 #pragma unroll
         for (int h = 0; h < kMaxG; ++h) {
           const float to = fmaxf(ref[h], by[h]);
           const float a = ref_weight(ref[h], to);
 #pragma unroll
           for (int c = 0; c < S::kChunks; ++c) acc[c][h] *= a;
+          by[h] = ref_weight(by[h], to) * (1.0f / kFirstPart);
           ref[h] = to;
         }
       }
-#pragma unroll
-      for (int h = 0; h < kMaxG; ++h) by[h] = ref_weight(by[h], ref[h]) * (1.0f / kFirstPart);
       tc::fence_after();
       const uint32_t d = tmem + 2 * kQCols + (it & 1) * S::kChunks * kPCols +
                          ((uint32_t)(warp * 32) << 16);
@@ -811,54 +898,13 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(v.bar(S::kOEmpty + (it & 1)));
     }
-    fail = fail || !wait(p, v, S::kLFull + (seg & 1), (seg >> 1) & 1);
+    fail = fail || !wait(p, v, S::kFFull + (seg & 1), (seg >> 1) & 1);
     if (any_in_group(1, kOut, fail)) return false;
     // ---- the segment's output or partial ----
-    const float* seg_l = reinterpret_cast<const float*>(v.base + S::kSegL) +
-                         (seg & 1) * kSoftmaxWarps * kMaxG;
-    const float* sr = reinterpret_cast<const float*>(v.base + S::kSegRef) +
-                      (seg & 1) * kGroups * kMaxG;
-    const bool nan = (v.seg_poison[(seg & 1) * kGroups] | v.seg_poison[(seg & 1) * kGroups + 1]) != 0;
-    const int first_cta = cta_of(s.pf, p.total_pages, p.grid);
-    const bool whole = s.U.n_parts == 1;
+    const float* factor = reinterpret_cast<const float*>(v.base + S::kFactor) + (seg & 1) * kMaxG;
     const size_t orow = (size_t)s.bt * p.Hq + s.g * p.G;
-    const size_t slot = s.U.part_base + (int)blockIdx.x - first_cta;
-    // A thread per head: its sum, and the factor of its outputs.
-    float* factor = reinterpret_cast<float*>(v.base + S::kFactor);
-    if (ct < kMaxG) {
-      float m = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) m = fmaxf(m, sr[g * kMaxG + ct]);
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const float* w = seg_l + g * kGroupWarps * kMaxG + ct;
-        l = fmaf(ref_weight(sr[g * kMaxG + ct], m),
-                 (w[0] + w[kMaxG]) + (w[2 * kMaxG] + w[3 * kMaxG]), l);
-      }
-      float f, x;
-      if (whole) {
-        f = 1.0f / l;
-        x = lse_of(m, l);
-        if (ct < p.G) {
-          p.lse[orow + ct] = nan ? qnan : x;
-          if (p.lse2) p.lse2[orow + ct] = nan ? qnan : x;
-        }
-      } else {
-        // The reference bounds V's scales too; the partial's is moved to the
-        // sum's own magnitude, so that partials of blocks whose V scales lie
-        // far apart still meet near their weights.
-        const int e = l > 0.f ? ((__float_as_int(l) >> 23) - 127 + 4) >> 3 << 3 : 0;
-        const int k = max(-112, min(112, e));
-        f = ptx::pow2i(-k);
-        p.part_ml[(slot * kMaxG + ct) * 2 + 0] = nan ? qnan : m + (float)k;
-        p.part_ml[(slot * kMaxG + ct) * 2 + 1] = l * f;
-      }
-      factor[ct] = nan ? qnan : f;
-    }
-    ptx::named_barrier(1, kOut);
-    if (lane == 0) ptx::mbar_arrive(v.bar(S::kLEmpty + (seg & 1)));
-    float* dst = (whole ? p.out + orow * D : p.part_o + slot * kMaxG * D) + ct;
-    float* dst2 = whole && p.out2 ? p.out2 + orow * D + ct : nullptr;
+    float* dst = (s.whole() ? p.out + orow * D : p.part_o + s.slot() * kMaxG * D) + ct;
+    float* dst2 = s.whole() && p.out2 ? p.out2 + orow * D + ct : nullptr;
 #pragma unroll
     for (int h = 0; h < kMaxG; ++h) {
       if (h >= p.G) break;
@@ -869,11 +915,15 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
         if (dst2) dst2[h * D + c * kChunk] = acc[c][h] * f;
       }
     }
-    if (whole)
-      finish_unit<D, kOut>(p, v, s.b, s.g, ct, warp, lane, 1, s.U.pair_total);
-    else
-      finish_split_unit<D, kOut>(p, v, s.U, s.u, s.b, s.bt, s.g, first_cta, ct, warp, lane);
-    ptx::named_barrier(1, kOut);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(v.bar(S::kFEmpty + (seg & 1)));
+    if (s.whole()) {
+      // without a merge pass nothing follows: the next segment may start
+      if (p.m_out) finish_unit<D, kOut>(p, v, s.b, s.g, ct, warp, lane, 1, s.U.pair_total);
+    } else {
+      finish_split_unit<D, kOut>(p, v, s.U, s.u, s.b, s.bt, s.g, s.U.first_cta, ct, warp, lane);
+      ptx::named_barrier(1, kOut);   // merge_info is read before it is written again
+    }
     return true;
   });
 }
@@ -909,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i >= S::kQFull && i < S::kQEmpty) n = kOutWarps;
       if (i >= S::kQEmpty && i < S::kLFull) n = kSoftmaxWarps + 1;    // and the last product
       if (i >= S::kLFull && i < S::kLEmpty) n = kSoftmaxWarps;
-      if (i >= S::kLEmpty && i < S::kDrain) n = kOutWarps;
+      if (i >= S::kFEmpty) n = kOutWarps;
       ptx::mbar_init(v.bar(i), n);
     }
     *v.abort_flag = 0;
@@ -932,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kProductWarp) {
     product_warp<D>(p, v, tmem);
   } else {
-    q_warp<D>(p, v, lane);
+    helper_warp<D>(p, v, lane);
   }
   __syncwarp();
   tc::fence_before();

@@ -67,7 +67,8 @@ struct Unit {
   int32_t tok_end;
   int32_t page_first;  // flattened index of the unit's first page in this launch
   int32_t part_base;   // first partial slot (units covered by several CTAs)
-  int32_t n_parts;     // CTAs covering the unit
+  int16_t n_parts;     // CTAs covering the unit
+  int16_t first_cta;   // the first of them
   int32_t pair_total;  // completions the (request, kv head) tile counter reaches (fused merge)
 };
 
@@ -457,7 +458,8 @@ int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int sms, Grid
       }
       const int k0 = cta_of(units[i].page_first, total, grid);
       const int k1 = cta_of(units[i].page_first + np - 1, total, grid);
-      units[i].n_parts = k1 - k0 + 1;
+      units[i].n_parts = static_cast<int16_t>(k1 - k0 + 1);
+      units[i].first_cta = static_cast<int16_t>(k0);
       if (units[i].n_parts > 1) {
         units[i].part_base = part_cursor;
         part_cursor += units[i].n_parts;
