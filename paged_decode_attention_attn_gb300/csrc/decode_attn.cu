@@ -921,7 +921,12 @@ int run(bool tensor_cores, const void* q, const void* pool, int64_t pool_pages,
   sms = std::min(sms, kMaxGrid);
 
   Plan plan;
-  const int rc_plan = plan_units(tiles, B, T, n_kv_heads, sms, launch_grid, kSegmentCharge, &plan);
+  const int rc_plan = plan_units(
+      tiles, B, T, n_kv_heads, kSegmentCharge,
+      [&](const Unit*, size_t, long long total, std::vector<int32_t>* starts) {
+        equal_starts(total, launch_grid(total, sms, n_kv_heads), starts);
+      },
+      &plan);
   if (rc_plan != PA_OK) return rc_plan;
   const std::vector<Unit>& units = plan.units;
 

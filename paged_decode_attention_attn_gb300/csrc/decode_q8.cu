@@ -73,7 +73,9 @@ constexpr int kTmaWarp = 12, kScoreWarp = 13, kProductWarp = 14;
 constexpr int kScaleCopies = 4;             // lanes that copy a step's scales
 constexpr int kThreads = 32 * 16;           // the last warp: per segment
 constexpr int kSegmentCharge = 6;           // pages charged per unit start
-constexpr int kWidePages = 32, kWideGridPct = 90;
+constexpr int kWholePages = 12;             // units this short are not split while SMs are idle
+constexpr int kMinPages = 4;                // pages per CTA at least, where units are split
+constexpr int kSnapPages = 4;               // how far a CTA's end moves to a unit's border
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kMaxScaleExp = 100;           // largest |log2| of a V scale
 
@@ -135,7 +137,6 @@ struct Params {
   float* part_o;
   float* part_ml;
   long long pool_pages;
-  long long total_pages;
   int max_pages;
   int T;
   int Hq;
@@ -153,6 +154,8 @@ struct Params {
   static constexpr bool kSecondOut = true;
   float* out2;
   float* lse2;
+  int32_t starts[kMaxGrid + 1];      // CTA k takes flattened pages [k], [k + 1)
+  int16_t first_unit[kMaxGrid + 1];  // and its first unit
   Unit units[kMaxUnits];
 };
 static_assert(sizeof(Params<kMaxUnitsLarge>) <= 32764, "kernel parameters too large");
@@ -229,10 +232,10 @@ struct Segment {
 // Calls f(segment, index) for every segment of this CTA until f returns false.
 template <class P, class F>
 __device__ __forceinline__ void for_segments(const P& p, F f) {
-  const int start = static_cast<int>((long long)blockIdx.x * p.total_pages / p.grid);
-  const int end = static_cast<int>((long long)(blockIdx.x + 1) * p.total_pages / p.grid);
+  const int start = p.starts[blockIdx.x];
+  const int end = p.starts[blockIdx.x + 1];
   int index = 0;
-  for (int u = first_unit(p, start); u < p.n_units && p.units[u].page_first < end; ++u) {
+  for (int u = p.first_unit[blockIdx.x]; u < p.n_units && p.units[u].page_first < end; ++u) {
     Segment s;
     s.U = p.units[u];
     const int np = unit_pages(s.U.tok_start, s.U.tok_end);
@@ -994,12 +997,67 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-int launch_grid(long long total, int sms, int n_kv_heads) {
-  if (total <= 0) return 1;
-  int grid = total >= (long long)kWidePages * sms ? std::max(1, sms * kWideGridPct / 100)
-                                                  : (int)std::min<long long>(sms, total);
-  if (grid >= n_kv_heads) grid -= grid % n_kv_heads;
-  return grid;
+// Cuts a launch's units into CTAs.  A unit on one CTA costs a step per two
+// pages (0.5-0.65 us); a unit on several costs partials and their merge, about
+// 2 us more.
+void cut(const Unit* units, size_t n, long long total, int sms, int heads,
+         std::vector<int32_t>* starts) {
+  int count = 0, most = 0, least = 1 << 30;   // units with pages
+  long long pages = 0;
+  for (size_t i = 0; i < n; ++i) {
+    const int np = unit_pages(units[i].tok_start, units[i].tok_end);
+    if (np == 0) continue;
+    ++count;
+    pages += np;
+    most = std::max(most, np);
+    least = std::min(least, np);
+  }
+  if (count == 0) {
+    starts->assign({0, 1});
+    return;
+  }
+  if (count <= sms && most <= kWholePages) {
+    starts->clear();
+    for (size_t i = 0; i < n; ++i)
+      if (unit_pages(units[i].tok_start, units[i].tok_end) != 0)
+        starts->push_back(starts->empty() ? 0 : units[i].page_first);
+    starts->push_back(static_cast<int32_t>(total));
+    return;
+  }
+  int grid = (int)std::max<long long>(1, std::min<long long>(sms, pages / kMinPages));
+  // As the bf16 kernel's: the CTAs at the same offset of each kv head's block
+  // of units stream the same pages at the same time.
+  if (grid >= heads) grid -= grid % heads;
+  if (most == least) {
+    // Units of one length: a grid that divides them, or that they divide, has no
+    // CTA with parts of two units.
+    for (int g = grid; g * 5 >= grid * 4; --g) {
+      if (count % g == 0 || g % count == 0) {
+        grid = g;
+        break;
+      }
+    }
+  }
+  starts->assign(1, 0);
+  long long at = 0;
+  size_t i = 0;
+  for (int k = 1; k < grid; ++k) {
+    long long to = at + (total - at) / (grid - k + 1);
+    // the unit that holds the border, if one does
+    while (i < n && (unit_pages(units[i].tok_start, units[i].tok_end) == 0 ||
+                     units[i].page_first + unit_pages(units[i].tok_start, units[i].tok_end) <= to))
+      ++i;
+    if (i < n && to > units[i].page_first) {
+      const long long lo = units[i].page_first;
+      const long long hi = lo + unit_pages(units[i].tok_start, units[i].tok_end);
+      if (to - lo <= kSnapPages && to - lo <= hi - to && lo > at) to = lo;
+      else if (hi - to <= kSnapPages) to = hi;
+    }
+    if (to <= at) continue;
+    starts->push_back(static_cast<int32_t>(to));
+    at = to;
+  }
+  if (total > at) starts->push_back(static_cast<int32_t>(total));
 }
 
 template <int D, int N>
@@ -1009,9 +1067,14 @@ int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L,
   Params<N> prm;
   std::memcpy(static_cast<void*>(&prm), &common, offsetof(Params<kMaxUnitsSmall>, units));
   prm.n_units = static_cast<int>(L.n);
-  prm.total_pages = L.total;
   prm.grid = L.grid;
   std::memcpy(prm.units, plan.units.data() + L.u0, L.n * sizeof(Unit));
+  std::memcpy(prm.starts, L.starts.data(), L.starts.size() * sizeof(int32_t));
+  for (int k = 0, u = 0; k < L.grid; ++k) {
+    // the last unit that starts at or before the CTA's first page
+    while (u + 1 < (int)L.n && prm.units[u + 1].page_first <= L.starts[k]) ++u;
+    prm.first_unit[k] = static_cast<int16_t>(u);
+  }
   static PerContext smem_limit;   // the attribute lives in the context
   cudaError_t e = smem_limit.apply([] {
     return cudaFuncSetAttribute(decode_q8_kernel<D, N>,
@@ -1081,7 +1144,12 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   if (sms <= 0) return fail(PA_ERR_CUDA, "cannot query the device's SM count");
   sms = std::min(sms, kMaxGrid);
   Plan plan;
-  int rc = plan_units(tiles, B, T, Hkv, sms, launch_grid, kSegmentCharge, &plan);
+  int rc = plan_units(
+      tiles, B, T, Hkv, kSegmentCharge,
+      [&](const Unit* units, size_t n, long long total, std::vector<int32_t>* starts) {
+        cut(units, n, total, sms, Hkv, starts);
+      },
+      &plan);
   if (rc != PA_OK) return rc;
 
   Params<kMaxUnitsSmall> common{};

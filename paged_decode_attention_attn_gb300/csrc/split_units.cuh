@@ -5,7 +5,7 @@
 // A unit is one (tile, kv head).  All units' pages are laid end to end and cut
 // into one contiguous page range per CTA.  A kernel's parameter struct P has
 // the fields these functions name (out, lse, status, arrivals, req_counters,
-// part_o, part_ml, total_pages, grid, T, Hq, Hkv, G, n_units, units, m_out,
+// part_o, part_ml, T, Hq, Hkv, G, n_units, units, m_out,
 // m_lse, wait_limit_ns, slice_wait_ns, and out2, lse2 where kSecondOut says that
 // outputs are written twice); its shared-memory view Sh has fin_flag
 // and merge_info.  The kConsumers threads that call a function meet at named
@@ -400,18 +400,26 @@ struct Launch {
   size_t u0, n;       // units [u0, u0 + n)
   long long total;    // flattened pages, at least 1
   int grid;
+  std::vector<int32_t> starts;   // [grid + 1] CTA k takes flattened pages [k], [k + 1)
 };
 struct Plan {
   std::vector<Unit> units;
   std::vector<Launch> launches;
 };
 
-// Lays a call's tiles out as units and launches.  grid_rule(total pages, SMs,
-// kv heads) gives a launch's CTAs, segment_charge the pages that hold no data
-// charged per unit start.
-template <class GridRule>
-int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int sms, GridRule grid_rule,
-               int segment_charge, Plan* plan) {
+// CTA boundaries that give `grid` CTAs equal shares.
+inline void equal_starts(long long total, int grid, std::vector<int32_t>* starts) {
+  starts->resize(grid + 1);
+  for (int k = 0; k <= grid; ++k) (*starts)[k] = static_cast<int32_t>(k * total / grid);
+}
+
+// Lays a call's tiles out as units and launches.  shape(units, n, total, starts)
+// cuts a launch's n units, laid out over `total` flattened pages, into CTAs;
+// segment_charge is the number of pages that hold no data charged per unit
+// start.
+template <class Shape>
+int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int segment_charge,
+               Shape shape, Plan* plan) {
   std::vector<Unit>& units = plan->units;
   units.reserve((size_t)B * T * n_kv_heads);
   // Kv-head-major order: the units of one kv head form a block of the page
@@ -448,17 +456,20 @@ int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int sms, Grid
       total += np;
       PA_REQUIRE(total < (1ll << 31), "too many pages in one launch");
     }
-    const int grid = grid_rule(total, sms, n_kv_heads);
-    int part_cursor = 0;
+    Launch L{u0, n, total > 0 ? total : 1, 1, {}};
+    shape(units.data() + u0, n, total, &L.starts);
+    L.grid = (int)L.starts.size() - 1;
+    int part_cursor = 0, k = 0;
     for (size_t i = u0; i < u0 + n; ++i) {
       const int np = unit_pages(units[i].tok_start, units[i].tok_end);
       if (np == 0) {
         units[i].n_parts = 0;
         continue;
       }
-      const int k0 = cta_of(units[i].page_first, total, grid);
-      const int k1 = cta_of(units[i].page_first + np - 1, total, grid);
-      units[i].n_parts = static_cast<int16_t>(k1 - k0 + 1);
+      while (L.starts[k + 1] <= units[i].page_first) ++k;
+      const int k0 = k;
+      while (L.starts[k + 1] < units[i].page_first + np) ++k;
+      units[i].n_parts = static_cast<int16_t>(k - k0 + 1);
       units[i].first_cta = static_cast<int16_t>(k0);
       if (units[i].n_parts > 1) {
         units[i].part_base = part_cursor;
@@ -468,7 +479,7 @@ int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int sms, Grid
     if ((size_t)part_cursor > slots)
       return fail(PA_ERR_INVALID, "internal: %d partial slots exceed the %zu reserved",
                   part_cursor, slots);
-    plan->launches.push_back({u0, n, total > 0 ? total : 1, grid});
+    plan->launches.push_back(std::move(L));
   }
   // Completions each (request, kv head) pair's tile count reaches: one per
   // unsplit or empty unit, one per merge slice of a split unit.
