@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 
+import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -510,93 +511,112 @@ def kv_append_rows(pool, page_table, positions, rows, status=None, stream=None,
                               _stream_handle(stream)))
 
 
-def _on(device, stream, call):
-    """Runs ``call(stream handle)`` with ``device`` current; ``stream`` None is
-    that device's current stream."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _on(device, stream, call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call_on(dev: int, stream, fn, *args):
+    """``fn(*args, stream handle)`` with device ``dev`` current; ``stream`` None
+    is that device's current stream."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call_on(dev, stream, fn, *args)
     if stream is None:
-        stream = torch.cuda.current_stream()
-    elif stream.device != device:
-        raise ValueError(f"stream of {stream.device}, tensors on {device}")
-    _check(call(stream.cuda_stream))
+        # (the handle alone: building the Stream object takes ~3 us)
+        handle = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
+    else:
+        if stream.device_index != dev:
+            raise ValueError(f"stream of device {stream.device_index}, tensors on device {dev}")
+        handle = stream.cuda_stream
+    rc = fn(*args, handle)
+    if rc != PA_OK:
+        raise PagedAttnError(rc, last_error())
 
 
-def _dev_on(device, t, dtype, name):
-    ptr = _dev(t, dtype, name)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the pool on {device}")
-    return ptr
+def _ptr(t, dtype, dev: int, name: str):
+    """Pointer of a contiguous tensor of ``dtype`` on CUDA device ``dev``."""
+    try:
+        if t.dtype == dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name)                      # raises for what it checks
+    raise ValueError(f"{name} is on {t.device}, the pool on cuda:{dev}")
 
 
-def _token_rows(device, t, name):
-    """Pointer and token stride of [tokens][heads][head_dim] activations whose
-    heads are dense within a token."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}, as the pool")
-    if t.dtype != torch.bfloat16 or t.dim() != 3:
-        raise ValueError(f"{name} must be bfloat16 [tokens][heads][head_dim]")
+def _token_rows(t, heads, n, d, dev: int, name: str):
+    """Pointer and token stride of bf16 [n][heads][d] activations whose heads
+    are dense within a token."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev}, as the pool")
+    if t.dtype != torch.bfloat16 or t.shape != (n, heads, d):
+        raise ValueError(f"{name} must be bfloat16 [{n}][{heads}][{d}], got {t.dtype} "
+                         f"{list(t.shape)}")
     st = t.stride()
-    if (st[2] != 1 and t.shape[2] > 1) or (st[1] != t.shape[2] and t.shape[1] > 1):
+    if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
         raise ValueError(f"{name} must be dense within a token")
     # the stride of a single token is never used and torch keeps any value there
-    return t.data_ptr(), st[0] if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return t.data_ptr(), st[0] if n > 1 else heads * d
 
 
-def _pages(pool, scales, dtype):
-    """Device, kv row elements of a pool tensor [pages][64][row]."""
-    if not isinstance(pool, torch.Tensor) or pool.device.type != "cuda":
+def _pages(pool, dtype) -> int:
+    """CUDA device index of a pool tensor [pages][64][row]."""
+    if not isinstance(pool, torch.Tensor) or not pool.is_cuda:
         raise ValueError("pool must be a CUDA tensor")
     if pool.dtype != dtype:
         raise ValueError(f"pool must be {dtype}, got {pool.dtype}")
     if pool.dim() != 3 or pool.shape[1] != PAGE_TOKENS or not pool.is_contiguous():
         raise ValueError("pool must be contiguous [pages][64][2*Hkv*D]")
-    if scales is not None:
-        _dev_on(pool.device, scales, torch.float32, "scales")
-    return pool.device
+    return pool.get_device()
+
+
+def _check_requests(page_table, positions, cu_tokens):
+    """B and max_pages of the per-request arguments."""
+    shape = page_table.shape
+    if len(shape) != 2 or positions.shape != shape[:1]:
+        raise ValueError("page_table must be [B][max_pages] and positions [B]")
+    if cu_tokens is not None and cu_tokens.shape != (shape[0] + 1,):
+        raise ValueError("cu_tokens must be [B + 1]")
+    return shape
 
 
 def _append_rope(fn, dtype, q, k, v, pool, scales, page_table, positions, inv_freq, q_out,
                  cu_tokens, interleaved, status, stream):
-    dev = _pages(pool, scales, dtype)
-    k_ptr, k_st = _token_rows(dev, k, "k")
-    v_ptr, v_st = _token_rows(dev, v, "v")
+    dev = _pages(pool, dtype)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a tensor [tokens][Hkv][D]")
     n, n_kv, d = k.shape
-    if v.shape != k.shape or pool.shape[2] != 2 * n_kv * d:
-        raise ValueError("k and v must be [tokens][Hkv][D] and pool rows 2*Hkv*D")
-    if scales is not None and tuple(scales.shape) != (pool.shape[0], 2 * n_kv,
-                                                      PAGE_TOKENS // SCALE_TOKENS):
-        raise ValueError("scales must be [pages][2*Hkv][4]")
+    n_pages, _, row = pool.shape
+    if row != 2 * n_kv * d:
+        raise ValueError(f"pool rows must hold 2*Hkv*D = {2 * n_kv * d} values, got {row}")
+    k_ptr, k_st = _token_rows(k, n_kv, n, d, dev, "k")
+    v_ptr, v_st = _token_rows(v, n_kv, n, d, dev, "v")
     q_ptr = o_ptr = None
     q_st = o_st = hq = 0
     if q is not None:
         if q_out is None:
             raise ValueError("q_out is required with q (q itself rotates in place)")
-        q_ptr, q_st = _token_rows(dev, q, "q")
-        o_ptr, o_st = _token_rows(dev, q_out, "q_out")
-        hq = q.shape[1]
-        if q.shape[0] != n or q.shape[2] != d or q_out.shape != q.shape:
-            raise ValueError("q and q_out must be [tokens][Hq][D]")
+        hq = q.shape[1] if q.dim() == 3 else 0
+        q_ptr, q_st = _token_rows(q, hq, n, d, dev, "q")
+        o_ptr, o_st = _token_rows(q_out, hq, n, d, dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    bn = page_table.shape[0]
-    if page_table.dim() != 2 or tuple(positions.shape) != (bn,):
-        raise ValueError("page_table must be [B][max_pages] and positions [B]")
-    if cu_tokens is not None and tuple(cu_tokens.shape) != (bn + 1,):
-        raise ValueError("cu_tokens must be [B + 1]")
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    args = [q_ptr, k_ptr, v_ptr, q_st, k_st, v_st, o_ptr, o_st,
-            None if cu_tokens is None else _dev_on(dev, cu_tokens, torch.int32, "cu_tokens"),
-            _dev_on(dev, positions, torch.int32, "positions"), n, bn, hq, n_kv, d,
-            None if inv_freq is None else _dev_on(dev, inv_freq, torch.float32, "inv_freq"), rot,
-            PA_ROPE_INTERLEAVED if interleaved else 0, pool.data_ptr()]
-    if scales is not None:
-        args.append(scales.data_ptr())
-    args += [pool.shape[0], _dev_on(dev, page_table, torch.int32, "page_table"),
-             page_table.shape[1],
-             None if status is None else _dev_on(dev, status, torch.int32, "status")]
-    _on(dev, stream, lambda s: fn(*args, s))
+    bn, max_pages = _check_requests(page_table, positions, cu_tokens)
+    i32 = torch.int32
+    cu = None if cu_tokens is None else _ptr(cu_tokens, i32, dev, "cu_tokens")
+    inv, rot = None, 0
+    if inv_freq is not None:
+        inv, rot = _ptr(inv_freq, torch.float32, dev, "inv_freq"), 2 * inv_freq.numel()
+    args = (q_ptr, k_ptr, v_ptr, q_st, k_st, v_st, o_ptr, o_st, cu,
+            _ptr(positions, i32, dev, "positions"), n, bn, hq, n_kv, d, inv, rot,
+            PA_ROPE_INTERLEAVED if interleaved else 0, pool.data_ptr())
+    tail = (n_pages, _ptr(page_table, i32, dev, "page_table"), max_pages,
+            None if status is None else _ptr(status, i32, dev, "status"))
+    if scales is None:
+        _call_on(dev, stream, fn, *args, *tail)
+        return
+    if scales.shape != (n_pages, 2 * n_kv, PAGE_TOKENS // SCALE_TOKENS):
+        raise ValueError("scales must be [pages][2*Hkv][4]")
+    _call_on(dev, stream, fn, *args, _ptr(scales, torch.float32, dev, "scales"), *tail)
 
 
 def kv_append_rope(q, k, v, pool, page_table, positions, inv_freq, q_out=None, cu_tokens=None,
@@ -629,25 +649,23 @@ def kv_gather_q8(pool, scales, page_table, positions, cu_tokens, out, status=Non
     None: one row per request)."""
     if scales is None or scales.dim() != 3:
         raise ValueError("scales must be [pages][2*Hkv][4]")
-    dev = _pages(pool, scales, torch.float8_e4m3fn)
+    dev = _pages(pool, torch.float8_e4m3fn)
+    n_pages, _, row = pool.shape
     heads = scales.shape[1]
-    if tuple(scales.shape) != (pool.shape[0], heads, PAGE_TOKENS // SCALE_TOKENS) or \
-            heads % 2 or heads == 0 or pool.shape[2] % heads:
+    if scales.shape != (n_pages, heads, PAGE_TOKENS // SCALE_TOKENS) or heads % 2 or \
+            heads == 0 or row % heads:
         raise ValueError("scales must be [pages][2*Hkv][4]")
-    if out.dim() != 2 or out.shape[1] != pool.shape[2]:
+    if out.dim() != 2 or out.shape[1] != row:
         raise ValueError("out must be [rows][2*Hkv*D]")
-    bn = page_table.shape[0]
-    if page_table.dim() != 2 or tuple(positions.shape) != (bn,):
-        raise ValueError("page_table must be [B][max_pages] and positions [B]")
-    if cu_tokens is not None and tuple(cu_tokens.shape) != (bn + 1,):
-        raise ValueError("cu_tokens must be [B + 1]")
-    args = (pool.data_ptr(), scales.data_ptr(), pool.shape[0],
-            _dev_on(dev, page_table, torch.int32, "page_table"), page_table.shape[1],
-            None if cu_tokens is None else _dev_on(dev, cu_tokens, torch.int32, "cu_tokens"),
-            _dev_on(dev, positions, torch.int32, "positions"), out.shape[0], bn, heads // 2,
-            pool.shape[2] // heads, _dev_on(dev, out, torch.bfloat16, "out"),
-            None if status is None else _dev_on(dev, status, torch.int32, "status"))
-    _on(dev, stream, lambda s: lib.kv_gather_q8(*args, s))
+    bn, max_pages = _check_requests(page_table, positions, cu_tokens)
+    i32 = torch.int32
+    _call_on(dev, stream, lib.kv_gather_q8, pool.data_ptr(),
+             _ptr(scales, torch.float32, dev, "scales"), n_pages,
+             _ptr(page_table, i32, dev, "page_table"), max_pages,
+             None if cu_tokens is None else _ptr(cu_tokens, i32, dev, "cu_tokens"),
+             _ptr(positions, i32, dev, "positions"), out.shape[0], bn, heads // 2, row // heads,
+             _ptr(out, torch.bfloat16, dev, "out"),
+             None if status is None else _ptr(status, i32, dev, "status"))
 
 
 def alloc_workspace_q8(B, T, n_q_heads, n_kv_heads, head_dim, device="cuda") -> torch.Tensor:
@@ -665,31 +683,38 @@ def paged_decode_attn_q8_lse(q, pool, scales, page_table, tiles, scale, out, lse
     tiles host int32 [B][T][2]; out fp32 [B][T][Hq][D], lse fp32 [B][T][Hq];
     ``merged_out`` [B][Hq][D] / ``merged_lse`` [B][Hq] receive the merge of
     every request's tiles in the same call."""
-    dev = _pages(pool, scales, torch.float8_e4m3fn)
+    dev = _pages(pool, torch.float8_e4m3fn)
     Bn, Hq, D = q.shape
-    n_kv = pool.shape[2] // (2 * D)
-    arr, tiles_ptr = _host_tiles(tiles)
-    if arr.ndim != 3 or arr.shape[0] != Bn or arr.shape[2] != 2:
+    n_pages, _, row = pool.shape
+    n_kv = row // (2 * D)
+    if tiles.__class__ is not np.ndarray or tiles.dtype != np.int32 or \
+            not tiles.flags.c_contiguous:
+        tiles = np.ascontiguousarray(np.asarray(tiles, dtype=np.int32))
+    if tiles.ndim != 3 or tiles.shape[0] != Bn or tiles.shape[2] != 2:
         raise ValueError("tiles must be [B][T][2]")
-    T = arr.shape[1]
-    if pool.shape[2] != 2 * n_kv * D or \
-            tuple(scales.shape) != (pool.shape[0], 2 * n_kv, PAGE_TOKENS // SCALE_TOKENS):
+    T = tiles.shape[1]
+    if row != 2 * n_kv * D or \
+            scales.shape != (n_pages, 2 * n_kv, PAGE_TOKENS // SCALE_TOKENS):
         raise ValueError("pool must be [pages][64][2*Hkv*D] and scales [pages][2*Hkv][4]")
-    if page_table.dim() != 2 or page_table.shape[0] != Bn:
+    table_shape = page_table.shape
+    if len(table_shape) != 2 or table_shape[0] != Bn:
         raise ValueError("page_table must be [B][max_pages]")
-    if tuple(out.shape) != (Bn, T, Hq, D) or tuple(lse.shape) != (Bn, T, Hq):
+    if out.shape != (Bn, T, Hq, D) or lse.shape != (Bn, T, Hq):
         raise ValueError("out must be [B][T][Hq][D] and lse [B][T][Hq]")
-    if merged_out is not None and (merged_lse is None or tuple(merged_out.shape) != (Bn, Hq, D)
-                                   or tuple(merged_lse.shape) != (Bn, Hq)):
-        raise ValueError("merged_out must be [B][Hq][D] and merged_lse [B][Hq]")
-    args = (_dev_on(dev, q, torch.bfloat16, "q"), pool.data_ptr(), scales.data_ptr(),
-            pool.shape[0], _dev_on(dev, page_table, torch.int32, "page_table"),
-            page_table.shape[1], tiles_ptr, Bn, T, Hq, n_kv, D, float(scale),
-            _dev_on(dev, out, torch.float32, "out"), _dev_on(dev, lse, torch.float32, "lse"),
-            None if merged_out is None else _dev_on(dev, merged_out, torch.float32, "merged_out"),
-            None if merged_lse is None else _dev_on(dev, merged_lse, torch.float32, "merged_lse"),
-            _dev_on(dev, workspace, torch.uint8, "workspace"), workspace.numel())
-    _on(dev, stream, lambda s: lib.paged_decode_attn_q8_lse(*args, s))
+    f32 = torch.float32
+    m_ptr = ml_ptr = None
+    if merged_out is not None or merged_lse is not None:
+        if merged_out is None or merged_lse is None or merged_out.shape != (Bn, Hq, D) or \
+                merged_lse.shape != (Bn, Hq):
+            raise ValueError("merged_out must be [B][Hq][D] and merged_lse [B][Hq]")
+        m_ptr = _ptr(merged_out, f32, dev, "merged_out")
+        ml_ptr = _ptr(merged_lse, f32, dev, "merged_lse")
+    _call_on(dev, stream, lib.paged_decode_attn_q8_lse, _ptr(q, torch.bfloat16, dev, "q"),
+             pool.data_ptr(), _ptr(scales, f32, dev, "scales"), n_pages,
+             _ptr(page_table, torch.int32, dev, "page_table"), table_shape[1],
+             tiles.ctypes.data, Bn, T, Hq, n_kv, D, float(scale),
+             _ptr(out, f32, dev, "out"), _ptr(lse, f32, dev, "lse"), m_ptr, ml_ptr,
+             _ptr(workspace, torch.uint8, dev, "workspace"), workspace.numel())
 
 
 class Arena:

@@ -75,6 +75,11 @@ constexpr int kThreads = 32 * 16;           // the last warp: per segment
 constexpr int kSegmentCharge = 6;           // pages charged per unit start
 constexpr int kWholePages = 12;             // units this short are not split while SMs are idle
 constexpr int kMinPages = 4;                // pages per CTA at least, where units are split
+// A launch of this many pages per SM runs on kLongGridPct percent of the SMs:
+// with HBM saturated, fewer and longer streams finish sooner (as the bf16
+// kernel's do; 100 / 90 / 85 / 80 percent on one box: 1 x 262,144 tokens 85.3 /
+// 84.4 / 83.7 / 83.2 us, 8 ragged of up to 131,072 247.5 / 245.5 / 244.5 / 242.1).
+constexpr int kLongPages = 64, kLongGridPct = 85;
 constexpr int kSnapPages = 4;               // how far a CTA's end moves to a unit's border
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kMaxScaleExp = 100;           // largest |log2| of a V scale
@@ -1000,31 +1005,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Cuts a launch's units into CTAs.  A unit on one CTA costs a step per two
 // pages (0.5-0.65 us); a unit on several costs partials and their merge, about
 // 2 us more.
-void cut(const Unit* units, size_t n, long long total, int sms, int heads,
+void cut(const Unit* units, const int32_t* pages, size_t n, long long total, int sms, int heads,
          std::vector<int32_t>* starts) {
   int count = 0, most = 0, least = 1 << 30;   // units with pages
-  long long pages = 0;
+  long long sum = 0;
   for (size_t i = 0; i < n; ++i) {
-    const int np = unit_pages(units[i].tok_start, units[i].tok_end);
-    if (np == 0) continue;
+    if (pages[i] == 0) continue;
     ++count;
-    pages += np;
-    most = std::max(most, np);
-    least = std::min(least, np);
+    sum += pages[i];
+    most = std::max(most, pages[i]);
+    least = std::min(least, pages[i]);
   }
   if (count == 0) {
     starts->assign({0, 1});
     return;
   }
+  starts->reserve(sms + 1);
   if (count <= sms && most <= kWholePages) {
-    starts->clear();
     for (size_t i = 0; i < n; ++i)
-      if (unit_pages(units[i].tok_start, units[i].tok_end) != 0)
-        starts->push_back(starts->empty() ? 0 : units[i].page_first);
+      if (pages[i] != 0) starts->push_back(starts->empty() ? 0 : units[i].page_first);
     starts->push_back(static_cast<int32_t>(total));
     return;
   }
-  int grid = (int)std::max<long long>(1, std::min<long long>(sms, pages / kMinPages));
+  int grid = sum >= (long long)kLongPages * sms ? sms * kLongGridPct / 100
+                                                : (int)std::min<long long>(sms, sum / kMinPages);
+  grid = std::max(grid, 1);
   // As the bf16 kernel's: the CTAs at the same offset of each kv head's block
   // of units stream the same pages at the same time.
   if (grid >= heads) grid -= grid % heads;
@@ -1038,23 +1043,20 @@ void cut(const Unit* units, size_t n, long long total, int sms, int heads,
       }
     }
   }
-  starts->assign(1, 0);
-  long long at = 0;
+  starts->push_back(0);
+  int at = 0;
   size_t i = 0;
   for (int k = 1; k < grid; ++k) {
-    long long to = at + (total - at) / (grid - k + 1);
+    int to = at + ((int)total - at) / (grid - k + 1);
     // the unit that holds the border, if one does
-    while (i < n && (unit_pages(units[i].tok_start, units[i].tok_end) == 0 ||
-                     units[i].page_first + unit_pages(units[i].tok_start, units[i].tok_end) <= to))
-      ++i;
+    while (i < n && (pages[i] == 0 || units[i].page_first + pages[i] <= to)) ++i;
     if (i < n && to > units[i].page_first) {
-      const long long lo = units[i].page_first;
-      const long long hi = lo + unit_pages(units[i].tok_start, units[i].tok_end);
+      const int lo = units[i].page_first, hi = lo + pages[i];
       if (to - lo <= kSnapPages && to - lo <= hi - to && lo > at) to = lo;
       else if (hi - to <= kSnapPages) to = hi;
     }
     if (to <= at) continue;
-    starts->push_back(static_cast<int32_t>(to));
+    starts->push_back(to);
     at = to;
   }
   if (total > at) starts->push_back(static_cast<int32_t>(total));
@@ -1145,10 +1147,9 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   sms = std::min(sms, kMaxGrid);
   Plan plan;
   int rc = plan_units(
-      tiles, B, T, Hkv, kSegmentCharge,
-      [&](const Unit* units, size_t n, long long total, std::vector<int32_t>* starts) {
-        cut(units, n, total, sms, Hkv, starts);
-      },
+      tiles, B, T, Hkv, kSegmentCharge, T > 1 && merged_out != nullptr,
+      [&](const Unit* units, const int32_t* pages, size_t n, long long total,
+          std::vector<int32_t>* starts) { cut(units, pages, n, total, sms, Hkv, starts); },
       &plan);
   if (rc != PA_OK) return rc;
 

@@ -404,6 +404,7 @@ struct Launch {
 };
 struct Plan {
   std::vector<Unit> units;
+  std::vector<int32_t> pages;      // of each unit
   std::vector<Launch> launches;
 };
 
@@ -413,26 +414,31 @@ inline void equal_starts(long long total, int grid, std::vector<int32_t>* starts
   for (int k = 0; k <= grid; ++k) (*starts)[k] = static_cast<int32_t>(k * total / grid);
 }
 
-// Lays a call's tiles out as units and launches.  shape(units, n, total, starts)
-// cuts a launch's n units, laid out over `total` flattened pages, into CTAs;
-// segment_charge is the number of pages that hold no data charged per unit
-// start.
+// Lays a call's tiles out as units and launches.  shape(units, their pages, n,
+// total, starts) cuts a launch's n units, laid out over `total` flattened
+// pages, into CTAs; segment_charge is the number of pages that hold no data
+// charged per unit start; merge: the call merges every request's tiles.
 template <class Shape>
-int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int segment_charge,
+int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int segment_charge, bool merge,
                Shape shape, Plan* plan) {
+  const size_t n_tiles = (size_t)B * T, n_units = n_tiles * n_kv_heads;
   std::vector<Unit>& units = plan->units;
-  units.reserve((size_t)B * T * n_kv_heads);
+  std::vector<int32_t>& pages = plan->pages;
+  units.resize(n_units);
+  pages.resize(n_units);
   // Kv-head-major order: the units of one kv head form a block of the page
   // sequence, and every block has the same unit sizes, so the CTAs at the
   // same offset of the n_kv_heads blocks stream the same physical pages (each
   // its head's slice of every row) at about the same time.
+  for (size_t bt = 0; bt < n_tiles; ++bt)
+    pages[bt] = unit_pages(tiles[2 * bt], tiles[2 * bt + 1]);
   for (int g = 0; g < n_kv_heads; ++g) {
-    for (int bt = 0; bt < B * T; ++bt) {
-      Unit u{};
-      u.bt_g = bt * n_kv_heads + g;
-      u.tok_start = tiles[2 * bt];
-      u.tok_end = tiles[2 * bt + 1];
-      units.push_back(u);
+    Unit* u = units.data() + g * n_tiles;
+    if (g > 0) std::copy_n(pages.data(), n_tiles, pages.data() + g * n_tiles);
+    for (size_t bt = 0; bt < n_tiles; ++bt) {
+      u[bt].bt_g = static_cast<int32_t>(bt * n_kv_heads + g);
+      u[bt].tok_start = tiles[2 * bt];
+      u[bt].tok_end = tiles[2 * bt + 1];
     }
   }
 
@@ -441,39 +447,35 @@ int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int segment_c
   // All launches are laid out first: the fused merge's per-(request, kv
   // head) count spans every launch that holds a tile of the pair.
   const size_t slots = part_slots(B, T, n_kv_heads);
-  for (size_t u0 = 0; u0 < units.size(); u0 += kMaxUnitsLarge) {
-    const size_t n = std::min<size_t>(kMaxUnitsLarge, units.size() - u0);
-    // The CTAs' equal shares are cut from the units' pages laid end to end,
-    // each unit preceded by segment_charge pages that hold no data: a segment
-    // (one unit's part on one CTA) costs a Q load, a combine and a partial
-    // whatever its length, so a CTA whose range holds a unit start (one more
-    // segment) gets that many fewer pages to stream.
+  for (size_t u0 = 0; u0 < n_units; u0 += kMaxUnitsLarge) {
+    const size_t n = std::min<size_t>(kMaxUnitsLarge, n_units - u0);
+    // The CTAs' shares are cut from the units' pages laid end to end, each unit
+    // preceded by segment_charge pages that hold no data: a segment (one unit's
+    // part on one CTA) costs a Q load, a combine and a partial whatever its
+    // length, so a CTA whose range holds a unit start (one more segment) gets
+    // that many fewer pages to stream.
     long long total = 0;
     for (size_t i = u0; i < u0 + n; ++i) {
-      const int np = unit_pages(units[i].tok_start, units[i].tok_end);
-      if (np > 0) total += segment_charge;
+      if (pages[i] > 0) total += segment_charge;
       units[i].page_first = static_cast<int32_t>(total);
-      total += np;
+      total += pages[i];
       PA_REQUIRE(total < (1ll << 31), "too many pages in one launch");
     }
     Launch L{u0, n, total > 0 ? total : 1, 1, {}};
-    shape(units.data() + u0, n, total, &L.starts);
+    shape(units.data() + u0, pages.data() + u0, n, total, &L.starts);
     L.grid = (int)L.starts.size() - 1;
     int part_cursor = 0, k = 0;
     for (size_t i = u0; i < u0 + n; ++i) {
-      const int np = unit_pages(units[i].tok_start, units[i].tok_end);
-      if (np == 0) {
-        units[i].n_parts = 0;
-        continue;
-      }
-      while (L.starts[k + 1] <= units[i].page_first) ++k;
+      Unit& u = units[i];
+      if (pages[i] == 0) continue;     // no parts
+      while (L.starts[k + 1] <= u.page_first) ++k;
       const int k0 = k;
-      while (L.starts[k + 1] < units[i].page_first + np) ++k;
-      units[i].n_parts = static_cast<int16_t>(k - k0 + 1);
-      units[i].first_cta = static_cast<int16_t>(k0);
-      if (units[i].n_parts > 1) {
-        units[i].part_base = part_cursor;
-        part_cursor += units[i].n_parts;
+      while (L.starts[k + 1] < u.page_first + pages[i]) ++k;
+      u.n_parts = static_cast<int16_t>(k - k0 + 1);
+      u.first_cta = static_cast<int16_t>(k0);
+      if (k > k0) {
+        u.part_base = part_cursor;
+        part_cursor += k - k0 + 1;
       }
     }
     if ((size_t)part_cursor > slots)
@@ -481,17 +483,16 @@ int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int segment_c
                   part_cursor, slots);
     plan->launches.push_back(std::move(L));
   }
+  if (!merge) return PA_OK;
   // Completions each (request, kv head) pair's tile count reaches: one per
   // unsplit or empty unit, one per merge slice of a split unit.
-  {
-    std::vector<int32_t> pair_total((size_t)B * n_kv_heads, 0);
-    auto pair_of = [&](const Unit& U) {
-      const int bt = U.bt_g / n_kv_heads;
-      return (size_t)(bt / T) * n_kv_heads + (U.bt_g - bt * n_kv_heads);
-    };
-    for (const Unit& U : units)
-      pair_total[pair_of(U)] += U.n_parts > 1 ? split_slices(U.n_parts) : 1;
-    for (Unit& U : units) U.pair_total = pair_total[pair_of(U)];
+  for (int g = 0; g < n_kv_heads; ++g) {
+    for (int b = 0; b < B; ++b) {
+      Unit* u = units.data() + (g * (size_t)B + b) * T;
+      int count = 0;
+      for (int t = 0; t < T; ++t) count += u[t].n_parts > 1 ? split_slices(u[t].n_parts) : 1;
+      for (int t = 0; t < T; ++t) u[t].pair_total = count;
+    }
   }
   return PA_OK;
 }
