@@ -6,14 +6,21 @@
 // position).  The angle is needed modulo one turn only, so inv_freq[i] / 2 pi
 // is held as a 64-bit binary fraction of a turn and multiplied by the position
 // in integers: the product wraps modulo one turn by itself and keeps its low
-// bits at any position (fp32 angles lose all of them near 2^24).  The sine and
-// cosine of a token's pairs are computed once per CTA and shared by its heads.
+// bits at any position (fp32 angles lose all of them near 2^24).  No fp64 is
+// used (its rate on this part made a prompt's angles cost more than its
+// bytes).  A token's sines and cosines are computed once for all its heads.
+//
+// Rows (bf16 pool, and q of both kinds): a warp takes a token row, or a share
+// of its heads when there are few rows; a lane keeps its pairs' sines and
+// cosines in registers and moves 16 (or 8) bytes per load.
 //
 // 8-bit blocks: kBlock consecutive tokens of one head share one fp32 scale, a
 // power of two, so rows that were already there are requantised exactly (but
 // for codes that become subnormal) when a larger row makes the scale grow.
-// One warp takes one (block, head): it holds the block's new rows in
-// registers, so the amax and the store read them once.
+// One warp takes one (block, head), once for the largest value and once for
+// the codes; the second reading of more than four rows comes from L1 (16 rows
+// in registers left two CTAs per SM, and the launch at 94 us where this takes
+// @@ for 2 prompts of ~4,000 tokens).
 //
 // All of it is bound by HBM at prompt sizes and by the latency of its
 // dependent loads (request, position, page, row) at decode sizes.
@@ -24,6 +31,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "common.h"
 #include "fp8.cuh"
@@ -38,6 +46,7 @@ constexpr int kBlocks = kPage / kBlock;   // scale blocks per page
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRows = 8;               // token rows per CTA of the row-wise kernels
+constexpr int kRowCtas = 304;             // CTAs that a launch keeps when it takes more rows each
 
 struct Tokens {
   const __nv_bfloat16* q;
@@ -87,163 +96,182 @@ __device__ __forceinline__ long long page_of(const int32_t* page_table, int max_
   return page < pool_pages ? page : -1;
 }
 
-// (cos, sin) of position p at inverse frequency f.
-__device__ __forceinline__ float2 turn(long long pos, float f) {
-  const double turns = (double)f * 0.15915494309189535;   // 1 / (2 pi)
-  const double part = turns - floor(turns);
-  const unsigned long long step = (unsigned long long)(part * 18446744073709551616.0);
-  const unsigned long long at = step * (unsigned long long)pos;
-  float2 cs;
-  sincospif((float)(int)(at >> 32) * 4.656612873077393e-10f, &cs.y, &cs.x);   // 2^-31
-  return cs;
+// Turns per position, modulo one, in units of 2^-64: f / (2 pi) from f's 24
+// significant bits and 1 / (2 pi) to 66 bits.
+__device__ __forceinline__ unsigned long long turn_step(float f) {
+  constexpr unsigned long long kInvTwoPi = 0xa2f9836e4e44152aull;  // 2^66 / (2 pi)
+  const unsigned bits = __float_as_uint(f);
+  const int e = (bits >> 23) & 255;
+  const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const unsigned long long lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
+  // f = m 2^(max(e, 1) - 150): the product is 2^(shift - 64) times the result
+  const int shift = 152 - max(e, 1);
+  unsigned long long x;
+  if (shift >= 64) x = shift < 128 ? hi >> (shift - 64) : 0ull;
+  else if (shift > 0) x = (hi << (64 - shift)) | (lo >> shift);
+  else x = shift > -64 ? lo << -shift : 0ull;
+  return (bits >> 31) ? 0ull - x : x;
 }
 
-// A lane holds four pairs of one head row as two 4-element vectors a and b at
-// element offsets oa and ob of the head: pairs 4l .. 4l+3, which lie half a
+// Sine and cosine at position p.
+__device__ __forceinline__ void turn(long long p, unsigned long long step, float* s, float* c) {
+  const unsigned long long at = step * (unsigned long long)p;
+  sincospif((float)(int)(at >> 32) * 4.656612873077393e-10f, s, c);   // 2^-31
+}
+
+template <int V>
+using Vec = typename std::conditional<V == 8, uint4, uint2>::type;
+
+// A lane holds V pairs of one head row as two V-element vectors a and b at
+// element offsets oa and ob of the head: pairs Vl .. Vl + V-1, which lie half a
 // rotation apart (a holds the first, b the second of each pair) or next to
-// each other (interleaved; a holds pairs 0 and 1, b pairs 2 and 3).  Lanes
+// each other (interleaved; a holds the first V/2 pairs, b the others).  Lanes
 // behind the rotated part hold the elements that pass.
 struct Lane {
   int oa, ob, pair;
   bool turns;
 };
+template <int V>
 __device__ __forceinline__ Lane lane_of(int l, int half, int interleaved) {
   Lane x;
-  x.pair = 4 * l;
+  x.pair = V * l;
   x.turns = x.pair < half;
   const bool apart = x.turns && !interleaved;
   x.oa = apart ? x.pair : 2 * x.pair;
-  x.ob = apart ? x.pair + half : 2 * x.pair + 4;
+  x.ob = apart ? x.pair + half : 2 * x.pair + V;
   return x;
 }
 
-// The lane's eight values, rotated in fp32: y[0..3] for a, y[4..7] for b.
-__device__ __forceinline__ void rotate(uint2 a, uint2 b, const Lane& ln, int interleaved,
-                                       const float2* cs, float (&y)[8]) {
-  y[0] = ptx::bf16_lo_to_f32(a.x);
-  y[1] = ptx::bf16_hi_to_f32(a.x);
-  y[2] = ptx::bf16_lo_to_f32(a.y);
-  y[3] = ptx::bf16_hi_to_f32(a.y);
-  y[4] = ptx::bf16_lo_to_f32(b.x);
-  y[5] = ptx::bf16_hi_to_f32(b.x);
-  y[6] = ptx::bf16_lo_to_f32(b.y);
-  y[7] = ptx::bf16_hi_to_f32(b.y);
-  if (!ln.turns) return;
-  const float4 c01 = *reinterpret_cast<const float4*>(cs + ln.pair);
-  const float4 c23 = *reinterpret_cast<const float4*>(cs + ln.pair + 2);
-  const float c[4] = {c01.x, c01.z, c23.x, c23.z};
-  const float s[4] = {c01.y, c01.w, c23.y, c23.w};
+// The lane's 2 V values in fp32, rotated by its pairs' c and s if turns: the
+// first V are a's.
+template <int V>
+__device__ __forceinline__ void rotate(const Vec<V>& a, const Vec<V>& b, bool turns,
+                                       int interleaved, const float* c, const float* s,
+                                       float (&y)[2 * V]) {
+  const uint32_t* wa = reinterpret_cast<const uint32_t*>(&a);
+  const uint32_t* wb = reinterpret_cast<const uint32_t*>(&b);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    y[2 * i] = ptx::bf16_lo_to_f32(wa[i]);
+    y[2 * i + 1] = ptx::bf16_hi_to_f32(wa[i]);
+    y[V + 2 * i] = ptx::bf16_lo_to_f32(wb[i]);
+    y[V + 2 * i + 1] = ptx::bf16_hi_to_f32(wb[i]);
+  }
+  if (!turns) return;
   if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < V; ++i) {
       const float u = y[2 * i], w = y[2 * i + 1];
       y[2 * i] = u * c[i] - w * s[i];
       y[2 * i + 1] = w * c[i] + u * s[i];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float u = y[i], w = y[i + 4];
+    for (int i = 0; i < V; ++i) {
+      const float u = y[i], w = y[i + V];
       y[i] = u * c[i] - w * s[i];
-      y[i + 4] = w * c[i] + u * s[i];
+      y[i + V] = w * c[i] + u * s[i];
     }
   }
 }
 
-__device__ __forceinline__ uint2 pack4(const float* y) {
-  return make_uint2(ptx::pack_bf16x2(__float2bfloat16_rn(y[0]), __float2bfloat16_rn(y[1])),
-                    ptx::pack_bf16x2(__float2bfloat16_rn(y[2]), __float2bfloat16_rn(y[3])));
+template <int V>
+__device__ __forceinline__ Vec<V> pack(const float* y) {
+  Vec<V> r;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i)
+    w[i] = ptx::pack_bf16x2(__float2bfloat16_rn(y[2 * i]), __float2bfloat16_rn(y[2 * i + 1]));
+  return r;
 }
 
-// Rotates the q heads of token rows [row0, row0 + rows) into q_out and, with
-// kKv, stores their k (rotated) and v heads in the bf16 pool.
-template <int D, bool kKv>
+// Rotates the q heads of `rows` (1, 2, 4 or 8) token rows from row0 on into
+// q_out and, with kKv, stores their k (rotated) and v heads in the bf16 pool.
+// Warps do not wait for each other.
+template <int D, int V, bool kKv>
 __device__ __forceinline__ void rotate_rows(const Tokens& t, __nv_bfloat16* pool, int row0,
                                             int rows) {
-  constexpr int kLanes = D / 8;              // lanes per head row
+  constexpr int kLanes = D / (2 * V);        // lanes per head row
   constexpr int kHeads = 32 / kLanes;        // head rows a warp takes at once
   constexpr int kUnroll = 4;
-  __shared__ __align__(16) float2 cs[kMaxRows][D / 2];
-  __shared__ long long s_pos[kMaxRows];
-  __shared__ long long s_dst[kMaxRows];      // pool element of the row; -1: not stored
-  __shared__ int s_live[kMaxRows];
+  __shared__ __align__(16) float table[kWarps][2][D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  rows = min(rows, t.n_tokens - row0);
-  for (int r = warp; r < rows; r += kWarps) {
-    int b = 0, first, end;
-    long long pos = 0, dst = -1;
-    const bool live = locate(t.cu, t.positions, t.B, t.n_tokens, row0 + r, lane, &b, &pos, &first,
-                             &end);
-    if (kKv && live) {
-      const long long page = page_of(t.page_table, t.max_pages, t.pool_pages, b, pos);
-      if (page >= 0) dst = (page * kPage + pos % kPage) * (2ll * t.Hkv * D);
-      else if (lane == 0 && t.status) atomicOr(t.status, PA_STATUS_BAD_ROW);
-    }
-    if (lane == 0) {
-      s_pos[r] = pos;
-      s_dst[r] = dst;
-      s_live[r] = live;
+  const int share = kWarps / rows;           // warps per row
+  const int row = row0 + warp / share;
+  if (row >= t.n_tokens) return;
+  int b = 0, first, end;
+  long long pos = 0;
+  if (!locate(t.cu, t.positions, t.B, t.n_tokens, row, lane, &b, &pos, &first, &end)) return;
+  __nv_bfloat16* dst_row = nullptr;
+  if (kKv) {
+    const long long page = page_of(t.page_table, t.max_pages, t.pool_pages, b, pos);
+    if (page >= 0) dst_row = pool + (page * kPage + pos % kPage) * (2ll * t.Hkv * D);
+    else if (lane == 0 && t.status) atomicOr(t.status, PA_STATUS_BAD_ROW);
+  }
+  for (int i = lane; i < t.half; i += 32)
+    turn(pos, turn_step(__ldg(t.inv_freq + i)), &table[warp][1][i], &table[warp][0][i]);
+  __syncwarp();
+  const Lane ln = lane_of<V>(lane % kLanes, t.half, t.interleaved);
+  float c[V], s[V];
+  if (ln.turns) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      *reinterpret_cast<float4*>(c + i) =
+          *reinterpret_cast<const float4*>(&table[warp][0][ln.pair + i]);
+      *reinterpret_cast<float4*>(s + i) =
+          *reinterpret_cast<const float4*>(&table[warp][1][ln.pair + i]);
     }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * t.half; i += kThreads) {
-    const int r = i / t.half, j = i - r * t.half;
-    if (s_live[r]) cs[r][j] = turn(s_pos[r], __ldg(t.inv_freq + j));
-  }
-  __syncthreads();
-  const Lane ln = lane_of(lane % kLanes, t.half, t.interleaved);
-  const int heads = t.Hq + (kKv ? 2 * t.Hkv : 0);
-  const int total = rows * heads;
-  for (int u0 = warp * kHeads + lane / kLanes; u0 < total; u0 += kUnroll * kWarps * kHeads) {
-    uint2 a[kUnroll], b[kUnroll];
+  const __nv_bfloat16* q = t.q + row * t.q_stride;
+  const __nv_bfloat16* k = t.k + row * t.k_stride;
+  const __nv_bfloat16* v = t.v + row * t.v_stride;
+  __nv_bfloat16* q_out = t.q_out + row * t.q_out_stride;
+  const int heads = t.Hq + (kKv && dst_row ? 2 * t.Hkv : 0);
+  const int step = share * kHeads;
+  for (int h0 = (warp % share) * kHeads + lane / kLanes; h0 < heads; h0 += kUnroll * step) {
+    Vec<V> va[kUnroll], vb[kUnroll];
     __nv_bfloat16* dst[kUnroll];
-    int row[kUnroll];
     bool turns[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int u = u0 + i * kWarps * kHeads;
-      const int r = u < total ? u / heads : 0;
-      const int h = u - r * heads;
-      const __nv_bfloat16* src;
+      const int h = h0 + i * step, g = h - t.Hq;
       dst[i] = nullptr;
-      row[i] = r;
-      turns[i] = true;
-      if (u >= total || !s_live[r]) continue;
-      if (h < t.Hq) {
-        src = t.q + (row0 + r) * t.q_stride + h * D;
-        dst[i] = t.q_out + (row0 + r) * t.q_out_stride + h * D;
+      if (h >= heads) continue;
+      const __nv_bfloat16* src;
+      turns[i] = ln.turns;
+      if (!kKv || g < 0) {
+        src = q + h * D;
+        dst[i] = q_out + h * D;
       } else {
-        const int g = h - t.Hq;
-        if (s_dst[r] < 0) continue;
-        turns[i] = g < t.Hkv;
-        src = turns[i] ? t.k + (row0 + r) * t.k_stride + g * D
-                       : t.v + (row0 + r) * t.v_stride + (g - t.Hkv) * D;
-        dst[i] = pool + s_dst[r] + g * D;
+        src = g < t.Hkv ? k + g * D : v + (g - t.Hkv) * D;
+        turns[i] = ln.turns && g < t.Hkv;
+        dst[i] = dst_row + g * D;
       }
-      a[i] = *reinterpret_cast<const uint2*>(src + ln.oa);
-      b[i] = *reinterpret_cast<const uint2*>(src + ln.ob);
+      va[i] = *reinterpret_cast<const Vec<V>*>(src + ln.oa);
+      vb[i] = *reinterpret_cast<const Vec<V>*>(src + ln.ob);
     }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       if (dst[i] == nullptr) continue;
-      if (turns[i] && ln.turns) {
-        float y[8];
-        rotate(a[i], b[i], ln, t.interleaved, cs[row[i]], y);
-        a[i] = pack4(y);
-        b[i] = pack4(y + 4);
+      if (turns[i]) {
+        float y[2 * V];
+        rotate<V>(va[i], vb[i], true, t.interleaved, c, s, y);
+        va[i] = pack<V>(y);
+        vb[i] = pack<V>(y + V);
       }
-      *reinterpret_cast<uint2*>(dst[i] + ln.oa) = a[i];
-      *reinterpret_cast<uint2*>(dst[i] + ln.ob) = b[i];
+      // an interleaved row's v (or a passing part) keeps its bits
+      *reinterpret_cast<Vec<V>*>(dst[i] + ln.oa) = va[i];
+      *reinterpret_cast<Vec<V>*>(dst[i] + ln.ob) = vb[i];
     }
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads)
+template <int D, int V>
+__global__ void __launch_bounds__(kThreads, 3)
     append_rope_kernel(const Tokens t, __nv_bfloat16* pool, int rows) {
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
-  rotate_rows<D, true>(t, pool, blockIdx.x * rows, rows);
+  rotate_rows<D, V, true>(t, pool, blockIdx.x * rows, rows);
 }
 
 // Smallest power of two s >= 2^-60 with amax <= 448 s (448 = 1.75 * 2^8 is the
@@ -257,14 +285,16 @@ __device__ __forceinline__ float block_scale(unsigned amax_bits) {
 // block's rows [first, first + n_new).
 template <int D>
 __device__ __forceinline__ void store_block(const Tokens& t, uint8_t* pool, float* scales,
-                                            const float2 (*cs)[D / 2], int row, int n_new,
+                                            const float (*cs)[2][D / 2], int row, int n_new,
                                             int first, long long page, int blk, int h, int lane) {
-  constexpr int kLanes = D / 8;
+  constexpr int V = 4;
+  constexpr int kLanes = D / (2 * V);
   constexpr int kRows = 32 / kLanes;         // token rows a warp takes at once
-  constexpr int kSteps = kBlock / kRows;
+  constexpr int kUnroll = 4;
   const int sub = lane / kLanes;
-  const Lane ln = lane_of(lane % kLanes, t.half, t.interleaved);
+  const Lane ln = lane_of<V>(lane % kLanes, t.half, t.interleaved);
   const bool is_k = h < t.Hkv;
+  const bool turns = ln.turns && is_k;
   const long long stride = is_k ? t.k_stride : t.v_stride;
   const __nv_bfloat16* src =
       (is_k ? t.k + h * D : t.v + (h - t.Hkv) * D) + (long long)row * stride;
@@ -272,32 +302,58 @@ __device__ __forceinline__ void store_block(const Tokens& t, uint8_t* pool, floa
   uint8_t* base = pool + ((size_t)page * kPage + blk * kBlock) * row_bytes + (size_t)h * D;
   float* scale = scales + ((size_t)page * 2 * t.Hkv + h) * kBlocks + blk;
   const float old = first > 0 ? *scale : 0.f;
-  uint2 a[kSteps], b[kSteps];
+  Vec<V> a[kUnroll], b[kUnroll];
+  auto load = [&](int r0) {
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int r = i * kRows + sub;
-    if (r < n_new) {
-      a[i] = *reinterpret_cast<const uint2*>(src + r * stride + ln.oa);
-      b[i] = *reinterpret_cast<const uint2*>(src + r * stride + ln.ob);
-    }
-  }
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int r = i * kRows + sub;
-    if (r < n_new) {
-      float y[8];
-      Lane l2 = ln;
-      l2.turns = ln.turns && is_k;
-      rotate(a[i], b[i], l2, t.interleaved, cs[r], y);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float m = fabsf(y[j]);
-        amax = fmaxf(amax, m <= FLT_MAX ? m : 0.f);   // infinities and NaN set no scale
+    for (int i = 0; i < kUnroll; ++i) {
+      const int r = r0 + i * kRows + sub;
+      if (r < n_new) {
+        a[i] = *reinterpret_cast<const Vec<V>*>(src + r * stride + ln.oa);
+        b[i] = *reinterpret_cast<const Vec<V>*>(src + r * stride + ln.ob);
       }
     }
+  };
+  // f(row, its rotated values) for the rows held
+  auto each = [&](int r0, auto f) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int r = r0 + i * kRows + sub;
+      if (r < n_new) {
+        float y[2 * V], c[V], s[V];
+        if (turns) {
+          *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(&cs[r][0][ln.pair]);
+          *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(&cs[r][1][ln.pair]);
+        }
+        rotate<V>(a[i], b[i], turns, t.interleaved, c, s, y);
+        f(r, y);
+      }
+    }
+  };
+  unsigned amax = 0;   // as bits, which order magnitudes
+  for (int r0 = 0; r0 < n_new; r0 += kUnroll * kRows) {
+    load(r0);
+    each(r0, [&](int, const float (&y)[2 * V]) {
+#pragma unroll
+      for (int j = 0; j < 2 * V; ++j) amax = max(amax, __float_as_uint(y[j]) & 0x7fffffffu);
+    });
   }
-  const float need = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  const bool odd = amax >= 0x7f800000u;   // infinities or NaN, which set no scale
+  if (odd) {
+    amax = 0;
+    for (int r0 = 0; r0 < n_new; r0 += kUnroll * kRows) {
+      if (n_new > kUnroll * kRows) load(r0);
+      each(r0, [&](int, const float (&y)[2 * V]) {
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) {
+          const unsigned m = __float_as_uint(y[j]) & 0x7fffffffu;
+          amax = max(amax, m < 0x7f800000u ? m : 0u);
+        }
+      });
+    }
+    amax = __reduce_max_sync(0xffffffffu, amax);
+  }
+  const float need = block_scale(amax);
   const float s = first > 0 ? fmaxf(old, need) : need;
   if (first > 0 && s != old) {
     // The scale grows: the block's older rows are requantised.
@@ -311,21 +367,18 @@ __device__ __forceinline__ void store_block(const Tokens& t, uint8_t* pool, floa
     }
   }
   const float inv = 1.0f / s;   // exact for a power of two
+  for (int r0 = 0; r0 < n_new; r0 += kUnroll * kRows) {
+    if (n_new > kUnroll * kRows) load(r0);
+    each(r0, [&](int r, float (&y)[2 * V]) {
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int r = i * kRows + sub;
-    if (r < n_new) {
-      float y[8];
-      Lane l2 = ln;
-      l2.turns = ln.turns && is_k;
-      rotate(a[i], b[i], l2, t.interleaved, cs[r], y);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        y[j] = fabsf(y[j]) <= FLT_MAX ? y[j] * inv : __int_as_float(0x7fc00000);
+      for (int j = 0; j < 2 * V; ++j) {
+        if (odd && !(fabsf(y[j]) <= FLT_MAX)) y[j] = __int_as_float(0x7fc00000);
+        y[j] *= inv;
+      }
       uint8_t* dst = base + (size_t)(first + r) * row_bytes;
       *reinterpret_cast<uint32_t*>(dst + ln.oa) = fp8::pack4(y[0], y[1], y[2], y[3]);
       *reinterpret_cast<uint32_t*>(dst + ln.ob) = fp8::pack4(y[4], y[5], y[6], y[7]);
-    }
+    });
   }
   if (lane == 0 && (first == 0 || s != old)) *scale = s;
 }
@@ -333,17 +386,17 @@ __device__ __forceinline__ void store_block(const Tokens& t, uint8_t* pool, floa
 // CTAs [0, kv_ctas) take `chunk` token rows each and store the blocks whose
 // first new row lies among them (a request's first new row, or a row on a
 // block border); the other CTAs rotate q rows.
-template <int D>
-__global__ void __launch_bounds__(kThreads)
+template <int D, int V>
+__global__ void __launch_bounds__(kThreads, 3)
     append_rope_q8_kernel(const Tokens t, uint8_t* pool, float* scales, int kv_ctas, int chunk,
                           int q_rows) {
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
   if ((int)blockIdx.x >= kv_ctas) {
-    rotate_rows<D, false>(t, nullptr, (blockIdx.x - kv_ctas) * q_rows, q_rows);
+    rotate_rows<D, V, false>(t, nullptr, (blockIdx.x - kv_ctas) * q_rows, q_rows);
     return;
   }
-  __shared__ __align__(16) float2 cs[kBlock][D / 2];
+  __shared__ __align__(16) float cs[kBlock][2][D / 2];
   __shared__ long long s_pos[kBlock], s_page[kBlock];
   __shared__ int s_new[kBlock];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -370,9 +423,11 @@ __global__ void __launch_bounds__(kThreads)
     const int n = s_new[r];
     if (n <= 0) continue;
     const long long pos = s_pos[r];
-    for (int i = threadIdx.x; i < n * t.half; i += kThreads) {
-      const int k = i / t.half, j = i - k * t.half;
-      cs[k][j] = turn(pos + k, __ldg(t.inv_freq + j));
+    constexpr int kPairs = D / 2;            // threads per row of the table
+    for (int j = threadIdx.x % kPairs; j < t.half; j += kPairs) {
+      const unsigned long long step = turn_step(__ldg(t.inv_freq + j));
+      for (int k = threadIdx.x / kPairs; k < n; k += kThreads / kPairs)
+        turn(pos + k, step, &cs[k][1][j], &cs[k][0][j]);
     }
     __syncthreads();
     const int in_page = (int)(pos % kPage);
@@ -412,31 +467,48 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   const int per_row = heads * d / 16;
-  for (int i = threadIdx.x; i < rows * per_row; i += kThreads) {
-    const int r = i / per_row, c = i - r * per_row;
+  constexpr int kUnroll = 4;
+  for (int r = threadIdx.x / 128; r < rows; r += kThreads / 128) {
     if (!s_live[r]) continue;
-    uint4 codes = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);   // NaN
-    float s = 1.f;
-    if (s_page[r] >= 0) {
-      const int at = (int)(s_pos[r] % kPage);
-      codes = __ldg(reinterpret_cast<const uint4*>(
-                        pool + ((size_t)s_page[r] * kPage + at) * heads * d) + c);
-      s = __ldg(scales + ((size_t)s_page[r] * heads + c * 16 / d) * kBlocks + at / kBlock);
-    }
-    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-    uint4 o[2];
-    uint32_t* ow = reinterpret_cast<uint32_t*>(o);
+    const bool there = s_page[r] >= 0;
+    const int at = (int)(s_pos[r] % kPage);
+    const uint4* src = reinterpret_cast<const uint4*>(
+        pool + ((size_t)(there ? s_page[r] : 0) * kPage + at) * heads * d);
+    const float* sc = scales + (size_t)(there ? s_page[r] : 0) * heads * kBlocks + at / kBlock;
+    uint4* dst = reinterpret_cast<uint4*>(out + (size_t)(row0 + r) * heads * d);
+    for (int c0 = threadIdx.x % 128; c0 < per_row; c0 += kUnroll * 128) {
+      uint4 codes[kUnroll];
+      float s[kUnroll];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float y[4];
-      fp8::unpack4(w[j], y);
-      ow[2 * j] = ptx::pack_bf16x2(__float2bfloat16_rn(y[0] * s), __float2bfloat16_rn(y[1] * s));
-      ow[2 * j + 1] =
-          ptx::pack_bf16x2(__float2bfloat16_rn(y[2] * s), __float2bfloat16_rn(y[3] * s));
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + i * 128;
+        codes[i] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);   // NaN
+        s[i] = 1.f;
+        if (c < per_row && there) {
+          codes[i] = __ldg(src + c);
+          s[i] = __ldg(sc + c * 16 / d * kBlocks);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + i * 128;
+        if (c >= per_row) break;
+        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+        uint4 o[2];
+        uint32_t* ow = reinterpret_cast<uint32_t*>(o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float y[4];
+          fp8::unpack4(w[j], y);
+          ow[2 * j] = ptx::pack_bf16x2(__float2bfloat16_rn(y[0] * s[i]),
+                                       __float2bfloat16_rn(y[1] * s[i]));
+          ow[2 * j + 1] = ptx::pack_bf16x2(__float2bfloat16_rn(y[2] * s[i]),
+                                           __float2bfloat16_rn(y[3] * s[i]));
+        }
+        dst[2 * c] = o[0];
+        dst[2 * c + 1] = o[1];
+      }
     }
-    uint4* dst = reinterpret_cast<uint4*>(out + (size_t)(row0 + r) * heads * d) + 2 * c;
-    dst[0] = o[0];
-    dst[1] = o[1];
   }
 }
 
@@ -446,9 +518,12 @@ __global__ void __launch_bounds__(kThreads)
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // Token rows per CTA of the row-wise kernels: one while the launch is small
-// (every CTA's dependent loads then run at the same time), more once there
-// are several CTAs per SM.
-int rows_per_cta(int n_tokens) { return std::max(1, std::min(kMaxRows, n_tokens / 1024)); }
+// (its warps then share the row's heads), more once there are CTAs enough.
+int rows_per_cta(int n_tokens) {
+  int rows = 1;
+  while (rows < kMaxRows && n_tokens / (2 * rows) >= kRowCtas) rows *= 2;
+  return rows;
+}
 
 int check_tokens(const Tokens& t, int head_dim, int rot_dim, unsigned flags, const void* pool) {
   PA_REQUIRE(t.n_tokens >= 0 && t.B >= 0, "n_tokens and B must be >= 0 (got %d, %d)", t.n_tokens,
@@ -509,14 +584,14 @@ Tokens tokens_of(const void* q, const void* k, const void* v, int64_t q_stride, 
   return t;
 }
 
-template <int D>
+template <int D, int V>
 cudaError_t launch_append(const Tokens& t, void* pool, cudaStream_t stream) {
   const int rows = rows_per_cta(t.n_tokens);
-  return launch_dependent(append_rope_kernel<D>, dim3((t.n_tokens + rows - 1) / rows),
+  return launch_dependent(append_rope_kernel<D, V>, dim3((t.n_tokens + rows - 1) / rows),
                           dim3(kThreads), 0, stream, t, static_cast<__nv_bfloat16*>(pool), rows);
 }
 
-template <int D>
+template <int D, int V>
 cudaError_t launch_append_q8(const Tokens& t, void* pool, float* scales, cudaStream_t stream) {
   const int rows = rows_per_cta(t.n_tokens);
   // A CTA of one row is either one block's or leaves at once, which is the
@@ -525,9 +600,12 @@ cudaError_t launch_append_q8(const Tokens& t, void* pool, float* scales, cudaStr
   const int chunk = t.cu == nullptr || t.n_tokens <= 1024 ? 1 : kBlock;
   const int kv = (t.n_tokens + chunk - 1) / chunk;
   const int q = t.q ? (t.n_tokens + rows - 1) / rows : 0;
-  return launch_dependent(append_rope_q8_kernel<D>, dim3(kv + q), dim3(kThreads), 0, stream, t,
+  return launch_dependent(append_rope_q8_kernel<D, V>, dim3(kv + q), dim3(kThreads), 0, stream, t,
                           static_cast<uint8_t*>(pool), scales, kv, chunk, rows);
 }
+
+// Pairs per lane: 8 (16-byte accesses) unless the rotated half is no multiple.
+bool wide(const Tokens& t) { return t.half % 8 == 0; }
 
 }  // namespace rope
 }  // namespace pa
@@ -550,9 +628,13 @@ extern "C" int kv_append_rope(const void* q, const void* k, const void* v, int64
                     head_dim);
   const int rc = check_tokens(t, head_dim, rot_dim, flags, pool);
   if (rc != PA_OK || n_tokens == 0 || B == 0) return rc;
-  PA_CHECK_CUDA(head_dim == 64    ? launch_append<64>(t, pool, stream)
-                : head_dim == 128 ? launch_append<128>(t, pool, stream)
-                                  : launch_append<256>(t, pool, stream));
+  const bool w = wide(t);
+  PA_CHECK_CUDA(head_dim == 64 ? (w ? launch_append<64, 8>(t, pool, stream)
+                                    : launch_append<64, 4>(t, pool, stream))
+                : head_dim == 128 ? (w ? launch_append<128, 8>(t, pool, stream)
+                                       : launch_append<128, 4>(t, pool, stream))
+                                  : (w ? launch_append<256, 8>(t, pool, stream)
+                                       : launch_append<256, 4>(t, pool, stream)));
   PA_CHECK_CUDA(cudaGetLastError());
   return PA_OK;
 }
@@ -575,8 +657,11 @@ extern "C" int kv_append_rope_q8(const void* q, const void* k, const void* v, in
   const int rc = check_tokens(t, head_dim, rot_dim, flags, pool);
   if (rc != PA_OK || n_tokens == 0 || B == 0) return rc;
   PA_REQUIRE(scales != nullptr && aligned16(scales), "scales must be non-null, 16-byte aligned");
-  PA_CHECK_CUDA(head_dim == 128 ? launch_append_q8<128>(t, pool, scales, stream)
-                                : launch_append_q8<256>(t, pool, scales, stream));
+  const bool w = wide(t);
+  PA_CHECK_CUDA(head_dim == 128 ? (w ? launch_append_q8<128, 8>(t, pool, scales, stream)
+                                     : launch_append_q8<128, 4>(t, pool, scales, stream))
+                                : (w ? launch_append_q8<256, 8>(t, pool, scales, stream)
+                                     : launch_append_q8<256, 4>(t, pool, scales, stream)));
   PA_CHECK_CUDA(cudaGetLastError());
   return PA_OK;
 }
