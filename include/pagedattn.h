@@ -339,7 +339,7 @@ int kv_append_rows(void* pool, int64_t pool_pages, const int32_t* page_table,
  *              overlap q otherwise, nor k or v.
  *   cu_tokens  device int32 [B+1], non-decreasing, cu_tokens[0] = 0; requests
  *              may have no tokens; rows at and behind cu_tokens[B] (padding)
- *              are neither read nor written.  NULL: one token per request,
+ *              take no part: nothing is written for them.  NULL: one token per request,
  *              n_tokens == B.
  *   positions  device int32 [B], position of each request's first new token.
  *   inv_freq   device fp32 [rot_dim / 2] (may be NULL when rot_dim is 0).

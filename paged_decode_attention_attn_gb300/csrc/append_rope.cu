@@ -199,19 +199,40 @@ __device__ __forceinline__ void rotate_rows(const Tokens& t, __nv_bfloat16* pool
   const int share = kWarps / rows;           // warps per row
   const int row = row0 + warp / share;
   if (row >= t.n_tokens) return;
+  const Lane ln = lane_of<V>(lane % kLanes, t.half, t.interleaved);
+  const __nv_bfloat16* q = t.q + row * t.q_stride;
+  const __nv_bfloat16* k = t.k + row * t.k_stride;
+  const __nv_bfloat16* v = t.v + row * t.v_stride;
+  const int heads = t.Hq + (kKv ? 2 * t.Hkv : 0);
+  const int step = share * kHeads;
+  int h0 = (warp % share) * kHeads + lane / kLanes;
+  Vec<V> va[kUnroll], vb[kUnroll];
+  auto load = [&]() {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int h = h0 + i * step, g = h - t.Hq;
+      if (h >= heads) continue;
+      const __nv_bfloat16* src = !kKv || g < 0 ? q + h * D
+                                 : g < t.Hkv   ? k + g * D
+                                               : v + (g - t.Hkv) * D;
+      va[i] = *reinterpret_cast<const Vec<V>*>(src + ln.oa);
+      vb[i] = *reinterpret_cast<const Vec<V>*>(src + ln.ob);
+    }
+  };
+  load();   // before the row's request, position and page are known
   int b = 0, first, end;
   long long pos = 0;
   if (!locate(t.cu, t.positions, t.B, t.n_tokens, row, lane, &b, &pos, &first, &end)) return;
-  __nv_bfloat16* dst_row = nullptr;
-  if (kKv) {
-    const long long page = page_of(t.page_table, t.max_pages, t.pool_pages, b, pos);
-    if (page >= 0) dst_row = pool + (page * kPage + pos % kPage) * (2ll * t.Hkv * D);
-    else if (lane == 0 && t.status) atomicOr(t.status, PA_STATUS_BAD_ROW);
-  }
   for (int i = lane; i < t.half; i += 32)
     turn(pos, turn_step(__ldg(t.inv_freq + i)), &table[warp][1][i], &table[warp][0][i]);
+  __nv_bfloat16* q_out = t.q_out + row * t.q_out_stride;
+  __nv_bfloat16* kv_out = nullptr;
+  if (kKv) {
+    const long long page = page_of(t.page_table, t.max_pages, t.pool_pages, b, pos);
+    if (page >= 0) kv_out = pool + (page * kPage + pos % kPage) * (2ll * t.Hkv * D);
+    else if (lane == 0 && t.status) atomicOr(t.status, PA_STATUS_BAD_ROW);
+  }
   __syncwarp();
-  const Lane ln = lane_of<V>(lane % kLanes, t.half, t.interleaved);
   float c[V], s[V];
   if (ln.turns) {
 #pragma unroll
@@ -222,47 +243,24 @@ __device__ __forceinline__ void rotate_rows(const Tokens& t, __nv_bfloat16* pool
           *reinterpret_cast<const float4*>(&table[warp][1][ln.pair + i]);
     }
   }
-  const __nv_bfloat16* q = t.q + row * t.q_stride;
-  const __nv_bfloat16* k = t.k + row * t.k_stride;
-  const __nv_bfloat16* v = t.v + row * t.v_stride;
-  __nv_bfloat16* q_out = t.q_out + row * t.q_out_stride;
-  const int heads = t.Hq + (kKv && dst_row ? 2 * t.Hkv : 0);
-  const int step = share * kHeads;
-  for (int h0 = (warp % share) * kHeads + lane / kLanes; h0 < heads; h0 += kUnroll * step) {
-    Vec<V> va[kUnroll], vb[kUnroll];
-    __nv_bfloat16* dst[kUnroll];
-    bool turns[kUnroll];
+  while (true) {
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const int h = h0 + i * step, g = h - t.Hq;
-      dst[i] = nullptr;
-      if (h >= heads) continue;
-      const __nv_bfloat16* src;
-      turns[i] = ln.turns;
-      if (!kKv || g < 0) {
-        src = q + h * D;
-        dst[i] = q_out + h * D;
-      } else {
-        src = g < t.Hkv ? k + g * D : v + (g - t.Hkv) * D;
-        turns[i] = ln.turns && g < t.Hkv;
-        dst[i] = dst_row + g * D;
-      }
-      va[i] = *reinterpret_cast<const Vec<V>*>(src + ln.oa);
-      vb[i] = *reinterpret_cast<const Vec<V>*>(src + ln.ob);
-    }
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      if (dst[i] == nullptr) continue;
-      if (turns[i]) {
+      if (h >= heads || (kKv && g >= 0 && kv_out == nullptr)) continue;
+      if (ln.turns && (!kKv || g < t.Hkv)) {   // v and what passes keep their bits
         float y[2 * V];
         rotate<V>(va[i], vb[i], true, t.interleaved, c, s, y);
         va[i] = pack<V>(y);
         vb[i] = pack<V>(y + V);
       }
-      // an interleaved row's v (or a passing part) keeps its bits
-      *reinterpret_cast<Vec<V>*>(dst[i] + ln.oa) = va[i];
-      *reinterpret_cast<Vec<V>*>(dst[i] + ln.ob) = vb[i];
+      __nv_bfloat16* dst = !kKv || g < 0 ? q_out + h * D : kv_out + g * D;
+      *reinterpret_cast<Vec<V>*>(dst + ln.oa) = va[i];
+      *reinterpret_cast<Vec<V>*>(dst + ln.ob) = vb[i];
     }
+    h0 += kUnroll * step;
+    if (h0 - lane / kLanes >= heads) break;
+    load();
   }
 }
 
@@ -383,24 +381,28 @@ __device__ __forceinline__ void store_block(const Tokens& t, uint8_t* pool, floa
   if (lane == 0 && (first == 0 || s != old)) *scale = s;
 }
 
-// CTAs [0, kv_ctas) take `chunk` token rows each and store the blocks whose
-// first new row lies among them (a request's first new row, or a row on a
-// block border); the other CTAs rotate q rows.
+// kv_ctas CTAs take `chunk` token rows each and store the blocks whose first
+// new row lies among them (a request's first new row, or a row on a block
+// border); the others rotate q rows.  The two kinds alternate, so that an SM
+// has CTAs that wait for their loads beside CTAs that stream.
 template <int D, int V>
 __global__ void __launch_bounds__(kThreads, 3)
     append_rope_q8_kernel(const Tokens t, uint8_t* pool, float* scales, int kv_ctas, int chunk,
                           int q_rows) {
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
-  if ((int)blockIdx.x >= kv_ctas) {
-    rotate_rows<D, V, false>(t, nullptr, (blockIdx.x - kv_ctas) * q_rows, q_rows);
+  const int pairs = min(kv_ctas, (int)gridDim.x - kv_ctas);
+  const bool paired = (int)blockIdx.x < 2 * pairs;
+  const int cta = paired ? blockIdx.x / 2 : blockIdx.x - pairs;
+  if (paired ? blockIdx.x & 1 : pairs == kv_ctas) {
+    rotate_rows<D, V, false>(t, nullptr, cta * q_rows, q_rows);
     return;
   }
   __shared__ __align__(16) float cs[kBlock][2][D / 2];
   __shared__ long long s_pos[kBlock], s_page[kBlock];
   __shared__ int s_new[kBlock];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row0 = blockIdx.x * chunk;
+  const int row0 = cta * chunk;
   for (int r = warp; r < chunk; r += kWarps) {
     const int row = row0 + r;
     int b, first, end, n = 0;
@@ -423,18 +425,26 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int n = s_new[r];
     if (n <= 0) continue;
     const long long pos = s_pos[r];
-    constexpr int kPairs = D / 2;            // threads per row of the table
-    for (int j = threadIdx.x % kPairs; j < t.half; j += kPairs) {
-      const unsigned long long step = turn_step(__ldg(t.inv_freq + j));
-      for (int k = threadIdx.x / kPairs; k < n; k += kThreads / kPairs)
-        turn(pos + k, step, &cs[k][1][j], &cs[k][0][j]);
-    }
-    __syncthreads();
     const int in_page = (int)(pos % kPage);
-    for (int h = warp; h < 2 * t.Hkv; h += kWarps)
+    // Half the warps take K heads, after they made the table of angles; the
+    // others V heads, which need none.
+    constexpr int kKWarps = kWarps / 2, kKThreads = 32 * kKWarps;
+    int h = warp;
+    if (warp < kKWarps) {
+      for (int j = threadIdx.x; j < t.half; j += kKThreads) {
+        const unsigned long long step = turn_step(__ldg(t.inv_freq + j));
+        for (int k = 0; k < n; ++k) turn(pos + k, step, &cs[k][1][j], &cs[k][0][j]);
+      }
+      ptx::named_barrier(1, kKThreads);
+    } else {
+      h = t.Hkv + warp - kKWarps;
+    }
+    const int end = warp < kKWarps ? t.Hkv : 2 * t.Hkv;
+    for (; h < end; h += kKWarps)
       store_block<D>(t, pool, scales, cs, row0 + r, n, in_page % kBlock, s_page[r],
                      in_page / kBlock, h, lane);
-    __syncthreads();
+    // (the table is not made again before every K warp is done with it)
+    if (warp < kKWarps) ptx::named_barrier(1, kKThreads);
   }
 }
 
@@ -467,47 +477,45 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   const int per_row = heads * d / 16;
+  const int total = rows * per_row;
   constexpr int kUnroll = 4;
-  for (int r = threadIdx.x / 128; r < rows; r += kThreads / 128) {
-    if (!s_live[r]) continue;
-    const bool there = s_page[r] >= 0;
-    const int at = (int)(s_pos[r] % kPage);
-    const uint4* src = reinterpret_cast<const uint4*>(
-        pool + ((size_t)(there ? s_page[r] : 0) * kPage + at) * heads * d);
-    const float* sc = scales + (size_t)(there ? s_page[r] : 0) * heads * kBlocks + at / kBlock;
-    uint4* dst = reinterpret_cast<uint4*>(out + (size_t)(row0 + r) * heads * d);
-    for (int c0 = threadIdx.x % 128; c0 < per_row; c0 += kUnroll * 128) {
-      uint4 codes[kUnroll];
-      float s[kUnroll];
+  for (int i0 = threadIdx.x; i0 < total; i0 += kUnroll * kThreads) {
+    uint4 codes[kUnroll];
+    float s[kUnroll];
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int c = c0 + i * 128;
-        codes[i] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);   // NaN
-        s[i] = 1.f;
-        if (c < per_row && there) {
-          codes[i] = __ldg(src + c);
-          s[i] = __ldg(sc + c * 16 / d * kBlocks);
-        }
+    for (int i = 0; i < kUnroll; ++i) {
+      const int item = i0 + i * kThreads;
+      codes[i] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);   // NaN
+      s[i] = 1.f;
+      if (item >= total) continue;
+      const int r = item / per_row, c = item - r * per_row;
+      if (s_page[r] < 0) continue;
+      const int at = (int)(s_pos[r] % kPage);
+      codes[i] = __ldg(reinterpret_cast<const uint4*>(
+                           pool + ((size_t)s_page[r] * kPage + at) * heads * d) + c);
+      s[i] = __ldg(scales + ((size_t)s_page[r] * heads + c * 16 / d) * kBlocks + at / kBlock);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int item = i0 + i * kThreads;
+      if (item >= total) break;
+      const int r = item / per_row, c = item - r * per_row;
+      if (!s_live[r]) continue;
+      const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+      uint4 o[2];
+      uint32_t* ow = reinterpret_cast<uint32_t*>(o);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float y[4];
+        fp8::unpack4(w[j], y);
+        ow[2 * j] = ptx::pack_bf16x2(__float2bfloat16_rn(y[0] * s[i]),
+                                     __float2bfloat16_rn(y[1] * s[i]));
+        ow[2 * j + 1] = ptx::pack_bf16x2(__float2bfloat16_rn(y[2] * s[i]),
+                                         __float2bfloat16_rn(y[3] * s[i]));
       }
-#pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int c = c0 + i * 128;
-        if (c >= per_row) break;
-        const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-        uint4 o[2];
-        uint32_t* ow = reinterpret_cast<uint32_t*>(o);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float y[4];
-          fp8::unpack4(w[j], y);
-          ow[2 * j] = ptx::pack_bf16x2(__float2bfloat16_rn(y[0] * s[i]),
-                                       __float2bfloat16_rn(y[1] * s[i]));
-          ow[2 * j + 1] = ptx::pack_bf16x2(__float2bfloat16_rn(y[2] * s[i]),
-                                           __float2bfloat16_rn(y[3] * s[i]));
-        }
-        dst[2 * c] = o[0];
-        dst[2 * c + 1] = o[1];
-      }
+      uint4* dst = reinterpret_cast<uint4*>(out + (size_t)(row0 + r) * heads * d) + 2 * c;
+      dst[0] = o[0];
+      dst[1] = o[1];
     }
   }
 }
