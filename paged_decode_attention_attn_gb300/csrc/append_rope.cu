@@ -19,8 +19,7 @@
 // for codes that become subnormal) when a larger row makes the scale grow.
 // One warp takes one (block, head), once for the largest value and once for
 // the codes; the second reading of more than four rows comes from L1 (16 rows
-// in registers left two CTAs per SM, and the launch at 94 us where this takes
-// @@ for 2 prompts of ~4,000 tokens).
+// in registers left two CTAs per SM and half the rate of the launch).
 //
 // All of it is bound by HBM at prompt sizes and by the latency of its
 // dependent loads (request, position, page, row) at decode sizes.
@@ -45,8 +44,7 @@ constexpr int kBlock = PA_SCALE_TOKENS;
 constexpr int kBlocks = kPage / kBlock;   // scale blocks per page
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxRows = 8;               // token rows per CTA of the row-wise kernels
-constexpr int kRowCtas = 304;             // CTAs that a launch keeps when it takes more rows each
+constexpr int kRowCtas = 304;             // CTAs up to which rows are shared by several warps
 
 struct Tokens {
   const __nv_bfloat16* q;
@@ -113,10 +111,27 @@ __device__ __forceinline__ unsigned long long turn_step(float f) {
   return (bits >> 31) ? 0ull - x : x;
 }
 
-// Sine and cosine at position p.
+// Sine and cosine at position p: the turn's nearest quarter, and the Taylor
+// polynomials of the rest (|x| <= pi / 4: the first terms left out are below
+// 2e-9 and 3e-10).  Half the instructions of sincospif, which reduces a float.
 __device__ __forceinline__ void turn(long long p, unsigned long long step, float* s, float* c) {
-  const unsigned long long at = step * (unsigned long long)p;
-  sincospif((float)(int)(at >> 32) * 4.656612873077393e-10f, s, c);   // 2^-31
+  const uint32_t at = (uint32_t)((step * (unsigned long long)p) >> 32);
+  const uint32_t quarter = (at + 0x20000000u) >> 30;
+  const float x = (float)(int)(at - (quarter << 30)) * 1.4629180792671596e-09f;   // 2 pi 2^-32
+  const float z = x * x;
+  float a = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  a = fmaf(a, z, 1.0f / 120.0f);
+  a = fmaf(a, z, -1.0f / 6.0f);
+  const float sx = fmaf(a * z, x, x);
+  float b = fmaf(z, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  b = fmaf(b, z, -1.0f / 720.0f);
+  b = fmaf(b, z, 1.0f / 24.0f);
+  b = fmaf(b, z, -0.5f);
+  const float cx = fmaf(b, z, 1.0f);
+  const bool odd = quarter & 1;
+  const float ss = odd ? cx : sx, cc = odd ? sx : cx;
+  *s = quarter & 2 ? -ss : ss;
+  *c = (quarter + 1) & 2 ? -cc : cc;
 }
 
 template <int V>
@@ -142,12 +157,9 @@ __device__ __forceinline__ Lane lane_of(int l, int half, int interleaved) {
   return x;
 }
 
-// The lane's 2 V values in fp32, rotated by its pairs' c and s if turns: the
-// first V are a's.
+// The lane's 2 V values in fp32; the first V are a's.
 template <int V>
-__device__ __forceinline__ void rotate(const Vec<V>& a, const Vec<V>& b, bool turns,
-                                       int interleaved, const float* c, const float* s,
-                                       float (&y)[2 * V]) {
+__device__ __forceinline__ void unpack(const Vec<V>& a, const Vec<V>& b, float (&y)[2 * V]) {
   const uint32_t* wa = reinterpret_cast<const uint32_t*>(&a);
   const uint32_t* wb = reinterpret_cast<const uint32_t*>(&b);
 #pragma unroll
@@ -157,7 +169,12 @@ __device__ __forceinline__ void rotate(const Vec<V>& a, const Vec<V>& b, bool tu
     y[V + 2 * i] = ptx::bf16_lo_to_f32(wb[i]);
     y[V + 2 * i + 1] = ptx::bf16_hi_to_f32(wb[i]);
   }
-  if (!turns) return;
+}
+
+// They turned by their pairs' c and s.
+template <int V>
+__device__ __forceinline__ void rotate(int interleaved, const float* c, const float* s,
+                                       float (&y)[2 * V]) {
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -185,29 +202,32 @@ __device__ __forceinline__ Vec<V> pack(const float* y) {
   return r;
 }
 
-// Rotates the q heads of `rows` (1, 2, 4 or 8) token rows from row0 on into
-// q_out and, with kKv, stores their k (rotated) and v heads in the bf16 pool.
-// Warps do not wait for each other.
+// Rotates the q heads of the token rows of CTA cta into q_out and, with kKv,
+// stores their k (rotated) and v heads in the bf16 pool: `share` (1, 2, 4 or 8)
+// warps to a row.  Warps do not wait for each other; a warp issues its row's
+// first loads before it looks the row up.  (Fewer CTAs whose warps take several
+// rows each, the next one's loads ahead, measured slower: 44.6 against 40.4 us
+// for 11 prompts of up to 2,500 tokens.)
 template <int D, int V, bool kKv>
-__device__ __forceinline__ void rotate_rows(const Tokens& t, __nv_bfloat16* pool, int row0,
-                                            int rows) {
+__device__ __forceinline__ void rotate_rows(const Tokens& t, __nv_bfloat16* pool, int cta,
+                                            int share) {
   constexpr int kLanes = D / (2 * V);        // lanes per head row
   constexpr int kHeads = 32 / kLanes;        // head rows a warp takes at once
   constexpr int kUnroll = 4;
   __shared__ __align__(16) float table[kWarps][2][D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int share = kWarps / rows;           // warps per row
-  const int row = row0 + warp / share;
-  if (row >= t.n_tokens) return;
+  const int per_cta = kWarps / share;
   const Lane ln = lane_of<V>(lane % kLanes, t.half, t.interleaved);
-  const __nv_bfloat16* q = t.q + row * t.q_stride;
-  const __nv_bfloat16* k = t.k + row * t.k_stride;
-  const __nv_bfloat16* v = t.v + row * t.v_stride;
   const int heads = t.Hq + (kKv ? 2 * t.Hkv : 0);
   const int step = share * kHeads;
-  int h0 = (warp % share) * kHeads + lane / kLanes;
+  const int first_h = (warp % share) * kHeads + lane / kLanes;
   Vec<V> va[kUnroll], vb[kUnroll];
-  auto load = [&]() {
+  const int row = cta * per_cta + warp / share;
+  if (row >= t.n_tokens) return;
+  auto load = [&](int h0) {
+    const __nv_bfloat16* q = t.q + row * t.q_stride;
+    const __nv_bfloat16* k = t.k + row * t.k_stride;
+    const __nv_bfloat16* v = t.v + row * t.v_stride;
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const int h = h0 + i * step, g = h - t.Hq;
@@ -219,7 +239,7 @@ __device__ __forceinline__ void rotate_rows(const Tokens& t, __nv_bfloat16* pool
       vb[i] = *reinterpret_cast<const Vec<V>*>(src + ln.ob);
     }
   };
-  load();   // before the row's request, position and page are known
+  load(first_h);
   int b = 0, first, end;
   long long pos = 0;
   if (!locate(t.cu, t.positions, t.B, t.n_tokens, row, lane, &b, &pos, &first, &end)) return;
@@ -243,14 +263,15 @@ __device__ __forceinline__ void rotate_rows(const Tokens& t, __nv_bfloat16* pool
           *reinterpret_cast<const float4*>(&table[warp][1][ln.pair + i]);
     }
   }
-  while (true) {
+  for (int h0 = first_h;;) {
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const int h = h0 + i * step, g = h - t.Hq;
       if (h >= heads || (kKv && g >= 0 && kv_out == nullptr)) continue;
       if (ln.turns && (!kKv || g < t.Hkv)) {   // v and what passes keep their bits
         float y[2 * V];
-        rotate<V>(va[i], vb[i], true, t.interleaved, c, s, y);
+        unpack<V>(va[i], vb[i], y);
+        rotate<V>(t.interleaved, c, s, y);
         va[i] = pack<V>(y);
         vb[i] = pack<V>(y + V);
       }
@@ -259,17 +280,17 @@ __device__ __forceinline__ void rotate_rows(const Tokens& t, __nv_bfloat16* pool
       *reinterpret_cast<Vec<V>*>(dst + ln.ob) = vb[i];
     }
     h0 += kUnroll * step;
-    if (h0 - lane / kLanes >= heads) break;
-    load();
+    if (h0 >= heads) break;
+    load(h0);
   }
 }
 
 template <int D, int V>
 __global__ void __launch_bounds__(kThreads, 3)
-    append_rope_kernel(const Tokens t, __nv_bfloat16* pool, int rows) {
+    append_rope_kernel(const Tokens t, __nv_bfloat16* pool, int share) {
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
-  rotate_rows<D, V, true>(t, pool, blockIdx.x * rows, rows);
+  rotate_rows<D, V, true>(t, pool, blockIdx.x, share);
 }
 
 // Smallest power of two s >= 2^-60 with amax <= 448 s (448 = 1.75 * 2^8 is the
@@ -280,8 +301,8 @@ __device__ __forceinline__ float block_scale(unsigned amax_bits) {
 }
 
 // One (block, head) by one warp: rows [row, row + n_new) of the step go to the
-// block's rows [first, first + n_new).
-template <int D>
+// block's rows [first, first + n_new).  h counts K heads, then V heads.
+template <int D, bool kKey>
 __device__ __forceinline__ void store_block(const Tokens& t, uint8_t* pool, float* scales,
                                             const float (*cs)[2][D / 2], int row, int n_new,
                                             int first, long long page, int blk, int h, int lane) {
@@ -290,13 +311,11 @@ __device__ __forceinline__ void store_block(const Tokens& t, uint8_t* pool, floa
   constexpr int kRows = 32 / kLanes;         // token rows a warp takes at once
   constexpr int kUnroll = 4;
   const int sub = lane / kLanes;
-  const Lane ln = lane_of<V>(lane % kLanes, t.half, t.interleaved);
-  const bool is_k = h < t.Hkv;
-  const bool turns = ln.turns && is_k;
-  const long long stride = is_k ? t.k_stride : t.v_stride;
+  const Lane ln = lane_of<V>(lane % kLanes, kKey ? t.half : 0, t.interleaved);
+  const long long stride = kKey ? t.k_stride : t.v_stride;
   const __nv_bfloat16* src =
-      (is_k ? t.k + h * D : t.v + (h - t.Hkv) * D) + (long long)row * stride;
-  const size_t row_bytes = (size_t)2 * t.Hkv * D;
+      (kKey ? t.k + h * D : t.v + (h - t.Hkv) * D) + (row + sub) * stride;
+  const int row_bytes = 2 * t.Hkv * D;
   uint8_t* base = pool + ((size_t)page * kPage + blk * kBlock) * row_bytes + (size_t)h * D;
   float* scale = scales + ((size_t)page * 2 * t.Hkv + h) * kBlocks + blk;
   const float old = first > 0 ? *scale : 0.f;
@@ -304,54 +323,47 @@ __device__ __forceinline__ void store_block(const Tokens& t, uint8_t* pool, floa
   auto load = [&](int r0) {
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int r = r0 + i * kRows + sub;
-      if (r < n_new) {
+      const int r = r0 + i * kRows;
+      if (r + sub < n_new) {
         a[i] = *reinterpret_cast<const Vec<V>*>(src + r * stride + ln.oa);
         b[i] = *reinterpret_cast<const Vec<V>*>(src + r * stride + ln.ob);
+      } else {
+        a[i] = b[i] = Vec<V>{};
       }
     }
   };
-  // f(row, its rotated values) for the rows held
-  auto each = [&](int r0, auto f) {
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int r = r0 + i * kRows + sub;
-      if (r < n_new) {
-        float y[2 * V], c[V], s[V];
-        if (turns) {
-          *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(&cs[r][0][ln.pair]);
-          *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(&cs[r][1][ln.pair]);
-        }
-        rotate<V>(a[i], b[i], turns, t.interleaved, c, s, y);
-        f(r, y);
-      }
+  auto values = [&](int i, int r, float (&y)[2 * V]) {   // of row r0 + r, held at i
+    unpack<V>(a[i], b[i], y);
+    if (kKey && ln.turns) {
+      float c[V], s[V];
+      *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(&cs[r][0][ln.pair]);
+      *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(&cs[r][1][ln.pair]);
+      rotate<V>(t.interleaved, c, s, y);
     }
   };
-  unsigned amax = 0;   // as bits, which order magnitudes
-  for (int r0 = 0; r0 < n_new; r0 += kUnroll * kRows) {
-    load(r0);
-    each(r0, [&](int, const float (&y)[2 * V]) {
-#pragma unroll
-      for (int j = 0; j < 2 * V; ++j) amax = max(amax, __float_as_uint(y[j]) & 0x7fffffffu);
-    });
-  }
-  amax = __reduce_max_sync(0xffffffffu, amax);
-  const bool odd = amax >= 0x7f800000u;   // infinities or NaN, which set no scale
-  if (odd) {
-    amax = 0;
+  // Largest magnitude but for NaN (finite: and infinities).
+  auto largest = [&](bool finite) {
+    float m = 0.f;
     for (int r0 = 0; r0 < n_new; r0 += kUnroll * kRows) {
-      if (n_new > kUnroll * kRows) load(r0);
-      each(r0, [&](int, const float (&y)[2 * V]) {
+      if (!finite || n_new > kUnroll * kRows) load(r0);
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        float y[2 * V];
+        // (rows behind the last are zeros, whatever they turn by)
+        values(i, (r0 + i * kRows + sub) % kBlock, y);
 #pragma unroll
         for (int j = 0; j < 2 * V; ++j) {
-          const unsigned m = __float_as_uint(y[j]) & 0x7fffffffu;
-          amax = max(amax, m < 0x7f800000u ? m : 0u);
+          if (finite && fabsf(y[j]) > FLT_MAX) y[j] = 0.f;
+          m = fmaxf(m, fabsf(y[j]));
         }
-      });
+      }
     }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-  }
-  const float need = block_scale(amax);
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+  };
+  float amax = largest(false);
+  const bool infinite = amax > FLT_MAX;
+  if (infinite) amax = largest(true);
+  const float need = block_scale(__float_as_uint(amax));
   const float s = first > 0 ? fmaxf(old, need) : need;
   if (first > 0 && s != old) {
     // The scale grows: the block's older rows are requantised.
@@ -365,18 +377,27 @@ __device__ __forceinline__ void store_block(const Tokens& t, uint8_t* pool, floa
     }
   }
   const float inv = 1.0f / s;   // exact for a power of two
+  uint8_t* dst = base + (first + sub) * row_bytes;
   for (int r0 = 0; r0 < n_new; r0 += kUnroll * kRows) {
     if (n_new > kUnroll * kRows) load(r0);
-    each(r0, [&](int r, float (&y)[2 * V]) {
 #pragma unroll
-      for (int j = 0; j < 2 * V; ++j) {
-        if (odd && !(fabsf(y[j]) <= FLT_MAX)) y[j] = __int_as_float(0x7fc00000);
-        y[j] *= inv;
+    for (int i = 0; i < kUnroll; ++i) {
+      const int r = r0 + i * kRows;
+      if (r + sub >= n_new) break;
+      float y[2 * V];
+      values(i, r + sub, y);
+      if (infinite) {   // (a NaN stays one by itself)
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j)
+          if (fabsf(y[j]) > FLT_MAX) y[j] = __int_as_float(0x7fc00000);
       }
-      uint8_t* dst = base + (size_t)(first + r) * row_bytes;
-      *reinterpret_cast<uint32_t*>(dst + ln.oa) = fp8::pack4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<uint32_t*>(dst + ln.ob) = fp8::pack4(y[4], y[5], y[6], y[7]);
-    });
+#pragma unroll
+      for (int j = 0; j < 2 * V; ++j) y[j] *= inv;
+      *reinterpret_cast<uint32_t*>(dst + r * row_bytes + ln.oa) =
+          fp8::pack4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint32_t*>(dst + r * row_bytes + ln.ob) =
+          fp8::pack4(y[4], y[5], y[6], y[7]);
+    }
   }
   if (lane == 0 && (first == 0 || s != old)) *scale = s;
 }
@@ -388,14 +409,14 @@ __device__ __forceinline__ void store_block(const Tokens& t, uint8_t* pool, floa
 template <int D, int V>
 __global__ void __launch_bounds__(kThreads, 3)
     append_rope_q8_kernel(const Tokens t, uint8_t* pool, float* scales, int kv_ctas, int chunk,
-                          int q_rows) {
+                          int share) {
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
   const int pairs = min(kv_ctas, (int)gridDim.x - kv_ctas);
   const bool paired = (int)blockIdx.x < 2 * pairs;
   const int cta = paired ? blockIdx.x / 2 : blockIdx.x - pairs;
   if (paired ? blockIdx.x & 1 : pairs == kv_ctas) {
-    rotate_rows<D, V, false>(t, nullptr, cta * q_rows, q_rows);
+    rotate_rows<D, V, false>(t, nullptr, cta, share);
     return;
   }
   __shared__ __align__(16) float cs[kBlock][2][D / 2];
@@ -439,68 +460,62 @@ __global__ void __launch_bounds__(kThreads, 3)
     } else {
       h = t.Hkv + warp - kKWarps;
     }
-    const int end = warp < kKWarps ? t.Hkv : 2 * t.Hkv;
-    for (; h < end; h += kKWarps)
-      store_block<D>(t, pool, scales, cs, row0 + r, n, in_page % kBlock, s_page[r],
-                     in_page / kBlock, h, lane);
-    // (the table is not made again before every K warp is done with it)
-    if (warp < kKWarps) ptx::named_barrier(1, kKThreads);
+    if (warp < kKWarps) {
+      for (; h < t.Hkv; h += kKWarps)
+        store_block<D, true>(t, pool, scales, cs, row0 + r, n, in_page % kBlock, s_page[r],
+                             in_page / kBlock, h, lane);
+      // (the table is not made again before every K warp is done with it)
+      ptx::named_barrier(1, kKThreads);
+    } else {
+      for (; h < 2 * t.Hkv; h += kKWarps)
+        store_block<D, false>(t, pool, scales, cs, row0 + r, n, in_page % kBlock, s_page[r],
+                              in_page / kBlock, h, lane);
+    }
   }
 }
 
-// Rows of an 8-bit pool as bf16 values: a thread turns 16 codes of one head.
+// Rows of an 8-bit pool as bf16 values: `share` warps to a row, a lane turns 16
+// codes of one head at a time.
 __global__ void __launch_bounds__(kThreads)
     gather_q8_kernel(const uint8_t* pool, const float* scales, long long pool_pages,
                      const int32_t* page_table, int max_pages, const int32_t* cu,
-                     const int32_t* positions, int n_tokens, int B, int heads, int d, int rows,
+                     const int32_t* positions, int n_tokens, int B, int heads, int d, int share,
                      __nv_bfloat16* out, int32_t* status) {
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
-  __shared__ long long s_pos[kMaxRows], s_page[kMaxRows];
-  __shared__ int s_live[kMaxRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row0 = blockIdx.x * rows;
-  rows = min(rows, n_tokens - row0);
-  for (int r = warp; r < rows; r += kWarps) {
-    int b = 0, first, end;
-    long long pos = 0, page = -1;
-    const bool live = locate(cu, positions, B, n_tokens, row0 + r, lane, &b, &pos, &first, &end);
-    if (live) {
-      page = page_of(page_table, max_pages, pool_pages, b, pos);
-      if (page < 0 && lane == 0 && status) atomicOr(status, PA_STATUS_BAD_ROW);
-    }
-    if (lane == 0) {
-      s_pos[r] = pos;
-      s_page[r] = page;
-      s_live[r] = live;
-    }
-  }
-  __syncthreads();
-  const int per_row = heads * d / 16;
-  const int total = rows * per_row;
+  const int row = blockIdx.x * (kWarps / share) + warp / share;
+  if (row >= n_tokens) return;
+  int b = 0, first, end;
+  long long pos = 0;
+  if (!locate(cu, positions, B, n_tokens, row, lane, &b, &pos, &first, &end)) return;
+  const long long page = page_of(page_table, max_pages, pool_pages, b, pos);
+  if (page < 0 && lane == 0 && status) atomicOr(status, PA_STATUS_BAD_ROW);
+  const int at = (int)(pos % kPage);
+  const uint4* src = reinterpret_cast<const uint4*>(
+      pool + ((size_t)(page < 0 ? 0 : page) * kPage + (page < 0 ? 0 : at)) * heads * d);
+  const float* sc = scales + (size_t)(page < 0 ? 0 : page) * heads * kBlocks +
+                    (page < 0 ? 0 : at / kBlock);
+  uint4* dst = reinterpret_cast<uint4*>(out + (size_t)row * heads * d);
+  const int per_row = heads * d / 16, step = 32 * share;
   constexpr int kUnroll = 4;
-  for (int i0 = threadIdx.x; i0 < total; i0 += kUnroll * kThreads) {
+  for (int c0 = (warp % share) * 32 + lane; c0 < per_row; c0 += kUnroll * step) {
     uint4 codes[kUnroll];
     float s[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int item = i0 + i * kThreads;
+      const int c = c0 + i * step;
       codes[i] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);   // NaN
       s[i] = 1.f;
-      if (item >= total) continue;
-      const int r = item / per_row, c = item - r * per_row;
-      if (s_page[r] < 0) continue;
-      const int at = (int)(s_pos[r] % kPage);
-      codes[i] = __ldg(reinterpret_cast<const uint4*>(
-                           pool + ((size_t)s_page[r] * kPage + at) * heads * d) + c);
-      s[i] = __ldg(scales + ((size_t)s_page[r] * heads + c * 16 / d) * kBlocks + at / kBlock);
+      if (c < per_row && page >= 0) {
+        codes[i] = __ldg(src + c);
+        s[i] = __ldg(sc + c * 16 / d * kBlocks);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int item = i0 + i * kThreads;
-      if (item >= total) break;
-      const int r = item / per_row, c = item - r * per_row;
-      if (!s_live[r]) continue;
+      const int c = c0 + i * step;
+      if (c >= per_row) break;
       const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
       uint4 o[2];
       uint32_t* ow = reinterpret_cast<uint32_t*>(o);
@@ -513,9 +528,8 @@ __global__ void __launch_bounds__(kThreads)
         ow[2 * j + 1] = ptx::pack_bf16x2(__float2bfloat16_rn(y[2] * s[i]),
                                          __float2bfloat16_rn(y[3] * s[i]));
       }
-      uint4* dst = reinterpret_cast<uint4*>(out + (size_t)(row0 + r) * heads * d) + 2 * c;
-      dst[0] = o[0];
-      dst[1] = o[1];
+      dst[2 * c] = o[0];
+      dst[2 * c + 1] = o[1];
     }
   }
 }
@@ -525,12 +539,13 @@ __global__ void __launch_bounds__(kThreads)
 // ---------------------------------------------------------------------------
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Token rows per CTA of the row-wise kernels: one while the launch is small
-// (its warps then share the row's heads), more once there are CTAs enough.
-int rows_per_cta(int n_tokens) {
-  int rows = 1;
-  while (rows < kMaxRows && n_tokens / (2 * rows) >= kRowCtas) rows *= 2;
-  return rows;
+// Warps per row and CTAs of the row-wise kernels: a CTA per row while there are
+// few (its warps share the row's heads), up to a row per warp.
+void row_grid(int n_tokens, int* share, int* ctas) {
+  *share = kWarps;
+  while (*share > 1 && (long long)n_tokens * *share > (long long)kRowCtas * kWarps) *share /= 2;
+  const int per_cta = kWarps / *share;
+  *ctas = (n_tokens + per_cta - 1) / per_cta;
 }
 
 int check_tokens(const Tokens& t, int head_dim, int rot_dim, unsigned flags, const void* pool) {
@@ -594,22 +609,23 @@ Tokens tokens_of(const void* q, const void* k, const void* v, int64_t q_stride, 
 
 template <int D, int V>
 cudaError_t launch_append(const Tokens& t, void* pool, cudaStream_t stream) {
-  const int rows = rows_per_cta(t.n_tokens);
-  return launch_dependent(append_rope_kernel<D, V>, dim3((t.n_tokens + rows - 1) / rows),
-                          dim3(kThreads), 0, stream, t, static_cast<__nv_bfloat16*>(pool), rows);
+  int share, ctas;
+  row_grid(t.n_tokens, &share, &ctas);
+  return launch_dependent(append_rope_kernel<D, V>, dim3(ctas), dim3(kThreads), 0, stream, t,
+                          static_cast<__nv_bfloat16*>(pool), share);
 }
 
 template <int D, int V>
 cudaError_t launch_append_q8(const Tokens& t, void* pool, float* scales, cudaStream_t stream) {
-  const int rows = rows_per_cta(t.n_tokens);
   // A CTA of one row is either one block's or leaves at once, which is the
   // shortest path while all rows' CTAs fit the GPU together; behind that, 16
   // rows (one block's worth) a CTA.
   const int chunk = t.cu == nullptr || t.n_tokens <= 1024 ? 1 : kBlock;
   const int kv = (t.n_tokens + chunk - 1) / chunk;
-  const int q = t.q ? (t.n_tokens + rows - 1) / rows : 0;
+  int share = 1, q = 0;
+  if (t.q) row_grid(t.n_tokens, &share, &q);
   return launch_dependent(append_rope_q8_kernel<D, V>, dim3(kv + q), dim3(kThreads), 0, stream, t,
-                          static_cast<uint8_t*>(pool), scales, kv, chunk, rows);
+                          static_cast<uint8_t*>(pool), scales, kv, chunk, share);
 }
 
 // Pairs per lane: 8 (16-byte accesses) unless the rotated half is no multiple.
@@ -691,11 +707,12 @@ extern "C" int kv_gather_q8(const void* pool, const float* scales, int64_t pool_
   PA_REQUIRE(aligned16(pool) && aligned16(scales) && aligned16(out),
              "pool, scales and out must be 16-byte aligned");
   PA_REQUIRE(pool_pages >= 1 && max_pages >= 1, "pool_pages and max_pages must be >= 1");
-  const int rows = rows_per_cta(n_tokens);
+  int share, ctas;
+  row_grid(n_tokens, &share, &ctas);
   PA_CHECK_CUDA(pa::launch_dependent(
-      gather_q8_kernel, dim3((n_tokens + rows - 1) / rows), dim3(kThreads), 0, stream,
+      gather_q8_kernel, dim3(ctas), dim3(kThreads), 0, stream,
       static_cast<const uint8_t*>(pool), scales, (long long)pool_pages, page_table, max_pages,
-      cu_tokens, positions, n_tokens, B, 2 * n_kv_heads, head_dim, rows,
+      cu_tokens, positions, n_tokens, B, 2 * n_kv_heads, head_dim, share,
       static_cast<__nv_bfloat16*>(out), status));
   PA_CHECK_CUDA(cudaGetLastError());
   return PA_OK;
