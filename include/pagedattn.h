@@ -387,7 +387,7 @@ int kv_append_rope_q8(const void* q, const void* k, const void* v, int64_t q_str
  * token positions[b] + r - cu_tokens[b] of request b, rows and requests as in
  * kv_append_rope.
  *   out     device bf16 [n_tokens][2*n_kv_heads*head_dim] (a bf16 pool's row),
- *           16-byte aligned; rows at and behind cu_tokens[B] are left alone.
+ *           32-byte aligned; rows at and behind cu_tokens[B] are left alone.
  * A position or page id outside the table or the pool gives a row of NaN and
  * PA_STATUS_BAD_ROW.  Supported head_dim: 128, 256. */
 int kv_gather_q8(const void* pool, const float* scales, int64_t pool_pages,

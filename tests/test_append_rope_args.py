@@ -53,7 +53,8 @@ def test_head_dims_that_are_not_built(B):
     assert append(B, True, scales=FAKE + 4) == B.PA_ERR_INVALID
     g = [FAKE, FAKE, 4, FAKE, 4, FAKE, FAKE, 4, 2, 2, 128, FAKE, None, None]
     for at, bad, code in ((0, None, -1), (1, FAKE + 4, -1), (2, 0, -1), (5, None, -1), (7, -1, -1),
-                          (9, 0, -1), (10, 64, -6), (11, FAKE + 8, -1), (11, None, -1)):
+                          (9, 0, -1), (10, 64, -6), (11, FAKE + 8, -1), (11, FAKE + 16, -1),
+                          (11, None, -1)):
         args = list(g)
         args[at] = bad
         assert B.lib.kv_gather_q8(*args) == code, (at, bad)
