@@ -80,7 +80,7 @@ static_assert(kSmemAlloc <= 232448, "shared memory budget");
 
 template <int kMaxUnits>
 struct Params {
-  static constexpr bool kSecondOut = false;
+  static constexpr bool kSecondOut = false, kAllSlices = false;
   const __nv_bfloat16* q;
   const int32_t* page_table;
   float* out;
@@ -921,7 +921,7 @@ int run(bool tensor_cores, const void* q, const void* pool, int64_t pool_pages,
   sms = std::min(sms, kMaxGrid);
 
   Plan plan;
-  const int rc_plan = plan_units(
+  const int rc_plan = plan_units<false>(
       tiles, B, T, n_kv_heads, kSegmentCharge, merged_out != nullptr,
       [&](const Unit*, const int32_t*, size_t, long long total, std::vector<int32_t>* starts) {
         equal_starts(total, launch_grid(total, sms, n_kv_heads), starts);

@@ -73,7 +73,7 @@ constexpr int kTmaWarp = 12, kScoreWarp = 13, kProductWarp = 14;
 constexpr int kScaleCopies = 4;             // lanes that copy a step's scales
 constexpr int kThreads = 32 * 16;           // the last warp: per segment
 constexpr int kSegmentCharge = 6;           // pages charged per unit start
-constexpr int kWholePages = 12;             // units this short are not split while SMs are idle
+constexpr int kWholePages = 16;             // units this short are not split while SMs are idle
 constexpr int kMinPages = 4;                // pages per CTA at least, where units are split
 // A launch of this many pages per SM runs on kLongGridPct percent of the SMs:
 // with HBM saturated, fewer and longer streams finish sooner (as the bf16
@@ -156,7 +156,7 @@ struct Params {
   float* m_out;
   float* m_lse;
   // One tile per request: its output is the merged one too, written with it.
-  static constexpr bool kSecondOut = true;
+  static constexpr bool kSecondOut = true, kAllSlices = true;
   float* out2;
   float* lse2;
   int32_t starts[kMaxGrid + 1];      // CTA k takes flattened pages [k], [k + 1)
@@ -1146,7 +1146,7 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   if (sms <= 0) return fail(PA_ERR_CUDA, "cannot query the device's SM count");
   sms = std::min(sms, kMaxGrid);
   Plan plan;
-  int rc = plan_units(
+  int rc = plan_units<true>(
       tiles, B, T, Hkv, kSegmentCharge, T > 1 && merged_out != nullptr,
       [&](const Unit* units, const int32_t* pages, size_t n, long long total,
           std::vector<int32_t>* starts) { cut(units, pages, n, total, sms, Hkv, starts); },

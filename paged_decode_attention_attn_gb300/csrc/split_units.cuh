@@ -7,7 +7,7 @@
 // the fields these functions name (out, lse, status, arrivals, req_counters,
 // part_o, part_ml, T, Hq, Hkv, G, n_units, units, m_out,
 // m_lse, wait_limit_ns, slice_wait_ns, and out2, lse2 where kSecondOut says that
-// outputs are written twice); its shared-memory view Sh has fin_flag
+// outputs are written twice; kAllSlices, see split_slices); its shared-memory view Sh has fin_flag
 // and merge_info.  The kConsumers threads that call a function meet at named
 // barrier 1.
 #pragma once
@@ -48,6 +48,7 @@ constexpr uint64_t kSliceWaitNs = 50000ull;
 // a widely split unit's CTAs leave at once (their SMs then take the next
 // launch's first page loads).
 constexpr int kMaxSlices = 16;
+constexpr int kMaxSlicesAll = 24;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;         // 2 s per bounded device wait
 // Per unit: a 64-bit arrival word (count | leavers << 16 | generation << 32).
 constexpr size_t kCounterBytes = 8 * kMaxUnitsLarge;
@@ -78,7 +79,13 @@ struct Unit {
 // one box: 4 x 31,744 tokens (n ~ 9) 77.76 -> 77.05 us, 2 x 32,768 (n ~ 19)
 // 44.18 -> 43.37 us, 1 x 32,768 (n ~ 38) and 1 x 262,144 unchanged; a third
 // of them cost 1 x 32,768 0.3 us, two thirds gained half as much.
+// kAll (a kernel that merges with 128 threads): all the slices there can be (every
+// CTA but the last ends in the unit), so that a slice takes one round of loads,
+// about 1 us across the dies, where half of them took two (1 x 32,768 tokens
+// 17.2 -> @@ us).
+template <bool kAll>
 __host__ __device__ __forceinline__ int split_slices(int n) {
+  if (kAll) return n - 1 < kMaxSlicesAll ? n - 1 : kMaxSlicesAll;
   return n / 2 < kMaxSlices ? n / 2 : kMaxSlices;
 }
 
@@ -299,7 +306,7 @@ __device__ __forceinline__ void finish_split_unit(const P& p, const Sh& sh, cons
                                                   int b, int bt, int g, int first_cta, int ct,
                                                   int warp, int lane) {
   const int n = U.n_parts;
-  const int S = split_slices(n);
+  const int S = split_slices<P::kAllSlices>(n);
   const int rank = (int)blockIdx.x - first_cta;
   const bool participant = rank < S;
   unsigned long long* arrival = p.arrivals + u;
@@ -418,7 +425,7 @@ inline void equal_starts(long long total, int grid, std::vector<int32_t>* starts
 // total, starts) cuts a launch's n units, laid out over `total` flattened
 // pages, into CTAs; segment_charge is the number of pages that hold no data
 // charged per unit start; merge: the call merges every request's tiles.
-template <class Shape>
+template <bool kAllSlices, class Shape>
 int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int segment_charge, bool merge,
                Shape shape, Plan* plan) {
   const size_t n_tiles = (size_t)B * T, n_units = n_tiles * n_kv_heads;
@@ -490,7 +497,7 @@ int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int segment_c
     for (int b = 0; b < B; ++b) {
       Unit* u = units.data() + (g * (size_t)B + b) * T;
       int count = 0;
-      for (int t = 0; t < T; ++t) count += u[t].n_parts > 1 ? split_slices(u[t].n_parts) : 1;
+      for (int t = 0; t < T; ++t) count += u[t].n_parts > 1 ? split_slices<kAllSlices>(u[t].n_parts) : 1;
       for (int t = 0; t < T; ++t) u[t].pair_total = count;
     }
   }
