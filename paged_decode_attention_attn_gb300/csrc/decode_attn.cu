@@ -80,7 +80,8 @@ static_assert(kSmemAlloc <= 232448, "shared memory budget");
 
 template <int kMaxUnits>
 struct Params {
-  static constexpr bool kSecondOut = false, kAllSlices = false;
+  static constexpr bool kSecondOut = false, kAllSlices = false, kTilesTogether = false;
+  static constexpr bool kMerge = true;
   const __nv_bfloat16* q;
   const int32_t* page_table;
   float* out;

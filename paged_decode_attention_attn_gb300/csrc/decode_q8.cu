@@ -129,7 +129,7 @@ struct Smem {
   static_assert(kAlloc <= 232448, "shared memory budget");
 };
 
-template <int kMaxUnits>
+template <int kMaxUnits, bool kMergeTiles>
 struct Params {
   const __nv_bfloat16* q;
   const float* scales;
@@ -155,15 +155,17 @@ struct Params {
   unsigned long long slice_wait_ns;
   float* m_out;
   float* m_lse;
-  // One tile per request: its output is the merged one too, written with it.
-  static constexpr bool kSecondOut = true, kAllSlices = true;
+  static constexpr bool kAllSlices = true, kTilesTogether = true;
+  // Several tiles per request, to be merged; else a tile's output may be the
+  // merged one too, written with it.
+  static constexpr bool kMerge = kMergeTiles, kSecondOut = !kMergeTiles;
   float* out2;
   float* lse2;
   int32_t starts[kMaxGrid + 1];      // CTA k takes flattened pages [k], [k + 1)
   int16_t first_unit[kMaxGrid + 1];  // and its first unit
   Unit units[kMaxUnits];
 };
-static_assert(sizeof(Params<kMaxUnitsLarge>) <= 32764, "kernel parameters too large");
+static_assert(sizeof(Params<kMaxUnitsLarge, true>) <= 32764, "kernel parameters too large");
 
 struct View {
   uint8_t* base;
@@ -622,7 +624,7 @@ __device__ __forceinline__ void helper_warp(const P& p, const View& v, int lane)
       p.lse[row + lane] = -INFINITY;
       if (p.lse2) p.lse2[row + lane] = -INFINITY;
     }
-    if (p.m_out) {
+    if (P::kMerge) {
       // its part in the pair's merge, as finish_unit does it
       int* counter = p.req_counters + b * p.Hkv + g;
       __syncwarp();
@@ -927,7 +929,7 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
     if (lane == 0) ptx::mbar_arrive(v.bar(S::kFEmpty + (seg & 1)));
     if (s.whole()) {
       // without a merge pass nothing follows: the next segment may start
-      if (p.m_out) finish_unit<D, kOut>(p, v, s.b, s.g, ct, warp, lane, 1, s.U.pair_total);
+      if (P::kMerge) finish_unit<D, kOut>(p, v, s.b, s.g, ct, warp, lane, 1, s.U.pair_total);
     } else {
       finish_split_unit<D, kOut>(p, v, s.U, s.u, s.b, s.bt, s.g, s.U.first_cta, ct, warp, lane);
       ptx::named_barrier(1, kOut);   // merge_info is read before it is written again
@@ -936,10 +938,10 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
   });
 }
 
-template <int D, int kMaxUnits>
+template <int D, int kMaxUnits, bool kMerge>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmap,
-                     const __grid_constant__ Params<kMaxUnits> p) {
+                     const __grid_constant__ Params<kMaxUnits, kMerge> p) {
   using S = Smem<D>;
   extern __shared__ uint8_t smem_raw[];
   View v;
@@ -1062,12 +1064,15 @@ void cut(const Unit* units, const int32_t* pages, size_t n, long long total, int
   if (total > at) starts->push_back(static_cast<int32_t>(total));
 }
 
-template <int D, int N>
-int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L,
-                 const Params<kMaxUnitsSmall>& common, cudaStream_t stream) {
-  static_assert(N >= kMaxUnitsSmall, "");
-  Params<N> prm;
-  std::memcpy(static_cast<void*>(&prm), &common, offsetof(Params<kMaxUnitsSmall>, units));
+using Common = Params<kMaxUnitsSmall, false>;
+
+template <int D, int N, bool kMerge>
+int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L, const Common& common,
+                 cudaStream_t stream) {
+  using Prm = Params<N, kMerge>;
+  static_assert(N >= kMaxUnitsSmall && offsetof(Prm, starts) == offsetof(Common, starts), "");
+  Prm prm;
+  std::memcpy(static_cast<void*>(&prm), &common, offsetof(Common, starts));
   prm.n_units = static_cast<int>(L.n);
   prm.grid = L.grid;
   std::memcpy(prm.units, plan.units.data() + L.u0, L.n * sizeof(Unit));
@@ -1079,16 +1084,27 @@ int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L,
   }
   static PerContext smem_limit;   // the attribute lives in the context
   cudaError_t e = smem_limit.apply([] {
-    return cudaFuncSetAttribute(decode_q8_kernel<D, N>,
+    return cudaFuncSetAttribute(decode_q8_kernel<D, N, kMerge>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kAlloc);
   });
   if (e == cudaSuccess)
-    e = launch_dependent(decode_q8_kernel<D, N>, dim3(L.grid), dim3(kThreads), Smem<D>::kAlloc,
+    e = launch_dependent(decode_q8_kernel<D, N, kMerge>, dim3(L.grid), dim3(kThreads), Smem<D>::kAlloc,
                          stream, tmap, prm);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess)
     return fail(PA_ERR_CUDA, "8-bit paged decode launch failed: %s", cudaGetErrorString(e));
   return PA_OK;
+}
+
+template <bool kMerge>
+int launch(int D, const CUtensorMap& tmap, const Plan& plan, const Launch& L, const Common& common,
+           cudaStream_t stream) {
+  const bool small = L.n <= (size_t)kMaxUnitsSmall;
+  if (D == 128)
+    return small ? launch_units<128, kMaxUnitsSmall, kMerge>(tmap, plan, L, common, stream)
+                 : launch_units<128, kMaxUnitsLarge, kMerge>(tmap, plan, L, common, stream);
+  return small ? launch_units<256, kMaxUnitsSmall, kMerge>(tmap, plan, L, common, stream)
+               : launch_units<256, kMaxUnitsLarge, kMerge>(tmap, plan, L, common, stream);
 }
 
 int run(const void* q, const void* pool, const float* scales, int64_t pool_pages,
@@ -1153,7 +1169,7 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
       &plan);
   if (rc != PA_OK) return rc;
 
-  Params<kMaxUnitsSmall> common{};
+  Common common{};
   common.q = static_cast<const __nv_bfloat16*>(q);
   common.scales = scales;
   common.page_table = page_table;
@@ -1179,13 +1195,8 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   common.stall_iteration = hooks.stall_iteration;
   common.slice_wait_ns = hooks.slice_wait_ns;
   for (const Launch& L : plan.launches) {
-    const bool small = L.n <= (size_t)kMaxUnitsSmall;
-    if (D == 128)
-      rc = small ? launch_units<128, kMaxUnitsSmall>(tmap, plan, L, common, stream)
-                 : launch_units<128, kMaxUnitsLarge>(tmap, plan, L, common, stream);
-    else
-      rc = small ? launch_units<256, kMaxUnitsSmall>(tmap, plan, L, common, stream)
-                 : launch_units<256, kMaxUnitsLarge>(tmap, plan, L, common, stream);
+    rc = common.m_out ? launch<true>(D, tmap, plan, L, common, stream)
+                      : launch<false>(D, tmap, plan, L, common, stream);
     if (rc != PA_OK) return rc;
   }
   return PA_OK;
