@@ -300,8 +300,8 @@ __global__ void __launch_bounds__(Shape<kTensorCores>::kThreads, 1)
       const int lo = max(cta_start, pf) - pf;
       const int hi = min(cta_end, pf + np) - pf;
       if (hi <= lo) continue;   // only the unit's segment charge falls in this range
-      const int bt = U.bt_g / Hkv;
-      const int g = U.bt_g - bt * Hkv;
+      const int bt = U.bt;
+      const int g = U.g;
       const int b = bt / p.T;
       const int32_t* prow = p.page_table + (size_t)b * p.max_pages + U.tok_start / kPage;
       const int xk = g * kD;
@@ -377,8 +377,8 @@ __global__ void __launch_bounds__(Shape<kTensorCores>::kThreads, 1)
   for (int u = blockIdx.x; u < p.n_units; u += p.grid) {
     const Unit U = p.units[u];
     if (unit_pages(U.tok_start, U.tok_end) != 0) continue;
-    const int bt = U.bt_g / Hkv;
-    const int g = U.bt_g - bt * Hkv;
+    const int bt = U.bt;
+    const int g = U.g;
     for (int idx = ct; idx < G * kD; idx += kConsumers) {
       const int row = idx / kD;
       const int d = idx - row * kD;
@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(Shape<kTensorCores>::kThreads, 1)
     const int lo = max(cta_start, pf) - pf;
     const int hi = min(cta_end, pf + np) - pf;
     if (hi <= lo) continue;
-    const int bt = U.bt_g / Hkv;
-    const int g = U.bt_g - bt * Hkv;
+    const int bt = U.bt;
+    const int g = U.g;
     const int b = bt / p.T;
     const int first_page_tok = (U.tok_start / kPage) * kPage;
     int poisoned = 0;

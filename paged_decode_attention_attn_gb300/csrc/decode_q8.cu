@@ -236,29 +236,40 @@ struct Segment {
   }
 };
 
+// This CTA's segments, one after the other.
+template <class P>
+struct Segments {
+  const P& p;
+  int start, end, u;
+  __device__ __forceinline__ explicit Segments(const P& params)
+      : p(params), start(params.starts[blockIdx.x]), end(params.starts[blockIdx.x + 1]),
+        u(params.first_unit[blockIdx.x]) {}
+  __device__ __forceinline__ bool next(Segment& s) {
+    for (; u < p.n_units && p.units[u].page_first < end; ++u) {
+      s.U = p.units[u];
+      const int np = unit_pages(s.U.tok_start, s.U.tok_end);
+      s.pf = s.U.page_first;
+      s.lo = max(start, s.pf) - s.pf;
+      s.hi = min(end, s.pf + np) - s.pf;
+      if (s.hi <= s.lo) continue;   // empty, or only its segment charge falls in this range
+      s.u = u++;
+      s.bt = s.U.bt;
+      s.g = s.U.g;
+      s.b = p.T == 1 ? s.bt : s.bt / p.T;
+      s.first_tok = s.U.tok_start / kPage * kPage;
+      return true;
+    }
+    return false;
+  }
+};
+
 // Calls f(segment, index) for every segment of this CTA until f returns false.
 template <class P, class F>
 __device__ __forceinline__ void for_segments(const P& p, F f) {
-  const int start = p.starts[blockIdx.x];
-  const int end = p.starts[blockIdx.x + 1];
-  int index = 0;
-  for (int u = p.first_unit[blockIdx.x]; u < p.n_units && p.units[u].page_first < end; ++u) {
-    Segment s;
-    s.U = p.units[u];
-    const int np = unit_pages(s.U.tok_start, s.U.tok_end);
-    if (np == 0) continue;
-    s.u = u;
-    s.pf = s.U.page_first;
-    s.lo = max(start, s.pf) - s.pf;
-    s.hi = min(end, s.pf + np) - s.pf;
-    if (s.hi <= s.lo) continue;   // only the unit's segment charge falls in this range
-    s.bt = s.U.bt_g / p.Hkv;
-    s.g = s.U.bt_g - s.bt * p.Hkv;
-    s.b = s.bt / p.T;
-    s.first_tok = s.U.tok_start / kPage * kPage;
+  Segments<P> segments(p);
+  Segment s;
+  for (int index = 0; segments.next(s); ++index)
     if (!f(s, index)) return;
-    ++index;
-  }
 }
 
 __device__ __forceinline__ bool any_in_group(int id, int threads, bool x) {
@@ -612,8 +623,7 @@ __device__ __forceinline__ void helper_warp(const P& p, const View& v, int lane)
   for (int u = blockIdx.x; u < p.n_units; u += p.grid) {
     const Unit& U = p.units[u];
     if (unit_pages(U.tok_start, U.tok_end) != 0) continue;
-    const int bt = U.bt_g / p.Hkv;
-    const int g = U.bt_g - bt * p.Hkv;
+    const int bt = U.bt, g = U.g;
     const int b = bt / p.T;
     const size_t row = (size_t)bt * p.Hq + g * p.G;
     for (int i = lane; i < p.G * D; i += 32) {
@@ -866,7 +876,10 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
       float by[kMaxG] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
       bool same = true;
 #pragma unroll
-      for (int h = 0; h < kMaxG; ++h) same = same && by[h] == ref[h];
+      for (int h = 0; h < kMaxG; ++h) {
+        if (i == 0) ref[h] = by[h];   // the segment's first
+        same = same && by[h] == ref[h];
+      }
       if (same) {
 #pragma unroll
         for (int h = 0; h < kMaxG; ++h) by[h] = 1.0f / kFirstPart;
