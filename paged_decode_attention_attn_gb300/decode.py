@@ -1,4 +1,5 @@
-"""One decode step of paged GQA attention over every layer, on three routes.
+"""One decode step of paged GQA attention over every layer, on three routes (and
+over an 8-bit pool: ResidentQ8Decode).
 
 Resident route: the whole history sits in a device pool; per layer one
 launch writes the new token's row into its page, returns per-tile (out, LSE)
@@ -151,6 +152,82 @@ class ResidentDecode:
                        t["positions"], t["new_rows"][i], self.tiles, geo.scale, o.tile_out[i],
                        o.tile_lse[i], self.workspace, self.status, o.part_offsets, o.out[i],
                        o.lse[i], self.stream, kv_ready=self.kv_ready)
+
+    def step(self):
+        for i in range(self.n_layers):
+            self.layer(i)
+
+    def kernel_status(self) -> int:
+        return int(self.workspace[:4].view(torch.int32).item()) | int(self.status.item())
+
+
+class ResidentQ8Decode:
+    """Decode step over a device-resident 8-bit pool [layers][pages][64][row]
+    (e4m3 codes, one fp32 scale per 16 tokens and head): half the bytes of
+    ResidentDecode's.
+
+    The pool is filled from ``t["pool"]``'s history (every row but each
+    request's newest, as they stand: keys of a cache are rotated already).  Per
+    layer, one launch turns the step's q and k by their positions and stores k
+    and v in the pages; one attends every tile and merges them.  ``inv_freq``
+    fp32 [rot_dim / 2], None: no rotation; ``interleaved``: pairs (2i, 2i + 1).
+    """
+
+    def __init__(self, w: DecodeWorkload, t: dict, inv_freq=None, interleaved: bool = False,
+                 stream=None):
+        geo = w.geometry
+        self.w, self.t, self.stream = w, t, stream
+        self.inv_freq, self.interleaved = inv_freq, interleaved
+        self.tiles = np.ascontiguousarray(w.tiles, dtype=np.int32)
+        self.n_layers = t["pool"].shape[0]
+        dev = t["pool"].device
+        shape = tuple(t["pool"].shape)
+        self.pool = torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+        self.scales = torch.zeros(
+            (self.n_layers, shape[1], 2 * geo.n_kv_heads, geo.page_tokens // B.SCALE_TOKENS),
+            dtype=torch.float32, device=dev)
+        self.o = _Outputs(w, self.n_layers, dev)
+        self.merged = torch.empty((self.n_layers, w.batch, geo.n_q_heads, geo.head_dim),
+                                  dtype=torch.float32, device=dev)
+        self.merged_lse = torch.empty((self.n_layers, w.batch, geo.n_q_heads),
+                                      dtype=torch.float32, device=dev)
+        self.q = torch.empty_like(t["q"])
+        self.workspace = B.alloc_workspace_q8(w.batch, self.tiles.shape[1], geo.n_q_heads,
+                                              geo.n_kv_heads, geo.head_dim, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._fill()
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream(dev))
+
+    def _kv(self, rows):
+        """K and V heads of pool rows [n][row_elems], as views."""
+        geo = self.w.geometry
+        heads = rows.view(rows.shape[0], 2 * geo.n_kv_heads, geo.head_dim)
+        return heads[:, :geo.n_kv_heads], heads[:, geo.n_kv_heads:]
+
+    def _fill(self):
+        zero = torch.zeros(1, dtype=torch.int32, device=self.pool.device)
+        for i in range(self.n_layers):
+            for r in range(self.w.batch):
+                n = int(self.w.lengths[r]) - 1
+                if n <= 0:
+                    continue
+                k, v = self._kv(history_rows(self.w, self.t["pool"][i], r)[:n])
+                cu = torch.tensor([0, n], dtype=torch.int32, device=self.pool.device)
+                B.kv_append_rope_q8(None, k, v, self.pool[i], self.scales[i],
+                                    self.t["page_table"][r:r + 1], zero, None, cu_tokens=cu,
+                                    status=self.status)
+
+    def layer(self, i: int):
+        t, o = self.t, self.o
+        k, v = self._kv(t["new_rows"][i])
+        B.kv_append_rope_q8(t["q"][i], k, v, self.pool[i], self.scales[i], t["page_table"],
+                            t["positions"], self.inv_freq, self.q[i],
+                            interleaved=self.interleaved, status=self.status, stream=self.stream)
+        B.paged_decode_attn_q8_lse(self.q[i], self.pool[i], self.scales[i], t["page_table"],
+                                   self.tiles, self.w.geometry.scale, o.tile_out[i],
+                                   o.tile_lse[i], self.workspace, merged_out=self.merged[i],
+                                   merged_lse=self.merged_lse[i], stream=self.stream)
 
     def step(self):
         for i in range(self.n_layers):

@@ -31,6 +31,31 @@ def B():
     return binding
 
 
+def check_request(K, V, q, tiles, scale, out, lse, merged, merged_lse, what):
+    """One request's tiles and merge against the oracle over K, V float64
+    [tokens][Hkv][D]."""
+    q = q.double().cpu().numpy()
+    outs, lses = oracle.tile_attention(q, K, V, tiles, scale)
+    want = list(zip(outs, lses)) + [oracle.lse_merge(outs, lses)]
+    got = [(out[t], lse[t]) for t in range(len(tiles))] + [(merged, merged_lse)]
+    G = q.shape[0] // K.shape[1]
+    for i, ((o, l), (wo, wl)) in enumerate(zip(got, want)):
+        o, l = o.double().cpu().numpy(), l.double().cpu().numpy()
+        if np.all(wl == -np.inf):
+            assert np.all(o == 0) and np.all(l == -np.inf), (what, i)
+            continue
+        for h in range(q.shape[0]):
+            if not np.isfinite(wl[h]):
+                assert np.isnan(o[h]).all() and np.isnan(l[h]), (what, i, h)
+                continue
+            A = scale * np.max(np.abs(K[:, h // G]) @ np.abs(q[h]))
+            e = 2.0 ** -21 * A + 2.0 ** -18
+            vmax = np.max(np.abs(V[:, h // G]))
+            err = np.max(np.abs(o[h] - wo[h]))
+            assert err <= (e + 2.0 ** -16) * vmax, (what, i, h, err, vmax, A)
+            assert abs(l[h] - wl[h]) <= e + 2.0 ** -22 * abs(wl[h]), (what, i, h)
+
+
 class Case:
     def __init__(self, lengths, tiles=None, hq=24, hkv=4, d=256, seed=0, spare=3, scale=None,
                  q_scale=1.0, v_exp=(-8, -5), k_exp=(-8, -5), max_pages=None):
@@ -94,29 +119,8 @@ class Case:
 
     def check(self, requests=None):
         for b in range(len(self.lengths)) if requests is None else requests:
-            K, V = self.history(b)
-            q = self.q[b].double().cpu().numpy()
-            outs, lses = oracle.tile_attention(q, K, V, self.tiles[b], self.scale)
-            want = list(zip(outs, lses)) + [oracle.lse_merge(outs, lses)]
-            got = [(self.out[b, t], self.lse[b, t]) for t in range(self.tiles.shape[1])]
-            got.append((self.merged[b], self.merged_lse[b]))
-            G = self.hq // self.hkv
-            for i, ((o, l), (wo, wl)) in enumerate(zip(got, want)):
-                o, l = o.double().cpu().numpy(), l.double().cpu().numpy()
-                what = f"request {b} tile {i}"
-                if np.all(wl == -np.inf):
-                    assert np.all(o == 0) and np.all(l == -np.inf), what
-                    continue
-                for h in range(self.hq):
-                    if not np.isfinite(wl[h]):
-                        assert np.isnan(o[h]).all() and np.isnan(l[h]), what
-                        continue
-                    A = self.scale * np.max(np.abs(K[:, h // G]) @ np.abs(q[h]))
-                    e = 2.0 ** -21 * A + 2.0 ** -18
-                    vmax = np.max(np.abs(V[:, h // G]))
-                    err = np.max(np.abs(o[h] - wo[h]))
-                    assert err <= (e + 2.0 ** -16) * vmax, (what, h, err, vmax, A)
-                    assert abs(l[h] - wl[h]) <= e + 2.0 ** -22 * abs(wl[h]), (what, h)
+            check_request(*self.history(b), self.q[b], self.tiles[b], self.scale, self.out[b],
+                          self.lse[b], self.merged[b], self.merged_lse[b], f"request {b}")
 
 
 LENGTHS = [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 191, 192, 193, 1000]
@@ -327,3 +331,114 @@ def test_a_wait_that_runs_out_is_reported_and_the_context_survives(B, iteration)
     c.out.zero_()
     assert c.run(B) == 0
     assert torch.equal(c.out, want)
+
+
+@pytest.mark.parametrize("rotated", [False, True])
+def test_the_decode_step_over_an_8_bit_pool(B, rotated):
+    """ResidentQ8Decode: the pool holds the bf16 history's nearest codes, the
+    step's rotated rows join it, and every layer's outputs match the oracle's
+    over what the pool holds; a captured step replays to the same bits."""
+    from paged_decode_attention_attn_gb300 import decode, workloads as wl
+    w = wl.custom([1500, 1, 65, 640], [[(0, 1000), (1000, 1500)], [(0, 1)], [(0, 65), (64, 65)],
+                                       [(0, 640)]], seed=31, n_layers=2)
+    t = wl.materialize(w, DEV)
+    geo = w.geometry
+    inv = torch.from_numpy((10000.0 ** (-np.arange(32) / 32)).astype(np.float32)).to(DEV)
+    dec = decode.ResidentQ8Decode(w, t, inv_freq=inv if rotated else None)
+    dec.step()
+    torch.cuda.synchronize()
+    assert dec.kernel_status() == 0
+    heads = 2 * geo.n_kv_heads
+    for i in range(w.n_layers):
+        for r in range(w.batch):
+            n = int(w.lengths[r])
+            pages = torch.from_numpy(w.page_table[r, :w.pages_of(r)].astype(np.int64)).to(DEV)
+            codes = dec.pool[i].view(torch.uint8)[pages].cpu().numpy().reshape(-1, heads, 256)
+            scales = dec.scales[i][pages].double().cpu().numpy().transpose(0, 2, 1)
+            scales = scales.reshape(-1, heads)
+            kv = R.pool_values(codes, scales)[:n]
+            want = wl.history_rows(w, t["pool"][i], r).double().cpu().numpy().reshape(n, heads, 256)
+            step = np.repeat(scales, 16, 0)[:n, :, None] * 2.0 ** -10
+            near = np.abs(kv - want) <= np.maximum(np.abs(want) / 16, step)
+            assert near[:n - 1].all()
+            new = t["new_rows"][i, r].double().cpu().numpy().reshape(heads, 256)
+            if rotated:
+                new[:4] = R.rotate(new[None, :4], [n - 1], inv.cpu().numpy())[0]
+            slack = 1e-6 * np.max(np.abs(new))
+            assert np.all(np.abs(kv[-1] - new) <= slack + np.maximum(np.abs(new) / 16, step[-1]))
+            check_request(kv[:, :4], kv[:, 4:], dec.q[i, r], w.tiles[r], geo.scale,
+                          dec.o.tile_out[i, r], dec.o.tile_lse[i, r], dec.merged[i, r],
+                          dec.merged_lse[i, r], f"layer {i} request {r}")
+    want = dec.merged.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dec.step()
+    for _ in range(2):
+        dec.merged.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert dec.kernel_status() == 0 and torch.equal(dec.merged, want)
+
+
+def test_two_graphs_with_workspaces_of_their_own_overlap(B):
+    """Two captured calls on two streams, each with its workspace, replayed
+    together: each gives what it gives alone."""
+    cases = [Case([9000, 30, 700], hq=24, hkv=4, d=256, seed=41),
+             Case([5000, 2500], hq=32, hkv=8, d=128, seed=42)]
+    graphs, wants, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for c in cases:
+        assert c.run(B) == 0
+        wants.append(c.out.clone())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(20):
+                B.paged_decode_attn_q8_lse(c.q, c.pool, c.scales, c.table_dev, c.tiles, c.scale,
+                                           c.out, c.lse, c.ws, merged_out=c.merged,
+                                           merged_lse=c.merged_lse)
+        graphs.append(g)
+        c.out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for c, want in zip(cases, wants):
+        assert int(c.ws[:4].view(torch.int32).item()) == 0
+        assert torch.equal(c.out, want)
+
+
+def test_sixty_four_tiles_per_request(B):
+    """Many tiles per request, empty and one-token ones among them, merged."""
+    rng = np.random.default_rng(64)
+    lengths, tiles = [9000, 1, 4097], []
+    for n in lengths:
+        cuts = np.sort(rng.integers(0, n + 1, 63))
+        cuts = [0] + [int(c) for c in cuts] + [n]
+        tiles.append(list(zip(cuts[:-1], cuts[1:])))
+    c = Case(lengths, tiles, hq=16, hkv=2, d=128, seed=43)
+    assert c.run(B) == 0
+    c.check()
+    whole = Case(lengths, hq=16, hkv=2, d=128, seed=43)
+    assert whole.run(B) == 0
+    assert float((c.merged - whole.merged).abs().max()) <= 1e-5 * float(whole.merged.abs().max())
+
+
+def test_requests_without_tokens(B):
+    c = Case([0, 5, 0], [[(0, 0), (0, 0)], [(0, 3), (3, 5)], [(0, 0), (0, 0)]], hq=8, hkv=2, d=128,
+             seed=44)
+    assert c.run(B) == 0
+    c.check()
+    c = Case([0, 0], hq=8, hkv=1, d=256, seed=45)
+    assert c.run(B) == 0
+    assert torch.all(c.merged == 0) and torch.all(c.merged_lse == -float("inf"))
+
+
+def test_q_that_is_not_finite_gives_nan_in_its_head_alone(B):
+    c = Case([200], hq=8, hkv=2, d=128, seed=46)
+    c.q[0, 1, 3], c.q[0, 6, 0] = float("inf"), float("nan")
+    assert c.run(B) == 0
+    bad = torch.zeros(8, dtype=torch.bool, device=DEV)
+    bad[1] = bad[6] = True
+    assert c.out[0, 0][bad].isnan().all() and c.lse[0, 0][bad].isnan().all()
+    assert c.out[0, 0][~bad].isfinite().all() and c.lse[0, 0][~bad].isfinite().all()
