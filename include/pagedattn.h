@@ -1,6 +1,7 @@
 /*
  * pagedattn.h -- C ABI of libpagedattn: paged GQA decode attention with a
- * per-tile log-sum-exp, an FP32 LSE merge, a staging arena that moves KV
+ * per-tile log-sum-exp over bf16 and 8-bit pools, appends with the position
+ * rotation, an FP32 LSE merge, a staging arena that moves KV
  * history from pinned host memory into bounded device slots (stage calls or
  * leases), an admission planner for a device pool, and a background converter
  * of fully written pages into a compact representation.
@@ -251,9 +252,10 @@ int paged_decode_attn_lse_append(const void* q, void* pool, int64_t pool_pages,
 
 /* Test hook for failure detection (no counterpart in the source pages): the
  * next decode call made on this thread (any paged_decode_attn_lse* entry
- * point) gives every bounded device wait up after wait_limit_ns (instead of
- * 2 s), and CTA 0 leaves its page load number `iteration` unarmed, so the
- * wait for that page runs out: the kernel sets PA_STATUS_TIMEOUT, lets the
+ * point, or paged_decode_attn_q8_lse) gives every bounded device wait up after
+ * wait_limit_ns (instead of 2 s), and CTA 0 leaves its page load (8-bit pool:
+ * its load of two pages' keys) number `iteration` unarmed, so the wait for
+ * that load runs out: the kernel sets PA_STATUS_TIMEOUT, lets the
  * loads it issued land and returns; the context stays usable.  Outputs of
  * that call are invalid and its workspace must be zero-filled again before
  * reuse.  (-1, 0) clears a pending setting.  PA_ERR_INVALID otherwise unless
@@ -324,7 +326,8 @@ int kv_append_rows(void* pool, int64_t pool_pages, const int32_t* page_table,
  * v in the pages and q in q_out: one launch.
  *
  * Token row r of the step belongs to the request b with cu_tokens[b] <= r <
- * cu_tokens[b+1] and has position p = positions[b] + r - cu_tokens[b].  For
+ * cu_tokens[b+1] and has position p = positions[b] + r - cu_tokens[b]; a call
+ * takes up to 2^30 rows.  For
  * i < rot_dim / 2 the pair (x1, x2) of every q and k head becomes
  *     (x1 cos a - x2 sin a, x2 cos a + x1 sin a),   a = p * inv_freq[i],
  * evaluated in FP32 with a reduced modulo 2 pi in 64-bit integers (any

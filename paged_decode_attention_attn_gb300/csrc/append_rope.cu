@@ -44,6 +44,7 @@ constexpr int kBlock = PA_SCALE_TOKENS;
 constexpr int kBlocks = kPage / kBlock;   // scale blocks per page
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxTokens = 1 << 30;       // rows of a call: CTA and row numbers stay in 32 bits
 constexpr int kRowCtas = 304;             // CTAs up to which rows are shared by several warps
 
 struct Tokens {
@@ -558,6 +559,7 @@ int check_tokens(const Tokens& t, int head_dim, int rot_dim, unsigned flags, con
   PA_REQUIRE(t.n_tokens >= 0 && t.B >= 0, "n_tokens and B must be >= 0 (got %d, %d)", t.n_tokens,
              t.B);
   if (t.n_tokens == 0 || t.B == 0) return PA_OK;
+  PA_REQUIRE(t.n_tokens <= kMaxTokens, "n_tokens (%d) above %d", t.n_tokens, kMaxTokens);
   PA_REQUIRE(t.Hkv >= 1 && t.Hkv <= 4096, "n_kv_heads (%d) must be in 1..4096", t.Hkv);
   PA_REQUIRE((t.q == nullptr) == (t.q_out == nullptr), "q and q_out go together");
   PA_REQUIRE(t.q == nullptr || (t.Hq >= 1 && t.Hq <= 65536), "n_q_heads (%d) must be in 1..65536",
@@ -624,9 +626,10 @@ cudaError_t launch_append(const Tokens& t, void* pool, cudaStream_t stream) {
 template <int D, int V>
 cudaError_t launch_append_q8(const Tokens& t, void* pool, float* scales, cudaStream_t stream) {
   // A CTA of one row is either one block's or leaves at once, which is the
-  // shortest path while all rows' CTAs fit the GPU together; behind that, 16
-  // rows (one block's worth) a CTA.
-  const int chunk = t.cu == nullptr || t.n_tokens <= 1024 ? 1 : kBlock;
+  // shortest path while all rows' CTAs fit the GPU together; behind that, as
+  // many rows a CTA as a request has on average, up to a block's 16.
+  const int chunk =
+      t.cu == nullptr || t.n_tokens <= 1024 ? 1 : std::clamp(t.n_tokens / t.B, 1, kBlock);
   const int kv = (t.n_tokens + chunk - 1) / chunk;
   int share = 1, q = 0;
   if (t.q) row_grid(t.n_tokens, &share, &q);
@@ -706,6 +709,7 @@ extern "C" int kv_gather_q8(const void* pool, const float* scales, int64_t pool_
   if (head_dim != 128 && head_dim != 256)
     return pa::fail(PA_ERR_UNSUPPORTED, "head_dim %d not built (supported: 128, 256)", head_dim);
   if (n_tokens == 0 || B == 0) return PA_OK;
+  PA_REQUIRE(n_tokens <= kMaxTokens, "n_tokens (%d) above %d", n_tokens, kMaxTokens);
   PA_REQUIRE(n_kv_heads >= 1 && n_kv_heads <= 4096, "n_kv_heads (%d) must be in 1..4096",
              n_kv_heads);
   PA_REQUIRE(pool && scales && page_table && positions && out, "null pointer argument");

@@ -60,6 +60,14 @@ def test_head_dims_that_are_not_built(B):
         assert B.lib.kv_gather_q8(*args) == code, (at, bad)
 
 
+def test_more_rows_than_32_bits_number_are_refused(B):
+    n = (1 << 30) + 1
+    for q8 in (False, True):
+        assert append(B, q8, n=n) == B.PA_ERR_INVALID and "n_tokens" in B.last_error()
+    assert B.lib.kv_gather_q8(FAKE, FAKE, 4, FAKE, 4, FAKE, FAKE, n, 2, 2, 128, FAKE, None,
+                              None) == B.PA_ERR_INVALID
+
+
 def test_nothing_to_do_is_no_error(B):
     assert append(B, n=0) == B.PA_OK
     assert append(B, True, batch=0) == B.PA_OK

@@ -369,3 +369,82 @@ def test_captured_append_replays_with_new_inputs(B, q8):
         assert torch.equal(q2, q_out)
         assert torch.equal(pool2.view(torch.uint8), pool.view(torch.uint8))
         assert torch.equal(scales2, scales)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(new=[1] * 1100, past=[i * 7 % 150 for i in range(1100)], hq=2, hkv=1, d=128, pad=2),
+    dict(new=[i % 9 for i in range(400)], past=[i * 11 % 90 for i in range(400)], hq=2, hkv=1,
+         d=128, rot=64),
+    dict(new=[0] * 300 + [1300] + [0] * 200, past=[0] * 300 + [7] + [0] * 200, hq=2, hkv=1, d=256),
+], ids=["single-tokens", "short", "one-among-empty"])
+def test_q8_appends_of_many_requests(B, kw):
+    """More rows than are given a CTA each, in requests of few tokens or none."""
+    test_q8_append_and_gather(B, kw)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_pages_past_4_gib_of_pool(B, q8):
+    """The same pages at the top of a 5.4 GB pool: the same bits are stored, and
+    read back."""
+    s = Step([70, 1, 300], [5, 63, 0], hq=4, hkv=4, d=256, seed=21)
+    row = 2 * s.hkv * s.d
+    small, sc_small = _filled(s)
+    if not q8:
+        small = torch.randn(s.pages, 64, row, device=DEV).bfloat16()
+    pages = 5_400_000_000 // (64 * row * small.element_size())
+    lift = pages - s.pages
+    assert lift * 64 * row * small.element_size() > 1 << 32
+    big = torch.zeros(pages, 64, row, dtype=torch.uint8 if q8 else torch.bfloat16, device=DEV)
+    big = big.view(E4M3) if q8 else big
+    raw = (lambda t: t.view(torch.uint8)) if q8 else (lambda t: t)
+    raw(big)[lift:] = raw(small)
+    sc_big = torch.ones(pages, 2 * s.hkv, 4, device=DEV)
+    sc_big[lift:] = sc_small
+    table = s.t["table"] + lift
+    for pool, scales, tab in ((small, sc_small, s.t["table"]), (big, sc_big, table)):
+        if q8:
+            B.kv_append_rope_q8(None, s.k, s.v, pool, scales, tab, s.t["pos"], s.t["inv"],
+                                cu_tokens=s.t["cu"])
+        else:
+            B.kv_append_rope(None, s.k, s.v, pool, tab, s.t["pos"], s.t["inv"],
+                             cu_tokens=s.t["cu"])
+    torch.cuda.synchronize()
+    bits = (lambda t: t.view(torch.uint8)) if q8 else (lambda t: t.view(torch.int16))
+    assert torch.equal(bits(big[lift:]), bits(small))
+    assert not raw(big)[:64].any()
+    if q8:
+        assert torch.equal(sc_big[lift:], sc_small)
+        outs = []
+        for pool, scales, tab in ((small, sc_small, s.t["table"]), (big, sc_big, table)):
+            outs.append(torch.empty(s.n, row, dtype=torch.bfloat16, device=DEV))
+            B.kv_gather_q8(pool, scales, tab, s.t["pos"], s.t["cu"], outs[-1])
+        torch.cuda.synchronize()
+        assert torch.equal(*outs)
+
+
+def test_padded_requests_of_a_captured_step(B):
+    """A graph captured for more requests than a step has: the spare ones hold
+    position -1, store nothing and say so; the others are as in a call of their
+    own."""
+    s = Step([1] * 6, [0, 15, 16, 63, 64, 500], hq=4, hkv=2, d=128, seed=22)
+    pool, scales = _filled(s)
+    want_pool, want_scales = pool.view(torch.uint8).clone().view(E4M3), scales.clone()
+    n = 11
+    q = torch.cat([s.q, s.q[:n - 6]])
+    k, v = torch.cat([s.k, s.k[:n - 6]]), torch.cat([s.v, s.v[:n - 6]])
+    table = torch.cat([s.t["table"], s.t["table"][:n - 6]])
+    pos = torch.cat([s.t["pos"], torch.full((n - 6,), -1, dtype=torch.int32, device=DEV)])
+    q_out = torch.empty_like(q)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        B.kv_append_rope_q8(q, k, v, pool, scales, table, pos, s.t["inv"], q_out, status=status)
+    graph.replay()
+    want_q = torch.empty_like(s.q, memory_format=torch.contiguous_format)
+    B.kv_append_rope_q8(s.q, s.k, s.v, want_pool, want_scales, s.t["table"], s.t["pos"],
+                        s.t["inv"], want_q)
+    torch.cuda.synchronize()
+    assert int(status.item()) == B.PA_STATUS_BAD_ROW
+    assert torch.equal(pool.view(torch.uint8), want_pool.view(torch.uint8))
+    assert torch.equal(scales, want_scales) and torch.equal(q_out[:6], want_q)

@@ -442,3 +442,51 @@ def test_q_that_is_not_finite_gives_nan_in_its_head_alone(B):
     bad[1] = bad[6] = True
     assert c.out[0, 0][bad].isnan().all() and c.lse[0, 0][bad].isnan().all()
     assert c.out[0, 0][~bad].isfinite().all() and c.lse[0, 0][~bad].isfinite().all()
+
+
+@pytest.mark.parametrize("n,full,tiles", [(256, 4, 1), (300, 3, 5), (1500, 2, 1), (200, 0, 3)])
+def test_many_requests_without_tokens(B, n, full, tiles):
+    """Padded batches: units without pages outnumber the others (and the CTAs)."""
+    rng = np.random.default_rng(n)
+    lengths = [0] * n
+    for b in rng.choice(n, full, replace=False):
+        lengths[b] = int(rng.integers(1, 900))
+    cut = [[(min(x, t * 200), x if t == tiles - 1 else min(x, t * 200 + 200))
+            for t in range(tiles)] for x in lengths]
+    c = Case(lengths, cut, hq=8, hkv=2, d=256, seed=47)
+    for _ in range(2):                      # the workspace is ready for another call
+        c.merged.fill_(7.0)
+        assert c.run(B) == 0
+        c.check([b for b in range(n) if lengths[b]])
+        empty = torch.tensor([x == 0 for x in lengths], device=DEV)
+        assert torch.all(c.merged[empty] == 0)
+        assert torch.all(c.merged_lse[empty] == -float("inf"))
+        assert torch.all(c.out[empty] == 0) and torch.all(c.lse[empty] == -float("inf"))
+
+
+def test_pages_past_4_gib_of_pool(B):
+    """The same pages at the top of a 5.4 GB pool: the same bits."""
+    c = Case([3000, 777], [[(0, 3000), (100, 2000)], [(0, 777), (777, 777)]], hq=24, hkv=4, d=256,
+             seed=48)
+    assert c.run(B) == 0
+    want = [t.clone() for t in (c.out, c.lse, c.merged, c.merged_lse)]
+    pages = 5_400_000_000 // (64 * 2 * c.hkv * c.d)
+    lift = pages - c.pages
+    pool = torch.full((pages, 64, 2 * c.hkv * c.d), 0x7F, dtype=torch.uint8, device=DEV)
+    pool[lift:] = c.pool.view(torch.uint8)
+    scales = torch.full((pages, 2 * c.hkv, 4), float("nan"), device=DEV)
+    scales[lift:] = c.scales
+    c.pool, c.scales, c.table_dev = pool.view(E4M3), scales, c.table_dev + lift
+    assert c.run(B) == 0
+    for a, b in zip((c.out, c.lse, c.merged, c.merged_lse), want):
+        assert torch.equal(a, b)
+
+
+def test_requests_that_share_pages(B):
+    """A prefix common to two requests is stored once: both attend it."""
+    c = Case([640, 1000, 700], hq=8, hkv=2, d=128, seed=49)
+    for b in (1, 2):
+        c.table[b, :6] = c.table[0, :6]
+    c.table_dev.copy_(torch.from_numpy(c.table))
+    assert c.run(B) == 0
+    c.check()
