@@ -80,8 +80,7 @@ static_assert(kSmemAlloc <= 232448, "shared memory budget");
 
 template <int kMaxUnits>
 struct Params {
-  static constexpr bool kSecondOut = false, kAllSlices = false, kTilesTogether = false;
-  static constexpr bool kMerge = true;
+  static constexpr bool kSecondOut = false, kAllSlices = false, kMerge = true;
   const __nv_bfloat16* q;
   const int32_t* page_table;
   float* out;

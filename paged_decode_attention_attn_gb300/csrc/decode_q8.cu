@@ -6,8 +6,8 @@
 // Both products therefore run on the fifth-generation tensor cores straight
 // from the codes as TMA leaves them in shared memory; no thread touches a code.
 //
-//  * Work split, partials and merge: as the bf16 kernel (split_units.cuh).  A
-//    CTA streams its pages two at a time: a step is 128 tokens of one kv head.
+//  * Work split and partials: as the bf16 kernel (split_units.cuh); a request's
+//    tiles are merged by a kernel of its own.  A CTA streams its pages two at a time: a step is 128 tokens of one kv head.
 //  * S = K Q^T: M = 128 tokens, N = 16, K = D.  q (bf16, 8 significant bits) is
 //    scaled by a power of two per head and held as hi + lo / 16 in e4m3 (4 bits
 //    each, and a sign between them): 16 columns for 8 heads, exact for values
@@ -130,7 +130,7 @@ struct Smem {
   static_assert(kAlloc <= 232448, "shared memory budget");
 };
 
-template <int kMaxUnits, bool kMergeTiles>
+template <int kMaxUnits>
 struct Params {
   const __nv_bfloat16* q;
   const float* scales;
@@ -139,7 +139,6 @@ struct Params {
   float* lse;
   int32_t* status;
   unsigned long long* arrivals;
-  int32_t* req_counters;
   float* part_o;
   float* part_ml;
   long long pool_pages;
@@ -155,19 +154,15 @@ struct Params {
   unsigned long long wait_limit_ns;
   int stall_iteration;
   unsigned long long slice_wait_ns;
-  float* m_out;
-  float* m_lse;
-  static constexpr bool kAllSlices = true, kTilesTogether = true;
-  // Several tiles per request, to be merged; else a tile's output may be the
-  // merged one too, written with it.
-  static constexpr bool kMerge = kMergeTiles, kSecondOut = !kMergeTiles;
+  // One tile per request: its output may be the merged one too, written with it.
+  static constexpr bool kAllSlices = true, kMerge = false, kSecondOut = true;
   float* out2;
   float* lse2;
   int32_t starts[kMaxGrid + 1];      // CTA k takes flattened pages [k], [k + 1)
   int16_t first_unit[kMaxGrid + 1];  // and its first unit
   Unit units[kMaxUnits];
 };
-static_assert(sizeof(Params<kMaxUnitsLarge, true>) <= 32764, "kernel parameters too large");
+static_assert(sizeof(Params<kMaxUnitsLarge>) <= 32764, "kernel parameters too large");
 
 struct View {
   uint8_t* base;
@@ -509,25 +504,33 @@ __device__ __forceinline__ void product_warp(const P& p, const View& v, uint32_t
 // heads each, for a CTA's first segment (on one warp it takes 3.7 us, the
 // longest part of a launch's start), by warp 15 ahead of time for the others.
 // ---------------------------------------------------------------------------
+template <int D>
+using QVec = typename std::conditional<D == 256, uint4, uint2>::type;   // D / 32 dims per lane
+
 template <int D, int kHeads, class P>
-__device__ __forceinline__ void convert_q(const P& p, const View& v, const Segment& s, int buffer,
-                                          int h0, int lane) {
-  using S = Smem<D>;
-  constexpr int kDims = D / 32;             // dims per lane
-  using Vec = typename std::conditional<kDims == 8, uint4, uint2>::type;
-  const __nv_bfloat16* src = p.q + ((size_t)s.b * p.Hq + s.g * p.G + h0) * D + lane * kDims;
-  Vec raw[kHeads];
+__device__ __forceinline__ void load_q(const P& p, const Segment& s, int h0, int lane,
+                                       QVec<D> (&raw)[kHeads]) {
+  const __nv_bfloat16* src = p.q + ((size_t)s.b * p.Hq + s.g * p.G + h0) * D + lane * (D / 32);
 #pragma unroll
   for (int h = 0; h < kHeads; ++h) {
-    raw[h] = Vec{};
-    if (h0 + h < p.G) raw[h] = __ldg(reinterpret_cast<const Vec*>(src + h * D));
+    raw[h] = QVec<D>{};
+    if (h0 + h < p.G) raw[h] = __ldg(reinterpret_cast<const QVec<D>*>(src + h * D));
   }
+}
+
+// The first `heads` (the others' columns are zero already).
+template <int D, int kHeads, class P>
+__device__ __forceinline__ void convert_q(const P& p, const View& v, const QVec<D> (&raw)[kHeads],
+                                          int buffer, int h0, int heads, int lane) {
+  using S = Smem<D>;
+  constexpr int kDims = D / 32;             // dims per lane
   float* qscale = reinterpret_cast<float*>(v.base + S::kQScale) + buffer * kMaxG + h0;
   const int col = lane * kDims;
   const uint32_t buf = v.addr + S::kQ + buffer * S::kQBytes + col / kChunk * S::kQChunkBytes +
                        (col & 15);
 #pragma unroll
   for (int h = 0; h < kHeads; ++h) {
+    if (h % 2 == 0 && h >= heads) break;
     const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[h]);
     unsigned amax = 0;
 #pragma unroll
@@ -576,9 +579,17 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, const
   const float* sr = reinterpret_cast<const float*>(v.base + S::kSegRef) + r.i * kGroups * kMaxG;
   float* factor = reinterpret_cast<float*>(v.base + S::kFactor) + r.i * kMaxG;
   const bool nan = (v.seg_poison[r.i * kGroups] | v.seg_poison[r.i * kGroups + 1]) != 0;
+  const float qnan = __int_as_float(0x7fc00000);
+  float m = -INFINITY, l = 0.f;
+  auto store_lse = [&]() {
+    if (lane >= p.G) return;
+    const size_t row = (size_t)s.bt * p.Hq + s.g * p.G + lane;
+    const float x = nan ? qnan : lse_of(m, l);
+    p.lse[row] = x;
+    if (p.lse2) p.lse2[row] = x;
+  };
   if (lane < kMaxG) {
-    const float qnan = __int_as_float(0x7fc00000);
-    float m = -INFINITY, l = 0.f, f;
+    float f;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) m = fmaxf(m, sr[g * kMaxG + lane]);
 #pragma unroll
@@ -589,12 +600,6 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, const
     }
     if (s.whole()) {
       f = 1.0f / l;
-      if (lane < p.G) {
-        const size_t row = (size_t)s.bt * p.Hq + s.g * p.G + lane;
-        const float x = nan ? qnan : lse_of(m, l);
-        p.lse[row] = x;
-        if (p.lse2) p.lse2[row] = x;
-      }
     } else {
       // The reference bounds V's scales too; the partial's is moved to the
       // sum's own magnitude, so that partials of blocks whose V scales lie far
@@ -613,6 +618,7 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, const
     ptx::mbar_arrive(v.bar(S::kFFull + r.i));
   }
   r.next();
+  if (s.whole()) store_lse();   // not in the outputs' way
   return true;
 }
 
@@ -624,9 +630,7 @@ __device__ __forceinline__ void helper_warp(const P& p, const View& v, int lane)
   // Empty units: output 0, LSE -inf.
   for (int u = p.n_full + blockIdx.x; u < p.n_units; u += p.grid) {
     const Unit& U = p.units[u];
-    const int bt = U.bt, g = U.g;
-    const int b = bt / p.T;
-    const size_t row = (size_t)bt * p.Hq + g * p.G;
+    const size_t row = (size_t)U.bt * p.Hq + U.g * p.G;
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = lane; i < p.G * D / 4; i += 32) {
       reinterpret_cast<float4*>(p.out + row * D)[i] = zero;
@@ -636,40 +640,33 @@ __device__ __forceinline__ void helper_warp(const P& p, const View& v, int lane)
       p.lse[row + lane] = -INFINITY;
       if (p.lse2) p.lse2[row + lane] = -INFINITY;
     }
-    if (P::kMerge) {
-      // its part in the pair's merge, as finish_unit does it
-      int* counter = p.req_counters + b * p.Hkv + g;
-      __syncwarp();
-      int prev = lane == 0 ? ptx::atomic_add_acq_rel_gpu(counter, 1) : 0;
-      prev = __shfl_sync(0xffffffffu, prev, 0);
-      if (prev + 1 == U.pair_total) {
-        for (int r = 0; r < p.G; ++r) {
-          const int h = g * p.G + r;
-          mergerow::merge_row<true>(p.out, p.lse, b * p.T, p.T, p.Hq, h, D,
-                                    p.m_out + ((size_t)b * p.Hq + h) * D,
-                                    p.m_lse + (size_t)b * p.Hq + h, lane);
-        }
-        if (lane == 0) *counter = 0;
-      }
-    }
   }
-  Segment last;
-  bool any = false, ok = true;
-  for_segments(p, [&](const Segment& s, int) {
-    if (any) {
-      ok = warp_wait(p, v, S::kQEmpty + qr.i, qr.phase ^ 1);
-      if (!ok) return false;
-      convert_q<D, kMaxG>(p, v, s, qr.i, 0, lane);
-      if (lane < kOutWarps) ptx::mbar_arrive(v.bar(S::kQFull + qr.i));
-      ok = segment_factors<D>(p, v, last, fr, lane);
-      if (!ok) return false;
-    }
-    qr.next();   // (the output warps convert the first segment's)
-    last = s;
-    any = true;
+  // q is loaded two segments ahead and converted one ahead (the first segment's
+  // is the output warps').
+  Segments<P> ahead(p);
+  Segment s;
+  QVec<D> raw[kMaxG];
+  bool more = ahead.next(s);
+  auto load_next = [&]() {
+    more = more && ahead.next(s);
+    if (more) load_q<D>(p, s, 0, lane, raw);
+  };
+  int heads = kMaxG;   // the first conversion clears the columns without a head
+  auto convert_next = [&]() {
+    qr.next();
+    if (!more) return true;
+    if (!warp_wait(p, v, S::kQEmpty + qr.i, qr.phase ^ 1)) return false;
+    convert_q<D>(p, v, raw, qr.i, 0, heads, lane);
+    heads = p.G;
+    if (lane < kOutWarps) ptx::mbar_arrive(v.bar(S::kQFull + qr.i));
+    load_next();
     return true;
+  };
+  load_next();
+  if (!convert_next()) return;
+  for_segments(p, [&](const Segment& now, int) {
+    return segment_factors<D>(p, v, now, fr, lane) && convert_next();
   });
-  if (any && ok) segment_factors<D>(p, v, last, fr, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -851,7 +848,10 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
   const int ct = warp * 32 + lane;
   ptx::grid_dependency_wait();   // earlier kernels write q and may still read the outputs
   for_segments(p, [&](const Segment& s, int) {
-    convert_q<D, kMaxG / kOutWarps>(p, v, s, 0, warp * (kMaxG / kOutWarps), lane);
+    constexpr int kHeads = kMaxG / kOutWarps;
+    QVec<D> raw[kHeads];
+    load_q<D>(p, s, warp * kHeads, lane, raw);
+    convert_q<D>(p, v, raw, 0, warp * kHeads, kHeads, lane);
     if (lane == 0) ptx::mbar_arrive(v.bar(S::kQFull));
     return false;   // the first segment's
   });
@@ -942,10 +942,7 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(v.bar(S::kFEmpty + (seg & 1)));
-    if (s.whole()) {
-      // without a merge pass nothing follows: the next segment may start
-      if (P::kMerge) finish_unit<D, kOut>(p, v, s.b, s.g, ct, warp, lane, 1, s.U.pair_total);
-    } else {
+    if (!s.whole()) {
       finish_split_unit<D, kOut>(p, v, s.U, s.u, s.b, s.bt, s.g, s.U.first_cta, ct, warp, lane);
       ptx::named_barrier(1, kOut);   // merge_info is read before it is written again
     }
@@ -953,10 +950,10 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
   });
 }
 
-template <int D, int kMaxUnits, bool kMerge>
+template <int D, int kMaxUnits>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmap,
-                     const __grid_constant__ Params<kMaxUnits, kMerge> p) {
+                     const __grid_constant__ Params<kMaxUnits> p) {
   using S = Smem<D>;
   extern __shared__ uint8_t smem_raw[];
   View v;
@@ -1014,6 +1011,84 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after();
   if (warp == kScoreWarp) tc::dealloc(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------------------
+// The merge of every request's T tiles, in lse_merge's arithmetic: a thread per
+// float4 of an output row, kBatch tiles' values in flight with the LSEs that
+// weigh them.  As a launch of its own it costs its wait and a round of loads,
+// 1.5-2.5 us; inside the attention kernel, by the CTA that completed a request's
+// tiles (as the bf16 kernel does it), such a CTA's stream stood still for an
+// arrival and its answer and for code and values met cold: 262,144 tokens in 8
+// tiles 88.2 -> 85.4 us, 700 in 7 tiles 11.8 -> 7.4, 42 requests of 593 in 6
+// tiles 42.4 -> 33.0, 60 of up to 3,828 in 7 tiles 116.6 -> 82.9.
+// ---------------------------------------------------------------------------
+constexpr int kMergeThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads)
+    merge_kernel(const float* out, const float* lse, int T, int Hq, int rows, float* m_out,
+                 float* m_lse) {
+  constexpr int kVec = D / 4, kBatch = 8;
+  ptx::launch_dependents();
+  ptx::grid_dependency_wait();
+  const int row = blockIdx.x * (kMergeThreads / kVec) + threadIdx.x / kVec;
+  if (row >= rows) return;
+  const int c = threadIdx.x % kVec;
+  const size_t first = (size_t)(row / Hq) * T * Hq + row % Hq;   // of tile 0; tile t: + t Hq
+  lse += first;
+  const float4* src = reinterpret_cast<const float4*>(out) + first * kVec + c;
+  const size_t step = (size_t)Hq * kVec;
+  float4 x[kBatch];
+  float l[kBatch];
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      l[i] = -INFINITY;
+      if (t0 + i < T) {
+        l[i] = __ldcg(lse + (size_t)(t0 + i) * Hq);
+        x[i] = __ldcg(src + (t0 + i) * step);
+      }
+    }
+  };
+  load(0);
+  float m = -INFINITY;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    nan |= l[i] != l[i];
+    m = fmaxf(m, l[i]);
+  }
+#pragma unroll 8
+  for (int t = kBatch; t < T; ++t) {
+    const float y = __ldcg(lse + (size_t)t * Hq);
+    nan |= y != y;
+    m = fmaxf(m, y);
+  }
+  float4* dst = reinterpret_cast<float4*>(m_out + (size_t)row * D) + c;
+  if (nan || m == -INFINITY) {
+    const float fill = nan ? __int_as_float(0x7fc00000) : 0.f;
+    *dst = make_float4(fill, fill, fill, fill);
+    if (c == 0) m_lse[row] = nan ? fill : -INFINITY;
+    return;
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float ws = 0.f;
+  for (int t0 = 0; t0 < T; t0 += kBatch) {
+    if (t0 > 0) load(t0);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (t0 + i >= T) break;
+      const float w = expf(l[i] - m);
+      ws += w;
+      acc.x = fmaf(w, x[i].x, acc.x);
+      acc.y = fmaf(w, x[i].y, acc.y);
+      acc.z = fmaf(w, x[i].z, acc.z);
+      acc.w = fmaf(w, x[i].w, acc.w);
+    }
+  }
+  *dst = make_float4(acc.x / ws, acc.y / ws, acc.z / ws, acc.w / ws);
+  if (c == 0) m_lse[row] = m + logf(ws);
 }
 
 // ---------------------------------------------------------------------------
@@ -1091,12 +1166,12 @@ void cut(const Unit* units, const int32_t* pages, size_t n, long long total, int
   if (starts->size() < ctas + 1) starts->resize(ctas + 1, starts->back());
 }
 
-using Common = Params<kMaxUnitsSmall, false>;
+using Common = Params<kMaxUnitsSmall>;
 
-template <int D, int N, bool kMerge>
+template <int D, int N>
 int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L, const Common& common,
                  cudaStream_t stream) {
-  using Prm = Params<N, kMerge>;
+  using Prm = Params<N>;
   static_assert(N >= kMaxUnitsSmall && offsetof(Prm, starts) == offsetof(Common, starts), "");
   Prm prm;
   std::memcpy(static_cast<void*>(&prm), &common, offsetof(Common, starts));
@@ -1119,11 +1194,11 @@ int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L, con
   }
   static PerContext smem_limit;   // the attribute lives in the context
   cudaError_t e = smem_limit.apply([] {
-    return cudaFuncSetAttribute(decode_q8_kernel<D, N, kMerge>,
+    return cudaFuncSetAttribute(decode_q8_kernel<D, N>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kAlloc);
   });
   if (e == cudaSuccess)
-    e = launch_dependent(decode_q8_kernel<D, N, kMerge>, dim3(L.grid), dim3(kThreads), Smem<D>::kAlloc,
+    e = launch_dependent(decode_q8_kernel<D, N>, dim3(L.grid), dim3(kThreads), Smem<D>::kAlloc,
                          stream, tmap, prm);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess)
@@ -1131,15 +1206,14 @@ int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L, con
   return PA_OK;
 }
 
-template <bool kMerge>
 int launch(int D, const CUtensorMap& tmap, const Plan& plan, const Launch& L, const Common& common,
            cudaStream_t stream) {
   const bool small = L.n <= (size_t)kMaxUnitsSmall;
   if (D == 128)
-    return small ? launch_units<128, kMaxUnitsSmall, kMerge>(tmap, plan, L, common, stream)
-                 : launch_units<128, kMaxUnitsLarge, kMerge>(tmap, plan, L, common, stream);
-  return small ? launch_units<256, kMaxUnitsSmall, kMerge>(tmap, plan, L, common, stream)
-               : launch_units<256, kMaxUnitsLarge, kMerge>(tmap, plan, L, common, stream);
+    return small ? launch_units<128, kMaxUnitsSmall>(tmap, plan, L, common, stream)
+                 : launch_units<128, kMaxUnitsLarge>(tmap, plan, L, common, stream);
+  return small ? launch_units<256, kMaxUnitsSmall>(tmap, plan, L, common, stream)
+               : launch_units<256, kMaxUnitsLarge>(tmap, plan, L, common, stream);
 }
 
 int run(const void* q, const void* pool, const float* scales, int64_t pool_pages,
@@ -1198,7 +1272,7 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   sms = std::min(sms, kMaxGrid);
   Plan plan;
   int rc = plan_units<true>(
-      tiles, B, T, Hkv, kSegmentCharge, T > 1 && merged_out != nullptr,
+      tiles, B, T, Hkv, kSegmentCharge, false,
       [&](const Unit* units, const int32_t* pages, size_t n, long long total,
           std::vector<int32_t>* starts) { cut(units, pages, n, total, sms, Hkv, starts); },
       &plan);
@@ -1213,7 +1287,6 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   const Workspace ws(workspace, B, T, Hkv, D);
   common.status = ws.status;
   common.arrivals = ws.arrivals;
-  common.req_counters = ws.req_counters;
   common.part_o = ws.part_o;
   common.part_ml = ws.part_ml;
   common.pool_pages = pool_pages;
@@ -1223,16 +1296,26 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   common.Hkv = Hkv;
   common.G = Hq / Hkv;
   common.scale_log2 = scale * kLog2e;
-  (T == 1 ? common.out2 : common.m_out) = merged_out;
-  (T == 1 ? common.lse2 : common.m_lse) = merged_lse;
+  if (T == 1) {
+    common.out2 = merged_out;
+    common.lse2 = merged_lse;
+  }
   const TestHooks hooks = take_test_hooks();
   common.wait_limit_ns = hooks.wait_limit_ns;
   common.stall_iteration = hooks.stall_iteration;
   common.slice_wait_ns = hooks.slice_wait_ns;
   for (const Launch& L : plan.launches) {
-    rc = common.m_out ? launch<true>(D, tmap, plan, L, common, stream)
-                      : launch<false>(D, tmap, plan, L, common, stream);
+    rc = launch(D, tmap, plan, L, common, stream);
     if (rc != PA_OK) return rc;
+  }
+  if (T > 1 && merged_out != nullptr) {
+    const int rows = B * Hq, per_block = kMergeThreads / (D / 4);
+    const dim3 grid((rows + per_block - 1) / per_block);
+    PA_CHECK_CUDA(launch_dependent(D == 128 ? merge_kernel<128> : merge_kernel<256>, grid,
+                                   dim3(kMergeThreads), 0, stream,
+                                   const_cast<const float*>(out), const_cast<const float*>(lse), T,
+                                   Hq, rows, merged_out, merged_lse));
+    PA_CHECK_CUDA(cudaGetLastError());
   }
   return PA_OK;
 }

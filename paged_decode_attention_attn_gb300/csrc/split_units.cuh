@@ -4,13 +4,12 @@
 //
 // A unit is one (tile, kv head).  All units' pages are laid end to end and cut
 // into one contiguous page range per CTA.  A kernel's parameter struct P has
-// the fields these functions name (out, lse, status, arrivals, req_counters,
-// part_o, part_ml, T, Hq, Hkv, G, n_units, units, m_out,
-// m_lse, wait_limit_ns, slice_wait_ns, and out2, lse2 where kSecondOut says that
-// outputs are written twice; kAllSlices, see split_slices; kTilesTogether,
-// see merge_tiles; kMerge: m_out may be set); its shared-memory view Sh has fin_flag
-// and merge_info.  The kConsumers threads that call a function meet at named
-// barrier 1.
+// the fields these functions name (out, lse, status, arrivals, part_o, part_ml,
+// T, Hq, Hkv, G, n_units, units, wait_limit_ns, slice_wait_ns; where kSecondOut
+// says that outputs are written twice, out2 and lse2; where kMerge says that the
+// kernel merges a request's tiles, m_out, m_lse and req_counters; kAllSlices,
+// see split_slices); its shared-memory view Sh has fin_flag and merge_info.  The
+// kConsumers threads that call a function meet at named barrier 1.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -140,75 +139,6 @@ __device__ __forceinline__ float ref_weight(float m, float big_m) {
   return (m == -INFINITY) ? 0.f : ptx::pow2i(static_cast<int>(m - big_m));
 }
 
-// The T tiles' merge of the G query heads of (request b, kv head g), a thread per
-// float4 of the outputs, in merge_row's arithmetic and order (same bits).  The
-// values of kBatch tiles are loaded together, the first ones with the LSEs that
-// weigh them, where merge_row waits for one tile's before it asks for the next
-// (7 ragged requests in 5 tiles: 22.5 -> 22.0 us; with 8 a batch it spills).
-template <int kD, int kConsumers, class P>
-__device__ __forceinline__ void merge_tiles(const P& p, int b, int g, int ct) {
-  constexpr int kVec = kD / 4, kBatch = 4;
-  for (int o = ct; o < p.G * kVec; o += kConsumers) {
-    const int r = o / kVec, c = o - r * kVec;
-    const int h = g * p.G + r;
-    const size_t row = (size_t)b * p.T * p.Hq + h;      // of tile 0; tile t: + t Hq
-    const float* lse = p.lse + row;
-    const float4* src = reinterpret_cast<const float4*>(p.out + row * kD) + c;
-    const size_t step = (size_t)p.Hq * kVec;
-    float4 x[kBatch];
-    float l[kBatch];
-    auto load = [&](int t0) {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        l[i] = -INFINITY;
-        if (t0 + i < p.T) {
-          l[i] = __ldcg(lse + (size_t)(t0 + i) * p.Hq);
-          x[i] = __ldcg(src + (t0 + i) * step);
-        }
-      }
-    };
-    load(0);
-    float m = -INFINITY;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      nan |= l[i] != l[i];
-      m = fmaxf(m, l[i]);
-    }
-    for (int t = kBatch; t < p.T; ++t) {
-      const float y = __ldcg(lse + (size_t)t * p.Hq);
-      nan |= y != y;
-      m = fmaxf(m, y);
-    }
-    float4* dst = reinterpret_cast<float4*>(p.m_out + ((size_t)b * p.Hq + h) * kD) + c;
-    float* dst_lse = p.m_lse + (size_t)b * p.Hq + h;
-    if (nan || m == -INFINITY) {
-      const float fill = nan ? __int_as_float(0x7fc00000) : 0.f;
-      *dst = make_float4(fill, fill, fill, fill);
-      if (c == 0) *dst_lse = nan ? fill : -INFINITY;
-      continue;
-    }
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float ws = 0.f;
-    for (int t0 = 0; t0 < p.T; t0 += kBatch) {
-      if (t0 > 0) load(t0);
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (t0 + i >= p.T) break;
-        const float w = expf(l[i] - m);
-        ws += w;
-        acc.x = fmaf(w, x[i].x, acc.x);
-        acc.y = fmaf(w, x[i].y, acc.y);
-        acc.z = fmaf(w, x[i].z, acc.z);
-        acc.w = fmaf(w, x[i].w, acc.w);
-      }
-    }
-    *dst = make_float4(acc.x / ws, acc.y / ws, acc.z / ws, acc.w / ws);
-    if (c == 0) *dst_lse = m + logf(ws);
-  }
-}
-
-
 // Called by every consumer thread once it has stored `done` parts of the
 // tile outputs of (request b, kv head g): a whole unsplit (or empty) unit
 // counts 1, a slice of a split unit 1.  With the fused merge, the CTA whose
@@ -220,28 +150,25 @@ template <int kD, int kConsumers, class P, class Sh>
 __device__ __forceinline__ void finish_unit(const P& p, const Sh& sh, int b,
                                             int g, int ct, int warp, int lane, int done,
                                             int total) {
-  if constexpr (!P::kMerge) return;
-  if (p.m_out == nullptr) return;
-  ptx::named_barrier(1, kConsumers);       // this CTA's outputs are all stored
-  if (ct == 0) {
-    const int prev = ptx::atomic_add_acq_rel_gpu(p.req_counters + b * p.Hkv + g, done);
-    *sh.fin_flag = (prev + done == total) ? 1 : 0;
-  }
-  ptx::named_barrier(1, kConsumers);
-  if (*sh.fin_flag) {
-    if constexpr (P::kTilesTogether) {
-      merge_tiles<kD, kConsumers>(p, b, g, ct);
-    } else {
+  if constexpr (P::kMerge) {
+    if (p.m_out == nullptr) return;
+    ptx::named_barrier(1, kConsumers);       // this CTA's outputs are all stored
+    if (ct == 0) {
+      const int prev = ptx::atomic_add_acq_rel_gpu(p.req_counters + b * p.Hkv + g, done);
+      *sh.fin_flag = (prev + done == total) ? 1 : 0;
+    }
+    ptx::named_barrier(1, kConsumers);
+    if (*sh.fin_flag) {
       for (int r = warp; r < p.G; r += kConsumers / 32) {
         const int h = g * p.G + r;
         mergerow::merge_row<true>(p.out, p.lse, b * p.T, p.T, p.Hq, h, kD,
                                   p.m_out + ((size_t)b * p.Hq + h) * kD,
                                   p.m_lse + (size_t)b * p.Hq + h, lane);
       }
+      if (ct == 0) p.req_counters[b * p.Hkv + g] = 0;
     }
-    if (ct == 0) p.req_counters[b * p.Hkv + g] = 0;
+    ptx::named_barrier(1, kConsumers);
   }
-  ptx::named_barrier(1, kConsumers);
 }
 
 // Merges output float4s [o_lo, o_hi) of a split unit (o = row * kD/4 + float4
