@@ -1,10 +1,10 @@
 /*
  * pagedattn.h -- C ABI of libpagedattn: paged GQA decode attention with a
  * per-tile log-sum-exp over bf16 and 8-bit pools, appends with the position
- * rotation, an FP32 LSE merge, a staging arena that moves KV
- * history from pinned host memory into bounded device slots (stage calls or
- * leases), an admission planner for a device pool, and a background converter
- * of fully written pages into a compact representation.
+ * rotation, an FP32 LSE merge, a staging arena that moves KV history from
+ * pinned host memory into bounded device slots (stage calls or leases), an
+ * admission planner for a device pool, and a background converter of fully
+ * written pages into a compact representation.
  *
  * Sources (web pages, cited by title and section):
  *   [KVE-exact]  "KV-cache engineering", section "Exact recent pages, compact
@@ -327,8 +327,8 @@ int kv_append_rows(void* pool, int64_t pool_pages, const int32_t* page_table,
  *
  * Token row r of the step belongs to the request b with cu_tokens[b] <= r <
  * cu_tokens[b+1] and has position p = positions[b] + r - cu_tokens[b]; a call
- * takes up to 2^30 rows.  For
- * i < rot_dim / 2 the pair (x1, x2) of every q and k head becomes
+ * takes up to 2^30 rows.  For i < rot_dim / 2 the pair (x1, x2) of every q and
+ * k head becomes
  *     (x1 cos a - x2 sin a, x2 cos a + x1 sin a),   a = p * inv_freq[i],
  * evaluated in FP32 with a reduced modulo 2 pi in 64-bit integers (any
  * position keeps its angle to about 1e-7 for |inv_freq| <= 1); values behind
@@ -342,8 +342,8 @@ int kv_append_rows(void* pool, int64_t pool_pages, const int32_t* page_table,
  *              overlap q otherwise, nor k or v.
  *   cu_tokens  device int32 [B+1], non-decreasing, cu_tokens[0] = 0; requests
  *              may have no tokens; rows at and behind cu_tokens[B] (padding)
- *              take no part: nothing is written for them.  NULL: one token per request,
- *              n_tokens == B.
+ *              take no part: nothing is written for them.  NULL: one token per
+ *              request, n_tokens == B.
  *   positions  device int32 [B], position of each request's first new token.
  *   inv_freq   device fp32 [rot_dim / 2] (may be NULL when rot_dim is 0).
  *   rot_dim    a multiple of 8 in [0, head_dim].
