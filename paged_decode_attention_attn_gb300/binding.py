@@ -511,13 +511,16 @@ def kv_append_rows(pool, page_table, positions, rows, status=None, stream=None,
                               _stream_handle(stream)))
 
 
+# A call of few tokens lasts as long as its checks here: each of them reads an
+# attribute once, and what is wrong is looked for again to say so.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call_on(dev: int, stream, fn, *args):
     """``fn(*args, stream handle)`` with device ``dev`` current; ``stream`` None
     is that device's current stream."""
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with torch.cuda.device(dev):
             return _call_on(dev, stream, fn, *args)
     if stream is None:
@@ -532,91 +535,113 @@ def _call_on(dev: int, stream, fn, *args):
         raise PagedAttnError(rc, last_error())
 
 
-def _ptr(t, dtype, dev: int, name: str):
-    """Pointer of a contiguous tensor of ``dtype`` on CUDA device ``dev``."""
+def _ptr(t, dtype, dev: int, name: str, shape=None):
+    """Pointer of a contiguous tensor of ``dtype`` (and ``shape``) on CUDA device
+    ``dev``."""
     try:
-        if t.dtype == dtype and t.get_device() == dev and t.is_contiguous():
+        if (t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and
+                (shape is None or t.shape == shape)):
             return t.data_ptr()
     except AttributeError:
         pass
     _dev(t, dtype, name)                      # raises for what it checks
-    raise ValueError(f"{name} is on {t.device}, the pool on cuda:{dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the pool on cuda:{dev}")
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
-def _token_rows(t, heads, n, d, dev: int, name: str):
-    """Pointer and token stride of bf16 [n][heads][d] activations whose heads
+def _token_rows(t, shape, dev: int, name: str):
+    """Pointer and token stride of bf16 activations [n][heads][d] whose heads
     are dense within a token."""
+    try:
+        if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == dev:
+            n, heads, d = shape
+            st, st_h, st_d = t.stride()
+            if (st_d == 1 or d == 1) and (st_h == d or heads == 1):
+                # the stride of a single token is never used; torch keeps any value there
+                return t.data_ptr(), st if n > 1 else heads * d
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         raise ValueError(f"{name} must be a tensor on cuda:{dev}, as the pool")
-    if t.dtype != torch.bfloat16 or t.shape != (n, heads, d):
-        raise ValueError(f"{name} must be bfloat16 [{n}][{heads}][{d}], got {t.dtype} "
-                         f"{list(t.shape)}")
-    st = t.stride()
-    if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
-        raise ValueError(f"{name} must be dense within a token")
-    # the stride of a single token is never used and torch keeps any value there
-    return t.data_ptr(), st[0] if n > 1 else heads * d
+    if t.dtype != torch.bfloat16 or t.shape != shape:
+        raise ValueError(f"{name} must be bfloat16 {list(shape)}, got {t.dtype} {list(t.shape)}")
+    raise ValueError(f"{name} must be dense within a token")
 
 
-def _pages(pool, dtype) -> int:
-    """CUDA device index of a pool tensor [pages][64][row]."""
-    if not isinstance(pool, torch.Tensor) or not pool.is_cuda:
-        raise ValueError("pool must be a CUDA tensor")
-    if pool.dtype != dtype:
-        raise ValueError(f"pool must be {dtype}, got {pool.dtype}")
-    if pool.dim() != 3 or pool.shape[1] != PAGE_TOKENS or not pool.is_contiguous():
-        raise ValueError("pool must be contiguous [pages][64][2*Hkv*D]")
-    return pool.get_device()
+def _pages(pool, dtype):
+    """CUDA device index, pages and row length of a pool tensor [pages][64][row]."""
+    try:
+        if pool.dtype is dtype and pool.is_contiguous():
+            dev = pool.get_device()
+            n_pages, tokens, row = pool.shape
+            if dev >= 0 and tokens == PAGE_TOKENS:
+                return dev, n_pages, row
+    except (AttributeError, ValueError):
+        pass
+    _dev(pool, dtype, "pool", contiguous=False)
+    raise ValueError("pool must be contiguous [pages][64][2*Hkv*D]")
 
 
-def _check_requests(page_table, positions, cu_tokens):
-    """B and max_pages of the per-request arguments."""
+def _host_ptr(a) -> int:
+    """Address of a numpy array's values."""
+    try:
+        return ctypes.addressof(ctypes.c_char.from_buffer(a))   # a third of .ctypes.data's time
+    except (TypeError, ValueError):                             # read-only, or empty
+        return a.ctypes.data
+
+
+def _check_requests(page_table, positions, cu_tokens, dev):
+    """B, max_pages and the pointers of the per-request arguments."""
+    i32 = torch.int32
+    table = _ptr(page_table, i32, dev, "page_table")
     shape = page_table.shape
-    if len(shape) != 2 or positions.shape != shape[:1]:
-        raise ValueError("page_table must be [B][max_pages] and positions [B]")
-    if cu_tokens is not None and cu_tokens.shape != (shape[0] + 1,):
-        raise ValueError("cu_tokens must be [B + 1]")
-    return shape
+    if len(shape) != 2:
+        raise ValueError("page_table must be [B][max_pages]")
+    bn, max_pages = shape
+    return (bn, max_pages, table, _ptr(positions, i32, dev, "positions", (bn,)),
+            None if cu_tokens is None else _ptr(cu_tokens, i32, dev, "cu_tokens", (bn + 1,)))
 
 
 def _append_rope(fn, dtype, q, k, v, pool, scales, page_table, positions, inv_freq, q_out,
                  cu_tokens, interleaved, status, stream):
-    dev = _pages(pool, dtype)
+    dev, n_pages, row = _pages(pool, dtype)
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be a tensor [tokens][Hkv][D]")
-    n, n_kv, d = k.shape
-    n_pages, _, row = pool.shape
+    kv_shape = k.shape
+    n, n_kv, d = kv_shape
     if row != 2 * n_kv * d:
         raise ValueError(f"pool rows must hold 2*Hkv*D = {2 * n_kv * d} values, got {row}")
-    k_ptr, k_st = _token_rows(k, n_kv, n, d, dev, "k")
-    v_ptr, v_st = _token_rows(v, n_kv, n, d, dev, "v")
+    k_ptr, k_st = _token_rows(k, kv_shape, dev, "k")
+    v_ptr, v_st = _token_rows(v, kv_shape, dev, "v")
     q_ptr = o_ptr = None
     q_st = o_st = hq = 0
     if q is not None:
         if q_out is None:
             raise ValueError("q_out is required with q (q itself rotates in place)")
-        hq = q.shape[1] if q.dim() == 3 else 0
-        q_ptr, q_st = _token_rows(q, hq, n, d, dev, "q")
-        o_ptr, o_st = _token_rows(q_out, hq, n, d, dev, "q_out")
+        q_shape = q.shape
+        hq = q_shape[1] if len(q_shape) == 3 else 0
+        if hq == 0 or q_shape[0] != n or q_shape[2] != d:
+            raise ValueError(f"q must be [{n}][Hq][{d}], got {list(q_shape)}")
+        q_ptr, q_st = _token_rows(q, q_shape, dev, "q")
+        o_ptr, o_st = (q_ptr, q_st) if q_out is q else _token_rows(q_out, q_shape, dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    bn, max_pages = _check_requests(page_table, positions, cu_tokens)
-    i32 = torch.int32
-    cu = None if cu_tokens is None else _ptr(cu_tokens, i32, dev, "cu_tokens")
+    bn, max_pages, table, pos, cu = _check_requests(page_table, positions, cu_tokens, dev)
     inv, rot = None, 0
     if inv_freq is not None:
         inv, rot = _ptr(inv_freq, torch.float32, dev, "inv_freq"), 2 * inv_freq.numel()
-    args = (q_ptr, k_ptr, v_ptr, q_st, k_st, v_st, o_ptr, o_st, cu,
-            _ptr(positions, i32, dev, "positions"), n, bn, hq, n_kv, d, inv, rot,
-            PA_ROPE_INTERLEAVED if interleaved else 0, pool.data_ptr())
-    tail = (n_pages, _ptr(page_table, i32, dev, "page_table"), max_pages,
-            None if status is None else _ptr(status, i32, dev, "status"))
+    st = None if status is None else _ptr(status, torch.int32, dev, "status")
+    flags = PA_ROPE_INTERLEAVED if interleaved else 0
     if scales is None:
-        _call_on(dev, stream, fn, *args, *tail)
-        return
-    if scales.shape != (n_pages, 2 * n_kv, PAGE_TOKENS // SCALE_TOKENS):
-        raise ValueError("scales must be [pages][2*Hkv][4]")
-    _call_on(dev, stream, fn, *args, _ptr(scales, torch.float32, dev, "scales"), *tail)
+        _call_on(dev, stream, fn, q_ptr, k_ptr, v_ptr, q_st, k_st, v_st, o_ptr, o_st, cu, pos, n,
+                 bn, hq, n_kv, d, inv, rot, flags, pool.data_ptr(), n_pages, table, max_pages, st)
+    else:
+        sc = _ptr(scales, torch.float32, dev, "scales",
+                  (n_pages, 2 * n_kv, PAGE_TOKENS // SCALE_TOKENS))
+        _call_on(dev, stream, fn, q_ptr, k_ptr, v_ptr, q_st, k_st, v_st, o_ptr, o_st, cu, pos, n,
+                 bn, hq, n_kv, d, inv, rot, flags, pool.data_ptr(), sc, n_pages, table, max_pages,
+                 st)
 
 
 def kv_append_rope(q, k, v, pool, page_table, positions, inv_freq, q_out=None, cu_tokens=None,
@@ -649,23 +674,20 @@ def kv_gather_q8(pool, scales, page_table, positions, cu_tokens, out, status=Non
     None: one row per request)."""
     if scales is None or scales.dim() != 3:
         raise ValueError("scales must be [pages][2*Hkv][4]")
-    dev = _pages(pool, torch.float8_e4m3fn)
-    n_pages, _, row = pool.shape
+    dev, n_pages, row = _pages(pool, torch.float8_e4m3fn)
     heads = scales.shape[1]
-    if scales.shape != (n_pages, heads, PAGE_TOKENS // SCALE_TOKENS) or heads % 2 or \
-            heads == 0 or row % heads:
+    if heads % 2 or heads == 0 or row % heads:
         raise ValueError("scales must be [pages][2*Hkv][4]")
-    if out.dim() != 2 or out.shape[1] != row:
+    sc = _ptr(scales, torch.float32, dev, "scales",
+              (n_pages, heads, PAGE_TOKENS // SCALE_TOKENS))
+    o = _ptr(out, torch.bfloat16, dev, "out")
+    shape = out.shape
+    if len(shape) != 2 or shape[1] != row:
         raise ValueError("out must be [rows][2*Hkv*D]")
-    bn, max_pages = _check_requests(page_table, positions, cu_tokens)
-    i32 = torch.int32
-    _call_on(dev, stream, lib.kv_gather_q8, pool.data_ptr(),
-             _ptr(scales, torch.float32, dev, "scales"), n_pages,
-             _ptr(page_table, i32, dev, "page_table"), max_pages,
-             None if cu_tokens is None else _ptr(cu_tokens, i32, dev, "cu_tokens"),
-             _ptr(positions, i32, dev, "positions"), out.shape[0], bn, heads // 2, row // heads,
-             _ptr(out, torch.bfloat16, dev, "out"),
-             None if status is None else _ptr(status, i32, dev, "status"))
+    bn, max_pages, table, pos, cu = _check_requests(page_table, positions, cu_tokens, dev)
+    _call_on(dev, stream, lib.kv_gather_q8, pool.data_ptr(), sc, n_pages, table, max_pages, cu, pos,
+             shape[0], bn, heads // 2, row // heads, o,
+             None if status is None else _ptr(status, torch.int32, dev, "status"))
 
 
 def alloc_workspace_q8(B, T, n_q_heads, n_kv_heads, head_dim, device="cuda") -> torch.Tensor:
@@ -683,38 +705,35 @@ def paged_decode_attn_q8_lse(q, pool, scales, page_table, tiles, scale, out, lse
     tiles host int32 [B][T][2]; out fp32 [B][T][Hq][D], lse fp32 [B][T][Hq];
     ``merged_out`` [B][Hq][D] / ``merged_lse`` [B][Hq] receive the merge of
     every request's tiles in the same call."""
-    dev = _pages(pool, torch.float8_e4m3fn)
-    Bn, Hq, D = q.shape
-    n_pages, _, row = pool.shape
-    n_kv = row // (2 * D)
+    dev, n_pages, row = _pages(pool, torch.float8_e4m3fn)
+    q_shape = q.shape
+    if len(q_shape) != 3 or q_shape[2] == 0:
+        raise ValueError("q must be [B][Hq][D]")
+    bn, hq, d = q_shape
+    n_kv = row // (2 * d)
+    if row != 2 * n_kv * d:
+        raise ValueError(f"pool rows must hold 2*Hkv*D values with D = {d}, got {row}")
     if tiles.__class__ is not np.ndarray or tiles.dtype != np.int32 or \
             not tiles.flags.c_contiguous:
         tiles = np.ascontiguousarray(np.asarray(tiles, dtype=np.int32))
-    if tiles.ndim != 3 or tiles.shape[0] != Bn or tiles.shape[2] != 2:
+    if tiles.ndim != 3 or tiles.shape[0] != bn or tiles.shape[2] != 2:
         raise ValueError("tiles must be [B][T][2]")
     T = tiles.shape[1]
-    if row != 2 * n_kv * D or \
-            scales.shape != (n_pages, 2 * n_kv, PAGE_TOKENS // SCALE_TOKENS):
-        raise ValueError("pool must be [pages][64][2*Hkv*D] and scales [pages][2*Hkv][4]")
-    table_shape = page_table.shape
-    if len(table_shape) != 2 or table_shape[0] != Bn:
-        raise ValueError("page_table must be [B][max_pages]")
-    if out.shape != (Bn, T, Hq, D) or lse.shape != (Bn, T, Hq):
-        raise ValueError("out must be [B][T][Hq][D] and lse [B][T][Hq]")
     f32 = torch.float32
+    table = _ptr(page_table, torch.int32, dev, "page_table")
+    table_shape = page_table.shape
+    if len(table_shape) != 2 or table_shape[0] != bn:
+        raise ValueError("page_table must be [B][max_pages]")
     m_ptr = ml_ptr = None
     if merged_out is not None or merged_lse is not None:
-        if merged_out is None or merged_lse is None or merged_out.shape != (Bn, Hq, D) or \
-                merged_lse.shape != (Bn, Hq):
-            raise ValueError("merged_out must be [B][Hq][D] and merged_lse [B][Hq]")
-        m_ptr = _ptr(merged_out, f32, dev, "merged_out")
-        ml_ptr = _ptr(merged_lse, f32, dev, "merged_lse")
+        m_ptr = _ptr(merged_out, f32, dev, "merged_out", q_shape)
+        ml_ptr = _ptr(merged_lse, f32, dev, "merged_lse", (bn, hq))
     _call_on(dev, stream, lib.paged_decode_attn_q8_lse, _ptr(q, torch.bfloat16, dev, "q"),
-             pool.data_ptr(), _ptr(scales, f32, dev, "scales"), n_pages,
-             _ptr(page_table, torch.int32, dev, "page_table"), table_shape[1],
-             tiles.ctypes.data, Bn, T, Hq, n_kv, D, float(scale),
-             _ptr(out, f32, dev, "out"), _ptr(lse, f32, dev, "lse"), m_ptr, ml_ptr,
-             _ptr(workspace, torch.uint8, dev, "workspace"), workspace.numel())
+             pool.data_ptr(),
+             _ptr(scales, f32, dev, "scales", (n_pages, 2 * n_kv, PAGE_TOKENS // SCALE_TOKENS)),
+             n_pages, table, table_shape[1], _host_ptr(tiles), bn, T, hq, n_kv, d, float(scale),
+             _ptr(out, f32, dev, "out", (bn, T, hq, d)), _ptr(lse, f32, dev, "lse", (bn, T, hq)),
+             m_ptr, ml_ptr, _ptr(workspace, torch.uint8, dev, "workspace"), workspace.numel())
 
 
 class Arena:

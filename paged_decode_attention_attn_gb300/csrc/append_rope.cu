@@ -484,7 +484,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
 
 // Rows of an 8-bit pool as bf16 values: `share` warps to a row, a lane turns 16
 // codes of one head at a time and stores them whole (two 16-byte stores a lane
-// took 13.8 us where this takes 10.7, for 8,100 rows of 2,048 codes).
+// took 13.8 us where this takes 10.7, for 8,000 rows of 2,048 codes).
 __global__ void __launch_bounds__(kThreads)
     gather_q8_kernel(const uint8_t* pool, const float* scales, long long pool_pages,
                      const int32_t* page_table, int max_pages, const int32_t* cu,
