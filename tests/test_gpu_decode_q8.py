@@ -490,3 +490,21 @@ def test_requests_that_share_pages(B):
     c.table_dev.copy_(torch.from_numpy(c.table))
     assert c.run(B) == 0
     c.check()
+
+
+@pytest.mark.parametrize("tiles", [2, 8, 9, 37])
+@pytest.mark.parametrize("d", [128, 256])
+def test_merge_of_any_number_of_tiles(B, tiles, d):
+    """Requests whose tiles are all there, partly empty, all empty, and one with
+    a NaN scale in its last tile."""
+    step = 70
+    lengths = [step * tiles, step * (tiles // 2) + 1, 0, step * tiles]
+    cut = [[(min(n, t * step), min(n, t * step + step)) for t in range(tiles)] for n in lengths]
+    c = Case(lengths, cut, hq=6, hkv=2, d=d, seed=50)
+    last = int(c.table[3, (lengths[3] - 1) // 64])
+    c.scales[last, 2 * c.hkv - 1, (lengths[3] - 1) % 64 // 16] = float("nan")   # V of head 1
+    assert c.run(B) == 0
+    c.check([0, 1])
+    assert torch.all(c.merged[2] == 0) and torch.all(c.merged_lse[2] == -float("inf"))
+    assert c.merged[3, 3:].isnan().all()
+    assert c.merged[3, :3].isfinite().all() and c.merged_lse[3, :3].isfinite().all()
