@@ -3,8 +3,8 @@
 The compute path is the C-ABI library ``libpagedattn.so`` (hand-written sm_103a
 CUDA kernels plus the native staging runtime, admission planner and page
 converter); ``binding`` is a thin ctypes layer over it, ``decode`` sequences
-its calls into decode steps (resident, staged, per-tile staged and planned
-routes), ``busmodel`` is the staged route's latency model and ``workloads``
+its calls into decode steps (resident, resident in 8 bits, staged, per-tile
+staged and planned routes), ``busmodel`` is the staged route's latency model and ``workloads``
 holds the seeded synthetic inputs.  ``build`` compiles the library in place.
 """
 
