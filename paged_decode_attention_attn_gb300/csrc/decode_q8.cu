@@ -96,7 +96,7 @@ struct Smem {
   static constexpr int kHalfBytes = kChunks * kChunkBytes;       // K (or V) of a step
   static constexpr int kStages = D == 256 ? 3 : 6;               // of K, and of V
   static constexpr int kV = kStages * kHalfBytes;
-  static constexpr int kPBytes = kPCols * kChunk;
+  static constexpr int kPBytes = kPCols * kStep;
   static constexpr int kQChunkBytes = kQCols * kChunk;
   static constexpr int kQBytes = kChunks * kQChunkBytes;
   static constexpr int kP = 2 * kV;
@@ -421,7 +421,7 @@ __device__ __forceinline__ void drain(const P& p, const View& v, int bar) {
 template <int D, class P>
 __device__ __forceinline__ void score_warp(const P& p, const View& v, uint32_t tmem) {
   using S = Smem<D>;
-  constexpr uint32_t kIdesc = tc::idesc_e4m3(kStep, kQCols, false);
+  constexpr uint32_t kIdesc = tc::idesc_e4m3(kStep, kQCols, false, false);
   Ring<S::kStages> kr;
   Ring<2> sr, qr;
   for_segments(p, [&](const Segment& s, int) {
@@ -461,8 +461,9 @@ __device__ __forceinline__ void score_warp(const P& p, const View& v, uint32_t t
 template <int D, class P>
 __device__ __forceinline__ void product_warp(const P& p, const View& v, uint32_t tmem) {
   using S = Smem<D>;
-  constexpr uint32_t kIdesc = tc::idesc_e4m3(kChunk, kPCols, true);
-  constexpr uint32_t kSlice = 32 * kChunk >> 4;   // 32 tokens of a chunk, in descriptor units
+  constexpr uint32_t kIdesc = tc::idesc_e4m3(kChunk, kPCols, true, true);
+  // 32 tokens of a chunk, and of the probabilities, in descriptor units
+  constexpr uint32_t kSlice = 32 * kChunk >> 4, kPSlice = 32 * kPCols >> 4;
   Ring<S::kStages> vr;
   Ring<2> pr;
   for_segments(p, [&](const Segment& s, int) {
@@ -474,17 +475,17 @@ __device__ __forceinline__ void product_warp(const P& p, const View& v, uint32_t
         return false;
       tc::fence_after();
       const uint64_t a = tc::desc_sw128(v.addr + S::kV + vr.i * S::kHalfBytes);
-      const uint64_t b = tc::desc_sw128(v.addr + S::kP + pr.i * S::kPBytes);
+      const uint64_t b = tc::desc_sw32(v.addr + S::kP + pr.i * S::kPBytes);
       const uint32_t d = tmem + 2 * kQCols + pr.i * S::kChunks * kPCols;
       if (elect()) {
 #pragma unroll
         for (int c = 0; c < S::kChunks; ++c) {
           const uint64_t ac = a + (c * S::kChunkBytes >> 4);
           tc::mma_e4m3(d + c * kPCols, ac, b, kIdesc, false);
-          tc::mma_e4m3(d + c * kPCols, ac + kSlice, b + 2, kIdesc, true);
+          tc::mma_e4m3(d + c * kPCols, ac + kSlice, b + kPSlice, kIdesc, true);
           if (two) {
-            tc::mma_e4m3(d + c * kPCols, ac + 2 * kSlice, b + 4, kIdesc, true);
-            tc::mma_e4m3(d + c * kPCols, ac + 3 * kSlice, b + 6, kIdesc, true);
+            tc::mma_e4m3(d + c * kPCols, ac + 2 * kSlice, b + 2 * kPSlice, kIdesc, true);
+            tc::mma_e4m3(d + c * kPCols, ac + 3 * kSlice, b + 3 * kPSlice, kIdesc, true);
           }
         }
         tc::commit(v.bar(S::kOFull + pr.i));
@@ -760,8 +761,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
         for (int h = 0; h < kMaxG; ++h) to[h] = ref[h];
         ptx::mbar_arrive(v.bar(S::kRefFull + it % kRefs));
       }
-      const uint32_t prow = v.addr + S::kP + group * S::kPBytes + (tok & 15);
-      const int chunk = tok >> 4;
+      uint32_t codes[2 * kParts];   // this token's row: kParts times the eight heads
 #pragma unroll
       for (int h = 0; h < kMaxG; h += 2) {
         float w[2];
@@ -774,15 +774,8 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
           const uint32_t c = fp8::pack2(w[0], w[1]);
-          const int row = part * kMaxG + h;
-          asm volatile("st.shared.u8 [%0], %1;" ::"r"(prow + row * kChunk +
-                                                       ((chunk ^ (row & 7)) << 4)),
-                       "r"(c)
-                       : "memory");
-          asm volatile("st.shared.u8 [%0], %1;" ::"r"(prow + (row + 1) * kChunk +
-                                                       ((chunk ^ ((row + 1) & 7)) << 4)),
-                       "r"(c >> 8)
-                       : "memory");
+          uint32_t& to = codes[2 * part + h / 4];
+          to = h % 4 ? to | c << 16 : c;
           if (part + 1 < kParts) {
             const float2 f = fp8::unpack2(c);
             w[0] = (w[0] - f.x) * kPartRatio;
@@ -790,6 +783,14 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
           }
         }
       }
+      const uint32_t prow = v.addr + S::kP + group * S::kPBytes + tok * kPCols;
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         prow + ((half << 4) ^ ((tok & 4) << 2))),
+                     "r"(codes[4 * half]), "r"(codes[4 * half + 1]), "r"(codes[4 * half + 2]),
+                     "r"(codes[4 * half + 3])
+                     : "memory");
       if (loaded && !live) {
         // A NaN code in a row outside the tile would reach the product (0 x NaN).
         const int stage = it % S::kStages;

@@ -17,11 +17,20 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
          (2ull << 61);
 }
 
-// Instruction descriptor: e4m3 x e4m3 -> fp32, M x N, B K-major, A K-major or
-// (a_mn) MN-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n, bool a_mn) {
-  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | ((uint32_t)(n >> 3) << 17) |
-         ((uint32_t)(m >> 4) << 24);
+// The same for a 32-byte-swizzled MN-major operand (its tile 256-byte aligned):
+// rows of 32 bytes, a K index with 32 values, groups of eight rows 256 bytes
+// apart; the two 16-byte halves of rows 4-7 of a group change places.
+__device__ __forceinline__ uint64_t desc_sw32(uint32_t addr) {
+  constexpr uint64_t kGroup = 256 >> 4;
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | (kGroup << 16) | (kGroup << 32) | (1ull << 46) |
+         (6ull << 61);
+}
+
+// Instruction descriptor: e4m3 x e4m3 -> fp32, M x N, each operand K-major or
+// (a_mn, b_mn) MN-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // D[tmem] (+)= A B over 32 values of K; issued by one thread.
