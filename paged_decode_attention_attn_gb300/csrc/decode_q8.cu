@@ -71,7 +71,6 @@ constexpr int kGroupWarps = 4, kOutWarps = 4;
 constexpr int kOut = kOutWarps * 32;
 constexpr int kSoftmaxWarps = kGroups * kGroupWarps;
 constexpr int kTmaWarp = 12, kScoreWarp = 13, kProductWarp = 14;
-constexpr int kScaleCopies = 4;             // lanes that copy a step's scales
 constexpr int kThreads = 32 * 16;           // the last warp: per segment
 constexpr int kSegmentCharge = 6;           // pages charged per unit start
 constexpr int kWholePages = 16;             // units this short are not split while SMs are idle
@@ -101,10 +100,12 @@ struct Smem {
   static constexpr int kQBytes = kChunks * kQChunkBytes;
   static constexpr int kP = 2 * kV;
   static constexpr int kQ = kP + 2 * kPBytes;
-  // Scales and poison marks of a step come with its K.  The K of step i + kStages
-  // is loaded once the scores of step i are done, which the softmax of step i - 2
-  // (it has read its scales) precedes: kStages + 2 slots.
-  static constexpr int kSlots = kStages + 2;
+  // Scales come for up to 16 steps at a time, a page of them per lane of the TMA
+  // warp.  When those of steps i .. i + 15 are asked for, the K of step i - 1 is,
+  // so the scores of step i - 1 - kStages are done, and the softmax of the step
+  // two before it has read its scales: 32 slots hold them all.
+  static constexpr int kSlots = 32;
+  static_assert(kStages + 3 <= 17, "slots of scales");
   static constexpr int kScales = kQ + 2 * kQBytes;               // [slot][K | V][block]
   static constexpr int kScaleBytes = 2 * kStepBlocks * 4;
   static constexpr int kQScale = kScales + kSlots * kScaleBytes;  // [2][kMaxG]
@@ -344,12 +345,10 @@ __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtens
     ++values;
     return true;
   };
-  const int lane_page = (lane >> 1) & 1, lane_kind = lane & 1;   // scale copies of lanes 0-3
   for_segments(p, [&](const Segment& s, int seg) {
     if (seg == 0) ptx::grid_dependency_wait();
     const int32_t* prow = p.page_table + (size_t)s.b * p.max_pages + s.U.tok_start / kPage;
-    const float* scales = p.scales + ((size_t)lane_kind * p.Hkv + s.g) * kBlocksPerPage;
-    const int scale_stride = 2 * p.Hkv * kBlocksPerPage;
+    const float* scales = p.scales + s.g * kBlocksPerPage;   // K's; V's lie Hkv heads behind
     int next_pid = s.lo + lane < s.hi ? __ldg(prow + s.lo + lane) : 0;
     for (int base = s.lo; base < s.hi; base += 32) {
       const int cnt = min(32, s.hi - base);
@@ -358,6 +357,13 @@ __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtens
       const uint32_t bad_pages = __ballot_sync(0xffffffffu, bad);
       const int my_pid = bad ? 0 : next_pid;
       if (bad) atomicOr(p.status, PA_STATUS_BAD_PAGE);
+      if (lane < cnt) {
+        const float* src = scales + (size_t)my_pid * (2 * p.Hkv * kBlocksPerPage);
+        const uint32_t dst = v.addr + S::kScales +
+                             (keys + (lane >> 1)) % S::kSlots * S::kScaleBytes + (lane & 1) * 16;
+        copy16(dst, src);
+        copy16(dst + kStepBlocks * 4, src + p.Hkv * kBlocksPerPage);
+      }
       if (base + 32 + lane < s.hi) next_pid = __ldg(prow + base + 32 + lane);
       for (int j = 0; j < cnt; j += 2) {
         const int pid0 = __shfl_sync(0xffffffffu, my_pid, j);
@@ -371,14 +377,7 @@ __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtens
             ptx::mbar_arrive_expect_tx(full, n * S::kChunks * S::kPageBytes);
             boxes(v.addr + kr.i * S::kHalfBytes, full, s.g * D, pid0 * kPage, pid1 * kPage, n);
           }
-          // The scales (K's and V's of each page, 16 bytes) by four lanes.
-          if (lane < kScaleCopies) {
-            if (lane_page < n)
-              copy16(v.addr + S::kScales + slot.i * S::kScaleBytes + lane_kind * kStepBlocks * 4 +
-                         lane_page * 16,
-                     scales + (size_t)(lane_page ? pid1 : pid0) * scale_stride);
-            arrive_after_copies(full);
-          }
+          arrive_after_copies(full);   // every lane's scales (of this step and earlier ones)
           __syncwarp();
         }
         kr.next();
@@ -398,6 +397,7 @@ __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtens
   if (lane == 0) ptx::launch_dependents();
   // The copies issued land before the CTA can exit, whatever became of the
   // other warps.
+  asm volatile("cp.async.wait_all;" ::: "memory");
   for (int k = max(0, keys - S::kStages); k < keys; ++k)
     ptx::mbar_wait_bounded(v.bar(S::kKFull + k % S::kStages), (k / S::kStages) & 1,
                            p.wait_limit_ns);
@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kNumBars; ++i) {
       int n = 1;
-      if (i < S::kKEmpty) n = 1 + kScaleCopies;                       // K full
+      if (i < S::kKEmpty) n = 1 + 32;                                 // K full: and scales
       if (i >= S::kSFull && i < S::kSEmpty) n = 2;                    // products and scales
       if (i >= S::kSEmpty && i < S::kOFull) n = kGroupWarps;          // S empty, P full
       if (i >= S::kOEmpty && i < S::kQFull) n = kOutWarps;
