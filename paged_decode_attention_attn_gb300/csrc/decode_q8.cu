@@ -310,40 +310,44 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// Warp 12: the pages' K (with the step's scales) and V into their rings.  V
-// follows a step behind K, in the order in which the stages become free.
+// Warp 12: the pages' K (with the scales) and V into their rings, V kLag steps
+// behind K.  At 256 dims (three stages) V follows two steps behind, as a product
+// does its scores, and one wait and one branch serve both; at 128 (six stages) it
+// follows one step behind, with a wait of its own.  Together / apart: 1 x 262,144
+// tokens 82.9 / 84.8 us, 64 x 2,048 41.1 / 41.8, 4 x 31,744 44.7 / 45.0, and at
+// 128 dims 16 x 8,192 45.1 / 43.9, 256 x 512 58.2 / 55.9.  (At 128 dims a step
+// lasts about as long as this warp's instructions for it.)
 // ---------------------------------------------------------------------------
+struct StepPages {
+  int row0, row1, n, col;   // first rows of its pages in the pool, pages, V's column
+};
+
 template <int D, class P>
 __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtensorMap* tmap,
                                          int lane) {
   using S = Smem<D>;
+  constexpr bool kTogether = D == 256;
+  constexpr int kLag = kTogether ? 2 : 1;
   Ring<S::kStages> kr, vr;
   Ring<S::kSlots> slot;
   int keys = 0, values = 0;            // steps loaded
-  int row0 = 0, row1 = 0, n_last = 0, col_last = 0;   // the step whose V is next
+  StepPages late[kLag] = {};           // the steps whose V is next
   const uint64_t pol = ptx::policy_evict_first();   // every page is read once
-  auto boxes = [&](uint32_t dst, uint32_t full, int col, int r0, int r1, int n) {
+  const int stall = blockIdx.x == 0 ? p.stall_iteration : -1;
+  auto boxes = [&](uint32_t dst, uint32_t full, int col, const StepPages& at) {
+    ptx::mbar_arrive_expect_tx(full, at.n * S::kChunks * S::kPageBytes);
 #pragma unroll
     for (int c = 0; c < S::kChunks; ++c)
-      ptx::tma_load_2d_hint(dst + c * S::kChunkBytes, tmap, col + c * kChunk, r0, full, pol);
-    if (n > 1) {
+      ptx::tma_load_2d_hint(dst + c * S::kChunkBytes, tmap, col + c * kChunk, at.row0, full, pol);
+    if (at.n > 1) {
 #pragma unroll
       for (int c = 0; c < S::kChunks; ++c)
-        ptx::tma_load_2d_hint(dst + c * S::kChunkBytes + S::kPageBytes, tmap, col + c * kChunk, r1,
-                              full, pol);
+        ptx::tma_load_2d_hint(dst + c * S::kChunkBytes + S::kPageBytes, tmap, col + c * kChunk,
+                              at.row1, full, pol);
     }
   };
-  auto load_values = [&]() {
-    if (!warp_wait(p, v, S::kVEmpty + vr.i, vr.phase ^ 1)) return false;
-    if (elect()) {
-      const uint32_t full = v.bar(S::kVFull + vr.i);
-      ptx::mbar_arrive_expect_tx(full, n_last * S::kChunks * S::kPageBytes);
-      boxes(v.addr + S::kV + vr.i * S::kHalfBytes, full, col_last, row0, row1, n_last);
-    }
-    __syncwarp();
-    vr.next();
-    ++values;
-    return true;
+  auto load_values = [&]() {   // by one lane, into a free stage
+    boxes(v.addr + S::kV + vr.i * S::kHalfBytes, v.bar(S::kVFull + vr.i), late[0].col, late[0]);
   };
   for_segments(p, [&](const Segment& s, int seg) {
     if (seg == 0) ptx::grid_dependency_wait();
@@ -366,32 +370,59 @@ __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtens
       }
       if (base + 32 + lane < s.hi) next_pid = __ldg(prow + base + 32 + lane);
       for (int j = 0; j < cnt; j += 2) {
-        const int pid0 = __shfl_sync(0xffffffffu, my_pid, j);
-        const int pid1 = __shfl_sync(0xffffffffu, my_pid, (j + 1) & 31);
-        const int n = min(2, cnt - j);
-        if (!warp_wait(p, v, S::kKEmpty + kr.i, kr.phase ^ 1)) return false;
+        const StepPages now = {__shfl_sync(0xffffffffu, my_pid, j) * kPage,
+                               __shfl_sync(0xffffffffu, my_pid, (j + 1) & 31) * kPage,
+                               min(2, cnt - j), (p.Hkv + s.g) * D};
+        const bool with_values = keys >= kLag;
+        if constexpr (kTogether) {
+          const int kbar = S::kKEmpty + kr.i, vbar = with_values ? S::kVEmpty + vr.i : kbar;
+          const uint32_t kpar = kr.phase ^ 1, vpar = with_values ? vr.phase ^ 1 : kpar;
+          const bool kfree = ptx::mbar_try_wait(v.bar(kbar), kpar);
+          const bool vfree = ptx::mbar_try_wait(v.bar(vbar), vpar);
+          if (!__all_sync(0xffffffffu, kfree && vfree) &&
+              (!warp_wait(p, v, kbar, kpar) || !warp_wait(p, v, vbar, vpar)))
+            return false;
+        } else {
+          if (!warp_wait(p, v, S::kKEmpty + kr.i, kr.phase ^ 1)) return false;
+        }
         const uint32_t full = v.bar(S::kKFull + kr.i);
-        if (keys != p.stall_iteration || blockIdx.x != 0) {
+        if (keys != stall) {
           if (elect()) {
             v.poison[slot.i] = (bad_pages >> j) & 3;   // set before the arrival that publishes it
-            ptx::mbar_arrive_expect_tx(full, n * S::kChunks * S::kPageBytes);
-            boxes(v.addr + kr.i * S::kHalfBytes, full, s.g * D, pid0 * kPage, pid1 * kPage, n);
+            boxes(v.addr + kr.i * S::kHalfBytes, full, s.g * D, now);
+            if (kTogether && with_values) load_values();
           }
-          arrive_after_copies(full);   // every lane's scales (of this step and earlier ones)
-          __syncwarp();
+        } else if (kTogether && with_values && elect()) {
+          load_values();
         }
+        arrive_after_copies(full);   // every lane's scales (of this step and earlier ones)
+        __syncwarp();
         kr.next();
         slot.next();
-        if (keys++ > 0 && !load_values()) return false;
-        row0 = pid0 * kPage;
-        row1 = pid1 * kPage;
-        n_last = n;
-        col_last = (p.Hkv + s.g) * D;
+        ++keys;
+        if (with_values) {
+          if constexpr (!kTogether) {
+            if (!warp_wait(p, v, S::kVEmpty + vr.i, vr.phase ^ 1)) return false;
+            if (elect()) load_values();
+            __syncwarp();
+          }
+          vr.next();
+          ++values;
+        }
+        if (kLag > 1) late[0] = late[kLag - 1];
+        late[kLag - 1] = now;
       }
     }
     return true;
   });
-  if (values < keys) load_values();
+  if (keys < kLag) late[0] = late[kLag - 1];
+  while (values < keys && warp_wait(p, v, S::kVEmpty + vr.i, vr.phase ^ 1)) {
+    if (elect()) load_values();
+    __syncwarp();
+    vr.next();
+    ++values;
+    late[0] = late[kLag - 1];
+  }
   // Every page of this CTA is requested: the next kernel in the stream may
   // start its prologue.
   if (lane == 0) ptx::launch_dependents();
