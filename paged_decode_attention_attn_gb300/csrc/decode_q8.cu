@@ -106,7 +106,8 @@ struct Smem {
   // two before it has read its scales: 32 slots hold them all.
   static constexpr int kSlots = 32;
   static_assert(kStages + 3 <= 17, "slots of scales");
-  static constexpr int kScales = kQ + 2 * kQBytes;               // [slot][K | V][block]
+  static constexpr int kQRaw = kQ + 2 * kQBytes;                 // [head][dim] of a later segment
+  static constexpr int kScales = kQRaw + kMaxG * D * 2;          // [slot][K | V][block]
   static constexpr int kScaleBytes = 2 * kStepBlocks * 4;
   static constexpr int kQScale = kScales + kSlots * kScaleBytes;  // [2][kMaxG]
   static constexpr int kRef = kQScale + 2 * kMaxG * 4;             // [kRefs][kMaxG]
@@ -292,10 +293,15 @@ __device__ __forceinline__ bool elect() {
   return r != 0;
 }
 
-// 16 bytes from global to shared memory, and an arrival at `bar` once the
-// thread's copies have landed.
+// 16 bytes (copy_own: a value of 8 or 16) from global to shared memory, and an
+// arrival at `bar` once the thread's copies have landed.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <class T>
+__device__ __forceinline__ void copy_own(uint32_t dst, const T* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(sizeof(T))
+               : "memory");
 }
 __device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -535,64 +541,55 @@ __device__ __forceinline__ void product_warp(const P& p, const View& v, uint32_t
 // q of a segment as hi and lo parts, and its scales: by the output warps, two
 // heads each, for a CTA's first segment (on one warp it takes 3.7 us, the
 // longest part of a launch's start), by warp 15 ahead of time for the others.
+// That warp loops over the heads, from shared memory: code that runs once per
+// segment is fetched anew each time, and eight heads unrolled were 11 KB of it
+// (252 requests of 103 / 256 tokens 27.2 / 30.8 -> 23.8 / 26.7 us).
 // ---------------------------------------------------------------------------
 template <int D>
 using QVec = typename std::conditional<D == 256, uint4, uint2>::type;   // D / 32 dims per lane
 
-template <int D, int kHeads, class P>
-__device__ __forceinline__ void load_q(const P& p, const Segment& s, int h0, int lane,
-                                       QVec<D> (&raw)[kHeads]) {
-  const __nv_bfloat16* src = p.q + ((size_t)s.b * p.Hq + s.g * p.G + h0) * D + lane * (D / 32);
-#pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
-    raw[h] = QVec<D>{};
-    if (h0 + h < p.G) raw[h] = __ldg(reinterpret_cast<const QVec<D>*>(src + h * D));
-  }
+// A lane's dims of head h of a segment.
+template <int D, class P>
+__device__ __forceinline__ const QVec<D>* q_of(const P& p, const Segment& s, int h, int lane) {
+  return reinterpret_cast<const QVec<D>*>(
+      p.q + ((size_t)s.b * p.Hq + s.g * p.G + h) * D + lane * (D / 32));
 }
 
-// The first `heads` (the others' columns are zero already).
-template <int D, int kHeads, class P>
-__device__ __forceinline__ void convert_q(const P& p, const View& v, const QVec<D> (&raw)[kHeads],
-                                          int buffer, int h0, int heads, int lane) {
+template <int D, class P>
+__device__ __forceinline__ void convert_head(const P& p, const View& v, const QVec<D>& raw,
+                                             int buffer, int h, int lane) {
   using S = Smem<D>;
   constexpr int kDims = D / 32;             // dims per lane
-  float* qscale = reinterpret_cast<float*>(v.base + S::kQScale) + buffer * kMaxG + h0;
   const int col = lane * kDims;
-  const uint32_t buf = v.addr + S::kQ + buffer * S::kQBytes + col / kChunk * S::kQChunkBytes +
-                       (col & 15);
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
+  unsigned amax = 0;
 #pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
-    if (h % 2 == 0 && h >= heads) break;
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[h]);
-    unsigned amax = 0;
+  for (int k = 0; k < kDims / 2; ++k)
+    amax = max(amax, max(w[k] << 16 & 0x7fffffffu, w[k] & 0x7fff0000u));
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  // Largest value to [128, 256).  A head with a NaN or an infinity becomes
+  // NaN (its scores would be).
+  const int e = amax ? min(7 - ((int)(amax >> 23) - 127), 120) : 0;
+  const float up = amax < 0x7f800000u ? ptx::pow2i(e) : __int_as_float(0x7fc00000);
+  if (lane == 0)
+    reinterpret_cast<float*>(v.base + S::kQScale)[buffer * kMaxG + h] =
+        p.scale_log2 * ptx::pow2i(-e);
+  const uint32_t at = v.addr + S::kQ + buffer * S::kQBytes + col / kChunk * S::kQChunkBytes +
+                      (col & 15) + h * kChunk + (((col % kChunk >> 4) ^ h) << 4);
 #pragma unroll
-    for (int k = 0; k < kDims / 2; ++k)
-      amax = max(amax, max(w[k] << 16 & 0x7fffffffu, w[k] & 0x7fff0000u));
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    // Largest value to [128, 256).  A head with a NaN or an infinity becomes
-    // NaN (its scores would be).
-    const int e = amax ? min(7 - ((int)(amax >> 23) - 127), 120) : 0;
-    const float up = amax < 0x7f800000u ? ptx::pow2i(e) : __int_as_float(0x7fc00000);
-    if (lane == 0) qscale[h] = p.scale_log2 * ptx::pow2i(-e);
-    const uint32_t at = buf + (h0 + h) * kChunk + (((col % kChunk >> 4) ^ (h0 + h)) << 4);
-#pragma unroll
-    for (int k = 0; k < kDims / 4; ++k) {
-      const float z0 = ptx::bf16_lo_to_f32(w[2 * k]) * up;
-      const float z1 = ptx::bf16_hi_to_f32(w[2 * k]) * up;
-      const float z2 = ptx::bf16_lo_to_f32(w[2 * k + 1]) * up;
-      const float z3 = ptx::bf16_hi_to_f32(w[2 * k + 1]) * up;
-      const uint32_t hi = fp8::pack4(z0, z1, z2, z3);
-      float f[4];
-      fp8::unpack4(hi, f);
-      const uint32_t lo = fp8::pack4((z0 - f[0]) * 16.f, (z1 - f[1]) * 16.f, (z2 - f[2]) * 16.f,
-                                     (z3 - f[3]) * 16.f);
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * k), "r"(hi) : "memory");
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + kMaxG * kChunk + 4 * k), "r"(lo)
-                   : "memory");
-    }
+  for (int k = 0; k < kDims / 4; ++k) {
+    const float z0 = ptx::bf16_lo_to_f32(w[2 * k]) * up;
+    const float z1 = ptx::bf16_hi_to_f32(w[2 * k]) * up;
+    const float z2 = ptx::bf16_lo_to_f32(w[2 * k + 1]) * up;
+    const float z3 = ptx::bf16_hi_to_f32(w[2 * k + 1]) * up;
+    const uint32_t hi = fp8::pack4(z0, z1, z2, z3);
+    float f[4];
+    fp8::unpack4(hi, f);
+    const uint32_t lo = fp8::pack4((z0 - f[0]) * 16.f, (z1 - f[1]) * 16.f, (z2 - f[2]) * 16.f,
+                                   (z3 - f[3]) * 16.f);
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * k), "r"(hi) : "memory");
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + kMaxG * kChunk + 4 * k), "r"(lo) : "memory");
   }
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
 }
 
 // ---------------------------------------------------------------------------
@@ -673,23 +670,31 @@ __device__ __forceinline__ void helper_warp(const P& p, const View& v, int lane)
       if (p.lse2) p.lse2[row + lane] = -INFINITY;
     }
   }
-  // q is loaded two segments ahead and converted one ahead (the first segment's
-  // is the output warps').
+  // q is loaded two segments ahead (a lane's dims by that lane, so no lane waits
+  // for another) and converted one ahead (the first segment's by the output warps).
   Segments<P> ahead(p);
   Segment s;
-  QVec<D> raw[kMaxG];
+  QVec<D>* staged = reinterpret_cast<QVec<D>*>(v.base + S::kQRaw) + lane;   // [head][lane]
   bool more = ahead.next(s);
   auto load_next = [&]() {
     more = more && ahead.next(s);
-    if (more) load_q<D>(p, s, 0, lane, raw);
+    if (!more) return;
+#pragma unroll 1
+    for (int h = 0; h < p.G; ++h)
+      copy_own(ptx::smem_addr(staged + 32 * h), q_of<D>(p, s, h, lane));
   };
   int heads = kMaxG;   // the first conversion clears the columns without a head
   auto convert_next = [&]() {
     qr.next();
     if (!more) return true;
     if (!warp_wait(p, v, S::kQEmpty + qr.i, qr.phase ^ 1)) return false;
-    convert_q<D>(p, v, raw, qr.i, 0, heads, lane);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+    for (int h = 0; h < heads; ++h)
+      convert_head<D>(p, v, h < p.G ? staged[32 * h] : QVec<D>{}, qr.i, h, lane);
     heads = p.G;
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
     if (lane < kOutWarps) ptx::mbar_arrive(v.bar(S::kQFull + qr.i));
     load_next();
     return true;
@@ -882,8 +887,15 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
   for_segments(p, [&](const Segment& s, int) {
     constexpr int kHeads = kMaxG / kOutWarps;
     QVec<D> raw[kHeads];
-    load_q<D>(p, s, warp * kHeads, lane, raw);
-    convert_q<D>(p, v, raw, 0, warp * kHeads, kHeads, lane);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      raw[i] = QVec<D>{};
+      if (warp * kHeads + i < p.G) raw[i] = __ldg(q_of<D>(p, s, warp * kHeads + i, lane));
+    }
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) convert_head<D>(p, v, raw[i], 0, warp * kHeads + i, lane);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
     if (lane == 0) ptx::mbar_arrive(v.bar(S::kQFull));
     return false;   // the first segment's
   });
