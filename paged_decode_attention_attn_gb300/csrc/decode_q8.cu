@@ -115,7 +115,7 @@ struct Smem {
   static constexpr int kSegRef = kSegL + 2 * kSoftmaxWarps * kMaxG * 4;   // [2][group][kMaxG]
   static constexpr int kWarpMax = kSegRef + 2 * kGroups * kMaxG * 4;      // [warp][kMaxG]
   static constexpr int kFactor = kWarpMax + kSoftmaxWarps * kMaxG * 4;    // [2][kMaxG]
-  static constexpr int kBars = kFactor + 2 * kMaxG * 4;
+  static constexpr int kBars = kFactor + 2 * 3 * kMaxG * 4;
   // mbarriers: full, empty per K and V stage; S, P, product, q, sums: full and
   // empty; all of a warp's products done; reference slots written; a segment's
   // factors: full and empty
@@ -130,6 +130,13 @@ struct Smem {
   static constexpr int kUsed = kMisc + (kSlots + 2 * kGroups + 6) * 4;
   static constexpr int kAlloc = kUsed + 1024;
   static_assert(kAlloc <= 232448, "shared memory budget");
+};
+
+// A unit as the kernel reads it: three 8-byte loads.
+struct alignas(8) DevUnit {
+  int32_t page_first, bt, tok_start, tok_end;
+  uint16_t g, part_base;
+  int16_t n_parts, first_cta;
 };
 
 template <int kMaxUnits>
@@ -162,7 +169,7 @@ struct Params {
   float* lse2;
   int32_t starts[kMaxGrid + 1];      // CTA k takes flattened pages [k], [k + 1)
   int16_t first_unit[kMaxGrid + 1];  // and its first unit
-  Unit units[kMaxUnits];
+  DevUnit units[kMaxUnits];
 };
 static_assert(sizeof(Params<kMaxUnitsLarge>) <= 32764, "kernel parameters too large");
 
@@ -225,8 +232,8 @@ __device__ __forceinline__ bool warp_wait(const P& p, const View& v, int bar, ui
 
 // A CTA's part of a unit: its pages [lo, hi).
 struct Segment {
-  Unit U;
-  int u, pf, lo, hi, bt, b, g, first_tok;
+  DevUnit U;
+  int u, pf, lo, hi, bt, g, first_tok;
   __device__ __forceinline__ int steps() const { return (hi - lo + 1) / 2; }
   __device__ __forceinline__ bool whole() const { return U.n_parts == 1; }
   // the segment's partial slot, where the unit has several
@@ -237,6 +244,11 @@ struct Segment {
 
 // This CTA's segments, one after the other.
 template <class P>
+__device__ __forceinline__ int request_of(const P& p, int bt) {
+  return p.T == 1 ? bt : bt / p.T;
+}
+
+template <class P>
 struct Segments {
   const P& p;
   int start, end, u;
@@ -245,7 +257,8 @@ struct Segments {
         u(params.first_unit[blockIdx.x]) {}
   __device__ __forceinline__ bool next(Segment& s) {
     for (; u < p.n_full && p.units[u].page_first < end; ++u) {
-      s.U = p.units[u];
+      const DevUnit& from = p.units[u];
+      s.U = from;
       const int np = unit_pages(s.U.tok_start, s.U.tok_end);
       s.pf = s.U.page_first;
       s.lo = max(start, s.pf) - s.pf;
@@ -254,7 +267,6 @@ struct Segments {
       s.u = u++;
       s.bt = s.U.bt;
       s.g = s.U.g;
-      s.b = p.T == 1 ? s.bt : s.bt / p.T;
       s.first_tok = s.U.tok_start / kPage * kPage;
       return true;
     }
@@ -357,7 +369,7 @@ __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtens
   };
   for_segments(p, [&](const Segment& s, int seg) {
     if (seg == 0) ptx::grid_dependency_wait();
-    const int32_t* prow = p.page_table + (size_t)s.b * p.max_pages + s.U.tok_start / kPage;
+    const int32_t* prow = p.page_table + (size_t)request_of(p, s.bt) * p.max_pages + s.U.tok_start / kPage;
     const float* scales = p.scales + s.g * kBlocksPerPage;   // K's; V's lie Hkv heads behind
     int next_pid = s.lo + lane < s.hi ? __ldg(prow + s.lo + lane) : 0;
     for (int base = s.lo; base < s.hi; base += 32) {
@@ -552,7 +564,14 @@ using QVec = typename std::conditional<D == 256, uint4, uint2>::type;   // D / 3
 template <int D, class P>
 __device__ __forceinline__ const QVec<D>* q_of(const P& p, const Segment& s, int h, int lane) {
   return reinterpret_cast<const QVec<D>*>(
-      p.q + ((size_t)s.b * p.Hq + s.g * p.G + h) * D + lane * (D / 32));
+      p.q + ((size_t)request_of(p, s.bt) * p.Hq + s.g * p.G + h) * D + lane * (D / 32));
+}
+
+__device__ __forceinline__ void store_shared(uint32_t at, const uint32_t (&x)[1]) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(x[0]) : "memory");
+}
+__device__ __forceinline__ void store_shared(uint32_t at, const uint32_t (&x)[2]) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(x[0]), "r"(x[1]) : "memory");
 }
 
 template <int D, class P>
@@ -576,29 +595,30 @@ __device__ __forceinline__ void convert_head(const P& p, const View& v, const QV
         p.scale_log2 * ptx::pow2i(-e);
   const uint32_t at = v.addr + S::kQ + buffer * S::kQBytes + col / kChunk * S::kQChunkBytes +
                       (col & 15) + h * kChunk + (((col % kChunk >> 4) ^ h) << 4);
+  // z = q * up is exact in fp16 (8 significant bits), and so is what hi leaves.
+  uint32_t hi[kDims / 4], lo[kDims / 4];
 #pragma unroll
-  for (int k = 0; k < kDims / 4; ++k) {
-    const float z0 = ptx::bf16_lo_to_f32(w[2 * k]) * up;
-    const float z1 = ptx::bf16_hi_to_f32(w[2 * k]) * up;
-    const float z2 = ptx::bf16_lo_to_f32(w[2 * k + 1]) * up;
-    const float z3 = ptx::bf16_hi_to_f32(w[2 * k + 1]) * up;
-    const uint32_t hi = fp8::pack4(z0, z1, z2, z3);
-    float f[4];
-    fp8::unpack4(hi, f);
-    const uint32_t lo = fp8::pack4((z0 - f[0]) * 16.f, (z1 - f[1]) * 16.f, (z2 - f[2]) * 16.f,
-                                   (z3 - f[3]) * 16.f);
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * k), "r"(hi) : "memory");
-    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + kMaxG * kChunk + 4 * k), "r"(lo) : "memory");
+  for (int k = 0; k < kDims / 2; ++k) {
+    const __half2 z = __floats2half2_rn(ptx::bf16_lo_to_f32(w[k]) * up,
+                                        ptx::bf16_hi_to_f32(w[k]) * up);
+    const uint32_t a = fp8::pack2(z);
+    const uint32_t b = fp8::pack2(
+        __hmul2(__hsub2(z, fp8::unpack2_half(a)), __float2half2_rn(16.f)));
+    hi[k / 2] = k % 2 ? hi[k / 2] | a << 16 : a;
+    lo[k / 2] = k % 2 ? lo[k / 2] | b << 16 : b;
   }
+  store_shared(at, hi);
+  store_shared(at + kMaxG * kChunk, lo);
 }
 
 // ---------------------------------------------------------------------------
 // Warp 15: what is not done per step: q ahead of its segment, the factors of a
 // segment's outputs (and its log-sum-exp) from its sums, and empty units.
 // ---------------------------------------------------------------------------
+// slot: the segment's partial slot, negative where it is a whole unit.
 template <int D, class P>
-__device__ __forceinline__ bool segment_factors(const P& p, const View& v, const Segment& s,
-                                                Ring<2>& r, int lane) {
+__device__ __forceinline__ bool segment_factors(const P& p, const View& v, int slot, Ring<2>& r,
+                                                int lane) {
   using S = Smem<D>;
   if (!warp_wait(p, v, S::kFEmpty + r.i, r.phase ^ 1) ||
       !warp_wait(p, v, S::kLFull + r.i, r.phase))
@@ -606,19 +626,11 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, const
   const float* seg_l = reinterpret_cast<const float*>(v.base + S::kSegL) +
                        r.i * kSoftmaxWarps * kMaxG;
   const float* sr = reinterpret_cast<const float*>(v.base + S::kSegRef) + r.i * kGroups * kMaxG;
-  float* factor = reinterpret_cast<float*>(v.base + S::kFactor) + r.i * kMaxG;
+  float* factor = reinterpret_cast<float*>(v.base + S::kFactor) + r.i * 3 * kMaxG;
   const bool nan = (v.seg_poison[r.i * kGroups] | v.seg_poison[r.i * kGroups + 1]) != 0;
-  const float qnan = __int_as_float(0x7fc00000);
-  float m = -INFINITY, l = 0.f;
-  auto store_lse = [&]() {
-    if (lane >= p.G) return;
-    const size_t row = (size_t)s.bt * p.Hq + s.g * p.G + lane;
-    const float x = nan ? qnan : lse_of(m, l);
-    p.lse[row] = x;
-    if (p.lse2) p.lse2[row] = x;
-  };
   if (lane < kMaxG) {
-    float f;
+    const float qnan = __int_as_float(0x7fc00000);
+    float m = -INFINITY, l = 0.f, f;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) m = fmaxf(m, sr[g * kMaxG + lane]);
 #pragma unroll
@@ -627,8 +639,11 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, const
       l = fmaf(ref_weight(sr[g * kMaxG + lane], m),
                (w[0] + w[kMaxG]) + (w[2 * kMaxG] + w[3 * kMaxG]), l);
     }
-    if (s.whole()) {
+    if (slot < 0) {
       f = 1.0f / l;
+      // for the log-sum-exp, which the output warps take from these
+      factor[kMaxG + lane] = m;
+      factor[2 * kMaxG + lane] = nan ? qnan : l;
     } else {
       // The reference bounds V's scales too; the partial's is moved to the
       // sum's own magnitude, so that partials of blocks whose V scales lie far
@@ -636,7 +651,7 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, const
       const int e = l > 0.f ? ((__float_as_int(l) >> 23) - 127 + 4) >> 3 << 3 : 0;
       const int k = max(-112, min(112, e));
       f = ptx::pow2i(-k);
-      reinterpret_cast<float2*>(p.part_ml)[s.slot() * kMaxG + lane] =
+      reinterpret_cast<float2*>(p.part_ml)[(size_t)slot * kMaxG + lane] =
           make_float2(nan ? qnan : m + (float)k, l * f);
     }
     factor[lane] = nan ? qnan : f;
@@ -647,7 +662,6 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, const
     ptx::mbar_arrive(v.bar(S::kFFull + r.i));
   }
   r.next();
-  if (s.whole()) store_lse();   // not in the outputs' way
   return true;
 }
 
@@ -658,7 +672,7 @@ __device__ __forceinline__ void helper_warp(const P& p, const View& v, int lane)
   ptx::grid_dependency_wait();
   // Empty units: output 0, LSE -inf.
   for (int u = p.n_full + blockIdx.x; u < p.n_units; u += p.grid) {
-    const Unit& U = p.units[u];
+    const DevUnit& U = p.units[u];
     const size_t row = (size_t)U.bt * p.Hq + U.g * p.G;
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = lane; i < p.G * D / 4; i += 32) {
@@ -672,38 +686,47 @@ __device__ __forceinline__ void helper_warp(const P& p, const View& v, int lane)
   }
   // q is loaded two segments ahead (a lane's dims by that lane, so no lane waits
   // for another) and converted one ahead (the first segment's by the output warps).
+  constexpr int kNone = -2, kWholeUnit = -1;
   Segments<P> ahead(p);
   Segment s;
   QVec<D>* staged = reinterpret_cast<QVec<D>*>(v.base + S::kQRaw) + lane;   // [head][lane]
-  bool more = ahead.next(s);
-  auto load_next = [&]() {
-    more = more && ahead.next(s);
-    if (!more) return;
+  // The next segment's partial slot.
+  auto take = [&]() {
+    if (!ahead.next(s)) return kNone;
+    return s.whole() ? kWholeUnit : (int)s.slot();
+  };
+  auto take_and_load = [&]() {
+    const int slot = take();
+    if (slot == kNone) return slot;
 #pragma unroll 1
     for (int h = 0; h < p.G; ++h)
       copy_own(ptx::smem_addr(staged + 32 * h), q_of<D>(p, s, h, lane));
+    return slot;
   };
-  int heads = kMaxG;   // the first conversion clears the columns without a head
-  auto convert_next = [&]() {
+  int now = take();
+  if (now == kNone) return;
+  int next = take_and_load();
+  for (int heads = kMaxG;;) {
+    // q of `next`, and that of the segment behind it is asked for
+    int later = kNone;
     qr.next();
-    if (!more) return true;
-    if (!warp_wait(p, v, S::kQEmpty + qr.i, qr.phase ^ 1)) return false;
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (next != kNone) {
+      if (!warp_wait(p, v, S::kQEmpty + qr.i, qr.phase ^ 1)) return;
+      asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
-    for (int h = 0; h < heads; ++h)
-      convert_head<D>(p, v, h < p.G ? staged[32 * h] : QVec<D>{}, qr.i, h, lane);
-    heads = p.G;
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane < kOutWarps) ptx::mbar_arrive(v.bar(S::kQFull + qr.i));
-    load_next();
-    return true;
-  };
-  load_next();
-  if (!convert_next()) return;
-  for_segments(p, [&](const Segment& now, int) {
-    return segment_factors<D>(p, v, now, fr, lane) && convert_next();
-  });
+      for (int h = 0; h < heads; ++h)
+        convert_head<D>(p, v, h < p.G ? staged[32 * h] : QVec<D>{}, qr.i, h, lane);
+      heads = p.G;   // the first conversion clears the columns without a head
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane < kOutWarps) ptx::mbar_arrive(v.bar(S::kQFull + qr.i));
+      later = take_and_load();
+    }
+    if (!segment_factors<D>(p, v, now, fr, lane)) return;
+    if (next == kNone) return;
+    now = next;
+    next = later;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -970,7 +993,14 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
     fail = fail || !wait(p, v, S::kFFull + (seg & 1), (seg >> 1) & 1);
     if (any_in_group(1, kOut, fail)) return false;
     // ---- the segment's output or partial ----
-    const float* factor = reinterpret_cast<const float*>(v.base + S::kFactor) + (seg & 1) * kMaxG;
+    const float* factor = reinterpret_cast<const float*>(v.base + S::kFactor) +
+                          (seg & 1) * 3 * kMaxG;
+    float m = 0.f, l = 0.f;
+    const bool has_lse = s.whole() && warp == 0 && lane < p.G;
+    if (has_lse) {
+      m = factor[kMaxG + lane];
+      l = factor[2 * kMaxG + lane];
+    }
     const size_t orow = (size_t)s.bt * p.Hq + s.g * p.G;
     float* dst = (s.whole() ? p.out + orow * D : p.part_o + s.slot() * kMaxG * D) + ct;
     float* dst2 = s.whole() && p.out2 ? p.out2 + orow * D + ct : nullptr;
@@ -986,8 +1016,16 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(v.bar(S::kFEmpty + (seg & 1)));
+    if (has_lse) {
+      const float x = lse_of(m, l);
+      p.lse[orow + lane] = x;
+      if (p.lse2) p.lse2[orow + lane] = x;
+    }
     if (!s.whole()) {
-      finish_split_unit<D, kOut>(p, v, s.U, s.u, s.b, s.bt, s.g, s.U.first_cta, ct, warp, lane);
+      Unit U{};
+      U.n_parts = s.U.n_parts;
+      U.part_base = s.U.part_base;
+      finish_split_unit<D, kOut>(p, v, U, s.u, 0, s.bt, s.g, s.U.first_cta, ct, warp, lane);
       ptx::named_barrier(1, kOut);   // merge_info is read before it is written again
     }
     return true;
@@ -1247,12 +1285,15 @@ int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L, con
   // Units without pages go last: every role walks its CTA's units, and skipping
   // one costs it ~0.2 us (4 requests of 700 tokens and 252 without any: 64.5 us
   // with the others among them).
-  Unit* to = prm.units;
+  DevUnit* to = prm.units;
+  auto add = [&](const Unit& u) {
+    *to++ = {u.page_first, u.bt, u.tok_start, u.tok_end, u.g, u.part_base, u.n_parts, u.first_cta};
+  };
   for (size_t i = L.u0; i < L.u0 + L.n; ++i)
-    if (plan.pages[i] != 0) *to++ = plan.units[i];
+    if (plan.pages[i] != 0) add(plan.units[i]);
   prm.n_full = static_cast<int>(to - prm.units);
   for (size_t i = L.u0; i < L.u0 + L.n && to < prm.units + L.n; ++i)
-    if (plan.pages[i] == 0) *to++ = plan.units[i];
+    if (plan.pages[i] == 0) add(plan.units[i]);
   std::memcpy(prm.starts, L.starts.data(), L.starts.size() * sizeof(int32_t));
   for (int k = 0, u = 0; k < L.grid; ++k) {
     // the last unit that starts at or before the CTA's first page

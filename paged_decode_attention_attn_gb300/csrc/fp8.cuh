@@ -20,11 +20,23 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   return pack2(a, b) | (pack2(c, d) << 16);
 }
 
-// Two e4m3 codes to fp32 (exact).
-__device__ __forceinline__ float2 unpack2(uint32_t codes) {
+// The same from fp16.
+__device__ __forceinline__ uint32_t pack2(__half2 x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
+      : "=h"(r)
+      : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+  return r;
+}
+
+// Two e4m3 codes to fp16 (exact), to fp32.
+__device__ __forceinline__ __half2 unpack2_half(uint32_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return *reinterpret_cast<const __half2*>(&h);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t codes) {
+  return __half22float2(unpack2_half(codes));
 }
 
 __device__ __forceinline__ void unpack4(uint32_t codes, float (&y)[4]) {
