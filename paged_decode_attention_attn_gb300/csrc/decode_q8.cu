@@ -7,7 +7,8 @@
 // from the codes as TMA leaves them in shared memory; no thread touches a code.
 //
 //  * Work split and partials: as the bf16 kernel (split_units.cuh); a request's
-//    tiles are merged by a kernel of its own.  A CTA streams its pages two at a time: a step is 128 tokens of one kv head.
+//    tiles are merged by a kernel of its own.  A CTA streams its pages two at a
+//    time: a step is 128 tokens of one kv head.
 //  * S = K Q^T: M = 128 tokens, N = 16, K = D.  q (bf16, 8 significant bits) is
 //    scaled by a power of two per head and held as hi + lo / 16 in e4m3 (4 bits
 //    each, and a sign between them): 16 columns for 8 heads, exact for values
@@ -21,7 +22,7 @@
 //    of what the parts before left, 32 times finer (that stays below 256 =
 //    2^8, as w 2^8 does): 4 bits and a sign per part, 2^-33 absolute at the end.
 //  * O^T = V^T P^T: M = 128 dims (a step's V codes as they lie, M-major), N =
-//    8 kParts, K = 128 tokens.  Every step's product starts from zero in tensor
+//    8 kParts (a token's row of P, N-major), K = 128 tokens.  Every step's product starts from zero in tensor
 //    memory and is added to fp32 registers (a thread per dim), so the long sum
 //    is rounded to nearest and rescaled there.
 //  * Warps: 0-7 softmax, 8-11 output, 12 TMA, 13 scores, 14 products, 15 what is
@@ -114,7 +115,8 @@ struct Smem {
   static constexpr int kSegL = kRef + kRefs * kMaxG * 4;           // [2][warp][kMaxG]
   static constexpr int kSegRef = kSegL + 2 * kSoftmaxWarps * kMaxG * 4;   // [2][group][kMaxG]
   static constexpr int kWarpMax = kSegRef + 2 * kGroups * kMaxG * 4;      // [warp][kMaxG]
-  static constexpr int kFactor = kWarpMax + kSoftmaxWarps * kMaxG * 4;    // [2][kMaxG]
+  // [2][factor | reference | sum][kMaxG]
+  static constexpr int kFactor = kWarpMax + kSoftmaxWarps * kMaxG * 4;
   static constexpr int kBars = kFactor + 2 * 3 * kMaxG * 4;
   // mbarriers: full, empty per K and V stage; S, P, product, q, sums: full and
   // empty; all of a warp's products done; reference slots written; a segment's
@@ -369,7 +371,8 @@ __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtens
   };
   for_segments(p, [&](const Segment& s, int seg) {
     if (seg == 0) ptx::grid_dependency_wait();
-    const int32_t* prow = p.page_table + (size_t)request_of(p, s.bt) * p.max_pages + s.U.tok_start / kPage;
+    const int32_t* prow =
+        p.page_table + (size_t)request_of(p, s.bt) * p.max_pages + s.U.tok_start / kPage;
     const float* scales = p.scales + s.g * kBlocksPerPage;   // K's; V's lie Hkv heads behind
     int next_pid = s.lo + lane < s.hi ? __ldg(prow + s.lo + lane) : 0;
     for (int base = s.lo; base < s.hi; base += 32) {
@@ -1429,8 +1432,8 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
     if (rc != PA_OK) return rc;
   }
   if (T > 1 && merged_out != nullptr) {
-    PA_CHECK_CUDA(D == 128 ? launch_merge<128>(out, lse, T, Hq, B * Hq, merged_out, merged_lse, stream)
-                           : launch_merge<256>(out, lse, T, Hq, B * Hq, merged_out, merged_lse, stream));
+    auto merge = D == 128 ? launch_merge<128> : launch_merge<256>;
+    PA_CHECK_CUDA(merge(out, lse, T, Hq, B * Hq, merged_out, merged_lse, stream));
     PA_CHECK_CUDA(cudaGetLastError());
   }
   return PA_OK;
