@@ -921,7 +921,7 @@ int run(bool tensor_cores, const void* q, const void* pool, int64_t pool_pages,
   sms = std::min(sms, kMaxGrid);
 
   Plan plan;
-  const int rc_plan = plan_units<false>(
+  const int rc_plan = plan_units(
       tiles, B, T, n_kv_heads, kSegmentCharge, merged_out != nullptr,
       [&](const Unit*, const int32_t*, size_t, long long total, std::vector<int32_t>* starts) {
         equal_starts(total, launch_grid(total, sms, n_kv_heads), starts);

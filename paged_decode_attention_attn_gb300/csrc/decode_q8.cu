@@ -22,9 +22,9 @@
 //    of what the parts before left, 32 times finer (that stays below 256 =
 //    2^8, as w 2^8 does): 4 bits and a sign per part, 2^-33 absolute at the end.
 //  * O^T = V^T P^T: M = 128 dims (a step's V codes as they lie, M-major), N =
-//    8 kParts (a token's row of P, N-major), K = 128 tokens.  Every step's product starts from zero in tensor
-//    memory and is added to fp32 registers (a thread per dim), so the long sum
-//    is rounded to nearest and rescaled there.
+//    8 kParts (a token's row of P, N-major), K = 128 tokens.  Every step's
+//    product starts from zero in tensor memory and is added to fp32 registers (a
+//    thread per dim), so the long sum is rounded to nearest and rescaled there.
 //  * Warps: 0-7 softmax, 8-11 output, 12 TMA, 13 scores, 14 products, 15 what is
 //    done per segment (q, factors of the outputs, empty units); 16 warps leave
 //    128 registers a thread, 17 would leave 96.  All waits are on mbarriers
@@ -129,7 +129,7 @@ struct Smem {
                        kRefFull = kDrain + 2, kFFull = kRefFull + kRefs, kFEmpty = kFFull + 2,
                        kNumBars = kFEmpty + 2;
   static constexpr int kMisc = kBars + kNumBars * 8;               // ints, see View
-  static constexpr int kUsed = kMisc + (kSlots + 2 * kGroups + 6) * 4;
+  static constexpr int kUsed = kMisc + (kSlots + 2 * kGroups + 4) * 4;
   static constexpr int kAlloc = kUsed + 1024;
   static_assert(kAlloc <= 232448, "shared memory budget");
 };
@@ -182,7 +182,6 @@ struct View {
   volatile int* poison;      // [slots] step holds a page that is not there
   volatile int* seg_poison;  // [2][group]
   volatile int* abort_flag;
-  volatile int* fin_flag;
   volatile int* merge_info;
   __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
 };
@@ -1052,9 +1051,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   v.seg_poison = misc;
   misc += 2 * kGroups;
   v.abort_flag = misc;
-  v.fin_flag = misc + 1;
-  v.merge_info = misc + 2;
-  int* tmem_slot = misc + 4;
+  v.merge_info = misc + 1;
+  int* tmem_slot = misc + 3;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kNumBars; ++i) {
@@ -1394,7 +1392,7 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   if (sms <= 0) return fail(PA_ERR_CUDA, "cannot query the device's SM count");
   sms = std::min(sms, kMaxGrid);
   Plan plan;
-  int rc = plan_units<true>(
+  int rc = plan_units(
       tiles, B, T, Hkv, kSegmentCharge, false,
       [&](const Unit* units, const int32_t* pages, size_t n, long long total,
           std::vector<int32_t>* starts) { cut(units, pages, n, total, sms, Hkv, starts); },

@@ -8,8 +8,8 @@
 // T, Hq, Hkv, G, n_units, units, wait_limit_ns, slice_wait_ns; where kSecondOut
 // says that outputs are written twice, out2 and lse2; where kMerge says that the
 // kernel merges a request's tiles, m_out, m_lse and req_counters; kAllSlices,
-// see split_slices); its shared-memory view Sh has fin_flag and merge_info.  The
-// kConsumers threads that call a function meet at named barrier 1.
+// see split_slices); its shared-memory view Sh has merge_info and, with kMerge,
+// fin_flag.  The kConsumers threads that call a function meet at named barrier 1.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -427,8 +427,8 @@ inline void equal_starts(long long total, int grid, std::vector<int32_t>* starts
 // Lays a call's tiles out as units and launches.  shape(units, their pages, n,
 // total, starts) cuts a launch's n units, laid out over `total` flattened
 // pages, into CTAs; segment_charge is the number of pages that hold no data
-// charged per unit start; merge: the call merges every request's tiles.
-template <bool kAllSlices, class Shape>
+// charged per unit start; merge: the kernel merges every request's tiles.
+template <class Shape>
 int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int segment_charge, bool merge,
                Shape shape, Plan* plan) {
   PA_REQUIRE(n_kv_heads <= 65535, "n_kv_heads (%d) above 65,535", n_kv_heads);
@@ -502,7 +502,7 @@ int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int segment_c
     for (int b = 0; b < B; ++b) {
       Unit* u = units.data() + (g * (size_t)B + b) * T;
       int count = 0;
-      for (int t = 0; t < T; ++t) count += u[t].n_parts > 1 ? split_slices<kAllSlices>(u[t].n_parts) : 1;
+      for (int t = 0; t < T; ++t) count += u[t].n_parts > 1 ? split_slices<false>(u[t].n_parts) : 1;
       for (int t = 0; t < T; ++t) u[t].pair_total = count;
     }
   }
