@@ -81,6 +81,7 @@ constexpr int kMinPages = 4;                // pages per CTA at least, where uni
 // kernel's do; 100 / 90 / 85 / 80 percent on one box: 1 x 262,144 tokens 85.3 /
 // 84.4 / 83.7 / 83.2 us, 8 ragged of up to 131,072 247.5 / 245.5 / 244.5 / 242.1).
 constexpr int kLongPages = 64, kLongGridPct = 85;
+constexpr int kTwoPartsBytes = 400 << 10;   // worth what a CTA loses with parts of two units
 constexpr int kSnapPages = 4;               // how far a CTA's end moves to a unit's border
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kMaxScaleExp = 100;           // largest |log2| of a V scale
@@ -1200,11 +1201,36 @@ __global__ void __launch_bounds__(kMergeThreads)
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
+// Pages that each CTA has at most if no CTA takes parts of two units (the fewest
+// for which the units' CTAs fit the grid), or 0 where that is more than
+// kTwoPartsBytes above an equal share.  A CTA with a part of a split unit before
+// another segment is ~5 us behind the others: a table row, q, an arrival and its
+// fence lie between the two.  (Against equal shares: 7 ragged requests in 5 tiles
+// 24.9 -> 23.6 us, 20,000 tokens in 3 tiles 15.7 -> 14.5, 9,000 and 800 tokens 12.3
+// -> 10.5, 3 x 54,748 in 4 tiles unchanged; 200 KB or 300 KB did as well but for 12
+// x 9,000 in 3 tiles, 26.0 -> 25.4.)
+int pages_alone(const int32_t* pages, size_t n, long long sum, int count, int grid, int d) {
+  if (count > grid) return 0;
+  auto fits = [&](long long most) {
+    long long ctas = 0;
+    for (size_t i = 0; i < n; ++i) ctas += (pages[i] + most - 1) / most;
+    return ctas <= grid;
+  };
+  long long lo = (sum + grid - 1) / grid, hi = sum / grid + kTwoPartsBytes / (2 * kPage * d);
+  if (!fits(hi)) return 0;
+  while (lo < hi) {
+    const long long mid = (lo + hi) / 2;
+    if (fits(mid)) hi = mid;
+    else lo = mid + 1;
+  }
+  return (int)lo;
+}
+
 // Cuts a launch's units into CTAs.  A unit on one CTA costs a step per two
 // pages (0.5-0.65 us); a unit on several costs partials and their merge, about
 // 2 us more.
 void cut_pages(const Unit* units, const int32_t* pages, size_t n, long long total, int sms,
-               int heads, std::vector<int32_t>* starts) {
+               int heads, int d, std::vector<int32_t>* starts) {
   int count = 0, most = 0, least = 1 << 30;   // units with pages
   long long sum = 0;
   for (size_t i = 0; i < n; ++i) {
@@ -1231,6 +1257,17 @@ void cut_pages(const Unit* units, const int32_t* pages, size_t n, long long tota
   // As the bf16 kernel's: the CTAs at the same offset of each kv head's block
   // of units stream the same pages at the same time.
   if (grid >= heads) grid -= grid % heads;
+  const int alone = most == least ? 0 : pages_alone(pages, n, sum, count, grid, d);
+  if (alone > 0) {
+    for (size_t i = 0; i < n; ++i) {
+      const int parts = (pages[i] + alone - 1) / alone;
+      for (int k = 0; k < parts; ++k)
+        starts->push_back(starts->empty() ? 0
+                                          : units[i].page_first + (int)((long long)pages[i] * k / parts));
+    }
+    starts->push_back(static_cast<int32_t>(total));
+    return;
+  }
   if (most == least) {
     // Units of one length: a grid that divides them, or that they divide, has no
     // CTA with parts of two units.
@@ -1265,8 +1302,8 @@ void cut_pages(const Unit* units, const int32_t* pages, size_t n, long long tota
 // out to all CTAs, a warp each (4 requests of 700 tokens and 252 without any:
 // 8.1 us, 24.8 without these CTAs; 1 and 63: 7.6, 21.2).
 void cut(const Unit* units, const int32_t* pages, size_t n, long long total, int sms, int heads,
-         std::vector<int32_t>* starts) {
-  cut_pages(units, pages, n, total, sms, heads, starts);
+         int d, std::vector<int32_t>* starts) {
+  cut_pages(units, pages, n, total, sms, heads, d, starts);
   const size_t empty = std::count(pages, pages + n, 0);
   const size_t ctas = std::min<size_t>(sms, empty);
   if (starts->size() < ctas + 1) starts->resize(ctas + 1, starts->back());
@@ -1395,7 +1432,7 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   int rc = plan_units(
       tiles, B, T, Hkv, kSegmentCharge, false,
       [&](const Unit* units, const int32_t* pages, size_t n, long long total,
-          std::vector<int32_t>* starts) { cut(units, pages, n, total, sms, Hkv, starts); },
+          std::vector<int32_t>* starts) { cut(units, pages, n, total, sms, Hkv, D, starts); },
       &plan);
   if (rc != PA_OK) return rc;
 
