@@ -82,6 +82,8 @@ constexpr int kMinPages = 4;                // pages per CTA at least, where uni
 // 84.4 / 83.7 / 83.2 us, 8 ragged of up to 131,072 247.5 / 245.5 / 244.5 / 242.1).
 constexpr int kLongPages = 64, kLongGridPct = 85;
 constexpr int kTwoPartsBytes = 400 << 10;   // worth what a CTA loses with parts of two units
+constexpr int kWholeBytes = 1600 << 10;     // beyond an equal share, for units kept whole
+constexpr int kUnitCharge = 3;              // pages that a whole unit costs beside its own
 constexpr int kSnapPages = 4;               // how far a CTA's end moves to a unit's border
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kMaxScaleExp = 100;           // largest |log2| of a V scale
@@ -1262,8 +1264,8 @@ void cut_pages(const Unit* units, const int32_t* pages, size_t n, long long tota
     for (size_t i = 0; i < n; ++i) {
       const int parts = (pages[i] + alone - 1) / alone;
       for (int k = 0; k < parts; ++k)
-        starts->push_back(starts->empty() ? 0
-                                          : units[i].page_first + (int)((long long)pages[i] * k / parts));
+        starts->push_back(starts->empty() ? 0 : units[i].page_first +
+                                                    (int)((long long)pages[i] * k / parts));
     }
     starts->push_back(static_cast<int32_t>(total));
     return;
@@ -1297,23 +1299,101 @@ void cut_pages(const Unit* units, const int32_t* pages, size_t n, long long tota
   if (total > at) starts->push_back(static_cast<int32_t>(total));
 }
 
-// The same, with CTAs that have no pages where units without pages (padded
-// requests, tiles behind a request's end) outnumber the CTAs: those are dealt
-// out to all CTAs, a warp each (4 requests of 700 tokens and 252 without any:
-// 8.1 us, 24.8 without these CTAs; 1 and 63: 7.6, 21.2).
+// Adds CTAs that have no pages where units without pages (padded requests, tiles
+// behind a request's end) outnumber the CTAs: those are dealt out to all CTAs, a
+// warp each (4 requests of 700 tokens and 252 without any: 8.1 us, 24.8 without
+// these CTAs; 1 and 63: 7.6, 21.2).
+void deal_empty(size_t empty, int sms, std::vector<int32_t>* starts) {
+  const size_t ctas = std::min<size_t>(sms, empty);
+  if (starts->size() < ctas + 1) starts->resize(ctas + 1, starts->back());
+}
+
 void cut(const Unit* units, const int32_t* pages, size_t n, long long total, int sms, int heads,
          int d, std::vector<int32_t>* starts) {
   cut_pages(units, pages, n, total, sms, heads, d, starts);
-  const size_t empty = std::count(pages, pages + n, 0);
-  const size_t ctas = std::min<size_t>(sms, empty);
-  if (starts->size() < ctas + 1) starts->resize(ctas + 1, starts->back());
+  deal_empty(std::count(pages, pages + n, 0), sms, starts);
+}
+
+// Lays a launch's units out anew so that every CTA has whole ones, the longest
+// first dealt to the CTA with the least, where that comes within kWholeBytes
+// of equal shares: no unit is split, and nothing merged.  A CTA takes its
+// shortest first, so that launches end in long streams.  (Shortest / longest
+// first, and equal shares: 64 requests of up to 2,500 tokens 32.9 / 33.6 / 35.6
+// us, at 256 dims 29.8 / 29.7 / 33.5, 256 of up to 600 33.9 / 37.6 / 37.1, 120 of
+// up to 2,000 with 2 kv heads 14.5 / 14.9 / 19.3.  Giving each kv head CTAs of its
+// own, which then read the same pages at the same time, made no difference; with
+// 400 KB for kWholeBytes 42 of up to 4,000 took 34.4 us instead of 32.0, with 3.2
+// MB nothing changed.)
+// Linear in the units: a sort by counting, and CTAs kept in lists by their load
+// (the least load only grows).  Returns the order of the units that have pages, or
+// nothing if they stay as they are.
+std::vector<int> pack(Plan* plan, Launch* L, int sms, int d) {
+  const int32_t* pages = plan->pages.data() + L->u0;
+  Unit* units = plan->units.data() + L->u0;
+  const int n = (int)L->n;
+  long long sum = 0;
+  int count = 0, most = 0, least = 1 << 30;   // units with pages
+  for (int i = 0; i < n; ++i) {
+    if (pages[i] == 0) continue;
+    ++count;
+    sum += pages[i];
+    most = std::max(most, pages[i]);
+    least = std::min(least, pages[i]);
+  }
+  const int grid = sum >= (long long)kLongPages * sms ? sms * kLongGridPct / 100 : sms;
+  if (count <= grid || most == least) return {};
+  // Loads are pages and a few more per unit.
+  const long long limit =
+      (sum + (long long)kUnitCharge * count) / grid + kWholeBytes / (2 * kPage * d);
+  if (most + kUnitCharge > limit || limit > 1 << 20) return {};
+  // Units by their pages, and CTAs by their loads: heads of lists.
+  std::vector<int> of_pages(most + 1, -1), of_load(limit + 1, -1), next_unit(n), next_cta(grid),
+      first(grid, -1);
+  for (int i = n - 1; i >= 0; --i) {
+    next_unit[i] = of_pages[pages[i]];
+    of_pages[pages[i]] = i;
+  }
+  for (int k = 0; k < grid; ++k) next_cta[k] = k + 1 < grid ? k + 1 : -1;
+  of_load[0] = 0;
+  int load = 0;
+  for (int p = most; p > 0; --p) {
+    for (int i = of_pages[p]; i >= 0;) {
+      while (of_load[load] < 0) ++load;
+      const int k = of_load[load], to = load + p + kUnitCharge, next = next_unit[i];
+      if (to > limit) return {};
+      of_load[load] = next_cta[k];
+      next_cta[k] = of_load[to];
+      of_load[to] = k;
+      next_unit[i] = first[k];   // the CTA's last comes first
+      first[k] = i;
+      i = next;
+    }
+  }
+  std::vector<int> order;
+  order.reserve(count);
+  L->starts.clear();
+  int32_t at = 0;
+  for (int k = 0; k < grid; ++k) {
+    L->starts.push_back(at);
+    for (int i = first[k]; i >= 0; i = next_unit[i]) {
+      order.push_back(i);
+      units[i].page_first = at;
+      units[i].n_parts = 1;
+      units[i].first_cta = static_cast<int16_t>(k);
+      at += pages[i];
+    }
+  }
+  L->starts.push_back(at);
+  deal_empty(n - count, sms, &L->starts);
+  L->grid = (int)L->starts.size() - 1;
+  return order;
 }
 
 using Common = Params<kMaxUnitsSmall>;
 
 template <int D, int N>
-int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L, const Common& common,
-                 cudaStream_t stream) {
+int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L,
+                 const std::vector<int>& order, const Common& common, cudaStream_t stream) {
   using Prm = Params<N>;
   static_assert(N >= kMaxUnitsSmall && offsetof(Prm, starts) == offsetof(Common, starts), "");
   Prm prm;
@@ -1327,7 +1407,8 @@ int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L, con
   auto add = [&](const Unit& u) {
     *to++ = {u.page_first, u.bt, u.tok_start, u.tok_end, u.g, u.part_base, u.n_parts, u.first_cta};
   };
-  for (size_t i = L.u0; i < L.u0 + L.n; ++i)
+  for (int i : order) add(plan.units[L.u0 + i]);
+  for (size_t i = L.u0; order.empty() && i < L.u0 + L.n; ++i)
     if (plan.pages[i] != 0) add(plan.units[i]);
   prm.n_full = static_cast<int>(to - prm.units);
   for (size_t i = L.u0; i < L.u0 + L.n && to < prm.units + L.n; ++i)
@@ -1352,14 +1433,14 @@ int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L, con
   return PA_OK;
 }
 
-int launch(int D, const CUtensorMap& tmap, const Plan& plan, const Launch& L, const Common& common,
-           cudaStream_t stream) {
+int launch(int D, const CUtensorMap& tmap, const Plan& plan, const Launch& L,
+           const std::vector<int>& order, const Common& common, cudaStream_t stream) {
   const bool small = L.n <= (size_t)kMaxUnitsSmall;
   if (D == 128)
-    return small ? launch_units<128, kMaxUnitsSmall>(tmap, plan, L, common, stream)
-                 : launch_units<128, kMaxUnitsLarge>(tmap, plan, L, common, stream);
-  return small ? launch_units<256, kMaxUnitsSmall>(tmap, plan, L, common, stream)
-               : launch_units<256, kMaxUnitsLarge>(tmap, plan, L, common, stream);
+    return small ? launch_units<128, kMaxUnitsSmall>(tmap, plan, L, order, common, stream)
+                 : launch_units<128, kMaxUnitsLarge>(tmap, plan, L, order, common, stream);
+  return small ? launch_units<256, kMaxUnitsSmall>(tmap, plan, L, order, common, stream)
+               : launch_units<256, kMaxUnitsLarge>(tmap, plan, L, order, common, stream);
 }
 
 // One thread per float4 for up to kOneTeamTiles tiles (one round of loads), a
@@ -1462,8 +1543,9 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   common.wait_limit_ns = hooks.wait_limit_ns;
   common.stall_iteration = hooks.stall_iteration;
   common.slice_wait_ns = hooks.slice_wait_ns;
-  for (const Launch& L : plan.launches) {
-    rc = launch(D, tmap, plan, L, common, stream);
+  for (Launch& L : plan.launches) {
+    const std::vector<int> order = pack(&plan, &L, sms, D);
+    rc = launch(D, tmap, plan, L, order, common, stream);
     if (rc != PA_OK) return rc;
   }
   if (T > 1 && merged_out != nullptr) {

@@ -508,3 +508,20 @@ def test_merge_of_any_number_of_tiles(B, tiles, d):
     assert torch.all(c.merged[2] == 0) and torch.all(c.merged_lse[2] == -float("inf"))
     assert c.merged[3, 3:].isnan().all()
     assert c.merged[3, :3].isfinite().all() and c.merged_lse[3, :3].isfinite().all()
+
+
+@pytest.mark.parametrize("n,top,geo", [(64, 900, (8, 8, 128)), (200, 300, (6, 2, 256)),
+                                       (400, 150, (16, 4, 128)), (170, 2000, (4, 1, 256))])
+def test_batches_of_more_units_than_ctas(B, n, top, geo):
+    """Units of very different lengths, dealt to CTAs whole and out of order, in
+    one launch or several, some of them empty."""
+    hq, hkv, d = geo
+    rng = np.random.default_rng(n)
+    lengths = rng.integers(0, top, n).tolist()
+    tiles = [[(0, x // 3), (x // 3, x)] for x in lengths]
+    c = Case(lengths, tiles, hq=hq, hkv=hkv, d=d, seed=51)
+    assert c.run(B) == 0
+    c.check(rng.choice(n, 24, replace=False).tolist() + [int(np.argmax(lengths))])
+    want = [t.clone() for t in (c.out, c.lse, c.merged, c.merged_lse)]
+    assert c.run(B) == 0
+    assert all(torch.equal(a, b) for a, b in zip(want, (c.out, c.lse, c.merged, c.merged_lse)))
