@@ -250,15 +250,17 @@ int paged_decode_attn_lse_append(const void* q, void* pool, int64_t pool_pages,
                                  void* workspace, size_t workspace_bytes,
                                  unsigned flags, cudaStream_t stream);
 
+#define PA_STALL_VALUES (1 << 30)   /* see paged_decode_attn_test_stall */
+
 /* Test hook for failure detection (no counterpart in the source pages): the
  * next decode call made on this thread (any paged_decode_attn_lse* entry
  * point, or paged_decode_attn_q8_lse) gives every bounded device wait up after
  * wait_limit_ns (instead of 2 s), and CTA 0 leaves its page load (8-bit pool:
- * its load of two pages' keys) number `iteration` unarmed, so the wait for
- * that load runs out: the kernel sets PA_STATUS_TIMEOUT, lets the
- * loads it issued land and returns; the context stays usable.  Outputs of
- * that call are invalid and its workspace must be zero-filled again before
- * reuse.  (-1, 0) clears a pending setting.  PA_ERR_INVALID otherwise unless
+ * its load of two pages' keys, or, with PA_STALL_VALUES added to `iteration`,
+ * of their values) number `iteration` unarmed, so the wait for that load runs
+ * out: the kernel sets PA_STATUS_TIMEOUT, lets the loads it issued land and
+ * returns; the context stays usable.  Outputs of that call are invalid and its
+ * workspace must be zero-filled again before reuse.  (-1, 0) clears a pending setting.  PA_ERR_INVALID otherwise unless
  * iteration >= 0 and 0 < wait_limit_ns <= 2 s.  Nothing else calls it;
  * production calls never stall. */
 int paged_decode_attn_test_stall(int iteration, uint64_t wait_limit_ns);

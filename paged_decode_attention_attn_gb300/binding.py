@@ -33,6 +33,7 @@ PA_STATUS_BAD_ROW = 4
 PA_ARENA_RECORD_ONLY = 1
 PA_PAGE_EXACT, PA_PAGE_QUEUED, PA_PAGE_PUBLISHED, PA_PAGE_NOT_CONVERTIBLE = 0, 1, 2, 3
 PA_DECODE_KV_READY = 1
+PA_STALL_VALUES = 1 << 30
 PA_ROPE_INTERLEAVED = 1
 PAGE_TOKENS = 64
 SCALE_TOKENS = 16
@@ -471,10 +472,12 @@ def paged_decode_attn_lse_append(q, pool, page_table, tiles, scale, positions, n
         workspace.numel(), PA_DECODE_KV_READY if kv_ready else 0, _stream_handle(stream)))
 
 
-def test_stall(iteration: int, wait_limit_ns: int):
+def test_stall(iteration: int, wait_limit_ns: int, values: bool = False):
     """Failure-detection test hook: the next decode call on this thread stalls
-    CTA 0 at page load ``iteration`` and gives waits up after wait_limit_ns."""
-    _check(lib.paged_decode_attn_test_stall(int(iteration), int(wait_limit_ns)))
+    CTA 0 at page load ``iteration`` (``values``: an 8-bit call's load of V) and
+    gives waits up after wait_limit_ns."""
+    _check(lib.paged_decode_attn_test_stall(int(iteration) + (PA_STALL_VALUES if values else 0),
+                                            int(wait_limit_ns)))
 
 
 def test_slice_wait(slice_wait_ns: int):

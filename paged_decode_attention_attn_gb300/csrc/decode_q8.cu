@@ -229,9 +229,14 @@ __device__ __forceinline__ bool wait(const P& p, const View& v, int bar, uint32_
   return ptx::mbar_try_wait(b, parity) ||
          wait_long(b, parity, p.wait_limit_ns, p.status, v.abort_flag);
 }
+// The same for a converged warp, with one answer for all its lanes: false too if
+// `ok` is false in one of them.  A warp skips tensor memory loads, and leaves its
+// loop, by such an answer alone: lanes that gave up by themselves would be missed at
+// the next instruction that takes the whole warp, by a wait without a limit.
 template <class P>
-__device__ __forceinline__ bool warp_wait(const P& p, const View& v, int bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait(p, v, bar, parity));
+__device__ __forceinline__ bool warp_wait(const P& p, const View& v, int bar, uint32_t parity,
+                                          bool ok = true) {
+  return __all_sync(0xffffffffu, ok && wait(p, v, bar, parity));
 }
 
 // A CTA's part of a unit: its pages [lo, hi).
@@ -356,6 +361,7 @@ __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtens
   StepPages late[kLag] = {};           // the steps whose V is next
   const uint64_t pol = ptx::policy_evict_first();   // every page is read once
   const int stall = blockIdx.x == 0 ? p.stall_iteration : -1;
+  const int stall_values = stall - (int)PA_STALL_VALUES;   // (negative without the flag)
   auto boxes = [&](uint32_t dst, uint32_t full, int col, const StepPages& at) {
     ptx::mbar_arrive_expect_tx(full, at.n * S::kChunks * S::kPageBytes);
 #pragma unroll
@@ -369,6 +375,7 @@ __device__ __forceinline__ void tma_warp(const P& p, const View& v, const CUtens
     }
   };
   auto load_values = [&]() {   // by one lane, into a free stage
+    if (values == stall_values) return;
     boxes(v.addr + S::kV + vr.i * S::kHalfBytes, v.bar(S::kVFull + vr.i), late[0].col, late[0]);
   };
   for_segments(p, [&](const Segment& s, int seg) {
@@ -716,8 +723,9 @@ __device__ __forceinline__ void helper_warp(const P& p, const View& v, int lane)
     int later = kNone;
     qr.next();
     if (next != kNone) {
-      if (!warp_wait(p, v, S::kQEmpty + qr.i, qr.phase ^ 1)) return;
+      const bool free = warp_wait(p, v, S::kQEmpty + qr.i, qr.phase ^ 1);
       asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!free) return;
 #pragma unroll 1
       for (int h = 0; h < heads; ++h)
         convert_head<D>(p, v, h < p.G ? staged[32 * h] : QVec<D>{}, qr.i, h, lane);
@@ -727,8 +735,11 @@ __device__ __forceinline__ void helper_warp(const P& p, const View& v, int lane)
       if (lane < kOutWarps) ptx::mbar_arrive(v.bar(S::kQFull + qr.i));
       later = take_and_load();
     }
-    if (!segment_factors<D>(p, v, now, fr, lane)) return;
-    if (next == kNone) return;
+    const bool done = segment_factors<D>(p, v, now, fr, lane);
+    if (!done || next == kNone) {   // (copies asked for may be in flight where it gave up)
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      return;
+    }
     now = next;
     next = later;
   }
@@ -744,7 +755,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
   const int barrier = 2 + 2 * group;
   const int tok = warp * 32 + lane;
   int it = 0;
-  bool fail = false;
+  bool fail = false;   // of this lane; the wait for a step's scores asks all of the warp
   float* wmax = reinterpret_cast<float*>(v.base + S::kWarpMax) + group * kGroupWarps * kMaxG;
   for_segments(p, [&](const Segment& s, int seg) {
     float qs[kMaxG], ref[kMaxG], l[kMaxG];
@@ -771,7 +782,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       float x[kMaxG];
       float sv = 0.f, up = 0.f;
       bool need = false;
-      fail = fail || !wait(p, v, S::kSFull + group, phase);
+      fail = !warp_wait(p, v, S::kSFull + group, phase, !fail);
       if (!fail) {
         const float* sc = reinterpret_cast<const float*>(v.base + S::kScales +
                                                          slot * S::kScaleBytes);
@@ -941,8 +952,8 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
     for (int i = 0; i < steps; ++i, ++it) {
       // A slot is written again four steps on, behind a product that waits
       // for this step's buffer.
-      fail = !wait(p, v, S::kRefFull + it % kRefs, (it / kRefs) & 1) ||
-             !wait(p, v, S::kOFull + (it & 1), (it >> 1) & 1);
+      fail = !warp_wait(p, v, S::kOFull + (it & 1), (it >> 1) & 1,
+                        wait(p, v, S::kRefFull + it % kRefs, (it / kRefs) & 1));
       if (fail) break;
       const float4* slot = reinterpret_cast<const float4*>(v.base + S::kRef) +
                            (it % kRefs) * (kMaxG / 4);
