@@ -14,11 +14,14 @@
 //    each, and a sign between them): 16 columns for 8 heads, exact for values
 //    down to 2^-14 of the head's largest.
 //  * Softmax: a thread per token, two groups of threads taking every other step,
-//    each with its own reference and sum.  Scores are kept relative to a running
-//    reference per head, a multiple of 8 (log2), that bounds x_j + log2 sv_j
-//    (sv the token's V scale), so w_j = 2^(x_j - ref) sv_j lies in [0, 1] and
-//    the largest in (2^-8, 1] whatever the scales; it moves rarely, and then by
-//    an exact power of two.  w is held as kParts e4m3 parts, each the rounding
+//    each with its own references and sum.  A head has two running references,
+//    multiples of 8 (log2).  One, m, is near the largest score x_j and serves the
+//    sum of e_j = 2^(x_j - m), whatever V's scales are.  The other, ref, bounds
+//    x_j + log2 sv_j (sv the token's V scale), so w_j = 2^(x_j - ref) sv_j =
+//    e_j sv_j 2^(m - ref) lies in [0, 1] and the largest in (2^-8, 1] whatever the
+//    scales.  (One reference for both lost keys from the sum where V's scales lay
+//    more than 2^126 apart, and small probabilities beside V scales near 2^100.)
+//    They move rarely, and then by an exact power of two.  w is held as kParts e4m3 parts, each the rounding
 //    of what the parts before left, 32 times finer (that stays below 256 =
 //    2^8, as w 2^8 does): 4 bits and a sign per part, 2^-33 absolute at the end.
 //  * O^T = V^T P^T: M = 128 dims (a step's V codes as they lie, M-major), N =
@@ -45,6 +48,7 @@
 #include <vector>
 
 #include "common.h"
+#include "f32x2.cuh"
 #include "fp8.cuh"
 #include "ptx.cuh"
 #include "split_units.cuh"
@@ -86,9 +90,23 @@ constexpr int kWholeBytes = 1600 << 10;     // beyond an equal share, for units 
 constexpr int kUnitCharge = 3;              // pages that a whole unit costs beside its own
 constexpr int kSnapPages = 4;               // how far a CTA's end moves to a unit's border
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr int kMaxScaleExp = 100;           // largest |log2| of a V scale
+constexpr int kMinScaleExp = -100, kMaxScaleExp = 120;   // log2 of V scales
+// e_j may lie above 1, up to 2^kSlack: a sum of 2^30 of them is still finite.
+constexpr float kSlack = 96.f;
+constexpr float kMaxUnder = 104.f;          // how far ref may lie below m
+// A reference before the first score, and of a head whose scores are all -inf.
+constexpr float kNoRef = -1e30f;
 
 static_assert(kStep == kGroupWarps * 32 && kChunk == kOut, "a thread per token and per dim");
+
+// A softmax group's references, per head; weight: 2^(m - ref) times the first part's
+// scale; by: what the sums are multiplied by at a move; gap: ref - m.
+struct alignas(16) State {
+  float2 minus_m[kMaxG / 2], weight[kMaxG / 2];
+  float4 ref[kMaxG / 4];
+  float2 by[kMaxG / 2], gap[kMaxG / 2];
+};
+constexpr int kStateBytes = sizeof(State);
 
 // Shared memory of a CTA; offsets from a 1024-byte boundary.
 template <int D>
@@ -116,11 +134,22 @@ struct Smem {
   static constexpr int kQScale = kScales + kSlots * kScaleBytes;  // [2][kMaxG]
   static constexpr int kRef = kQScale + 2 * kMaxG * 4;             // [kRefs][kMaxG]
   static constexpr int kSegL = kRef + kRefs * kMaxG * 4;           // [2][warp][kMaxG]
-  static constexpr int kSegRef = kSegL + 2 * kSoftmaxWarps * kMaxG * 4;   // [2][group][kMaxG]
-  static constexpr int kWarpMax = kSegRef + 2 * kGroups * kMaxG * 4;      // [warp][kMaxG]
-  // [2][factor | reference | sum][kMaxG]
-  static constexpr int kFactor = kWarpMax + kSoftmaxWarps * kMaxG * 4;
-  static constexpr int kBars = kFactor + 2 * 3 * kMaxG * 4;
+  // [2][group][m | ref][kMaxG]
+  static constexpr int kSegRef = kSegL + 2 * kSoftmaxWarps * kMaxG * 4;
+  // A group's references now (see State), and what a move of them looks at: log2 sv
+  // of the step's blocks, and its scores [token][head].  At 256 dims the scores lie in
+  // the group's buffer of P, once the product before is done with it; at 128 there is
+  // room for one of their own (256 x 512 tokens in a buffer of P 56.4 us, so 54.7).
+  static constexpr int kState = kSegRef + 2 * kGroups * 2 * kMaxG * 4;   // [group]
+  static constexpr int kUp = kState + kGroups * kStateBytes;             // [group][block]
+  static constexpr bool kOwnScores = D == 128;
+  static constexpr int kScores = kOwnScores ? kUp + kGroups * kStepBlocks * 4 : kP;
+  static constexpr int kScoreBytes = kStep * kMaxG * 4;
+  static_assert(kOwnScores || kScoreBytes == kPBytes, "scores in a buffer of P");
+  // [2][two factors | m | sum][kMaxG]
+  static constexpr int kFactor =
+      kUp + kGroups * (kStepBlocks * 4 + (kOwnScores ? kScoreBytes : 0));
+  static constexpr int kBars = kFactor + 2 * 4 * kMaxG * 4;
   // mbarriers: full, empty per K and V stage; S, P, product, q, sums: full and
   // empty; all of a warp's products done; reference slots written; a segment's
   // factors: full and empty
@@ -326,14 +355,6 @@ __device__ __forceinline__ void copy_own(uint32_t dst, const T* src) {
 }
 __device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// Largest of a warp's floats (NaN ignored): integer maximum of an order-preserving
-// mapping.
-__device__ __forceinline__ float warp_max(float x) {
-  const int b = __float_as_int(fmaxf(x, -INFINITY));
-  const int m = __reduce_max_sync(0xffffffffu, b ^ ((b >> 31) & 0x7fffffff));
-  return __int_as_float(m ^ ((m >> 31) & 0x7fffffff));
 }
 
 // ---------------------------------------------------------------------------
@@ -637,36 +658,42 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, int s
     return false;
   const float* seg_l = reinterpret_cast<const float*>(v.base + S::kSegL) +
                        r.i * kSoftmaxWarps * kMaxG;
-  const float* sr = reinterpret_cast<const float*>(v.base + S::kSegRef) + r.i * kGroups * kMaxG;
-  float* factor = reinterpret_cast<float*>(v.base + S::kFactor) + r.i * 3 * kMaxG;
+  const float* sr = reinterpret_cast<const float*>(v.base + S::kSegRef) +
+                    r.i * kGroups * 2 * kMaxG;
+  float* factor = reinterpret_cast<float*>(v.base + S::kFactor) + r.i * 4 * kMaxG;
   const bool nan = (v.seg_poison[r.i * kGroups] | v.seg_poison[r.i * kGroups + 1]) != 0;
   if (lane < kMaxG) {
     const float qnan = __int_as_float(0x7fc00000);
-    float m = -INFINITY, l = 0.f, f;
+    float m = kNoRef, ref = kNoRef, l = 0.f;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) m = fmaxf(m, sr[g * kMaxG + lane]);
+    for (int g = 0; g < kGroups; ++g) {
+      m = fmaxf(m, sr[g * 2 * kMaxG + lane]);
+      ref = fmaxf(ref, sr[(g * 2 + 1) * kMaxG + lane]);
+    }
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const float* w = seg_l + g * kGroupWarps * kMaxG + lane;
-      l = fmaf(ref_weight(sr[g * kMaxG + lane], m),
+      l = fmaf(ref_weight(sr[g * 2 * kMaxG + lane], m),
                (w[0] + w[kMaxG]) + (w[2 * kMaxG] + w[3 * kMaxG]), l);
     }
+    // The sum of products is relative to ref; the output, or the partial, to the sum's
+    // own magnitude 2^(m + k), with l 2^-k in (2^-8, 1].  (Two factors: 2^(ref - m - k)
+    // may be as large as the largest V scale.)
+    const int k = l > 0.f ? ((__float_as_int(l) >> 23) - 127 + 8) >> 3 << 3 : 0;
+    const int by = max(-240, min(240, (int)(ref - m) - k));
+    l *= ptx::pow2i(max(-126, -k));
+    float f = ptx::pow2i(by - (by >> 1));
     if (slot < 0) {
-      f = 1.0f / l;
+      f /= l;
       // for the log-sum-exp, which the output warps take from these
-      factor[kMaxG + lane] = m;
-      factor[2 * kMaxG + lane] = nan ? qnan : l;
+      factor[2 * kMaxG + lane] = m + (float)k;
+      factor[3 * kMaxG + lane] = nan ? qnan : l;
     } else {
-      // The reference bounds V's scales too; the partial's is moved to the
-      // sum's own magnitude, so that partials of blocks whose V scales lie far
-      // apart still meet near their weights.
-      const int e = l > 0.f ? ((__float_as_int(l) >> 23) - 127 + 4) >> 3 << 3 : 0;
-      const int k = max(-112, min(112, e));
-      f = ptx::pow2i(-k);
       reinterpret_cast<float2*>(p.part_ml)[(size_t)slot * kMaxG + lane] =
-          make_float2(nan ? qnan : m + (float)k, l * f);
+          make_float2(nan ? qnan : m + (float)k, l);
     }
-    factor[lane] = nan ? qnan : f;
+    factor[lane] = ptx::pow2i(by >> 1);
+    factor[kMaxG + lane] = nan ? qnan : f;
   }
   __syncwarp();
   if (lane == 0) {
@@ -756,20 +783,24 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
   const int tok = warp * 32 + lane;
   int it = 0;
   bool fail = false;   // of this lane; the wait for a step's scores asks all of the warp
-  float* wmax = reinterpret_cast<float*>(v.base + S::kWarpMax) + group * kGroupWarps * kMaxG;
+  State& st = reinterpret_cast<State*>(v.base + S::kState)[group];
+  float* ups = reinterpret_cast<float*>(v.base + S::kUp) + group * kStepBlocks;
+  float* scores = reinterpret_cast<float*>(v.base + S::kScores + group * S::kScoreBytes);
   for_segments(p, [&](const Segment& s, int seg) {
-    float qs[kMaxG], ref[kMaxG], l[kMaxG];
+    // Tokens whose log2 sv is below `lowest` might lie above m by more than kSlack.
+    float2 qs[kMaxG / 2], l[kMaxG / 2];
+    float lowest = 0.f;
     fail |= !wait(p, v, S::kQFull + (seg & 1), (seg >> 1) & 1);
-    const float* qscale = reinterpret_cast<float*>(v.base + S::kQScale) + (seg & 1) * kMaxG;
+    const float2* qscale = reinterpret_cast<float2*>(v.base + S::kQScale) + (seg & 1) * (kMaxG / 2);
 #pragma unroll
-    for (int h = 0; h < kMaxG; ++h) {
+    for (int h = 0; h < kMaxG / 2; ++h) {
       qs[h] = qscale[h];
-      ref[h] = -INFINITY;
-      l[h] = 0.f;
+      l[h] = f32x2::both(0.f);
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(v.bar(S::kQEmpty + (seg & 1)));
     int poisoned = 0;
+    bool first = true;
     const int steps = s.steps();
     for (int i = 0; i < steps; ++i, ++it) {
       if ((it & 1) != group) continue;
@@ -779,9 +810,8 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       const int pages = min(2, s.hi - (s.lo + 2 * i));
       const bool loaded = tok < pages * kPage;
       const bool live = loaded && tok0 + tok >= s.U.tok_start && tok0 + tok < s.U.tok_end;
-      float x[kMaxG];
+      float2 x[kMaxG / 2];
       float sv = 0.f, up = 0.f;
-      bool need = false;
       fail = !warp_wait(p, v, S::kSFull + group, phase, !fail);
       if (!fail) {
         const float* sc = reinterpret_cast<const float*>(v.base + S::kScales +
@@ -796,66 +826,101 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
         tc::fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(v.bar(S::kSEmpty + group));
-        // 2^up >= |sv|
+        // 2^up >= |sv| (a scale of zero weighs nothing)
         const unsigned sb = __float_as_uint(sv) & 0x7fffffffu;
-        if (!(fabsf(sv) <= ptx::pow2i(kMaxScaleExp))) sv = __int_as_float(0x7fc00000);
         up = (float)max(min((int)(sb >> 23) - 127 + ((sb & 0x7fffffu) ? 1 : 0), kMaxScaleExp),
-                        -kMaxScaleExp);
+                        kMinScaleExp);
+        if (sb == 0) up = kNoRef;
+        if (!(fabsf(sv) <= ptx::pow2i(kMaxScaleExp))) sv = __int_as_float(0x7fc00000);
+        if (!live) sv = 0.f;   // whatever its row holds
 #pragma unroll
-        for (int h = 0; h < kMaxG; ++h) {
-          const float d = __uint_as_float(r[h]) + __uint_as_float(r[kMaxG + h]) * 0.0625f;
-          x[h] = live ? d * sk * qs[h] : -INFINITY;
-          need |= x[h] + up > ref[h];
+        for (int h = 0; h < kMaxG / 2; ++h) {
+          auto pair = [&](int k) {
+            return make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+          };
+          const float2 d = f32x2::fma(pair(kMaxG + 2 * h), f32x2::both(0.0625f), pair(2 * h));
+          x[h] = f32x2::mul(f32x2::mul(d, f32x2::both(sk)), qs[h]);
+          if (!live) x[h] = f32x2::both(-INFINITY);
         }
       }
-      if (any_in_group(barrier, kStep, need || fail)) {
-        if (any_in_group(barrier + 1, kStep, fail)) return false;
+      float2 e[kMaxG / 2], w[kMaxG / 2];
+      for (bool move = first;; move = true) {
+        if (move) {
+          // The references move: sixteen threads look at a head's scores, eight tokens of
+          // one block each.
+          if (!S::kOwnScores) fail |= !wait(p, v, S::kOFull + group, phase ^ 1);
+          if (any_in_group(barrier + 1, kStep, fail)) return false;
+          if (tok % kBlock == 0) ups[tok / kBlock] = up;
 #pragma unroll
-        for (int h = 0; h < kMaxG; ++h) {
-          const float m = warp_max(x[h] + up);
-          if (lane == 0) wmax[warp * kMaxG + h] = m;
+          for (int k = 0; k < kMaxG / 4; ++k)
+            reinterpret_cast<float4*>(scores + tok * kMaxG)[k] =
+                make_float4(x[2 * k].x, x[2 * k].y, x[2 * k + 1].x, x[2 * k + 1].y);
+          ptx::named_barrier(barrier, kStep);
+          const int h = tok >> 4, first_tok = (tok & 15) * 8;
+          float a = -INFINITY;   // largest x, and x + log2 sv (NaN ignored)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)   // (each thread begins at another bank)
+            a = fmaxf(a, scores[(first_tok + ((k + tok) & 7)) * kMaxG + h]);
+          float b = a + ups[first_tok / kBlock];
+#pragma unroll
+          for (int k = 1; k < 16; k <<= 1) {
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, k));
+            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, k));
+          }
+          if ((tok & 15) == 0) {
+            auto at = [&](void* f) -> float& { return reinterpret_cast<float*>(f)[h]; };
+            const float old = first ? kNoRef : -at(st.minus_m), m = fmaxf(old, ref_ceil(a));
+            const float ref = fmaxf(fmaxf(first ? kNoRef : at(st.ref), ref_ceil(b)), m - kMaxUnder);
+            at(st.minus_m) = -m;
+            at(st.ref) = ref;
+            at(st.weight) = kFirstPart * ptx::pow2i((int)(m - ref));
+            at(st.by) = ref_weight(old, m);
+            // (a head without a reference yet looks at every token)
+            at(st.gap) = m == kNoRef ? -kNoRef : ref - m;
+          }
+          ptx::named_barrier(barrier, kStep);
+          lowest = kNoRef;
+#pragma unroll
+          for (int h = 0; h < kMaxG / 2; ++h) {
+            lowest = fmaxf(lowest, fmaxf(st.gap[h].x, st.gap[h].y));
+            l[h] = f32x2::mul(l[h], st.by[h]);
+          }
+          lowest -= kSlack;
+          first = false;
         }
-        ptx::named_barrier(barrier, kStep);
+        float most = 0.f;
 #pragma unroll
-        for (int h = 0; h < kMaxG; ++h) {
-          float m = wmax[h];
-#pragma unroll
-          for (int w = 1; w < kGroupWarps; ++w) m = fmaxf(m, wmax[w * kMaxG + h]);
-          const float to = fmaxf(ref[h], ref_ceil(m));
-          l[h] *= ref_weight(ref[h], to);
-          ref[h] = to;
+        for (int h = 0; h < kMaxG / 2; ++h) {
+          const float2 y = f32x2::add(x[h], st.minus_m[h]);
+          e[h] = make_float2(ptx::ex2(y.x), ptx::ex2(y.y));
+          w[h] = f32x2::mul(f32x2::mul(e[h], f32x2::both(sv)), st.weight[h]);
+          most = fmaxf(most, fmaxf(w[h].x, w[h].y));
         }
+        const bool need = most > kFirstPart || (live && up < lowest);
+        if (move || !any_in_group(barrier, kStep, need || fail)) break;
       }
       // Step it - 2's product is done: its P buffer is free, and so is the
       // reference slot of step it - 4 (the product waited for the output warps
       // to be through with that step).
       fail = !wait(p, v, S::kOFull + group, phase ^ 1);
       if (tok == 0) {
-        float* to = reinterpret_cast<float*>(v.base + S::kRef) + (it % kRefs) * kMaxG;
+        float4* to = reinterpret_cast<float4*>(v.base + S::kRef) + (it % kRefs) * (kMaxG / 4);
 #pragma unroll
-        for (int h = 0; h < kMaxG; ++h) to[h] = ref[h];
+        for (int k = 0; k < kMaxG / 4; ++k) to[k] = st.ref[k];
         ptx::mbar_arrive(v.bar(S::kRefFull + it % kRefs));
       }
       uint32_t codes[2 * kParts];   // this token's row: kParts times the eight heads
 #pragma unroll
-      for (int h = 0; h < kMaxG; h += 2) {
-        float w[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float e = ptx::ex2(x[h + k] - (ref[h + k] == -INFINITY ? 0.f : ref[h + k]));
-          l[h + k] += e;
-          w[k] = live ? e * sv * kFirstPart : 0.f;
-        }
+      for (int h = 0; h < kMaxG / 2; ++h) {
+        l[h] = f32x2::add(l[h], e[h]);
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
-          const uint32_t c = fp8::pack2(w[0], w[1]);
-          uint32_t& to = codes[2 * part + h / 4];
-          to = h % 4 ? to | c << 16 : c;
-          if (part + 1 < kParts) {
-            const float2 f = fp8::unpack2(c);
-            w[0] = (w[0] - f.x) * kPartRatio;
-            w[1] = (w[1] - f.y) * kPartRatio;
-          }
+          const uint32_t c = fp8::pack2(w[h].x, w[h].y);
+          uint32_t& to = codes[2 * part + h / 2];
+          to = h % 2 ? to | c << 16 : c;
+          if (part + 1 < kParts)   // (w - c) kPartRatio
+            w[h] = f32x2::fma(fp8::unpack2(c), f32x2::both(-kPartRatio),
+                              f32x2::mul(w[h], f32x2::both(kPartRatio)));
         }
       }
       const uint32_t prow = v.addr + S::kP + group * S::kPBytes + tok * kPCols;
@@ -889,23 +954,31 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
                    ((seg & 1) * kSoftmaxWarps + group * kGroupWarps + warp) * kMaxG;
     // Eight sums over 32 lanes: each exchange halves the heads a lane holds, the
     // last two add lanes of one head.
+    float sum[kMaxG];
+#pragma unroll
+    for (int h = 0; h < kMaxG; ++h) sum[h] = h % 2 ? l[h / 2].y : l[h / 2].x;
 #pragma unroll
     for (int n = kMaxG / 2; n; n >>= 1) {
       const bool upper = lane & (4 * n);
 #pragma unroll
       for (int h = 0; h < n; ++h) {
-        const float give = upper ? l[h] : l[h + n];
-        l[h] = (upper ? l[h + n] : l[h]) + __shfl_xor_sync(0xffffffffu, give, 4 * n);
+        const float give = upper ? sum[h] : sum[h + n];
+        sum[h] = (upper ? sum[h + n] : sum[h]) + __shfl_xor_sync(0xffffffffu, give, 4 * n);
       }
     }
-    l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
-    l[0] += __shfl_xor_sync(0xffffffffu, l[0], 2);
-    if ((lane & 3) == 0) seg_l[lane >> 2] = l[0];
+    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
+    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
+    if ((lane & 3) == 0) seg_l[lane >> 2] = sum[0];
     if (tok == 0) {
-      float* sr = reinterpret_cast<float*>(v.base + S::kSegRef) +
-                  ((seg & 1) * kGroups + group) * kMaxG;
+      float4* sr = reinterpret_cast<float4*>(v.base + S::kSegRef) +
+                   ((seg & 1) * kGroups + group) * 2 * (kMaxG / 4);
+      const float4 none = make_float4(kNoRef, kNoRef, kNoRef, kNoRef);
 #pragma unroll
-      for (int h = 0; h < kMaxG; ++h) sr[h] = ref[h];
+      for (int k = 0; k < kMaxG / 4; ++k) {
+        const float4 m = reinterpret_cast<const float4*>(st.minus_m)[k];
+        sr[k] = first ? none : make_float4(-m.x, -m.y, -m.z, -m.w);
+        sr[kMaxG / 4 + k] = first ? none : st.ref[k];
+      }
       v.seg_poison[(seg & 1) * kGroups + group] = poisoned;
     }
     __syncwarp();
@@ -943,7 +1016,7 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
     float acc[S::kChunks][kMaxG], ref[kMaxG];
 #pragma unroll
     for (int h = 0; h < kMaxG; ++h) {
-      ref[h] = -INFINITY;
+      ref[h] = kNoRef;
 #pragma unroll
       for (int c = 0; c < S::kChunks; ++c) acc[c][h] = 0.f;
     }
@@ -1010,12 +1083,12 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
     if (any_in_group(1, kOut, fail)) return false;
     // ---- the segment's output or partial ----
     const float* factor = reinterpret_cast<const float*>(v.base + S::kFactor) +
-                          (seg & 1) * 3 * kMaxG;
+                          (seg & 1) * 4 * kMaxG;
     float m = 0.f, l = 0.f;
     const bool has_lse = s.whole() && warp == 0 && lane < p.G;
     if (has_lse) {
-      m = factor[kMaxG + lane];
-      l = factor[2 * kMaxG + lane];
+      m = factor[2 * kMaxG + lane];
+      l = factor[3 * kMaxG + lane];
     }
     const size_t orow = (size_t)s.bt * p.Hq + s.g * p.G;
     float* dst = (s.whole() ? p.out + orow * D : p.part_o + s.slot() * kMaxG * D) + ct;
@@ -1023,11 +1096,12 @@ __device__ __forceinline__ void output_warps(const P& p, const View& v, uint32_t
 #pragma unroll
     for (int h = 0; h < kMaxG; ++h) {
       if (h >= p.G) break;
-      const float f = factor[h];
+      const float f = factor[h], f2 = factor[kMaxG + h];
 #pragma unroll
       for (int c = 0; c < S::kChunks; ++c) {
-        dst[h * D + c * kChunk] = acc[c][h] * f;
-        if (dst2) dst2[h * D + c * kChunk] = acc[c][h] * f;
+        const float y = acc[c][h] * f * f2;
+        dst[h * D + c * kChunk] = y;
+        if (dst2) dst2[h * D + c * kChunk] = y;
       }
     }
     __syncwarp();
