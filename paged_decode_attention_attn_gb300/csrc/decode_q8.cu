@@ -21,9 +21,14 @@
 //    e_j sv_j 2^(m - ref) lies in [0, 1] and the largest in (2^-8, 1] whatever the
 //    scales.  (One reference for both lost keys from the sum where V's scales lay
 //    more than 2^126 apart, and small probabilities beside V scales near 2^100.)
-//    They move rarely, and then by an exact power of two.  w is held as kParts e4m3 parts, each the rounding
-//    of what the parts before left, 32 times finer (that stays below 256 =
-//    2^8, as w 2^8 does): 4 bits and a sign per part, 2^-33 absolute at the end.
+//    They move rarely, and then by an exact power of two.  w is cut to 19 bits
+//    and held as kParts e4m3 parts, each the rounding of what the parts before left,
+//    32 times finer (that stays below 256 = 2^8, as w 2^8 does): a part takes 5 bits
+//    (4 and a sign), so the parts hold all 19, or what lies above 2^-33 of the row's
+//    bound.  The outputs are divided by the sum of these probabilities as they were
+//    cut, so a row that hangs on few keys loses nothing to that; the log-sum-exp takes
+//    the sum of the whole ones.  (|sv| = f 2^k with 1 <= f < 2: it is e_j f that is cut,
+//    and what the sums get is divided by f.)
 //  * O^T = V^T P^T: M = 128 dims (a step's V codes as they lie, M-major), N =
 //    8 kParts (a token's row of P, N-major), K = 128 tokens.  Every step's
 //    product starts from zero in tensor memory and is added to fp32 registers (a
@@ -102,8 +107,7 @@ static_assert(kStep == kGroupWarps * 32 && kChunk == kOut, "a thread per token a
 // A softmax group's references, per head; weight: 2^(m - ref) times the first part's
 // scale; by: what the sums are multiplied by at a move; gap: ref - m.
 struct alignas(16) State {
-  float2 minus_m[kMaxG / 2], weight[kMaxG / 2];
-  float4 ref[kMaxG / 4];
+  float2 minus_m[kMaxG / 2], weight[kMaxG / 2], minus_ref[kMaxG / 2];
   float2 by[kMaxG / 2], gap[kMaxG / 2];
 };
 constexpr int kStateBytes = sizeof(State);
@@ -133,9 +137,9 @@ struct Smem {
   static constexpr int kScaleBytes = 2 * kStepBlocks * 4;
   static constexpr int kQScale = kScales + kSlots * kScaleBytes;  // [2][kMaxG]
   static constexpr int kRef = kQScale + 2 * kMaxG * 4;             // [kRefs][kMaxG]
-  static constexpr int kSegL = kRef + kRefs * kMaxG * 4;           // [2][warp][kMaxG]
+  static constexpr int kSegL = kRef + kRefs * kMaxG * 4;    // [2][warp][sums | rounded][kMaxG]
   // [2][group][m | ref][kMaxG]
-  static constexpr int kSegRef = kSegL + 2 * kSoftmaxWarps * kMaxG * 4;
+  static constexpr int kSegRef = kSegL + 2 * kSoftmaxWarps * 2 * kMaxG * 4;
   // A group's references now (see State), and what a move of them looks at: log2 sv
   // of the step's blocks, and its scores [token][head].  At 256 dims the scores lie in
   // the group's buffer of P, once the product before is done with it; at 128 there is
@@ -146,9 +150,10 @@ struct Smem {
   static constexpr int kScores = kOwnScores ? kUp + kGroups * kStepBlocks * 4 : kP;
   static constexpr int kScoreBytes = kStep * kMaxG * 4;
   static_assert(kOwnScores || kScoreBytes == kPBytes, "scores in a buffer of P");
-  // [2][two factors | m | sum][kMaxG]
-  static constexpr int kFactor =
+  static constexpr int kQs =   // a softmax warp's scales of q: [warp][kMaxG]
       kUp + kGroups * (kStepBlocks * 4 + (kOwnScores ? kScoreBytes : 0));
+  // [2][two factors | m | sum][kMaxG]
+  static constexpr int kFactor = kQs + kSoftmaxWarps * kMaxG * 4;
   static constexpr int kBars = kFactor + 2 * 4 * kMaxG * 4;
   // mbarriers: full, empty per K and V stage; S, P, product, q, sums: full and
   // empty; all of a warp's products done; reference slots written; a segment's
@@ -657,14 +662,14 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, int s
       !warp_wait(p, v, S::kLFull + r.i, r.phase))
     return false;
   const float* seg_l = reinterpret_cast<const float*>(v.base + S::kSegL) +
-                       r.i * kSoftmaxWarps * kMaxG;
+                       r.i * kSoftmaxWarps * 2 * kMaxG;
   const float* sr = reinterpret_cast<const float*>(v.base + S::kSegRef) +
                     r.i * kGroups * 2 * kMaxG;
   float* factor = reinterpret_cast<float*>(v.base + S::kFactor) + r.i * 4 * kMaxG;
   const bool nan = (v.seg_poison[r.i * kGroups] | v.seg_poison[r.i * kGroups + 1]) != 0;
   if (lane < kMaxG) {
     const float qnan = __int_as_float(0x7fc00000);
-    float m = kNoRef, ref = kNoRef, l = 0.f;
+    float m = kNoRef, ref = kNoRef, l = 0.f, rounded = 0.f;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       m = fmaxf(m, sr[g * 2 * kMaxG + lane]);
@@ -672,25 +677,29 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, int s
     }
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
-      const float* w = seg_l + g * kGroupWarps * kMaxG + lane;
-      l = fmaf(ref_weight(sr[g * 2 * kMaxG + lane], m),
-               (w[0] + w[kMaxG]) + (w[2 * kMaxG] + w[3 * kMaxG]), l);
+      const float* w = seg_l + g * kGroupWarps * 2 * kMaxG + lane;
+      const float a = ref_weight(sr[g * 2 * kMaxG + lane], m);
+      l = fmaf(a, (w[0] + w[2 * kMaxG]) + (w[4 * kMaxG] + w[6 * kMaxG]), l);
+      w += kMaxG;
+      rounded = fmaf(a, (w[0] + w[2 * kMaxG]) + (w[4 * kMaxG] + w[6 * kMaxG]), rounded);
     }
     // The sum of products is relative to ref; the output, or the partial, to the sum's
     // own magnitude 2^(m + k), with l 2^-k in (2^-8, 1].  (Two factors: 2^(ref - m - k)
     // may be as large as the largest V scale.)
     const int k = l > 0.f ? ((__float_as_int(l) >> 23) - 127 + 8) >> 3 << 3 : 0;
     const int by = max(-240, min(240, (int)(ref - m) - k));
-    l *= ptx::pow2i(max(-126, -k));
-    float f = ptx::pow2i(by - (by >> 1));
+    const float scale = ptx::pow2i(max(-126, -k));
+    l *= scale;
+    rounded *= scale;
+    float f = ptx::pow2i(by - (by >> 1)) / rounded;
     if (slot < 0) {
-      f /= l;
       // for the log-sum-exp, which the output warps take from these
       factor[2 * kMaxG + lane] = m + (float)k;
       factor[3 * kMaxG + lane] = nan ? qnan : l;
     } else {
       reinterpret_cast<float2*>(p.part_ml)[(size_t)slot * kMaxG + lane] =
           make_float2(nan ? qnan : m + (float)k, l);
+      f *= l;   // a partial's products belong to the sum that the merge divides by
     }
     factor[lane] = ptx::pow2i(by >> 1);
     factor[kMaxG + lane] = nan ? qnan : f;
@@ -772,6 +781,20 @@ __device__ __forceinline__ void helper_warp(const P& p, const View& v, int lane)
   }
 }
 
+__device__ __forceinline__ float warp_max(float x) {   // (NaN ignored)
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float2 negative(float2 x) { return make_float2(-x.x, -x.y); }
+
+// Cut off behind 19 bits (NaN stays).
+__device__ __forceinline__ float2 cut19(float2 x) {
+  return make_float2(__uint_as_float(__float_as_uint(x.x) & ~31u),
+                     __uint_as_float(__float_as_uint(x.y) & ~31u));
+}
+
 // ---------------------------------------------------------------------------
 // Warps 0-3 and 4-7: a thread per token of every other step.
 // ---------------------------------------------------------------------------
@@ -786,17 +809,16 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
   State& st = reinterpret_cast<State*>(v.base + S::kState)[group];
   float* ups = reinterpret_cast<float*>(v.base + S::kUp) + group * kStepBlocks;
   float* scores = reinterpret_cast<float*>(v.base + S::kScores + group * S::kScoreBytes);
+  float* qs = reinterpret_cast<float*>(v.base + S::kQs) + (group * kGroupWarps + warp) * kMaxG;
   for_segments(p, [&](const Segment& s, int seg) {
     // Tokens whose log2 sv is below `lowest` might lie above m by more than kSlack.
-    float2 qs[kMaxG / 2], l[kMaxG / 2];
+    float2 l[kMaxG / 2], rounded[kMaxG / 2];
     float lowest = 0.f;
     fail |= !wait(p, v, S::kQFull + (seg & 1), (seg >> 1) & 1);
-    const float2* qscale = reinterpret_cast<float2*>(v.base + S::kQScale) + (seg & 1) * (kMaxG / 2);
+    if (lane < kMaxG)
+      qs[lane] = reinterpret_cast<const float*>(v.base + S::kQScale)[(seg & 1) * kMaxG + lane];
 #pragma unroll
-    for (int h = 0; h < kMaxG / 2; ++h) {
-      qs[h] = qscale[h];
-      l[h] = f32x2::both(0.f);
-    }
+    for (int h = 0; h < kMaxG / 2; ++h) l[h] = rounded[h] = f32x2::both(0.f);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(v.bar(S::kQEmpty + (seg & 1)));
     int poisoned = 0;
@@ -812,6 +834,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       const bool live = loaded && tok0 + tok >= s.U.tok_start && tok0 + tok < s.U.tok_end;
       float2 x[kMaxG / 2];
       float sv = 0.f, up = 0.f;
+      unsigned fraction = 0;
       fail = !warp_wait(p, v, S::kSFull + group, phase, !fail);
       if (!fail) {
         const float* sc = reinterpret_cast<const float*>(v.base + S::kScales +
@@ -826,12 +849,16 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
         tc::fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(v.bar(S::kSEmpty + group));
-        // 2^up >= |sv| (a scale of zero weighs nothing)
+        // |sv| = f 2^k with 1 <= f < 2, of which 2^k stays in sv; up: its logarithm rounded
+        // up (a scale of zero weighs nothing).
         const unsigned sb = __float_as_uint(sv) & 0x7fffffffu;
-        up = (float)max(min((int)(sb >> 23) - 127 + ((sb & 0x7fffffu) ? 1 : 0), kMaxScaleExp),
+        const bool fits = sb <= __float_as_uint(ptx::pow2i(kMaxScaleExp));
+        fraction = sb & 0x7fffffu;
+        up = (float)max(min((int)(sb >> 23) - 127 + (fraction ? 1 : 0), kMaxScaleExp),
                         kMinScaleExp);
         if (sb == 0) up = kNoRef;
-        if (!(fabsf(sv) <= ptx::pow2i(kMaxScaleExp))) sv = __int_as_float(0x7fc00000);
+        sv = __uint_as_float(__float_as_uint(sv) & 0xff800000u);
+        if (!fits) sv = __int_as_float(0x7fc00000);
         if (!live) sv = 0.f;   // whatever its row holds
 #pragma unroll
         for (int h = 0; h < kMaxG / 2; ++h) {
@@ -839,90 +866,118 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
             return make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
           };
           const float2 d = f32x2::fma(pair(kMaxG + 2 * h), f32x2::both(0.0625f), pair(2 * h));
-          x[h] = f32x2::mul(f32x2::mul(d, f32x2::both(sk)), qs[h]);
-          if (!live) x[h] = f32x2::both(-INFINITY);
+          x[h] = f32x2::mul(f32x2::mul(d, f32x2::both(sk)), reinterpret_cast<float2*>(qs)[h]);
+        }
+        if (pages < 2 || tok0 < s.U.tok_start || tok0 + kStep > s.U.tok_end) {
+#pragma unroll
+          for (int h = 0; h < kMaxG / 2; ++h)
+            if (!live) x[h] = f32x2::both(-INFINITY);
         }
       }
-      float2 e[kMaxG / 2], w[kMaxG / 2];
-      for (bool move = first;; move = true) {
-        if (move) {
-          // The references move: sixteen threads look at a head's scores, eight tokens of
-          // one block each.
-          if (!S::kOwnScores) fail |= !wait(p, v, S::kOFull + group, phase ^ 1);
-          if (any_in_group(barrier + 1, kStep, fail)) return false;
-          if (tok % kBlock == 0) ups[tok / kBlock] = up;
-#pragma unroll
-          for (int k = 0; k < kMaxG / 4; ++k)
-            reinterpret_cast<float4*>(scores + tok * kMaxG)[k] =
-                make_float4(x[2 * k].x, x[2 * k].y, x[2 * k + 1].x, x[2 * k + 1].y);
-          ptx::named_barrier(barrier, kStep);
-          const int h = tok >> 4, first_tok = (tok & 15) * 8;
-          float a = -INFINITY;   // largest x, and x + log2 sv (NaN ignored)
-#pragma unroll
-          for (int k = 0; k < 8; ++k)   // (each thread begins at another bank)
-            a = fmaxf(a, scores[(first_tok + ((k + tok) & 7)) * kMaxG + h]);
-          float b = a + ups[first_tok / kBlock];
-#pragma unroll
-          for (int k = 1; k < 16; k <<= 1) {
-            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, k));
-            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, k));
-          }
-          if ((tok & 15) == 0) {
-            auto at = [&](void* f) -> float& { return reinterpret_cast<float*>(f)[h]; };
-            const float old = first ? kNoRef : -at(st.minus_m), m = fmaxf(old, ref_ceil(a));
-            const float ref = fmaxf(fmaxf(first ? kNoRef : at(st.ref), ref_ceil(b)), m - kMaxUnder);
-            at(st.minus_m) = -m;
-            at(st.ref) = ref;
-            at(st.weight) = kFirstPart * ptx::pow2i((int)(m - ref));
-            at(st.by) = ref_weight(old, m);
-            // (a head without a reference yet looks at every token)
-            at(st.gap) = m == kNoRef ? -kNoRef : ref - m;
-          }
-          ptx::named_barrier(barrier, kStep);
-          lowest = kNoRef;
-#pragma unroll
-          for (int h = 0; h < kMaxG / 2; ++h) {
-            lowest = fmaxf(lowest, fmaxf(st.gap[h].x, st.gap[h].y));
-            l[h] = f32x2::mul(l[h], st.by[h]);
-          }
-          lowest -= kSlack;
-          first = false;
-        }
-        float most = 0.f;
+      bool move = first;
+      if (!move) {
+        // A token above a ref, or one that might lie too far above an m?
+        float most = -INFINITY;
 #pragma unroll
         for (int h = 0; h < kMaxG / 2; ++h) {
-          const float2 y = f32x2::add(x[h], st.minus_m[h]);
-          e[h] = make_float2(ptx::ex2(y.x), ptx::ex2(y.y));
-          w[h] = f32x2::mul(f32x2::mul(e[h], f32x2::both(sv)), st.weight[h]);
-          most = fmaxf(most, fmaxf(w[h].x, w[h].y));
+          const float2 y = f32x2::add(x[h], st.minus_ref[h]);
+          most = fmaxf(most, fmaxf(y.x, y.y));
         }
-        const bool need = most > kFirstPart || (live && up < lowest);
-        if (move || !any_in_group(barrier, kStep, need || fail)) break;
+        move = any_in_group(barrier, kStep, fail || most > -up || (live && up < lowest));
+      }
+      if (move) {
+        // The references move.
+        if (!S::kOwnScores) fail |= !wait(p, v, S::kOFull + group, phase ^ 1);
+        if (tok % kBlock == 0) ups[tok / kBlock] = up;
+#pragma unroll
+        for (int k = 0; k < kMaxG / 4; ++k)
+          reinterpret_cast<float4*>(scores + tok * kMaxG)[k] =
+              make_float4(x[2 * k].x, x[2 * k].y, x[2 * k + 1].x, x[2 * k + 1].y);
+        if (any_in_group(barrier + 1, kStep, fail)) return false;
+        // A warp looks at two heads, a lane at every 32nd token.
+        float a[2], b[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          a[i] = b[i] = -INFINITY;   // largest x, and x + log2 sv (NaN ignored)
+#pragma unroll
+          for (int k = 0; k < kStep / 32; ++k) {
+            const float y = scores[(lane + 32 * k) * kMaxG + 2 * warp + i];
+            a[i] = fmaxf(a[i], y);
+            b[i] = fmaxf(b[i], y + ups[(lane + 32 * k) / kBlock]);
+          }
+          a[i] = warp_max(a[i]);
+          b[i] = warp_max(b[i]);
+        }
+        if (lane < 2) {
+          const int h = 2 * warp + lane;
+          const float top = lane ? a[1] : a[0], top_sv = lane ? b[1] : b[0];
+          auto at = [&](void* f) -> float& { return reinterpret_cast<float*>(f)[h]; };
+          const float old = first ? kNoRef : -at(st.minus_m), m = fmaxf(old, ref_ceil(top));
+          const float had = first ? kNoRef : -at(st.minus_ref);
+          const float ref = fmaxf(fmaxf(had, ref_ceil(top_sv)), m - kMaxUnder);
+          at(st.minus_m) = -m;
+          at(st.minus_ref) = -ref;
+          at(st.weight) = kFirstPart * ptx::pow2i((int)(m - ref));
+          at(st.by) = ref_weight(old, m);
+          // (a head without a reference yet looks at every token)
+          at(st.gap) = m == kNoRef ? -kNoRef : ref - m;
+        }
+        ptx::named_barrier(barrier, kStep);
+        lowest = kNoRef;
+#pragma unroll
+        for (int h = 0; h < kMaxG / 2; ++h) {
+          lowest = fmaxf(lowest, fmaxf(st.gap[h].x, st.gap[h].y));
+          l[h] = f32x2::mul(l[h], st.by[h]);
+          rounded[h] = f32x2::mul(rounded[h], st.by[h]);
+        }
+        lowest -= kSlack;
+        first = false;
+      }
+      float2 e[kMaxG / 2];
+#pragma unroll
+      for (int h = 0; h < kMaxG / 2; ++h) {
+        const float2 y = f32x2::add(x[h], st.minus_m[h]);
+        e[h] = make_float2(ptx::ex2(y.x), ptx::ex2(y.y));
+      }
+      float f_inv = 1.f;
+      if (fraction != 0) {
+        const float f = __uint_as_float(fraction | 0x3f800000u);
+        f_inv = __fdividef(1.f, f);
+#pragma unroll
+        for (int h = 0; h < kMaxG / 2; ++h) e[h] = f32x2::mul(e[h], f32x2::both(f));
+      }
+      uint32_t codes[2 * kParts];   // this token's row: kParts times the eight heads
+#pragma unroll
+      for (int k = 0; k < kMaxG / 4; ++k) {
+        float2 w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int h = 2 * k + i;
+          const float2 r = cut19(e[h]);
+          l[h] = f32x2::fma(e[h], f32x2::both(f_inv), l[h]);
+          rounded[h] = f32x2::fma(r, f32x2::both(f_inv), rounded[h]);
+          w[i] = f32x2::mul(f32x2::mul(r, f32x2::both(sv)), st.weight[h]);
+        }
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          codes[2 * part + k] = fp8::pack4(w[0].x, w[0].y, w[1].x, w[1].y);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)   // and w becomes (w - code) kPartRatio
+            w[i] = f32x2::fma(fp8::unpack2(codes[2 * part + k] >> 16 * i), f32x2::both(-kPartRatio),
+                              f32x2::mul(w[i], f32x2::both(kPartRatio)));
+        }
+        const __half2 u0 = __floats2half2_rn(w[0].x, w[0].y);   // 10 bits are left: exact
+        const __half2 u1 = __floats2half2_rn(w[1].x, w[1].y);
+        const __half2 ratio = __float2half2_rn(kPartRatio);
+        const uint32_t c = fp8::pack4(u0, u1);
+        codes[4 + k] = c;
+        codes[6 + k] = fp8::pack4(__hmul2(__hsub2(u0, fp8::unpack2_half(c)), ratio),
+                                  __hmul2(__hsub2(u1, fp8::unpack2_half(c >> 16)), ratio));
       }
       // Step it - 2's product is done: its P buffer is free, and so is the
       // reference slot of step it - 4 (the product waited for the output warps
       // to be through with that step).
       fail = !wait(p, v, S::kOFull + group, phase ^ 1);
-      if (tok == 0) {
-        float4* to = reinterpret_cast<float4*>(v.base + S::kRef) + (it % kRefs) * (kMaxG / 4);
-#pragma unroll
-        for (int k = 0; k < kMaxG / 4; ++k) to[k] = st.ref[k];
-        ptx::mbar_arrive(v.bar(S::kRefFull + it % kRefs));
-      }
-      uint32_t codes[2 * kParts];   // this token's row: kParts times the eight heads
-#pragma unroll
-      for (int h = 0; h < kMaxG / 2; ++h) {
-        l[h] = f32x2::add(l[h], e[h]);
-#pragma unroll
-        for (int part = 0; part < kParts; ++part) {
-          const uint32_t c = fp8::pack2(w[h].x, w[h].y);
-          uint32_t& to = codes[2 * part + h / 2];
-          to = h % 2 ? to | c << 16 : c;
-          if (part + 1 < kParts)   // (w - c) kPartRatio
-            w[h] = f32x2::fma(fp8::unpack2(c), f32x2::both(-kPartRatio),
-                              f32x2::mul(w[h], f32x2::both(kPartRatio)));
-        }
-      }
       const uint32_t prow = v.addr + S::kP + group * S::kPBytes + tok * kPCols;
 #pragma unroll
       for (int half = 0; half < 2; ++half)
@@ -947,37 +1002,50 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(v.bar(S::kPFull + group));
+      if (tok == 0) {   // (behind P: the output warps need it a product later)
+        float2* to = reinterpret_cast<float2*>(v.base + S::kRef) + (it % kRefs) * (kMaxG / 2);
+#pragma unroll
+        for (int k = 0; k < kMaxG / 2; ++k) to[k] = negative(st.minus_ref[k]);
+        ptx::mbar_arrive(v.bar(S::kRefFull + it % kRefs));
+      }
     }
     // ---- the segment's sums, references and poison to the output warps ----
     fail |= !wait(p, v, S::kLEmpty + (seg & 1), ((seg >> 1) & 1) ^ 1);
     float* seg_l = reinterpret_cast<float*>(v.base + S::kSegL) +
-                   ((seg & 1) * kSoftmaxWarps + group * kGroupWarps + warp) * kMaxG;
-    // Eight sums over 32 lanes: each exchange halves the heads a lane holds, the
-    // last two add lanes of one head.
-    float sum[kMaxG];
+                   ((seg & 1) * kSoftmaxWarps + group * kGroupWarps + warp) * 2 * kMaxG;
+    // Eight sums of both kinds over 32 lanes: each exchange halves the heads a lane
+    // holds, the last two add lanes of one head.
+    float2 sum[kMaxG];
 #pragma unroll
-    for (int h = 0; h < kMaxG; ++h) sum[h] = h % 2 ? l[h / 2].y : l[h / 2].x;
+    for (int h = 0; h < kMaxG / 2; ++h) {
+      sum[2 * h] = make_float2(l[h].x, rounded[h].x);
+      sum[2 * h + 1] = make_float2(l[h].y, rounded[h].y);
+    }
 #pragma unroll
     for (int n = kMaxG / 2; n; n >>= 1) {
       const bool upper = lane & (4 * n);
 #pragma unroll
       for (int h = 0; h < n; ++h) {
-        const float give = upper ? sum[h] : sum[h + n];
-        sum[h] = (upper ? sum[h + n] : sum[h]) + __shfl_xor_sync(0xffffffffu, give, 4 * n);
+        const float2 give = upper ? sum[h] : sum[h + n], keep = upper ? sum[h + n] : sum[h];
+        sum[h] = f32x2::add(keep, make_float2(__shfl_xor_sync(0xffffffffu, give.x, 4 * n),
+                                              __shfl_xor_sync(0xffffffffu, give.y, 4 * n)));
       }
     }
-    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 1);
-    sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 2);
-    if ((lane & 3) == 0) seg_l[lane >> 2] = sum[0];
-    if (tok == 0) {
-      float4* sr = reinterpret_cast<float4*>(v.base + S::kSegRef) +
-                   ((seg & 1) * kGroups + group) * 2 * (kMaxG / 4);
-      const float4 none = make_float4(kNoRef, kNoRef, kNoRef, kNoRef);
 #pragma unroll
-      for (int k = 0; k < kMaxG / 4; ++k) {
-        const float4 m = reinterpret_cast<const float4*>(st.minus_m)[k];
-        sr[k] = first ? none : make_float4(-m.x, -m.y, -m.z, -m.w);
-        sr[kMaxG / 4 + k] = first ? none : st.ref[k];
+    for (int n = 1; n < 4; n <<= 1)
+      sum[0] = f32x2::add(sum[0], make_float2(__shfl_xor_sync(0xffffffffu, sum[0].x, n),
+                                              __shfl_xor_sync(0xffffffffu, sum[0].y, n)));
+    if ((lane & 3) == 0) {
+      seg_l[lane >> 2] = sum[0].x;
+      seg_l[kMaxG + (lane >> 2)] = sum[0].y;
+    }
+    if (tok == 0) {
+      float2* sr = reinterpret_cast<float2*>(v.base + S::kSegRef) +
+                   ((seg & 1) * kGroups + group) * 2 * (kMaxG / 2);
+#pragma unroll
+      for (int k = 0; k < kMaxG / 2; ++k) {
+        sr[k] = first ? f32x2::both(kNoRef) : negative(st.minus_m[k]);
+        sr[kMaxG / 2 + k] = first ? f32x2::both(kNoRef) : negative(st.minus_ref[k]);
       }
       v.seg_poison[(seg & 1) * kGroups + group] = poisoned;
     }

@@ -17,7 +17,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
-  return pack2(a, b) | (pack2(c, d) << 16);
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
 
 // The same from fp16.
@@ -26,6 +31,15 @@ __device__ __forceinline__ uint32_t pack2(__half2 x) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
       : "=h"(r)
       : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack4(__half2 x, __half2 y) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f16x2 lo, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 hi, %2;\n\tmov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "r"(*reinterpret_cast<const uint32_t*>(&x)), "r"(*reinterpret_cast<const uint32_t*>(&y)));
   return r;
 }
 
