@@ -9,10 +9,12 @@
 //  * Work split and partials: as the bf16 kernel (split_units.cuh); a request's
 //    tiles are merged by a kernel of its own.  A CTA streams its pages two at a
 //    time: a step is 128 tokens of one kv head.
-//  * S = K Q^T: M = 128 tokens, N = 16, K = D.  q (bf16, 8 significant bits) is
-//    scaled by a power of two per head and held as hi + lo / 16 in e4m3 (4 bits
-//    each, and a sign between them): 16 columns for 8 heads, exact for values
-//    down to 2^-14 of the head's largest.
+//  * S = K Q^T: M = 128 tokens, N = 32, K = D.  q (bf16, 8 significant bits) is
+//    scaled by a power of two per head and held as four e4m3 parts (4 bits each, and
+//    a sign between them): two hold all bits of values down to 2^-14 of the head's
+//    largest, two more those down to 2^-24, and 2^-32 of the largest of any.  (Most
+//    heads have nothing in the last two, but a K that is large where q is small
+//    would show what they lack.)
 //  * Softmax: a thread per token, two groups of threads taking every other step,
 //    each with its own references and sum.  A head has two running references,
 //    multiples of 8 (log2).  One, m, is near the largest score x_j and serves the
@@ -72,7 +74,11 @@ constexpr int kParts = 4;                   // e4m3 parts of a probability
 constexpr float kFirstPart = 256.f;         // scale of the first part
 constexpr float kPartRatio = 32.f;          // of each further one
 constexpr int kPCols = kParts * kMaxG;      // N of the second product
-constexpr int kQCols = 2 * kMaxG;           // N of the first product
+constexpr int kQParts = 4;                  // e4m3 parts of q, each scaled up from the
+// one before by these: the second holds what the first leaves of 8 bits, and what
+// these two leave, of values below 256, is at most 2^-15.
+constexpr float kQScale1 = 32.f, kQScale2 = 1 << 18, kQScale3 = 32.f;
+constexpr int kQCols = kQParts * kMaxG;     // N of the first product
 constexpr int kChunk = 128;                 // dims per 128-byte row
 constexpr int kTmemCols = 256;
 constexpr int kRefs = 4;                    // reference slots, two steps more than P buffers
@@ -612,6 +618,13 @@ __device__ __forceinline__ void store_shared(uint32_t at, const uint32_t (&x)[2]
   asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(x[0]), "r"(x[1]) : "memory");
 }
 
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) {
+  return *reinterpret_cast<const __nv_bfloat162*>(&x);
+}
+
+// A head of q, as its four parts, into a buffer.  (All four of every head: most heads
+// have nothing in the last two, but a test for that and its branch took as long, 252
+// requests of 103 tokens 24.8 us with and 24.7 without.)
 template <int D, class P>
 __device__ __forceinline__ void convert_head(const P& p, const View& v, const QVec<D>& raw,
                                              int buffer, int h, int lane) {
@@ -619,34 +632,40 @@ __device__ __forceinline__ void convert_head(const P& p, const View& v, const QV
   constexpr int kDims = D / 32;             // dims per lane
   const int col = lane * kDims;
   const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
-  unsigned amax = 0;
+  __nv_bfloat162 most = __habs2(as_bf162(w[0]));   // NaN if there is one
 #pragma unroll
-  for (int k = 0; k < kDims / 2; ++k)
-    amax = max(amax, max(w[k] << 16 & 0x7fffffffu, w[k] & 0x7fff0000u));
-  amax = __reduce_max_sync(0xffffffffu, amax);
+  for (int k = 1; k < kDims / 2; ++k) most = __hmax2_nan(most, __habs2(as_bf162(w[k])));
+  const unsigned amax = __reduce_max_sync(
+      0xffffffffu, __bfloat16_as_ushort(__hmax_nan(__low2bfloat16(most), __high2bfloat16(most))));
   // Largest value to [128, 256).  A head with a NaN or an infinity becomes
   // NaN (its scores would be).
-  const int e = amax ? min(7 - ((int)(amax >> 23) - 127), 120) : 0;
-  const float up = amax < 0x7f800000u ? ptx::pow2i(e) : __int_as_float(0x7fc00000);
+  const int e = amax ? min(7 - ((int)(amax >> 7) - 127), 120) : 0;
+  const float up = amax < 0x7f80u ? ptx::pow2i(e) : __int_as_float(0x7fc00000);
   if (lane == 0)
     reinterpret_cast<float*>(v.base + S::kQScale)[buffer * kMaxG + h] =
         p.scale_log2 * ptx::pow2i(-e);
-  const uint32_t at = v.addr + S::kQ + buffer * S::kQBytes + col / kChunk * S::kQChunkBytes +
-                      (col & 15) + h * kChunk + (((col % kChunk >> 4) ^ h) << 4);
-  // z = q * up is exact in fp16 (8 significant bits), and so is what hi leaves.
-  uint32_t hi[kDims / 4], lo[kDims / 4];
+  // z = q * up is exact in fp16 down to steps of 2^-24, and so is what each part leaves.
+  uint32_t code[kQParts][kDims / 4];
 #pragma unroll
   for (int k = 0; k < kDims / 2; ++k) {
-    const __half2 z = __floats2half2_rn(ptx::bf16_lo_to_f32(w[k]) * up,
-                                        ptx::bf16_hi_to_f32(w[k]) * up);
-    const uint32_t a = fp8::pack2(z);
-    const uint32_t b = fp8::pack2(
-        __hmul2(__hsub2(z, fp8::unpack2_half(a)), __float2half2_rn(16.f)));
-    hi[k / 2] = k % 2 ? hi[k / 2] | a << 16 : a;
-    lo[k / 2] = k % 2 ? lo[k / 2] | b << 16 : b;
+    auto take = [&](int part, __half2 x) {   // returns what the part leaves
+      const uint32_t c = fp8::pack2(x);
+      uint32_t& to = code[part][k / 2];
+      to = k % 2 ? to | c << 16 : c;
+      return __hsub2(x, fp8::unpack2_half(c));
+    };
+    __half2 z = __floats2half2_rn(ptx::bf16_lo_to_f32(w[k]) * up,
+                                  ptx::bf16_hi_to_f32(w[k]) * up);
+    z = take(1, __hmul2(take(0, z), __float2half2_rn(kQScale1)));
+    const __half2 by = __float2half2_rn(512.f);   // 2^18 in two factors: fp16 ends at 2^16
+    z = take(2, __hmul2(__hmul2(z, by), by));
+    take(3, __hmul2(z, __float2half2_rn(kQScale3)));
   }
-  store_shared(at, hi);
-  store_shared(at + kMaxG * kChunk, lo);
+  const uint32_t at = v.addr + S::kQ + buffer * S::kQBytes + col / kChunk * S::kQChunkBytes +
+                      (col & 15) + h * kChunk + (((col % kChunk >> 4) ^ h) << 4);
+#pragma unroll
+  for (int part = 0; part < kQParts; ++part)
+    store_shared(at + part * kMaxG * kChunk, code[part]);
 }
 
 // ---------------------------------------------------------------------------
@@ -843,9 +862,12 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
         sv = sc[kStepBlocks + tok / kBlock];
         poisoned |= v.poison[slot];
         tc::fence_after();
-        uint32_t r[16];
-        tc::ld16(tmem + group * kQCols + ((uint32_t)(warp * 32) << 16), r);
-        tc::wait_ld(r);
+        uint32_t r[2][16];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          tc::ld16(tmem + group * kQCols + 16 * k + ((uint32_t)(warp * 32) << 16), r[k]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) tc::wait_ld(r[k]);
         tc::fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(v.bar(S::kSEmpty + group));
@@ -862,10 +884,14 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
         if (!live) sv = 0.f;   // whatever its row holds
 #pragma unroll
         for (int h = 0; h < kMaxG / 2; ++h) {
-          auto pair = [&](int k) {
-            return make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+          auto part = [&](int k) {
+            const int col = k * kMaxG + 2 * h;
+            return make_float2(__uint_as_float(r[col / 16][col % 16]),
+                               __uint_as_float(r[col / 16][col % 16 + 1]));
           };
-          const float2 d = f32x2::fma(pair(kMaxG + 2 * h), f32x2::both(0.0625f), pair(2 * h));
+          float2 d = f32x2::fma(part(3), f32x2::both(1.f / kQScale3), part(2));
+          d = f32x2::fma(d, f32x2::both(1.f / kQScale2), part(1));
+          d = f32x2::fma(d, f32x2::both(1.f / kQScale1), part(0));
           x[h] = f32x2::mul(f32x2::mul(d, f32x2::both(sk)), reinterpret_cast<float2*>(qs)[h]);
         }
         if (pages < 2 || tok0 < s.U.tok_start || tok0 + kStep > s.U.tok_end) {
