@@ -415,7 +415,8 @@ size_t paged_decode_attn_q8_workspace_bytes(int B, int T, int n_q_heads, int n_k
  *           scales of the attended blocks must lie in [2^-100, 2^120] in
  *           magnitude or be 0 (kv_append_rope_q8's do), and may differ that
  *           much within a tile; a V scale above that, or a NaN, makes the
- *           tile's output NaN.
+ *           tile's output NaN.  K scales may be any for which the scores are
+ *           finite.
  * Codes of rows outside a tile may hold anything, NaN codes too; scales of
  * blocks wholly outside the tiles are not used.
  * Products run on the tensor cores in e4m3 with FP32 sums; q and the

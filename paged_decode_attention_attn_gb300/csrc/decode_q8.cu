@@ -50,6 +50,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <vector>
@@ -79,6 +80,10 @@ constexpr int kQParts = 4;                  // e4m3 parts of q, each scaled up f
 // these two leave, of values below 256, is at most 2^-15.
 constexpr float kQScale1 = 32.f, kQScale2 = 1 << 18, kQScale3 = 32.f;
 constexpr int kQCols = kQParts * kMaxG;     // N of the first product
+// A product of codes of K and q lies below 2^25.  It is multiplied by K's scale (up to
+// 2^120) and by a factor per head; this much of the one goes to the other, so that a
+// score within range has every step of its product there too.
+constexpr int kScaleShift = 17;
 constexpr int kChunk = 128;                 // dims per 128-byte row
 constexpr int kTmemCols = 256;
 constexpr int kRefs = 4;                    // reference slots, two steps more than P buffers
@@ -204,7 +209,7 @@ struct Params {
   int n_units;
   int n_full;   // units with pages; the others follow them
   int grid;
-  float scale_log2;
+  float scale_log2;   // times 2^kScaleShift
   unsigned long long wait_limit_ns;
   int stall_iteration;
   unsigned long long slice_wait_ns;
@@ -834,8 +839,10 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
     float2 l[kMaxG / 2], rounded[kMaxG / 2];
     float lowest = 0.f;
     fail |= !wait(p, v, S::kQFull + (seg & 1), (seg >> 1) & 1);
-    if (lane < kMaxG)
-      qs[lane] = reinterpret_cast<const float*>(v.base + S::kQScale)[(seg & 1) * kMaxG + lane];
+    if (lane < kMaxG) {
+      const float x = reinterpret_cast<const float*>(v.base + S::kQScale)[(seg & 1) * kMaxG + lane];
+      qs[lane] = fminf(fmaxf(x, -FLT_MAX), FLT_MAX);   // (infinite for |q| above 2^113)
+    }
 #pragma unroll
     for (int h = 0; h < kMaxG / 2; ++h) l[h] = rounded[h] = f32x2::both(0.f);
     __syncwarp();
@@ -858,7 +865,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       if (!fail) {
         const float* sc = reinterpret_cast<const float*>(v.base + S::kScales +
                                                          slot * S::kScaleBytes);
-        const float sk = sc[tok / kBlock];
+        const float sk = sc[tok / kBlock] * ptx::pow2i(-kScaleShift);
         sv = sc[kStepBlocks + tok / kBlock];
         poisoned |= v.poison[slot];
         tc::fence_after();
@@ -1715,7 +1722,7 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   common.Hq = Hq;
   common.Hkv = Hkv;
   common.G = Hq / Hkv;
-  common.scale_log2 = scale * kLog2e;
+  common.scale_log2 = std::ldexp(scale * kLog2e, kScaleShift);
   if (T == 1) {
     common.out2 = merged_out;
     common.lse2 = merged_lse;

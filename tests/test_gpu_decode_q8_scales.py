@@ -148,3 +148,29 @@ def test_the_largest_rows_an_append_can_write(B):
     assert float(r.scales[:, HKV:].max()) == 2.0 ** 120
     r.run(B)
     r.check()
+
+
+@pytest.mark.parametrize("k_exp,q_exp", [(112, -113), (113, -114), (112, -118), (119, -125),
+                                         (104, -110), (-60, 60), (60, -66), (-60, 110)])
+def test_scores_within_range_from_factors_far_apart(B, k_exp, q_exp):
+    """K's scale and q far from 1, their product near it."""
+    n = 20
+    r = Rows([k_exp] * n, [-6] * n, seed=k_exp + 200)
+    r.q = (r.q.float() * 2.0 ** min(q_exp, 100)).bfloat16()
+    if q_exp > 100:
+        r.q = (r.q.float() * 2.0 ** (q_exp - 100)).bfloat16()
+        r.scale *= 2.0 ** -(q_exp + k_exp + 6)
+    r.run(B)
+    r.check()
+    assert r.out.isfinite().all()
+
+
+def test_rows_of_zeros_in_a_block_of_a_large_scale(B):
+    """K codes of zero under a scale near the top, and q large: their scores are 0."""
+    n = 8
+    r = Rows([119] * n, [-6] * n, seed=17)
+    r.pool.view(torch.uint8).view(-1, 2, HKV * r.d)[:, 0] = 0
+    r.q = (r.q.float() * 2.0 ** 30).bfloat16()
+    r.run(B)
+    r.check()
+    assert r.out.isfinite().all() and torch.allclose(r.lse, torch.log(torch.tensor(16.0 * n)))
