@@ -347,7 +347,8 @@ int kv_append_rows(void* pool, int64_t pool_pages, const int32_t* page_table,
  *              take no part: nothing is written for them.  NULL: one token per
  *              request, n_tokens == B.
  *   positions  device int32 [B], position of each request's first new token.
- *   inv_freq   device fp32 [rot_dim / 2] (may be NULL when rot_dim is 0).
+ *   inv_freq   device fp32 [rot_dim / 2] (may be NULL when rot_dim is 0).  One
+ *              that is not finite makes its pairs NaN, at any position.
  *   rot_dim    a multiple of 8 in [0, head_dim].
  *   flags      0 or PA_ROPE_INTERLEAVED.
  *   pool       device bf16 pages (layout above).  A token whose position or

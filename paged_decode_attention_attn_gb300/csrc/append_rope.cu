@@ -112,10 +112,14 @@ __device__ __forceinline__ unsigned long long turn_step(float f) {
   return (bits >> 31) ? 0ull - x : x;
 }
 
+// 0, or NaN for a frequency that is not finite, whose pairs become NaN.
+__device__ __forceinline__ float not_finite(float f) { return f - f; }
+
 // Sine and cosine at position p: the turn's nearest quarter, and the Taylor
 // polynomials of the rest (|x| <= pi / 4: the first terms left out are below
 // 2e-9 and 3e-10).  Half the instructions of sincospif, which reduces a float.
-__device__ __forceinline__ void turn(long long p, unsigned long long step, float* s, float* c) {
+__device__ __forceinline__ void turn(long long p, unsigned long long step, float nan, float* s,
+                                     float* c) {
   const uint32_t at = (uint32_t)((step * (unsigned long long)p) >> 32);
   const uint32_t quarter = (at + 0x20000000u) >> 30;
   const float x = (float)(int)(at - (quarter << 30)) * 1.4629180792671596e-09f;   // 2 pi 2^-32
@@ -131,8 +135,8 @@ __device__ __forceinline__ void turn(long long p, unsigned long long step, float
   const float cx = fmaf(b, z, 1.0f);
   const bool odd = quarter & 1;
   const float ss = odd ? cx : sx, cc = odd ? sx : cx;
-  *s = quarter & 2 ? -ss : ss;
-  *c = (quarter + 1) & 2 ? -cc : cc;
+  *s = (quarter & 2 ? -ss : ss) + nan;
+  *c = ((quarter + 1) & 2 ? -cc : cc) + nan;
 }
 
 template <int V>
@@ -244,8 +248,10 @@ __device__ __forceinline__ void rotate_rows(const Tokens& t, __nv_bfloat16* pool
   int b = 0, first, end;
   long long pos = 0;
   if (!locate(t.cu, t.positions, t.B, t.n_tokens, row, lane, &b, &pos, &first, &end)) return;
-  for (int i = lane; i < t.half; i += 32)
-    turn(pos, turn_step(__ldg(t.inv_freq + i)), &table[warp][1][i], &table[warp][0][i]);
+  for (int i = lane; i < t.half; i += 32) {
+    const float f = __ldg(t.inv_freq + i);
+    turn(pos, turn_step(f), not_finite(f), &table[warp][1][i], &table[warp][0][i]);
+  }
   __nv_bfloat16* q_out = t.q_out + row * t.q_out_stride;
   __nv_bfloat16* kv_out = nullptr;
   if (kKv) {
@@ -454,8 +460,9 @@ __global__ void __launch_bounds__(kThreads, 3)
     int h = warp;
     if (warp < kKWarps) {
       for (int j = threadIdx.x; j < t.half; j += kKThreads) {
-        const unsigned long long step = turn_step(__ldg(t.inv_freq + j));
-        for (int k = 0; k < n; ++k) turn(pos + k, step, &cs[k][1][j], &cs[k][0][j]);
+        const float f = __ldg(t.inv_freq + j), nan = not_finite(f);
+        const unsigned long long step = turn_step(f);
+        for (int k = 0; k < n; ++k) turn(pos + k, step, nan, &cs[k][1][j], &cs[k][0][j]);
       }
       ptx::named_barrier(1, kKThreads);
     } else {
