@@ -184,9 +184,9 @@ struct Smem {
 
 // A unit as the kernel reads it: three 8-byte loads.
 struct alignas(8) DevUnit {
-  int32_t page_first, bt, tok_start, tok_end;
-  uint16_t g, part_base;
-  int16_t n_parts, first_cta;
+  int32_t page_first, bt, tok_start, tok_end, g;
+  uint16_t part_base;
+  uint8_t n_parts, first_cta;
 };
 
 template <int kMaxUnits>
@@ -1567,7 +1567,7 @@ std::vector<int> pack(Plan* plan, Launch* L, int sms, int d) {
       order.push_back(i);
       units[i].page_first = at;
       units[i].n_parts = 1;
-      units[i].first_cta = static_cast<int16_t>(k);
+      units[i].first_cta = static_cast<uint8_t>(k);
       at += pages[i];
     }
   }

@@ -61,16 +61,17 @@ constexpr float kLn2Lo = 1.428606765330187045e-06f; // ln 2 - kLn2Hi
 constexpr float kRefStep = 8.0f;
 
 static_assert(kMaxSlices <= kMaxGrid - 1, "slices per split unit");
+static_assert(kMaxGrid <= 255 && kMaxUnitsLarge + 1024 <= 65536, "fields of Unit");
 
 struct Unit {
   int32_t bt;          // b * T + t
   int32_t tok_start;
   int32_t tok_end;
   int32_t page_first;  // flattened index of the unit's first page in this launch
-  uint16_t g;          // kv head
+  int32_t g;           // kv head
   uint16_t part_base;  // first partial slot (units covered by several CTAs)
-  int16_t n_parts;     // CTAs covering the unit
-  int16_t first_cta;   // the first of them
+  uint8_t n_parts;     // CTAs covering the unit
+  uint8_t first_cta;   // the first of them
   int32_t pair_total;  // completions the (request, kv head) tile counter reaches (fused merge)
 };
 
@@ -431,7 +432,6 @@ inline void equal_starts(long long total, int grid, std::vector<int32_t>* starts
 template <class Shape>
 int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int segment_charge, bool merge,
                Shape shape, Plan* plan) {
-  PA_REQUIRE(n_kv_heads <= 65535, "n_kv_heads (%d) above 65,535", n_kv_heads);
   const size_t n_tiles = (size_t)B * T, n_units = n_tiles * n_kv_heads;
   std::vector<Unit>& units = plan->units;
   std::vector<int32_t>& pages = plan->pages;
@@ -448,7 +448,7 @@ int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int segment_c
     if (g > 0) std::copy_n(pages.data(), n_tiles, pages.data() + g * n_tiles);
     for (size_t bt = 0; bt < n_tiles; ++bt) {
       u[bt].bt = static_cast<int32_t>(bt);
-      u[bt].g = static_cast<uint16_t>(g);
+      u[bt].g = g;
       u[bt].tok_start = tiles[2 * bt];
       u[bt].tok_end = tiles[2 * bt + 1];
     }
@@ -483,8 +483,8 @@ int plan_units(const int32_t* tiles, int B, int T, int n_kv_heads, int segment_c
       while (L.starts[k + 1] <= u.page_first) ++k;
       const int k0 = k;
       while (L.starts[k + 1] < u.page_first + pages[i]) ++k;
-      u.n_parts = static_cast<int16_t>(k - k0 + 1);
-      u.first_cta = static_cast<int16_t>(k0);
+      u.n_parts = static_cast<uint8_t>(k - k0 + 1);
+      u.first_cta = static_cast<uint8_t>(k0);
       if (k > k0) {
         u.part_base = static_cast<uint16_t>(part_cursor);
         part_cursor += k - k0 + 1;
