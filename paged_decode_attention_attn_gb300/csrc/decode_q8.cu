@@ -907,6 +907,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
             if (!live) x[h] = f32x2::both(-INFINITY);
         }
       }
+      const bool odd = __any_sync(0xffffffffu, fraction != 0);
       bool move = first;
       if (!move) {
         // A token above a ref, or one that might lie too far above an m?
@@ -973,7 +974,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
         e[h] = make_float2(ptx::ex2(y.x), ptx::ex2(y.y));
       }
       float f_inv = 1.f;
-      if (fraction != 0) {
+      if (odd) {
         const float f = __uint_as_float(fraction | 0x3f800000u);
         f_inv = __fdividef(1.f, f);
 #pragma unroll
