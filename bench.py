@@ -215,6 +215,17 @@ def traffic_file(workload):
     return os.path.join(ROOT, "profiles", f"paged_decode_kernel_{workload}.md")
 
 
+def short_leg(leg):
+    """A staged leg's figures.  How they were taken, what the timeline shows and the
+    single steps stand beside the main workload's leg alone: the whole output is one
+    line, kept below 16 KB."""
+    drop = {"timeline": ("reading", "slow_stages"),
+            "pairs": ("what", "step_ms", "probe_all_layers_GBps", "stage_min_GBps")}
+    return {k: {a: b for a, b in v.items() if a not in drop[k]}
+            if k in drop and isinstance(v, dict) else v
+            for k, v in leg.items() if k != "link_probe"}
+
+
 def kernel_source_sha():
     h = hashlib.sha256()
     for f in KERNEL_SOURCES:
@@ -625,9 +636,13 @@ def run_ours(args):
             line["workloads"] = {}
             for n in names:
                 entry = dict(summaries[n])
-                entry["config"] = workload_config(wls[n], world, fused, kv_ready, args)
+                cfg = workload_config(wls[n], world, fused, kv_ready, args)
+                entry["config"] = {k: v for k, v in cfg.items() if line["config"].get(k) != v}
                 if n in staged:
-                    entry["e2e"] = staged[n]
+                    entry["e2e"] = short_leg(staged[n])
+                    if n == args.workload:   # the line's own e2e
+                        entry["e2e"] = {"value": staged[n]["value"], "unit": staged[n]["unit"],
+                                        "timeline": {"stages": staged[n]["timeline"]["stages"]}}
                 line["workloads"][n] = entry
         if merge_stress is not None:
             line["merge_stress"] = merge_stress
@@ -636,16 +651,16 @@ def run_ours(args):
         if e2e_resident is not None:
             line["e2e_resident"] = e2e_resident
         if e2e_compact is not None:
-            line["e2e_compact"] = e2e_compact
+            line["e2e_compact"] = short_leg(e2e_compact)
         if e2e_tiled is not None:
-            line["e2e_tiled"] = e2e_tiled
+            line["e2e_tiled"] = short_leg(e2e_tiled)
         if e2e_planned is not None:
             line["e2e_planned"] = e2e_planned
         if bus is not None:
             line["bus_model"] = bus
         if cpu is not None:
             line["cpu_baseline"] = cpu
-        print(json.dumps(line), flush=True)
+        print(json.dumps(line, separators=(",", ":")), flush=True)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
