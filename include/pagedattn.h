@@ -423,9 +423,9 @@ size_t paged_decode_attn_q8_workspace_bytes(int B, int T, int n_q_heads, int n_k
  * Products run on the tensor cores in e4m3 with FP32 sums; q and the
  * probabilities enter them as sums of several e4m3 parts.  A value of q keeps
  * all its bits down to 2^-24 of its head's largest, and is held to 2^-32 of
- * that below.  A probability times its V scale is cut to 19 bits, and held to
- * 2^-25 of the row's largest at least; the output is divided by the sum of the
- * probabilities as they were cut (a row of one key is that key's V to FP32
+ * that below.  A probability times its V scale is held to 2^-19 of itself, or
+ * to 2^-25 of the row's largest; the output is divided by the sum of the
+ * probabilities as they are held (a row of one key is that key's V to FP32
  * rounding), the log-sum-exp takes the sum of the whole ones.
  * Supported: head_dim 128 and 256, n_q_heads / n_kv_heads in 1..8. */
 int paged_decode_attn_q8_lse(const void* q, const void* pool, const float* scales,

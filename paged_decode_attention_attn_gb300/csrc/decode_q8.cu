@@ -23,14 +23,15 @@
 //    e_j sv_j 2^(m - ref) lies in [0, 1] and the largest in (2^-8, 1] whatever the
 //    scales.  (One reference for both lost keys from the sum where V's scales lay
 //    more than 2^126 apart, and small probabilities beside V scales near 2^100.)
-//    They move rarely, and then by an exact power of two.  w is cut to 19 bits
-//    and held as kParts e4m3 parts, each the rounding of what the parts before left,
-//    32 times finer (that stays below 256 = 2^8, as w 2^8 does): a part takes 5 bits
-//    (4 and a sign), so the parts hold all 19, or what lies above 2^-33 of the row's
-//    bound.  The outputs are divided by the sum of these probabilities as they were
-//    cut, so a row that hangs on few keys loses nothing to that; the log-sum-exp takes
-//    the sum of the whole ones.  (|sv| = f 2^k with 1 <= f < 2: it is e_j f that is cut,
-//    and what the sums get is divided by f.)
+//    They move rarely, and then by an exact power of two.  w is held
+//    as kParts e4m3 parts, each the rounding of what the parts before left, 32 times
+//    finer (that stays below 256 = 2^8, as w 2^8 does): a part takes 5 bits (4 and a
+//    sign), so a w is within 2^-19 of itself, 3.5e-7 on the root mean square, or
+//    within 2^-33 of the row's bound.  What the last part leaves in the first case is
+//    summed too, as left_j / sv_j, and taken from the sum that divides the outputs:
+//    numerator and denominator have the same probabilities, and a row that hangs on
+//    few keys loses nothing to the parts.  (Cutting w to the 19 bits that every w has did the same
+//    at twice the error on long rows.)  The log-sum-exp takes the whole sum.
 //  * O^T = V^T P^T: M = 128 dims (a step's V codes as they lie, M-major), N =
 //    8 kParts (a token's row of P, N-major), K = 128 tokens.  Every step's
 //    product starts from zero in tensor memory and is added to fp32 registers (a
@@ -74,6 +75,7 @@ constexpr int kBlocksPerPage = kPage / kBlock;
 constexpr int kParts = 4;                   // e4m3 parts of a probability
 constexpr float kFirstPart = 256.f;         // scale of the first part
 constexpr float kPartRatio = 32.f;          // of each further one
+constexpr float kLastPart = 1.f / (kFirstPart * kPartRatio * kPartRatio * kPartRatio);
 constexpr int kPCols = kParts * kMaxG;      // N of the second product
 constexpr int kQParts = 4;                  // e4m3 parts of q, each scaled up from the
 // one before by these: the second holds what the first leaves of 8 bits, and what
@@ -116,11 +118,16 @@ constexpr float kNoRef = -1e30f;
 static_assert(kStep == kGroupWarps * 32 && kChunk == kOut, "a thread per token and per dim");
 
 // A softmax group's references, per head; weight: 2^(m - ref) times the first part's
-// scale; by: what the sums are multiplied by at a move; gap: ref - m.
-struct alignas(16) State {
-  float2 minus_m[kMaxG / 2], weight[kMaxG / 2], minus_ref[kMaxG / 2];
-  float2 by[kMaxG / 2], gap[kMaxG / 2];
+// scale; by, by_ref: what is relative to m, or ref, is multiplied by at a move; gap:
+// ref - m.
+struct State {
+  float4 minus_m[kMaxG / 4], weight[kMaxG / 4], minus_ref[kMaxG / 4], ref[kMaxG / 4];
+  float4 by[kMaxG / 4], by_ref[kMaxG / 4], gap[kMaxG / 4];
 };
+// Two heads of four.
+__device__ __forceinline__ float2 half_of(const float4& x, int i) {
+  return i ? make_float2(x.z, x.w) : make_float2(x.x, x.y);
+}
 constexpr int kStateBytes = sizeof(State);
 
 // Shared memory of a CTA; offsets from a 1024-byte boundary.
@@ -148,7 +155,7 @@ struct Smem {
   static constexpr int kScaleBytes = 2 * kStepBlocks * 4;
   static constexpr int kQScale = kScales + kSlots * kScaleBytes;  // [2][kMaxG]
   static constexpr int kRef = kQScale + 2 * kMaxG * 4;             // [kRefs][kMaxG]
-  static constexpr int kSegL = kRef + kRefs * kMaxG * 4;    // [2][warp][sums | rounded][kMaxG]
+  static constexpr int kSegL = kRef + kRefs * kMaxG * 4;    // [2][warp][sums | left][kMaxG]
   // [2][group][m | ref][kMaxG]
   static constexpr int kSegRef = kSegL + 2 * kSoftmaxWarps * 2 * kMaxG * 4;
   // A group's references now (see State), and what a move of them looks at: log2 sv
@@ -693,7 +700,7 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, int s
   const bool nan = (v.seg_poison[r.i * kGroups] | v.seg_poison[r.i * kGroups + 1]) != 0;
   if (lane < kMaxG) {
     const float qnan = __int_as_float(0x7fc00000);
-    float m = kNoRef, ref = kNoRef, l = 0.f, rounded = 0.f;
+    float m = kNoRef, ref = kNoRef, l = 0.f, left = 0.f;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       m = fmaxf(m, sr[g * 2 * kMaxG + lane]);
@@ -705,17 +712,17 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, int s
       const float a = ref_weight(sr[g * 2 * kMaxG + lane], m);
       l = fmaf(a, (w[0] + w[2 * kMaxG]) + (w[4 * kMaxG] + w[6 * kMaxG]), l);
       w += kMaxG;
-      rounded = fmaf(a, (w[0] + w[2 * kMaxG]) + (w[4 * kMaxG] + w[6 * kMaxG]), rounded);
+      left = fmaf(ref_weight(sr[(g * 2 + 1) * kMaxG + lane], ref),
+                  (w[0] + w[2 * kMaxG]) + (w[4 * kMaxG] + w[6 * kMaxG]), left);
     }
     // The sum of products is relative to ref; the output, or the partial, to the sum's
     // own magnitude 2^(m + k), with l 2^-k in (2^-8, 1].  (Two factors: 2^(ref - m - k)
     // may be as large as the largest V scale.)
     const int k = l > 0.f ? ((__float_as_int(l) >> 23) - 127 + 8) >> 3 << 3 : 0;
     const int by = max(-240, min(240, (int)(ref - m) - k));
-    const float scale = ptx::pow2i(max(-126, -k));
-    l *= scale;
-    rounded *= scale;
-    float f = ptx::pow2i(by - (by >> 1)) / rounded;
+    l *= ptx::pow2i(max(-126, -k));
+    const float f1 = ptx::pow2i(by >> 1), f2 = ptx::pow2i(by - (by >> 1));
+    float f = f2 / (l - left * kLastPart * f1 * f2);
     if (slot < 0) {
       // for the log-sum-exp, which the output warps take from these
       factor[2 * kMaxG + lane] = m + (float)k;
@@ -725,7 +732,7 @@ __device__ __forceinline__ bool segment_factors(const P& p, const View& v, int s
           make_float2(nan ? qnan : m + (float)k, l);
       f *= l;   // a partial's products belong to the sum that the merge divides by
     }
-    factor[lane] = ptx::pow2i(by >> 1);
+    factor[lane] = f1;
     factor[kMaxG + lane] = nan ? qnan : f;
   }
   __syncwarp();
@@ -811,12 +818,13 @@ __device__ __forceinline__ float warp_max(float x) {   // (NaN ignored)
   return r;
 }
 
-__device__ __forceinline__ float2 negative(float2 x) { return make_float2(-x.x, -x.y); }
-
-// Cut off behind 19 bits (NaN stays).
-__device__ __forceinline__ float2 cut19(float2 x) {
-  return make_float2(__uint_as_float(__float_as_uint(x.x) & ~31u),
-                     __uint_as_float(__float_as_uint(x.y) & ~31u));
+// A word of x's bytes' bits 7, each copied through a byte (kSelect: prmt's, with its
+// sign bits).
+template <int kSelect>
+__device__ __forceinline__ uint32_t sign_bytes(uint32_t x) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "n"(kSelect));
+  return r;
 }
 
 // ---------------------------------------------------------------------------
@@ -836,7 +844,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
   float* qs = reinterpret_cast<float*>(v.base + S::kQs) + (group * kGroupWarps + warp) * kMaxG;
   for_segments(p, [&](const Segment& s, int seg) {
     // Tokens whose log2 sv is below `lowest` might lie above m by more than kSlack.
-    float2 l[kMaxG / 2], rounded[kMaxG / 2];
+    float2 l[kMaxG / 2], left[kMaxG / 2];
     float lowest = 0.f;
     fail |= !wait(p, v, S::kQFull + (seg & 1), (seg >> 1) & 1);
     if (lane < kMaxG) {
@@ -844,7 +852,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       qs[lane] = fminf(fmaxf(x, -FLT_MAX), FLT_MAX);   // (infinite for |q| above 2^113)
     }
 #pragma unroll
-    for (int h = 0; h < kMaxG / 2; ++h) l[h] = rounded[h] = f32x2::both(0.f);
+    for (int h = 0; h < kMaxG / 2; ++h) l[h] = left[h] = f32x2::both(0.f);
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(v.bar(S::kQEmpty + (seg & 1)));
     int poisoned = 0;
@@ -860,14 +868,13 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       const bool live = loaded && tok0 + tok >= s.U.tok_start && tok0 + tok < s.U.tok_end;
       float2 x[kMaxG / 2];
       float sv = 0.f, up = 0.f;
-      unsigned fraction = 0;
       fail = !warp_wait(p, v, S::kSFull + group, phase, !fail);
       if (!fail) {
         const float* sc = reinterpret_cast<const float*>(v.base + S::kScales +
                                                          slot * S::kScaleBytes);
         const float sk = sc[tok / kBlock] * ptx::pow2i(-kScaleShift);
         sv = sc[kStepBlocks + tok / kBlock];
-        poisoned |= v.poison[slot];
+        if (tok == 0) poisoned |= v.poison[slot];
         tc::fence_after();
         uint32_t r[2][16];
 #pragma unroll
@@ -878,28 +885,29 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
         tc::fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(v.bar(S::kSEmpty + group));
-        // |sv| = f 2^k with 1 <= f < 2, of which 2^k stays in sv; up: its logarithm rounded
-        // up (a scale of zero weighs nothing).
+        // 2^up >= |sv| (a scale of zero weighs nothing)
         const unsigned sb = __float_as_uint(sv) & 0x7fffffffu;
-        const bool fits = sb <= __float_as_uint(ptx::pow2i(kMaxScaleExp));
-        fraction = sb & 0x7fffffu;
-        up = (float)max(min((int)(sb >> 23) - 127 + (fraction ? 1 : 0), kMaxScaleExp),
+        up = (float)max(min((int)(sb >> 23) - 127 + ((sb & 0x7fffffu) ? 1 : 0), kMaxScaleExp),
                         kMinScaleExp);
         if (sb == 0) up = kNoRef;
-        sv = __uint_as_float(__float_as_uint(sv) & 0xff800000u);
-        if (!fits) sv = __int_as_float(0x7fc00000);
+        if (sb > __float_as_uint(ptx::pow2i(kMaxScaleExp))) sv = __int_as_float(0x7fc00000);
         if (!live) sv = 0.f;   // whatever its row holds
 #pragma unroll
-        for (int h = 0; h < kMaxG / 2; ++h) {
-          auto part = [&](int k) {
-            const int col = k * kMaxG + 2 * h;
-            return make_float2(__uint_as_float(r[col / 16][col % 16]),
-                               __uint_as_float(r[col / 16][col % 16 + 1]));
-          };
-          float2 d = f32x2::fma(part(3), f32x2::both(1.f / kQScale3), part(2));
-          d = f32x2::fma(d, f32x2::both(1.f / kQScale2), part(1));
-          d = f32x2::fma(d, f32x2::both(1.f / kQScale1), part(0));
-          x[h] = f32x2::mul(f32x2::mul(d, f32x2::both(sk)), reinterpret_cast<float2*>(qs)[h]);
+        for (int k = 0; k < kMaxG / 4; ++k) {
+          const float4 q4 = reinterpret_cast<const float4*>(qs)[k];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int h = 2 * k + i;
+            auto part = [&](int n) {
+              const int col = n * kMaxG + 2 * h;
+              return make_float2(__uint_as_float(r[col / 16][col % 16]),
+                                 __uint_as_float(r[col / 16][col % 16 + 1]));
+            };
+            float2 d = f32x2::fma(part(3), f32x2::both(1.f / kQScale3), part(2));
+            d = f32x2::fma(d, f32x2::both(1.f / kQScale2), part(1));
+            d = f32x2::fma(d, f32x2::both(1.f / kQScale1), part(0));
+            x[h] = f32x2::mul(f32x2::mul(d, f32x2::both(sk)), half_of(q4, i));
+          }
         }
         if (pages < 2 || tok0 < s.U.tok_start || tok0 + kStep > s.U.tok_end) {
 #pragma unroll
@@ -907,15 +915,16 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
             if (!live) x[h] = f32x2::both(-INFINITY);
         }
       }
-      const bool odd = __any_sync(0xffffffffu, fraction != 0);
       bool move = first;
       if (!move) {
         // A token above a ref, or one that might lie too far above an m?
         float most = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < kMaxG / 2; ++h) {
-          const float2 y = f32x2::add(x[h], st.minus_ref[h]);
-          most = fmaxf(most, fmaxf(y.x, y.y));
+        for (int k = 0; k < kMaxG / 4; ++k) {
+          const float4 r4 = st.minus_ref[k];
+          const float2 a = f32x2::add(x[2 * k], half_of(r4, 0));
+          const float2 b = f32x2::add(x[2 * k + 1], half_of(r4, 1));
+          most = fmaxf(most, fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)));
         }
         move = any_in_group(barrier, kStep, fail || most > -up || (live && up < lowest));
       }
@@ -951,62 +960,54 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
           const float ref = fmaxf(fmaxf(had, ref_ceil(top_sv)), m - kMaxUnder);
           at(st.minus_m) = -m;
           at(st.minus_ref) = -ref;
+          at(st.ref) = ref;
           at(st.weight) = kFirstPart * ptx::pow2i((int)(m - ref));
           at(st.by) = ref_weight(old, m);
+          at(st.by_ref) = ref_weight(had, ref);
           // (a head without a reference yet looks at every token)
           at(st.gap) = m == kNoRef ? -kNoRef : ref - m;
         }
         ptx::named_barrier(barrier, kStep);
         lowest = kNoRef;
 #pragma unroll
-        for (int h = 0; h < kMaxG / 2; ++h) {
-          lowest = fmaxf(lowest, fmaxf(st.gap[h].x, st.gap[h].y));
-          l[h] = f32x2::mul(l[h], st.by[h]);
-          rounded[h] = f32x2::mul(rounded[h], st.by[h]);
+        for (int k = 0; k < kMaxG / 4; ++k) {
+          const float4 g = st.gap[k], a = st.by[k], b = st.by_ref[k];
+          lowest = fmaxf(lowest, fmaxf(fmaxf(g.x, g.y), fmaxf(g.z, g.w)));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            l[2 * k + i] = f32x2::mul(l[2 * k + i], half_of(a, i));
+            left[2 * k + i] = f32x2::mul(left[2 * k + i], half_of(b, i));
+          }
         }
         lowest -= kSlack;
         first = false;
       }
-      float2 e[kMaxG / 2];
-#pragma unroll
-      for (int h = 0; h < kMaxG / 2; ++h) {
-        const float2 y = f32x2::add(x[h], st.minus_m[h]);
-        e[h] = make_float2(ptx::ex2(y.x), ptx::ex2(y.y));
-      }
-      float f_inv = 1.f;
-      if (odd) {
-        const float f = __uint_as_float(fraction | 0x3f800000u);
-        f_inv = __fdividef(1.f, f);
-#pragma unroll
-        for (int h = 0; h < kMaxG / 2; ++h) e[h] = f32x2::mul(e[h], f32x2::both(f));
-      }
       uint32_t codes[2 * kParts];   // this token's row: kParts times the eight heads
+      __half2 last[kMaxG / 2];      // what the last part rounds
 #pragma unroll
       for (int k = 0; k < kMaxG / 4; ++k) {
+        const float4 m4 = st.minus_m[k], w4 = st.weight[k];
         float2 w[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int h = 2 * k + i;
-          const float2 r = cut19(e[h]);
-          l[h] = f32x2::fma(e[h], f32x2::both(f_inv), l[h]);
-          rounded[h] = f32x2::fma(r, f32x2::both(f_inv), rounded[h]);
-          w[i] = f32x2::mul(f32x2::mul(r, f32x2::both(sv)), st.weight[h]);
+          const float2 y = f32x2::add(x[h], half_of(m4, i));
+          const float2 e = make_float2(ptx::ex2(y.x), ptx::ex2(y.y));
+          l[h] = f32x2::add(l[h], e);
+          w[i] = f32x2::mul(f32x2::mul(e, f32x2::both(sv)), half_of(w4, i));
         }
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
+        for (int part = 0; part + 1 < kParts; ++part) {
           codes[2 * part + k] = fp8::pack4(w[0].x, w[0].y, w[1].x, w[1].y);
 #pragma unroll
           for (int i = 0; i < 2; ++i)   // and w becomes (w - code) kPartRatio
             w[i] = f32x2::fma(fp8::unpack2(codes[2 * part + k] >> 16 * i), f32x2::both(-kPartRatio),
                               f32x2::mul(w[i], f32x2::both(kPartRatio)));
         }
-        const __half2 u0 = __floats2half2_rn(w[0].x, w[0].y);   // 10 bits are left: exact
-        const __half2 u1 = __floats2half2_rn(w[1].x, w[1].y);
-        const __half2 ratio = __float2half2_rn(kPartRatio);
-        const uint32_t c = fp8::pack4(u0, u1);
-        codes[4 + k] = c;
-        codes[6 + k] = fp8::pack4(__hmul2(__hsub2(u0, fp8::unpack2_half(c)), ratio),
-                                  __hmul2(__hsub2(u1, fp8::unpack2_half(c >> 16)), ratio));
+#pragma unroll
+        for (int i = 0; i < 2; ++i)     // (exact: 10 bits are left)
+          last[2 * k + i] = __floats2half2_rn(w[i].x, w[i].y);
+        codes[2 * kParts - 2 + k] = fp8::pack4(last[2 * k], last[2 * k + 1]);
       }
       // Step it - 2's product is done: its P buffer is free, and so is the
       // reference slot of step it - 4 (the product waited for the output warps
@@ -1036,10 +1037,29 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(v.bar(S::kPFull + group));
-      if (tok == 0) {   // (behind P: the output warps need it a product later)
-        float2* to = reinterpret_cast<float2*>(v.base + S::kRef) + (it % kRefs) * (kMaxG / 2);
+      // What is left of the w that have all 19 bits, 2^-6 and more: their first part's
+      // exponent is not zero.  (The parts of smaller ones end at a step of their own; where
+      // V's scale is small that is a large share of a probability, which counts in full.)
+      const float inv = sv == 0.f ? 0.f : __fdividef(1.f, sv);
 #pragma unroll
-        for (int k = 0; k < kMaxG / 2; ++k) to[k] = negative(st.minus_ref[k]);
+      for (int k = 0; k < kMaxG / 4; ++k) {
+        const uint32_t normal = (codes[k] & 0x78787878u) + 0x78787878u;   // in each byte's bit 7
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int h = 2 * k + i;
+          const __half2 rest = __hsub2(
+              last[h], fp8::unpack2_half(codes[2 * kParts - 2 + k] >> 16 * i));
+          const uint32_t bits = *reinterpret_cast<const uint32_t*>(&rest) &
+                                (i ? sign_bytes<0xbbaa>(normal) : sign_bytes<0x9988>(normal));
+          left[h] = f32x2::fma(__half22float2(*reinterpret_cast<const __half2*>(&bits)),
+                               f32x2::both(inv), left[h]);
+        }
+      }
+      // (behind P, as the above: the output warps need it a product later)
+      if (tok == 0) {
+        float4* to = reinterpret_cast<float4*>(v.base + S::kRef) + (it % kRefs) * (kMaxG / 4);
+#pragma unroll
+        for (int k = 0; k < kMaxG / 4; ++k) to[k] = st.ref[k];
         ptx::mbar_arrive(v.bar(S::kRefFull + it % kRefs));
       }
     }
@@ -1052,8 +1072,8 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
     float2 sum[kMaxG];
 #pragma unroll
     for (int h = 0; h < kMaxG / 2; ++h) {
-      sum[2 * h] = make_float2(l[h].x, rounded[h].x);
-      sum[2 * h + 1] = make_float2(l[h].y, rounded[h].y);
+      sum[2 * h] = make_float2(l[h].x, left[h].x);
+      sum[2 * h + 1] = make_float2(l[h].y, left[h].y);
     }
 #pragma unroll
     for (int n = kMaxG / 2; n; n >>= 1) {
@@ -1074,12 +1094,14 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       seg_l[kMaxG + (lane >> 2)] = sum[0].y;
     }
     if (tok == 0) {
-      float2* sr = reinterpret_cast<float2*>(v.base + S::kSegRef) +
-                   ((seg & 1) * kGroups + group) * 2 * (kMaxG / 2);
+      float4* sr = reinterpret_cast<float4*>(v.base + S::kSegRef) +
+                   ((seg & 1) * kGroups + group) * 2 * (kMaxG / 4);
+      const float4 none = make_float4(kNoRef, kNoRef, kNoRef, kNoRef);
 #pragma unroll
-      for (int k = 0; k < kMaxG / 2; ++k) {
-        sr[k] = first ? f32x2::both(kNoRef) : negative(st.minus_m[k]);
-        sr[kMaxG / 2 + k] = first ? f32x2::both(kNoRef) : negative(st.minus_ref[k]);
+      for (int k = 0; k < kMaxG / 4; ++k) {
+        const float4 m = st.minus_m[k];
+        sr[k] = first ? none : make_float4(-m.x, -m.y, -m.z, -m.w);
+        sr[kMaxG / 4 + k] = first ? none : st.ref[k];
       }
       v.seg_poison[(seg & 1) * kGroups + group] = poisoned;
     }

@@ -3,7 +3,7 @@ float64 oracle.
 
 Bounds.  With A = scale max_j sum_d |q_d k_jd|, a score is within 8 steps of 2^-24 of
 A, the exponential of it within 2^-21: d = 2^-21 A + 2^-21 relative for a probability
-before it is rounded, to nearest at 19 bits: 2^-19 more.  An error d_j of the
+before it is held in four parts of 4 bits and a sign: 2^-19 more.  An error d_j of the
 probabilities p_j moves the output, whose sum has the same errors, by sum p_j d_j
 (V_j - out), at most (d + 2^-19) sum_j p_j |V_j - out|; the rest is a few FP32
 roundings, 8 of 2^-24 of sum_j p_j |V_j|.  A probability times its V scale s_j is held relative to a

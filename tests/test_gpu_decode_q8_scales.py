@@ -174,3 +174,15 @@ def test_rows_of_zeros_in_a_block_of_a_large_scale(B):
     r.run(B)
     r.check()
     assert r.out.isfinite().all() and torch.allclose(r.lse, torch.log(torch.tensor(16.0 * n)))
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("apart", [6, 9, 12, 14, 16, 20, 26, 32])
+def test_probabilities_beside_a_larger_v_scale_count_in_full(B, apart, d):
+    """A block whose V scale is 2^apart below the next one's: what its keys' products lose
+    to the parts' smallest step does not change what they weigh."""
+    for seed in range(4):
+        r = Rows([-7] * 9, [40 - apart] * 4 + [40] + [40 - apart] * 4, d=d, seed=apart + 50 * seed,
+                 q_scale=[1.0, 4.0, 2.0, 0.1][seed], tiles=[(0, 144), (63, 70), (50, 144)])
+        r.run(B)
+        r.check()

@@ -5,7 +5,7 @@ Bounds.  K is zero where q is large, so the scores come from the small values al
 with A = scale max_j sum_d |q_d k_jd| over those, FP32 sums and the scaling leave 8
 steps of 2^-24 of A, the exponential 2^-21, and q's own representation 2^-32 of its
 largest value: r = scale 2^-32 max |q| max_j sum_d |k_jd|.  d = 2^-21 A + 2^-21 + r
-relative for a probability, and 2^-19 more where it is cut to 19 bits; the output is
+relative for a probability, and 2^-19 more where it is held in parts; the output is
 within (d + 2^-19) sum_j p_j |V_j - out| + 2^-21 sum_j p_j |V_j| + 2^-25 max_j(p_j s_j)
 sum_j |code_j| (steps of the smallest probabilities, s_j V's scale), the log-sum-exp
 within d + 2^-22 of itself.
