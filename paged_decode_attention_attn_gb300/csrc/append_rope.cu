@@ -632,8 +632,8 @@ cudaError_t launch_append(const Tokens& t, void* pool, cudaStream_t stream) {
 
 // Token rows a CTA looks through for blocks to store: a power of two that leaves
 // about two waves of CTAs (one that finds none leaves at once; one that finds
-// several takes them one after the other), and no more than 2 where most rows
-// are a request, and so a block, of their own.  (1 / 2 / 4 / 8 / 16 rows, with q:
+// several takes them one after the other), but no more than a request has on
+// average, or 2 where most rows are a request, and so a block, of their own.  (1 / 2 / 4 / 8 / 16 rows, with q:
 // 40 requests of up to 71 tokens 17.5 / 16.1 / 15.9 / 18.0 / 22.6 us; 3 of 600
 // 20.5 / 17.9 / 17.1 / 17.9 / 20.8; 2 of 4,050 57.8 / 51.5 / 48.4 / 46.6 / 45.8;
 // 1,200 of one 19.4 / 16.6 / 19.8 / 23.4 / 41.6.)

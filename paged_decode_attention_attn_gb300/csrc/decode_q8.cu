@@ -4,7 +4,12 @@
 // The bytes of the codes bound it: 2 D bytes per token and kv head, half of the
 // bf16 pool's, so each SM has half the time per token that the bf16 kernel has.
 // Both products therefore run on the fifth-generation tensor cores straight
-// from the codes as TMA leaves them in shared memory; no thread touches a code.
+// from the codes as TMA leaves them in shared memory.  No thread reads a code; the
+// softmax threads write some: rows of V outside the tile (a NaN code there would
+// reach the product) are cleared in the stage, before the fence and the arrival
+// that hand the product its P.
+// Times beside a choice compare it with the alternative on one box at the time it
+// was made; what whole launches take now is measured on the finished kernel.
 //
 //  * Work split and partials: as the bf16 kernel (split_units.cuh); a request's
 //    tiles are merged by a kernel of its own.  A CTA streams its pages two at a
@@ -23,15 +28,15 @@
 //    e_j sv_j 2^(m - ref) lies in [0, 1] and the largest in (2^-8, 1] whatever the
 //    scales.  (One reference for both lost keys from the sum where V's scales lay
 //    more than 2^126 apart, and small probabilities beside V scales near 2^100.)
-//    They move rarely, and then by an exact power of two.  w is held
-//    as kParts e4m3 parts, each the rounding of what the parts before left, 32 times
-//    finer (that stays below 256 = 2^8, as w 2^8 does): a part takes 5 bits (4 and a
-//    sign), so a w is within 2^-19 of itself, 3.5e-7 on the root mean square, or
-//    within 2^-33 of the row's bound.  What the last part leaves in the first case is
-//    summed too, as left_j / sv_j, and taken from the sum that divides the outputs:
-//    numerator and denominator have the same probabilities, and a row that hangs on
-//    few keys loses nothing to the parts.  (Cutting w to the 19 bits that every w has did the same
-//    at twice the error on long rows.)  The log-sum-exp takes the whole sum.
+//    They move rarely, and then by an exact power of two.  w is held as kParts e4m3
+//    parts, each the rounding of what the parts before left, 32 times finer (that
+//    stays below 256 = 2^8, as w 2^8 does): a part takes 5 bits (4 and a sign), so a w
+//    is within 2^-19 of itself, 3.5e-7 on the root mean square, or within 2^-33 of the
+//    row's bound.  What the last part leaves in the first case is summed too, as
+//    left_j / sv_j, and taken from the sum that divides the outputs: numerator and
+//    denominator have the same probabilities, and a row that hangs on few keys loses
+//    nothing to the parts.  (Cutting w to the 19 bits that every w has did the same at
+//    twice the error on long rows.)  The log-sum-exp takes the whole sum.
 //  * O^T = V^T P^T: M = 128 dims (a step's V codes as they lie, M-major), N =
 //    8 kParts (a token's row of P, N-major), K = 128 tokens.  Every step's
 //    product starts from zero in tensor memory and is added to fp32 registers (a
