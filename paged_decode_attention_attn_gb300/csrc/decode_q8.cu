@@ -1045,7 +1045,7 @@ __device__ __forceinline__ void softmax_warps(const P& p, const View& v, uint32_
       // What is left of the w that have all 19 bits, 2^-6 and more: their first part's
       // exponent is not zero.  (The parts of smaller ones end at a step of their own; where
       // V's scale is small that is a large share of a probability, which counts in full.)
-      const float inv = sv == 0.f ? 0.f : __fdividef(1.f, sv);
+      const float inv = fabsf(sv) >= ptx::pow2i(kMinScaleExp) ? __fdividef(1.f, sv) : 0.f;
 #pragma unroll
       for (int k = 0; k < kMaxG / 4; ++k) {
         const uint32_t normal = (codes[k] & 0x78787878u) + 0x78787878u;   // in each byte's bit 7

@@ -186,3 +186,13 @@ def test_probabilities_beside_a_larger_v_scale_count_in_full(B, apart, d):
                  q_scale=[1.0, 4.0, 2.0, 0.1][seed], tiles=[(0, 144), (63, 70), (50, 144)])
         r.run(B)
         r.check()
+
+
+@pytest.mark.parametrize("exp", [-140, -127, -120])
+def test_v_scales_below_the_range_are_as_good_as_zero(B, exp):
+    """Beside scales of 1: the keys count, their values do not show."""
+    for v in ([exp] * 16 + [0] * 16, [0] * 16 + [exp] * 16, [exp] * 31 + [0]):
+        r = Rows([-7] * 32, v, seed=3)
+        r.run(B)
+        assert r.out.isfinite().all() and r.merged.isfinite().all()
+        r.check()
