@@ -366,6 +366,24 @@ int kv_append_rope(const void* q, const void* k, const void* v, int64_t q_stride
                    const int32_t* page_table, int max_pages, int32_t* status,
                    cudaStream_t stream);
 
+/* kv_append_rope with a root-mean-square norm of every q and k head ahead of the
+ * rotation: with x the head's head_dim values,
+ *     y = x * w / sqrt(mean(x^2) + eps),
+ * w = q_weight for q heads and k_weight for k heads, in FP32 (whatever the size of
+ * finite x: sums that pass FP32's range are scaled).  The result is rotated and
+ * rounded once, to bf16.  A head that holds a NaN becomes NaN, one that holds an
+ * infinity NaN there and 0 elsewhere.  v passes unchanged.  Arguments as above, and:
+ *   q_weight, k_weight  device fp32 [head_dim] (q_weight may be NULL without q).
+ *   eps                 in [2^-60, 1]. */
+int kv_append_norm_rope(const void* q, const void* k, const void* v, int64_t q_stride,
+                        int64_t k_stride, int64_t v_stride, void* q_out, int64_t q_out_stride,
+                        const int32_t* cu_tokens, const int32_t* positions, int n_tokens, int B,
+                        int n_q_heads, int n_kv_heads, int head_dim, const float* q_weight,
+                        const float* k_weight, float eps, const float* inv_freq, int rot_dim,
+                        unsigned flags, void* pool, int64_t pool_pages,
+                        const int32_t* page_table, int max_pages, int32_t* status,
+                        cudaStream_t stream);
+
 /* kv_append_rope into an 8-bit pool.  Arguments as above, except:
  *   pool    device e4m3 pages, 16-byte aligned;  scales  device fp32, 16-byte
  *           aligned (both as described at PA_SCALE_TOKENS).
@@ -429,6 +447,65 @@ size_t paged_decode_attn_q8_workspace_bytes(int B, int T, int n_q_heads, int n_k
  * rounding), the log-sum-exp takes the sum of the whole ones.
  * Supported: head_dim 128 and 256, n_q_heads / n_kv_heads in 1..8. */
 int paged_decode_attn_q8_lse(const void* q, const void* pool, const float* scales,
+                             int64_t pool_pages, const int32_t* page_table, int max_pages,
+                             const int32_t* tiles, int B, int T, int n_q_heads, int n_kv_heads,
+                             int head_dim, float scale, float* out, float* lse,
+                             float* merged_out, float* merged_lse, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The 4-bit pool  (no counterpart in the source pages)                     */
+/* ------------------------------------------------------------------------ */
+
+/* 4-bit pool: for every page and every K head (first Hkv) and V head the page's
+ * PA_PAGE_TOKENS rows, one after the other,
+ *   pool    uint8 [pool_pages][2*Hkv][64][head_dim / 2]: e2m1 codes (a sign, two
+ *           exponent bits, a fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), value 2i of
+ *           a head in the low and 2i + 1 in the high bits of byte i;
+ *   scales  uint8 [pool_pages][2*Hkv][64][head_dim / 32]: one for PA_Q4_GROUP
+ *           neighbouring values of a token's head; e stands for 2^(e - 127), 255 for
+ *           NaN.
+ * A value is code * scale: the microscaling format of 4-bit floats with blocks of 32
+ * along the head.  A token's codes and scales depend on no other token. */
+#define PA_Q4_GROUP 32
+
+/* kv_append_norm_rope into a 4-bit pool.  Arguments as there, except:
+ *   q_weight, k_weight  both NULL: no norm (eps is not looked at).
+ *   pool, scales        device, 16-byte aligned (both as described above).
+ * For every group of 32 values of the normed and rotated k, and of v, in FP32: the
+ * scale is the smallest power of two s >= 2^-60 with |x| <= 6 s for all of them, and
+ * the codes are x / s rounded to nearest even.  A group with a value that is not
+ * finite gets the scale NaN.  Rows of other tokens are left as they are.
+ * Supported head_dim: 128, 256. */
+int kv_append_rope_q4(const void* q, const void* k, const void* v, int64_t q_stride,
+                      int64_t k_stride, int64_t v_stride, void* q_out, int64_t q_out_stride,
+                      const int32_t* cu_tokens, const int32_t* positions, int n_tokens, int B,
+                      int n_q_heads, int n_kv_heads, int head_dim, const float* q_weight,
+                      const float* k_weight, float eps, const float* inv_freq, int rot_dim,
+                      unsigned flags, void* pool, uint8_t* scales, int64_t pool_pages,
+                      const int32_t* page_table, int max_pages, int32_t* status,
+                      cudaStream_t stream);
+
+/* Rows of a 4-bit pool as bf16 values (exact): arguments and padding rows as
+ * kv_gather_q8.  A position or page id outside the table or the pool gives a row of
+ * NaN and PA_STATUS_BAD_ROW.  Supported head_dim: 128, 256. */
+int kv_gather_q4(const void* pool, const uint8_t* scales, int64_t pool_pages,
+                 const int32_t* page_table, int max_pages, const int32_t* cu_tokens,
+                 const int32_t* positions, int n_tokens, int B, int n_kv_heads, int head_dim,
+                 void* out, int32_t* status, cudaStream_t stream);
+
+/* Workspace bytes paged_decode_attn_q4_lse needs (as
+ * paged_decode_attn_lse_workspace_bytes; 0 for an unsupported geometry). */
+size_t paged_decode_attn_q4_workspace_bytes(int B, int T, int n_q_heads, int n_kv_heads,
+                                            int head_dim);
+
+/* paged_decode_attn_lse over a 4-bit pool: the same definition with K_j, V_j = codes *
+ * scales, the same tiles, status word, workspace rules and merged outputs as
+ * paged_decode_attn_q8_lse.  Arguments as there, except:
+ *   pool, scales  device, 16-byte aligned, as described at PA_Q4_GROUP.
+ * Rows outside a tile may hold anything, NaN scales too.
+ * Supported: head_dim 128 and 256, n_q_heads / n_kv_heads in 1..8. */
+int paged_decode_attn_q4_lse(const void* q, const void* pool, const uint8_t* scales,
                              int64_t pool_pages, const int32_t* page_table, int max_pages,
                              const int32_t* tiles, int B, int T, int n_q_heads, int n_kv_heads,
                              int head_dim, float scale, float* out, float* lse,

@@ -9,7 +9,8 @@ imports nothing from that package.
 Everything is plain NumPy in float64 (the compact-page format's own steps in
 binary32, as the format defines them).  Parity of every function here is
 pinned by the ``-m "not gpu"`` tests in ``tests/test_oracle_pins.py``,
-``tests/test_oracle_compact_pins.py`` and ``tests/test_oracle_rope_q8_pins.py``
+``tests/test_oracle_compact_pins.py``, ``tests/test_oracle_rope_q8_pins.py`` and
+``tests/test_oracle_rope_q4_pins.py``
 (brute force, closed forms, invariants, a published check value and library
 second opinions); no function is "parity unpinned".
 """
@@ -26,3 +27,4 @@ from .paged_attention import (  # noqa: F401
 )
 from . import compact_pages  # noqa: F401,E402
 from . import rope_q8  # noqa: F401,E402
+from . import rope_q4  # noqa: F401,E402

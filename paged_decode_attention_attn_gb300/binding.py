@@ -37,6 +37,7 @@ PA_STALL_VALUES = 1 << 30
 PA_ROPE_INTERLEAVED = 1
 PAGE_TOKENS = 64
 SCALE_TOKENS = 16
+Q4_GROUP = 32
 
 # Every symbol pagedattn.h declares.
 EXPORTED = [
@@ -47,6 +48,8 @@ EXPORTED = [
     "paged_decode_attn_test_slice_wait", "lse_merge",
     "kv_append_rows", "kv_append_rope", "kv_append_rope_q8", "kv_gather_q8",
     "paged_decode_attn_q8_workspace_bytes", "paged_decode_attn_q8_lse",
+    "kv_append_norm_rope", "kv_append_rope_q4", "kv_gather_q4",
+    "paged_decode_attn_q4_workspace_bytes", "paged_decode_attn_q4_lse",
     "kv_arena_create", "kv_arena_destroy", "kv_arena_drain", "kv_stage_layer",
     "kv_mark_attention_done", "kv_writeback_tail", "kv_load_resident", "kv_arena_get_stats",
     "kv_arena_fail_after", "kv_arena_call_log",
@@ -247,6 +250,7 @@ def _load():
     lib.kv_append_rows.argtypes = [vp, i64, vp, i32, vp, vp, i32, i32, vp, vp]
     rope = [vp, vp, vp, i64, i64, i64, vp, i64, vp, vp, i32, i32, i32, i32, i32, vp, i32,
             ctypes.c_uint, vp]
+    norm = rope[:15] + [vp, vp, ctypes.c_float] + rope[15:]
     lib.kv_append_rope.restype = i32
     lib.kv_append_rope.argtypes = rope + [i64, vp, i32, vp, vp]
     lib.kv_append_rope_q8.restype = i32
@@ -258,6 +262,16 @@ def _load():
     lib.paged_decode_attn_q8_lse.restype = i32
     lib.paged_decode_attn_q8_lse.argtypes = [vp, vp, vp, i64, vp, i32, vp, i32, i32, i32, i32, i32,
                                              ctypes.c_float, vp, vp, vp, vp, vp, sz, vp]
+    lib.kv_append_norm_rope.restype = i32
+    lib.kv_append_norm_rope.argtypes = norm + [i64, vp, i32, vp, vp]
+    lib.kv_append_rope_q4.restype = i32
+    lib.kv_append_rope_q4.argtypes = norm + [vp, i64, vp, i32, vp, vp]
+    lib.kv_gather_q4.restype = i32
+    lib.kv_gather_q4.argtypes = lib.kv_gather_q8.argtypes
+    lib.paged_decode_attn_q4_workspace_bytes.restype = sz
+    lib.paged_decode_attn_q4_workspace_bytes.argtypes = [i32] * 5
+    lib.paged_decode_attn_q4_lse.restype = i32
+    lib.paged_decode_attn_q4_lse.argtypes = lib.paged_decode_attn_q8_lse.argtypes
     lib.kv_arena_create.restype = i32
     lib.kv_arena_create.argtypes = [ctypes.POINTER(KvArenaDesc), ctypes.POINTER(vp)]
     for name in ("kv_arena_destroy", "kv_arena_drain"):
@@ -606,15 +620,12 @@ def _check_requests(page_table, positions, cu_tokens, dev):
             None if cu_tokens is None else _ptr(cu_tokens, i32, dev, "cu_tokens", (bn + 1,)))
 
 
-def _append_rope(fn, dtype, q, k, v, pool, scales, page_table, positions, inv_freq, q_out,
-                 cu_tokens, interleaved, status, stream):
-    dev, n_pages, row = _pages(pool, dtype)
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("k must be a tensor [tokens][Hkv][D]")
+def _append_rope(fn, q, k, v, pool, scales, dev, n_pages, page_table, positions, inv_freq, q_out,
+                 cu_tokens, interleaved, status, stream, norm=()):
+    """The call of an append: ``scales`` the pointer of the pool's scales or None,
+    ``norm`` the norms' arguments where the call has them."""
     kv_shape = k.shape
     n, n_kv, d = kv_shape
-    if row != 2 * n_kv * d:
-        raise ValueError(f"pool rows must hold 2*Hkv*D = {2 * n_kv * d} values, got {row}")
     k_ptr, k_st = _token_rows(k, kv_shape, dev, "k")
     v_ptr, v_st = _token_rows(v, kv_shape, dev, "v")
     q_ptr = o_ptr = None
@@ -638,13 +649,38 @@ def _append_rope(fn, dtype, q, k, v, pool, scales, page_table, positions, inv_fr
     flags = PA_ROPE_INTERLEAVED if interleaved else 0
     if scales is None:
         _call_on(dev, stream, fn, q_ptr, k_ptr, v_ptr, q_st, k_st, v_st, o_ptr, o_st, cu, pos, n,
-                 bn, hq, n_kv, d, inv, rot, flags, pool.data_ptr(), n_pages, table, max_pages, st)
+                 bn, hq, n_kv, d, *norm, inv, rot, flags, pool.data_ptr(), n_pages, table,
+                 max_pages, st)
     else:
-        sc = _ptr(scales, torch.float32, dev, "scales",
-                  (n_pages, 2 * n_kv, PAGE_TOKENS // SCALE_TOKENS))
         _call_on(dev, stream, fn, q_ptr, k_ptr, v_ptr, q_st, k_st, v_st, o_ptr, o_st, cu, pos, n,
-                 bn, hq, n_kv, d, inv, rot, flags, pool.data_ptr(), sc, n_pages, table, max_pages,
-                 st)
+                 bn, hq, n_kv, d, *norm, inv, rot, flags, pool.data_ptr(), scales, n_pages, table,
+                 max_pages, st)
+
+
+def _token_shape(k):
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a tensor [tokens][Hkv][D]")
+    return k.shape
+
+
+def _row_pool(pool, dtype, k):
+    """Device and pages of a pool of token rows [pages][64][2*Hkv*D]."""
+    dev, n_pages, row = _pages(pool, dtype)
+    _, n_kv, d = _token_shape(k)
+    if row != 2 * n_kv * d:
+        raise ValueError(f"pool rows must hold 2*Hkv*D = {2 * n_kv * d} values, got {row}")
+    return dev, n_pages
+
+
+def _norm_args(q, d, q_weight, k_weight, eps, dev):
+    shape = (d,)
+    if q is None:
+        qw = None
+    elif q_weight is None:
+        raise ValueError("q_weight is required with q")
+    else:
+        qw = _ptr(q_weight, torch.float32, dev, "q_weight", shape)
+    return qw, _ptr(k_weight, torch.float32, dev, "k_weight", shape), float(eps)
 
 
 def kv_append_rope(q, k, v, pool, page_table, positions, inv_freq, q_out=None, cu_tokens=None,
@@ -656,8 +692,21 @@ def kv_append_rope(q, k, v, pool, page_table, positions, inv_freq, q_out=None, c
     [B+1]: each request's rows (None: one row per request); ``inv_freq`` fp32
     [rot_dim/2], None: no rotation; ``interleaved``: pairs (2i, 2i+1) instead
     of (i, i + rot_dim/2)."""
-    _append_rope(lib.kv_append_rope, torch.bfloat16, q, k, v, pool, None, page_table, positions,
+    dev, n_pages = _row_pool(pool, torch.bfloat16, k)
+    _append_rope(lib.kv_append_rope, q, k, v, pool, None, dev, n_pages, page_table, positions,
                  inv_freq, q_out, cu_tokens, interleaved, status, stream)
+
+
+def kv_append_norm_rope(q, k, v, pool, page_table, positions, inv_freq, q_weight, k_weight,
+                        q_out=None, cu_tokens=None, interleaved=False, eps=1e-6, status=None,
+                        stream=None):
+    """kv_append_rope with a root-mean-square norm of every q and k head ahead of
+    the rotation: x * weight / sqrt(mean(x^2) + eps), ``q_weight`` and
+    ``k_weight`` fp32 [D] (q_weight None without q)."""
+    dev, n_pages = _row_pool(pool, torch.bfloat16, k)
+    norm = _norm_args(q, k.shape[2], q_weight, k_weight, eps, dev)
+    _append_rope(lib.kv_append_norm_rope, q, k, v, pool, None, dev, n_pages, page_table, positions,
+                 inv_freq, q_out, cu_tokens, interleaved, status, stream, norm)
 
 
 def kv_append_rope_q8(q, k, v, pool, scales, page_table, positions, inv_freq, q_out=None,
@@ -667,8 +716,11 @@ def kv_append_rope_q8(q, k, v, pool, scales, page_table, positions, inv_freq, q_
     head)."""
     if scales is None:
         raise ValueError("scales must be [pages][2*Hkv][4]")
-    _append_rope(lib.kv_append_rope_q8, torch.float8_e4m3fn, q, k, v, pool, scales, page_table,
-                 positions, inv_freq, q_out, cu_tokens, interleaved, status, stream)
+    dev, n_pages = _row_pool(pool, torch.float8_e4m3fn, k)
+    sc = _ptr(scales, torch.float32, dev, "scales",
+              (n_pages, 2 * k.shape[1], PAGE_TOKENS // SCALE_TOKENS))
+    _append_rope(lib.kv_append_rope_q8, q, k, v, pool, sc, dev, n_pages, page_table, positions,
+                 inv_freq, q_out, cu_tokens, interleaved, status, stream)
 
 
 def kv_gather_q8(pool, scales, page_table, positions, cu_tokens, out, status=None, stream=None):
@@ -709,13 +761,25 @@ def paged_decode_attn_q8_lse(q, pool, scales, page_table, tiles, scale, out, lse
     ``merged_out`` [B][Hq][D] / ``merged_lse`` [B][Hq] receive the merge of
     every request's tiles in the same call."""
     dev, n_pages, row = _pages(pool, torch.float8_e4m3fn)
-    q_shape = q.shape
-    if len(q_shape) != 3 or q_shape[2] == 0:
+    if q.dim() != 3 or q.shape[2] == 0:
         raise ValueError("q must be [B][Hq][D]")
-    bn, hq, d = q_shape
+    d = q.shape[2]
     n_kv = row // (2 * d)
     if row != 2 * n_kv * d:
         raise ValueError(f"pool rows must hold 2*Hkv*D values with D = {d}, got {row}")
+    sc = _ptr(scales, torch.float32, dev, "scales",
+              (n_pages, 2 * n_kv, PAGE_TOKENS // SCALE_TOKENS))
+    _decode_tiles(lib.paged_decode_attn_q8_lse, q, pool, sc, dev, n_pages, n_kv, d, page_table,
+                  tiles, scale, out, lse, workspace, merged_out, merged_lse, stream)
+
+
+def _decode_tiles(fn, q, pool, sc, dev, n_pages, n_kv, d, page_table, tiles, scale, out, lse,
+                  workspace, merged_out, merged_lse, stream):
+    """The call of a decode over a pool with scales."""
+    q_shape = q.shape
+    if len(q_shape) != 3 or q_shape[2] != d:
+        raise ValueError(f"q must be [B][Hq][{d}], got {list(q_shape)}")
+    bn, hq, _ = q_shape
     if tiles.__class__ is not np.ndarray or tiles.dtype != np.int32 or \
             not tiles.flags.c_contiguous:
         tiles = np.ascontiguousarray(np.asarray(tiles, dtype=np.int32))
@@ -731,12 +795,86 @@ def paged_decode_attn_q8_lse(q, pool, scales, page_table, tiles, scale, out, lse
     if merged_out is not None or merged_lse is not None:
         m_ptr = _ptr(merged_out, f32, dev, "merged_out", q_shape)
         ml_ptr = _ptr(merged_lse, f32, dev, "merged_lse", (bn, hq))
-    _call_on(dev, stream, lib.paged_decode_attn_q8_lse, _ptr(q, torch.bfloat16, dev, "q"),
-             pool.data_ptr(),
-             _ptr(scales, f32, dev, "scales", (n_pages, 2 * n_kv, PAGE_TOKENS // SCALE_TOKENS)),
-             n_pages, table, table_shape[1], _host_ptr(tiles), bn, T, hq, n_kv, d, float(scale),
+    _call_on(dev, stream, fn, _ptr(q, torch.bfloat16, dev, "q"), pool.data_ptr(), sc, n_pages,
+             table, table_shape[1], _host_ptr(tiles), bn, T, hq, n_kv, d, float(scale),
              _ptr(out, f32, dev, "out", (bn, T, hq, d)), _ptr(lse, f32, dev, "lse", (bn, T, hq)),
              m_ptr, ml_ptr, _ptr(workspace, torch.uint8, dev, "workspace"), workspace.numel())
+
+
+def _q4_pool(pool, scales):
+    """CUDA device, pages, 2*Hkv, D and the scales' pointer of a 4-bit pool [pages][2*Hkv][64][D/2]
+    with scales [pages][2*Hkv][64][D/32]."""
+    u8 = torch.uint8
+    try:
+        if pool.dtype is u8 and pool.is_contiguous():
+            dev = pool.get_device()
+            n_pages, heads, tokens, half = pool.shape
+            if dev >= 0 and tokens == PAGE_TOKENS and heads > 0 and heads % 2 == 0 and \
+                    half > 0 and half % (Q4_GROUP // 2) == 0:
+                return dev, n_pages, heads, 2 * half, _ptr(
+                    scales, u8, dev, "scales", (n_pages, heads, tokens, 2 * half // Q4_GROUP))
+    except (AttributeError, ValueError):
+        pass
+    _dev(pool, u8, "pool", contiguous=False)
+    if not pool.is_contiguous() or pool.dim() != 4 or pool.shape[1] % 2 or \
+            pool.shape[2] != PAGE_TOKENS or 0 in pool.shape[1:] or \
+            pool.shape[3] % (Q4_GROUP // 2):
+        raise ValueError("pool must be contiguous [pages][2*Hkv][64][D/2]")
+    n_pages, heads, tokens, half = pool.shape
+    _ptr(scales, u8, pool.get_device(), "scales",
+         (n_pages, heads, tokens, 2 * half // Q4_GROUP))     # raises for what it checks
+    raise ValueError("scales must be [pages][2*Hkv][64][D/32]")
+
+
+def kv_append_rope_q4(q, k, v, pool, scales, page_table, positions, inv_freq, q_out=None,
+                      cu_tokens=None, interleaved=False, q_weight=None, k_weight=None, eps=1e-6,
+                      status=None, stream=None):
+    """kv_append_rope into a 4-bit pool: pool uint8 [pages][2*Hkv][64][D/2] (two
+    e2m1 codes a byte), scales uint8 [pages][2*Hkv][64][D/32] (2^(e - 127) for 32
+    values); with ``q_weight`` and ``k_weight`` (fp32 [D]) the norms of
+    kv_append_norm_rope, without both no norm."""
+    dev, n_pages, heads, d, sc = _q4_pool(pool, scales)
+    if tuple(_token_shape(k)[1:]) != (heads // 2, d):
+        raise ValueError(f"pool is for k [tokens][{heads // 2}][{d}], got {list(k.shape)}")
+    norm = (None, None, 0.0)
+    if k_weight is not None:
+        norm = _norm_args(q, d, q_weight, k_weight, eps, dev)
+    elif q_weight is not None:
+        raise ValueError("q_weight without k_weight")
+    _append_rope(lib.kv_append_rope_q4, q, k, v, pool, sc, dev, n_pages, page_table, positions,
+                 inv_freq, q_out, cu_tokens, interleaved, status, stream, norm)
+
+
+def kv_gather_q4(pool, scales, page_table, positions, cu_tokens, out, status=None, stream=None):
+    """Rows of a 4-bit pool as bf16 values: out [rows][2*Hkv*D]; row r is token
+    positions[b] + r - cu_tokens[b] of the request b that holds it (cu_tokens
+    None: one row per request)."""
+    dev, n_pages, heads, d, sc = _q4_pool(pool, scales)
+    o = _ptr(out, torch.bfloat16, dev, "out")
+    shape = out.shape
+    if len(shape) != 2 or shape[1] != heads * d:
+        raise ValueError("out must be [rows][2*Hkv*D]")
+    bn, max_pages, table, pos, cu = _check_requests(page_table, positions, cu_tokens, dev)
+    _call_on(dev, stream, lib.kv_gather_q4, pool.data_ptr(), sc, n_pages, table, max_pages, cu, pos,
+             shape[0], bn, heads // 2, d, o,
+             None if status is None else _ptr(status, torch.int32, dev, "status"))
+
+
+def alloc_workspace_q4(B, T, n_q_heads, n_kv_heads, head_dim, device="cuda") -> torch.Tensor:
+    """Zero-filled workspace for paged_decode_attn_q4_lse."""
+    n = int(lib.paged_decode_attn_q4_workspace_bytes(B, T, n_q_heads, n_kv_heads, head_dim))
+    if n == 0:
+        raise PagedAttnError(PA_ERR_UNSUPPORTED, "geometry not supported")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def paged_decode_attn_q4_lse(q, pool, scales, page_table, tiles, scale, out, lse, workspace,
+                             merged_out=None, merged_lse=None, stream=None):
+    """paged_decode_attn_lse over a 4-bit pool (kv_append_rope_q4's); the other
+    arguments as paged_decode_attn_q8_lse's."""
+    dev, n_pages, heads, d, sc = _q4_pool(pool, scales)
+    _decode_tiles(lib.paged_decode_attn_q4_lse, q, pool, sc, dev, n_pages, heads // 2, d,
+                  page_table, tiles, scale, out, lse, workspace, merged_out, merged_lse, stream)
 
 
 class Arena:

@@ -24,8 +24,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedattn.so")
 
-SOURCES = ["common.cpp", "decode_attn.cu", "lse_merge.cu", "append_rope.cu", "decode_q8.cu",
-           "arena.cu", "planner.cpp", "compact.cpp"]
+SOURCES = ["common.cpp", "decode_attn.cu", "lse_merge.cu", "append_rope.cu", "append_q4.cu",
+           "decode_q8.cu", "decode_q4.cu", "arena.cu", "planner.cpp", "compact.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
           "-Xcompiler", "-Wall"]

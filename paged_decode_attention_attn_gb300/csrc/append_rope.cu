@@ -35,269 +35,28 @@
 #include "common.h"
 #include "fp8.cuh"
 #include "ptx.cuh"
+#include "rope_rows.cuh"
 
 namespace pa {
 namespace rope {
 
-constexpr int kPage = PA_PAGE_TOKENS;
 constexpr int kBlock = PA_SCALE_TOKENS;
 constexpr int kBlocks = kPage / kBlock;   // scale blocks per page
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxTokens = 1 << 30;       // rows of a call: CTA and row numbers stay in 32 bits
-constexpr int kRowCtas = 304;             // CTAs up to which rows are shared by several warps
-
-struct Tokens {
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* k;
-  const __nv_bfloat16* v;
-  __nv_bfloat16* q_out;
-  long long q_stride, k_stride, v_stride, q_out_stride;   // elements per token
-  const int32_t* cu;          // [B + 1] or null: one token per request
-  const int32_t* positions;   // [B] position of each request's first new token
-  const float* inv_freq;      // [half]
-  const int32_t* page_table;
-  int32_t* status;
-  long long pool_pages;
-  int n_tokens, B, Hq, Hkv, half, interleaved, max_pages;
-};
-
-// Request of token row `row` (all lanes of a warp): the first whose end lies
-// behind the row.  B or more if there is none.
-__device__ __forceinline__ int request_of(const int32_t* cu, int B, int row, int lane) {
-  if (cu == nullptr) return row;
-  int n = 0;
-  for (int b = lane; b < B; b += 32) n += __ldg(cu + b + 1) <= row ? 1 : 0;
-  return __reduce_add_sync(0xffffffffu, n);
-}
-
-// Position of row `row` and the rows of its request [first, end); false if no
-// request holds the row.
-__device__ __forceinline__ bool locate(const int32_t* cu, const int32_t* positions, int B,
-                                       int n_tokens, int row, int lane, int* request,
-                                       long long* pos, int* first, int* end) {
-  const int b = request_of(cu, B, row, lane);
-  if (b >= B) return false;
-  *request = b;
-  *first = cu ? __ldg(cu + b) : row;
-  *end = cu ? min(__ldg(cu + b + 1), n_tokens) : row + 1;
-  if (row < *first) return false;
-  *pos = (long long)__ldg(positions + b) + (row - *first);
-  return true;
-}
-
-// Physical page of a token, -1 if its position or page is outside the table
-// or the pool.
-__device__ __forceinline__ long long page_of(const int32_t* page_table, int max_pages,
-                                             long long pool_pages, int b, long long pos) {
-  if (pos < 0 || pos / kPage >= max_pages) return -1;
-  const long long page = __ldg(page_table + (size_t)b * max_pages + pos / kPage);
-  return page < pool_pages ? page : -1;
-}
-
-// Turns per position, modulo one, in units of 2^-64: f / (2 pi) from f's 24
-// significant bits and 1 / (2 pi) to 66 bits.
-__device__ __forceinline__ unsigned long long turn_step(float f) {
-  constexpr unsigned long long kInvTwoPi = 0xa2f9836e4e44152aull;  // 2^66 / (2 pi)
-  const unsigned bits = __float_as_uint(f);
-  const int e = (bits >> 23) & 255;
-  const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
-  const unsigned long long lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
-  // f = m 2^(max(e, 1) - 150): the product is 2^(shift - 64) times the result
-  const int shift = 152 - max(e, 1);
-  unsigned long long x;
-  if (shift >= 64) x = shift < 128 ? hi >> (shift - 64) : 0ull;
-  else if (shift > 0) x = (hi << (64 - shift)) | (lo >> shift);
-  else x = shift > -64 ? lo << -shift : 0ull;
-  return (bits >> 31) ? 0ull - x : x;
-}
-
-// 0, or NaN for a frequency that is not finite, whose pairs become NaN.
-__device__ __forceinline__ float not_finite(float f) { return f - f; }
-
-// Sine and cosine at position p: the turn's nearest quarter, and the Taylor
-// polynomials of the rest (|x| <= pi / 4: the first terms left out are below
-// 2e-9 and 3e-10).  Half the instructions of sincospif, which reduces a float.
-__device__ __forceinline__ void turn(long long p, unsigned long long step, float nan, float* s,
-                                     float* c) {
-  const uint32_t at = (uint32_t)((step * (unsigned long long)p) >> 32);
-  const uint32_t quarter = (at + 0x20000000u) >> 30;
-  const float x = (float)(int)(at - (quarter << 30)) * 1.4629180792671596e-09f;   // 2 pi 2^-32
-  const float z = x * x;
-  float a = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
-  a = fmaf(a, z, 1.0f / 120.0f);
-  a = fmaf(a, z, -1.0f / 6.0f);
-  const float sx = fmaf(a * z, x, x);
-  float b = fmaf(z, -1.0f / 3628800.0f, 1.0f / 40320.0f);
-  b = fmaf(b, z, -1.0f / 720.0f);
-  b = fmaf(b, z, 1.0f / 24.0f);
-  b = fmaf(b, z, -0.5f);
-  const float cx = fmaf(b, z, 1.0f);
-  const bool odd = quarter & 1;
-  const float ss = odd ? cx : sx, cc = odd ? sx : cx;
-  *s = (quarter & 2 ? -ss : ss) + nan;
-  *c = ((quarter + 1) & 2 ? -cc : cc) + nan;
-}
-
-template <int V>
-using Vec = typename std::conditional<V == 8, uint4, uint2>::type;
-
-// A lane holds V pairs of one head row as two V-element vectors a and b at
-// element offsets oa and ob of the head: pairs Vl .. Vl + V-1, which lie half a
-// rotation apart (a holds the first, b the second of each pair) or next to
-// each other (interleaved; a holds the first V/2 pairs, b the others).  Lanes
-// behind the rotated part hold the elements that pass.
-struct Lane {
-  int oa, ob, pair;
-  bool turns;
-};
-template <int V>
-__device__ __forceinline__ Lane lane_of(int l, int half, int interleaved) {
-  Lane x;
-  x.pair = V * l;
-  x.turns = x.pair < half;
-  const bool apart = x.turns && !interleaved;
-  x.oa = apart ? x.pair : 2 * x.pair;
-  x.ob = apart ? x.pair + half : 2 * x.pair + V;
-  return x;
-}
-
-// The lane's 2 V values in fp32; the first V are a's.
-template <int V>
-__device__ __forceinline__ void unpack(const Vec<V>& a, const Vec<V>& b, float (&y)[2 * V]) {
-  const uint32_t* wa = reinterpret_cast<const uint32_t*>(&a);
-  const uint32_t* wb = reinterpret_cast<const uint32_t*>(&b);
-#pragma unroll
-  for (int i = 0; i < V / 2; ++i) {
-    y[2 * i] = ptx::bf16_lo_to_f32(wa[i]);
-    y[2 * i + 1] = ptx::bf16_hi_to_f32(wa[i]);
-    y[V + 2 * i] = ptx::bf16_lo_to_f32(wb[i]);
-    y[V + 2 * i + 1] = ptx::bf16_hi_to_f32(wb[i]);
-  }
-}
-
-// They turned by their pairs' c and s.
-template <int V>
-__device__ __forceinline__ void rotate(int interleaved, const float* c, const float* s,
-                                       float (&y)[2 * V]) {
-  if (interleaved) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float u = y[2 * i], w = y[2 * i + 1];
-      y[2 * i] = u * c[i] - w * s[i];
-      y[2 * i + 1] = w * c[i] + u * s[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float u = y[i], w = y[i + V];
-      y[i] = u * c[i] - w * s[i];
-      y[i + V] = w * c[i] + u * s[i];
-    }
-  }
-}
-
-template <int V>
-__device__ __forceinline__ Vec<V> pack(const float* y) {
-  Vec<V> r;
-  uint32_t* w = reinterpret_cast<uint32_t*>(&r);
-#pragma unroll
-  for (int i = 0; i < V / 2; ++i)
-    w[i] = ptx::pack_bf16x2(__float2bfloat16_rn(y[2 * i]), __float2bfloat16_rn(y[2 * i + 1]));
-  return r;
-}
-
-// Rotates the q heads of the token rows of CTA cta into q_out and, with kKv,
-// stores their k (rotated) and v heads in the bf16 pool: `share` (1, 2, 4 or 8)
-// warps to a row.  Warps do not wait for each other; a warp issues its row's
-// first loads before it looks the row up.  (Fewer CTAs whose warps take several
-// rows each, the next one's loads ahead, measured slower: 44.6 against 40.4 us
-// for 11 prompts of up to 2,500 tokens.)
-template <int D, int V, bool kKv>
-__device__ __forceinline__ void rotate_rows(const Tokens& t, __nv_bfloat16* pool, int cta,
-                                            int share) {
-  constexpr int kLanes = D / (2 * V);        // lanes per head row
-  constexpr int kHeads = 32 / kLanes;        // head rows a warp takes at once
-  constexpr int kUnroll = 4;
-  __shared__ __align__(16) float table[kWarps][2][D / 2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_cta = kWarps / share;
-  const Lane ln = lane_of<V>(lane % kLanes, t.half, t.interleaved);
-  const int heads = t.Hq + (kKv ? 2 * t.Hkv : 0);
-  const int step = share * kHeads;
-  const int first_h = (warp % share) * kHeads + lane / kLanes;
-  Vec<V> va[kUnroll], vb[kUnroll];
-  const int row = cta * per_cta + warp / share;
-  if (row >= t.n_tokens) return;
-  auto load = [&](int h0) {
-    const __nv_bfloat16* q = t.q + row * t.q_stride;
-    const __nv_bfloat16* k = t.k + row * t.k_stride;
-    const __nv_bfloat16* v = t.v + row * t.v_stride;
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int h = h0 + i * step, g = h - t.Hq;
-      if (h >= heads) continue;
-      const __nv_bfloat16* src = !kKv || g < 0 ? q + h * D
-                                 : g < t.Hkv   ? k + g * D
-                                               : v + (g - t.Hkv) * D;
-      va[i] = *reinterpret_cast<const Vec<V>*>(src + ln.oa);
-      vb[i] = *reinterpret_cast<const Vec<V>*>(src + ln.ob);
-    }
-  };
-  load(first_h);
-  int b = 0, first, end;
-  long long pos = 0;
-  if (!locate(t.cu, t.positions, t.B, t.n_tokens, row, lane, &b, &pos, &first, &end)) return;
-  for (int i = lane; i < t.half; i += 32) {
-    const float f = __ldg(t.inv_freq + i);
-    turn(pos, turn_step(f), not_finite(f), &table[warp][1][i], &table[warp][0][i]);
-  }
-  __nv_bfloat16* q_out = t.q_out + row * t.q_out_stride;
-  __nv_bfloat16* kv_out = nullptr;
-  if (kKv) {
-    const long long page = page_of(t.page_table, t.max_pages, t.pool_pages, b, pos);
-    if (page >= 0) kv_out = pool + (page * kPage + pos % kPage) * (2ll * t.Hkv * D);
-    else if (lane == 0 && t.status) atomicOr(t.status, PA_STATUS_BAD_ROW);
-  }
-  __syncwarp();
-  float c[V], s[V];
-  if (ln.turns) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      *reinterpret_cast<float4*>(c + i) =
-          *reinterpret_cast<const float4*>(&table[warp][0][ln.pair + i]);
-      *reinterpret_cast<float4*>(s + i) =
-          *reinterpret_cast<const float4*>(&table[warp][1][ln.pair + i]);
-    }
-  }
-  for (int h0 = first_h;;) {
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int h = h0 + i * step, g = h - t.Hq;
-      if (h >= heads || (kKv && g >= 0 && kv_out == nullptr)) continue;
-      if (ln.turns && (!kKv || g < t.Hkv)) {   // v and what passes keep their bits
-        float y[2 * V];
-        unpack<V>(va[i], vb[i], y);
-        rotate<V>(t.interleaved, c, s, y);
-        va[i] = pack<V>(y);
-        vb[i] = pack<V>(y + V);
-      }
-      __nv_bfloat16* dst = !kKv || g < 0 ? q_out + h * D : kv_out + g * D;
-      *reinterpret_cast<Vec<V>*>(dst + ln.oa) = va[i];
-      *reinterpret_cast<Vec<V>*>(dst + ln.ob) = vb[i];
-    }
-    h0 += kUnroll * step;
-    if (h0 >= heads) break;
-    load(h0);
-  }
-}
 
 template <int D, int V>
 __global__ void __launch_bounds__(kThreads, 3)
     append_rope_kernel(const Tokens t, __nv_bfloat16* pool, int share) {
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
-  rotate_rows<D, V, true>(t, pool, blockIdx.x, share);
+  rotate_rows<D, V, true, false>(t, Norm{}, pool, blockIdx.x, share);
+}
+
+template <int D, int V>
+__global__ void __launch_bounds__(kThreads, 2)
+    append_norm_rope_kernel(const Tokens t, const Norm norm, __nv_bfloat16* pool, int share) {
+  ptx::launch_dependents();
+  ptx::grid_dependency_wait();
+  rotate_rows<D, V, true, true>(t, norm, pool, blockIdx.x, share);
 }
 
 // Smallest power of two s >= 2^-60 with amax <= 448 s (448 = 1.75 * 2^8 is the
@@ -423,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   const bool paired = (int)blockIdx.x < 2 * pairs;
   const int cta = paired ? blockIdx.x / 2 : blockIdx.x - pairs;
   if (paired ? blockIdx.x & 1 : pairs == kv_ctas) {
-    rotate_rows<D, V, false>(t, nullptr, cta, share);
+    rotate_rows<D, V, false, false>(t, Norm{}, nullptr, cta, share);
     return;
   }
   __shared__ __align__(16) float cs[kBlock][2][D / 2];
@@ -480,13 +239,6 @@ __global__ void __launch_bounds__(kThreads, 3)
                               in_page / kBlock, h, lane);
     }
   }
-}
-
-// 32 bytes (aligned) in one store.
-__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
 }
 
 // Rows of an 8-bit pool as bf16 values: `share` warps to a row, a lane turns 16
@@ -551,76 +303,6 @@ __global__ void __launch_bounds__(kThreads)
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
-// Warps per row and CTAs of the row-wise kernels: a CTA per row while there are
-// few (its warps share the row's heads), up to a row per warp.
-void row_grid(int n_tokens, int* share, int* ctas) {
-  *share = kWarps;
-  while (*share > 1 && (long long)n_tokens * *share > (long long)kRowCtas * kWarps) *share /= 2;
-  const int per_cta = kWarps / *share;
-  *ctas = (n_tokens + per_cta - 1) / per_cta;
-}
-
-int check_tokens(const Tokens& t, int head_dim, int rot_dim, unsigned flags, const void* pool) {
-  PA_REQUIRE(t.n_tokens >= 0 && t.B >= 0, "n_tokens and B must be >= 0 (got %d, %d)", t.n_tokens,
-             t.B);
-  if (t.n_tokens == 0 || t.B == 0) return PA_OK;
-  PA_REQUIRE(t.n_tokens <= kMaxTokens, "n_tokens (%d) above %d", t.n_tokens, kMaxTokens);
-  PA_REQUIRE(t.Hkv >= 1 && t.Hkv <= 4096, "n_kv_heads (%d) must be in 1..4096", t.Hkv);
-  PA_REQUIRE((t.q == nullptr) == (t.q_out == nullptr), "q and q_out go together");
-  PA_REQUIRE(t.q == nullptr || (t.Hq >= 1 && t.Hq <= 65536), "n_q_heads (%d) must be in 1..65536",
-             t.Hq);
-  PA_REQUIRE(t.k && t.v && t.positions && t.page_table && pool, "null pointer argument");
-  PA_REQUIRE(t.cu || t.n_tokens == t.B, "without cu_tokens there is one token per request");
-  PA_REQUIRE(rot_dim >= 0 && rot_dim <= head_dim && rot_dim % 8 == 0,
-             "rot_dim (%d) must be a multiple of 8 in [0, %d]", rot_dim, head_dim);
-  PA_REQUIRE(rot_dim == 0 || t.inv_freq, "inv_freq is required");
-  PA_REQUIRE((flags & ~PA_ROPE_INTERLEAVED) == 0, "unknown flags %#x", flags);
-  PA_REQUIRE(aligned16(t.q) && aligned16(t.q_out) && aligned16(t.k) && aligned16(t.v) &&
-                 aligned16(pool),
-             "q, q_out, k, v and pool must be 16-byte aligned");
-  const long long kv = (long long)t.Hkv * head_dim, qd = (long long)t.Hq * head_dim;
-  PA_REQUIRE(t.k_stride % 8 == 0 && t.v_stride % 8 == 0 && t.q_stride % 8 == 0 &&
-                 t.q_out_stride % 8 == 0,
-             "token strides must be multiples of 8 elements");
-  PA_REQUIRE((t.n_tokens == 1 || (t.k_stride >= kv && t.v_stride >= kv)) &&
-                 (t.q == nullptr || t.n_tokens == 1 ||
-                  (t.q_stride >= qd && t.q_out_stride >= qd)),
-             "token strides are smaller than a token's heads");
-  PA_REQUIRE(t.pool_pages >= 1 && t.max_pages >= 1, "pool_pages and max_pages must be >= 1");
-  return PA_OK;
-}
-
-Tokens tokens_of(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
-                 int64_t v_stride, void* q_out, int64_t q_out_stride, const int32_t* cu_tokens,
-                 const int32_t* positions, int n_tokens, int B, int n_q_heads, int n_kv_heads,
-                 const float* inv_freq, int rot_dim, unsigned flags, int64_t pool_pages,
-                 const int32_t* page_table, int max_pages, int32_t* status) {
-  Tokens t{};
-  t.q = static_cast<const __nv_bfloat16*>(q);
-  t.k = static_cast<const __nv_bfloat16*>(k);
-  t.v = static_cast<const __nv_bfloat16*>(v);
-  t.q_out = static_cast<__nv_bfloat16*>(q_out);
-  t.q_stride = q_stride;
-  t.k_stride = k_stride;
-  t.v_stride = v_stride;
-  t.q_out_stride = q_out_stride;
-  t.cu = cu_tokens;
-  t.positions = positions;
-  t.inv_freq = inv_freq;
-  t.page_table = page_table;
-  t.status = status;
-  t.pool_pages = pool_pages;
-  t.n_tokens = n_tokens;
-  t.B = B;
-  t.Hq = q ? n_q_heads : 0;
-  t.Hkv = n_kv_heads;
-  t.half = rot_dim / 2;
-  t.interleaved = (flags & PA_ROPE_INTERLEAVED) ? 1 : 0;
-  t.max_pages = max_pages;
-  return t;
-}
 
 template <int D, int V>
 cudaError_t launch_append(const Tokens& t, void* pool, cudaStream_t stream) {
@@ -628,6 +310,15 @@ cudaError_t launch_append(const Tokens& t, void* pool, cudaStream_t stream) {
   row_grid(t.n_tokens, &share, &ctas);
   return launch_dependent(append_rope_kernel<D, V>, dim3(ctas), dim3(kThreads), 0, stream, t,
                           static_cast<__nv_bfloat16*>(pool), share);
+}
+
+template <int D, int V>
+cudaError_t launch_append_norm(const Tokens& t, const Norm& norm, void* pool,
+                               cudaStream_t stream) {
+  int share, ctas;
+  row_grid(t.n_tokens, &share, &ctas);
+  return launch_dependent(append_norm_rope_kernel<D, V>, dim3(ctas), dim3(kThreads), 0, stream, t,
+                          norm, static_cast<__nv_bfloat16*>(pool), share);
 }
 
 // Token rows a CTA looks through for blocks to store: a power of two that leaves
@@ -652,9 +343,6 @@ cudaError_t launch_append_q8(const Tokens& t, void* pool, float* scales, cudaStr
   return launch_dependent(append_rope_q8_kernel<D, V>, dim3(kv + q), dim3(kThreads), 0, stream, t,
                           static_cast<uint8_t*>(pool), scales, kv, chunk, share);
 }
-
-// Pairs per lane: 8 (16-byte accesses) unless the rotated half is no multiple.
-bool wide(const Tokens& t) { return t.half % 8 == 0; }
 
 }  // namespace rope
 }  // namespace pa
@@ -684,6 +372,39 @@ extern "C" int kv_append_rope(const void* q, const void* k, const void* v, int64
                                        : launch_append<128, 4>(t, pool, stream))
                                   : (w ? launch_append<256, 8>(t, pool, stream)
                                        : launch_append<256, 4>(t, pool, stream)));
+  PA_CHECK_CUDA(cudaGetLastError());
+  return PA_OK;
+}
+
+extern "C" int kv_append_norm_rope(const void* q, const void* k, const void* v, int64_t q_stride,
+                                   int64_t k_stride, int64_t v_stride, void* q_out,
+                                   int64_t q_out_stride, const int32_t* cu_tokens,
+                                   const int32_t* positions, int n_tokens, int B, int n_q_heads,
+                                   int n_kv_heads, int head_dim, const float* q_weight,
+                                   const float* k_weight, float eps, const float* inv_freq,
+                                   int rot_dim, unsigned flags, void* pool, int64_t pool_pages,
+                                   const int32_t* page_table, int max_pages, int32_t* status,
+                                   cudaStream_t stream) {
+  using namespace pa::rope;
+  pa::clear_error();
+  const Tokens t = tokens_of(q, k, v, q_stride, k_stride, v_stride, q_out, q_out_stride, cu_tokens,
+                             positions, n_tokens, B, n_q_heads, n_kv_heads, inv_freq, rot_dim,
+                             flags, pool_pages, page_table, max_pages, status);
+  const Norm norm{q_weight, k_weight, eps};
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return pa::fail(PA_ERR_UNSUPPORTED, "head_dim %d not built (supported: 64, 128, 256)",
+                    head_dim);
+  int rc = check_tokens(t, head_dim, rot_dim, flags, pool);
+  if (rc != PA_OK || n_tokens == 0 || B == 0) return rc;
+  rc = check_norm(t, norm);
+  if (rc != PA_OK) return rc;
+  const bool w = wide(t);
+  PA_CHECK_CUDA(head_dim == 64 ? (w ? launch_append_norm<64, 8>(t, norm, pool, stream)
+                                    : launch_append_norm<64, 4>(t, norm, pool, stream))
+                : head_dim == 128 ? (w ? launch_append_norm<128, 8>(t, norm, pool, stream)
+                                       : launch_append_norm<128, 4>(t, norm, pool, stream))
+                                  : (w ? launch_append_norm<256, 8>(t, norm, pool, stream)
+                                       : launch_append_norm<256, 4>(t, norm, pool, stream)));
   PA_CHECK_CUDA(cudaGetLastError());
   return PA_OK;
 }

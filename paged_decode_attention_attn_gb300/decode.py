@@ -161,17 +161,12 @@ class ResidentDecode:
         return int(self.workspace[:4].view(torch.int32).item()) | int(self.status.item())
 
 
-class ResidentQ8Decode:
-    """Decode step over a device-resident 8-bit pool [layers][pages][64][row]
-    (e4m3 codes, one fp32 scale per 16 tokens and head): half the bytes of
-    ResidentDecode's.
+class _ResidentCoded:
+    """Decode step over a device-resident pool of codes and scales, one of each per
+    layer.  What a subclass gives: ``_pools`` (codes and scales of all layers),
+    ``_append`` (the call that stores rows) and the decode's entry points."""
 
-    The pool is filled from ``t["pool"]``'s history (every row but each
-    request's newest, as they stand: keys of a cache are rotated already).  Per
-    layer, one launch turns the step's q and k by their positions and stores k
-    and v in the pages; one attends every tile and merges them.  ``inv_freq``
-    fp32 [rot_dim / 2], None: no rotation; ``interleaved``: pairs (2i, 2i + 1).
-    """
+    _attend = _alloc_workspace = None
 
     def __init__(self, w: DecodeWorkload, t: dict, inv_freq=None, interleaved: bool = False,
                  stream=None):
@@ -181,19 +176,15 @@ class ResidentQ8Decode:
         self.tiles = np.ascontiguousarray(w.tiles, dtype=np.int32)
         self.n_layers = t["pool"].shape[0]
         dev = t["pool"].device
-        shape = tuple(t["pool"].shape)
-        self.pool = torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
-        self.scales = torch.zeros(
-            (self.n_layers, shape[1], 2 * geo.n_kv_heads, geo.page_tokens // B.SCALE_TOKENS),
-            dtype=torch.float32, device=dev)
+        self.pool, self.scales = self._pools(t["pool"].shape[1], dev)
         self.o = _Outputs(w, self.n_layers, dev)
         self.merged = torch.empty((self.n_layers, w.batch, geo.n_q_heads, geo.head_dim),
                                   dtype=torch.float32, device=dev)
         self.merged_lse = torch.empty((self.n_layers, w.batch, geo.n_q_heads),
                                       dtype=torch.float32, device=dev)
         self.q = torch.empty_like(t["q"])
-        self.workspace = B.alloc_workspace_q8(w.batch, self.tiles.shape[1], geo.n_q_heads,
-                                              geo.n_kv_heads, geo.head_dim, device=dev)
+        self.workspace = self._alloc_workspace(w.batch, self.tiles.shape[1], geo.n_q_heads,
+                                               geo.n_kv_heads, geo.head_dim, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self._fill()
         if stream is not None:
@@ -214,20 +205,19 @@ class ResidentQ8Decode:
                     continue
                 k, v = self._kv(history_rows(self.w, self.t["pool"][i], r)[:n])
                 cu = torch.tensor([0, n], dtype=torch.int32, device=self.pool.device)
-                B.kv_append_rope_q8(None, k, v, self.pool[i], self.scales[i],
-                                    self.t["page_table"][r:r + 1], zero, None, cu_tokens=cu,
-                                    status=self.status)
+                self._append(i, None, k, v, self.t["page_table"][r:r + 1], zero, None,
+                             cu_tokens=cu, status=self.status)
 
     def layer(self, i: int):
         t, o = self.t, self.o
         k, v = self._kv(t["new_rows"][i])
-        B.kv_append_rope_q8(t["q"][i], k, v, self.pool[i], self.scales[i], t["page_table"],
-                            t["positions"], self.inv_freq, self.q[i],
-                            interleaved=self.interleaved, status=self.status, stream=self.stream)
-        B.paged_decode_attn_q8_lse(self.q[i], self.pool[i], self.scales[i], t["page_table"],
-                                   self.tiles, self.w.geometry.scale, o.tile_out[i],
-                                   o.tile_lse[i], self.workspace, merged_out=self.merged[i],
-                                   merged_lse=self.merged_lse[i], stream=self.stream)
+        self._append(i, t["q"][i], k, v, t["page_table"], t["positions"], self.inv_freq,
+                     q_out=self.q[i], interleaved=self.interleaved, status=self.status,
+                     stream=self.stream)
+        self._attend(self.q[i], self.pool[i], self.scales[i], t["page_table"],
+                     self.tiles, self.w.geometry.scale, o.tile_out[i],
+                     o.tile_lse[i], self.workspace, merged_out=self.merged[i],
+                     merged_lse=self.merged_lse[i], stream=self.stream)
 
     def step(self):
         for i in range(self.n_layers):
@@ -235,6 +225,65 @@ class ResidentQ8Decode:
 
     def kernel_status(self) -> int:
         return int(self.workspace[:4].view(torch.int32).item()) | int(self.status.item())
+
+
+class ResidentQ8Decode(_ResidentCoded):
+    """Decode step over a device-resident 8-bit pool [layers][pages][64][row]
+    (e4m3 codes, one fp32 scale per 16 tokens and head): half the bytes of
+    ResidentDecode's.
+
+    The pool is filled from ``t["pool"]``'s history (every row but each
+    request's newest, as they stand: keys of a cache are rotated already).  Per
+    layer, one launch turns the step's q and k by their positions and stores k
+    and v in the pages; one attends every tile and merges them.  ``inv_freq``
+    fp32 [rot_dim / 2], None: no rotation; ``interleaved``: pairs (2i, 2i + 1).
+    """
+
+    _attend = staticmethod(B.paged_decode_attn_q8_lse)
+    _alloc_workspace = staticmethod(B.alloc_workspace_q8)
+
+    def _pools(self, n_pages, dev):
+        geo = self.w.geometry
+        pool = torch.zeros(self.t["pool"].shape, dtype=torch.uint8, device=dev)
+        scales = torch.zeros(
+            (self.n_layers, n_pages, 2 * geo.n_kv_heads, geo.page_tokens // B.SCALE_TOKENS),
+            dtype=torch.float32, device=dev)
+        return pool.view(torch.float8_e4m3fn), scales
+
+    def _append(self, i, q, k, v, table, positions, inv_freq, **kw):
+        B.kv_append_rope_q8(q, k, v, self.pool[i], self.scales[i], table, positions, inv_freq, **kw)
+
+
+class ResidentQ4Decode(_ResidentCoded):
+    """Decode step over a device-resident 4-bit pool [layers][pages][2*Hkv][64][D/2]
+    (two e2m1 codes a byte, one scale per 32 values of a token's head): 17/64 of
+    ResidentDecode's bytes.
+
+    Filled and stepped as ResidentQ8Decode; ``q_weight`` and ``k_weight`` (fp32
+    [layers][D], both or neither) are norms of the step's q and k heads ahead of the
+    rotation, with ``eps``.
+    """
+
+    _attend = staticmethod(B.paged_decode_attn_q4_lse)
+    _alloc_workspace = staticmethod(B.alloc_workspace_q4)
+
+    def __init__(self, w: DecodeWorkload, t: dict, inv_freq=None, interleaved: bool = False,
+                 q_weight=None, k_weight=None, eps: float = 1e-6, stream=None):
+        if (q_weight is None) != (k_weight is None):
+            raise ValueError("q_weight and k_weight go together")
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
+        super().__init__(w, t, inv_freq, interleaved, stream)
+
+    def _pools(self, n_pages, dev):
+        geo = self.w.geometry
+        shape = (self.n_layers, n_pages, 2 * geo.n_kv_heads, geo.page_tokens)
+        return [torch.zeros(shape + (n,), dtype=torch.uint8, device=dev)
+                for n in (geo.head_dim // 2, geo.head_dim // B.Q4_GROUP)]
+
+    def _append(self, i, q, k, v, table, positions, inv_freq, **kw):
+        if q is not None and self.q_weight is not None:   # a step's rows (the history's are as they are)
+            kw.update(q_weight=self.q_weight[i], k_weight=self.k_weight[i], eps=self.eps)
+        B.kv_append_rope_q4(q, k, v, self.pool[i], self.scales[i], table, positions, inv_freq, **kw)
 
 
 class HostHistory:
