@@ -68,6 +68,8 @@
 #include "split_units.cuh"
 #include "tc.cuh"
 #include "tile_merge.cuh"
+#include "unit_plan.h"
+#include "unit_walk.cuh"
 
 namespace pa {
 namespace decode_q8 {
@@ -101,18 +103,6 @@ constexpr int kOut = kOutWarps * 32;
 constexpr int kSoftmaxWarps = kGroups * kGroupWarps;
 constexpr int kTmaWarp = 12, kScoreWarp = 13, kProductWarp = 14;
 constexpr int kThreads = 32 * 16;           // the last warp: per segment
-constexpr int kSegmentCharge = 6;           // pages charged per unit start
-constexpr int kWholePages = 16;             // units this short are not split while SMs are idle
-constexpr int kMinPages = 4;                // pages per CTA at least, where units are split
-// A launch of this many pages per SM runs on kLongGridPct percent of the SMs:
-// with HBM saturated, fewer and longer streams finish sooner (as the bf16
-// kernel's do; 100 / 90 / 85 / 80 percent on one box: 1 x 262,144 tokens 85.3 /
-// 84.4 / 83.7 / 83.2 us, 8 ragged of up to 131,072 247.5 / 245.5 / 244.5 / 242.1).
-constexpr int kLongPages = 64, kLongGridPct = 85;
-constexpr int kTwoPartsBytes = 400 << 10;   // worth what a CTA loses with parts of two units
-constexpr int kWholeBytes = 1600 << 10;     // beyond an equal share, for units kept whole
-constexpr int kUnitCharge = 3;              // pages that a whole unit costs beside its own
-constexpr int kSnapPages = 4;               // how far a CTA's end moves to a unit's border
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kMinScaleExp = -100, kMaxScaleExp = 120;   // log2 of V scales
 // e_j may lie above 1, up to 2^kSlack: a sum of 2^30 of them is still finite.
@@ -195,13 +185,6 @@ struct Smem {
   static_assert(kAlloc <= 232448, "shared memory budget");
 };
 
-// A unit as the kernel reads it: three 8-byte loads.
-struct alignas(8) DevUnit {
-  int32_t page_first, bt, tok_start, tok_end, g;
-  uint16_t part_base;
-  uint8_t n_parts, first_cta;
-};
-
 template <int kMaxUnits>
 struct Params {
   const __nv_bfloat16* q;
@@ -228,6 +211,7 @@ struct Params {
   unsigned long long slice_wait_ns;
   // One tile per request: its output may be the merged one too, written with it.
   static constexpr bool kAllSlices = true, kMerge = false, kSecondOut = true;
+  static constexpr bool kInlineWaits = false;
   float* out2;
   float* lse2;
   int32_t starts[kMaxGrid + 1];      // CTA k takes flattened pages [k], [k + 1)
@@ -246,145 +230,6 @@ struct View {
   volatile int* merge_info;
   __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
 };
-
-// A position in a ring of kN buffers and the parity of its barriers' phase: a
-// reader waits for `full` with it, a writer for `empty` with the other parity
-// (which a fresh barrier passes).
-template <int kN>
-struct Ring {
-  int i = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++i == kN) {
-      i = 0;
-      phase ^= 1;
-    }
-  }
-};
-
-// The slow side of a wait, out of line: the roles' loops stay short (a warp on
-// its own runs ~6 cycles per instruction, and every line of code is fetched
-// cold in a launch).
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                       int32_t* status, volatile int* abort_flag) {
-  const uint64_t t0 = ptx::globaltimer_ns();
-  while (true) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (ptx::globaltimer_ns() - t0 > limit_ns) {
-      atomicOr(status, PA_STATUS_TIMEOUT);
-      *abort_flag = 1;
-      return false;
-    }
-  }
-}
-
-// Waits for the phase of the given parity to be complete.  False once the time
-// limit, or another warp's, has run out.
-template <class P>
-__device__ __forceinline__ bool wait(const P& p, const View& v, int bar, uint32_t parity) {
-  const uint32_t b = v.bar(bar);
-  return ptx::mbar_try_wait(b, parity) ||
-         wait_long(b, parity, p.wait_limit_ns, p.status, v.abort_flag);
-}
-// The same for a converged warp, with one answer for all its lanes: false too if
-// `ok` is false in one of them.  A warp skips tensor memory loads, and leaves its
-// loop, by such an answer alone: lanes that gave up by themselves would be missed at
-// the next instruction that takes the whole warp, by a wait without a limit.
-template <class P>
-__device__ __forceinline__ bool warp_wait(const P& p, const View& v, int bar, uint32_t parity,
-                                          bool ok = true) {
-  return __all_sync(0xffffffffu, ok && wait(p, v, bar, parity));
-}
-
-// A CTA's part of a unit: its pages [lo, hi).
-struct Segment {
-  DevUnit U;
-  int u, pf, lo, hi, bt, g, first_tok;
-  __device__ __forceinline__ int steps() const { return (hi - lo + 1) / 2; }
-  __device__ __forceinline__ bool whole() const { return U.n_parts == 1; }
-  // the segment's partial slot, where the unit has several
-  __device__ __forceinline__ size_t slot() const {
-    return U.part_base + (int)blockIdx.x - U.first_cta;
-  }
-};
-
-// This CTA's segments, one after the other.
-template <class P>
-__device__ __forceinline__ int request_of(const P& p, int bt) {
-  return p.T == 1 ? bt : bt / p.T;
-}
-
-template <class P>
-struct Segments {
-  const P& p;
-  int start, end, u;
-  __device__ __forceinline__ explicit Segments(const P& params)
-      : p(params), start(params.starts[blockIdx.x]), end(params.starts[blockIdx.x + 1]),
-        u(params.first_unit[blockIdx.x]) {}
-  __device__ __forceinline__ bool next(Segment& s) {
-    for (; u < p.n_full && p.units[u].page_first < end; ++u) {
-      const DevUnit& from = p.units[u];
-      s.U = from;
-      const int np = unit_pages(s.U.tok_start, s.U.tok_end);
-      s.pf = s.U.page_first;
-      s.lo = max(start, s.pf) - s.pf;
-      s.hi = min(end, s.pf + np) - s.pf;
-      if (s.hi <= s.lo) continue;   // only its segment charge falls in this range
-      s.u = u++;
-      s.bt = s.U.bt;
-      s.g = s.U.g;
-      s.first_tok = s.U.tok_start / kPage * kPage;
-      return true;
-    }
-    return false;
-  }
-};
-
-// Calls f(segment, index) for every segment of this CTA until f returns false.
-template <class P, class F>
-__device__ __forceinline__ void for_segments(const P& p, F f) {
-  Segments<P> segments(p);
-  Segment s;
-  for (int index = 0; segments.next(s); ++index)
-    if (!f(s, index)) return;
-}
-
-__device__ __forceinline__ bool any_in_group(int id, int threads, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(x ? 1u : 0u), "r"(id), "r"(threads)
-      : "memory");
-  return r != 0;
-}
-
-// One lane of a converged warp.  What a whole warp computes alike stays in
-// uniform registers, which TMA and tcgen05 instructions take their operands
-// from; a branch on the lane index would cost a move for each.
-__device__ __forceinline__ bool elect() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-
-// 16 bytes (copy_own: a value of 8 or 16) from global to shared memory, and an
-// arrival at `bar` once the thread's copies have landed.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-template <class T>
-__device__ __forceinline__ void copy_own(uint32_t dst, const T* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(sizeof(T))
-               : "memory");
-}
-__device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 
 // ---------------------------------------------------------------------------
 // Warp 12: the pages' K (with the scales) and V into their rings, V kLag steps
@@ -1317,192 +1162,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-// For units of one length, a grid (at least 80% of `grid`) that divides them, or
-// that they divide: no CTA has parts of two units.  0 if there is none.
-int even_grid(int count, int grid) {
-  for (int g = grid; g * 5 >= grid * 4; --g)
-    if (count % g == 0 || g % count == 0) return g;
-  return 0;
-}
-
-// Pages that each CTA has at most if no CTA takes parts of two units (the fewest
-// for which the units' CTAs fit the grid), or 0 where that is more than
-// kTwoPartsBytes above an equal share.  A CTA with a part of a split unit before
-// another segment is ~5 us behind the others: a table row, q, an arrival and its
-// fence lie between the two.  (Against equal shares: 7 ragged requests in 5 tiles
-// 24.9 -> 23.6 us, 20,000 tokens in 3 tiles 15.7 -> 14.5, 9,000 and 800 tokens 12.3
-// -> 10.5, 3 x 54,748 in 4 tiles unchanged; 200 KB or 300 KB did as well but for 12
-// x 9,000 in 3 tiles, 26.0 -> 25.4.)
-int pages_alone(const int32_t* pages, size_t n, long long sum, int count, int grid, int d) {
-  if (count > grid) return 0;
-  auto fits = [&](long long most) {
-    long long ctas = 0;
-    for (size_t i = 0; i < n; ++i) ctas += (pages[i] + most - 1) / most;
-    return ctas <= grid;
-  };
-  long long lo = (sum + grid - 1) / grid, hi = sum / grid + kTwoPartsBytes / (2 * kPage * d);
-  if (!fits(hi)) return 0;
-  while (lo < hi) {
-    const long long mid = (lo + hi) / 2;
-    if (fits(mid)) hi = mid;
-    else lo = mid + 1;
-  }
-  return (int)lo;
-}
-
-// Cuts a launch's units into CTAs.  A unit on one CTA costs a step per two
-// pages (0.5-0.65 us); a unit on several costs partials and their merge, about
-// 2 us more.
-void cut_pages(const Unit* units, const int32_t* pages, size_t n, long long total, int sms,
-               int heads, int d, std::vector<int32_t>* starts) {
-  int count = 0, most = 0, least = 1 << 30;   // units with pages
-  long long sum = 0;
-  for (size_t i = 0; i < n; ++i) {
-    if (pages[i] == 0) continue;
-    ++count;
-    sum += pages[i];
-    most = std::max(most, pages[i]);
-    least = std::min(least, pages[i]);
-  }
-  starts->reserve(sms + 1);
-  if (count == 0) {
-    starts->assign({0, 1});
-    return;
-  }
-  if (count <= sms && most <= kWholePages) {
-    for (size_t i = 0; i < n; ++i)
-      if (pages[i] != 0) starts->push_back(starts->empty() ? 0 : units[i].page_first);
-    starts->push_back(static_cast<int32_t>(total));
-    return;
-  }
-  int grid = sum >= (long long)kLongPages * sms ? sms * kLongGridPct / 100
-                                                : (int)std::min<long long>(sms, sum / kMinPages);
-  grid = std::max(grid, 1);
-  // As the bf16 kernel's: the CTAs at the same offset of each kv head's block
-  // of units stream the same pages at the same time.
-  if (grid >= heads) grid -= grid % heads;
-  const int alone = most == least ? 0 : pages_alone(pages, n, sum, count, grid, d);
-  if (alone > 0) {
-    for (size_t i = 0; i < n; ++i) {
-      const int parts = (pages[i] + alone - 1) / alone;
-      for (int k = 0; k < parts; ++k)
-        starts->push_back(starts->empty() ? 0 : units[i].page_first +
-                                                    (int)((long long)pages[i] * k / parts));
-    }
-    starts->push_back(static_cast<int32_t>(total));
-    return;
-  }
-  if (const int even = most == least ? even_grid(count, grid) : 0) grid = even;
-  starts->push_back(0);
-  int at = 0;
-  size_t i = 0;
-  for (int k = 1; k < grid; ++k) {
-    int to = at + ((int)total - at) / (grid - k + 1);
-    // the unit that holds the border, if one does
-    while (i < n && (pages[i] == 0 || units[i].page_first + pages[i] <= to)) ++i;
-    if (i < n && to > units[i].page_first) {
-      const int lo = units[i].page_first, hi = lo + pages[i];
-      if (to - lo <= kSnapPages && to - lo <= hi - to && lo > at) to = lo;
-      else if (hi - to <= kSnapPages) to = hi;
-    }
-    if (to <= at) continue;
-    starts->push_back(to);
-    at = to;
-  }
-  if (total > at) starts->push_back(static_cast<int32_t>(total));
-}
-
-// Adds CTAs that have no pages where units without pages (padded requests, tiles
-// behind a request's end) outnumber the CTAs: those are dealt out to all CTAs, a
-// warp each (4 requests of 700 tokens and 252 without any: 8.1 us, 24.8 without
-// these CTAs; 1 and 63: 7.6, 21.2).
-void deal_empty(size_t empty, int sms, std::vector<int32_t>* starts) {
-  const size_t ctas = std::min<size_t>(sms, empty);
-  if (starts->size() < ctas + 1) starts->resize(ctas + 1, starts->back());
-}
-
-void cut(const Unit* units, const int32_t* pages, size_t n, long long total, int sms, int heads,
-         int d, std::vector<int32_t>* starts) {
-  cut_pages(units, pages, n, total, sms, heads, d, starts);
-  deal_empty(std::count(pages, pages + n, 0), sms, starts);
-}
-
-// Lays a launch's units out anew so that every CTA has whole ones, the longest
-// first dealt to the CTA with the least, where that comes within kWholeBytes
-// of equal shares: no unit is split, and nothing merged.  A CTA takes its
-// shortest first, so that launches end in long streams.  (Shortest / longest
-// first, and equal shares: 64 requests of up to 2,500 tokens 32.9 / 33.6 / 35.6
-// us, at 256 dims 29.8 / 29.7 / 33.5, 256 of up to 600 33.9 / 37.6 / 37.1, 120 of
-// up to 2,000 with 2 kv heads 14.5 / 14.9 / 19.3.  Giving each kv head CTAs of its
-// own, which then read the same pages at the same time, made no difference; with
-// 400 KB for kWholeBytes 42 of up to 4,000 took 34.4 us instead of 32.0, with 3.2
-// MB nothing changed.)
-// Linear in the units: a sort by counting, and CTAs kept in lists by their load
-// (the least load only grows).  Returns the order of the units that have pages, or
-// nothing if they stay as they are.
-std::vector<int> pack(Plan* plan, Launch* L, int sms, int d) {
-  const int32_t* pages = plan->pages.data() + L->u0;
-  Unit* units = plan->units.data() + L->u0;
-  const int n = (int)L->n;
-  long long sum = 0;
-  int count = 0, most = 0, least = 1 << 30;   // units with pages
-  for (int i = 0; i < n; ++i) {
-    if (pages[i] == 0) continue;
-    ++count;
-    sum += pages[i];
-    most = std::max(most, pages[i]);
-    least = std::min(least, pages[i]);
-  }
-  const int grid = sum >= (long long)kLongPages * sms ? sms * kLongGridPct / 100 : sms;
-  if (count <= grid) return {};
-  // (Units of one length stay in an even grid: 64 x 2,048 tokens 42.9 us, 43.9 dealt
-  // out; 180 x 1,000 60.5 and 62.4.  Without one, 50 x 1,000 23.4 and 22.5.)
-  if (most == least && even_grid(count, grid)) return {};
-  // Loads are pages and a few more per unit.
-  const long long limit =
-      (sum + (long long)kUnitCharge * count) / grid + kWholeBytes / (2 * kPage * d);
-  if (most + kUnitCharge > limit || limit > 1 << 20) return {};
-  // Units by their pages, and CTAs by their loads: heads of lists.
-  std::vector<int> of_pages(most + 1, -1), of_load(limit + 1, -1), next_unit(n), next_cta(grid),
-      first(grid, -1);
-  for (int i = n - 1; i >= 0; --i) {
-    next_unit[i] = of_pages[pages[i]];
-    of_pages[pages[i]] = i;
-  }
-  for (int k = 0; k < grid; ++k) next_cta[k] = k + 1 < grid ? k + 1 : -1;
-  of_load[0] = 0;
-  int load = 0;
-  for (int p = most; p > 0; --p) {
-    for (int i = of_pages[p]; i >= 0;) {
-      while (of_load[load] < 0) ++load;
-      const int k = of_load[load], to = load + p + kUnitCharge, next = next_unit[i];
-      if (to > limit) return {};
-      of_load[load] = next_cta[k];
-      next_cta[k] = of_load[to];
-      of_load[to] = k;
-      next_unit[i] = first[k];   // the CTA's last comes first
-      first[k] = i;
-      i = next;
-    }
-  }
-  std::vector<int> order;
-  order.reserve(count);
-  L->starts.clear();
-  int32_t at = 0;
-  for (int k = 0; k < grid; ++k) {
-    L->starts.push_back(at);
-    for (int i = first[k]; i >= 0; i = next_unit[i]) {
-      order.push_back(i);
-      units[i].page_first = at;
-      units[i].n_parts = 1;
-      units[i].first_cta = static_cast<uint8_t>(k);
-      at += pages[i];
-    }
-  }
-  L->starts.push_back(at);
-  deal_empty(n - count, sms, &L->starts);
-  L->grid = (int)L->starts.size() - 1;
-  return order;
+// A launch of 64 pages per SM runs on 85% of the SMs: with HBM saturated, fewer and
+// longer streams finish sooner (as the bf16 kernel's do; 100 / 90 / 85 / 80 percent on
+// one box: 1 x 262,144 tokens 85.3 / 84.4 / 83.7 / 83.2 us, 8 ragged of up to 131,072
+// 247.5 / 245.5 / 244.5 / 242.1).
+Rules rules_of(int D) {
+  const int page_bytes = 2 * kPage * D;
+  return {6, 16, 4, 64, 85, (400 << 10) / page_bytes, (1600 << 10) / page_bytes, 3, 4};
 }
 
 using Common = Params<kMaxUnitsSmall>;
@@ -1514,27 +1180,7 @@ int launch_units(const CUtensorMap& tmap, const Plan& plan, const Launch& L,
   static_assert(N >= kMaxUnitsSmall && offsetof(Prm, starts) == offsetof(Common, starts), "");
   Prm prm;
   std::memcpy(static_cast<void*>(&prm), &common, offsetof(Common, starts));
-  prm.n_units = static_cast<int>(L.n);
-  prm.grid = L.grid;
-  // Units without pages go last: every role walks its CTA's units, and skipping
-  // one costs it ~0.2 us (4 requests of 700 tokens and 252 without any: 64.5 us
-  // with the others among them).
-  DevUnit* to = prm.units;
-  auto add = [&](const Unit& u) {
-    *to++ = {u.page_first, u.bt, u.tok_start, u.tok_end, u.g, u.part_base, u.n_parts, u.first_cta};
-  };
-  for (int i : order) add(plan.units[L.u0 + i]);
-  for (size_t i = L.u0; order.empty() && i < L.u0 + L.n; ++i)
-    if (plan.pages[i] != 0) add(plan.units[i]);
-  prm.n_full = static_cast<int>(to - prm.units);
-  for (size_t i = L.u0; i < L.u0 + L.n && to < prm.units + L.n; ++i)
-    if (plan.pages[i] == 0) add(plan.units[i]);
-  std::memcpy(prm.starts, L.starts.data(), L.starts.size() * sizeof(int32_t));
-  for (int k = 0, u = 0; k < L.grid; ++k) {
-    // the last unit that starts at or before the CTA's first page
-    while (u + 1 < prm.n_full && prm.units[u + 1].page_first <= L.starts[k]) ++u;
-    prm.first_unit[k] = static_cast<int16_t>(u);
-  }
+  fill_units(plan, L, order, &prm);
   static PerContext smem_limit;   // the attribute lives in the context
   cudaError_t e = smem_limit.apply([] {
     return cudaFuncSetAttribute(decode_q8_kernel<D, N>,
@@ -1565,36 +1211,10 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
         void* workspace, size_t ws_bytes, cudaStream_t stream) {
   PA_REQUIRE(B >= 0 && T >= 0, "B and T must be >= 0 (got %d, %d)", B, T);
   if ((long long)B * T == 0) return PA_OK;
-  if (D != 128 && D != 256)
-    return fail(PA_ERR_UNSUPPORTED, "head_dim %d not built (supported: 128, 256)", D);
-  PA_REQUIRE(Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0,
-             "n_q_heads (%d) must be a positive multiple of n_kv_heads (%d)", Hq, Hkv);
-  if (Hq / Hkv > kMaxG)
-    return fail(PA_ERR_UNSUPPORTED, "group size %d above the supported %d", Hq / Hkv, kMaxG);
-  PA_REQUIRE(q && pool && scales && page_table && tiles && out && lse && workspace,
-             "null pointer argument");
-  PA_REQUIRE(max_pages >= 1 && pool_pages >= 1, "max_pages and pool_pages must be >= 1");
-  auto aligned = [](const void* ptr, int n) { return reinterpret_cast<uintptr_t>(ptr) % n == 0; };
-  PA_REQUIRE(aligned(q, 16), "q must be 16-byte aligned");
-  PA_REQUIRE(aligned(pool, 16), "pool must be 16-byte aligned");
-  PA_REQUIRE(aligned(scales, 16), "scales must be 16-byte aligned");
-  PA_REQUIRE(aligned(out, 16), "out must be 16-byte aligned");
-  PA_REQUIRE(aligned(workspace, 256), "workspace must be 256-byte aligned");
-  PA_REQUIRE((merged_out == nullptr) == (merged_lse == nullptr),
-             "merged_out and merged_lse go together");
-  PA_REQUIRE(aligned(merged_out, 16), "merged_out must be 16-byte aligned");
-  PA_REQUIRE(pool_pages < (1ll << 31) / kPage, "pool too large for 32-bit row coordinates");
-  PA_REQUIRE((long long)B * T * Hq < (1ll << 31), "output too large");
-  const size_t need = workspace_bytes(B, T, Hkv, D);
-  PA_REQUIRE(ws_bytes >= need, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes,
-             need);
-  const long long max_tok = (long long)max_pages * kPage;
-  for (long long i = 0; i < (long long)B * T; ++i) {
-    const int s = tiles[2 * i], e = tiles[2 * i + 1];
-    PA_REQUIRE(s >= 0 && s <= e && e <= max_tok,
-               "tile %lld of request %lld is [%d, %d), outside [0, %lld]", i % T, i / T, s, e,
-               max_tok);
-  }
+  int rc = check_decode(q, pool, scales, pool_pages, (1ll << 31) / kPage, page_table, max_pages,
+                        tiles, B, T, Hq, Hkv, D, out, lse, merged_out, merged_lse, workspace,
+                        ws_bytes);
+  if (rc != PA_OK) return rc;
   EncodeTiledFn enc = encode_tiled();
   if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable from the driver");
   CUtensorMap tmap;
@@ -1614,10 +1234,11 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   if (sms <= 0) return fail(PA_ERR_CUDA, "cannot query the device's SM count");
   sms = std::min(sms, kMaxGrid);
   Plan plan;
-  int rc = plan_units(
-      tiles, B, T, Hkv, kSegmentCharge, false,
+  const Rules rules = rules_of(D);
+  rc = plan_units(
+      tiles, B, T, Hkv, rules.segment_charge, false,
       [&](const Unit* units, const int32_t* pages, size_t n, long long total,
-          std::vector<int32_t>* starts) { cut(units, pages, n, total, sms, Hkv, D, starts); },
+          std::vector<int32_t>* starts) { cut(units, pages, n, total, sms, Hkv, rules, starts); },
       &plan);
   if (rc != PA_OK) return rc;
 
@@ -1648,7 +1269,7 @@ int run(const void* q, const void* pool, const float* scales, int64_t pool_pages
   common.stall_iteration = hooks.stall_iteration;
   common.slice_wait_ns = hooks.slice_wait_ns;
   for (Launch& L : plan.launches) {
-    const std::vector<int> order = pack(&plan, &L, sms, D);
+    const std::vector<int> order = pack(&plan, &L, sms, rules);
     rc = launch(D, tmap, plan, L, order, common, stream);
     if (rc != PA_OK) return rc;
   }

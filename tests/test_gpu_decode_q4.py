@@ -351,6 +351,21 @@ def test_ctas_that_leave_the_merge_to_the_last_one(B):
     assert all(torch.equal(a, b) for a, b in zip(want, (c.out, c.lse, c.merged, c.merged_lse)))
 
 
+@pytest.mark.parametrize("iteration", [0, 1, 4])
+def test_a_wait_that_runs_out_is_reported_and_the_context_survives(B, iteration):
+    """One step's loads of CTA 0 stay unarmed; with a 50 ms limit every warp
+    gives up, the call reports it, and the next one is right again."""
+    c = Case([64000], hq=24, hkv=4, d=256, seed=21)
+    assert c.run(B) == 0
+    want = c.out.clone()
+    B.test_stall(iteration, 50_000_000)
+    assert c.run(B) & B.PA_STATUS_TIMEOUT
+    c.ws = None
+    c.out.zero_()
+    assert c.run(B) == 0
+    assert torch.equal(c.out, want)
+
+
 @pytest.mark.parametrize("normed", [False, True])
 def test_the_decode_step_over_a_4_bit_pool(B, normed):
     """ResidentQ4Decode: the pool holds the bf16 history's nearest codes, the step's
