@@ -76,6 +76,22 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
       : "memory");
 }
 
+// Instruction descriptor: fp16 x fp16 -> fp32, as idesc_e4m3.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool a_mn, bool b_mn) {
+  return idesc_e4m3(m, n, a_mn, b_mn);   // (type 0 of either kind)
+}
+
+// D[tmem] (+)= A[tmem] B over 16 values of K, in fp16: a lane of A is a row, a column two
+// values of K.  Issued by one thread.
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                        bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
 // Arrives at `bar` once every tcgen05.mma this thread issued before is done.
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile(
@@ -122,6 +138,36 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
                  "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
+}
+
+// The same of 8 columns, and by the number of registers.
+__device__ __forceinline__ void ld_cols(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(addr));
+}
+__device__ __forceinline__ void wait_ld_cols(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void ld_cols(uint32_t addr, uint32_t (&r)[16]) { ld16(addr, r); }
+__device__ __forceinline__ void wait_ld_cols(uint32_t (&r)[16]) { wait_ld(r); }
+
+// 16 lanes (from the lane field of addr) by 16 columns: register 2 i (+ 1) of thread t holds
+// lane t / 4 (+ 8), column 4 i + t % 4.  wait_st() returns once this thread's stores are done.
+__device__ __forceinline__ void st_16x128b_x4(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+__device__ __forceinline__ void wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 }  // namespace tc
