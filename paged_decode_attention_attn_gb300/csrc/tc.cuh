@@ -1,5 +1,5 @@
 // Inline-PTX wrappers of the fifth-generation tensor cores (sm_103a): tensor
-// memory, tcgen05.mma on e4m3 and e2m1 operands in shared memory, and its completion.
+// memory, tcgen05.mma on e4m3 operands in shared memory, and its completion.
 #pragma once
 
 #include <cstdint>
@@ -40,55 +40,6 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
-      : "memory");
-}
-
-// An operand without swizzle: rows of 16 bytes, groups of eight rows 128 bytes apart.
-__device__ __forceinline__ uint64_t desc_plain(uint32_t addr) {
-  constexpr uint64_t kGroup = 128 >> 4;
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | (kGroup << 16) | (kGroup << 32) | (1ull << 46);
-}
-
-// Scales of 128 rows of an operand and four blocks of 32 K values, from shared memory to
-// four columns of tensor memory: 32 rows of 16 bytes, row r holding the rows r, r + 32,
-// r + 64 and r + 96 of the operand, four bytes (of the four blocks) each.  Issued by the
-// thread that issues the products that read them, which follow it in order.
-__device__ __forceinline__ void copy_scales(uint32_t dst, uint64_t src) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(dst), "l"(src) : "memory");
-}
-
-// Instruction descriptor: e2m1 (in bytes, as TMA unpacks them: 16 codes in 8 of 16 bytes) x
-// e4m3 -> fp32, M x N, both K-major, each with a power-of-two scale per row and 32 values of
-// K; `block` (0 .. 3) picks the byte of the scales' columns.
-__host__ __device__ constexpr uint32_t idesc_e2m1_e4m3(int m, int n, int block) {
-  return ((uint32_t)block << 4) | (5u << 7) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
-         ((uint32_t)(m >> 4) << 24) | ((uint32_t)block << 29);
-}
-
-// D[tmem] (+)= (A scales_a) (B scales_b) over 32 values of K; issued by one thread.
-__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t scales_a, uint32_t scales_b, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
-      "[%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(scales_a), "r"(scales_b), "r"(accumulate ? 1u : 0u)
-      : "memory");
-}
-
-// Instruction descriptor: fp16 x fp16 -> fp32, as idesc_e4m3.
-__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool a_mn, bool b_mn) {
-  return idesc_e4m3(m, n, a_mn, b_mn);   // (type 0 of either kind)
-}
-
-// D[tmem] (+)= A[tmem] B over 16 values of K, in fp16: a lane of A is a row, a column two
-// values of K.  Issued by one thread.
-__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                        bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 
@@ -138,36 +89,6 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[16]) {
                  "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
-}
-
-// The same of 8 columns, and by the number of registers.
-__device__ __forceinline__ void ld_cols(uint32_t addr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(addr));
-}
-__device__ __forceinline__ void wait_ld_cols(uint32_t (&r)[8]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void ld_cols(uint32_t addr, uint32_t (&r)[16]) { ld16(addr, r); }
-__device__ __forceinline__ void wait_ld_cols(uint32_t (&r)[16]) { wait_ld(r); }
-
-// 16 lanes (from the lane field of addr) by 16 columns: register 2 i (+ 1) of thread t holds
-// lane t / 4 (+ 8), column 4 i + t % 4.  wait_st() returns once this thread's stores are done.
-__device__ __forceinline__ void st_16x128b_x4(uint32_t addr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
-}
-__device__ __forceinline__ void wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 }  // namespace tc
