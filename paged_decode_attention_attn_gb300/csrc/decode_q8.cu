@@ -211,7 +211,6 @@ struct Params {
   unsigned long long slice_wait_ns;
   // One tile per request: its output may be the merged one too, written with it.
   static constexpr bool kAllSlices = true, kMerge = false, kSecondOut = true;
-  static constexpr bool kInlineWaits = false;
   float* out2;
   float* lse2;
   int32_t starts[kMaxGrid + 1];      // CTA k takes flattened pages [k], [k + 1)

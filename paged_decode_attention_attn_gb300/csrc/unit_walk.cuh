@@ -35,9 +35,10 @@ struct Ring {
   }
 };
 
-// The slow side of a wait.
-__device__ __forceinline__ bool wait_loop(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                          int32_t* status, volatile int* abort_flag) {
+// The slow side of a wait, out of line: the roles' loops stay short (a warp on its own runs ~6
+// cycles per instruction, and every line of code is fetched cold in a launch).
+inline __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                       int32_t* status, volatile int* abort_flag) {
   const uint64_t t0 = ptx::globaltimer_ns();
   while (true) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
@@ -49,13 +50,6 @@ __device__ __forceinline__ bool wait_loop(uint32_t bar, uint32_t parity, uint64_
     }
   }
 }
-// Out of line the roles' loops stay short (a warp on its own runs ~6 cycles per
-// instruction, and every line of code is fetched cold in a launch).  A kernel that moves
-// registers between its warps has kInlineWaits: the compiler spills none there beside a call.
-inline __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint64_t limit_ns,
-                                       int32_t* status, volatile int* abort_flag) {
-  return wait_loop(bar, parity, limit_ns, status, abort_flag);
-}
 
 // Waits for the phase of the given parity to be complete.  False once the time
 // limit, or another warp's, has run out.
@@ -63,8 +57,7 @@ template <class P, class V>
 __device__ __forceinline__ bool wait(const P& p, const V& v, int bar, uint32_t parity) {
   const uint32_t b = v.bar(bar);
   if (ptx::mbar_try_wait(b, parity)) return true;
-  if constexpr (P::kInlineWaits) return wait_loop(b, parity, p.wait_limit_ns, p.status, v.abort_flag);
-  else return wait_long(b, parity, p.wait_limit_ns, p.status, v.abort_flag);
+  return wait_long(b, parity, p.wait_limit_ns, p.status, v.abort_flag);
 }
 // The same for a converged warp, with one answer for all its lanes: false too if
 // `ok` is false in one of them.  A warp skips tensor memory loads, and leaves its
