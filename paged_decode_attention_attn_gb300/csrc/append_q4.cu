@@ -28,6 +28,71 @@ namespace rope {
 
 constexpr int kGroup = PA_Q4_GROUP;
 
+// A key that lies at a border between two codes goes as plain fp32 arithmetic has it, so the
+// rows here are computed in its steps: sines and cosines rounded from more bits, products
+// and sums rounded apart, squares summed in the order of a reduction by 32 lanes.
+
+// Sine and cosine at position p (see turn()) to ~0.55 units in the last place: the angle's
+// rest in two floats, the leading terms' rounding carried to the end.
+__device__ __forceinline__ void turn_fine(long long p, unsigned long long step, float nan,
+                                          float* s, float* c) {
+  const unsigned long long at = step * (unsigned long long)p;
+  const unsigned quarter = (unsigned)((at + (1ull << 61)) >> 62);
+  const long long rest = (long long)(at - ((unsigned long long)quarter << 62));
+  constexpr float kHi = 3.40612167e-19f, kLo = -9.47839643e-27f;   // 2 pi 2^-64
+  const float hi = __ll2float_rn(rest), lo = __ll2float_rn(rest - __float2ll_rn(hi));
+  const float x = hi * kHi, x_lo = fmaf(hi, kHi, -x) + fmaf(hi, kLo, lo * kHi);
+  const float z = x * x, z_lo = fmaf(x, x, -z) + 2.f * x * x_lo;
+  float a = fmaf(z, -1.0f / 39916800.0f, 1.0f / 362880.0f);
+  a = fmaf(a, z, -1.0f / 5040.0f);
+  a = fmaf(a, z, 1.0f / 120.0f);
+  a = fmaf(a, z, -1.0f / 6.0f);
+  const float sx = __fadd_rn(x, fmaf(a * z, x, x_lo));
+  float b = fmaf(z, 1.0f / 479001600.0f, -1.0f / 3628800.0f);
+  b = fmaf(b, z, 1.0f / 40320.0f);
+  b = fmaf(b, z, -1.0f / 720.0f);
+  b = fmaf(b, z, 1.0f / 24.0f);
+  const float h = __fsub_rn(1.f, 0.5f * z);
+  const float cx = __fadd_rn(h, fmaf(b * z, z, __fsub_rn(1.f, h) - 0.5f * z - 0.5f * z_lo));
+  const bool odd = quarter & 1;
+  const float ss = odd ? cx : sx, cc = odd ? sx : cx;
+  *s = (quarter & 2 ? -ss : ss) + nan;
+  *c = ((quarter + 1) & 2 ? -cc : cc) + nan;
+}
+
+// The sum of a head's squares: a lane has 8 neighbours, the head D / 8 lanes.  All lanes call.
+template <int D>
+__device__ __forceinline__ float sum_of_squares(const float (&y)[8], float by) {
+  float t[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = y[j] * by;
+    t[j] = __fmul_rn(x, x);
+  }
+  float ss;
+  if constexpr (D == 256) {   // the two halves; four neighbours in turn; neighbours' sums
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = __fadd_rn(t[j], __shfl_xor_sync(0xffffffffu, t[j], 16));
+    ss = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(t[0], t[1]), t[2]), t[3]),
+                   __fadd_rn(__fadd_rn(__fadd_rn(t[4], t[5]), t[6]), t[7]));
+  } else {                    // the four quarters in turn; neighbours' sums
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int at = threadIdx.x & 0x13;
+      float u = __shfl_sync(0xffffffffu, t[j], at);
+#pragma unroll
+      for (int k = 1; k < 4; ++k) u = __fadd_rn(u, __shfl_sync(0xffffffffu, t[j], at + 4 * k));
+      t[j] = u;
+    }
+    ss = __fadd_rn(__fadd_rn(__fadd_rn(t[0], t[1]), __fadd_rn(t[2], t[3])),
+                   __fadd_rn(__fadd_rn(t[4], t[5]), __fadd_rn(t[6], t[7])));
+  }
+#pragma unroll
+  for (int off = 1; off < (D == 256 ? 16 : 4); off *= 2)
+    ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, off));
+  return ss;
+}
+
 // The k and v heads of a row into the 4-bit pool.  `share` warps to a row, this one the
 // w-th; cs: the row's cosines and sines.
 template <int D, bool kNorm>
@@ -88,7 +153,7 @@ __device__ __forceinline__ void store_row_q4(const Tokens& t, const Norm& norm,
       }
       float r = 1.f, pre = 1.f;
       if constexpr (kNorm) {
-        r = head_norm<D>(y, norm.eps, &pre);
+        r = norm_of<D>([&](float by) { return sum_of_squares<D>(y, by); }, norm.eps, &pre);
         if (key) {
 #pragma unroll
           for (int j = 0; j < kN; ++j) y[j] = y[j] * pre * r * weights[1][d0 + j];
@@ -104,8 +169,8 @@ __device__ __forceinline__ void store_row_q4(const Tokens& t, const Norm& norm,
             for (int m = 0; m < 2; ++m) {
               const float c = cs[0][pair[j] + m], s = cs[1][pair[j] + m];
               const float a = x[2 * m], b = x[2 * m + 1];
-              x[2 * m] = a * c - b * s;
-              x[2 * m + 1] = b * c + a * s;
+              x[2 * m] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+              x[2 * m + 1] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
             }
           } else {
             float z[4] = {ptx::bf16_lo_to_f32(far[i][j].x), ptx::bf16_hi_to_f32(far[i][j].x),
@@ -117,7 +182,7 @@ __device__ __forceinline__ void store_row_q4(const Tokens& t, const Norm& norm,
             for (int m = 0; m < 4; ++m) {
               if constexpr (kNorm)
                 z[m] = z[m] * pre * r * weights[1][d0 + 4 * j + other[j] + m];
-              x[m] = x[m] * c[m] + sign[j] * (z[m] * s[m]);
+              x[m] = __fadd_rn(__fmul_rn(x[m], c[m]), sign[j] * __fmul_rn(z[m], s[m]));
             }
           }
         }
@@ -167,7 +232,7 @@ __device__ __forceinline__ void store_rows_q4(const Tokens& t, const Norm& norm,
   }
   for (int i = lane; i < t.half; i += 32) {
     const float f = __ldg(t.inv_freq + i);
-    turn(pos, turn_step(f), not_finite(f), &cs[warp][1][i], &cs[warp][0][i]);
+    turn_fine(pos, turn_step(f), not_finite(f), &cs[warp][1][i], &cs[warp][0][i]);
   }
   __syncwarp();
   store_row_q4<D, kNorm>(t, norm, weights, cs[warp], row, pool, scales, page, (int)(pos % kPage),

@@ -196,27 +196,18 @@ struct Norm {
   float eps;
 };
 
-// The lanes' values of a head (D / N consecutive lanes hold one), each lane's N:
-// 1 / sqrt(mean + eps) of their squares, and `pre`, the power of two that the values
-// are multiplied by first (1, unless squares pass the range of fp32: bf16 values reach
-// 2^128, and x 2^-70 has a square and a sum in range, beside which eps is nothing).
-// All lanes of the warp call.
-template <int D, int N>
-__device__ __forceinline__ float head_norm(const float (&y)[N], float eps, float* pre) {
-  constexpr int kLanes = D / N;
-  auto sum_of_squares = [&](float by) {
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < N; ++j) ss = fmaf(y[j] * by, y[j] * by, ss);
-#pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    return ss;
-  };
-  float ss = sum_of_squares(1.f);
+// A head's 1 / sqrt(mean + eps) of its D squares, and `pre`, the power of two that its
+// values are multiplied by first (1, unless squares pass the range of fp32: bf16 values
+// reach 2^128, and x 2^-70 has a square and a sum in range, beside which eps is nothing).
+// sum(by): of the squares of the values times `by`, in all lanes of the head.  All lanes of
+// the warp call.
+template <int D, class Sum>
+__device__ __forceinline__ float norm_of(Sum sum, float eps, float* pre) {
+  float ss = sum(1.f);
   *pre = 1.f;
   const bool large = !(ss <= FLT_MAX);
   if (__any_sync(0xffffffffu, large)) {
-    const float again = sum_of_squares(ptx::pow2i(-70));
+    const float again = sum(ptx::pow2i(-70));
     if (large) {
       ss = again;
       eps = 0.f;
@@ -224,6 +215,19 @@ __device__ __forceinline__ float head_norm(const float (&y)[N], float eps, float
     }
   }
   return rsqrtf(fmaf(ss, 1.f / D, eps));
+}
+// The same of values that D / N consecutive lanes hold, each lane N.
+template <int D, int N>
+__device__ __forceinline__ float head_norm(const float (&y)[N], float eps, float* pre) {
+  constexpr int kLanes = D / N;
+  return norm_of<D>([&](float by) {
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) ss = fmaf(y[j] * by, y[j] * by, ss);
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+    return ss;
+  }, eps, pre);
 }
 
 // The weights of both norms into shared memory: every thread of the CTA, a barrier
