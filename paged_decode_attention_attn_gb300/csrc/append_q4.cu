@@ -93,6 +93,27 @@ __device__ __forceinline__ float sum_of_squares(const float (&y)[8], float by) {
   return ss;
 }
 
+// A head's 1 / sqrt(mean + eps) of its D squares, and `pre`, the power of two that its
+// values are multiplied by first (1, unless squares pass the range of fp32: bf16 values
+// reach 2^128, and x 2^-70 has a square and a sum in range, beside which eps is nothing).
+// sum(by): of the squares of the values times `by`, in all lanes of the head.  All lanes of
+// the warp call.
+template <int D, class Sum>
+__device__ __forceinline__ float norm_of(Sum sum, float eps, float* pre) {
+  float ss = sum(1.f);
+  *pre = 1.f;
+  const bool large = !(ss <= FLT_MAX);
+  if (__any_sync(0xffffffffu, large)) {
+    const float again = sum(ptx::pow2i(-70));
+    if (large) {
+      ss = again;
+      eps = 0.f;
+      *pre = ptx::pow2i(-70);
+    }
+  }
+  return rsqrtf(fmaf(ss, 1.f / D, eps));
+}
+
 // The k and v heads of a row into the 4-bit pool.  `share` warps to a row, this one the
 // w-th; cs: the row's cosines and sines.
 template <int D, bool kNorm>
@@ -250,10 +271,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int pairs = min(kv_ctas, (int)gridDim.x - kv_ctas);
   const bool paired = (int)blockIdx.x < 2 * pairs;
   const int cta = paired ? blockIdx.x / 2 : blockIdx.x - pairs;
-  if (paired ? blockIdx.x & 1 : pairs == kv_ctas)
-    rotate_rows<D, V, false, kNorm>(t, norm, nullptr, cta, q_share);
-  else
+  if (paired ? blockIdx.x & 1 : pairs == kv_ctas) {
+    if constexpr (kNorm) norm_rows<D, V, false>(t, norm, nullptr, cta, q_share);
+    else rotate_rows<D, V, false>(t, nullptr, cta, q_share);
+  } else {
     store_rows_q4<D, kNorm>(t, norm, pool, scales, cta, kv_share);
+  }
 }
 
 // Rows of a 4-bit pool as bf16 values: `share` warps to a row, a lane turns 16 codes of

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     append_rope_kernel(const Tokens t, __nv_bfloat16* pool, int share) {
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
-  rotate_rows<D, V, true, false>(t, Norm{}, pool, blockIdx.x, share);
+  rotate_rows<D, V, true>(t, pool, blockIdx.x, share);
 }
 
 template <int D, int V>
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     append_norm_rope_kernel(const Tokens t, const Norm norm, __nv_bfloat16* pool, int share) {
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
-  rotate_rows<D, V, true, true>(t, norm, pool, blockIdx.x, share);
+  norm_rows<D, V, true>(t, norm, pool, blockIdx.x, share);
 }
 
 // Smallest power of two s >= 2^-60 with amax <= 448 s (448 = 1.75 * 2^8 is the
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   const bool paired = (int)blockIdx.x < 2 * pairs;
   const int cta = paired ? blockIdx.x / 2 : blockIdx.x - pairs;
   if (paired ? blockIdx.x & 1 : pairs == kv_ctas) {
-    rotate_rows<D, V, false, false>(t, Norm{}, nullptr, cta, share);
+    rotate_rows<D, V, false>(t, nullptr, cta, share);
     return;
   }
   __shared__ __align__(16) float cs[kBlock][2][D / 2];

@@ -10,6 +10,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "f32x2.cuh"
 #include "ptx.cuh"
 
 namespace pa {
@@ -196,40 +197,6 @@ struct Norm {
   float eps;
 };
 
-// A head's 1 / sqrt(mean + eps) of its D squares, and `pre`, the power of two that its
-// values are multiplied by first (1, unless squares pass the range of fp32: bf16 values
-// reach 2^128, and x 2^-70 has a square and a sum in range, beside which eps is nothing).
-// sum(by): of the squares of the values times `by`, in all lanes of the head.  All lanes of
-// the warp call.
-template <int D, class Sum>
-__device__ __forceinline__ float norm_of(Sum sum, float eps, float* pre) {
-  float ss = sum(1.f);
-  *pre = 1.f;
-  const bool large = !(ss <= FLT_MAX);
-  if (__any_sync(0xffffffffu, large)) {
-    const float again = sum(ptx::pow2i(-70));
-    if (large) {
-      ss = again;
-      eps = 0.f;
-      *pre = ptx::pow2i(-70);
-    }
-  }
-  return rsqrtf(fmaf(ss, 1.f / D, eps));
-}
-// The same of values that D / N consecutive lanes hold, each lane N.
-template <int D, int N>
-__device__ __forceinline__ float head_norm(const float (&y)[N], float eps, float* pre) {
-  constexpr int kLanes = D / N;
-  return norm_of<D>([&](float by) {
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < N; ++j) ss = fmaf(y[j] * by, y[j] * by, ss);
-#pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    return ss;
-  }, eps, pre);
-}
-
 // The weights of both norms into shared memory: every thread of the CTA, a barrier
 // before they are read.
 template <int D, bool kKey>
@@ -242,19 +209,17 @@ __device__ __forceinline__ void load_weights(const Norm& norm, bool q, float (*w
 
 // Rotates the q heads of the token rows of CTA cta into q_out and, with kKv,
 // stores their k (rotated) and v heads in the bf16 pool: `share` (1, 2, 4 or 8)
-// warps to a row.  kNorm: q and k heads are normed first.  Warps do not wait for
-// each other (but for the weights); a warp issues its row's first loads before it
-// looks the row up.  (Fewer CTAs whose warps take several rows each, the next one's
-// loads ahead, measured slower: 44.6 against 40.4 us for 11 prompts of up to 2,500
-// tokens.)
-template <int D, int V, bool kKv, bool kNorm>
-__device__ __forceinline__ void rotate_rows(const Tokens& t, const Norm& norm,
-                                            __nv_bfloat16* pool, int cta, int share) {
+// warps to a row.  Warps do not wait for each other; a warp issues its row's first
+// loads before it looks the row up.  (Fewer CTAs whose warps take several rows each,
+// the next one's loads ahead, measured slower: 44.6 against 40.4 us for 11 prompts of
+// up to 2,500 tokens.)
+template <int D, int V, bool kKv>
+__device__ __forceinline__ void rotate_rows(const Tokens& t, __nv_bfloat16* pool, int cta,
+                                            int share) {
   constexpr int kLanes = D / (2 * V);        // lanes per head row
   constexpr int kHeads = 32 / kLanes;        // head rows a warp takes at once
   constexpr int kUnroll = 4;
   __shared__ __align__(16) float table[kWarps][2][D / 2];
-  __shared__ __align__(16) float weights[kNorm ? 2 : 1][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_cta = kWarps / share;
   const Lane ln = lane_of<V>(lane % kLanes, t.half, t.interleaved);
@@ -263,7 +228,7 @@ __device__ __forceinline__ void rotate_rows(const Tokens& t, const Norm& norm,
   const int first_h = (warp % share) * kHeads, sub = lane / kLanes;
   Vec<V> va[kUnroll], vb[kUnroll];
   const int row = cta * per_cta + warp / share;
-  if (!kNorm && row >= t.n_tokens) return;
+  if (row >= t.n_tokens) return;
   auto load = [&](int h0) {
     const __nv_bfloat16* q = t.q + row * t.q_stride;
     const __nv_bfloat16* k = t.k + row * t.k_stride;
@@ -279,12 +244,7 @@ __device__ __forceinline__ void rotate_rows(const Tokens& t, const Norm& norm,
       vb[i] = *reinterpret_cast<const Vec<V>*>(src + ln.ob);
     }
   };
-  if (!kNorm || row < t.n_tokens) load(first_h);
-  if constexpr (kNorm) {
-    load_weights<D, kKv>(norm, t.Hq > 0, weights);
-    __syncthreads();
-    if (row >= t.n_tokens) return;
-  }
+  load(first_h);
   int b = 0, first, end;
   long long pos = 0;
   if (!locate(t.cu, t.positions, t.B, t.n_tokens, row, lane, &b, &pos, &first, &end)) return;
@@ -314,25 +274,9 @@ __device__ __forceinline__ void rotate_rows(const Tokens& t, const Norm& norm,
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const int h = h0 + sub + i * step, g = h - t.Hq;
-      if (kNorm && h0 + i * step >= heads) break;   // (of the whole warp)
       const bool turned = h < heads && (!kKv || g < t.Hkv);   // v keeps its bits
-      if constexpr (kNorm) {
-        float y[2 * V], pre;
-        if (h >= heads) va[i] = vb[i] = Vec<V>{};
-        unpack<V>(va[i], vb[i], y);
-        const float r = head_norm<D>(y, norm.eps, &pre);
-        if (turned) {
-          const float* w = weights[kKv && g >= 0 ? 1 : 0];
-#pragma unroll
-          for (int j = 0; j < 2 * V; ++j)
-            y[j] = y[j] * pre * r * w[j < V ? ln.oa + j : ln.ob + j - V];
-          if (ln.turns) rotate<V>(t.interleaved, c, s, y);
-          va[i] = pack<V>(y);
-          vb[i] = pack<V>(y + V);
-        }
-      }
       if (h >= heads || (kKv && g >= 0 && kv_out == nullptr)) continue;
-      if (!kNorm && ln.turns && turned) {   // what passes keeps its bits too
+      if (ln.turns && turned) {   // what passes keeps its bits too
         float y[2 * V];
         unpack<V>(va[i], vb[i], y);
         rotate<V>(t.interleaved, c, s, y);
@@ -346,6 +290,167 @@ __device__ __forceinline__ void rotate_rows(const Tokens& t, const Norm& norm,
     h0 += kUnroll * step;
     if (h0 >= heads) break;
     load(h0);
+  }
+}
+
+// The same with the norm of q and k heads ahead of the rotation.  A row's weights and
+// turns meet once, y[j] = x[j] r p[j] + x'[j] r q[j] with x' the pair's other, for all its
+// q heads and again for its k heads.  Slots of a row go through the warp one after the
+// other, q heads, k heads, v heads, the load of a slot four ahead.  (With the turn after
+// the norm of each head, weights from shared memory, and a batch's loads after the one
+// before it: 252 instructions for 16 values of a lane, 87.7 us for 13 prompts of up to
+// 2,100 tokens.)
+template <int D, int V, bool kKv>
+__device__ __forceinline__ void norm_rows(const Tokens& t, const Norm& norm, __nv_bfloat16* pool,
+                                          int cta, int share) {
+  constexpr int kLanes = D / (2 * V);        // lanes per head row
+  constexpr int kHeads = 32 / kLanes;        // head rows a warp takes at once
+  constexpr int kAhead = 4;
+  __shared__ __align__(16) float table[kWarps][2][D / 2];
+  __shared__ __align__(16) float weights[2][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_cta = kWarps / share;
+  const Lane ln = lane_of<V>(lane % kLanes, t.half, t.interleaved);
+  const int step = share * kHeads, h0 = (warp % share) * kHeads + lane / kLanes;
+  const int q_slots = (t.Hq + step - 1) / step, k_slots = kKv ? (t.Hkv + step - 1) / step : 0;
+  const int slots = q_slots + 2 * k_slots;
+  const long long row = (long long)cta * per_cta + warp / share;
+  Vec<V> va[kAhead], vb[kAhead];
+  auto load = [&](int slot, Vec<V>& a, Vec<V>& b) {
+    const __nv_bfloat16* src;
+    int h = h0 + slot * step;
+    bool there = h < t.Hq;
+    if (slot < q_slots) {
+      src = t.q + row * t.q_stride;
+    } else {
+      const bool value = slot >= q_slots + k_slots;
+      h = h0 + (slot - q_slots - (value ? k_slots : 0)) * step;
+      there = h < t.Hkv && slot < slots;
+      src = value ? t.v + row * t.v_stride : t.k + row * t.k_stride;
+    }
+    a = b = Vec<V>{};
+    if (!there) return;
+    a = *reinterpret_cast<const Vec<V>*>(src + h * D + ln.oa);
+    b = *reinterpret_cast<const Vec<V>*>(src + h * D + ln.ob);
+  };
+  if (row < t.n_tokens) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(i, va[i], vb[i]);
+  }
+  load_weights<D, kKv>(norm, t.Hq > 0, weights);
+  __syncthreads();
+  if (row >= t.n_tokens) return;
+  int b = 0, first, end;
+  long long pos = 0;
+  if (!locate(t.cu, t.positions, t.B, t.n_tokens, (int)row, lane, &b, &pos, &first, &end)) return;
+  for (int i = lane; i < t.half; i += 32) {
+    const float f = __ldg(t.inv_freq + i);
+    turn(pos, turn_step(f), not_finite(f), &table[warp][1][i], &table[warp][0][i]);
+  }
+  __nv_bfloat16* q_out = t.q_out + row * t.q_out_stride;
+  __nv_bfloat16* kv_out = nullptr;
+  if (kKv) {
+    const long long page = page_of(t.page_table, t.max_pages, t.pool_pages, b, pos);
+    if (page >= 0) kv_out = pool + (page * kPage + pos % kPage) * (2ll * t.Hkv * D);
+    else if (lane == 0 && t.status) atomicOr(t.status, PA_STATUS_BAD_ROW);
+  }
+  __syncwarp();
+  float2 p[V], q[V];
+  auto meet = [&](const float* w) {          // q 0 where nothing turns
+    float x[2 * V], c[V] = {}, s[V] = {};
+    auto four = [](float* to, const float* from) {
+      *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(from);
+    };
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      four(x + j, w + ln.oa + j);
+      four(x + V + j, w + ln.ob + j);
+      if (ln.turns) {
+        four(c + j, &table[warp][0][ln.pair + j]);
+        four(s + j, &table[warp][1][ln.pair + j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2 * V; ++j) {
+      // its pair, and whether it is the first of it, in the two layouts
+      const float cj = t.interleaved ? c[j / 2] : c[j % V], sj = t.interleaved ? s[j / 2] : s[j % V];
+      const float other = t.interleaved ? x[j ^ 1] : x[(j + V) % (2 * V)];
+      const bool is_first = t.interleaved ? j % 2 == 0 : j < V;
+      (j % 2 ? p[j / 2].y : p[j / 2].x) = ln.turns ? x[j] * cj : x[j];
+      (j % 2 ? q[j / 2].y : q[j / 2].x) = ln.turns ? (is_first ? -other : other) * sj : 0.f;
+    }
+  };
+  meet(weights[q_slots ? 0 : 1]);
+  auto slot_of = [&](int slot, Vec<V>& a, Vec<V>& b2) {
+    Vec<V> oa = a, ob = b2;
+    const bool value = slot >= q_slots + k_slots, key = !value && slot >= q_slots;
+    const int h = h0 + (slot - (key ? q_slots : value ? q_slots + k_slots : 0)) * step;
+    if (key && slot == q_slots && q_slots) meet(weights[1]);
+    if (!value) {
+      float2 y[V];
+      {
+        float x[2 * V];
+        unpack<V>(a, b2, x);
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = make_float2(x[2 * j], x[2 * j + 1]);
+      }
+      load(slot + kAhead, a, b2);
+      auto sum_of_squares = [&]() {
+        float2 z = f32x2::mul(y[0], y[0]);
+#pragma unroll
+        for (int j = 1; j < V; ++j) z = f32x2::fma(y[j], y[j], z);
+        float ss = z.x + z.y;
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        return ss;
+      };
+      float ss = sum_of_squares(), eps = norm.eps;
+      // Squares beyond the range of fp32 (bf16 values reach 2^128): x 2^-70 has a square and
+      // a sum in range, beside which eps is nothing.
+      if (__any_sync(0xffffffffu, !(ss <= FLT_MAX))) {
+        const bool large = !(ss <= FLT_MAX);
+        if (large) eps = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = f32x2::mul(y[j], f32x2::both(large ? ptx::pow2i(-70) : 1.f));
+        ss = sum_of_squares();
+      }
+      const float2 r = f32x2::both(rsqrtf(fmaf(ss, 1.f / D, eps)));
+#pragma unroll
+      for (int j = 0; j < V; ++j) y[j] = f32x2::mul(y[j], r);
+      float2 z[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) z[j] = f32x2::mul(y[j], p[j]);
+      if (ln.turns) {
+        if (t.interleaved) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) z[j] = f32x2::fma(make_float2(y[j].y, y[j].x), q[j], z[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) z[j] = f32x2::fma(y[(j + V / 2) % V], q[j], z[j]);
+        }
+      }
+      float x[2 * V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        x[2 * j] = z[j].x;
+        x[2 * j + 1] = z[j].y;
+      }
+      oa = pack<V>(x);
+      ob = pack<V>(x + V);
+    } else {
+      load(slot + kAhead, a, b2);
+    }
+    if (h >= (key || value ? t.Hkv : t.Hq) || (kv_out == nullptr && (key || value))) return;
+    __nv_bfloat16* dst = key ? kv_out + h * D : value ? kv_out + (t.Hkv + h) * D : q_out + h * D;
+    *reinterpret_cast<Vec<V>*>(dst + ln.oa) = oa;
+    *reinterpret_cast<Vec<V>*>(dst + ln.ob) = ob;
+  };
+  for (int s0 = 0; s0 < slots; s0 += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (s0 + i >= slots) break;            // (of the whole warp)
+      slot_of(s0 + i, va[i], vb[i]);
+    }
   }
 }
 
