@@ -254,10 +254,10 @@ int paged_decode_attn_lse_append(const void* q, void* pool, int64_t pool_pages,
 
 /* Test hook for failure detection (no counterpart in the source pages): the
  * next decode call made on this thread (any paged_decode_attn_lse* entry
- * point, or paged_decode_attn_q8_lse) gives every bounded device wait up after
- * wait_limit_ns (instead of 2 s), and CTA 0 leaves its page load (8-bit pool:
- * its load of two pages' keys, or, with PA_STALL_VALUES added to `iteration`,
- * of their values) number `iteration` unarmed, so the wait for that load runs
+ * point, paged_decode_attn_q8_lse or paged_decode_attn_q4_lse) gives every bounded
+ * device wait up after wait_limit_ns (instead of 2 s), and CTA 0 leaves its page
+ * load (8-bit pool: its load of two pages' keys, or, with PA_STALL_VALUES added to
+ * `iteration`, of their values) number `iteration` unarmed, so the wait for that load runs
  * out: the kernel sets PA_STATUS_TIMEOUT, lets the loads it issued land and
  * returns; the context stays usable.  Outputs of that call are invalid and its
  * workspace must be zero-filled again before reuse.  (-1, 0) clears a pending setting.  PA_ERR_INVALID otherwise unless
@@ -475,7 +475,9 @@ int paged_decode_attn_q8_lse(const void* q, const void* pool, const float* scale
  * For every group of 32 values of the normed and rotated k, and of v, in FP32: the
  * scale is the smallest power of two s >= 2^-60 with |x| <= 6 s for all of them, and
  * the codes are x / s rounded to nearest even.  A group with a value that is not
- * finite gets the scale NaN.  Rows of other tokens are left as they are.
+ * finite gets the scale NaN.  (k is normed and rotated in the steps of plain FP32
+ * arithmetic, each product and sum rounded, so that a value at a border between two
+ * codes goes as it would there.)  Rows of other tokens are left as they are.
  * Supported head_dim: 128, 256. */
 int kv_append_rope_q4(const void* q, const void* k, const void* v, int64_t q_stride,
                       int64_t k_stride, int64_t v_stride, void* q_out, int64_t q_out_stride,
@@ -504,6 +506,10 @@ size_t paged_decode_attn_q4_workspace_bytes(int B, int T, int n_q_heads, int n_k
  * paged_decode_attn_q8_lse.  Arguments as there, except:
  *   pool, scales  device, 16-byte aligned, as described at PA_Q4_GROUP.
  * Rows outside a tile may hold anything, NaN scales too.
+ * A probability times its V scales is held to 2^-23 of itself, or to 2^-37 of the largest
+ * so far in a row's part of a tile, for each group of 32 dims by itself while V's scales lie
+ * within 2^16 of each other (further apart: in FP32); probabilities below 2^-110 of the
+ * largest count as zero.
  * Supported: head_dim 128 and 256, n_q_heads / n_kv_heads in 1..8. */
 int paged_decode_attn_q4_lse(const void* q, const void* pool, const uint8_t* scales,
                              int64_t pool_pages, const int32_t* page_table, int max_pages,

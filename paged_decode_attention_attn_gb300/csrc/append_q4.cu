@@ -10,8 +10,10 @@
 // (from L1) instead of exchanged.  q rows go as in the appends to the other pools, by
 // CTAs of their own.
 //
-// Bound by HBM at prompt sizes and by the latency of its dependent loads (request,
-// position, page, row) at decode sizes.
+// Decode sizes are bound by the latency of dependent loads (request, position, page, row:
+// 1-96 tokens 3.5-4 us and 2 us for the gather); prompts by instructions and their loads'
+// latency (8,000 tokens of 24 q and 4 kv heads of 256 dims with norms 66 us where the bytes
+// take 35, their gather 10.6).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -263,7 +265,7 @@ __device__ __forceinline__ void store_rows_q4(const Tokens& t, const Norm& norm,
 // kv_ctas CTAs store rows of k and v, the others rotate q rows; the kinds alternate, so
 // that an SM has both.
 template <int D, int V, bool kNorm>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kNorm ? 3 : 2)
     append_rope_q4_kernel(const Tokens t, const Norm norm, uint8_t* pool, uint8_t* scales,
                           int kv_ctas, int kv_share, int q_share) {
   ptx::launch_dependents();
@@ -349,11 +351,14 @@ cudaError_t launch_append_q4(const Tokens& t, const Norm& norm, void* pool, uint
                           q_share);
 }
 
-template <int D, int V>
+// (q rows with norms go by 4 pairs of a lane, three CTAs to an SM: two prompts 76.2 us; by 8,
+// two CTAs: 78.7.)
+template <int D>
 cudaError_t launch_append_q4(const Tokens& t, const Norm& norm, bool normed, void* pool,
                              uint8_t* scales, cudaStream_t stream) {
-  return normed ? launch_append_q4<D, V, true>(t, norm, pool, scales, stream)
-                : launch_append_q4<D, V, false>(t, norm, pool, scales, stream);
+  return normed    ? launch_append_q4<D, 4, true>(t, norm, pool, scales, stream)
+         : wide(t) ? launch_append_q4<D, 8, false>(t, norm, pool, scales, stream)
+                   : launch_append_q4<D, 4, false>(t, norm, pool, scales, stream);
 }
 
 }  // namespace rope
@@ -381,12 +386,8 @@ extern "C" int kv_append_rope_q4(const void* q, const void* k, const void* v, in
   if (rc != PA_OK || n_tokens == 0 || B == 0) return rc;
   PA_REQUIRE(scales != nullptr && aligned16(scales), "scales must be non-null, 16-byte aligned");
   if (normed && (rc = check_norm(t, norm)) != PA_OK) return rc;
-  const bool w = wide(t);
-  PA_CHECK_CUDA(head_dim == 128
-                    ? (w ? launch_append_q4<128, 8>(t, norm, normed, pool, scales, stream)
-                         : launch_append_q4<128, 4>(t, norm, normed, pool, scales, stream))
-                    : (w ? launch_append_q4<256, 8>(t, norm, normed, pool, scales, stream)
-                         : launch_append_q4<256, 4>(t, norm, normed, pool, scales, stream)));
+  PA_CHECK_CUDA(head_dim == 128 ? launch_append_q4<128>(t, norm, normed, pool, scales, stream)
+                                : launch_append_q4<256>(t, norm, normed, pool, scales, stream));
   PA_CHECK_CUDA(cudaGetLastError());
   return PA_OK;
 }

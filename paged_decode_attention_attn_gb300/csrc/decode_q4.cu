@@ -901,8 +901,7 @@ __device__ __forceinline__ void tma_thread(const P& p, const View& v, const CUte
   int loads = 0;
   uint32_t marked = 0;     // stages marked as bad
   const uint64_t pol = ptx::policy_evict_first();   // every page is read once
-  const int stall = blockIdx.x == 0 && p.stall_iteration >= 0
-                        ? p.stall_iteration & ~(int)PA_STALL_VALUES : -1;
+  const int stall = blockIdx.x == 0 ? p.stall_iteration : -1;
   ptx::grid_dependency_wait();
   for_segments(p, [&](const Segment& s, int) {
     const int32_t* prow =
