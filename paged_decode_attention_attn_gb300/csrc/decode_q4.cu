@@ -83,6 +83,7 @@ constexpr float kMostExp = 0x1p64f;          // e may lie above 1, up to this
 constexpr int kSlack = 3;                    // what m' leaves above the largest weight so far (log2)
 constexpr float kMostWeight = 65000.f;       // in fp16, which ends at 65504
 constexpr int kSpread = 16;                  // see attend()
+constexpr int kTiny = fp4::kScaleBias + fp4::kMinScaleExp;   // the smallest scale appends write
 
 // Shared memory of a CTA; offsets from a 1024-byte boundary.
 template <int D>
@@ -469,7 +470,9 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
   // Weights are fp16 pairs, and a group of dims is held to its own size as long as its
   // scales lie within 2^kSpread of the largest scale that the team has met (a weight that
   // counts for it is then at least 2^-3 and has 22 bits).  The test takes bounds that are a
-  // little closer, and bytes of rows that are not live with the others.
+  // little closer, and bytes of rows that are not live with the others.  Scales as small as
+  // the smallest that appends write do not count: their groups are zeros (heads padded to
+  // 128 or 256 dims have them in every token), or nothing beside the others.
   uint32_t in = 0x80008000u;
 #pragma unroll
   for (int tile = 0; tile < kTiles; ++tile) {
@@ -477,7 +480,8 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
     e[tile] = bytes[tile].largest();
 #pragma unroll
     for (int i = 0; i < Bytes<D>::kWords; ++i) {
-      in &= bytes[tile].b[i] + 0x00010001u * (0x8000 - max(part.most - (kSpread - 4), 0));
+      in &= (bytes[tile].b[i] + 0x00010001u * (0x8000 - max(part.most - (kSpread - 4), 0))) |
+            ~(bytes[tile].b[i] + 0x00010001u * (0x8000 - kTiny - 1));
       if (!first) publish_factor(tile, i, factor(tile, i));
     }
     in &= ~(e[tile] + 0x00010001u * (0x7fff - min(part.most + 4, 254)));
@@ -525,7 +529,7 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
         } else if (row >= lo && row < hi) {
           const uint4 c = lds128(codes + S::kHalf +
                                  run_at<D>(row, Bytes<D>::kWords * t + (k >> 1)));
-          if ((c.x | c.y | c.z | c.w) & 0x77777777u) least = min(least, b);
+          if (b > kTiny && ((c.x | c.y | c.z | c.w) & 0x77777777u)) least = min(least, b);
         }
       }
       e[tile] = bytes[tile].largest();

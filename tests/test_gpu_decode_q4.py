@@ -558,3 +558,17 @@ def test_batches_of_more_units_than_ctas(B, n, top, geo):
     want = [t.clone() for t in (c.out, c.lse, c.merged, c.merged_lse)]
     assert c.run(B) == 0
     assert all(torch.equal(a, b) for a, b in zip(want, (c.out, c.lse, c.merged, c.merged_lse)))
+
+
+@pytest.mark.parametrize("geo,zero", [((24, 4, 256), slice(192, 256)), ((8, 8, 128), slice(96, 128)),
+                                      ((4, 1, 256), slice(0, 256))])
+def test_heads_padded_with_zeros(B, geo, zero):
+    """Groups of V that are zeros, with the smallest scale that appends write: outputs of
+    those dims are zero, the others as the oracle's."""
+    c = Case([3000, 65, 1], hq=geo[0], hkv=geo[1], d=geo[2], seed=31)
+    c.pool[:, geo[1]:, :, zero.start // 2:zero.stop // 2] = 0
+    live = c.scales[:, geo[1]:, :, zero.start // 32:zero.stop // 32]
+    live[live != 255] = 127 - 60
+    assert c.run(B) == 0
+    c.check()
+    assert torch.all(c.merged[..., zero] == 0)
