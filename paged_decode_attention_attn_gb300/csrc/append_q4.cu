@@ -175,7 +175,7 @@ __device__ __forceinline__ void store_row_q4(const Tokens& t, const Norm& norm,
         y[2 * j + 1] = ptx::bf16_hi_to_f32(word[j]);
       }
       float r = 1.f, pre = 1.f;
-      if constexpr (kNorm) {
+      if (kNorm && h - sub < t.Hkv) {   // (of the whole warp: a k head is among its)
         r = norm_of<D>([&](float by) { return sum_of_squares<D>(y, by); }, norm.eps, &pre);
         if (key) {
 #pragma unroll
@@ -220,8 +220,8 @@ __device__ __forceinline__ void store_row_q4(const Tokens& t, const Norm& norm,
       const int e = finite ? fp4::scale_exp(amax) : 0;
       const float inv = finite ? ptx::pow2i(-e) : 0.f;   // exact
 #pragma unroll
-      for (int j = 0; j < kN; ++j) y[j] = finite ? y[j] * inv : 0.f;
-      const uint32_t codes = fp4::pack8(y);
+      for (int j = 0; j < kN; ++j) y[j] *= inv;
+      const uint32_t codes = finite ? fp4::pack8(y) : 0u;
       if (h >= heads) continue;
       const size_t place = ((size_t)page * heads + h) * kPage + at;
       *reinterpret_cast<uint32_t*>(pool + place * (D / 2) + 4 * l) = codes;
@@ -329,8 +329,7 @@ __global__ void __launch_bounds__(kThreads)
         fp4::unpack8(j ? codes[i].y : codes[i].x, y);
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-          o[4 * j + m] = ptx::pack_bf16x2(__float2bfloat16_rn(y[2 * m] * s),
-                                          __float2bfloat16_rn(y[2 * m + 1] * s));
+          o[4 * j + m] = ptx::round_bf16x2(y[2 * m] * s, y[2 * m + 1] * s);
       }
       store32(dst + 2 * c, o);
     }

@@ -179,7 +179,7 @@ __device__ __forceinline__ Vec<V> pack(const float* y) {
   uint32_t* w = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
   for (int i = 0; i < V / 2; ++i)
-    w[i] = ptx::pack_bf16x2(__float2bfloat16_rn(y[2 * i]), __float2bfloat16_rn(y[2 * i + 1]));
+    w[i] = ptx::round_bf16x2(y[2 * i], y[2 * i + 1]);
   return r;
 }
 
@@ -316,22 +316,20 @@ __device__ __forceinline__ void norm_rows(const Tokens& t, const Norm& norm, __n
   const int slots = q_slots + 2 * k_slots;
   const long long row = (long long)cta * per_cta + warp / share;
   Vec<V> va[kAhead], vb[kAhead];
+  // (a lane without a head of its own takes the last one's values and stores nothing)
   auto load = [&](int slot, Vec<V>& a, Vec<V>& b) {
-    const __nv_bfloat16* src;
-    int h = h0 + slot * step;
-    bool there = h < t.Hq;
-    if (slot < q_slots) {
-      src = t.q + row * t.q_stride;
-    } else {
+    const __nv_bfloat16* src = t.q + row * t.q_stride;
+    int h = h0 + slot * step, last = t.Hq - 1;
+    if (kKv && slot >= q_slots) {
       const bool value = slot >= q_slots + k_slots;
-      h = h0 + (slot - q_slots - (value ? k_slots : 0)) * step;
-      there = h < t.Hkv && slot < slots;
+      h -= (value ? q_slots + k_slots : q_slots) * step;
+      last = t.Hkv - 1;
       src = value ? t.v + row * t.v_stride : t.k + row * t.k_stride;
     }
-    a = b = Vec<V>{};
-    if (!there) return;
-    a = *reinterpret_cast<const Vec<V>*>(src + h * D + ln.oa);
-    b = *reinterpret_cast<const Vec<V>*>(src + h * D + ln.ob);
+    if (slot >= slots) return;
+    src += min(h, last) * D + ln.oa;
+    a = *reinterpret_cast<const Vec<V>*>(src);
+    b = *reinterpret_cast<const Vec<V>*>(src + (ln.ob - ln.oa));
   };
   if (row < t.n_tokens) {
 #pragma unroll
@@ -442,8 +440,9 @@ __device__ __forceinline__ void norm_rows(const Tokens& t, const Norm& norm, __n
     }
     if (h >= (key || value ? t.Hkv : t.Hq) || (kv_out == nullptr && (key || value))) return;
     __nv_bfloat16* dst = key ? kv_out + h * D : value ? kv_out + (t.Hkv + h) * D : q_out + h * D;
-    *reinterpret_cast<Vec<V>*>(dst + ln.oa) = oa;
-    *reinterpret_cast<Vec<V>*>(dst + ln.ob) = ob;
+    dst += ln.oa;
+    *reinterpret_cast<Vec<V>*>(dst) = oa;
+    *reinterpret_cast<Vec<V>*>(dst + (ln.ob - ln.oa)) = ob;
   };
   for (int s0 = 0; s0 < slots; s0 += kAhead) {
 #pragma unroll
