@@ -6,15 +6,15 @@
 // an SM has ~750 cycles for a page of 64 tokens at 256 dims.  What bounds the kernel is work on
 // the codes: 128 conversions of two codes, 48 products and 64 multiplications by V's scales a
 // warp and page, ~940 cycles with four warps per scheduler and all in shared memory (products
-// share their issue with fp32 and fp16 arithmetic), ~1,000 in place.  4 x 31,744 tokens of 4 kv
+// share their issue with fp32 and fp16 arithmetic), ~1,150 in place.  4 x 31,744 tokens of 4 kv
 // heads of 256 dims: 40 us (20 at the memory's rate), 262,144 tokens 81 (42).
 //
 // Scales differ along the dims of a head, so they cannot go with the rows of a product as the
 // 8-bit pool's do: codes become fp16 in registers and both products run as mma.sync m16n8k16
 // with fp32 sums.  (The fifth-generation tensor cores take K with its scales as it lies, but
-// V's scales are per token, its sum's index.  With their scores alone the warps that multiply
-// by V were held up, 4 x 31,744 tokens 41 us but 64 requests of up to 3,000 tokens 49 instead
-// of 35; with V's fp16 values in tensor memory 61 and 57.)
+// V's scales are per token, its sum's index.  With their scores, four softmax warps and eight for
+// the products: 4 x 31,744 tokens 38 us, but 64 requests of up to 3,000 tokens of 128 dims 40
+// instead of 35; with V's fp16 values in tensor memory 52 and 44.)
 //
 //  * Work split and partials: as the other decode kernels (split_units.cuh, unit_plan.h);
 //    a request's tiles are merged by a kernel of its own (tile_merge.cuh).
