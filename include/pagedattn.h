@@ -475,9 +475,13 @@ int paged_decode_attn_q8_lse(const void* q, const void* pool, const float* scale
  * For every group of 32 values of the normed and rotated k, and of v, in FP32: the
  * scale is the smallest power of two s >= 2^-60 with |x| <= 6 s for all of them, and
  * the codes are x / s rounded to nearest even.  A group with a value that is not
- * finite gets the scale NaN.  (k is normed and rotated in the steps of plain FP32
- * arithmetic, each product and sum rounded, so that a value at a border between two
- * codes goes as it would there.)  Rows of other tokens are left as they are.
+ * finite gets the scale NaN.  Rows of other tokens are left as they are.
+ * A key near a border between two codes goes as in this form of plain FP32 arithmetic (but
+ * for one code in 10^10): x * rsqrtf(sum / head_dim + eps) * w with rounded products; a c - b s
+ * and b c + a s with both products and the result rounded, c and s the floats nearest to the
+ * angle's cosine and sine; sum over the rounded squares, at 256 dims those of dims i and i + 128,
+ * then of four neighbours in turn, then neighbouring sums pair by pair, at 128 dims those of
+ * dims i, i + 32, i + 64 and i + 96 in turn, then pair by pair.
  * Supported head_dim: 128, 256. */
 int kv_append_rope_q4(const void* q, const void* k, const void* v, int64_t q_stride,
                       int64_t k_stride, int64_t v_stride, void* q_out, int64_t q_out_stride,

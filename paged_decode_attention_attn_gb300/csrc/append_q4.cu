@@ -30,12 +30,32 @@ namespace rope {
 
 constexpr int kGroup = PA_Q4_GROUP;
 
-// A key that lies at a border between two codes goes as plain fp32 arithmetic has it, so the
-// rows here are computed in its steps: sines and cosines rounded from more bits, products
-// and sums rounded apart, squares summed in the order of a reduction by 32 lanes.
+// A key near a border between two codes may go either way by the rounding of its norm and
+// turn.  Which way is fixed here as that of one form in plain fp32, an array library's for a
+// GPU, so that a pool filled here and one filled by such a form agree code by code:
+// x * rsqrt(sum / D + eps) * w with each product rounded, sines and cosines the nearest floats,
+// a c - b s with both products and the difference rounded, and the squares of a row of D
+// summed as written at sum_of_squares().
 
-// Sine and cosine at position p (see turn()) to ~0.55 units in the last place: the angle's
-// rest in two floats, the leading terms' rounding carried to the end.
+// A product of two sums of two floats each, the second of each the small part.
+__device__ __forceinline__ float2 times_fine(float2 a, float2 b) {
+  const float h = __fmul_rn(a.x, b.x);
+  return make_float2(h, fmaf(a.x, b.x, -h) + fmaf(a.x, b.y, a.y * b.x));
+}
+// a + b for |b| <= |a|, rounded once.
+__device__ __forceinline__ float add_fine(float a, float2 b, float a_lo) {
+  const float s = __fadd_rn(a, b.x), rest = __fadd_rn(__fsub_rn(a, s), b.x);
+  return __fadd_rn(s, rest + (b.y + a_lo));
+}
+// c + q z, |q z| <= |c| / 2.
+__device__ __forceinline__ float2 fma_fine(float q, float2 z, float2 c) {
+  const float h = fmaf(q, z.x, c.x);
+  return make_float2(h, fmaf(q, z.x, __fsub_rn(c.x, h)) + fmaf(q, z.y, c.y));
+}
+
+// Sine and cosine at position p (see turn()), the nearest floats but for 2 in 100,000 (at most
+// 0.5003 units in the last place): the angle's rest x, and the series' terms behind x and 1 -
+// x^2 / 2, in two floats each.
 __device__ __forceinline__ void turn_fine(long long p, unsigned long long step, float nan,
                                           float* s, float* c) {
   const unsigned long long at = step * (unsigned long long)p;
@@ -43,19 +63,24 @@ __device__ __forceinline__ void turn_fine(long long p, unsigned long long step, 
   const long long rest = (long long)(at - ((unsigned long long)quarter << 62));
   constexpr float kHi = 3.40612167e-19f, kLo = -9.47839643e-27f;   // 2 pi 2^-64
   const float hi = __ll2float_rn(rest), lo = __ll2float_rn(rest - __float2ll_rn(hi));
-  const float x = hi * kHi, x_lo = fmaf(hi, kHi, -x) + fmaf(hi, kLo, lo * kHi);
-  const float z = x * x, z_lo = fmaf(x, x, -z) + 2.f * x * x_lo;
-  float a = fmaf(z, -1.0f / 39916800.0f, 1.0f / 362880.0f);
-  a = fmaf(a, z, -1.0f / 5040.0f);
-  a = fmaf(a, z, 1.0f / 120.0f);
-  a = fmaf(a, z, -1.0f / 6.0f);
-  const float sx = __fadd_rn(x, fmaf(a * z, x, x_lo));
-  float b = fmaf(z, 1.0f / 479001600.0f, -1.0f / 3628800.0f);
-  b = fmaf(b, z, 1.0f / 40320.0f);
-  b = fmaf(b, z, -1.0f / 720.0f);
-  b = fmaf(b, z, 1.0f / 24.0f);
-  const float h = __fsub_rn(1.f, 0.5f * z);
-  const float cx = __fadd_rn(h, fmaf(b * z, z, __fsub_rn(1.f, h) - 0.5f * z - 0.5f * z_lo));
+  float2 x, z;
+  x.x = __fmul_rn(hi, kHi);
+  x.y = fmaf(hi, kHi, -x.x) + fmaf(hi, kLo, lo * kHi);
+  z.x = __fmul_rn(x.x, x.x);
+  z.y = fmaf(x.x, x.x, -z.x) + 2.f * x.x * x.y;
+  constexpr float kLo6 = 4.967054e-09f, kLo24 = -1.2417635e-09f, kLo120 = -4.346172e-10f;
+  float a = fmaf(z.x, -1.0f / 39916800.0f, 1.0f / 362880.0f);
+  a = fmaf(a, z.x, -1.0f / 5040.0f);
+  const float2 a2 = fma_fine(a, z, make_float2(1.0f / 120.0f, kLo120));
+  float2 a3 = fma_fine(a2.x, z, make_float2(-1.0f / 6.0f, kLo6));
+  a3.y = fmaf(a2.y, z.x, a3.y);
+  const float sx = add_fine(x.x, times_fine(x, times_fine(z, a3)), x.y);
+  float b = fmaf(z.x, 1.0f / 479001600.0f, -1.0f / 3628800.0f);
+  b = fmaf(b, z.x, 1.0f / 40320.0f);
+  b = fmaf(b, z.x, -1.0f / 720.0f);
+  const float2 b2 = fma_fine(b, z, make_float2(1.0f / 24.0f, kLo24));
+  const float h = __fsub_rn(1.f, 0.5f * z.x), h_lo = __fsub_rn(1.f, h) - 0.5f * z.x - 0.5f * z.y;
+  const float cx = add_fine(h, times_fine(times_fine(z, z), b2), h_lo);
   const bool odd = quarter & 1;
   const float ss = odd ? cx : sx, cc = odd ? sx : cx;
   *s = (quarter & 2 ? -ss : ss) + nan;
@@ -63,6 +88,8 @@ __device__ __forceinline__ void turn_fine(long long p, unsigned long long step, 
 }
 
 // The sum of a head's squares: a lane has 8 neighbours, the head D / 8 lanes.  All lanes call.
+// Of 256: those of dims i and i + 128, then of four neighbours in turn, then of neighbouring
+// sums pair by pair; of 128: of dims i, i + 32, i + 64 and i + 96 in turn, then pair by pair.
 template <int D>
 __device__ __forceinline__ float sum_of_squares(const float (&y)[8], float by) {
   float t[8];
@@ -72,12 +99,12 @@ __device__ __forceinline__ float sum_of_squares(const float (&y)[8], float by) {
     t[j] = __fmul_rn(x, x);
   }
   float ss;
-  if constexpr (D == 256) {   // the two halves; four neighbours in turn; neighbours' sums
+  if constexpr (D == 256) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) t[j] = __fadd_rn(t[j], __shfl_xor_sync(0xffffffffu, t[j], 16));
     ss = __fadd_rn(__fadd_rn(__fadd_rn(__fadd_rn(t[0], t[1]), t[2]), t[3]),
                    __fadd_rn(__fadd_rn(__fadd_rn(t[4], t[5]), t[6]), t[7]));
-  } else {                    // the four quarters in turn; neighbours' sums
+  } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int at = threadIdx.x & 0x13;
