@@ -286,6 +286,7 @@ struct Part {
   float m[2], l[2];
   int rho[2];
   int most;                 // largest byte of V's scales so far
+  bool beyond;              // 2^v of a weight may pass fp32's range (m' bounds e 2^v alone)
 };
 
 // Scale bytes of V: word i holds those of group kWords t + i of rows g (low half) and g + 8 of a
@@ -325,9 +326,12 @@ __device__ __forceinline__ void attend_wide(Part& part, uint32_t codes, uint32_t
     if (row < lo || row >= hi) continue;
     const float2 e = *reinterpret_cast<const float2*>(probs + i * kMaxG + 2 * t);
     const int b = lds8(vscales + row * S::kScaleRow + own);
-    float2 w = make_float2(
-        e.x * __int_as_float(__viaddmin_s32_relu(b, kTop + kUp - part.rho[0], 254) << 23),
-        e.y * __int_as_float(__viaddmin_s32_relu(b, kTop + kUp - part.rho[1], 254) << 23));
+    // e 2^n, n = v + kTop + kUp - rho, in two steps: e is small where n is beyond the exponents
+    auto weight = [&](float x, int rho) {
+      const int n = b - fp4::kScaleBias + kTop + kUp - rho;
+      return x * ptx::pow2i(min(n, 127)) * ptx::pow2i(min(max(n - 127, 0), 127));
+    };
+    float2 w = make_float2(weight(e.x, part.rho[0]), weight(e.y, part.rho[1]));
     if (b == fp4::kNanScale) w = f32x2::both(__int_as_float(0x7fc00000));
     float y[8];
     fp4::unpack8(lds32(codes + run_at<D>(row, own) + 4 * (g & 3)), y);
@@ -500,8 +504,8 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
     }
   }
   if (!ok && lane == 0) v.given_up[team] = 1;
-  bool move = first;
-  if (!first) {
+  bool move = first || part.beyond;          // (the whole team's)
+  if (!move) {
     weigh();
     publish();
     move = any_in_group(2 + team, 32 * S::kTeam,
@@ -592,7 +596,6 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
       part.most = max(part.most, all.most[n]);
       least = min(least, all.least[n]);
     }
-    wide = least < part.most - kSpread;
     float m[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -624,6 +627,10 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
       part.m[h] = m[h];
       part.rho[h] = rho;
     }
+    // (until the next move scales are at most 2^4 above the largest; a head of NaN has no rho)
+    auto over = [&](int rho) { return rho != kNoRho && part.most + 4 + kTop - rho > 254; };
+    part.beyond = __any_sync(0xffffffffu, over(part.rho[0]) || over(part.rho[1]));
+    wide = part.beyond || least < part.most - kSpread;
     weigh();
     if (wide) {
 #pragma unroll
@@ -712,6 +719,7 @@ __device__ __forceinline__ void consumer_warp(const P& p, const View& v, int war
     part.l[0] = part.l[1] = 0.f;
     part.rho[0] = part.rho[1] = 0;
     part.most = -1000;
+    part.beyond = false;
     ok = warp_wait(p, v, S::kQFull + qr.i, qr.phase, ok);
     const uint32_t q = v.addr + S::kQ + qr.i * S::kQBytes;
     const float2 qf =

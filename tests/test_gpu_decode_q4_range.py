@@ -1,0 +1,109 @@
+"""The 4-bit decode where scales and scores lie far apart, against the float64 oracle's values.
+
+Tolerances.  With A the largest of scale sum_d |q_d k_jd| over the row's keys, a probability
+p_j is within e = 2^-21 A + 2^-20 of itself (FP32 scores, the exponential, the parts that a
+probability is held in, their sums), so with S_d = sum_j p_j |V_jd| an output is within (e + 2^-19)
+of the largest S of its group of 32 dims: this has no floor, so that groups and keys are held to
+their own size.  The log-sum-exp is within e + 2^-22 |lse|."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import rope_q4 as Q
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+HKV = 2
+
+
+@pytest.fixture(scope="module")
+def B():
+    from paged_decode_attention_attn_gb300 import build
+    build.build()
+    from paged_decode_attention_attn_gb300 import binding
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return binding
+
+
+class Rows:
+    """One request of n tokens in order over its pages: `kv` codes' bytes [n][2 Hkv][D / 2] and
+    `scales` bytes [n][2 Hkv][D / 32] are put there by run()."""
+
+    def __init__(self, n, d, seed=0, groups=4):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        self.n, self.d, self.hq = n, d, HKV * groups
+        self.codes = torch.randint(0, 256, (n, 2 * HKV, d // 2), generator=g, device=DEV,
+                                   dtype=torch.uint8)
+        self.scales = torch.full((n, 2 * HKV, d // 32), 126, dtype=torch.uint8, device=DEV)
+        self.q = torch.randn(1, self.hq, d, generator=g, device=DEV).bfloat16()
+        self.scale = d ** -0.5
+
+    def run(self, B):
+        n, d, pages = self.n, self.d, -(-self.n // 64)
+        pool = torch.zeros(pages * 64, 2 * HKV, d // 2, dtype=torch.uint8, device=DEV)
+        scales = torch.full((pages * 64, 2 * HKV, d // 32), 255, dtype=torch.uint8, device=DEV)
+        pool[:n], scales[:n] = self.codes, self.scales
+        pool, scales = (x.view(pages, 64, 2 * HKV, -1).transpose(1, 2).contiguous()
+                        for x in (pool, scales))
+        table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+        self.out = torch.empty(1, 1, self.hq, d, device=DEV)
+        self.lse = torch.empty(1, 1, self.hq, device=DEV)
+        ws = B.alloc_workspace_q4(1, 1, self.hq, HKV, d)
+        B.paged_decode_attn_q4_lse(self.q, pool, scales, table, [[[0, n]]], self.scale, self.out,
+                                   self.lse, ws)
+        torch.cuda.synchronize()
+        assert int(ws[:4].view(torch.int32).item()) == 0
+
+    def check(self):
+        kv = Q.values(self.codes.cpu().numpy(), self.scales.cpu().numpy())
+        q = self.q[0].double().cpu().numpy()
+        G = self.hq // HKV
+        for h in range(self.hq):
+            k, v = kv[:, h // G], kv[:, HKV + h // G]
+            x = self.scale * (k @ q[h])
+            A = self.scale * np.max(np.abs(k) @ np.abs(q[h]))
+            e = 2.0 ** -21 * A + 2.0 ** -20
+            lse = np.max(x) + np.log(np.sum(np.exp(x - np.max(x))))
+            p = np.exp(x - lse)
+            S = np.repeat((p @ np.abs(v)).reshape(-1, 32).max(1), 32)
+            err = np.abs(self.out[0, 0, h].double().cpu().numpy() - p @ v)
+            assert np.all(err <= (e + 2.0 ** -19) * S), (h, np.max(err / S), e)
+            assert abs(float(self.lse[0, 0, h]) - lse) <= e + 2.0 ** -22 * abs(lse), h
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("n,at", [(2, 1), (300, 7), (300, 299), (9000, 4000), (9000, 8999)])
+@pytest.mark.parametrize("p_exp,v_exp", [(-104, 105), (-104, 106), (-108, 109), (-110, 110),
+                                         (-100, 60), (-60, 100)])
+def test_a_key_of_little_weight_and_far_larger_values(B, d, n, at, p_exp, v_exp):
+    """Key 0 has the largest score and V near 2^-30, key `at` the probability 2^p_exp and V 2^v_exp
+    times as large; the others' scores lie as far below again."""
+    r = Rows(n, d, seed=at)
+    r.q[:] = 1.0
+    r.scale = -p_exp * np.log(2.0) / d
+    r.codes[:, :HKV] = 0xAA                               # minus ones
+    r.codes[0, :HKV], r.codes[at, :HKV] = 0x22, 0         # ones, zeros
+    r.scales[:, :HKV] = 127
+    r.scales[:, HKV:] = 127 - 30
+    r.scales[at, HKV:] = 127 - 30 + v_exp
+    r.run(B)
+    r.check()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("top,low,v_exp", [(104, 0, 96), (106, 4, 112), (106, 4, 105), (107, 3, 111)])
+def test_a_page_of_little_weight_and_far_larger_values(B, d, top, low, v_exp):
+    """The same with a whole page of such keys, alike in scale, behind the first in one CTA's
+    part of a long history: scores of top and -low top / 128 in powers of two."""
+    r = Rows(80_000, d, seed=3)
+    r.q[:] = 1.0
+    r.scale = top * np.log(2.0) / d
+    r.codes[:, :HKV] = 0xAA
+    r.codes[0, :HKV], r.codes[512:576, :HKV] = 0x22, 0
+    r.codes[512:576, :HKV, :low * d // 256] = 0xAA
+    r.scales[:, :HKV] = 127
+    r.scales[:, HKV:] = 127 - 30
+    r.scales[512:576, HKV:] = 127 - 30 + v_exp
+    r.run(B)
+    r.check()
