@@ -30,7 +30,7 @@
 //    is idle.  A 16-byte run of a row is one scale's group; ldmatrix gives a lane 8 of its
 //    values in one word, two products sum the group, and an fp32 FMA with the token's scale
 //    adds it to the score.  q is scaled by a power of two per head and held in fp16: all its
-//    8 bits down to 2^-32 of the head's largest.
+//    8 bits down to 2^-31 of the head's largest.
 //  * Softmax: e = 2^(x - m) for the sum, with m a multiple of 8 near the largest score; the
 //    product's weight is w = e 2^(v - m') in fp16 as a high and a low part (22 bits), with 2^v
 //    the token's largest V scale and m' such that w is at most 2^15 whatever the scales: a
@@ -83,6 +83,8 @@ constexpr float kMostExp = 0x1p64f;          // e may lie above 1, up to this
 constexpr int kSlack = 3;                    // what m' leaves above the largest weight so far (log2)
 constexpr float kMostWeight = 65000.f;       // in fp16, which ends at 65504
 constexpr int kSpread = 16;                  // see attend()
+constexpr int kAlways = 4096;                // see Part::most
+constexpr float kLargeFactor = 0x1p60f;      // (a product is below 2^23: 2^-127 of it 2^-44 here)
 constexpr int kTiny = fp4::kScaleBias + fp4::kMinScaleExp;   // the smallest scale appends write
 
 // Shared memory of a CTA; offsets from a 1024-byte boundary.
@@ -285,8 +287,7 @@ struct Part {
   float2 o[4][2];           // [byte of codes][dim of the byte]
   float m[2], l[2];
   int rho[2];
-  int most;                 // largest byte of V's scales so far
-  bool beyond;              // 2^v of a weight may pass fp32's range (m' bounds e 2^v alone)
+  int most;                 // largest byte of V's scales so far, less kAlways: every page moves
 };
 
 // Scale bytes of V: word i holds those of group kWords t + i of rows g (low half) and g + 8 of a
@@ -313,25 +314,22 @@ struct Bytes {
   }
 };
 
-// The products of a page whose V scales lie far apart: in fp32, token by token, from the
-// probabilities of its scores.
+// The products of a page whose V scales lie far apart: in fp32, token by token, from the weights
+// and largest scales of its tokens.
 template <int D>
 __device__ __forceinline__ void attend_wide(Part& part, uint32_t codes, uint32_t vscales,
-                                            const float* probs, int own, int lo, int hi, int lane) {
+                                            const float* weights, uint32_t largest, int own,
+                                            int lo, int hi, int lane) {
   using S = Smem<D>;
   const int g = lane >> 2, t = lane & 3;
-#pragma unroll 1
+#pragma unroll (D == 128 ? 2 : 1)
   for (int i = 0; i < kPage; ++i) {
     const int row = (i & ~7) + place<D>(i & 7);
     if (row < lo || row >= hi) continue;
-    const float2 e = *reinterpret_cast<const float2*>(probs + i * kMaxG + 2 * t);
     const int b = lds8(vscales + row * S::kScaleRow + own);
-    // e 2^n, n = v + kTop + kUp - rho, in two steps: e is small where n is beyond the exponents
-    auto weight = [&](float x, int rho) {
-      const int n = b - fp4::kScaleBias + kTop + kUp - rho;
-      return x * ptx::pow2i(min(n, 127)) * ptx::pow2i(min(max(n - 127, 0), 127));
-    };
-    float2 w = make_float2(weight(e.x, part.rho[0]), weight(e.y, part.rho[1]));
+    float2 w = f32x2::mul(
+        *reinterpret_cast<const float2*>(weights + i * kMaxG + 2 * t),
+        f32x2::both(__int_as_float(max(b - (int)lds8(largest + i) + kUp + 127, 0) << 23)));
     if (b == fp4::kNanScale) w = f32x2::both(__int_as_float(0x7fc00000));
     float y[8];
     fp4::unpack8(lds32(codes + run_at<D>(row, own) + 4 * (g & 3)), y);
@@ -401,9 +399,54 @@ __device__ __forceinline__ void scores(float2 (&x)[kTiles][2], uint32_t codes, u
   }
 }
 
+// A lane's scores that are not finite, or of a head with a factor so large that a scale of 2^-127
+// counts, once more: K's scales come ahead of q's factors, and products may pass fp32's range
+// where scores do not, so here a group's product meets the smaller of the two first.  What is not
+// finite then is NaN.  x: [token][head] of the page.  (Rare, so it is short: with the matrix
+// products a second time, or a call, first pages paid for its code or its registers, 252 requests
+// of 103 tokens 25.0 us for 23.)
+template <int D, int kTiles>
+__device__ __forceinline__ void scores_far(float* x, uint32_t codes, uint32_t scales, uint32_t q,
+                                           float2 qf, int item0, int lo, int hi, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll 1
+  for (int i = 0; i < 2 * kTiles; ++i) {
+    const int row = item0 + 8 * i + place<D>(g);
+    if (row < lo || row >= hi) continue;
+    float2 y = f32x2::both(0.f);
+#pragma unroll 1
+    for (int c = 0; c < D / kGroup; ++c) {
+      float2 s = f32x2::both(0.f);
+#pragma unroll 1
+      for (int u = 0; u < 4; ++u) {          // 8 dims
+        float k[8];
+        fp4::unpack8(lds32(codes + run_at<D>(row, c) + 4 * u), k);
+        const uint32_t at = q + (c * 32 + 8 * t + u) * 16;
+        const uint4 a = lds128(at), b = lds128(at + 64);
+        const uint32_t qa[4] = {a.x, a.y, a.z, a.w}, qb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&qa[j]));
+          const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&qb[j]));
+          s.x = fmaf(k[2 * j + 1], fa.y, fmaf(k[2 * j], fa.x, s.x));
+          s.y = fmaf(k[2 * j + 1], fb.y, fmaf(k[2 * j], fb.x, s.y));
+        }
+      }
+      const float k = fp4::scale_of(lds8(scales + row * Smem<D>::kScaleRow + c));
+      y.x += fabsf(qf.x) < k ? s.x * qf.x * k : s.x * k * qf.x;   // (NaN of a NaN)
+      y.y += fabsf(qf.y) < k ? s.y * qf.y * k : s.y * k * qf.y;
+    }
+    float2& z = *reinterpret_cast<float2*>(x + (item0 + 8 * i + g) * kMaxG + 2 * t);
+    if (!(fabsf(z.x) <= FLT_MAX) || fabsf(qf.x) > kLargeFactor) z.x = y.x;
+    if (!(fabsf(z.y) <= FLT_MAX) || fabsf(qf.y) > kLargeFactor) z.y = y.y;
+    z = f32x2::fma(z, f32x2::both(0.f), z);
+  }
+}
+
 // A page, by warp w of a team.  lo, hi: its live rows; buf: of the team's two buffers; first: in
-// the segment; ok: false once a wait of this warp has run out, and of all the team's from the next page on (they
-// meet at barriers without a time limit, so a warp that has given up goes on meeting).
+// the segment; ok: false once a wait of this warp has run out, and of all the team's from the next
+// page on (they meet at barriers without a time limit, so a warp that has given up goes on
+// meeting).
 template <int D>
 __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uint32_t q, float2 qf,
                                        int team, int w, int buf, bool first, int lo, int hi,
@@ -490,32 +533,44 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
     }
     in &= ~(e[tile] + 0x00010001u * (0x7fff - min(part.most + 4, 254)));
   }
+  auto live = [&](int i) {                   // tile i / 2, row g or g + 8
+    const int row = item0 + 16 * (i >> 1) + 8 * (i & 1) + place<D>(g);
+    return row >= lo && row < hi;
+  };
+  float2 sum = f32x2::both(0.f);
 #pragma unroll
   for (int i = 0; i < 2 * kTiles; ++i) {
     float2& y = x[i >> 1][i & 1];
     y = f32x2::mul(y, qf);
-    y = f32x2::fma(y, f32x2::both(0.f), y);   // an infinite score is NaN
+    sum = f32x2::add(sum, y);
   }
   if (lo > item0 || hi < item0 + S::kOwn) {
+    sum = f32x2::both(0.f);
 #pragma unroll
     for (int i = 0; i < 2 * kTiles; ++i) {
-      const int row = item0 + 16 * (i >> 1) + 8 * (i & 1) + place<D>(g);
-      if (row < lo || row >= hi) x[i >> 1][i & 1] = f32x2::both(-INFINITY);
+      float2& y = x[i >> 1][i & 1];
+      if (live(i)) sum = f32x2::add(sum, y);
+      else y = f32x2::both(-INFINITY);
     }
   }
+  // K's scales came ahead of q's factors, so products may pass fp32's range where scores do
+  // not; and a scale of 2^-127 was zero, which shows beside the largest factors.
+  auto passes = [](float s, float f) { return !(fabsf(s) <= FLT_MAX) && f == f; };
+  auto large = [](float f) { return fabsf(f) > kLargeFactor; };
+  const bool again = passes(sum.x, qf.x) || passes(sum.y, qf.y);
   if (!ok && lane == 0) v.given_up[team] = 1;
-  bool move = first || part.beyond;          // (the whole team's)
-  if (!move) {
+  bool move = first;
+  if (!first) {
     weigh();
     publish();
     move = any_in_group(2 + team, 32 * S::kTeam,
-                        !ok || in != 0x80008000u || largest(wt) > kMostWeight ||
+                        !ok || again || in != 0x80008000u || largest(wt) > kMostWeight ||
                             largest(p) > kMostExp);
   }
   bool wide = false;
   if (move) {
-    // The references move, and scales are looked at again: of live rows and groups that are
-    // not all zeros, without NaN.
+    // The references move, and scores and scales are looked at again: of live rows, scales of
+    // groups that are not all zeros, without NaN.
     Meet<D>& all = reinterpret_cast<Meet<D>*>(v.base + S::kMeet)[team];
     int most = 0, least = 255;
 #pragma unroll
@@ -558,6 +613,16 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
       all.most[w] = most;
       all.least[w] = least;
     }
+    if (__builtin_expect(again || large(qf.x) || large(qf.y), 0)) {
+      float2* far = reinterpret_cast<float2*>(to) + (item0 + g) * (kMaxG / 2) + t;
+#pragma unroll
+      for (int i = 0; i < 2 * kTiles; ++i) far[8 * i * (kMaxG / 2)] = x[i >> 1][i & 1];
+      scores_far<D, kTiles>(reinterpret_cast<float*>(to), codes, scales_at, q, qf, item0, lo, hi,
+                            lane);
+#pragma unroll
+      for (int i = 0; i < 2 * kTiles; ++i) x[i >> 1][i & 1] = far[8 * i * (kMaxG / 2)];
+    }
+    __syncwarp();
     // this warp's largest scores, and largest weights relative to them (NaN ignored)
     auto heads_max = [](float2 y) {
 #pragma unroll
@@ -591,9 +656,10 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
       ok = false;
       return;
     }
+    most = part.most < -2000 ? part.most + kAlways : part.most;
 #pragma unroll
     for (int n = 0; n < S::kTeam; ++n) {
-      part.most = max(part.most, all.most[n]);
+      most = max(most, all.most[n]);
       least = min(least, all.least[n]);
     }
     float m[2];
@@ -627,16 +693,30 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
       part.m[h] = m[h];
       part.rho[h] = rho;
     }
-    // (until the next move scales are at most 2^4 above the largest; a head of NaN has no rho)
-    auto over = [&](int rho) { return rho != kNoRho && part.most + 4 + kTop - rho > 254; };
-    part.beyond = __any_sync(0xffffffffu, over(part.rho[0]) || over(part.rho[1]));
-    wide = part.beyond || least < part.most - kSpread;
+    // m' bounds e 2^v, not 2^v, which may pass the range of weigh()'s factors; until the next move
+    // scales are at most 2^4 above the largest.  (A head of NaN has no rho.)
+    auto over = [&](int rho) { return rho != kNoRho && most + 4 + kTop - rho > 254; };
+    const bool beyond = __any_sync(0xffffffffu, over(part.rho[0]) || over(part.rho[1]));
+    wide = least < most - kSpread;
+    part.most = __any_sync(0xffffffffu, beyond || large(qf.x) || large(qf.y)) ? most - kAlways : most;
     weigh();
+    if (beyond) {
+      // what the factors of weigh() were cut by
+#pragma unroll
+      for (int i = 0; i < 2 * kTiles; ++i) {
+        const int b = i & 1 ? e[i >> 1] >> 16 : e[i >> 1] & 0xffff;
+        float2& y = wt[i >> 1][i & 1];
+        y.x *= ptx::pow2i(min(max(b + kTop - part.rho[0] - 254, 0), 127));
+        y.y *= ptx::pow2i(min(max(b + kTop - part.rho[1] - 254, 0), 127));
+      }
+    }
     if (wide) {
 #pragma unroll
-      for (int i = 0; i < 2 * kTiles; ++i)
-        *reinterpret_cast<float2*>(to + ((item0 + 8 * i + g) * kMaxG + 2 * t) * 4) =
-            p[i >> 1][i & 1];
+      for (int i = 0; i < 2 * kTiles; ++i) {
+        const int item = item0 + 8 * i + g;
+        *reinterpret_cast<float2*>(to + (item * kMaxG + 2 * t) * 4) = wt[i >> 1][i & 1];
+        if (t == 0) factors[item] = (uint8_t)(i & 1 ? e[i >> 1] >> 16 : e[i >> 1]);
+      }
     } else {
       publish();
     }
@@ -650,8 +730,8 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
   // ---- products ----
   const int own = 2 * w + (g >> 2);          // this lane's group
   if (wide) {
-    attend_wide<D>(part, codes + S::kHalf, vscales, reinterpret_cast<const float*>(to), own, lo,
-                   hi, lane);
+    attend_wide<D>(part, codes + S::kHalf, vscales, reinterpret_cast<const float*>(to),
+                   ptx::smem_addr(factors), own, lo, hi, lane);
     return;
   }
   const uint32_t b_at = ptx::smem_addr(to) + lane * 16,
@@ -719,7 +799,6 @@ __device__ __forceinline__ void consumer_warp(const P& p, const View& v, int war
     part.l[0] = part.l[1] = 0.f;
     part.rho[0] = part.rho[1] = 0;
     part.most = -1000;
-    part.beyond = false;
     ok = warp_wait(p, v, S::kQFull + qr.i, qr.phase, ok);
     const uint32_t q = v.addr + S::kQ + qr.i * S::kQBytes;
     const float2 qf =
@@ -984,9 +1063,10 @@ __device__ __forceinline__ void helper_warp(const P& p, const View& v, int lane)
     most = max(most & 0xffffu, most >> 16);
     most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
     most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-    // Largest value to [2^14, 2^15).  A head with a NaN or an infinity becomes NaN (its
-    // scores would be).
-    const int e = most ? min(14 - ((int)(most >> 7) - 127), 120) : 0;
+    // Largest value to [2^14, 2^15), unless that takes the factor below fp32's range.  A head
+    // with a NaN or an infinity becomes NaN (its scores would be).
+    const int of_scale = (__float_as_int(fabsf(p.scale_log2)) >> 23) - 127;
+    const int e = most ? min(14 - ((int)(most >> 7) - 127), 120 + min(of_scale, 0)) : 0;
     const float up = ptx::pow2i(e);
     const float back = most < 0x7f80u ? p.scale_log2 * ptx::pow2i(-e) : __int_as_float(0x7fc00000);
     if (!warp_wait(p, v, S::kQEmpty + ring.i, ring.phase ^ 1)) return false;

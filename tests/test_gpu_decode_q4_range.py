@@ -39,10 +39,10 @@ class Rows:
         self.q = torch.randn(1, self.hq, d, generator=g, device=DEV).bfloat16()
         self.scale = d ** -0.5
 
-    def run(self, B):
+    def run(self, B, behind=255):
         n, d, pages = self.n, self.d, -(-self.n // 64)
         pool = torch.zeros(pages * 64, 2 * HKV, d // 2, dtype=torch.uint8, device=DEV)
-        scales = torch.full((pages * 64, 2 * HKV, d // 32), 255, dtype=torch.uint8, device=DEV)
+        scales = torch.full((pages * 64, 2 * HKV, d // 32), behind, dtype=torch.uint8, device=DEV)
         pool[:n], scales[:n] = self.codes, self.scales
         pool, scales = (x.view(pages, 64, 2 * HKV, -1).transpose(1, 2).contiguous()
                         for x in (pool, scales))
@@ -107,3 +107,65 @@ def test_a_page_of_little_weight_and_far_larger_values(B, d, top, low, v_exp):
     r.scales[512:576, HKV:] = 127 - 30 + v_exp
     r.run(B)
     r.check()
+
+
+def times(x, e):
+    """bf16 x * 2^e for any e in range."""
+    return (x.float() * 2.0 ** (e // 2) * 2.0 ** (e - e // 2)).bfloat16()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("k_exp,q_exp", [(112, -113), (113, -114), (112, -118), (119, -125),
+                                         (106, -107), (126, -131), (-60, 60), (60, -66),
+                                         (-60, 110), (-127, 122), (-126, 121), (-100, 90),
+                                         (112, -107), (112, -105), (126, -106), (120, -40),
+                                         (111, 0)])
+def test_scores_within_range_from_factors_far_apart(B, d, k_exp, q_exp):
+    """K's scale and q far from 1, the scores near it."""
+    r = Rows(200, d, seed=k_exp + 200)
+    r.scales[:, :HKV] = 127 + k_exp
+    r.q = times(r.q, q_exp)
+    r.scale *= 2.0 ** -(q_exp + k_exp)
+    r.run(B)
+    r.check()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_a_few_keys_of_large_scales(B, d):
+    """Every 17th key is large, the others small beside it; a head of q is zero."""
+    r = Rows(700, d, seed=5)
+    r.scales[:, :HKV] = 127 + 100
+    r.scales[::17, :HKV] = 127 + 110
+    r.q = times(r.q, -111)
+    r.q[0, 3] = 0
+    r.run(B)
+    r.check()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_far_scores_stay_finite(B, d):
+    """Scores of 10^34: finite, and the key of the largest has the whole weight."""
+    r = Rows(70, d, seed=6)
+    r.codes[:, :HKV] = 0x77                               # sixes
+    r.codes[::2, :HKV] = 0xFF
+    r.codes[41, :HKV], r.codes[40, :HKV] = 0x77, 0xFF
+    r.scales[:, :HKV] = 127 + 106
+    r.scales[41, :HKV] = 127 + 107
+    r.q[:] = 1.0
+    r.scale = 1 / 16
+    r.run(B)
+    v = Q.values(*(x[41, HKV:].cpu().numpy() for x in (r.codes, r.scales)))
+    assert np.array_equal(r.out[0, 0].double().cpu().numpy(), np.repeat(v, 4, 0))
+    want = d * 6 * 2.0 ** 107 / 16
+    assert torch.all((r.lse.double() / want - 1).abs() <= 2.0 ** -21)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_rows_that_are_not_live_do_not_reach_the_bits_of_others(B, d):
+    outs = []
+    for behind in (255, 254, 0, 127):
+        r = Rows(130, d, seed=7)
+        r.run(B, behind)
+        r.check()
+        outs.append((r.out, r.lse))
+    assert all(torch.equal(a, b) for o in outs for a, b in zip(o, outs[0]))
