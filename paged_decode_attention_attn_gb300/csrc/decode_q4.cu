@@ -85,7 +85,6 @@ constexpr float kMostWeight = 65000.f;       // in fp16, which ends at 65504
 constexpr int kSpread = 16;                  // see attend()
 constexpr int kAlways = 4096;                // see Part::most
 constexpr float kLargeFactor = 0x1p60f;      // (a product is below 2^23: 2^-127 of it 2^-44 here)
-constexpr int kTiny = fp4::kScaleBias + fp4::kMinScaleExp;   // the smallest scale appends write
 
 // Shared memory of a CTA; offsets from a 1024-byte boundary.
 template <int D>
@@ -517,21 +516,34 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
   // Weights are fp16 pairs, and a group of dims is held to its own size as long as its
   // scales lie within 2^kSpread of the largest scale that the team has met (a weight that
   // counts for it is then at least 2^-3 and has 22 bits).  The test takes bounds that are a
-  // little closer, and bytes of rows that are not live with the others.  Scales as small as
-  // the smallest that appends write do not count: their groups are zeros (heads padded to
-  // 128 or 256 dims have them in every token), or nothing beside the others.
-  uint32_t in = 0x80008000u;
+  // little closer, and bytes of rows that are not live with the others.  A group that lies
+  // further down does not count if it is all zeros (heads padded to 128 or 256 dims have
+  // such ones in every token).
+  uint32_t in = 0x80008000u, near = in;
+  const int floor = max(part.most - (kSpread - 4), 0);
 #pragma unroll
   for (int tile = 0; tile < kTiles; ++tile) {
     bytes[tile].load(vscales + (item0 + 16 * tile + place<D>(g)) * S::kScaleRow, t);
     e[tile] = bytes[tile].largest();
 #pragma unroll
     for (int i = 0; i < Bytes<D>::kWords; ++i) {
-      in &= (bytes[tile].b[i] + 0x00010001u * (0x8000 - max(part.most - (kSpread - 4), 0))) |
-            ~(bytes[tile].b[i] + 0x00010001u * (0x8000 - kTiny - 1));
+      near &= bytes[tile].b[i] + 0x00010001u * (0x8000 - floor);
       if (!first) publish_factor(tile, i, factor(tile, i));
     }
     in &= ~(e[tile] + 0x00010001u * (0x7fff - min(part.most + 4, 254)));
+  }
+  auto holds_codes = [&](int tile, int k) {  // of V, group kWords t + k / 2 of row g + 8 (k % 2)
+    const uint4 c = lds128(codes + S::kHalf + run_at<D>(item0 + 16 * tile + 8 * (k & 1) + place<D>(g),
+                                                        Bytes<D>::kWords * t + (k >> 1)));
+    return ((c.x | c.y | c.z | c.w) & 0x77777777u) != 0;
+  };
+  if (near != 0x80008000u) {
+#pragma unroll
+    for (int i = 0; i < 2 * Bytes<D>::kWords * kTiles; ++i) {
+      const int tile = i / (2 * Bytes<D>::kWords), k = i % (2 * Bytes<D>::kWords);
+      const uint32_t word = bytes[tile].b[k >> 1];
+      if ((int)(k & 1 ? word >> 16 : word & 0xffffu) < floor && holds_codes(tile, k)) in = 0;
+    }
   }
   auto live = [&](int i) {                   // tile i / 2, row g or g + 8
     const int row = item0 + 16 * (i >> 1) + 8 * (i & 1) + place<D>(g);
@@ -586,9 +598,7 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
           nan |= 1u << k;
           word &= ~half;
         } else if (row >= lo && row < hi) {
-          const uint4 c = lds128(codes + S::kHalf +
-                                 run_at<D>(row, Bytes<D>::kWords * t + (k >> 1)));
-          if (b > kTiny && ((c.x | c.y | c.z | c.w) & 0x77777777u)) least = min(least, b);
+          if (holds_codes(tile, k)) least = min(least, b);
         }
       }
       e[tile] = bytes[tile].largest();

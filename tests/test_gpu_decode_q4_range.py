@@ -68,7 +68,7 @@ class Rows:
             p = np.exp(x - lse)
             S = np.repeat((p @ np.abs(v)).reshape(-1, 32).max(1), 32)
             err = np.abs(self.out[0, 0, h].double().cpu().numpy() - p @ v)
-            assert np.all(err <= (e + 2.0 ** -19) * S), (h, np.max(err / S), e)
+            assert np.all(err <= (e + 2.0 ** -19) * S), (h, np.max(err / np.maximum(S, 1e-300)), e)
             assert abs(float(self.lse[0, 0, h]) - lse) <= e + 2.0 ** -22 * abs(lse), h
 
 
@@ -169,3 +169,32 @@ def test_rows_that_are_not_live_do_not_reach_the_bits_of_others(B, d):
         r.check()
         outs.append((r.out, r.lse))
     assert all(torch.equal(a, b) for o in outs for a, b in zip(o, outs[0]))
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("at,gap", [(-60, 20), (-60, 27), (-80, 24), (-60, 18), (-127, 30), (-60, 70)])
+@pytest.mark.parametrize("n,every", [(70, 3), (700, 64), (3000, 2999)])
+def test_small_groups_beside_larger_ones_of_other_keys(B, d, at, gap, n, every):
+    """The last group of dims has the scale 2^at in every key, the others too but for the first, and
+    each `every`-th key after it, where they are 2^gap times as large."""
+    r = Rows(n, d, seed=gap)
+    r.scales[:, HKV:] = 127 + at
+    r.scales[::every, HKV:, :-1] = 127 + at + gap
+    r.run(B)
+    r.check()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("byte", [0, 67, 100])
+def test_groups_of_zeros_of_any_scale(B, d, byte):
+    """Groups without codes do not change a bit of the others, whatever their scale."""
+    outs = []
+    for b in (byte, 126):
+        r = Rows(1000, d, seed=8)
+        r.codes[:, HKV:, -32:] = 0
+        r.scales[:, HKV:, -2:] = b
+        r.run(B)
+        assert torch.all(r.out[..., -64:] == 0)
+        r.check() if b == 126 else None
+        outs.append((r.out, r.lse))
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
