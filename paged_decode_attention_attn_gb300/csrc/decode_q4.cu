@@ -817,10 +817,12 @@ __device__ __forceinline__ void consumer_warp(const P& p, const View& v, int war
     const int first = team < at ? team - at + S::kTeams : team - at;
     int poisoned = 0;
     for (int i = first; i < pages; i += S::kTeams) {
-      // The stage's last page was another team's: a wait for this load has a meaning once that
-      // page is done with (parities tell two loads apart, not three).  The one before it is:
-      // the load of this team's last page came after it.
-      ok = warp_wait(p, v, S::kEmpty + stage, phase ^ 1, ok);
+      // Where stages are not a multiple of the teams (9 and 4), the stage's last page was another
+      // team's: a wait for this load has a meaning once that page is done with (parities tell
+      // two loads apart, not three).  The one before it is: the load of this team's last page
+      // came after it.  Otherwise (16 and 8) this team was done with the stage's last page itself.
+      if constexpr (S::kStages % S::kTeams != 0)
+        ok = warp_wait(p, v, S::kEmpty + stage, phase ^ 1, ok);
       ok = warp_wait(p, v, S::kFull + stage, phase, ok);
       poisoned |= v.poison[stage];
       // the page's live tokens, from its first
