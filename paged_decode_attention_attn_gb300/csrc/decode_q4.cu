@@ -1122,8 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Smem<D>;
   extern __shared__ uint8_t smem_raw[];
   View v;
-  v.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                      ~uintptr_t(1023));
+  v.base = smem_raw + (-ptx::smem_addr(smem_raw) & 1023);   // (known to be shared memory so)
   v.addr = ptx::smem_addr(v.base);
   v.bars = v.addr + S::kBars;
   int* misc = reinterpret_cast<int*>(v.base + S::kMisc);
