@@ -516,7 +516,7 @@ size_t paged_decode_attn_q4_workspace_bytes(int B, int T, int n_q_heads, int n_k
  * so far in a row's part of a tile, for each group of 32 dims by itself while V's scales lie
  * within 2^16 of each other; in FP32 where they lie further apart, which takes about three times
  * as long.  (Groups of zeros have no scale in this.)  Probabilities below 2^-110 of the largest,
- * and products of one with its V scales below 2^-110 of the largest, count as zero.
+ * and products of one with a V scale below 2^-75 of the largest such product, count as zero.
  * Supported: head_dim 128 and 256, n_q_heads / n_kv_heads in 1..8. */
 int paged_decode_attn_q4_lse(const void* q, const void* pool, const uint8_t* scales,
                              int64_t pool_pages, const int32_t* page_table, int max_pages,

@@ -198,3 +198,26 @@ def test_groups_of_zeros_of_any_scale(B, d, byte):
         r.check() if b == 126 else None
         outs.append((r.out, r.lse))
     assert all(torch.equal(x, y) for x, y in zip(*outs))
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("offsets", [[0, 20], [0, 30], [0, 50, 20, 30], [0, 0, 0, 70], [0, 16], [0, 17]])
+@pytest.mark.parametrize("n", [3, 64, 1000])
+def test_groups_of_fixed_distances_in_every_key(B, d, offsets, n):
+    """Groups of dims 2^offset below the first in all keys alike: each is held to its own size."""
+    r = Rows(n, d, seed=n)
+    e = torch.tensor((offsets * 8)[: d // 32], dtype=torch.uint8, device=DEV)
+    r.scales[:, HKV:] = 127 + 20 - e
+    r.run(B)
+    r.check()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("at", [0, 100, 9_999, 19_999])
+@pytest.mark.parametrize("groups", [slice(None), slice(0, 1), slice(2, 3)])
+def test_one_key_of_far_larger_values_in_a_long_history(B, d, at, groups):
+    """Its pages, and those that its team has after it, go in fp32."""
+    r = Rows(20_000, d, seed=at)
+    r.scales[at, HKV:, groups] = 127 + 22
+    r.run(B)
+    r.check()
