@@ -372,7 +372,8 @@ int kv_append_rope(const void* q, const void* k, const void* v, int64_t q_stride
  * w = q_weight for q heads and k_weight for k heads, in FP32 (whatever the size of
  * finite x: sums that pass FP32's range are scaled).  The result is rotated and
  * rounded once, to bf16.  A head that holds a NaN becomes NaN, one that holds an
- * infinity NaN there and 0 elsewhere.  v passes unchanged.  Arguments as above, and:
+ * infinity NaN there (and, rotated, in the other value of its pair) and 0 elsewhere.
+ * v passes unchanged.  Arguments as above, and:
  *   q_weight, k_weight  device fp32 [head_dim] (q_weight may be NULL without q).
  *   eps                 in [2^-60, 1]. */
 int kv_append_norm_rope(const void* q, const void* k, const void* v, int64_t q_stride,

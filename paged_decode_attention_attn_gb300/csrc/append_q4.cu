@@ -11,9 +11,9 @@
 // CTAs of their own.
 //
 // Decode sizes are bound by the latency of dependent loads (request, position, page, row:
-// 1-96 tokens 3.5-4 us and 2 us for the gather); prompts by instructions and their loads'
-// latency (8,000 tokens of 24 q and 4 kv heads of 256 dims with norms 61 us where the bytes
-// take 35, their gather 10.6).
+// 1-96 tokens 3.7-4.5 us and 2 us for the gather); prompts by instructions and their loads'
+// latency (8,000 tokens of 24 q and 4 kv heads of 256 dims with norms 63.3 us where the bytes
+// take 35, their gather 7.4 where they take 6.2).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -377,8 +377,9 @@ cudaError_t launch_append_q4(const Tokens& t, const Norm& norm, void* pool, uint
                           q_share);
 }
 
-// (q rows with norms go by 4 pairs of a lane, three CTAs to an SM: two prompts 71.7 us; by 8,
-// two CTAs: 73.9.)
+// (q rows with norms go by 4 pairs of a lane, three CTAs to an SM: two prompts of 8,054 tokens with
+// 24 q and 4 kv heads of 256 dims 63.6 us, 32 and 8 of 128 50.4; by 8, two CTAs: 66.5 and 53.6.
+// 1-96 tokens alike.)
 template <int D>
 cudaError_t launch_append_q4(const Tokens& t, const Norm& norm, bool normed, void* pool,
                              uint8_t* scales, cudaStream_t stream) {

@@ -6,8 +6,9 @@
 // an SM has ~750 cycles for a page of 64 tokens at 256 dims.  What bounds the kernel is work on
 // the codes: 128 conversions of two codes, 48 products and 64 multiplications by V's scales a
 // warp and page, ~940 cycles with four warps per scheduler and all in shared memory (products
-// share their issue with fp32 and fp16 arithmetic), ~1,150 in place.  4 x 31,744 tokens of 4 kv
-// heads of 256 dims: 40 us (20 at the memory's rate), 262,144 tokens 81 (42).
+// share their issue with fp32 and fp16 arithmetic), ~1,150 in place, where no pipe is full and a
+// scheduler's warps wait for each other's results and barriers.  4 x 31,744 tokens of 4 kv heads
+// of 256 dims: 39.5 us (20 at the memory's rate), 262,144 tokens 80.4 (42).
 //
 // Scales differ along the dims of a head, so they cannot go with the rows of a product as the
 // 8-bit pool's do: codes become fp16 in registers and both products run as mma.sync m16n8k16
@@ -1163,8 +1164,10 @@ using Common = Params<kMaxUnitsSmall>;
 
 // As the 8-bit kernel's where not noted.  A page costs less, and sums per CTA are fewer, so
 // units are split further: at least 2 pages to a CTA (4: 900 tokens 13.3 us instead of 10.1;
-// 1: 12.6), whole up to 4 (16: 15.6).  The SMs' time bounds long launches, so they run on all
-// (85%: 64 requests of up to 3,000 tokens 40.4 us, 34.9 on all).
+// 1: 12.6), whole up to 4 (16: 15.6).  The SMs' time bounds long launches, so they are cut for
+// all SMs (85%: 64 requests of up to 3,000 tokens 40.4 us, 34.9 on all); but units of one length
+// still go to the next grid that divides them (144 CTAs for 16 units, 128 for 32).  The two rules
+// in bytes are the 8-bit kernel's and have not been measured here.
 Rules rules_of(int D) {
   const int page_bytes = 2 * (kPage * D / 2 + kPage * D / kGroup);
   Rules r;
