@@ -511,8 +511,9 @@ size_t paged_decode_attn_q4_workspace_bytes(int B, int T, int n_q_heads, int n_k
  * paged_decode_attn_q8_lse.  Arguments as there, except:
  *   pool, scales  device, 16-byte aligned, as described at PA_Q4_GROUP.
  * Rows outside a tile may hold anything, NaN scales too.  K scales may be any for which the
- * scores, and their parts of 32 dims, are finite (and |q| scale is).  A value of q keeps all its bits down to 2^-31 of its
- * head's largest, or to 2^-136 / scale if that is more, and is held to 2^-8 of that below.
+ * scores, and their parts of 32 dims, are finite (and |q| scale is).  A value of q keeps all
+ * its bits down to 2^-31 of its head's largest, or to 2^-136 / scale if that is more, and is
+ * held to 2^-8 of that below.
  * A probability times its V scales is held to 2^-23 of itself, or to 2^-37 of the largest
  * so far in a row's part of a tile, for each group of 32 dims by itself while V's scales lie
  * within 2^16 of each other; in FP32 where they lie further apart, which takes about three times
