@@ -534,8 +534,8 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
     in &= ~(e[tile] + 0x00010001u * (0x7fff - min(part.most + 4, 254)));
   }
   auto holds_codes = [&](int tile, int k) {  // of V, group kWords t + k / 2 of row g + 8 (k % 2)
-    const uint4 c = lds128(codes + S::kHalf + run_at<D>(item0 + 16 * tile + 8 * (k & 1) + place<D>(g),
-                                                        Bytes<D>::kWords * t + (k >> 1)));
+    const int row = item0 + 16 * tile + 8 * (k & 1) + place<D>(g);
+    const uint4 c = lds128(codes + S::kHalf + run_at<D>(row, Bytes<D>::kWords * t + (k >> 1)));
     return ((c.x | c.y | c.z | c.w) & 0x77777777u) != 0;
   };
   if (near != 0x80008000u) {
@@ -709,7 +709,8 @@ __device__ __forceinline__ void attend(Part& part, const View& v, int stage, uin
     auto over = [&](int rho) { return rho != kNoRho && most + 4 + kTop - rho > 254; };
     const bool beyond = __any_sync(0xffffffffu, over(part.rho[0]) || over(part.rho[1]));
     wide = least < most - kSpread;
-    part.most = __any_sync(0xffffffffu, beyond || large(qf.x) || large(qf.y)) ? most - kAlways : most;
+    const bool always = __any_sync(0xffffffffu, beyond || large(qf.x) || large(qf.y));
+    part.most = always ? most - kAlways : most;
     weigh();
     if (beyond) {
       // what the factors of weigh() were cut by
